@@ -61,6 +61,7 @@ extern "C" {
 #define MXFP8_FLAG_POLL_TIMEOUT 0x1 /* the consumer's poll ran out of time   */
 #define MXFP8_FLAG_GEMM_TIMEOUT 0x2 /* a GEMM pipeline wait ran out of time  */
 #define MXFP8_FLAG_BAD_STATE 0x4    /* a kernel read a generation not in 0..2 */
+#define MXFP8_FLAG_BAD_INDEX 0x8    /* an adapter, page, length or row index out of range */
 
 typedef enum mxfp8_status {
   MXFP8_OK = 0,
@@ -308,6 +309,7 @@ mxfp8_status mailbox_consume(void* mailbox, int32_t* stage_state, int32_t capaci
 
 /* Synchronises `stream`, copies stage_state (device int32[4]) into words
  * (host int32[4]) and reports: MXFP8_ERR_TIMEOUT if a timeout flag is set,
+ * MXFP8_ERR_INVALID if a run met an adapter index out of range,
  * MXFP8_ERR_STATE if the bad-state flag is set or a generation word is not in
  * 0..2, else MXFP8_OK. */
 mxfp8_status mxfp8_mailbox_status(const int32_t* stage_state, int32_t* words, void* stream);
@@ -417,6 +419,125 @@ mxfp8_status mxfp8_publish_gemm_run_noalloc(const mxfp8_gemm_desc* desc, const v
                                             const void* w_scale, const void* x,
                                             const void* x_scale, int32_t m, void* c,
                                             void* mailbox, int32_t* stage_state, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Low-rank adapters beside the projection: every row of a call may name one
+ * adapter i, and its output becomes
+ *
+ *   C[t] = alpha W x[t] + gain[i] B[i] (A[i] x[t]),
+ *
+ * summed in FP32, added to the GEMM's compensated sum and rounded once: what
+ * a weight with the adapter merged into it gives.  x is the MXFP8 row that the
+ * projection reads.
+ * ------------------------------------------------------------------------ */
+#define MXFP8_MAX_ADAPTER_RANK 256
+
+typedef struct mxfp8_adapters {
+  const void* a;        /* device, 16-byte aligned, [count][rank][K] BF16                 */
+  const void* b;        /* device, 16-byte aligned, [count][N][rank8] BF16, rank8 = rank
+                           rounded up to a multiple of 8 (the columns past rank are not
+                           used and may hold anything)                                    */
+  const float* gain;    /* device, [count], or NULL for 1                                 */
+  const int32_t* ranks; /* device, [count] each adapter's own rank (clamped to 0..rank;
+                           its rows of a and columns of b from there on are not used), or
+                           NULL for rank                                                  */
+  int32_t count;        /* adapters, at least 1                                           */
+  int32_t rank;         /* 1..MXFP8_MAX_ADAPTER_RANK                                      */
+} mxfp8_adapters;
+
+/* Workspace bytes of a call with adapters of up to `rank`; 0 for an invalid
+ * shape. */
+size_t mxfp8_adapters_workspace_bytes(int32_t n, int32_t k, int32_t rank);
+
+/* mxfp8_publish_gemm_run_scaled with adapters: which (device int32[m]) names
+ * each row's adapter, -1 for none; another index raises MXFP8_FLAG_BAD_INDEX
+ * in stage_state[3] and counts as none.  workspace: device, 16-byte aligned,
+ * mxfp8_adapters_workspace_bytes(N, K, rank) bytes, written by every call, so
+ * calls that share one must be ordered on one stream.  Nothing is kept of
+ * *adapters beyond the call.  Three kernels, programmatically serialised: the
+ * GEMM's weight stream starts beside the adapters' products.  As after
+ * mxfp8_publish_gemm_run, one mailbox_consume must follow. */
+mxfp8_status mxfp8_publish_gemm_run_adapted(mxfp8_publish_gemm* gemm, const void* x,
+                                            const void* x_scale, int32_t m, const float* alpha,
+                                            const mxfp8_adapters* adapters, const int32_t* which,
+                                            void* workspace, size_t workspace_bytes, void* c,
+                                            void* stream);
+
+/* ------------------------------------------------------------------------
+ * Latent attention in its absorbed form, the step before the projection.  A
+ * token's keys and values of all heads are linear in one latent vector c of
+ * `latent` numbers, beside a rotary key r of MXFP8_LATENT_ROPE numbers shared
+ * by the heads.  Multiplying the key matrix into the query and the value
+ * matrix into the output leaves attention over the latents themselves:
+ *
+ *   q[t][h]   = [ Wq[h] q_nope[t][h], q_rope[t][h] ]         mxfp8_latent_query
+ *   out[t][h] = softmax_p(scale q[t][h] . [c_p, r_p]) c_p    mxfp8_latent_attend
+ *   x[t][h]   = MXFP8(Wv[h] out[t][h])                       mxfp8_latent_values
+ *
+ * and x, x_scale are the projection's activations (K = heads x value).
+ * ------------------------------------------------------------------------ */
+#define MXFP8_LATENT_ROPE 64
+#define MXFP8_MAX_HEADS 256
+#define MXFP8_MAX_REQUESTS 256
+#define MXFP8_MAX_LATENT_ROWS 65535
+
+/* q [rows][heads][latent + 64] BF16 = each head's query in the latent space
+ * (w [heads][latent][nope] BF16 times q_nope [rows][heads][nope] BF16, summed
+ * in FP32, rounded once) with q_rope [rows][heads][64] BF16 behind it.  nope:
+ * a multiple of 32 in 32..512; latent: 256 or 512; all pointers device,
+ * 16-byte aligned.  rows = 0 launches nothing. */
+mxfp8_status mxfp8_latent_query(const void* q_nope, const void* q_rope, const void* w, void* q,
+                                int32_t rows, int32_t heads, int32_t nope, int32_t latent,
+                                void* stream);
+
+/* x [rows][heads x value] E4M3 and x_scale [rows][heads x value / 32] E8M0 =
+ * each head's values (w [heads][value][latent] BF16 times o
+ * [rows][heads][latent] BF16, summed in FP32) in MXFP8: a block of 32 takes
+ * the smallest power of two under which no element passes 448, then rounds to
+ * nearest even (a block of zeros takes 2^0; NaN elements stay NaN and do not
+ * count towards a block's scale).  value: a multiple of 32 in 32..512. */
+mxfp8_status mxfp8_latent_values(const void* o, const void* w, void* x, void* x_scale,
+                                 int32_t rows, int32_t heads, int32_t latent, int32_t value,
+                                 void* stream);
+
+typedef struct mxfp8_latent_desc {
+  int32_t heads;         /* query heads on the one latent: 1..MXFP8_MAX_HEADS              */
+  int32_t latent;        /* 256 or 512                                                     */
+  int32_t rows;          /* query rows of all requests: 0..MXFP8_MAX_LATENT_ROWS           */
+  int32_t requests;      /* 0..MXFP8_MAX_REQUESTS                                          */
+  int32_t page_size;     /* tokens in a page: a multiple of 8                              */
+  int32_t pages;         /* pages in the pool                                              */
+  int32_t table_width;   /* page-table entries of a request                                */
+  float scale;           /* of the scores before the softmax: positive, finite             */
+  int64_t token_stride;  /* elements between tokens of a page: a multiple of 8             */
+  int64_t page_stride;   /* elements between pages: a multiple of 8                        */
+} mxfp8_latent_desc;
+
+/* Workspace bytes of mxfp8_latent_attend; 0 for an unsupported latent. */
+size_t mxfp8_latent_workspace_bytes(int32_t latent);
+
+/* out [rows][heads][latent] BF16 of q [rows][heads][latent + 64] BF16 over
+ * cache [pages][page_size][latent + 64] BF16 (strided; page_table
+ * int32[requests][table_width] names each request's pages in order).  Request
+ * b's query rows are row_begin[b] .. row_begin[b + 1] - 1 (ascending; a row in
+ * no request gives zeros) and its tokens 0 .. lengths[b] - 1, of which the last
+ * T = row_begin[b + 1] - row_begin[b] are the rows' own, the drafts.  Every row sees
+ * the tokens before the drafts; row t sees draft j iff bit j of tree[row_begin[b]
+ * + t] is set (j < 64), or without a tree (NULL) iff j <= t.  A row that sees
+ * nothing gives zeros.  What lies in pages past a request's length, or in
+ * drafts that a row does not see, has no effect on it, NaN included.  A
+ * non-finite number in the latent of a draft makes the rows that see it NaN.
+ * lengths, row_begin and page_table are read on the device; a page outside the
+ * pool (read as zeros), a length past the table (cut) or rows outside q (cut)
+ * raise MXFP8_FLAG_BAD_INDEX in *flags (device int32, may be NULL), and a wait
+ * of the pipeline that runs out raises MXFP8_FLAG_GEMM_TIMEOUT.  workspace:
+ * device, 256-byte aligned; calls that share one must be ordered on one
+ * stream. */
+mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* desc, const void* q, const void* cache,
+                                 const int32_t* page_table, const int32_t* lengths,
+                                 const int32_t* row_begin, const int64_t* tree, void* out,
+                                 void* workspace, size_t workspace_bytes, int32_t* flags,
+                                 void* stream);
 
 /* Text of the calling thread's last error ("" if none). */
 const char* mxfp8_last_error(void);

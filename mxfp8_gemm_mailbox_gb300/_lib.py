@@ -20,10 +20,13 @@ TMEM_LOAD_16X256B = 2
 FLAG_POLL_TIMEOUT = 0x1
 FLAG_GEMM_TIMEOUT = 0x2
 FLAG_BAD_STATE = 0x4
+FLAG_BAD_INDEX = 0x8
 GENERATIONS = 3
 SENTINEL = 0x80000000
 MAX_ROWS = 8
 NOALLOC_SCRATCH_BYTES = 4 << 20
+LATENT_ROPE = 64
+MAX_ADAPTER_RANK = 256
 
 # Every symbol the header declares, with (restype, argtypes).
 _vp = ctypes.c_void_p
@@ -37,6 +40,18 @@ class GemmDesc(ctypes.Structure):
                 ("cta_k", _i32), ("stages", _i32), ("acc_blocks", _i32), ("w_layout", _i32),
                 ("l2_prefetch", _i32), ("pipes", _i32), ("tmem_load", _i32),
                 ("fold", _i32), ("l2_prefetch_early", _i32), ("wait_limit_ms", _i32)]
+
+
+class Adapters(ctypes.Structure):
+    _fields_ = [("a", _vp), ("b", _vp), ("gain", _vp), ("ranks", _vp), ("count", _i32),
+                ("rank", _i32)]
+
+
+class LatentDesc(ctypes.Structure):
+    _fields_ = [("heads", _i32), ("latent", _i32), ("rows", _i32), ("requests", _i32),
+                ("page_size", _i32), ("pages", _i32), ("table_width", _i32),
+                ("scale", ctypes.c_float), ("token_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64)]
 
 
 SIGNATURES = {
@@ -55,6 +70,15 @@ SIGNATURES = {
     "mxfp8_publish_gemm_run": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp]),
     "mxfp8_gemm_run_unfused": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp]),
     "mxfp8_publish_gemm_run_scaled": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _vp]),
+    "mxfp8_adapters_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "mxfp8_publish_gemm_run_adapted": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp,
+                                                      ctypes.POINTER(Adapters), _vp, _vp, _sz,
+                                                      _vp, _vp]),
+    "mxfp8_latent_query": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp]),
+    "mxfp8_latent_values": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp]),
+    "mxfp8_latent_workspace_bytes": (_sz, [_i32]),
+    "mxfp8_latent_attend": (ctypes.c_int, [ctypes.POINTER(LatentDesc), _vp, _vp, _vp, _vp, _vp,
+                                           _vp, _vp, _vp, _sz, _vp, _vp]),
     "mailbox_publish": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp]),
     "mailbox_consume": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _u64, _vp]),
     "mxfp8_mailbox_status": (ctypes.c_int, [_vp, ctypes.POINTER(_i32), _vp]),

@@ -219,6 +219,30 @@ class PublishGemm:
               "mxfp8_publish_gemm_run_scaled")
         return c
 
+    def run_adapted(self, x: torch.Tensor, x_scale: torch.Tensor, adapters: "Adapters",
+                    which: torch.Tensor, alpha: torch.Tensor | None = None,
+                    c: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+        """``run_scaled`` with a low-rank adapter on each row: row t's output
+        gains ``gain[i] B[i] (A[i] x[t])`` for ``i = which[t]`` (int32 [m] on
+        the device, -1 for none) before its one rounding.  An index outside
+        ``-1 .. count - 1`` counts as none and sets FLAG_BAD_INDEX, which
+        ``mailbox.status`` reports."""
+        if alpha is not None and (alpha.dtype != torch.float32 or not alpha.is_cuda):
+            raise TypeError("alpha must be a float32 CUDA tensor")
+        m = self._rows(x, x_scale, c)
+        if adapters.n != self.n or adapters.k != self.k:
+            raise ValueError(f"the adapters are for N={adapters.n}, K={adapters.k}; the "
+                             f"projection has N={self.n}, K={self.k}")
+        if which.dtype != torch.int32 or which.dim() != 1 or which.shape[0] < m:
+            raise ValueError(f"which must be int32 [>= {m}], got {which.dtype} "
+                             f"{tuple(which.shape)}")
+        _on_device(which, "which")
+        check(_lib.load().mxfp8_publish_gemm_run_adapted(
+            self._handle, _ptr(x), _ptr(x_scale), m, _ptr(alpha), ctypes.byref(adapters.desc),
+            _ptr(which), _ptr(adapters.workspace), adapters.workspace.nbytes, _ptr(c),
+            _stream(stream)), "mxfp8_publish_gemm_run_adapted")
+        return c
+
     def run_unfused(self, x: torch.Tensor, x_scale: torch.Tensor, c: torch.Tensor,
                     stream=None) -> torch.Tensor:
         m = self._rows(x, x_scale, c)
@@ -244,6 +268,45 @@ class PublishGemm:
             self.close()
         except Exception:
             pass
+
+
+class Adapters:
+    """Low-rank adapters of one projection: ``a [count][rank][K]`` and
+    ``b [count][N][rank]`` BF16, with an optional FP32 ``gain [count]`` and each
+    adapter's own rank, int32 ``ranks [count]`` (at most ``rank``; what lies
+    past it is not used).  The tensors stay borrowed; ``b`` is copied once, its
+    rows padded, where ``rank`` is not a multiple of 8.  The workspace of the
+    calls lives here, so calls with one object are ordered on one stream."""
+
+    def __init__(self, a: torch.Tensor, b: torch.Tensor, gain: torch.Tensor | None = None,
+                 ranks: torch.Tensor | None = None):
+        if a.dtype != torch.bfloat16 or b.dtype != torch.bfloat16:
+            raise TypeError(f"a and b must be bfloat16, got {a.dtype} and {b.dtype}")
+        if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+            raise ValueError("a must be [count][rank][K] and b [count][N][rank], got "
+                             f"{tuple(a.shape)} and {tuple(b.shape)}")
+        self.count, self.rank, self.k = a.shape
+        self.n = b.shape[1]
+        nbytes = _lib.load().mxfp8_adapters_workspace_bytes(self.n, self.k, self.rank)
+        if nbytes == 0 or self.count == 0:
+            raise ValueError(f"invalid adapters: count={self.count}, rank={self.rank} (at most "
+                             f"{_lib.MAX_ADAPTER_RANK}), N={self.n}, K={self.k}")
+        _on_device(a, "a")
+        _on_device(b, "b")
+        for t, name, dtype in ((gain, "gain", torch.float32), (ranks, "ranks", torch.int32)):
+            if t is not None:
+                if t.dtype != dtype or tuple(t.shape) != (self.count,):
+                    raise ValueError(f"{name} must be {dtype} [{self.count}], got {t.dtype} "
+                                     f"{tuple(t.shape)}")
+                _on_device(t, name)
+        if self.rank % 8:
+            b = torch.nn.functional.pad(b, (0, 8 - self.rank % 8))
+        self.a, self.b, self.gain, self.ranks = a, b, gain, ranks
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=a.device)
+        self.desc = _lib.Adapters(a.data_ptr(), b.data_ptr(),
+                                  gain.data_ptr() if gain is not None else None,
+                                  ranks.data_ptr() if ranks is not None else None,
+                                  self.count, self.rank)
 
 
 class LamportGather:

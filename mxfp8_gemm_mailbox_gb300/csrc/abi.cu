@@ -47,6 +47,10 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace mxfp8 {
+
 mxfp8_status fail(mxfp8_status status, const std::string& message) {
   g_last_error = message;
   return status;
@@ -56,7 +60,23 @@ mxfp8_status cuda_fail(cudaError_t err, const char* what) {
   return fail(MXFP8_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(err));
 }
 
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+EncodeTiled encode_tiled() {
+  static EncodeTiled fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiled>(p);
+  });
+  return fn;
+}
+
+}  // namespace mxfp8
+
+namespace {
 
 constexpr uint64_t kDefaultPollTimeoutNs = 1000000000ull;
 constexpr int kDefaultGemmWaitLimitMs = 2000;
@@ -81,25 +101,6 @@ constexpr int kEarlyCtaPercent = 70;
 // grid never holds columns an earlier one waits for: each CTA allocates before
 // it lets its dependents launch.
 constexpr uint32_t kMaxTmemCols = 256;
-
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static EncodeTiled fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiled>(p);
-  });
-  return fn;
-}
 
 // A 2-D uint8 tensor [outer][inner] (row stride `inner` bytes), read in boxes
 // of box_outer rows x 128 bytes with the 128-byte swizzle; out-of-range
@@ -409,7 +410,8 @@ mxfp8_status check_rows(const mxfp8_publish_gemm* g, int32_t m) {
 }
 
 mxfp8_status run_gemm(mxfp8_publish_gemm* g, const void* x, const void* x_scale, int32_t m,
-                      void* c, void* stream, bool publish, const float* alpha = nullptr) {
+                      void* c, void* stream, bool publish, const float* alpha = nullptr,
+                      const float* addend = nullptr) {
   if (!g) return fail(MXFP8_ERR_INVALID, "gemm handle is NULL");
   mxfp8_status st = check_rows(g, m);
   if (st != MXFP8_OK) return st;
@@ -452,6 +454,7 @@ mxfp8_status run_gemm(mxfp8_publish_gemm* g, const void* x, const void* x_scale,
   p.w_tiled = g->w_tiled;
   p.c = static_cast<uint16_t*>(c);
   p.alpha = alpha;
+  p.addend = addend;
   p.mailbox = g->mailbox;
   p.state = g->state;
   p.wait_limit_ns = static_cast<uint64_t>(g->desc.wait_limit_ms) * 1000000ull;
@@ -649,6 +652,68 @@ mxfp8_status mxfp8_publish_gemm_run_scaled(mxfp8_publish_gemm* gemm, const void*
   return run_gemm(gemm, x, x_scale, m, c, stream, true, alpha);
 }
 
+size_t mxfp8_adapters_workspace_bytes(int32_t n, int32_t k, int32_t rank) {
+  if (n <= 0 || n % kBlockN || k <= 0 || k % 32 || k > 32768 || rank < 1 ||
+      rank > MXFP8_MAX_ADAPTER_RANK)
+    return 0;
+  return (adapter_inner_floats(k, rank) + static_cast<size_t>(MXFP8_MAX_ROWS) * n) * sizeof(float);
+}
+
+mxfp8_status mxfp8_publish_gemm_run_adapted(mxfp8_publish_gemm* gemm, const void* x,
+                                            const void* x_scale, int32_t m, const float* alpha,
+                                            const mxfp8_adapters* adapters, const int32_t* which,
+                                            void* workspace, size_t workspace_bytes, void* c,
+                                            void* stream) {
+  if (!gemm) return fail(MXFP8_ERR_INVALID, "gemm handle is NULL");
+  mxfp8_status st = check_rows(gemm, m);
+  if (st != MXFP8_OK) return st;
+  if (!x || !aligned(x, 16)) return fail(MXFP8_ERR_INVALID, "x must be a 16-byte aligned device pointer");
+  if (!x_scale) return fail(MXFP8_ERR_INVALID, "x_scale is NULL");
+  if (c && !aligned(c, 16)) return fail(MXFP8_ERR_INVALID, "c must be 16-byte aligned");
+  if (alpha && !aligned(alpha, 4)) return fail(MXFP8_ERR_INVALID, "alpha must be 4-byte aligned");
+  if (!adapters) return fail(MXFP8_ERR_INVALID, "adapters is NULL");
+  if (adapters->count < 1) return fail(MXFP8_ERR_INVALID, "adapters.count must be positive");
+  if (adapters->rank < 1 || adapters->rank > MXFP8_MAX_ADAPTER_RANK)
+    return fail(MXFP8_ERR_UNSUPPORTED, "adapters.rank must be in 1.." +
+                                           std::to_string(MXFP8_MAX_ADAPTER_RANK) + ", got " +
+                                           std::to_string(adapters->rank));
+  if (!adapters->a || !aligned(adapters->a, 16) || !adapters->b || !aligned(adapters->b, 16))
+    return fail(MXFP8_ERR_INVALID, "adapters.a and .b must be 16-byte aligned device pointers");
+  if (!aligned(adapters->gain, 4) || !aligned(adapters->ranks, 4))
+    return fail(MXFP8_ERR_INVALID, "adapters.gain and .ranks must be 4-byte aligned");
+  if (!which || !aligned(which, 4))
+    return fail(MXFP8_ERR_INVALID, "which must be a 4-byte aligned device pointer");
+  const size_t need =
+      mxfp8_adapters_workspace_bytes(gemm->desc.n, gemm->desc.k, adapters->rank);
+  if (!workspace || !aligned(workspace, 16) || workspace_bytes < need)
+    return fail(MXFP8_ERR_INVALID, "the workspace must be 16-byte aligned and hold " +
+                                       std::to_string(need) + " bytes");
+  int device = -1;
+  if (cudaGetDevice(&device) != cudaSuccess || device != gemm->device)
+    return fail(MXFP8_ERR_INVALID, "the handle was created on device " +
+                                       std::to_string(gemm->device) +
+                                       ", the current device is " + std::to_string(device));
+  AdapterParams p{};
+  p.m = m;
+  p.n = gemm->desc.n;
+  p.k = gemm->desc.k;
+  p.rank = adapters->rank;
+  p.count = adapters->count;
+  p.x = static_cast<const uint8_t*>(x);
+  p.x_scale = static_cast<const uint8_t*>(x_scale);
+  p.a = static_cast<const uint16_t*>(adapters->a);
+  p.b = static_cast<const uint16_t*>(adapters->b);
+  p.gain = adapters->gain;
+  p.ranks = adapters->ranks;
+  p.which = which;
+  p.inner = static_cast<float*>(workspace);
+  p.delta = p.inner + adapter_inner_floats(p.k, p.rank);
+  p.flags = gemm->state + 3;
+  const cudaError_t e = launch_adapters(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "launching the adapters");
+  return run_gemm(gemm, x, x_scale, m, c, stream, true, alpha, p.delta);
+}
+
 mxfp8_status mxfp8_gemm_run_unfused(mxfp8_publish_gemm* gemm, const void* x, const void* x_scale,
                                     int32_t m, void* c, void* stream) {
   return run_gemm(gemm, x, x_scale, m, c, stream, false);
@@ -779,6 +844,8 @@ mxfp8_status mxfp8_mailbox_status(const int32_t* stage_state, int32_t* words, vo
   if (words[3] & (MXFP8_FLAG_POLL_TIMEOUT | MXFP8_FLAG_GEMM_TIMEOUT))
     return fail(MXFP8_ERR_TIMEOUT, "a device-side wait ran out of time (flags " +
                                        std::to_string(words[3]) + ")");
+  if (words[3] & MXFP8_FLAG_BAD_INDEX)
+    return fail(MXFP8_ERR_INVALID, "an adapter index was outside -1..count-1");
   if ((words[3] & MXFP8_FLAG_BAD_STATE) || words[0] < 0 || words[0] >= MXFP8_MAILBOX_GENERATIONS ||
       words[1] < 0 || words[1] >= MXFP8_MAILBOX_GENERATIONS)
     return fail(MXFP8_ERR_STATE, "the state words hold a generation outside 0..2");

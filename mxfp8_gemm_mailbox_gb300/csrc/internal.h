@@ -4,10 +4,22 @@
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
+#include <string>
 
 #include "mxfp8_mailbox.h"
 
 namespace mxfp8 {
+
+// Set mxfp8_last_error()'s text for the calling thread and return `status`.
+mxfp8_status fail(mxfp8_status status, const std::string& message);
+mxfp8_status cuda_fail(cudaError_t err, const char* what);
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled();  // nullptr when the driver has none
 
 constexpr int kBlockN = 128;      // the MMA's M: output columns per CTA (128 / fold folded)
 constexpr int kRows = 8;          // activation rows per x tile: the MMA's N (8 fold folded)
@@ -79,6 +91,7 @@ struct GemmParams {
   const uint8_t* w_tiled;   // [n/R][k_tiles][16384] shared-memory images of W, or nullptr
   uint16_t* c;              // [m][n] BF16 or nullptr
   const float* alpha;       // global scale of C (device scalar) or nullptr for 1
+  const float* addend;      // [m][n] FP32 added to the scaled sum before its rounding, or nullptr
   uint16_t* mailbox;        // [3][capacity][n] BF16
   int32_t* state;           // int32[4]
   uint64_t wait_limit_ns;
@@ -130,5 +143,44 @@ cudaError_t launch_tagged_consume(const void* pairs, int n, int m, uint32_t tag,
                                   uint64_t timeout_ns, int32_t* flags, cudaStream_t stream);
 cudaError_t launch_mailbox_publish(uint16_t* mailbox, int32_t* state, int capacity, int n, int m,
                                    const uint16_t* c, cudaStream_t stream);
+
+// Low-rank adapters: x MXFP8 [m][k], one adapter index per row (-1: none).
+struct AdapterParams {
+  int32_t m, n, k, rank, count;  // b's rows hold rank rounded up to 8 values
+  const uint8_t* x;
+  const uint8_t* x_scale;
+  const uint16_t* a;       // [count][rank][k] BF16
+  const uint16_t* b;       // [count][n][rank8] BF16
+  const float* gain;       // [count] or nullptr for 1
+  const int32_t* ranks;    // [count] or nullptr for `rank`
+  const int32_t* which;    // [m]
+  float* inner;            // FP32 workspace: the products with A
+  float* delta;            // [m][n] FP32
+  int32_t* flags;          // MXFP8_FLAG_BAD_INDEX for an index outside -1..count-1
+};
+size_t adapter_inner_floats(int k, int rank);
+cudaError_t launch_adapters(const AdapterParams& p, cudaStream_t stream);
+
+// Latent attention (latent_project.cu, latent_attend.cu).
+cudaError_t launch_latent_query(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w,
+                                uint16_t* q, int rows, int heads, int nope, int latent,
+                                cudaStream_t stream);
+cudaError_t launch_latent_values(const uint16_t* o, const uint16_t* w, uint8_t* x,
+                                 uint8_t* x_scale, int rows, int heads, int latent, int value,
+                                 cudaStream_t stream);
+struct LatentParams {
+  int32_t heads, rows, requests, page_size, pages, table_width;
+  int64_t token_stride, page_stride;  // elements
+  float scale_log2;                   // softmax scale x log2(e)
+  const uint16_t* q;         // [rows][heads][latent + 64]
+  const uint16_t* cache;     // [pages][page_size][latent + 64], strided
+  const int32_t* table;      // [requests][table_width]
+  const int32_t* lengths;    // [requests]
+  const int32_t* row_begin;  // [requests + 1]
+  const int64_t* tree;       // [rows] bit masks over the request's drafts, or nullptr for a chain
+  uint16_t* out;             // [rows][heads][latent]
+  int32_t* flags;            // or nullptr
+};
+cudaError_t launch_latent_attend(const LatentParams& p, int latent, cudaStream_t stream);
 
 }  // namespace mxfp8

@@ -129,6 +129,18 @@ __device__ __forceinline__ void two_sum_add(float& hi, float& lo, float v) {
   lo = __fadd_rn(lo, err);
 }
 
+// The same for an FP32 addend that may be infinite or NaN, or push the sum
+// past FP32: such a sum has no rounding error to keep.
+__device__ __forceinline__ void add_addend(float& hi, float& lo, float v) {
+  const float s = __fadd_rn(hi, v);
+  if (isfinite(s)) {
+    two_sum_add(hi, lo, v);
+  } else {
+    hi = s;
+    lo = 0.0f;
+  }
+}
+
 // BF16 bits of the exact value hi + lo, rounded once to nearest with ties to
 // even.  TwoSum gives s = fl(hi + lo) and the exact remainder e with
 // |e| <= ulp(s) / 2.  A BF16 midpoint has low 16 bits 0x8000 in FP32, and
@@ -832,6 +844,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
           sl = __fmaf_rn(a, sl, pe);
           sh = ph;
         }
+        const int t = t_local + static_cast<int>(split) * kShard;
+        if (p.addend != nullptr && t < p.m)
+          add_addend(sh, sl,
+                     p.addend[static_cast<size_t>(t) * p.n + tile * kTileRows + col]);
         ctile[t_local * kTileRows + col] = bf16_bits_from_pair(sh, sl);
       };
       if constexpr (S == 1) {
@@ -990,6 +1006,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
           const float pe = __fmaf_rn(a, own_hi[jj], -ph);
           own_lo[jj] = __fmaf_rn(a, own_lo[jj], pe);
           own_hi[jj] = ph;
+        }
+      }
+      // The rows' low-rank adapters (a BF16 result of the whole sum: the addend
+      // joins the compensated pair before its one rounding).
+      if (p.addend != nullptr) {
+#pragma unroll
+        for (int jj = 0; jj < kShard; ++jj) {
+          const int t = static_cast<int>(split) * kShard + jj;
+          if (t < p.m)
+            add_addend(own_hi[jj], own_lo[jj],
+                       p.addend[static_cast<size_t>(t) * p.n + tile * kTileRows + col]);
         }
       }
 

@@ -1,0 +1,184 @@
+"""Low-rank adapters beside the publishing projection, against float64.
+
+Tolerance: C is rounded once (2^-9 of itself; doubled, since the sum that is
+rounded carries FP32 errors that can move it across a midpoint), and both
+adapter sums are FP32: 2^-18 of the sum of magnitudes covers 16384 products
+summed in any order at their typical growth."""
+import pytest
+import torch
+
+import mxfp8_gemm_mailbox_gb300 as mx
+from tests.latent_cases import normal
+
+pytestmark = pytest.mark.gpu
+
+
+def codes(seed, rows, k, low=-4, high=2):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(rows, k, generator=gen, device="cuda").to(torch.float8_e4m3fn)
+    e = torch.randint(low + 127, high + 128, (rows, k // 32), generator=gen, device="cuda")
+    return x.view(torch.uint8), e.to(torch.uint8)
+
+
+def dense(x, scale):
+    return (x.view(torch.float8_e4m3fn).float().double()
+            * torch.exp2(scale.double() - 127).repeat_interleave(32, 1))
+
+
+class Projection:
+    def __init__(self, n, k, seed=0, **tactic):
+        self.n, self.k = n, k
+        self.w, self.ws = codes(seed + 100, n, k)
+        self.mailbox = mx.Mailbox(8, n)
+        self.gemm = mx.PublishGemm(self.w, self.ws, self.mailbox, **tactic)
+
+    def expected(self, x, xs, a, b, gain, ranks, which, alpha=1.0):
+        xd, wd = dense(x, xs), dense(self.w, self.ws)
+        want, size = alpha * (xd @ wd.t()), abs(alpha) * (xd.abs() @ wd.abs().t())
+        for t, i in enumerate(which):
+            if 0 <= i < a.shape[0]:
+                r = a.shape[1] if ranks is None else min(max(ranks[i], 0), a.shape[1])
+                g = 1.0 if gain is None else float(gain[i])
+                want[t] += g * (b[i, :, :r].double() @ (a[i, :r].double() @ xd[t]))
+                size[t] += abs(g) * (b[i, :, :r].double().abs()
+                                     @ (a[i, :r].double().abs() @ xd[t].abs()))
+        return want, size
+
+
+def close(got, want, size):
+    assert torch.isfinite(got).all()
+    err = (got.double() - want).abs()
+    tol = 2.0 ** -8 * want.abs() + 2.0 ** -18 * size
+    worst = (err / tol).max().item()
+    assert worst <= 1.0, f"{worst:.2f} x the tolerance"
+
+
+def check(p, m, count, rank, which, gain=True, ranks=None, alpha=None, seed=1):
+    x, xs = codes(seed, m, p.k)
+    a, b = normal(seed + 1, count, rank, p.k, std=p.k ** -0.5), normal(seed + 2, count, p.n, rank)
+    g = torch.linspace(-0.5, 1.5, count, device="cuda") if gain else None
+    r = None if ranks is None else torch.tensor(ranks, dtype=torch.int32, device="cuda")
+    al = None if alpha is None else torch.tensor([alpha], device="cuda")
+    adapters = mx.Adapters(a, b, g, r)
+    w = torch.tensor(which, dtype=torch.int32, device="cuda")
+    c = torch.full((m, p.n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    p.gemm.run_adapted(x, xs, adapters, w, alpha=al, c=c)
+    out = p.mailbox.consume(m)
+    close(out, *p.expected(x, xs, a, b, g, ranks, which, alpha or 1.0))
+    assert torch.equal(out, c + 0.0)  # the mailbox clears negative zero
+    st, words = p.mailbox.status()
+    assert st == mx.OK and words[3] == 0
+    return x, xs, out
+
+
+@pytest.mark.parametrize("rank", [1, 2, 7, 8, 16, 24, 33, 64, 128, 255, 256])
+def test_ranks(cuda, rank):
+    check(Projection(256, 512), 3, 2, rank, [0, 1, 0])
+
+
+@pytest.mark.parametrize("m", range(1, 9))
+def test_rows_each_with_its_own_adapter(cuda, m):
+    check(Projection(384, 1024), m, m, 16, list(range(m)))
+
+
+@pytest.mark.parametrize("k", [32, 96, 256, 1056, 4096, 8224])
+def test_ragged_k(cuda, k):
+    check(Projection(256, k), 5, 3, 20, [2, 0, -1, 1, 2])
+
+
+@pytest.mark.parametrize("tactic", [dict(split_k=1, fold=1), dict(split_k=2), dict(split_k=4),
+                                    dict(split_k=8), dict(split_k=1, fold=2),
+                                    dict(split_k=2, fold=4), dict(split_k=4, fold=2),
+                                    dict(fold=8, split_k=1), dict(cta_k=256, split_k=2),
+                                    dict(tmem_load=2, fold=1)])
+def test_every_epilogue(cuda, tactic):
+    check(Projection(512, 2048, **tactic), 8, 4, 32, [0, 1, 2, 3, -1, 3, 2, 0], alpha=0.75)
+
+
+def test_workload_shapes(cuda):
+    check(Projection(7168, 16384, split_k=4), 8, 8, 64, list(range(8)))
+    check(Projection(4096, 4096, split_k=1), 1, 2, 16, [1])
+
+
+def test_own_ranks_and_unused_parts(cuda):
+    p = Projection(256, 512)
+    x, xs = codes(1, 4, 512)
+    a, b = normal(2, 3, 20, 512, std=0.05), normal(3, 3, 256, 20)
+    ranks = [20, 5, 0]
+    for i, r in enumerate(ranks):
+        a[i, r:] = float("nan")
+        b[i, :, r:] = float("inf")
+    r = torch.tensor(ranks, dtype=torch.int32, device="cuda")
+    which = [1, 0, 2, 1]
+    p.gemm.run_adapted(x, xs, mx.Adapters(a, b, None, r),
+                       torch.tensor(which, dtype=torch.int32, device="cuda"))
+    out = p.mailbox.consume(4)
+    close(out, *p.expected(x, xs, a, b, None, ranks, which))
+
+
+def test_rows_without_an_adapter_keep_the_projections_bits(cuda):
+    p = Projection(512, 4096)
+    x, xs, out = check(p, 8, 2, 8, [-1, 0, -1, 1, -1, -1, 0, -1])
+    p.gemm.run(x, xs)
+    plain = p.mailbox.consume(8)
+    for t in (0, 2, 4, 5, 7):
+        assert torch.equal(out[t], plain[t])
+    assert not torch.equal(out[1], plain[1])
+
+
+def test_an_index_out_of_range_counts_as_none_and_raises_the_flag(cuda):
+    p = Projection(256, 512)
+    x, xs = codes(1, 3, 512)
+    a, b = normal(2, 2, 8, 512), normal(3, 2, 256, 8)
+    p.gemm.run(x, xs)
+    plain = p.mailbox.consume(3)
+    p.gemm.run_adapted(x, xs, mx.Adapters(a, b),
+                       torch.tensor([2, -5, 1 << 30], dtype=torch.int32, device="cuda"))
+    assert torch.equal(p.mailbox.consume(3), plain)
+    st, words = p.mailbox.status()
+    assert st == mx.ERR_INVALID and words[3] == mx.FLAG_BAD_INDEX
+
+
+def test_non_finite_adapters_reach_their_rows_alone(cuda):
+    p = Projection(256, 512)
+    x, xs = codes(1, 3, 512)
+    a, b = normal(2, 2, 8, 512).abs(), normal(3, 2, 256, 8)
+    b[0, 7, 3] = float("inf")
+    b[0, 9, 3] = float("nan")
+    p.gemm.run_adapted(x, xs, mx.Adapters(a, b),
+                       torch.tensor([1, 0, -1], dtype=torch.int32, device="cuda"))
+    out = p.mailbox.consume(3)
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2]).all()
+    assert torch.isinf(out[1, 7]) and torch.isnan(out[1, 9])
+    keep = torch.ones(256, dtype=torch.bool)
+    keep[[7, 9]] = False
+    assert torch.isfinite(out[1, keep.cuda()]).all()
+
+
+def test_same_bits_again_and_from_a_graph(cuda):
+    p = Projection(1024, 8192, split_k=2)
+    x, xs = codes(1, 8, 8192)
+    adapters = mx.Adapters(normal(2, 4, 40, 8192, std=0.01), normal(3, 4, 1024, 40))
+    which = torch.tensor([0, 1, 2, 3, 3, 2, -1, 0], dtype=torch.int32, device="cuda")
+    p.gemm.run_adapted(x, xs, adapters, which)
+    first = p.mailbox.consume(8)
+    out = torch.empty_like(first)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        p.gemm.run_adapted(x, xs, adapters, which)
+        p.mailbox.consume(8, out)
+    for _ in range(5):
+        out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    # the rows' adapters are read on the device
+    which.fill_(-1)
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    p.gemm.run(x, xs)
+    assert torch.equal(out, p.mailbox.consume(8))

@@ -1,0 +1,342 @@
+"""Latent attention on the GPU against float64.
+
+Tolerances.  attend: the softmax weights are rounded to BF16 (2^-9 relative,
+so 2^-9 of the weights' sum over |c|) and the result once more (2^-9 of
+itself); FP32 sums, the exponential and the normaliser add a few 2^-20, which
+the factor 2 covers: 2^-8 (|y| + sum p |c|).  query: one BF16 rounding, 2^-9
+|y|, and FP32 sums of up to 512 products, 512 x 2^-24 of the absolute sum.
+values: E4M3's half step, 2^-4 of an element or 2^-10 of its block's scale."""
+import pytest
+import torch
+
+import mxfp8_gemm_mailbox_gb300 as mx
+from tests.latent_cases import ROPE, Paged, masks_tensor, normal
+
+pytestmark = pytest.mark.gpu
+SCALE = 192 ** -0.5
+
+
+def close(got, want, weight):
+    assert got.shape == want.shape and got.dtype == torch.bfloat16
+    assert torch.isfinite(got).all()
+    err = (got.double() - want).abs()
+    tol = 2.0 ** -8 * (want.abs() + weight) + 1e-30
+    worst = (err / tol).max().item() if err.numel() else 0.0
+    assert worst <= 1.0, f"{worst:.2f} x the tolerance"
+
+
+def attend(cuda, paged, heads, masks=None, seed=5, scale=SCALE, q=None, cache=None, at=None):
+    at = at or mx.LatentAttention(heads, paged.latent)
+    q = normal(seed, paged.rows, heads, paged.latent + ROPE) if q is None else q
+    tree = None if masks is None else masks_tensor(masks)
+    got = at.run(q, paged.cache if cache is None else cache, paged.table, paged.lengths,
+                 paged.begin, scale, tree=tree)
+    assert at.status() == 0
+    close(got, *paged.expected(q, scale, masks))
+    return got
+
+
+@pytest.mark.parametrize("latent", [256, 512])
+@pytest.mark.parametrize("context", [0, 1, 62, 63, 64, 65, 127, 128, 700])
+def test_context_lengths_around_a_tile(cuda, latent, context):
+    attend(cuda, Paged([context], [1], latent, 64), 16)
+
+
+@pytest.mark.parametrize("heads", [1, 5, 31, 32, 33, 64, 100, 128, 130, 256])
+def test_head_counts(cuda, heads):
+    attend(cuda, Paged([300, 70], [2, 1], 512, 32), heads)
+
+
+@pytest.mark.parametrize("page", [8, 16, 24, 32, 40, 64, 96, 128, 1024])
+@pytest.mark.parametrize("latent", [256, 512])
+def test_page_sizes(cuda, page, latent):
+    attend(cuda, Paged([517, 90, 8], [3, 1, 2], latent, page, seed=page), 24)
+
+
+@pytest.mark.parametrize("drafts", [1, 2, 7, 8, 33, 64])
+def test_chains_and_trees(cuda, drafts):
+    paged = Paged([201, 0, 64], [drafts, drafts, max(1, drafts - 1)], 512, 32, seed=drafts)
+    attend(cuda, paged, 20)
+    attend(cuda, paged, 20, masks=paged.random_tree(drafts))
+
+
+def test_a_long_chain_without_a_tree(cuda):
+    attend(cuda, Paged([100], [150], 256, 16), 6)
+
+
+def test_long_contexts_split_over_the_gpu(cuda):
+    attend(cuda, Paged([20011], [1], 512, 64), 128)
+    attend(cuda, Paged([9000, 17, 4000], [2, 4, 2], 512, 128, seed=1), 64)
+
+
+def test_many_requests_some_without_rows(cuda):
+    contexts = [(37 * b) % 211 for b in range(256)]
+    drafts = [(b * 5) % 3 for b in range(256)]
+    attend(cuda, Paged(contexts, drafts, 256, 8), 3)
+
+
+def test_rows_that_see_nothing_give_zeros(cuda):
+    paged = Paged([0, 5], [3, 2], 512, 16)
+    masks = [0, 0b010, 0, 0, 0b10]
+    got = attend(cuda, paged, 40, masks=masks)
+    assert (got[0] == 0).all() and (got[2] == 0).all()
+    assert (got[3] != 0).any()
+    # a length of zero, with rows: nothing to see either
+    at = mx.LatentAttention(40)
+    empty = torch.zeros_like(paged.lengths)
+    out = at.run(normal(1, 5, 40, 576), paged.cache, paged.table, empty, paged.begin, SCALE)
+    assert (out == 0).all() and at.status() == 0
+
+
+def test_rows_outside_every_request_give_zeros(cuda):
+    paged = Paged([30], [2], 256, 16)
+    at = mx.LatentAttention(8, 256)
+    q = normal(2, 5, 8, 320)
+    out = at.run(q, paged.cache, paged.table, paged.lengths, paged.begin, SCALE)
+    want, weight = paged.expected(q[:2], SCALE)
+    close(out[:2], want, weight)
+    assert (out[2:] == 0).all()
+
+
+def test_no_rows_launch_nothing(cuda):
+    paged = Paged([30], [0], 256, 16)
+    at = mx.LatentAttention(8, 256)
+    out = at.run(normal(2, 0, 8, 320), paged.cache, paged.table, paged.lengths, paged.begin, SCALE)
+    assert out.shape == (0, 8, 256)
+    assert mx.latent_query(normal(1, 0, 4, 64), normal(1, 0, 4, 64), normal(1, 4, 256, 64)).shape \
+        == (0, 4, 320)
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -3e38])
+def test_poison_past_the_length_has_no_effect(cuda, poison):
+    for context in (0, 40, 63, 64, 100):
+        attend(cuda, Paged([context, 3], [1, 2], 512, 32, poison=poison), 16)
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("at_column", [0, 200, 300, 511, 512, 575])
+def test_poison_in_a_draft_reaches_only_the_rows_that_see_it(cuda, value, at_column):
+    paged = Paged([61], [6], 512, 16)
+    bad = 2
+    masks = [0b1, 0b11, 0b111, 0b1001, 0b11001, 0b100111]
+    q = normal(9, 6, 40, 576)
+    want, weight = paged.expected(q, SCALE, masks)
+    position = 61 + bad
+    page = int(paged.table[0, position // 16])
+    paged.cache[page, position % 16, at_column] = value
+    at = mx.LatentAttention(40)
+    got = at.run(q, paged.cache, paged.table, paged.lengths, paged.begin, SCALE,
+                 tree=masks_tensor(masks))
+    for row, mask in enumerate(masks):
+        if not mask >> bad & 1:
+            close(got[row], want[row], weight[row])
+        elif at_column < 512:
+            assert torch.isnan(got[row]).all()
+
+
+def test_growing_scores_move_the_running_maximum(cuda):
+    # Keys along q with growing length: every tile holds a new maximum, far past the last.
+    def keys(b, n, width):
+        base = normal(3, 1, width)
+        return (base * torch.linspace(0.01, 3.0, n, device="cuda")[:, None]).to(torch.bfloat16)
+
+    paged = Paged([640], [1], 512, 64, keys=keys)
+    q = (normal(3, 1, 576) * torch.linspace(0.5, 2, 128, device="cuda")[:, None]).to(torch.bfloat16)
+    attend(cuda, paged, 128, q=q[None], scale=1.0)
+    attend(cuda, paged, 128, q=-q[None], scale=1.0)  # falling ones: the first tile holds it
+
+
+def test_scores_of_very_negative_and_equal_values(cuda):
+    def keys(b, n, width):
+        return torch.full((n, width), -8.0, dtype=torch.bfloat16, device="cuda")
+
+    paged = Paged([130], [2], 256, 32, keys=keys)
+    q = torch.full((2, 16, 320), 64.0, dtype=torch.bfloat16, device="cuda")
+    got = attend(cuda, paged, 16, q=q, scale=4.0)
+    assert (got == -8.0).all()
+
+
+def test_strided_pool(cuda):
+    paged = Paged([300], [2], 512, 16)
+    pool = torch.full((paged.cache.shape[0], 3, 16, 584), float("nan"), dtype=torch.bfloat16,
+                      device="cuda")
+    pool[:, 1, :, :576] = paged.cache
+    attend(cuda, paged, 48, cache=pool[:, 1, :, :576])
+
+
+def test_offsets_past_32_bits(cuda):
+    # 2^32 elements before the pages in use.
+    paged = Paged([400], [2], 512, 64, spare=0)
+    first = (1 << 32) // (64 * 576) + 1
+    pool = torch.empty((first + paged.cache.shape[0], 64, 576), dtype=torch.bfloat16, device="cuda")
+    pool[first:] = paged.cache
+    paged.table += first
+    attend(cuda, paged, 16, cache=pool)
+
+
+def test_same_bits_again_on_another_stream_and_from_a_graph(cuda):
+    paged = Paged([5000, 300], [3, 2], 512, 64)
+    at = mx.LatentAttention(128)
+    q = normal(4, 5, 128, 576)
+    args = (q, paged.cache, paged.table, paged.lengths, paged.begin, SCALE)
+    first = at.run(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        second = at.run(*args)
+    third = at.run(*args, out=torch.full_like(first, float("nan")), stream=side)
+    side.synchronize()
+    assert torch.equal(first, second) and torch.equal(first, third)
+    out = torch.empty_like(first)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            at.run(*args, out=out)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+    # lengths are read on the device: the same graph serves a shorter cache
+    paged.lengths.copy_(torch.tensor([1003, 17], dtype=torch.int32))
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    paged.contexts = [1000, 15]
+    paged.tokens = [paged.tokens[0][:1003], paged.tokens[1][:17]]
+    close(out, *paged.expected(q, SCALE))
+    assert at.status() == 0
+
+
+def test_indexes_out_of_range_raise_the_flag(cuda):
+    paged = Paged([100], [2], 512, 32)
+    q = normal(4, 2, 16, 576)
+
+    def run(table=None, lengths=None, begin=None):
+        at = mx.LatentAttention(16)
+        out = at.run(q, paged.cache, paged.table if table is None else table,
+                     paged.lengths if lengths is None else lengths,
+                     paged.begin if begin is None else begin, SCALE)
+        return out, at.status()
+
+    assert run()[1] == 0
+    for page in (-1, paged.cache.shape[0], 1 << 30):
+        table = paged.table.clone()
+        table[0, 1] = page
+        out, flags = run(table=table)
+        assert flags == mx.FLAG_BAD_INDEX and torch.isfinite(out).all()
+    long = torch.full_like(paged.lengths, 10 ** 9)
+    # cut at the table's end: the last slots hold poison there, so only the flag is checked
+    assert run(lengths=long)[1] & mx.FLAG_BAD_INDEX
+    begin = paged.begin.clone()
+    begin[1] = 40
+    assert run(begin=begin)[1] & mx.FLAG_BAD_INDEX
+
+
+@pytest.mark.parametrize("rows,heads,nope,latent", [
+    (1, 1, 32, 256), (1, 16, 128, 512), (3, 7, 96, 512), (8, 128, 128, 512), (9, 5, 192, 256),
+    (40, 3, 64, 512), (2, 4, 512, 512)])
+def test_query(cuda, rows, heads, nope, latent):
+    q, rope = normal(1, rows, heads, nope), normal(2, rows, heads, ROPE)
+    w = normal(3, heads, latent, nope)
+    got = mx.latent_query(q, rope, w)
+    want = torch.einsum("thi,hoi->tho", q.double(), w.double())
+    size = torch.einsum("thi,hoi->tho", q.double().abs(), w.double().abs())
+    assert got.shape == (rows, heads, latent + ROPE)
+    err = (got[..., :latent].double() - want).abs()
+    assert (err <= 2.0 ** -9 * want.abs() + 512 * 2.0 ** -24 * size).all()
+    assert torch.equal(got[..., latent:], rope)
+
+
+@pytest.mark.parametrize("rows,heads,value,latent", [
+    (1, 1, 32, 256), (1, 32, 128, 512), (3, 7, 96, 512), (8, 128, 128, 512), (9, 5, 64, 256),
+    (40, 3, 160, 512), (2, 4, 512, 512)])
+def test_values(cuda, rows, heads, value, latent):
+    o, w = normal(1, rows, heads, latent), normal(3, heads, value, latent, std=0.1)
+    x, scale = mx.latent_values(o, w)
+    y = torch.einsum("thi,hoi->tho", o.double(), w.double()).reshape(rows, -1, 32)
+    size = torch.einsum("thi,hoi->tho", o.double().abs(), w.double().abs()).reshape(rows, -1, 32)
+    top = y.abs().amax(-1)
+    s = torch.exp2(scale.view(torch.uint8).double() - 127)
+    slack = 512 * 2.0 ** -24 * size.amax(-1)
+    assert (top <= 448 * s + slack).all(), "an element passes 448"
+    assert (top >= 224 * s - slack).all(), "the scale is not the smallest"
+    v = x.float().double().reshape(rows, -1, 32) * s[..., None]
+    err = (v - y).abs()
+    tol = torch.maximum(2.0 ** -4 * y.abs(), 2.0 ** -10 * s[..., None]) + 512 * 2.0 ** -24 * size
+    assert (err <= tol).all()
+
+
+def test_values_of_zeros_extremes_and_nan(cuda):
+    w = torch.zeros((2, 64, 256), dtype=torch.bfloat16, device="cuda")
+    w[:, torch.arange(64), torch.arange(64)] = 1.0  # y = o's first 64 numbers
+    o = torch.zeros((5, 2, 256), dtype=torch.bfloat16, device="cuda")
+    o[0, 0, 0], o[0, 0, 1] = 448.0, -1.0
+    o[0, 1, 40] = 449.0 * 2  # past 448 x 2^0 ... takes the next power
+    o[1, 0, 3], o[1, 0, 4] = float("nan"), 2.0
+    o[2, 0, 0] = 2.0 ** -126
+    o[3, 0, 0] = 3.0e38
+    x, scale = mx.latent_values(o, w)
+    codes = scale.view(torch.uint8)
+    v = x.float()
+    assert codes[4].eq(127).all() and v[4].eq(0).all()
+    assert codes[0, 0] == 127 and v[0, 0] == 448 and v[0, 1] == -1
+    assert codes[0, 3] == 129 and v[0, 64 + 40] == 224
+    assert torch.isnan(v[1, 3]) and v[1, 4] == 256 and codes[1, 0] == 120
+    assert codes[2, 0] == 0 and v[2, 0] > 0
+    assert codes[3, 0] == 127 + 127 - 8 + 1 and v[3, 0] == 224
+
+
+def test_the_whole_step_feeds_the_projection(cuda):
+    """query, attend, values, projection with adapters, consumer, in one graph,
+    against float64 of the rounded intermediates."""
+    heads, value, nope, latent, n, rows = 16, 128, 64, 512, 256, 4
+    k = heads * value
+    paged = Paged([90, 300], [3, 1], latent, 16)
+    masks = paged.random_tree(1)
+    wq, wv = normal(1, heads, latent, nope, std=0.1), normal(2, heads, value, latent, std=0.05)
+    q_nope, q_rope = normal(3, rows, heads, nope), normal(4, rows, heads, ROPE)
+    w = torch.randn(n, k, device="cuda").to(torch.float8_e4m3fn).view(torch.uint8)
+    ws = torch.randint(120, 130, (n, k // 32), dtype=torch.uint8, device="cuda")
+    mailbox = mx.Mailbox(8, n)
+    gemm = mx.PublishGemm(w, ws, mailbox)
+    a, b = normal(5, 2, 12, k, std=0.02), normal(6, 2, n, 12)
+    adapters = mx.Adapters(a, b)
+    which = torch.tensor([1, -1, 0, 1], dtype=torch.int32, device="cuda")
+    at = mx.LatentAttention(heads, latent)
+    out = torch.empty((rows, n), dtype=torch.bfloat16, device="cuda")
+    tree = masks_tensor(masks)
+
+    def step():
+        q = mx.latent_query(q_nope, q_rope, wq)
+        o = at.run(q, paged.cache, paged.table, paged.lengths, paged.begin, SCALE, tree=tree)
+        x, xs = mx.latent_values(o, wv)
+        gemm.run_adapted(x, xs, adapters, which)
+        mailbox.consume(rows, out)
+        return q, o, x, xs
+
+    q, o, x, xs = step()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    eager = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, eager)
+    close(o, *paged.expected(q, SCALE, masks))
+    dense = lambda c, s: (c.view(torch.float8_e4m3fn).float().double()  # noqa: E731
+                          * torch.exp2(s.view(torch.uint8).double() - 127).repeat_interleave(32, 1))
+    xd = dense(x, xs)
+    want = xd @ dense(w, ws).t()
+    size = xd.abs() @ dense(w, ws).abs().t()
+    for t, i in enumerate([1, -1, 0, 1]):
+        if i >= 0:
+            want[t] += b[i].double() @ (a[i].double() @ xd[t])
+            size[t] += b[i].double().abs() @ (a[i].double().abs() @ xd[t].abs())
+    err = (eager.double() - want).abs()
+    assert (err <= 2.0 ** -8 * want.abs() + 2.0 ** -18 * size).all()
+    assert mailbox.status()[0] == mx.OK
