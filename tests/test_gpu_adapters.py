@@ -1,8 +1,7 @@
 """Low-rank adapters beside the publishing projection, against float64.
 
-Tolerance: C is rounded once (2^-9 of itself; doubled, since the sum that is
-rounded carries FP32 errors that can move it across a midpoint), and both
-adapter sums are FP32: 2^-18 of the sum of magnitudes covers 16384 products
+Tolerance: C is rounded once (2^-8 of itself at most), and both adapter sums
+are FP32: 2^-18 of the sum of magnitudes covers 16384 products
 summed in any order at their typical growth."""
 import pytest
 import torch
