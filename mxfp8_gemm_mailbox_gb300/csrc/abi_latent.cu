@@ -88,7 +88,7 @@ mxfp8_status mxfp8_latent_values(const void* o, const void* w, void* x, void* x_
 
 size_t mxfp8_latent_workspace_bytes(int32_t latent) {
   if (latent != 256 && latent != 512) return 0;
-  return 256;
+  return latent_workspace_bytes(latent);
 }
 
 mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* d, const void* q, const void* cache,
@@ -149,7 +149,7 @@ mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* d, const void* q, cons
   p.tree = tree;
   p.out = static_cast<uint16_t*>(out);
   p.flags = flags;
-  const cudaError_t e = launch_latent_attend(p, d->latent, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_latent_attend(p, d->latent, workspace, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the latent attention");
   return MXFP8_OK;
 }

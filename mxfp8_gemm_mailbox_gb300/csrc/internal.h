@@ -181,6 +181,8 @@ struct LatentParams {
   uint16_t* out;             // [rows][heads][latent]
   int32_t* flags;            // or nullptr
 };
-cudaError_t launch_latent_attend(const LatentParams& p, int latent, cudaStream_t stream);
+size_t latent_workspace_bytes(int latent);
+cudaError_t launch_latent_attend(const LatentParams& p, int latent, void* workspace,
+                                 cudaStream_t stream);
 
 }  // namespace mxfp8

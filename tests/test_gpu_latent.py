@@ -275,7 +275,8 @@ def test_values_of_zeros_extremes_and_nan(cuda):
     w[:, torch.arange(64), torch.arange(64)] = 1.0  # y = o's first 64 numbers
     o = torch.zeros((5, 2, 256), dtype=torch.bfloat16, device="cuda")
     o[0, 0, 0], o[0, 0, 1] = 448.0, -1.0
-    o[0, 1, 40] = 449.0 * 2  # past 448 x 2^0 ... takes the next power
+    o[0, 1, 40] = 898.0  # 896 in BF16: 448 x 2 exactly
+    o[0, 0, 40] = 900.0  # past it: the next power, 225 rounded to 224
     o[1, 0, 3], o[1, 0, 4] = float("nan"), 2.0
     o[2, 0, 0] = 2.0 ** -126
     o[3, 0, 0] = 3.0e38
@@ -284,7 +285,8 @@ def test_values_of_zeros_extremes_and_nan(cuda):
     v = x.float()
     assert codes[4].eq(127).all() and v[4].eq(0).all()
     assert codes[0, 0] == 127 and v[0, 0] == 448 and v[0, 1] == -1
-    assert codes[0, 3] == 129 and v[0, 64 + 40] == 224
+    assert codes[0, 3] == 128 and v[0, 64 + 40] == 448
+    assert codes[0, 1] == 129 and v[0, 40] == 224
     assert torch.isnan(v[1, 3]) and v[1, 4] == 256 and codes[1, 0] == 120
     assert codes[2, 0] == 0 and v[2, 0] > 0
     assert codes[3, 0] == 127 + 127 - 8 + 1 and v[3, 0] == 224
