@@ -34,8 +34,11 @@
 //   1      MMA issuer: scores of tile j + 1, then outputs of tile j;
 //   2      mender of the tiles that reach the drafts or the length: zeroes the
 //          tokens past the length and drafts that are not finite;
-//   4-11   softmax: thread = row (tensor-memory lane), two warps a row, 32 of
-//          the 64 tokens each.
+//   4-19   softmax, two groups of eight that take the tiles in turn, so one
+//          group's exchange and exponentials run under the other's products:
+//          thread = row (tensor-memory lane), two warps a row, 32 of the 64
+//          tokens each.  The reference of a row's exponentials passes from
+//          tile to tile, and so between the groups, through shared memory.
 //
 // Precision: scores, maxima, sums, outputs and partials FP32; the weights e_p
 // are rounded to BF16, the MMA's operand type (2^-8 relative at most), and the
@@ -54,7 +57,7 @@ namespace {
 constexpr int kRope = 64;
 constexpr int kTokens = 64;     // tokens in a tile
 constexpr int kTileRows = 128;  // rows in a tile
-constexpr int kAttendThreads = 384;
+constexpr int kAttendThreads = 640;
 constexpr int kSoftmaxWarp = 4;
 constexpr int kMaxRequests = MXFP8_MAX_REQUESTS;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
@@ -86,18 +89,19 @@ struct Shape {
 struct Misc {
   uint64_t kv_full[6], kv_empty[6], kv_ready[6];
   uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t recv_full[2][8], credit[2][8];
-  uint64_t pair[4];  // the two warps of a lane quarter
+  uint64_t recv_full[2][8], credit[2][8];  // [group][warp of the group]
+  uint64_t decided[2][4];                  // [tile parity][lane quarter]
   uint64_t q_ready, drained;
   uint64_t bad[6];  // non-finite drafts of a stage's tile, one bit a token
   uint32_t tmem;
   int32_t abort;
-  float top[2][2][kTileRows];  // [exchange parity][column half][row]
-  float total[2][kTileRows];
+  float top[2][2][kTileRows];       // [group][token half][row]
+  float reference[2][kTileRows];    // [tile parity][row]
+  float total[2][2][kTileRows];     // [group][token half][row]
   int64_t first[kMaxRequests + 1];  // tiles before each request
   int32_t length[kMaxRequests];
-  int32_t begin[kMaxRequests];
-  int32_t drafts[kMaxRequests];
+  uint16_t begin[kMaxRequests];     // rows are at most MXFP8_MAX_LATENT_ROWS
+  uint16_t drafts[kMaxRequests];
 };
 
 // The device-side inputs of one request, cut to what the buffers hold.
@@ -176,25 +180,32 @@ __device__ __forceinline__ bool special(const Segment& s, int kv) {
   return (kv + 1) * kTokens > s.context;
 }
 
+// Bounded waits of a warp's converged lanes.  One that runs out sets `abort`,
+// after which every wait of the CTA returns at once: the roles then run their
+// loops out on whatever the buffers hold, so that no barrier is left short of
+// an arrival, and the kernel ends with its flag set.
 struct Waiter {
   int32_t* abort;
   int32_t* flags;
-  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    return slow(bar, parity, false);
+  __device__ __forceinline__ bool operator()(const uint64_t& b, uint32_t parity) const {
+    const uint32_t bar = ptx::smem_addr(&b);
+    return __all_sync(~0u, ptx::mbar_try_wait(bar, parity & 1u)) || slow(bar, parity & 1u, false);
   }
-  __device__ __forceinline__ bool cluster(uint32_t bar, uint32_t parity) const {
-    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-    return slow(bar, parity, true);
+  // With acquire over the cluster, for what a peer CTA signals.
+  __device__ __forceinline__ bool cluster(const uint64_t& b, uint32_t parity) const {
+    const uint32_t bar = ptx::smem_addr(&b);
+    return __all_sync(~0u, ptx::mbar_try_wait_cluster(bar, parity & 1u)) ||
+           slow(bar, parity & 1u, true);
   }
   __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity, bool wide) const {
     const uint64_t start = ptx::globaltimer();
     for (;;) {
+      if (__any_sync(~0u, *reinterpret_cast<volatile int32_t*>(abort) != 0)) return false;
       for (int i = 0; i < 32; ++i)
-        if (wide ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity))
+        if (__all_sync(~0u, wide ? ptx::mbar_try_wait_cluster(bar, parity)
+                                 : ptx::mbar_try_wait(bar, parity)))
           return true;
-      if (*reinterpret_cast<volatile int32_t*>(abort)) return false;
-      if (ptx::globaltimer() - start > kWaitLimitNs) {
+      if (__any_sync(~0u, ptx::globaltimer() - start > kWaitLimitNs)) {
         *reinterpret_cast<volatile int32_t*>(abort) = 1;
         raise(flags, MXFP8_FLAG_GEMM_TIMEOUT);
         return false;
@@ -241,13 +252,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       ptx::mbar_init(bar(m.s_full[i]), 1);
       ptx::mbar_init(bar(m.p_full[i]), 8);
       ptx::mbar_init(bar(m.pv_done[i]), 1);
+      for (int w = 0; w < 4; ++w) ptx::mbar_init(bar(m.decided[i][w]), 2);
       for (int w = 0; w < 8; ++w) {
         ptx::mbar_init(bar(m.recv_full[i][w]), 1);
         ptx::mbar_init(bar(m.credit[i][w]), 1);
       }
     }
-    for (int i = 0; i < 4; ++i) ptx::mbar_init(bar(m.pair[i]), 2);
-    ptx::mbar_init(bar(m.q_ready), 8);
+    ptx::mbar_init(bar(m.q_ready), 16);
     ptx::mbar_init(bar(m.drained), 1);
     m.abort = 0;
     ptx::fence_mbarrier_init();
@@ -274,8 +285,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         const Request r = load_request(p, b);
         if (r.cut && blockIdx.x == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
         m.length[b] = r.length;
-        m.begin[b] = r.begin;
-        m.drafts[b] = r.drafts;
+        m.begin[b] = static_cast<uint16_t>(r.begin);
+        m.drafts[b] = static_cast<uint16_t>(r.drafts);
         tiles = static_cast<int64_t>(row_tiles(r.drafts, p.heads)) * token_tiles(r.length);
       }
       for (int o = 1; o < 32; o *= 2) {
@@ -292,20 +303,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   const int64_t run = run_length(all, ap.clusters);
   const int64_t run_begin = min(all, cluster * run);
   Walk walk{run_begin, min(all, run_begin + run), 0};
-  Segment seg;
+  Segment seg{};
   const Waiter wait{&m.abort, p.flags};
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
+    // A lane a box (one thread's copies are served one after another); the
+    // page of a lane's box is looked up one tile ahead.
+    constexpr int kItems = (8 * (L::kAtoms + 1) + 31) / 32;  // of a lane, boxes of 8 tokens
+    auto page_of = [&](int kv, int i) {
+      const int token = kv * kTokens + i / (L::kAtoms + 1) * ap.box;
+      if (token >= seg.length) return 0;
+      const int page = p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
+      if (page >= 0 && page < p.pages) return page;
+      raise(p.flags, MXFP8_FLAG_BAD_INDEX);
+      return p.pages;  // past the tensor: the copy fills zeros
+    };
     const int boxes_per_tile = kTokens / ap.box;
     int g = 0;
     bool ok = true;
     while (ok && next_segment(m, p, walk, seg)) {
+      int page[kItems];
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int i = lane + 32 * k;
+        page[k] = i < boxes_per_tile * (L::kAtoms + 1) ? page_of(seg.kv0, i) : 0;
+      }
       for (int kv = seg.kv0; kv < seg.kv1; ++kv, ++g) {
         const int stage = g % kStages;
-        const uint32_t use = static_cast<uint32_t>(g / kStages) & 1u;
-        if (g >= kStages) ok = wait(bar(m.kv_empty[stage]), use ^ 1u);
-        ok = __all_sync(~0u, ok);
+        const uint32_t use = static_cast<uint32_t>(g / kStages);
+        int next[kItems];
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+          const int i = lane + 32 * k;
+          next[k] = kv + 1 < seg.kv1 && i < boxes_per_tile * (L::kAtoms + 1) ? page_of(kv + 1, i)
+                                                                             : 0;
+        }
+        if (g >= kStages) ok = wait(m.kv_empty[stage], use - 1);
         if (!ok) break;
         const int boxes = min(boxes_per_tile, (seg.length - kv * kTokens + ap.box - 1) / ap.box);
         const uint32_t full = bar(m.kv_full[stage]);
@@ -313,26 +347,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * ap.box) *
                                                (L::kHalf * 2u + 64u));
         __syncwarp();
-        // A lane a box: one thread's copies are served one after another.
-        for (int i = lane; i < boxes * (L::kAtoms + 1); i += 32) {
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+          const int i = lane + 32 * k;
+          if (i >= boxes * (L::kAtoms + 1)) continue;
           const int box = i / (L::kAtoms + 1), atom = i % (L::kAtoms + 1);
-          const int token = kv * kTokens + box * ap.box;
-          int page = p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
-          if (page < 0 || page >= p.pages) {
-            raise(p.flags, MXFP8_FLAG_BAD_INDEX);
-            page = p.pages;  // past the tensor: the copy fills zeros
-          }
+          const int at = (kv * kTokens + box * ap.box) % p.page_size;
           const uint32_t dst = sbase + stage * L::kStageBytes;
           if (atom < L::kAtoms)
             ptx::tma_load_3d(dst + atom * kAtomBytes + box * ap.box * 128, &tmap_c,
-                             static_cast<int>(rank) * L::kHalf + atom * 64, token % p.page_size,
-                             page, full, ptx::policy_evict_last());
+                             static_cast<int>(rank) * L::kHalf + atom * 64, at, page[k], full,
+                             ptx::policy_evict_last());
           else
             ptx::tma_load_3d(dst + L::kAtoms * kAtomBytes + box * ap.box * 64, &tmap_r,
-                             static_cast<int>(rank) * 32, token % p.page_size, page, full,
+                             static_cast<int>(rank) * 32, at, page[k], full,
                              ptx::policy_evict_last());
         }
         __syncwarp();
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) page[k] = next[k];
       }
     }
     // Copies in flight land before the CTA leaves (they have, unless a wait
@@ -342,19 +375,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                      kWaitLimitNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kScores = ptx::idesc_bf16(kTokens, false);
-      constexpr uint32_t kOutputs = ptx::idesc_bf16(L::kHalf, true);
-      const uint32_t q_rope = sbase + L::kQRope;
-      int g = 0, segments = 0;
-      bool ok = true;
-      auto scores = [&](int j, const Segment& s, int kv) {
-        const int stage = j % kStages;
-        const uint32_t use = static_cast<uint32_t>(j / kStages) & 1u;
-        if (!wait(bar(special(s, kv) ? m.kv_ready[stage] : m.kv_full[stage]), use)) return false;
-        ptx::tc_fence_after();
-        const uint32_t kvb = sbase + stage * L::kStageBytes;
-        const uint32_t d = tmem + L::kS + (j & 1) * kTokens;
+    // The warp stays converged and one elected lane issues: 32 clocks a
+    // 128 x 64 x 16 product with the queries in tensor memory, the rate of the
+    // tensor core; from a branch on the lane number it took 46.
+    constexpr uint32_t kScores = ptx::idesc_bf16(kTokens, false);
+    constexpr uint32_t kOutputs = ptx::idesc_bf16(L::kHalf, true);
+    const uint32_t q_rope = sbase + L::kQRope;
+    int g = 0;
+    uint32_t segments = 0;
+    bool ok = true;
+    auto scores = [&](int j, int kv) {
+      const int stage = j % kStages;
+      if (!wait(special(seg, kv) ? m.kv_ready[stage] : m.kv_full[stage], j / kStages)) return false;
+      ptx::tc_fence_after();
+      const uint32_t kvb = sbase + stage * L::kStageBytes;
+      const uint32_t d = tmem + L::kS + (j & 1) * kTokens;
+      const uint32_t done = bar(m.s_full[j & 1]);
+      if (ptx::elect_one()) {
 #pragma unroll
         for (int k = 0; k < L::kHalf / 16; ++k)
           ptx::mma_f16_ts(d, tmem + L::kQ + k * 8,
@@ -365,35 +402,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           ptx::mma_f16_ss(d, ptx::desc_kmajor_sw64(q_rope + k * 32),
                           ptx::desc_kmajor_sw64(kvb + L::kAtoms * kAtomBytes + k * 32), kScores,
                           1u);
-        ptx::mma_commit(bar(m.s_full[j & 1]));
-        return true;
-      };
-      while (ok && next_segment(m, p, walk, seg)) {
-        ok = wait(bar(m.q_ready), static_cast<uint32_t>(segments++) & 1u);
+        ptx::mma_commit(done);
+      }
+      __syncwarp();
+      return true;
+    };
+    while (ok && next_segment(m, p, walk, seg)) {
+      ok = wait(m.q_ready, segments++);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      ok = scores(g, seg.kv0);
+      if (ok && seg.kv0 + 1 < seg.kv1) ok = scores(g + 1, seg.kv0 + 1);
+      for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g) {
+        ok = wait(m.p_full[g & 1], g >> 1);
         if (!ok) break;
         ptx::tc_fence_after();
-        ok = scores(g, seg, seg.kv0);
-        for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g) {
-          if (kv + 1 < seg.kv1) ok = scores(g + 1, seg, kv + 1);
-          if (!ok || !wait(bar(m.p_full[g & 1]), static_cast<uint32_t>(g >> 1) & 1u)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
-          const int stage = g % kStages;
-          const uint32_t kvb = sbase + stage * L::kStageBytes;
+        const int stage = g % kStages;
+        const uint32_t kvb = sbase + stage * L::kStageBytes;
+        const uint32_t a = tmem + L::kS + (g & 1) * kTokens;
+        const uint32_t add = kv > seg.kv0;
+        const uint32_t empty = bar(m.kv_empty[stage]), done = bar(m.pv_done[g & 1]);
+        if (ptx::elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTokens / 16; ++k)
-            ptx::mma_f16_ts(tmem, tmem + L::kS + (g & 1) * kTokens + k * 8,
-                            ptx::desc_mnmajor_sw128(kvb + k * 2048, kAtomBytes), kOutputs,
-                            kv > seg.kv0 || k > 0);
-          ptx::mma_commit(bar(m.kv_empty[stage]));
-          ptx::mma_commit(bar(m.pv_done[g & 1]));
+            ptx::mma_f16_ts(tmem, a + k * 8, ptx::desc_mnmajor_sw128(kvb + k * 2048, kAtomBytes),
+                            kOutputs, k > 0 ? 1u : add);
+          ptx::mma_commit(empty);
+          ptx::mma_commit(done);
         }
+        __syncwarp();
+        // Its weights read, the score buffer takes the tile after the next.
+        if (kv + 2 < seg.kv1) ok = scores(g + 2, kv + 2);
       }
-      ptx::mma_commit(bar(m.drained));  // nothing runs on when tensor memory is freed
-      ptx::mbar_wait(bar(m.drained), 0, kWaitLimitNs);
     }
+    // Nothing runs on when tensor memory is freed.
+    if (ptx::elect_one()) ptx::mma_commit(bar(m.drained));
+    __syncwarp();
+    ptx::mbar_wait(bar(m.drained), 0, kWaitLimitNs);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- mender
     int g = 0;
@@ -401,8 +446,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     while (ok && next_segment(m, p, walk, seg)) {
       for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g) {
         const int stage = g % kStages;
-        ok = wait(bar(m.kv_full[stage]), static_cast<uint32_t>(g / kStages) & 1u);
-        ok = __all_sync(~0u, ok);
+        ok = wait(m.kv_full[stage], g / kStages);
         if (!ok) break;
         if (special(seg, kv)) {
           uint8_t* kvp = smem + stage * L::kStageBytes;
@@ -445,30 +489,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     }
   } else if (warp >= kSoftmaxWarp) {
     // --------------------------------------------------------------- softmax
-    const int sw = warp - kSoftmaxWarp;
+    const int group = (warp - kSoftmaxWarp) / 8;  // takes the tiles of this parity
+    const int sw = (warp - kSoftmaxWarp) % 8;
     const int quarter = warp & 3;  // the 32 tensor-memory lanes this warp reaches
     const int half = sw >> 2;      // its 32 of a tile's 64 tokens
+    const int part = group * 2 + half;  // its quarter of the columns, in and out
     const int row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t score = lanes + L::kS + group * kTokens;
     const uint32_t peer = rank ^ 1u;
-    const uint32_t recv_offset = L::kRecv + static_cast<uint32_t>(sw) * 4096u + lane * 16u;
-    // Waits give up together: the lanes of a warp never part.
-    auto warp_wait = [&](const uint64_t& b, uint32_t parity) {
-      return __all_sync(~0u, wait(bar(b), parity & 1u));
-    };
-    auto warp_wait_cluster = [&](const uint64_t& b, uint32_t parity) {
-      return __all_sync(~0u, wait.cluster(bar(b), parity & 1u));
-    };
-    uint32_t meetings = 0;
-    auto meet = [&] {  // the two warps of this quarter
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(m.pair[quarter]));
-      return warp_wait(m.pair[quarter], meetings++);
-    };
-    int g = 0;         // token tiles so far
-    int exchange = 0;  // of which this warp exchanged
-    bool ok = true;
-    while (ok && next_segment(m, p, walk, seg)) {
+    const uint32_t recv_offset = L::kRecv + group * kRecvBytes + static_cast<uint32_t>(sw) * 4096u;
+    const uint32_t recv_bar = bar(m.recv_full[group][sw]);
+    const uint32_t to = ptx::map_to_rank(sbase + recv_offset + lane * 16u, peer);
+    const uint32_t to_bar = ptx::map_to_rank(recv_bar, peer);
+    const uint32_t credit_bar = ptx::map_to_rank(bar(m.credit[group][sw]), peer);
+    const float4* recv = reinterpret_cast<const float4*>(smem + recv_offset) + lane;
+    constexpr int kPart = L::kHalf / 4;
+    uint32_t exchanges = 0;  // tiles this warp exchanged
+    uint32_t decisions = 0;  // tiles this quarter's rows took part in, of both groups
+    int g = 0;               // token tiles before the segment
+    for (uint32_t segments = 0; next_segment(m, p, walk, seg);
+         g += seg.kv1 - seg.kv0, ++segments) {
       const size_t q_row = static_cast<size_t>(seg.begin) * p.heads + seg.row0 + row;
       const bool mine = row < seg.valid;
       const bool active = quarter * 32 < seg.valid;  // of the warp
@@ -477,96 +518,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       {
         const uint4* src = reinterpret_cast<const uint4*>(p.q + q_row * kWidth);
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        uint32_t v[kPart / 2];
 #pragma unroll
-        for (int part = 0; part < L::kHalf / 128; ++part) {
-          uint32_t v[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 x = mine ? src[(rank * L::kHalf + half * (L::kHalf / 2)) / 8 + part * 8 + i]
-                                 : zero;
-            v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
-          }
-          ptx::tmem_st_32x32b_x32(lanes + L::kQ + half * (L::kHalf / 4) + part * 32, v);
+        for (int i = 0; i < kPart / 8; ++i) {
+          const uint4 x = mine ? src[(rank * L::kHalf + part * kPart) / 8 + i] : zero;
+          v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int chunk = half * 2 + i;
-          const uint4 x = mine ? src[kLatent / 8 + rank * 4 + chunk] : zero;
-          *reinterpret_cast<uint4*>(smem + L::kQRope + row * 64 +
-                                    ((chunk ^ ((row >> 1) & 3)) * 16)) = x;
-        }
+        if constexpr (kPart == 64)
+          ptx::tmem_st_32x32b_x32(lanes + L::kQ + part * (kPart / 2), v);
+        else
+          ptx::tmem_st_32x32b_x16(lanes + L::kQ + part * (kPart / 2), v);
+        const uint4 x = mine ? src[kLatent / 8 + rank * 4 + part] : zero;
+        *reinterpret_cast<uint4*>(smem + L::kQRope + row * 64 + ((part ^ ((row >> 1) & 3)) * 16)) =
+            x;
         ptx::tmem_wait_st();
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(m.q_ready));
       }
+      const int tiles = seg.kv1 - seg.kv0;
+      if (!active) {
+        for (int i = (g & 1) != group; i < tiles; i += 2) {
+          wait(m.s_full[group], (g + i) >> 1);
+          if (lane == 0) ptx::mbar_arrive(bar(m.p_full[group]));
+        }
+        // Not on to the next segment's queries before every warp's of this one.
+        wait(m.q_ready, segments);
+        continue;
+      }
       // What this row sees of the drafts.
       const int t = (seg.row0 + row) / p.heads;
       const uint64_t tree =
           p.tree != nullptr && mine ? static_cast<uint64_t>(p.tree[seg.begin + t]) : 0;
-      float reference = -INFINITY, total = 0.0f;
+      float reference = -INFINITY, total = 0.0f;  // of this warp's tiles
 
-      float next[32];
-      // This CTA's partial scores of tile j, sent to the peer.
-      auto take = [&](int j, int kv) {
-        if (!warp_wait(m.s_full[j & 1], j >> 1)) return false;
+      for (int i = (g & 1) != group; i < tiles; i += 2, ++exchanges) {
+        const int kv = seg.kv0 + i;
+        const uint32_t decision = decisions + i;
+        // This CTA's partial scores, sent to the peer and joined with its own.
+        wait(m.s_full[group], (g + i) >> 1);
         ptx::tc_fence_after();
         uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(lanes + L::kS + (j & 1) * kTokens + half * 32, v);
+        ptx::tmem_ld_32x32b_x32(score + half * 32, v);
         ptx::tmem_wait_ld();
         if (special(seg, kv)) {
-          const int stage = j % kStages;
-          if (!warp_wait(m.kv_ready[stage], j / kStages)) return false;
+          const int stage = (g + i) % kStages;
+          wait(m.kv_ready[stage], (g + i) / kStages);
           const uint32_t bad = static_cast<uint32_t>(m.bad[stage] >> (32 * half));
           if (bad != 0u)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (bad >> i & 1u) v[i] = 0x7FC00000u;
+            for (int c = 0; c < 32; ++c)
+              if (bad >> c & 1u) v[c] = 0x7FC00000u;
         }
-        const int e = exchange + (j - g);
-        if (e >= 2 && !warp_wait_cluster(m.credit[e & 1][sw], (e - 2) >> 1)) return false;
-        const uint32_t full = bar(m.recv_full[e & 1][sw]);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(full, 4096);
+        if (exchanges > 0) wait.cluster(m.credit[group][sw], exchanges - 1);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(recv_bar, 4096);
         __syncwarp();
-        const uint32_t to =
-            ptx::map_to_rank(sbase + recv_offset + (e & 1) * kRecvBytes, peer);
-        const uint32_t to_bar = ptx::map_to_rank(full, peer);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int c = 0; c < 8; ++c)
           ptx::st_async_remote_v4(
-              to + i * 512, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]), to_bar);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) next[i] = __uint_as_float(v[i]);
-        return true;
-      };
-
-      if (!active) {
-        for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g) {
-          ok = warp_wait(m.s_full[g & 1], g >> 1);
-          if (ok && lane == 0) ptx::mbar_arrive(bar(m.p_full[g & 1]));
-        }
-        continue;
-      }
-      ok = take(g, seg.kv0);
-      for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g, ++exchange) {
+              to + c * 512, make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]), to_bar);
+        wait.cluster(m.recv_full[group][sw], exchanges);
         float z[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) z[i] = next[i];
-        if (kv + 1 < seg.kv1) ok = take(g + 1, kv + 1);
-        if (!ok) break;
-        const int e = exchange & 1;
-        ok = warp_wait_cluster(m.recv_full[e][sw], exchange >> 1);
-        if (!ok) break;
-        const float4* recv =
-            reinterpret_cast<const float4*>(smem + recv_offset + e * kRecvBytes);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 v = recv[i * 32];
-          z[4 * i] += v.x, z[4 * i + 1] += v.y, z[4 * i + 2] += v.z, z[4 * i + 3] += v.w;
+        for (int c = 0; c < 8; ++c) {
+          const float4 x = recv[c * 32];
+          z[4 * c] = __uint_as_float(v[4 * c]) + x.x;
+          z[4 * c + 1] = __uint_as_float(v[4 * c + 1]) + x.y;
+          z[4 * c + 2] = __uint_as_float(v[4 * c + 2]) + x.z;
+          z[4 * c + 3] = __uint_as_float(v[4 * c + 3]) + x.w;
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_remote(ptx::map_to_rank(bar(m.credit[e][sw]), peer));
         if (special(seg, kv)) {
           const int at = kv * kTokens;
           uint64_t sees;
@@ -580,77 +601,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           sees &= low_ones(seg.length - at);
           const uint32_t bits = static_cast<uint32_t>(sees >> (32 * half));
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (!(bits >> i & 1u)) z[i] = -INFINITY;
+          for (int c = 0; c < 32; ++c)
+            if (!(bits >> c & 1u)) z[c] = -INFINITY;
         }
         float top = z[0];
 #pragma unroll
-        for (int i = 1; i < 32; ++i) top = fmaxf(top, z[i]);
-        m.top[e][half][row] = top;
-        ok = meet();
-        if (!ok) break;
-        top = fmaxf(top, m.top[e][half ^ 1][row]) * p.scale_log2;
-        const bool move = top > reference + kLazy;
-        if (__any_sync(~0u, move)) {
-          const float to = move ? top : reference;
-          const float f = move ? exp2_approx(reference - to) : 1.0f;
-          total *= f;
-          reference = to;
-          if (kv > seg.kv0) {
-            // The outputs so far, once the previous tile's have been added.
-            ok = warp_wait(m.pv_done[(g - 1) & 1], (g - 1) >> 1);
-            if (!ok) break;
-            ptx::tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < L::kHalf / 2; c += 32) {
-              uint32_t v[32];
-              ptx::tmem_ld_32x32b_x32(lanes + half * (L::kHalf / 2) + c, v);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-              ptx::tmem_st_32x32b_x32(lanes + half * (L::kHalf / 2) + c, v);
-            }
-          }
+        for (int c = 1; c < 32; ++c) top = fmaxf(top, z[c]);
+        m.top[group][half][row] = top;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + group * 4 + quarter) : "memory");
+        top = fmaxf(top, m.top[group][half ^ 1][row]) * p.scale_log2;
+
+        // The reference after the tile before this one, moved if the new
+        // maximum passes it by more than kLazy.
+        float now = -INFINITY;
+        if (i > 0) {
+          wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
+          now = m.reference[(decision - 1) & 1][row];
         }
-        const float base = reference == -INFINITY ? 0.0f : reference;
+        const bool move = top > now + kLazy;
+        if (i > 0 && __any_sync(~0u, move)) {
+          // The outputs so far, once the previous tile's have been added.
+          const float f = move ? exp2_approx(now - top) : 1.0f;
+          wait(m.pv_done[group ^ 1], (g + i - 1) >> 1);
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < L::kHalf / 2; c += 32) {
+            ptx::tmem_ld_32x32b_x32(lanes + half * (L::kHalf / 2) + c, v);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * f);
+            ptx::tmem_st_32x32b_x32(lanes + half * (L::kHalf / 2) + c, v);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+        }
+        if (move) now = top;
+        if (half == 0) m.reference[decision & 1][row] = now;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
+        if (now != reference) {
+          total *= exp2_approx(reference - now);
+          reference = now;
+        }
+        const float base = now == -INFINITY ? 0.0f : now;
         uint32_t w[16];
         float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          w[i] = pack_bf16(exp2_approx(fmaf(z[2 * i], p.scale_log2, -base)),
-                           exp2_approx(fmaf(z[2 * i + 1], p.scale_log2, -base)));
-          sum0 += __uint_as_float(w[i] << 16);
-          sum1 += __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int c = 0; c < 16; ++c) {
+          w[c] = pack_bf16(exp2_approx(fmaf(z[2 * c], p.scale_log2, -base)),
+                           exp2_approx(fmaf(z[2 * c + 1], p.scale_log2, -base)));
+          sum0 += __uint_as_float(w[c] << 16);
+          sum1 += __uint_as_float(w[c] & 0xFFFF0000u);
         }
         total += sum0 + sum1;
-        ptx::tmem_st_32x32b_x16(lanes + L::kS + (g & 1) * kTokens + half * 16, w);
+        ptx::tmem_st_32x32b_x16(score + half * 16, w);
         ptx::tmem_wait_st();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(m.p_full[g & 1]));
+        if (lane == 0) {
+          ptx::mbar_arrive(bar(m.p_full[group]));
+          // The peer may overwrite the receive buffer.  (Last: a release over
+          // the cluster waits for this thread's own remote stores.)
+          ptx::mbar_arrive_remote(credit_bar);
+        }
       }
-      if (!ok) break;
 
-      // The row tile's outputs.
-      ok = warp_wait(m.pv_done[(g - 1) & 1], (g - 1) >> 1);
-      if (!ok) break;
+      // The row tile's outputs: the last tile's have been added, and the sums of
+      // the row's four warps join under the last reference.
+      const uint32_t last = decisions + tiles - 1;
+      decisions += tiles;
+      // In this order: once the last tile is decided its outputs' barrier is at
+      // most one phase ahead of a look at its parity.
+      wait(m.decided[last & 1][quarter], last >> 1);
+      wait(m.pv_done[(g + tiles - 1) & 1], (g + tiles - 1) >> 1);
       ptx::tc_fence_after();
-      m.total[half][row] = total;
-      ok = meet();
-      if (!ok) break;
-      // (Written again only after the next tile's meeting, past this read.)
-      total = m.total[0][row] + m.total[1][row];
+      const float now = m.reference[last & 1][row];
+      if (now != reference) total *= exp2_approx(reference - now);
+      m.total[group][half][row] = total;
+      asm volatile("bar.sync %0, 128;" ::"r"(9 + quarter) : "memory");
+      total = (m.total[0][0][row] + m.total[0][1][row]) + (m.total[1][0][row] + m.total[1][1][row]);
       const bool whole = seg.kv0 == 0 && seg.kv1 == seg.kv_tiles;
-      const int column0 = static_cast<int>(rank) * L::kHalf + half * (L::kHalf / 2);
-      const int slot =
-          2 * cluster + (walk.at - (seg.kv1 - seg.kv0) == run_begin ? 0 : 1);
+      const int column0 = static_cast<int>(rank) * L::kHalf + part * kPart;
+      const int slot = 2 * cluster + (walk.at - tiles == run_begin ? 0 : 1);
       const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
-      if (!whole && rank == 0 && half == 0 && mine)
-        ap.stats[slot * kTileRows + row] = make_float2(reference, total);
+      if (!whole && rank == 0 && part == 0 && mine)
+        ap.stats[slot * kTileRows + row] = make_float2(now, total);
 #pragma unroll 1
-      for (int c = 0; c < L::kHalf / 2; c += 32) {
+      for (int c = 0; c < kPart; c += 32) {
         uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(lanes + half * (L::kHalf / 2) + c, v);
+        ptx::tmem_ld_32x32b_x32(lanes + part * kPart + c, v);
         ptx::tmem_wait_ld();
         if (!mine) continue;
         if (whole) {
@@ -665,12 +704,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             out[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
         } else {
-          float4* part = ap.partial +
-                         (static_cast<size_t>(slot) * (kLatent / 4) + (column0 + c) / 4) * kTileRows +
-                         row;
+          float4* to_part = ap.partial +
+                            (static_cast<size_t>(slot) * (kLatent / 4) + (column0 + c) / 4) *
+                                kTileRows +
+                            row;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            part[i * kTileRows] =
+            to_part[i * kTileRows] =
                 make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
         }
@@ -767,6 +807,8 @@ constexpr int kMaxClusters = 80;
 
 template <int kLatent>
 constexpr uint32_t smem_bytes() {
+  static_assert(MXFP8_MAX_LATENT_ROWS <= 65535, "row numbers fit 16 bits");
+  static_assert(Shape<kLatent>::kMisc + sizeof(Misc) + 1024 <= 232448, "shared memory of a CTA");
   return Shape<kLatent>::kMisc + sizeof(Misc) + 1024;
 }
 

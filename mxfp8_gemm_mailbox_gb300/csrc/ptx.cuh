@@ -258,6 +258,16 @@ __device__ __forceinline__ uint64_t desc_rows16(uint32_t saddr) {
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
+// True in one lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 // BF16 MMA (kind::f16), D[tmem] (+)= A B^T, one elected thread; A in shared
 // memory (`a_desc`) or in tensor memory (lane = row, a 32-bit column = two
 // consecutive K elements).
