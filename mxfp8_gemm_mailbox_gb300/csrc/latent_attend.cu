@@ -18,29 +18,36 @@
 // MMA's M.  128 rows x 512 FP32 outputs would take all of an SM's tensor
 // memory, so a cluster of two CTAs shares a tile: CTA r holds columns
 // [r latent/2, (r+1) latent/2) of the latent (and half of the rotary key) of
-// every token, as key and as value.  A token crosses from L2 once per cluster
-// and each CTA multiplies only its own columns: its scores are partial sums,
-// exchanged in FP32 through distributed shared memory and added (the same two
-// numbers in both CTAs, so both derive the same softmax), then multiplied into
-// the CTA's own output columns.
+// every token, as key and as value, so a token crosses from L2 once per
+// cluster.  Per tile of 64 tokens a CTA
+//   1. multiplies its columns: partial scores of all 64 tokens;
+//   2. sends the peer its partials of the peer's 32 tokens (FP32, distributed
+//      shared memory) and adds the peer's partials of its own 32;
+//   3. exponentiates its 32 and sends the peer their weights (BF16), straight
+//      into the peer's MMA operand;
+//   4. multiplies the weights of all 64 into its own output columns.
+// The two halves exchange their maxima in a row tile's first token tile, whose
+// common maximum becomes the row's reference (the exponent subtracted from its
+// scores).  Later each half moves the reference it knows by whole steps alone,
+// and the two agree on the larger afterwards: weights formed under different
+// ones differ by a power of two, so bringing them together rounds nothing.
 //
-// Work: the (request, row tile, 64-token tile) triples form one list, cut into
-// equal runs, one a cluster, so ragged lengths balance by themselves.  A row
-// tile cut between clusters leaves FP32 partial outputs with their maxima and
-// sums, which a second kernel joins in a fixed order.
+// Work.  The row tiles' token tiles are dealt to the clusters in runs: whole
+// pieces of one row tile each where that costs little more than an even deal,
+// else equal runs of the whole list.  A row tile cut between clusters leaves
+// FP32 partial outputs with their references and sums, which a second kernel
+// joins in a fixed order.
 //
 // Warps of a CTA:
-//   0      producer: TMA boxes of a token tile into a ring, one lane a box;
-//   1      MMA issuer: scores of tile j + 1, then outputs of tile j;
+//   0      producer: TMA boxes of a token tile into a ring, a lane a box;
+//   1      MMA issuer;
 //   2      mender of the tiles that reach the drafts or the length: zeroes the
 //          tokens past the length and drafts that are not finite;
-//   4-19   softmax, two groups of eight that take the tiles in turn, so one
-//          group's exchange and exponentials run under the other's products:
-//          thread = row (tensor-memory lane), two warps a row, 32 of the 64
-//          tokens each.  The reference of a row's exponentials passes from
-//          tile to tile, and so between the groups, through shared memory.
+//   3      loads a row tile's queries;
+//   4-11   softmax, two groups of four that take the token tiles in turn, so
+//          one group's exchanges run under the other's: thread = row.
 //
-// Precision: scores, maxima, sums, outputs and partials FP32; the weights e_p
+// Precision: scores, references, sums, outputs and partials FP32; the weights
 // are rounded to BF16, the MMA's operand type (2^-8 relative at most), and the
 // normaliser sums the rounded ones, so the weights that are applied sum to 1.
 #include <cuda_bf16.h>
@@ -57,18 +64,25 @@ namespace {
 constexpr int kRope = 64;
 constexpr int kTokens = 64;     // tokens in a tile
 constexpr int kTileRows = 128;  // rows in a tile
-constexpr int kAttendThreads = 640;
+constexpr int kSmallBox = 8;    // tokens of a box in a tile that reaches drafts or length
+constexpr int kAttendThreads = 384;
 constexpr int kSoftmaxWarp = 4;
 constexpr int kMaxRequests = MXFP8_MAX_REQUESTS;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // A new maximum moves the reference of a row's exponentials only when it
-// passes it by this many powers of two: the weights then stay below 2^8, far
+// passes it by this many powers of two: the weights then stay below 2^9, far
 // inside FP32 and BF16, and the outputs in tensor memory are seldom rescaled.
 constexpr float kLazy = 8.0f;
+// Pieces of one row tile a cluster may be this many token tiles longer than an
+// even deal's runs: about what a second row tile in a run costs.
+constexpr int kPieceSlack = 5;
+constexpr int kMinRun = 2;
 constexpr uint32_t kAtomBytes = kTokens * 128;  // 64 tokens x 64 columns
 constexpr uint32_t kRopeBytes = kTokens * 64;   // 64 tokens x 32 rotary columns
+constexpr uint32_t kQAtomBytes = kTileRows * 128;
 constexpr uint32_t kQRopeBytes = kTileRows * 64;
-constexpr uint32_t kRecvBytes = kTileRows * kTokens * 4;
+constexpr uint32_t kRecvBytes = kTileRows * 32 * 4;  // partial scores from the peer
+constexpr uint32_t kPBytes = kTileRows * 128;        // weights, 64 BF16 a row
 
 template <int kLatent>
 struct Shape {
@@ -77,30 +91,38 @@ struct Shape {
   static constexpr uint32_t kStageBytes = kAtoms * kAtomBytes + kRopeBytes;
   static constexpr int kStages = kLatent == 512 ? 4 : 6;
   // Tensor-memory columns: outputs, queries (two BF16 a column), two score
-  // tiles (their weights overwrite them).
+  // tiles.
   static constexpr uint32_t kQ = kHalf;
   static constexpr uint32_t kS = kHalf + kHalf / 2;
+  // Shared memory: the ring; received scores and weights of the two groups,
+  // where a row tile's queries land before its first token tile; the rotary
+  // part of the queries.
   static constexpr uint32_t kRecv = kStages * kStageBytes;
-  static constexpr uint32_t kQRope = kRecv + 2 * kRecvBytes;
+  static constexpr uint32_t kP = kRecv + 2 * kRecvBytes;
+  static constexpr uint32_t kQRope = kP + 2 * kPBytes;
   static constexpr uint32_t kMisc = kQRope + kQRopeBytes;
   static_assert(kS + 2 * kTokens <= 512, "tensor memory");
+  static_assert(kAtoms * kQAtomBytes <= 2 * kRecvBytes + 2 * kPBytes, "queries' landing place");
 };
 
 struct Misc {
+  // Every barrier but `drained` completes once a use, in order.
   uint64_t kv_full[6], kv_empty[6], kv_ready[6];
-  uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t recv_full[2][8], credit[2][8];  // [group][warp of the group]
-  uint64_t decided[2][4];                  // [tile parity][lane quarter]
-  uint64_t q_ready, drained;
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];        // [tile parity]
+  uint64_t recv[2][4], recv_credit[2][4];                      // [group][lane quarter]
+  uint64_t weights[2][4], weights_credit[2][4], decided[2][4];
+  uint64_t tops[4];                                            // [lane quarter]
+  uint64_t q_full, q_ready, q_free, drained;
   uint64_t bad[6];  // non-finite drafts of a stage's tile, one bit a token
   uint32_t tmem;
   int32_t abort;
-  float top[2][2][kTileRows];       // [group][token half][row]
-  float reference[2][kTileRows];    // [tile parity][row]
-  float total[2][2][kTileRows];     // [group][token half][row]
-  int64_t first[kMaxRequests + 1];  // tiles before each request
+  int32_t piece;  // token tiles of a piece, 0 for an even deal
+  float reference[2][kTileRows];    // [tile parity][row], after that tile
+  float2 mine[2][kTileRows];        // [group][row]: (reference, sum) of this CTA's tokens
+  float2 peer[2][kTileRows];        // ... of the peer's, as it sent them
+  int64_t first[kMaxRequests + 1];  // runs (pieces, or token tiles) before each request
   int32_t length[kMaxRequests];
-  uint16_t begin[kMaxRequests];     // rows are at most MXFP8_MAX_LATENT_ROWS
+  uint16_t begin[kMaxRequests];  // rows are at most MXFP8_MAX_LATENT_ROWS
   uint16_t drafts[kMaxRequests];
 };
 
@@ -124,11 +146,6 @@ __device__ __forceinline__ int row_tiles(int drafts, int heads) {
 __device__ __forceinline__ int token_tiles(int length) {
   return (length + kTokens - 1) / kTokens;
 }
-// Tiles of a cluster's run.
-__device__ __forceinline__ int64_t run_length(int64_t tiles, int clusters) {
-  return max(static_cast<int64_t>(1), (tiles + clusters - 1) / clusters);
-}
-
 __device__ __forceinline__ void raise(int32_t* flags, uint32_t bit) {
   if (flags != nullptr) atomicOr(reinterpret_cast<unsigned int*>(flags), bit);
 }
@@ -140,24 +157,32 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 2^(from - to) for references from <= to; equal infinities give 1.
+__device__ __forceinline__ float shift_factor(float from, float to) {
+  return from == to ? 1.0f : exp2_approx(from - to);
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t w, float f) {
+  return pack_bf16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+}
 
-// One row tile's run of token tiles inside a cluster's run.
+// One row tile's run of token tiles inside a cluster's share.
 struct Segment {
   int b, kv0, kv1, kv_tiles;
   int length, context, drafts, begin;
   int row0;   // first row of the tile within the request (drafts x heads rows)
   int valid;  // rows of the tile, at most 128
+  int slot;   // of its partial outputs
 };
 struct Walk {
-  int64_t at, end;
+  int64_t at, end, from;  // of the list of runs
   int b;
 };
-__device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& p, Walk& w,
-                                             Segment& s) {
+__device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& p, int cluster,
+                                             Walk& w, Segment& s) {
   if (w.at >= w.end) return false;
   while (w.at >= m.first[w.b + 1]) ++w.b;
   s.b = w.b;
@@ -167,12 +192,25 @@ __device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& 
   s.context = max(s.length - s.drafts, 0);
   s.kv_tiles = token_tiles(s.length);
   const int64_t local = w.at - m.first[w.b];
-  const int tile = static_cast<int>(local / s.kv_tiles);
-  s.kv0 = static_cast<int>(local % s.kv_tiles);
-  s.kv1 = static_cast<int>(min(static_cast<int64_t>(s.kv_tiles), s.kv0 + (w.end - w.at)));
+  int tile;
+  if (m.piece > 0) {
+    const int pieces = (s.kv_tiles + m.piece - 1) / m.piece;
+    tile = static_cast<int>(local / pieces);
+    const int k = static_cast<int>(local % pieces);
+    s.kv0 = static_cast<int>(static_cast<int64_t>(s.kv_tiles) * k / pieces);
+    s.kv1 = static_cast<int>(static_cast<int64_t>(s.kv_tiles) * (k + 1) / pieces);
+    s.slot = 2 * cluster;
+    ++w.at;
+  } else {
+    tile = static_cast<int>(local / s.kv_tiles);
+    s.kv0 = static_cast<int>(local % s.kv_tiles);
+    s.kv1 = static_cast<int>(min(static_cast<int64_t>(s.kv_tiles), s.kv0 + (w.end - w.at)));
+    // Only a share's first and last row tiles can be cut.
+    s.slot = 2 * cluster + (w.at == w.from ? 0 : 1);
+    w.at += s.kv1 - s.kv0;
+  }
   s.row0 = tile * kTileRows;
   s.valid = min(kTileRows, s.drafts * p.heads - s.row0);
-  w.at += s.kv1 - s.kv0;
   return true;
 }
 // Whether a token tile reaches the drafts or the length.
@@ -181,9 +219,8 @@ __device__ __forceinline__ bool special(const Segment& s, int kv) {
 }
 
 // Bounded waits of a warp's converged lanes.  One that runs out sets `abort`,
-// after which every wait of the CTA returns at once: the roles then run their
-// loops out on whatever the buffers hold, so that no barrier is left short of
-// an arrival, and the kernel ends with its flag set.
+// after which every wait of the CTA returns at once and the kernel ends with
+// its flag set.
 struct Waiter {
   int32_t* abort;
   int32_t* flags;
@@ -198,14 +235,16 @@ struct Waiter {
            slow(bar, parity & 1u, true);
   }
   __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity, bool wide) const {
-    const uint64_t start = ptx::globaltimer();
-    for (;;) {
+    uint64_t start = 0;
+    for (int i = 0;; ++i) {
+      if (__all_sync(~0u, wide ? ptx::mbar_try_wait_cluster(bar, parity)
+                               : ptx::mbar_try_wait(bar, parity)))
+        return true;
+      if (i % 16) continue;
       if (__any_sync(~0u, *reinterpret_cast<volatile int32_t*>(abort) != 0)) return false;
-      for (int i = 0; i < 32; ++i)
-        if (__all_sync(~0u, wide ? ptx::mbar_try_wait_cluster(bar, parity)
-                                 : ptx::mbar_try_wait(bar, parity)))
-          return true;
-      if (__any_sync(~0u, ptx::globaltimer() - start > kWaitLimitNs)) {
+      const uint64_t now = ptx::globaltimer();
+      if (i == 0) start = now;
+      if (__any_sync(~0u, now - start > kWaitLimitNs)) {
         *reinterpret_cast<volatile int32_t*>(abort) = 1;
         raise(flags, MXFP8_FLAG_GEMM_TIMEOUT);
         return false;
@@ -217,18 +256,91 @@ struct Waiter {
 struct AttendParams {
   LatentParams in;
   int32_t clusters;
-  int32_t box;        // tokens of a TMA box: gcd(page_size, 64)
+  int32_t box;        // tokens of a TMA box: the largest of 64, 32, 16, 8 in a page
   float4* partial;    // [2 clusters][latent / 4][128 rows] x 4 columns
-  float2* stats;      // [2 clusters][128 rows] (reference exponent, sum)
+  float2* stats;      // [2 clusters][128 rows] (reference, sum)
+  int32_t* piece;     // the deal: token tiles of a piece, 0 for equal runs
 };
+struct AttendMaps {
+  CUtensorMap latent, rope;              // boxes of `box` tokens
+  CUtensorMap latent_small, rope_small;  // boxes of 8
+  CUtensorMap q, q_rope;                 // boxes of 128 rows
+};
+
+// Token tiles of a cluster's run in an even deal.
+__device__ __forceinline__ int64_t run_length(int64_t tiles, int clusters) {
+  return max(static_cast<int64_t>(kMinRun), (tiles + clusters - 1) / clusters);
+}
+
+// The deal, by one warp: fills Misc's lists.
+__device__ __forceinline__ void deal(Misc& m, const AttendParams& ap, int lane) {
+  const LatentParams& p = ap.in;
+  int64_t before = 0;
+  int tiles_of_rows = 0;
+  for (int base = 0; base < p.requests; base += 32) {
+    const int b = base + lane;
+    int64_t tiles = 0;
+    int rt = 0;
+    if (b < p.requests) {
+      const Request r = load_request(p, b);
+      if (r.cut && blockIdx.x == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
+      m.length[b] = r.length;
+      m.begin[b] = static_cast<uint16_t>(r.begin);
+      m.drafts[b] = static_cast<uint16_t>(r.drafts);
+      rt = r.length > 0 ? row_tiles(r.drafts, p.heads) : 0;
+      tiles = static_cast<int64_t>(rt) * token_tiles(r.length);
+    }
+    tiles_of_rows += __reduce_add_sync(~0u, rt);
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t v = __shfl_up_sync(~0u, tiles, o);
+      if (lane >= o) tiles += v;
+    }
+    if (b < p.requests) m.first[b + 1] = before + tiles;
+    before += __shfl_sync(~0u, tiles, 31);
+  }
+  // Pieces: the shortest length, from that of the even deal on, at which all
+  // pieces fit the clusters, one a cluster; a lane a length.
+  const int64_t run = run_length(before, ap.clusters);
+  int piece = 0;
+  __syncwarp();
+  if (tiles_of_rows <= ap.clusters && run < (1 << 24)) {
+    const int length = static_cast<int>(run) + lane;
+    int pieces = 0;
+    for (int b = 0; b < p.requests; ++b)
+      pieces += m.length[b] > 0 ? row_tiles(m.drafts[b], p.heads) *
+                                      ((token_tiles(m.length[b]) + length - 1) / length)
+                                : 0;
+    const uint32_t fits = __ballot_sync(~0u, lane <= kPieceSlack && pieces <= ap.clusters);
+    if (fits != 0u) piece = static_cast<int>(run) + __ffs(fits) - 1;
+  }
+  if (piece > 0) {
+    before = 0;
+    for (int base = 0; base < p.requests; base += 32) {
+      const int b = base + lane;
+      int64_t pieces = 0;
+      if (b < p.requests && m.length[b] > 0)
+        pieces = static_cast<int64_t>(row_tiles(m.drafts[b], p.heads)) *
+                 ((token_tiles(m.length[b]) + piece - 1) / piece);
+      for (int o = 1; o < 32; o *= 2) {
+        const int64_t v = __shfl_up_sync(~0u, pieces, o);
+        if (lane >= o) pieces += v;
+      }
+      if (b < p.requests) m.first[b + 1] = before + pieces;
+      before += __shfl_sync(~0u, pieces, 31);
+    }
+  }
+  if (lane == 0) {
+    m.first[0] = 0;
+    m.piece = piece;
+    if (blockIdx.x == 0) *ap.piece = piece;
+  }
+}
 
 template <int kLatent>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
-    attend_kernel(const __grid_constant__ CUtensorMap tmap_c,
-                  const __grid_constant__ CUtensorMap tmap_r,
+    attend_kernel(const __grid_constant__ AttendMaps maps,
                   const __grid_constant__ AttendParams ap) {
   using L = Shape<kLatent>;
-  constexpr int kWidth = kLatent + kRope;
   constexpr int kStages = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -240,69 +352,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   const int cluster = blockIdx.x / 2;
   auto bar = [&](const uint64_t& b) { return ptx::smem_addr(&b); };
 
-  if (tid == 0) {
-    ptx::prefetch_tensormap(&tmap_c);
-    ptx::prefetch_tensormap(&tmap_r);
-    for (int i = 0; i < kStages; ++i) {
-      ptx::mbar_init(bar(m.kv_full[i]), 1);
-      ptx::mbar_init(bar(m.kv_empty[i]), 2);  // the outputs' commit and the mender
-      ptx::mbar_init(bar(m.kv_ready[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(bar(m.s_full[i]), 1);
-      ptx::mbar_init(bar(m.p_full[i]), 8);
-      ptx::mbar_init(bar(m.pv_done[i]), 1);
-      for (int w = 0; w < 4; ++w) ptx::mbar_init(bar(m.decided[i][w]), 2);
-      for (int w = 0; w < 8; ++w) {
-        ptx::mbar_init(bar(m.recv_full[i][w]), 1);
-        ptx::mbar_init(bar(m.credit[i][w]), 1);
-      }
-    }
-    ptx::mbar_init(bar(m.q_ready), 16);
-    ptx::mbar_init(bar(m.drained), 1);
-    m.abort = 0;
+  if (warp == 0) {
+    // Barriers, a lane a kind.
+    auto init = [&](uint64_t* b, int n, uint32_t count) {
+      for (int i = 0; i < n; ++i) ptx::mbar_init(bar(b[i]), count);
+    };
+    if (lane == 0) init(m.kv_full, kStages, 1);
+    if (lane == 1) init(m.kv_empty, kStages, 2);  // the outputs' commit and the mender
+    if (lane == 2) init(m.kv_ready, kStages, 1);
+    if (lane == 3) init(m.s_full, 2, 1), init(m.s_free, 2, 4);
+    if (lane == 4) init(m.p_full, 2, 4), init(m.pv_done, 2, 1);
+    if (lane == 5) init(m.recv[0], 8, 1);
+    if (lane == 6) init(m.recv_credit[0], 8, 1);
+    if (lane == 7) init(m.weights[0], 8, 1);
+    if (lane == 8) init(m.weights_credit[0], 8, 1);
+    if (lane == 9) init(m.decided[0], 8, 1);
+    if (lane == 10) init(&m.q_full, 1, 1), init(&m.q_ready, 1, 8);
+    if (lane == 11) init(&m.q_free, 1, 8), init(&m.drained, 1, 1);
+    if (lane == 12) init(m.tops, 4, 1);
+    if (lane == 13) m.abort = 0;
     ptx::fence_mbarrier_init();
     ptx::fence_proxy_async_smem();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(bar(reinterpret_cast<uint64_t&>(m.tmem)), 512);
+    ptx::tmem_alloc(ptx::smem_addr(&m.tmem), 512);
     ptx::tmem_relinquish();
   }
+  if (warp == 2 && lane < 6)
+    ptx::prefetch_tensormap(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   ptx::tc_fence_before();
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = m.tmem;
   if (tid == 0) ptx::launch_dependents();
   ptx::grid_dependency_wait();
-
-  // Tiles before each request, by one warp.
-  if (warp == 0) {
-    int64_t before = 0;
-    for (int base = 0; base < p.requests; base += 32) {
-      const int b = base + lane;
-      int64_t tiles = 0;
-      if (b < p.requests) {
-        const Request r = load_request(p, b);
-        if (r.cut && blockIdx.x == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
-        m.length[b] = r.length;
-        m.begin[b] = static_cast<uint16_t>(r.begin);
-        m.drafts[b] = static_cast<uint16_t>(r.drafts);
-        tiles = static_cast<int64_t>(row_tiles(r.drafts, p.heads)) * token_tiles(r.length);
-      }
-      for (int o = 1; o < 32; o *= 2) {
-        const int64_t v = __shfl_up_sync(~0u, tiles, o);
-        if (lane >= o) tiles += v;
-      }
-      if (b < p.requests) m.first[b + 1] = before + tiles;
-      before += __shfl_sync(~0u, tiles, 31);
-    }
-    if (lane == 0) m.first[0] = 0;
-  }
+  if (warp == 0) deal(m, ap, lane);
   __syncthreads();
+
   const int64_t all = m.first[p.requests];
-  const int64_t run = run_length(all, ap.clusters);
-  const int64_t run_begin = min(all, cluster * run);
-  Walk walk{run_begin, min(all, run_begin + run), 0};
+  const int64_t run = m.piece > 0 ? 1 : run_length(all, ap.clusters);
+  const int64_t from = min(all, cluster * run);
+  Walk walk{from, min(all, from + run), from, 0};
   Segment seg{};
   const Waiter wait{&m.abort, p.flags};
 
@@ -310,58 +400,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     // -------------------------------------------------------------- producer
     // A lane a box (one thread's copies are served one after another); the
     // page of a lane's box is looked up one tile ahead.
-    constexpr int kItems = (8 * (L::kAtoms + 1) + 31) / 32;  // of a lane, boxes of 8 tokens
+    constexpr int kItems = (kTokens / kSmallBox * (L::kAtoms + 1) + 31) / 32;  // of a lane
+    const uint64_t keep = ptx::policy_evict_last();
+    auto box_of = [&](int kv) { return special(seg, kv) ? kSmallBox : ap.box; };
     auto page_of = [&](int kv, int i) {
-      const int token = kv * kTokens + i / (L::kAtoms + 1) * ap.box;
-      if (token >= seg.length) return 0;
+      const int box = box_of(kv);
+      const int token = kv * kTokens + i / (L::kAtoms + 1) * box;
+      // Past the length, and past the pool, the copy fills zeros.
+      if (i >= kTokens / box * (L::kAtoms + 1) || token >= seg.length) return p.pages;
       const int page = p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
       if (page >= 0 && page < p.pages) return page;
       raise(p.flags, MXFP8_FLAG_BAD_INDEX);
-      return p.pages;  // past the tensor: the copy fills zeros
+      return p.pages;
     };
-    const int boxes_per_tile = kTokens / ap.box;
     int g = 0;
     bool ok = true;
-    while (ok && next_segment(m, p, walk, seg)) {
+    while (ok && next_segment(m, p, cluster, walk, seg)) {
       int page[kItems];
 #pragma unroll
-      for (int k = 0; k < kItems; ++k) {
-        const int i = lane + 32 * k;
-        page[k] = i < boxes_per_tile * (L::kAtoms + 1) ? page_of(seg.kv0, i) : 0;
-      }
+      for (int k = 0; k < kItems; ++k) page[k] = page_of(seg.kv0, lane + 32 * k);
       for (int kv = seg.kv0; kv < seg.kv1; ++kv, ++g) {
         const int stage = g % kStages;
-        const uint32_t use = static_cast<uint32_t>(g / kStages);
         int next[kItems];
 #pragma unroll
-        for (int k = 0; k < kItems; ++k) {
-          const int i = lane + 32 * k;
-          next[k] = kv + 1 < seg.kv1 && i < boxes_per_tile * (L::kAtoms + 1) ? page_of(kv + 1, i)
-                                                                             : 0;
-        }
-        if (g >= kStages) ok = wait(m.kv_empty[stage], use - 1);
+        for (int k = 0; k < kItems; ++k)
+          next[k] = kv + 1 < seg.kv1 ? page_of(kv + 1, lane + 32 * k) : p.pages;
+        if (g >= kStages) ok = wait(m.kv_empty[stage], g / kStages - 1);
         if (!ok) break;
-        const int boxes = min(boxes_per_tile, (seg.length - kv * kTokens + ap.box - 1) / ap.box);
         const uint32_t full = bar(m.kv_full[stage]);
-        if (lane == 0)
-          ptx::mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * ap.box) *
-                                               (L::kHalf * 2u + 64u));
+        if (lane == 0) ptx::mbar_arrive_expect_tx(full, L::kStageBytes);
         __syncwarp();
+        const bool fine = special(seg, kv);
+        const int box = box_of(kv);
+        const int items = kTokens / box * (L::kAtoms + 1);
+        const uint32_t dst = sbase + stage * L::kStageBytes;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
           const int i = lane + 32 * k;
-          if (i >= boxes * (L::kAtoms + 1)) continue;
-          const int box = i / (L::kAtoms + 1), atom = i % (L::kAtoms + 1);
-          const int at = (kv * kTokens + box * ap.box) % p.page_size;
-          const uint32_t dst = sbase + stage * L::kStageBytes;
+          if (i >= items) continue;
+          const int at = i / (L::kAtoms + 1) * box, atom = i % (L::kAtoms + 1);
+          const int slot = (kv * kTokens + at) % p.page_size;
           if (atom < L::kAtoms)
-            ptx::tma_load_3d(dst + atom * kAtomBytes + box * ap.box * 128, &tmap_c,
-                             static_cast<int>(rank) * L::kHalf + atom * 64, at, page[k], full,
-                             ptx::policy_evict_last());
+            ptx::tma_load_3d(dst + atom * kAtomBytes + at * 128,
+                             fine ? &maps.latent_small : &maps.latent,
+                             static_cast<int>(rank) * L::kHalf + atom * 64, slot, page[k], full,
+                             keep);
           else
-            ptx::tma_load_3d(dst + L::kAtoms * kAtomBytes + box * ap.box * 64, &tmap_r,
-                             static_cast<int>(rank) * 32, at, page[k], full,
-                             ptx::policy_evict_last());
+            ptx::tma_load_3d(dst + L::kAtoms * kAtomBytes + at * 64,
+                             fine ? &maps.rope_small : &maps.rope, static_cast<int>(rank) * 32,
+                             slot, page[k], full, keep);
         }
         __syncwarp();
 #pragma unroll
@@ -407,32 +494,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       __syncwarp();
       return true;
     };
-    while (ok && next_segment(m, p, walk, seg)) {
+    while (ok && next_segment(m, p, cluster, walk, seg)) {
       ok = wait(m.q_ready, segments++);
       if (!ok) break;
       ptx::tc_fence_after();
       ok = scores(g, seg.kv0);
       if (ok && seg.kv0 + 1 < seg.kv1) ok = scores(g + 1, seg.kv0 + 1);
       for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g) {
-        ok = wait(m.p_full[g & 1], g >> 1);
-        if (!ok) break;
+        // The scores read out, their buffer takes the tile after the next.
+        if (kv + 2 < seg.kv1) ok = wait(m.s_free[g & 1], g >> 1) && scores(g + 2, kv + 2);
+        if (!ok || !wait(m.p_full[g & 1], g >> 1)) {
+          ok = false;
+          break;
+        }
         ptx::tc_fence_after();
         const int stage = g % kStages;
         const uint32_t kvb = sbase + stage * L::kStageBytes;
-        const uint32_t a = tmem + L::kS + (g & 1) * kTokens;
+        const uint32_t weights = sbase + L::kP + (g & 1) * kPBytes;
         const uint32_t add = kv > seg.kv0;
         const uint32_t empty = bar(m.kv_empty[stage]), done = bar(m.pv_done[g & 1]);
         if (ptx::elect_one()) {
 #pragma unroll
           for (int k = 0; k < kTokens / 16; ++k)
-            ptx::mma_f16_ts(tmem, a + k * 8, ptx::desc_mnmajor_sw128(kvb + k * 2048, kAtomBytes),
-                            kOutputs, k > 0 ? 1u : add);
+            ptx::mma_f16_ss(tmem, ptx::desc_kmajor_sw128(weights + k * 32),
+                            ptx::desc_mnmajor_sw128(kvb + k * 2048, kAtomBytes), kOutputs,
+                            k > 0 ? 1u : add);
           ptx::mma_commit(empty);
           ptx::mma_commit(done);
         }
         __syncwarp();
-        // Its weights read, the score buffer takes the tile after the next.
-        if (kv + 2 < seg.kv1) ok = scores(g + 2, kv + 2);
       }
     }
     // Nothing runs on when tensor memory is freed.
@@ -443,7 +533,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     // ---------------------------------------------------------------- mender
     int g = 0;
     bool ok = true;
-    while (ok && next_segment(m, p, walk, seg)) {
+    while (ok && next_segment(m, p, cluster, walk, seg)) {
       for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g) {
         const int stage = g % kStages;
         ok = wait(m.kv_full[stage], g / kStages);
@@ -457,9 +547,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           uint64_t bad = 0;
           for (int n = n0; n < n1; ++n) {
             bool finite = true;
-            for (int i = lane; i < L::kAtoms * 8; i += 32) {
-              const uint4 v = *reinterpret_cast<const uint4*>(kvp + (i / 8) * kAtomBytes +
-                                                              n * 128 + (i % 8) * 16);
+            if (lane < L::kAtoms * 8) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kvp + (lane / 8) * kAtomBytes +
+                                                              n * 128 + (lane % 8) * 16);
               const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int q = 0; q < 4; ++q)
@@ -468,14 +558,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             }
             if (!__all_sync(~0u, finite)) bad |= 1ull << n;
           }
-          for (int n = n0; n < kTokens; ++n) {
-            if (n < n1 && !(bad >> n & 1)) continue;
-            for (int i = lane; i < L::kAtoms * 8 + 4; i += 32) {
-              uint8_t* at = i < L::kAtoms * 8
-                                ? kvp + (i / 8) * kAtomBytes + n * 128 + (i % 8) * 16
-                                : kvp + L::kAtoms * kAtomBytes + n * 64 + (i - L::kAtoms * 8) * 16;
-              *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
-            }
+          // Boxes of 8 tokens past the length came as zeros; the rest of the
+          // last one is filled here.
+          uint64_t fill = bad | (low_ones((n1 + kSmallBox - 1) / kSmallBox * kSmallBox) &
+                                 ~low_ones(n1));
+          while (fill != 0) {
+            const int n = __ffsll(static_cast<long long>(fill)) - 1;
+            fill &= fill - 1;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            if (lane < L::kAtoms * 8)
+              *reinterpret_cast<uint4*>(kvp + (lane / 8) * kAtomBytes + n * 128 +
+                                        (lane % 8) * 16) = zero;
+            if (lane < 4)
+              *reinterpret_cast<uint4*>(kvp + L::kAtoms * kAtomBytes + n * 64 + lane * 16) = zero;
           }
           if (lane == 0) m.bad[stage] = bad;
           ptx::fence_proxy_async_smem();
@@ -487,106 +582,170 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         }
       }
     }
-  } else if (warp >= kSoftmaxWarp) {
+  } else if (warp == 3) {
+    // --------------------------------------------------------- query loader
+    uint32_t segments = 0;
+    while (next_segment(m, p, cluster, walk, seg)) {
+      if (segments > 0) wait(m.q_free, segments - 1);
+      ++segments;
+      const uint32_t full = bar(m.q_full);
+      if (lane == 0)
+        ptx::mbar_arrive_expect_tx(full, L::kAtoms * kQAtomBytes + kQRopeBytes);
+      __syncwarp();
+      const int row = seg.begin * p.heads + seg.row0;
+      if (lane < L::kAtoms)
+        ptx::tma_load_2d(sbase + L::kRecv + lane * kQAtomBytes, &maps.q,
+                         static_cast<int>(rank) * L::kHalf + lane * 64, row, full,
+                         ptx::policy_evict_first());
+      else if (lane == L::kAtoms)
+        ptx::tma_load_2d(sbase + L::kQRope, &maps.q_rope, static_cast<int>(rank) * 32, row, full,
+                         ptx::policy_evict_first());
+      __syncwarp();
+    }
+    if (segments > 0) ptx::mbar_wait(bar(m.q_full), (segments - 1) & 1u, kWaitLimitNs);
+  } else {
     // --------------------------------------------------------------- softmax
-    const int group = (warp - kSoftmaxWarp) / 8;  // takes the tiles of this parity
-    const int sw = (warp - kSoftmaxWarp) % 8;
+    const int group = (warp - kSoftmaxWarp) / 4;  // takes the tiles of this parity
     const int quarter = warp & 3;  // the 32 tensor-memory lanes this warp reaches
-    const int half = sw >> 2;      // its 32 of a tile's 64 tokens
-    const int part = group * 2 + half;  // its quarter of the columns, in and out
     const int row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t score = lanes + L::kS + group * kTokens;
     const uint32_t peer = rank ^ 1u;
-    const uint32_t recv_offset = L::kRecv + group * kRecvBytes + static_cast<uint32_t>(sw) * 4096u;
-    const uint32_t recv_bar = bar(m.recv_full[group][sw]);
-    const uint32_t to = ptx::map_to_rank(sbase + recv_offset + lane * 16u, peer);
-    const uint32_t to_bar = ptx::map_to_rank(recv_bar, peer);
-    const uint32_t credit_bar = ptx::map_to_rank(bar(m.credit[group][sw]), peer);
-    const float4* recv = reinterpret_cast<const float4*>(smem + recv_offset) + lane;
-    constexpr int kPart = L::kHalf / 4;
+    const uint32_t recv_offset = L::kRecv + group * kRecvBytes + quarter * 4096u + lane * 16u;
+    const float4* recv = reinterpret_cast<const float4*>(smem + recv_offset);
+    // A row of weights is one 128-byte swizzled row: this CTA's 32 tokens are
+    // chunks 4 rank .. 4 rank + 3, in its own operand and in the peer's.
+    const uint32_t p_row = L::kP + group * kPBytes + row * 128u;
+    auto chunk_at = [&](uint32_t half, int c) { return ((half * 4u + c) ^ (row & 7u)) * 16u; };
+    const uint64_t& recv_bar = m.recv[group][quarter];
+    const uint64_t& weights_bar = m.weights[group][quarter];
+    const uint32_t to_scores = ptx::map_to_rank(sbase + recv_offset, peer);
+    const uint32_t to_scores_bar = ptx::map_to_rank(bar(recv_bar), peer);
+    const uint32_t to_weights = ptx::map_to_rank(sbase + p_row, peer);
+    const uint32_t to_weights_bar = ptx::map_to_rank(bar(weights_bar), peer);
+    const uint32_t to_sum = ptx::map_to_rank(ptx::smem_addr(&m.peer[group][row]), peer);
+    const uint32_t to_top = ptx::map_to_rank(ptx::smem_addr(&m.mine[group ^ 1][row]), peer);
+    const uint32_t to_top_bar = ptx::map_to_rank(bar(m.tops[quarter]), peer);
+    const uint32_t to_recv_credit = ptx::map_to_rank(bar(m.recv_credit[group][quarter]), peer);
+    const uint32_t to_weights_credit =
+        ptx::map_to_rank(bar(m.weights_credit[group][quarter]), peer);
     uint32_t exchanges = 0;  // tiles this warp exchanged
-    uint32_t decisions = 0;  // tiles this quarter's rows took part in, of both groups
+    uint32_t decisions = 0;  // tiles of this quarter's rows, of both groups
+    uint32_t firsts = 0;     // row tiles of this quarter
     int g = 0;               // token tiles before the segment
-    for (uint32_t segments = 0; next_segment(m, p, walk, seg);
+    for (uint32_t segments = 0; next_segment(m, p, cluster, walk, seg);
          g += seg.kv1 - seg.kv0, ++segments) {
       const size_t q_row = static_cast<size_t>(seg.begin) * p.heads + seg.row0 + row;
       const bool mine = row < seg.valid;
       const bool active = quarter * 32 < seg.valid;  // of the warp
-      // Queries: this CTA's columns into tensor memory, the rotary part into
-      // shared memory (64-byte swizzle); rows past the tile are zero.
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + q_row * kWidth);
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        uint32_t v[kPart / 2];
-#pragma unroll
-        for (int i = 0; i < kPart / 8; ++i) {
-          const uint4 x = mine ? src[(rank * L::kHalf + part * kPart) / 8 + i] : zero;
-          v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
-        }
-        if constexpr (kPart == 64)
-          ptx::tmem_st_32x32b_x32(lanes + L::kQ + part * (kPart / 2), v);
-        else
-          ptx::tmem_st_32x32b_x16(lanes + L::kQ + part * (kPart / 2), v);
-        const uint4 x = mine ? src[kLatent / 8 + rank * 4 + part] : zero;
-        *reinterpret_cast<uint4*>(smem + L::kQRope + row * 64 + ((part ^ ((row >> 1) & 3)) * 16)) =
-            x;
-        ptx::tmem_wait_st();
-        ptx::fence_proxy_async_smem();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(m.q_ready));
-      }
       const int tiles = seg.kv1 - seg.kv0;
-      if (!active) {
-        for (int i = (g & 1) != group; i < tiles; i += 2) {
-          wait(m.s_full[group], (g + i) >> 1);
-          if (lane == 0) ptx::mbar_arrive(bar(m.p_full[group]));
+      const int i0 = (g & 1) != group;  // this group's first tile
+      // Queries: from where they landed into tensor memory, half of this CTA's
+      // columns a group.
+      wait(m.q_full, segments);
+      if (active) {
+        const uint8_t* src = smem + L::kRecv + row * 128;
+#pragma unroll
+        for (int half = 0; half < L::kAtoms / 2; ++half) {
+          const int atom = group * (L::kAtoms / 2) + half;
+          uint32_t v[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4*>(src + atom * kQAtomBytes +
+                                                            ((i ^ (row & 7)) * 16));
+            v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
+          }
+          ptx::tmem_st_32x32b_x32(lanes + L::kQ + atom * 32, v);
         }
-        // Not on to the next segment's queries before every warp's of this one.
-        wait(m.q_ready, segments);
+        ptx::tmem_wait_st();
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(m.q_ready));
+      // Every warp has read the queries: their landing place is the peer's to
+      // send to.
+      wait(m.q_ready, segments);
+      if (!active) {
+        for (int i = i0; i < tiles; i += 2) {
+          wait(m.s_full[group], (g + i) >> 1);
+          if (lane == 0) {
+            ptx::mbar_arrive(bar(m.s_free[group]));
+            ptx::mbar_arrive(bar(m.p_full[group]));
+          }
+          // (The scores two tiles on may come before this tile's weights: no
+          // second arrival at one phase.)
+          wait(m.p_full[group], (g + i) >> 1);
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(m.q_free));
         continue;
+      }
+      if (lane == 0 && i0 < tiles) {
+        ptx::mbar_arrive_remote_relaxed(to_recv_credit);
+        ptx::mbar_arrive_remote_relaxed(to_weights_credit);
       }
       // What this row sees of the drafts.
       const int t = (seg.row0 + row) / p.heads;
       const uint64_t tree =
           p.tree != nullptr && mine ? static_cast<uint64_t>(p.tree[seg.begin + t]) : 0;
-      float reference = -INFINITY, total = 0.0f;  // of this warp's tiles
+      // After this group's last tile: the row's common reference, and this
+      // CTA's tokens' sum under `base`.
+      float known = -INFINITY, base = -INFINITY, total = 0.0f;
 
-      for (int i = (g & 1) != group; i < tiles; i += 2, ++exchanges) {
+      for (int i = i0; i < tiles; i += 2, ++exchanges) {
         const int kv = seg.kv0 + i;
         const uint32_t decision = decisions + i;
-        // This CTA's partial scores, sent to the peer and joined with its own.
+        const bool last_own = i + 2 >= tiles;
+        if (lane == 0) {
+          ptx::mbar_arrive_expect_tx(bar(recv_bar), 32u * 32u * 4u);
+          ptx::mbar_arrive_expect_tx(bar(weights_bar), 32u * (64u + 8u));
+          if (i == 0) ptx::mbar_arrive_expect_tx(bar(m.tops[quarter]), 32u * 8u);
+        }
         wait(m.s_full[group], (g + i) >> 1);
         ptx::tc_fence_after();
-        uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(score + half * 32, v);
+        uint32_t other[32], own[32];
+        ptx::tmem_ld_32x32b_x32(score + peer * 32, other);
+        ptx::tmem_ld_32x32b_x32(score + rank * 32, own);
         ptx::tmem_wait_ld();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(m.s_free[group]));
         if (special(seg, kv)) {
           const int stage = (g + i) % kStages;
           wait(m.kv_ready[stage], (g + i) / kStages);
-          const uint32_t bad = static_cast<uint32_t>(m.bad[stage] >> (32 * half));
-          if (bad != 0u)
+          const uint64_t bad = m.bad[stage];
+          if (bad != 0) {
+            const uint32_t bad_other = static_cast<uint32_t>(bad >> (32 * peer));
+            const uint32_t bad_own = static_cast<uint32_t>(bad >> (32 * rank));
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (bad >> c & 1u) v[c] = 0x7FC00000u;
+            for (int c = 0; c < 32; ++c) {
+              if (bad_other >> c & 1u) other[c] = 0x7FC00000u;
+              if (bad_own >> c & 1u) own[c] = 0x7FC00000u;
+            }
+          }
         }
-        if (exchanges > 0) wait.cluster(m.credit[group][sw], exchanges - 1);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(recv_bar, 4096);
-        __syncwarp();
+        // Scores: the peer's tokens out, its partials of this CTA's in.
+        wait.cluster(m.recv_credit[group][quarter], exchanges);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          ptx::st_async_remote_v4(
-              to + c * 512, make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]), to_bar);
-        wait.cluster(m.recv_full[group][sw], exchanges);
+          ptx::st_async_remote_v4(to_scores + c * 512,
+                                  make_uint4(other[4 * c], other[4 * c + 1], other[4 * c + 2],
+                                             other[4 * c + 3]),
+                                  to_scores_bar);
+        if (i > i0) {
+          // This group's last outputs are added: its weights' place is free.
+          wait(m.pv_done[group], (g + i - 2) >> 1);
+          if (lane == 0) ptx::mbar_arrive_remote_relaxed(to_weights_credit);
+        }
+        wait.cluster(recv_bar, exchanges);
         float z[32];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float4 x = recv[c * 32];
-          z[4 * c] = __uint_as_float(v[4 * c]) + x.x;
-          z[4 * c + 1] = __uint_as_float(v[4 * c + 1]) + x.y;
-          z[4 * c + 2] = __uint_as_float(v[4 * c + 2]) + x.z;
-          z[4 * c + 3] = __uint_as_float(v[4 * c + 3]) + x.w;
+          z[4 * c] = __uint_as_float(own[4 * c]) + x.x;
+          z[4 * c + 1] = __uint_as_float(own[4 * c + 1]) + x.y;
+          z[4 * c + 2] = __uint_as_float(own[4 * c + 2]) + x.z;
+          z[4 * c + 3] = __uint_as_float(own[4 * c + 3]) + x.w;
         }
         if (special(seg, kv)) {
           const int at = kv * kTokens;
@@ -599,118 +758,171 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             sees = low_ones(seg.context + t + 1 - at);
           }
           sees &= low_ones(seg.length - at);
-          const uint32_t bits = static_cast<uint32_t>(sees >> (32 * half));
+          const uint32_t bits = static_cast<uint32_t>(sees >> (32 * rank));
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (!(bits >> c & 1u)) z[c] = -INFINITY;
         }
-        float top = z[0];
+        float top = fmaxf(z[0], z[1]);
 #pragma unroll
-        for (int c = 1; c < 32; ++c) top = fmaxf(top, z[c]);
-        m.top[group][half][row] = top;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + group * 4 + quarter) : "memory");
-        top = fmaxf(top, m.top[group][half ^ 1][row]) * p.scale_log2;
-
-        // The reference after the tile before this one, moved if the new
-        // maximum passes it by more than kLazy.
-        float now = -INFINITY;
-        if (i > 0) {
-          wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
-          now = m.reference[(decision - 1) & 1][row];
-        }
-        const bool move = top > now + kLazy;
-        if (i > 0 && __any_sync(~0u, move)) {
-          // The outputs so far, once the previous tile's have been added.
-          const float f = move ? exp2_approx(now - top) : 1.0f;
-          wait(m.pv_done[group ^ 1], (g + i - 1) >> 1);
-          ptx::tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < L::kHalf / 2; c += 32) {
-            ptx::tmem_ld_32x32b_x32(lanes + half * (L::kHalf / 2) + c, v);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * f);
-            ptx::tmem_st_32x32b_x32(lanes + half * (L::kHalf / 2) + c, v);
-          }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-        }
-        if (move) now = top;
-        if (half == 0) m.reference[decision & 1][row] = now;
+        for (int c = 2; c < 32; c += 2) top = fmaxf(top, fmaxf(z[c], z[c + 1]));
+        top *= p.scale_log2;
+        // The received scores have returned their values (each went into the
+        // maximum), so the peer may overwrite them.
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
-        if (now != reference) {
-          total *= exp2_approx(reference - now);
-          reference = now;
+        if (lane == 0 && !last_own) ptx::mbar_arrive_remote_relaxed(to_recv_credit);
+        // Weights of this CTA's tokens: under the halves' common maximum in the
+        // first tile, then under the last reference this group knows, or one
+        // whole steps above it.
+        float under;
+        if (i == 0) {
+          // (It lands where the other group keeps its sums, which that group
+          // writes after this decision.)
+          ptx::st_async_remote_v2(to_top, __float_as_uint(top), __float_as_uint(top), to_top_bar);
+          wait.cluster(m.tops[quarter], firsts);
+          under = fmaxf(top, m.mine[group ^ 1][row].x);
+          m.reference[decision & 1][row] = under;
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
+        } else {
+          if (i == 1) {
+            wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
+            known = m.reference[(decision - 1) & 1][row];
+          }
+          under = !(top > known + kLazy)  ? known
+                  : known == -INFINITY    ? ceilf(top)
+                                          : known + ceilf(top - known);
         }
-        const float base = now == -INFINITY ? 0.0f : now;
+        total *= shift_factor(base, under);
+        base = under;
+        const float sub = under == -INFINITY ? 0.0f : under;
         uint32_t w[16];
         float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          w[c] = pack_bf16(exp2_approx(fmaf(z[2 * c], p.scale_log2, -base)),
-                           exp2_approx(fmaf(z[2 * c + 1], p.scale_log2, -base)));
+          w[c] = pack_bf16(exp2_approx(fmaf(z[2 * c], p.scale_log2, -sub)),
+                           exp2_approx(fmaf(z[2 * c + 1], p.scale_log2, -sub)));
           sum0 += __uint_as_float(w[c] << 16);
           sum1 += __uint_as_float(w[c] & 0xFFFF0000u);
         }
         total += sum0 + sum1;
-        ptx::tmem_st_32x32b_x16(score + half * 16, w);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
+        wait.cluster(m.weights_credit[group][quarter], exchanges);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          ptx::st_async_remote_v4(to_weights + chunk_at(rank, c),
+                                  make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]),
+                                  to_weights_bar);
+        ptx::st_async_remote_v2(to_sum, __float_as_uint(base), __float_as_uint(total),
+                                to_weights_bar);
+        m.mine[group][row] = make_float2(base, total);
+        // The row's reference after this tile: the largest of the one before
+        // and the two halves'.
+        wait.cluster(weights_bar, exchanges);
+        const float theirs = m.peer[group][row].x;
+        float before = -INFINITY;
+        if (i > 0) {
+          wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
+          before = m.reference[(decision - 1) & 1][row];
+        }
+        const float now = fmaxf(before, fmaxf(base, theirs));
+        if (i > 0) m.reference[decision & 1][row] = now;
+        if (__any_sync(~0u, now != base)) {
+          const float f = shift_factor(base, now);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) w[c] = scale_bf16(w[c], f);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(smem + p_row + chunk_at(rank, c)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        if (__any_sync(~0u, now != theirs)) {
+          const float f = shift_factor(theirs, now);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(smem + p_row + chunk_at(peer, c));
+            const uint4 v = *at;
+            *at = make_uint4(scale_bf16(v.x, f), scale_bf16(v.y, f), scale_bf16(v.z, f),
+                             scale_bf16(v.w, f));
+          }
+        }
+        if (i > 0 && __any_sync(~0u, now != before)) {
+          // The outputs so far, once the tile before has been added.
+          const float f = shift_factor(before, now);
+          wait(m.pv_done[group ^ 1], (g + i - 1) >> 1);
+          ptx::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < L::kHalf; c += 32) {
+            ptx::tmem_ld_32x32b_x32(lanes + c, own);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 32; ++q) own[q] = __float_as_uint(__uint_as_float(own[q]) * f);
+            ptx::tmem_st_32x32b_x32(lanes + c, own);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+        }
+        known = now;
+        ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
+          if (i > 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
           ptx::mbar_arrive(bar(m.p_full[group]));
-          // The peer may overwrite the receive buffer.  (Last: a release over
-          // the cluster waits for this thread's own remote stores.)
-          ptx::mbar_arrive_remote(credit_bar);
         }
       }
 
-      // The row tile's outputs: the last tile's have been added, and the sums of
-      // the row's four warps join under the last reference.
+      // The row tile's outputs: the last tile is decided, and added (in this
+      // order: then the barrier of the additions is at most one phase ahead of
+      // a look at its parity).
       const uint32_t last = decisions + tiles - 1;
       decisions += tiles;
-      // In this order: once the last tile is decided its outputs' barrier is at
-      // most one phase ahead of a look at its parity.
+      ++firsts;
       wait(m.decided[last & 1][quarter], last >> 1);
       wait(m.pv_done[(g + tiles - 1) & 1], (g + tiles - 1) >> 1);
       ptx::tc_fence_after();
+      ptx::fence_proxy_async_smem();  // the next queries come over what was read here
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar(m.q_free));
       const float now = m.reference[last & 1][row];
-      if (now != reference) total *= exp2_approx(reference - now);
-      m.total[group][half][row] = total;
-      asm volatile("bar.sync %0, 128;" ::"r"(9 + quarter) : "memory");
-      total = (m.total[0][0][row] + m.total[0][1][row]) + (m.total[1][0][row] + m.total[1][1][row]);
+      // Both halves' sums, of the groups that had a tile.
+      float sum_own = 0.0f, sum_peer = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (tiles < 2 && (g & 1) != q) continue;
+        const float2 a = m.mine[q][row], b = m.peer[q][row];
+        sum_own += a.y * shift_factor(a.x, now);
+        sum_peer += b.y * shift_factor(b.x, now);
+      }
+      total = sum_own + sum_peer;
       const bool whole = seg.kv0 == 0 && seg.kv1 == seg.kv_tiles;
-      const int column0 = static_cast<int>(rank) * L::kHalf + part * kPart;
-      const int slot = 2 * cluster + (walk.at - tiles == run_begin ? 0 : 1);
+      const int column0 = static_cast<int>(rank) * L::kHalf + group * (L::kHalf / 2);
       const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
-      if (!whole && rank == 0 && part == 0 && mine)
-        ap.stats[slot * kTileRows + row] = make_float2(now, total);
+      if (!whole && rank == 0 && group == 0 && mine)
+        ap.stats[seg.slot * kTileRows + row] = make_float2(now, total);
 #pragma unroll 1
-      for (int c = 0; c < kPart; c += 32) {
+      for (int c = 0; c < L::kHalf / 2; c += 32) {
         uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(lanes + part * kPart + c, v);
+        ptx::tmem_ld_32x32b_x32(lanes + group * (L::kHalf / 2) + c, v);
         ptx::tmem_wait_ld();
         if (!mine) continue;
         if (whole) {
-          uint4* out = reinterpret_cast<uint4*>(p.out + q_row * kLatent + column0 + c);
+          uint16_t* out = p.out + q_row * kLatent + column0 + c;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
+          for (int i = 0; i < 2; ++i) {
+            uint32_t w[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              w[q] = pack_bf16(__uint_as_float(v[8 * i + 2 * q]) * inverse,
-                               __uint_as_float(v[8 * i + 2 * q + 1]) * inverse);
-            out[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int q = 0; q < 8; ++q)
+              w[q] = pack_bf16(__uint_as_float(v[16 * i + 2 * q]) * inverse,
+                               __uint_as_float(v[16 * i + 2 * q + 1]) * inverse);
+            ptx::st_v8(out + 16 * i, w);
           }
         } else {
-          float4* to_part = ap.partial +
-                            (static_cast<size_t>(slot) * (kLatent / 4) + (column0 + c) / 4) *
-                                kTileRows +
-                            row;
+          float4* part = ap.partial +
+                         (static_cast<size_t>(seg.slot) * (kLatent / 4) + (column0 + c) / 4) *
+                             kTileRows +
+                         row;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            to_part[i * kTileRows] =
+            part[i * kTileRows] =
                 make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
         }
@@ -743,11 +955,15 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
   int tiles = 0, covered0 = p.rows, covered1 = p.rows;
   size_t out_row = 0;
   bool mine = false, found = false;
+  const int piece = *ap.piece;
   for (int b = 0; b < p.requests; ++b) {
     const Request r = load_request(p, b);
     if (b == 0) covered0 = r.begin;
     if (b == p.requests - 1) covered1 = r.begin + r.drafts;
-    const int rt = row_tiles(r.drafts, p.heads), kt = token_tiles(r.length);
+    // Runs of the list that a row tile makes up.
+    const int rt = row_tiles(r.drafts, p.heads);
+    int kt = token_tiles(r.length);
+    if (piece > 0) kt = (kt + piece - 1) / piece;
     const int tile = static_cast<int>(blockIdx.x) - tiles;
     if (tile >= 0 && tile < rt) {
       found = true;
@@ -777,13 +993,14 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
     write(out_row, zero);
     return;
   }
-  const int64_t run = run_length(all, ap.clusters);
+  // The clusters that shared the row tile: its pieces', or those whose runs
+  // meet it.
+  const int64_t run = piece > 0 ? 1 : run_length(all, ap.clusters);
   const int c0 = static_cast<int>(begin / run), c1 = static_cast<int>((end - 1) / run);
   if (c0 == c1) return;  // one cluster wrote the whole
   auto slot_of = [&](int c) { return 2 * c + (c * run < begin ? 1 : 0); };
   float top = -INFINITY;
   for (int c = c0; c <= c1; ++c) top = fmaxf(top, ap.stats[slot_of(c) * kTileRows + row].x);
-  if (top == -INFINITY) top = 0.0f;
   float4 sum = zero;
   float total = 0.0f;
 #pragma unroll 4
@@ -792,7 +1009,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
     const float2 st = ap.stats[slot * kTileRows + row];
     const float4 v =
         ap.partial[(static_cast<size_t>(slot) * (kLatent / 4) + column / 4) * kTileRows + row];
-    const float f = exp2_approx(st.x - top);
+    const float f = shift_factor(st.x, top);
     total = fmaf(f, st.y, total);
     sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
     sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
@@ -862,6 +1079,21 @@ CUresult encode_cache(CUtensorMap* map, const LatentParams& p, int first, int co
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+// q [rows x heads][latent + 64], boxes of 128 rows.
+CUresult encode_queries(CUtensorMap* map, const LatentParams& p, int latent, int first,
+                        int columns, int box_columns, CUtensorMapSwizzle swizzle) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return CUDA_ERROR_NOT_FOUND;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns),
+                        static_cast<cuuint64_t>(p.rows) * p.heads};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(latent + kRope) * 2};
+  cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box_columns), kTileRows};
+  cuuint32_t elem[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.q + first), dims,
+            strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 template <int kLatent>
 cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t stream) {
   AttendParams ap{};
@@ -873,11 +1105,16 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
   ap.partial = static_cast<float4*>(workspace);
   ap.stats = reinterpret_cast<float2*>(ap.partial + static_cast<size_t>(2) * kMaxClusters *
                                                         (kLatent / 4) * kTileRows);
-  CUtensorMap tmap_c, tmap_r;
-  if (encode_cache(&tmap_c, p, 0, kLatent, ap.box, 64, CU_TENSOR_MAP_SWIZZLE_128B) !=
-          CUDA_SUCCESS ||
-      encode_cache(&tmap_r, p, kLatent, kRope, ap.box, 32, CU_TENSOR_MAP_SWIZZLE_64B) !=
-          CUDA_SUCCESS)
+  ap.piece = reinterpret_cast<int32_t*>(ap.stats + static_cast<size_t>(2) * kMaxClusters *
+                                                       kTileRows);
+  AttendMaps maps;
+  constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, k64 = CU_TENSOR_MAP_SWIZZLE_64B;
+  if (encode_cache(&maps.latent, p, 0, kLatent, ap.box, 64, k128) != CUDA_SUCCESS ||
+      encode_cache(&maps.rope, p, kLatent, kRope, ap.box, 32, k64) != CUDA_SUCCESS ||
+      encode_cache(&maps.latent_small, p, 0, kLatent, kSmallBox, 64, k128) != CUDA_SUCCESS ||
+      encode_cache(&maps.rope_small, p, kLatent, kRope, kSmallBox, 32, k64) != CUDA_SUCCESS ||
+      encode_queries(&maps.q, p, kLatent, 0, kLatent, 64, k128) != CUDA_SUCCESS ||
+      encode_queries(&maps.q_rope, p, kLatent, kLatent, kRope, 32, k64) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
 
   cudaLaunchAttribute attr;
@@ -890,7 +1127,7 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
   cfg.gridDim = dim3(static_cast<unsigned>(2 * ap.clusters));
   cfg.blockDim = dim3(kAttendThreads);
   cfg.dynamicSmemBytes = smem_bytes<kLatent>();
-  e = cudaLaunchKernelEx(&cfg, attend_kernel<kLatent>, tmap_c, tmap_r, ap);
+  e = cudaLaunchKernelEx(&cfg, attend_kernel<kLatent>, maps, ap);
   if (e != cudaSuccess) return e;
   // Row tiles of all requests at most, and one block for the rows of none.
   const int tiles = static_cast<int>(static_cast<int64_t>(p.rows) * p.heads / kTileRows) +
@@ -905,7 +1142,8 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
 
 size_t latent_workspace_bytes(int latent) {
   return static_cast<size_t>(2) * kMaxClusters * kTileRows *
-         (static_cast<size_t>(latent) * sizeof(float) + sizeof(float2));
+             (static_cast<size_t>(latent) * sizeof(float) + sizeof(float2)) +
+         256;
 }
 
 cudaError_t launch_latent_attend(const LatentParams& p, int latent, void* workspace,

@@ -357,9 +357,11 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-// Arrive on a peer CTA's mbarrier (`remote_bar` from map_to_rank).
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t remote_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
+// Arrive on a peer CTA's mbarrier (`remote_bar` from map_to_rank), ordering
+// nothing: for a caller whose reads have returned their values already.  (The
+// release form waits for the thread's earlier remote stores.)
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
                : "memory");
 }
 // Store 16 bytes (16-byte aligned) into a peer CTA's shared memory; the byte
@@ -371,6 +373,12 @@ __device__ __forceinline__ void st_async_remote_v4(uint32_t remote_addr, uint4 v
       "[%5];" ::"r"(remote_addr),
       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(remote_bar)
       : "memory");
+}
+// 32 bytes to global memory (32-byte aligned), one sector.
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 // Store 8 bytes (8-byte aligned) into a peer CTA's shared memory; the byte
 // count completes on the peer's mbarrier.
