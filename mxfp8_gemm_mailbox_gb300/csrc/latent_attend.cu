@@ -39,11 +39,11 @@
 // joins in a fixed order.
 //
 // Warps of a CTA:
-//   0      producer: TMA boxes of a token tile into a ring, a lane a box;
+//   0      producer: TMA boxes into a ring, a lane a box: a row tile's queries
+//          in two places of it, then its token tiles;
 //   1      MMA issuer;
 //   2      mender of the tiles that reach the drafts or the length: zeroes the
 //          tokens past the length and drafts that are not finite;
-//   3      loads a row tile's queries;
 //   4-11   softmax, two groups of four that take the token tiles in turn, so
 //          one group's exchanges run under the other's: thread = row.
 //
@@ -81,49 +81,50 @@ constexpr uint32_t kAtomBytes = kTokens * 128;  // 64 tokens x 64 columns
 constexpr uint32_t kRopeBytes = kTokens * 64;   // 64 tokens x 32 rotary columns
 constexpr uint32_t kQAtomBytes = kTileRows * 128;
 constexpr uint32_t kQRopeBytes = kTileRows * 64;
-constexpr uint32_t kRecvBytes = kTileRows * 32 * 4;  // partial scores from the peer
-constexpr uint32_t kPBytes = kTileRows * 128;        // weights, 64 BF16 a row
+// A group's partial scores from the peer (128 rows x 32 tokens x 4 bytes), then,
+// read out, its weights (128 rows x 64 tokens x 2 bytes, swizzled): either way
+// a quarter of 32 rows keeps to its own 4096 bytes.
+constexpr uint32_t kExchangeBytes = kTileRows * 128;
 
 template <int kLatent>
 struct Shape {
   static constexpr int kHalf = kLatent / 2;  // columns of a CTA
   static constexpr int kAtoms = kHalf / 64;
   static constexpr uint32_t kStageBytes = kAtoms * kAtomBytes + kRopeBytes;
-  static constexpr int kStages = kLatent == 512 ? 4 : 6;
+  static constexpr int kStages = kLatent == 512 ? 5 : 8;
   // Tensor-memory columns: outputs, queries (two BF16 a column), two score
   // tiles.
   static constexpr uint32_t kQ = kHalf;
   static constexpr uint32_t kS = kHalf + kHalf / 2;
-  // Shared memory: the ring; received scores and weights of the two groups,
-  // where a row tile's queries land before its first token tile; the rotary
-  // part of the queries.
-  static constexpr uint32_t kRecv = kStages * kStageBytes;
-  static constexpr uint32_t kP = kRecv + 2 * kRecvBytes;
-  static constexpr uint32_t kQRope = kP + 2 * kPBytes;
+  // Shared memory: the ring; the two groups' exchanges; the rotary part of the
+  // queries.
+  static constexpr uint32_t kX = kStages * kStageBytes;
+  static constexpr uint32_t kQRope = kX + 2 * kExchangeBytes;
   static constexpr uint32_t kMisc = kQRope + kQRopeBytes;
   static_assert(kS + 2 * kTokens <= 512, "tensor memory");
-  static_assert(kAtoms * kQAtomBytes <= 2 * kRecvBytes + 2 * kPBytes, "queries' landing place");
+  static_assert(kAtoms / 2 * kQAtomBytes + kQRopeBytes / 2 == kStageBytes,
+                "half of the queries fill a place of the ring");
 };
 
+constexpr int kMaxStages = 8;
 struct Misc {
   // Every barrier but `drained` completes once a use, in order.
-  uint64_t kv_full[6], kv_empty[6], kv_ready[6];
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_ready[kMaxStages];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];        // [tile parity]
   uint64_t recv[2][4], recv_credit[2][4];                      // [group][lane quarter]
   uint64_t weights[2][4], weights_credit[2][4], decided[2][4];
   uint64_t tops[4];                                            // [lane quarter]
-  uint64_t q_full, q_ready, q_free, drained;
-  uint64_t bad[6];  // non-finite drafts of a stage's tile, one bit a token
+  uint64_t q_ready, drained;
+  uint64_t bad[kMaxStages];  // non-finite drafts of a stage's tile, one bit a token
   uint32_t tmem;
   int32_t abort;
   int32_t piece;  // token tiles of a piece, 0 for an even deal
-  float reference[2][kTileRows];    // [tile parity][row], after that tile
-  float2 mine[2][kTileRows];        // [group][row]: (reference, sum) of this CTA's tokens
-  float2 peer[2][kTileRows];        // ... of the peer's, as it sent them
-  int64_t first[kMaxRequests + 1];  // runs (pieces, or token tiles) before each request
+  float peer_top[kTileRows];         // the peer's maxima in the first tile
+  float reference[2][kTileRows];     // [tile parity][row], after that tile
+  float2 peer[2][kTileRows];         // [group][row]: (reference, sum) of the peer's tokens
+  uint32_t first[kMaxRequests + 1];  // runs (pieces, or token tiles) before each request
   int32_t length[kMaxRequests];
-  uint16_t begin[kMaxRequests];  // rows are at most MXFP8_MAX_LATENT_ROWS
-  uint16_t drafts[kMaxRequests];
+  uint16_t begin[kMaxRequests + 1];  // rows are at most MXFP8_MAX_LATENT_ROWS
 };
 
 // The device-side inputs of one request, cut to what the buffers hold.
@@ -135,7 +136,7 @@ __device__ __forceinline__ Request load_request(const LatentParams& p, int b) {
   const int begin = p.row_begin[b], end = p.row_begin[b + 1], length = p.lengths[b];
   Request r;
   r.begin = min(max(begin, 0), p.rows);
-  r.drafts = max(min(end, p.rows) - r.begin, 0);
+  r.drafts = max(min(max(end, 0), p.rows) - r.begin, 0);
   r.length = min(max(length, 0), p.table_width * p.page_size);
   r.cut = begin < 0 || end > p.rows || end < begin || length != r.length;
   return r;
@@ -161,12 +162,38 @@ __device__ __forceinline__ float exp2_approx(float x) {
 __device__ __forceinline__ float shift_factor(float from, float to) {
   return from == to ? 1.0f : exp2_approx(from - to);
 }
+// Pairs of FP32 numbers in one instruction, each as the single one rounds.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 __device__ __forceinline__ uint32_t scale_bf16(uint32_t w, float f) {
   return pack_bf16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+}
+
+__device__ __forceinline__ int drafts_of(const Misc& m, int b) {
+  return max(m.begin[b + 1] - m.begin[b], 0);
 }
 
 // One row tile's run of token tiles inside a cluster's share.
@@ -178,7 +205,7 @@ struct Segment {
   int slot;   // of its partial outputs
 };
 struct Walk {
-  int64_t at, end, from;  // of the list of runs
+  uint32_t at, end, from;  // of the list of runs
   int b;
 };
 __device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& p, int cluster,
@@ -188,23 +215,23 @@ __device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& 
   s.b = w.b;
   s.length = m.length[w.b];
   s.begin = m.begin[w.b];
-  s.drafts = m.drafts[w.b];
+  s.drafts = drafts_of(m, w.b);
   s.context = max(s.length - s.drafts, 0);
   s.kv_tiles = token_tiles(s.length);
-  const int64_t local = w.at - m.first[w.b];
+  const int local = static_cast<int>(w.at - m.first[w.b]);
   int tile;
   if (m.piece > 0) {
     const int pieces = (s.kv_tiles + m.piece - 1) / m.piece;
-    tile = static_cast<int>(local / pieces);
-    const int k = static_cast<int>(local % pieces);
+    tile = local / pieces;
+    const int k = local % pieces;
     s.kv0 = static_cast<int>(static_cast<int64_t>(s.kv_tiles) * k / pieces);
     s.kv1 = static_cast<int>(static_cast<int64_t>(s.kv_tiles) * (k + 1) / pieces);
     s.slot = 2 * cluster;
     ++w.at;
   } else {
-    tile = static_cast<int>(local / s.kv_tiles);
-    s.kv0 = static_cast<int>(local % s.kv_tiles);
-    s.kv1 = static_cast<int>(min(static_cast<int64_t>(s.kv_tiles), s.kv0 + (w.end - w.at)));
+    tile = local / s.kv_tiles;
+    s.kv0 = local % s.kv_tiles;
+    s.kv1 = min(s.kv_tiles, s.kv0 + static_cast<int>(w.end - w.at));
     // Only a share's first and last row tiles can be cut.
     s.slot = 2 * cluster + (w.at == w.from ? 0 : 1);
     w.at += s.kv1 - s.kv0;
@@ -218,37 +245,49 @@ __device__ __forceinline__ bool special(const Segment& s, int kv) {
   return (kv + 1) * kTokens > s.context;
 }
 
-// Bounded waits of a warp's converged lanes.  One that runs out sets `abort`,
+// Bounded waits of a warp's lanes, which come out together.  One that runs out sets `abort`,
 // after which every wait of the CTA returns at once and the kernel ends with
-// its flag set.
+// its flag set.  (The softmax warps then run their loops out on whatever the
+// buffers hold, so that none is missing at their barriers.)
 struct Waiter {
   int32_t* abort;
   int32_t* flags;
   __device__ __forceinline__ bool operator()(const uint64_t& b, uint32_t parity) const {
     const uint32_t bar = ptx::smem_addr(&b);
-    return __all_sync(~0u, ptx::mbar_try_wait(bar, parity & 1u)) || slow(bar, parity & 1u, false);
+    bool done = ptx::mbar_try_wait(bar, parity & 1u);
+    if (!done) done = slow(bar, parity & 1u, false);
+    __syncwarp();
+    return done;
   }
   // With acquire over the cluster, for what a peer CTA signals.
   __device__ __forceinline__ bool cluster(const uint64_t& b, uint32_t parity) const {
     const uint32_t bar = ptx::smem_addr(&b);
-    return __all_sync(~0u, ptx::mbar_try_wait_cluster(bar, parity & 1u)) ||
-           slow(bar, parity & 1u, true);
+    bool done = ptx::mbar_try_wait_cluster(bar, parity & 1u);
+    if (!done) done = slow(bar, parity & 1u, true);
+    __syncwarp();
+    return done;
+  }
+  // Whether it is over already.
+  __device__ __forceinline__ bool ready(const uint64_t& b, uint32_t parity) const {
+    return __all_sync(~0u, ptx::mbar_test_wait(ptx::smem_addr(&b), parity & 1u));
+  }
+  // For a loop over ready(): whether it may go on after `spins` empty rounds
+  // since `start` (set at the first).
+  __device__ __noinline__ bool patient(int spins, uint64_t& start) const {
+    const uint64_t now = ptx::globaltimer();
+    if (spins == 0) start = now;
+    if (*reinterpret_cast<volatile int32_t*>(abort) != 0) return false;
+    if (now - start <= kWaitLimitNs) return true;
+    *reinterpret_cast<volatile int32_t*>(abort) = 1;
+    raise(flags, MXFP8_FLAG_GEMM_TIMEOUT);
+    return false;
   }
   __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity, bool wide) const {
     uint64_t start = 0;
     for (int i = 0;; ++i) {
-      if (__all_sync(~0u, wide ? ptx::mbar_try_wait_cluster(bar, parity)
-                               : ptx::mbar_try_wait(bar, parity)))
+      if (wide ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity))
         return true;
-      if (i % 16) continue;
-      if (__any_sync(~0u, *reinterpret_cast<volatile int32_t*>(abort) != 0)) return false;
-      const uint64_t now = ptx::globaltimer();
-      if (i == 0) start = now;
-      if (__any_sync(~0u, now - start > kWaitLimitNs)) {
-        *reinterpret_cast<volatile int32_t*>(abort) = 1;
-        raise(flags, MXFP8_FLAG_GEMM_TIMEOUT);
-        return false;
-      }
+      if (i % 16 == 0 && !patient(i, start)) return false;
     }
   }
 };
@@ -264,69 +303,64 @@ struct AttendParams {
 struct AttendMaps {
   CUtensorMap latent, rope;              // boxes of `box` tokens
   CUtensorMap latent_small, rope_small;  // boxes of 8
-  CUtensorMap q, q_rope;                 // boxes of 128 rows
+  CUtensorMap q, q_rope;                 // boxes of 128 and of 64 rows
 };
 
 // Token tiles of a cluster's run in an even deal.
-__device__ __forceinline__ int64_t run_length(int64_t tiles, int clusters) {
-  return max(static_cast<int64_t>(kMinRun), (tiles + clusters - 1) / clusters);
+__device__ __forceinline__ uint32_t run_length(uint32_t tiles, int clusters) {
+  return max(static_cast<uint32_t>(kMinRun), (tiles + clusters - 1) / clusters);
 }
 
-// The deal, by one warp: fills Misc's lists.
+// The deal, by one warp: fills Misc's lists.  (The host has checked that all
+// token tiles number less than 2^31.)
 __device__ __forceinline__ void deal(Misc& m, const AttendParams& ap, int lane) {
   const LatentParams& p = ap.in;
-  int64_t before = 0;
+  uint32_t before = 0;
   int tiles_of_rows = 0;
+  auto list = [&](int b, uint32_t runs) {  // sums of `runs` over the requests up to b
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t v = __shfl_up_sync(~0u, runs, o);
+      if (lane >= o) runs += v;
+    }
+    if (b < p.requests) m.first[b + 1] = before + runs;
+    before += __shfl_sync(~0u, runs, 31);
+  };
   for (int base = 0; base < p.requests; base += 32) {
     const int b = base + lane;
-    int64_t tiles = 0;
+    uint32_t tiles = 0;
     int rt = 0;
     if (b < p.requests) {
       const Request r = load_request(p, b);
       if (r.cut && blockIdx.x == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
       m.length[b] = r.length;
       m.begin[b] = static_cast<uint16_t>(r.begin);
-      m.drafts[b] = static_cast<uint16_t>(r.drafts);
+      if (b == p.requests - 1) m.begin[b + 1] = static_cast<uint16_t>(r.begin + r.drafts);
       rt = r.length > 0 ? row_tiles(r.drafts, p.heads) : 0;
-      tiles = static_cast<int64_t>(rt) * token_tiles(r.length);
+      tiles = static_cast<uint32_t>(rt) * token_tiles(r.length);
     }
     tiles_of_rows += __reduce_add_sync(~0u, rt);
-    for (int o = 1; o < 32; o *= 2) {
-      const int64_t v = __shfl_up_sync(~0u, tiles, o);
-      if (lane >= o) tiles += v;
-    }
-    if (b < p.requests) m.first[b + 1] = before + tiles;
-    before += __shfl_sync(~0u, tiles, 31);
+    list(b, tiles);
   }
   // Pieces: the shortest length, from that of the even deal on, at which all
   // pieces fit the clusters, one a cluster; a lane a length.
-  const int64_t run = run_length(before, ap.clusters);
+  const int run = static_cast<int>(run_length(before, ap.clusters));
   int piece = 0;
   __syncwarp();
-  if (tiles_of_rows <= ap.clusters && run < (1 << 24)) {
-    const int length = static_cast<int>(run) + lane;
+  if (tiles_of_rows <= ap.clusters) {
     int pieces = 0;
     for (int b = 0; b < p.requests; ++b)
-      pieces += m.length[b] > 0 ? row_tiles(m.drafts[b], p.heads) *
-                                      ((token_tiles(m.length[b]) + length - 1) / length)
-                                : 0;
+      pieces += row_tiles(drafts_of(m, b), p.heads) *
+                ((token_tiles(m.length[b]) + run + lane - 1) / (run + lane));
     const uint32_t fits = __ballot_sync(~0u, lane <= kPieceSlack && pieces <= ap.clusters);
-    if (fits != 0u) piece = static_cast<int>(run) + __ffs(fits) - 1;
+    if (fits != 0u) piece = run + __ffs(fits) - 1;
   }
   if (piece > 0) {
     before = 0;
     for (int base = 0; base < p.requests; base += 32) {
       const int b = base + lane;
-      int64_t pieces = 0;
-      if (b < p.requests && m.length[b] > 0)
-        pieces = static_cast<int64_t>(row_tiles(m.drafts[b], p.heads)) *
-                 ((token_tiles(m.length[b]) + piece - 1) / piece);
-      for (int o = 1; o < 32; o *= 2) {
-        const int64_t v = __shfl_up_sync(~0u, pieces, o);
-        if (lane >= o) pieces += v;
-      }
-      if (b < p.requests) m.first[b + 1] = before + pieces;
-      before += __shfl_sync(~0u, pieces, 31);
+      list(b, b < p.requests ? row_tiles(drafts_of(m, b), p.heads) *
+                                   ((token_tiles(m.length[b]) + piece - 1) / piece)
+                             : 0);
     }
   }
   if (lane == 0) {
@@ -343,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   using L = Shape<kLatent>;
   constexpr int kStages = L::kStages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint8_t* smem = smem_raw;
   const uint32_t sbase = ptx::smem_addr(smem);
   Misc& m = *reinterpret_cast<Misc*>(smem + L::kMisc);
   const LatentParams& p = ap.in;
@@ -351,6 +385,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   const uint32_t rank = ptx::cluster_ctarank();
   const int cluster = blockIdx.x / 2;
   auto bar = [&](const uint64_t& b) { return ptx::smem_addr(&b); };
+  if (sbase % 1024u != 0) {  // the swizzles count from 1024-byte boundaries
+    raise(p.flags, MXFP8_FLAG_GEMM_TIMEOUT);
+    return;
+  }
 
   if (warp == 0) {
     // Barriers, a lane a kind.
@@ -367,8 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     if (lane == 7) init(m.weights[0], 8, 1);
     if (lane == 8) init(m.weights_credit[0], 8, 1);
     if (lane == 9) init(m.decided[0], 8, 1);
-    if (lane == 10) init(&m.q_full, 1, 1), init(&m.q_ready, 1, 8);
-    if (lane == 11) init(&m.q_free, 1, 8), init(&m.drained, 1, 1);
+    if (lane == 10) init(&m.q_ready, 1, 8), init(&m.drained, 1, 1);
     if (lane == 12) init(m.tops, 4, 1);
     if (lane == 13) m.abort = 0;
     ptx::fence_mbarrier_init();
@@ -389,9 +426,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   if (warp == 0) deal(m, ap, lane);
   __syncthreads();
 
-  const int64_t all = m.first[p.requests];
-  const int64_t run = m.piece > 0 ? 1 : run_length(all, ap.clusters);
-  const int64_t from = min(all, cluster * run);
+  const uint32_t all = m.first[p.requests];
+  const uint32_t run = m.piece > 0 ? 1 : run_length(all, ap.clusters);
+  const uint32_t from = min(all, cluster * run);
   Walk walk{from, min(all, from + run), from, 0};
   Segment seg{};
   const Waiter wait{&m.abort, p.flags};
@@ -413,27 +450,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       raise(p.flags, MXFP8_FLAG_BAD_INDEX);
       return p.pages;
     };
-    int g = 0;
+    int r = 0;  // places of the ring used
     bool ok = true;
+    auto place = [&](uint32_t& full) {  // the next one, once it is free
+      if (r >= kStages) ok = __all_sync(~0u, wait(m.kv_empty[r % kStages], r / kStages - 1));
+      full = bar(m.kv_full[r % kStages]);
+      if (ok && lane == 0) ptx::mbar_arrive_expect_tx(full, L::kStageBytes);
+      __syncwarp();
+      return ok;
+    };
     while (ok && next_segment(m, p, cluster, walk, seg)) {
       int page[kItems];
 #pragma unroll
       for (int k = 0; k < kItems; ++k) page[k] = page_of(seg.kv0, lane + 32 * k);
-      for (int kv = seg.kv0; kv < seg.kv1; ++kv, ++g) {
-        const int stage = g % kStages;
+      uint32_t full;
+      // The queries: half of this CTA's columns and half of the rows' rotary
+      // part a place.
+      for (int half = 0; half < 2 && place(full); ++half, ++r) {
+        const uint32_t dst = sbase + r % kStages * L::kStageBytes;
+        const int row = seg.begin * p.heads + seg.row0;
+        if (lane < L::kAtoms / 2)
+          ptx::tma_load_2d(dst + lane * kQAtomBytes, &maps.q,
+                           static_cast<int>(rank) * L::kHalf +
+                               (half * (L::kAtoms / 2) + lane) * 64,
+                           row, full, ptx::policy_evict_first());
+        else if (lane == L::kAtoms / 2)
+          ptx::tma_load_2d(dst + L::kAtoms * kAtomBytes, &maps.q_rope,
+                           static_cast<int>(rank) * 32, row + half * 64, full,
+                           ptx::policy_evict_first());
+        __syncwarp();
+      }
+      for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++r) {
         int next[kItems];
 #pragma unroll
         for (int k = 0; k < kItems; ++k)
           next[k] = kv + 1 < seg.kv1 ? page_of(kv + 1, lane + 32 * k) : p.pages;
-        if (g >= kStages) ok = wait(m.kv_empty[stage], g / kStages - 1);
-        if (!ok) break;
-        const uint32_t full = bar(m.kv_full[stage]);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(full, L::kStageBytes);
-        __syncwarp();
+        if (!place(full)) break;
         const bool fine = special(seg, kv);
         const int box = box_of(kv);
         const int items = kTokens / box * (L::kAtoms + 1);
-        const uint32_t dst = sbase + stage * L::kStageBytes;
+        const uint32_t dst = sbase + r % kStages * L::kStageBytes;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
           const int i = lane + 32 * k;
@@ -457,7 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     }
     // Copies in flight land before the CTA leaves (they have, unless a wait
     // ran out).
-    for (int i = max(0, g - kStages); i < g; ++i)
+    for (int i = max(0, r - kStages); i < r; ++i)
       ptx::mbar_wait(bar(m.kv_full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u,
                      kWaitLimitNs);
   } else if (warp == 1) {
@@ -468,12 +524,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     constexpr uint32_t kScores = ptx::idesc_bf16(kTokens, false);
     constexpr uint32_t kOutputs = ptx::idesc_bf16(L::kHalf, true);
     const uint32_t q_rope = sbase + L::kQRope;
-    int g = 0;
+    int g = 0;  // token tiles before the segment
+    int r = 0;  // places of the ring before its first token tile
     uint32_t segments = 0;
     bool ok = true;
-    auto scores = [&](int j, int kv) {
-      const int stage = j % kStages;
-      if (!wait(special(seg, kv) ? m.kv_ready[stage] : m.kv_full[stage], j / kStages)) return false;
+    auto tile_bar = [&](int i) -> const uint64_t& {
+      const int stage = (r + i) % kStages;
+      return special(seg, seg.kv0 + i) ? m.kv_ready[stage] : m.kv_full[stage];
+    };
+    auto scores = [&](int i) {
+      const int j = g + i, stage = (r + i) % kStages;
       ptx::tc_fence_after();
       const uint32_t kvb = sbase + stage * L::kStageBytes;
       const uint32_t d = tmem + L::kS + (j & 1) * kTokens;
@@ -492,38 +552,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         ptx::mma_commit(done);
       }
       __syncwarp();
-      return true;
+    };
+    auto outputs = [&](int i) {
+      const int j = g + i, stage = (r + i) % kStages;
+      ptx::tc_fence_after();
+      const uint32_t kvb = sbase + stage * L::kStageBytes;
+      const uint32_t weights = sbase + L::kX + (j & 1) * kExchangeBytes;
+      const uint32_t add = i > 0;
+      const uint32_t empty = bar(m.kv_empty[stage]), done = bar(m.pv_done[j & 1]);
+      if (ptx::elect_one()) {
+#pragma unroll
+        for (int k = 0; k < kTokens / 16; ++k)
+          ptx::mma_f16_ss(tmem, ptx::desc_kmajor_sw128(weights + k * 32),
+                          ptx::desc_mnmajor_sw128(kvb + k * 2048, kAtomBytes), kOutputs,
+                          k > 0 ? 1u : add);
+        ptx::mma_commit(empty);
+        ptx::mma_commit(done);
+      }
+      __syncwarp();
     };
     while (ok && next_segment(m, p, cluster, walk, seg)) {
-      ok = wait(m.q_ready, segments++);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      ok = scores(g, seg.kv0);
-      if (ok && seg.kv0 + 1 < seg.kv1) ok = scores(g + 1, seg.kv0 + 1);
-      for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g) {
-        // The scores read out, their buffer takes the tile after the next.
-        if (kv + 2 < seg.kv1) ok = wait(m.s_free[g & 1], g >> 1) && scores(g + 2, kv + 2);
-        if (!ok || !wait(m.p_full[g & 1], g >> 1)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const int stage = g % kStages;
-        const uint32_t kvb = sbase + stage * L::kStageBytes;
-        const uint32_t weights = sbase + L::kP + (g & 1) * kPBytes;
-        const uint32_t add = kv > seg.kv0;
-        const uint32_t empty = bar(m.kv_empty[stage]), done = bar(m.pv_done[g & 1]);
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kTokens / 16; ++k)
-            ptx::mma_f16_ss(tmem, ptx::desc_kmajor_sw128(weights + k * 32),
-                            ptx::desc_mnmajor_sw128(kvb + k * 2048, kAtomBytes), kOutputs,
-                            k > 0 ? 1u : add);
-          ptx::mma_commit(empty);
-          ptx::mma_commit(done);
-        }
-        __syncwarp();
+      ok = __all_sync(~0u, wait(m.q_ready, segments++));
+      if (lane == 0) {  // every softmax warp has read the queries
+        ptx::mbar_arrive(bar(m.kv_empty[r % kStages]));
+        ptx::mbar_arrive(bar(m.kv_empty[(r + 1) % kStages]));
       }
+      r += 2;
+      const int tiles = seg.kv1 - seg.kv0;
+      // Whichever is ready: the scores of tile s (its tokens there, and the
+      // scores of tile s - 2 read out of their buffer) or the outputs of tile o
+      // (its weights there).  Neither waits behind the other, so a late tile
+      // does not keep an earlier one's place in the ring.
+      int s = 0, o = 0, spins = 0;
+      uint64_t start = 0;
+      while (ok && o < tiles) {
+        if (s < tiles && s <= o + 2 && wait.ready(tile_bar(s), (r + s) / kStages) &&
+            (s < 2 || wait.ready(m.s_free[(g + s) & 1], (g + s - 2) >> 1))) {
+          scores(s++);
+          spins = 0;
+        } else if (o < s && wait.ready(m.p_full[(g + o) & 1], (g + o) >> 1)) {
+          outputs(o++);
+          spins = 0;
+        } else if (spins++ % 64 == 0) {
+          ok = __all_sync(~0u, wait.patient(spins - 1, start));
+        }
+      }
+      g += tiles;
+      r += tiles;
     }
     // Nothing runs on when tensor memory is freed.
     if (ptx::elect_one()) ptx::mma_commit(bar(m.drained));
@@ -531,14 +606,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     ptx::mbar_wait(bar(m.drained), 0, kWaitLimitNs);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- mender
-    int g = 0;
+    int r = 0;
     bool ok = true;
     while (ok && next_segment(m, p, cluster, walk, seg)) {
-      for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++g) {
-        const int stage = g % kStages;
-        ok = wait(m.kv_full[stage], g / kStages);
+      for (int kv = seg.kv0 - 2; ok && kv < seg.kv1; ++kv, ++r) {  // two of queries first
+        const int stage = r % kStages;
+        ok = __all_sync(~0u, wait(m.kv_full[stage], r / kStages));
         if (!ok) break;
-        if (special(seg, kv)) {
+        if (kv >= seg.kv0 && special(seg, kv)) {
           uint8_t* kvp = smem + stage * L::kStageBytes;
           const int n0 = max(seg.context - kv * kTokens, 0);
           const int n1 = min(seg.length - kv * kTokens, kTokens);
@@ -582,28 +657,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         }
       }
     }
-  } else if (warp == 3) {
-    // --------------------------------------------------------- query loader
-    uint32_t segments = 0;
-    while (next_segment(m, p, cluster, walk, seg)) {
-      if (segments > 0) wait(m.q_free, segments - 1);
-      ++segments;
-      const uint32_t full = bar(m.q_full);
-      if (lane == 0)
-        ptx::mbar_arrive_expect_tx(full, L::kAtoms * kQAtomBytes + kQRopeBytes);
-      __syncwarp();
-      const int row = seg.begin * p.heads + seg.row0;
-      if (lane < L::kAtoms)
-        ptx::tma_load_2d(sbase + L::kRecv + lane * kQAtomBytes, &maps.q,
-                         static_cast<int>(rank) * L::kHalf + lane * 64, row, full,
-                         ptx::policy_evict_first());
-      else if (lane == L::kAtoms)
-        ptx::tma_load_2d(sbase + L::kQRope, &maps.q_rope, static_cast<int>(rank) * 32, row, full,
-                         ptx::policy_evict_first());
-      __syncwarp();
-    }
-    if (segments > 0) ptx::mbar_wait(bar(m.q_full), (segments - 1) & 1u, kWaitLimitNs);
-  } else {
+  } else if (warp >= kSoftmaxWarp) {
     // --------------------------------------------------------------- softmax
     const int group = (warp - kSoftmaxWarp) / 4;  // takes the tiles of this parity
     const int quarter = warp & 3;  // the 32 tensor-memory lanes this warp reaches
@@ -611,11 +665,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t score = lanes + L::kS + group * kTokens;
     const uint32_t peer = rank ^ 1u;
-    const uint32_t recv_offset = L::kRecv + group * kRecvBytes + quarter * 4096u + lane * 16u;
+    const uint32_t recv_offset =
+        L::kX + group * kExchangeBytes + quarter * 4096u + lane * 16u;
     const float4* recv = reinterpret_cast<const float4*>(smem + recv_offset);
     // A row of weights is one 128-byte swizzled row: this CTA's 32 tokens are
     // chunks 4 rank .. 4 rank + 3, in its own operand and in the peer's.
-    const uint32_t p_row = L::kP + group * kPBytes + row * 128u;
+    const uint32_t p_row = L::kX + group * kExchangeBytes + row * 128u;
     auto chunk_at = [&](uint32_t half, int c) { return ((half * 4u + c) ^ (row & 7u)) * 16u; };
     const uint64_t& recv_bar = m.recv[group][quarter];
     const uint64_t& weights_bar = m.weights[group][quarter];
@@ -624,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     const uint32_t to_weights = ptx::map_to_rank(sbase + p_row, peer);
     const uint32_t to_weights_bar = ptx::map_to_rank(bar(weights_bar), peer);
     const uint32_t to_sum = ptx::map_to_rank(ptx::smem_addr(&m.peer[group][row]), peer);
-    const uint32_t to_top = ptx::map_to_rank(ptx::smem_addr(&m.mine[group ^ 1][row]), peer);
+    const uint32_t to_top = ptx::map_to_rank(ptx::smem_addr(&m.peer_top[row]), peer);
     const uint32_t to_top_bar = ptx::map_to_rank(bar(m.tops[quarter]), peer);
     const uint32_t to_recv_credit = ptx::map_to_rank(bar(m.recv_credit[group][quarter]), peer);
     const uint32_t to_weights_credit =
@@ -633,38 +688,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     uint32_t decisions = 0;  // tiles of this quarter's rows, of both groups
     uint32_t firsts = 0;     // row tiles of this quarter
     int g = 0;               // token tiles before the segment
-    for (uint32_t segments = 0; next_segment(m, p, cluster, walk, seg);
-         g += seg.kv1 - seg.kv0, ++segments) {
+    int r = 0;               // places of the ring before its first token tile
+    // The peer may send this group its scores; after that, a permit follows
+    // every tile whose outputs are added (its weights lay where scores land).
+    if (lane == 0) ptx::mbar_arrive_remote_relaxed(to_recv_credit);
+    for (uint32_t segments = 0; next_segment(m, p, cluster, walk, seg); ++segments) {
       const size_t q_row = static_cast<size_t>(seg.begin) * p.heads + seg.row0 + row;
       const bool mine = row < seg.valid;
       const bool active = quarter * 32 < seg.valid;  // of the warp
       const int tiles = seg.kv1 - seg.kv0;
       const int i0 = (g & 1) != group;  // this group's first tile
-      // Queries: from where they landed into tensor memory, half of this CTA's
-      // columns a group.
-      wait(m.q_full, segments);
+      // Queries, from the ring: half of this CTA's columns a group into tensor
+      // memory, and half of a row's rotary part (already swizzled).
+      wait(m.kv_full[r % kStages], r / kStages);
+      wait(m.kv_full[(r + 1) % kStages], (r + 1) / kStages);
       if (active) {
-        const uint8_t* src = smem + L::kRecv + row * 128;
+        const uint8_t* src = smem + (r + group) % kStages * L::kStageBytes + row * 128;
 #pragma unroll
         for (int half = 0; half < L::kAtoms / 2; ++half) {
-          const int atom = group * (L::kAtoms / 2) + half;
           uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + atom * kQAtomBytes +
+            const uint4 x = *reinterpret_cast<const uint4*>(src + half * kQAtomBytes +
                                                             ((i ^ (row & 7)) * 16));
             v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
           }
-          ptx::tmem_st_32x32b_x32(lanes + L::kQ + atom * 32, v);
+          ptx::tmem_st_32x32b_x32(lanes + L::kQ + (group * (L::kAtoms / 2) + half) * 32, v);
         }
+        const uint8_t* rope = smem + (r + row / 64) % kStages * L::kStageBytes +
+                              L::kAtoms * kAtomBytes + row % 64 * 64;
+#pragma unroll
+        for (int i = 2 * group; i < 2 * group + 2; ++i)
+          *reinterpret_cast<uint4*>(smem + L::kQRope + row * 64 + i * 16) =
+              *reinterpret_cast<const uint4*>(rope + i * 16);
         ptx::tmem_wait_st();
+        ptx::fence_proxy_async_smem();
       }
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(bar(m.q_ready));
-      // Every warp has read the queries: their landing place is the peer's to
-      // send to.
-      wait(m.q_ready, segments);
+      r += 2;
       if (!active) {
         for (int i = i0; i < tiles; i += 2) {
           wait(m.s_full[group], (g + i) >> 1);
@@ -676,13 +739,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           // second arrival at one phase.)
           wait(m.p_full[group], (g + i) >> 1);
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(m.q_free));
+        // Not on to the next segment before every warp has come to this one.
+        wait(m.q_ready, segments);
+        g += tiles;
+        r += tiles;
         continue;
-      }
-      if (lane == 0 && i0 < tiles) {
-        ptx::mbar_arrive_remote_relaxed(to_recv_credit);
-        ptx::mbar_arrive_remote_relaxed(to_weights_credit);
       }
       // What this row sees of the drafts.
       const int t = (seg.row0 + row) / p.heads;
@@ -695,11 +756,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       for (int i = i0; i < tiles; i += 2, ++exchanges) {
         const int kv = seg.kv0 + i;
         const uint32_t decision = decisions + i;
-        const bool last_own = i + 2 >= tiles;
+        if (i > i0) {
+          wait(m.pv_done[group], (g + i - 2) >> 1);
+          if (lane == 0) ptx::mbar_arrive_remote_relaxed(to_recv_credit);
+        }
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(bar(recv_bar), 32u * 32u * 4u);
           ptx::mbar_arrive_expect_tx(bar(weights_bar), 32u * (64u + 8u));
-          if (i == 0) ptx::mbar_arrive_expect_tx(bar(m.tops[quarter]), 32u * 8u);
+          if (i == 0) ptx::mbar_arrive_expect_tx(bar(m.tops[quarter]), 32u * 4u);
         }
         wait(m.s_full[group], (g + i) >> 1);
         ptx::tc_fence_after();
@@ -711,8 +775,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(m.s_free[group]));
         if (special(seg, kv)) {
-          const int stage = (g + i) % kStages;
-          wait(m.kv_ready[stage], (g + i) / kStages);
+          const int stage = (r + i) % kStages;
+          wait(m.kv_ready[stage], (r + i) / kStages);
           const uint64_t bad = m.bad[stage];
           if (bad != 0) {
             const uint32_t bad_other = static_cast<uint32_t>(bad >> (32 * peer));
@@ -732,20 +796,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                                   make_uint4(other[4 * c], other[4 * c + 1], other[4 * c + 2],
                                              other[4 * c + 3]),
                                   to_scores_bar);
-        if (i > i0) {
-          // This group's last outputs are added: its weights' place is free.
-          wait(m.pv_done[group], (g + i - 2) >> 1);
-          if (lane == 0) ptx::mbar_arrive_remote_relaxed(to_weights_credit);
-        }
         wait.cluster(recv_bar, exchanges);
         float z[32];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           const float4 x = recv[c * 32];
-          z[4 * c] = __uint_as_float(own[4 * c]) + x.x;
-          z[4 * c + 1] = __uint_as_float(own[4 * c + 1]) + x.y;
-          z[4 * c + 2] = __uint_as_float(own[4 * c + 2]) + x.z;
-          z[4 * c + 3] = __uint_as_float(own[4 * c + 3]) + x.w;
+          const float2 lo = add2(make_float2(__uint_as_float(own[4 * c]),
+                                             __uint_as_float(own[4 * c + 1])),
+                                 make_float2(x.x, x.y));
+          const float2 hi = add2(make_float2(__uint_as_float(own[4 * c + 2]),
+                                             __uint_as_float(own[4 * c + 3])),
+                                 make_float2(x.z, x.w));
+          z[4 * c] = lo.x, z[4 * c + 1] = lo.y, z[4 * c + 2] = hi.x, z[4 * c + 3] = hi.y;
         }
         if (special(seg, kv)) {
           const int at = kv * kTokens;
@@ -763,24 +825,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           for (int c = 0; c < 32; ++c)
             if (!(bits >> c & 1u)) z[c] = -INFINITY;
         }
-        float top = fmaxf(z[0], z[1]);
+        float tops[4];
 #pragma unroll
-        for (int c = 2; c < 32; c += 2) top = fmaxf(top, fmaxf(z[c], z[c + 1]));
-        top *= p.scale_log2;
+        for (int c = 0; c < 4; ++c) tops[c] = max3(z[c], z[c + 4], z[c + 8]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tops[c] = max3(tops[c], z[c + 12], z[c + 16]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tops[c] = max3(tops[c], z[c + 20], z[c + 24]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tops[c] = fmaxf(tops[c], z[c + 28]);
+        const float top =
+            fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
         // The received scores have returned their values (each went into the
-        // maximum), so the peer may overwrite them.
+        // maximum), so the peer's weights may come over them.  (A release here
+        // would wait for this CTA's own stores to the peer: it cost 60 us of 320
+        // on 8 x 64k tokens, 128 heads.)
         __syncwarp();
-        if (lane == 0 && !last_own) ptx::mbar_arrive_remote_relaxed(to_recv_credit);
+        if (lane == 0) ptx::mbar_arrive_remote_relaxed(to_weights_credit);
         // Weights of this CTA's tokens: under the halves' common maximum in the
         // first tile, then under the last reference this group knows, or one
         // whole steps above it.
         float under;
         if (i == 0) {
-          // (It lands where the other group keeps its sums, which that group
-          // writes after this decision.)
-          ptx::st_async_remote_v2(to_top, __float_as_uint(top), __float_as_uint(top), to_top_bar);
+          ptx::st_async_remote(to_top, __float_as_uint(top), to_top_bar);
           wait.cluster(m.tops[quarter], firsts);
-          under = fmaxf(top, m.mine[group ^ 1][row].x);
+          under = fmaxf(top, m.peer_top[row]);
           m.reference[decision & 1][row] = under;
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
@@ -797,15 +866,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         base = under;
         const float sub = under == -INFINITY ? 0.0f : under;
         uint32_t w[16];
-        float sum0 = 0.0f, sum1 = 0.0f;
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float2 by = make_float2(p.scale_log2, p.scale_log2), less = make_float2(-sub, -sub);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          w[c] = pack_bf16(exp2_approx(fmaf(z[2 * c], p.scale_log2, -sub)),
-                           exp2_approx(fmaf(z[2 * c + 1], p.scale_log2, -sub)));
-          sum0 += __uint_as_float(w[c] << 16);
-          sum1 += __uint_as_float(w[c] & 0xFFFF0000u);
+          const float2 x = fma2(make_float2(z[2 * c], z[2 * c + 1]), by, less);
+          w[c] = pack_bf16(exp2_approx(x.x), exp2_approx(x.y));
+          sum[c % 2] = add2(sum[c % 2], make_float2(__uint_as_float(w[c] << 16),
+                                                    __uint_as_float(w[c] & 0xFFFF0000u)));
         }
-        total += sum0 + sum1;
+        sum[0] = add2(sum[0], sum[1]);
+        total += sum[0].x + sum[0].y;
         wait.cluster(m.weights_credit[group][quarter], exchanges);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -814,52 +885,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                                   to_weights_bar);
         ptx::st_async_remote_v2(to_sum, __float_as_uint(base), __float_as_uint(total),
                                 to_weights_bar);
-        m.mine[group][row] = make_float2(base, total);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          *reinterpret_cast<uint4*>(smem + p_row + chunk_at(rank, c)) =
+              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         // The row's reference after this tile: the largest of the one before
         // and the two halves'.
-        wait.cluster(weights_bar, exchanges);
-        const float theirs = m.peer[group][row].x;
         float before = -INFINITY;
         if (i > 0) {
           wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
           before = m.reference[(decision - 1) & 1][row];
         }
+        wait.cluster(weights_bar, exchanges);
+        const float theirs = m.peer[group][row].x;
         const float now = fmaxf(before, fmaxf(base, theirs));
         if (i > 0) m.reference[decision & 1][row] = now;
-        if (__any_sync(~0u, now != base)) {
-          const float f = shift_factor(base, now);
+        // Seldom anything else: all three references are the same.
+        if (__any_sync(~0u, now != base || now != theirs || (i > 0 && now != before))) {
+          const float f_own = shift_factor(base, now), f_peer = shift_factor(theirs, now);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) w[c] = scale_bf16(w[c], f);
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(smem + p_row + chunk_at(rank, c)) =
-              make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        if (__any_sync(~0u, now != theirs)) {
-          const float f = shift_factor(theirs, now);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(smem + p_row + chunk_at(peer, c));
+          for (uint32_t c = 0; c < 8; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(smem + p_row + chunk_at(0, c));
+            const float f = c / 4 == rank ? f_own : f_peer;
             const uint4 v = *at;
             *at = make_uint4(scale_bf16(v.x, f), scale_bf16(v.y, f), scale_bf16(v.z, f),
                              scale_bf16(v.w, f));
           }
-        }
-        if (i > 0 && __any_sync(~0u, now != before)) {
-          // The outputs so far, once the tile before has been added.
-          const float f = shift_factor(before, now);
-          wait(m.pv_done[group ^ 1], (g + i - 1) >> 1);
-          ptx::tc_fence_after();
+          if (i > 0) {
+            // The outputs so far, once the tile before has been added.
+            const float f = shift_factor(before, now);
+            wait(m.pv_done[group ^ 1], (g + i - 1) >> 1);
+            ptx::tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < L::kHalf; c += 32) {
-            ptx::tmem_ld_32x32b_x32(lanes + c, own);
-            ptx::tmem_wait_ld();
+            for (int c = 0; c < L::kHalf; c += 32) {
+              ptx::tmem_ld_32x32b_x32(lanes + c, own);
+              ptx::tmem_wait_ld();
 #pragma unroll
-            for (int q = 0; q < 32; ++q) own[q] = __float_as_uint(__uint_as_float(own[q]) * f);
-            ptx::tmem_st_32x32b_x32(lanes + c, own);
+              for (int q = 0; q < 32; ++q) own[q] = __float_as_uint(__uint_as_float(own[q]) * f);
+              ptx::tmem_st_32x32b_x32(lanes + c, own);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
           }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
         }
         known = now;
         ptx::fence_proxy_async_smem();
@@ -879,20 +946,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       wait(m.decided[last & 1][quarter], last >> 1);
       wait(m.pv_done[(g + tiles - 1) & 1], (g + tiles - 1) >> 1);
       ptx::tc_fence_after();
-      ptx::fence_proxy_async_smem();  // the next queries come over what was read here
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(m.q_free));
       const float now = m.reference[last & 1][row];
-      // Both halves' sums, of the groups that had a tile.
-      float sum_own = 0.0f, sum_peer = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        if (tiles < 2 && (g & 1) != q) continue;
-        const float2 a = m.mine[q][row], b = m.peer[q][row];
-        sum_own += a.y * shift_factor(a.x, now);
-        sum_peer += b.y * shift_factor(b.x, now);
-      }
-      total = sum_own + sum_peer;
+      // The sums, of both groups and both halves, under it.  The groups' pass
+      // through the place of the last tile's weights, which its outputs have read
+      // and the peer has no permit for yet.
+      float* sums = reinterpret_cast<float*>(smem + L::kX + ((g + tiles - 1) & 1) * kExchangeBytes +
+                                             quarter * 4096) +
+                    lane;
+      total *= shift_factor(base, now);
+      if (i0 < tiles) total += m.peer[group][row].y * shift_factor(m.peer[group][row].x, now);
+      sums[group * 32] = i0 < tiles ? total : 0.0f;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+      total = sums[0] + sums[32];
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
+      if (lane == 0 && i0 < tiles) ptx::mbar_arrive_remote_relaxed(to_recv_credit);
       const bool whole = seg.kv0 == 0 && seg.kv1 == seg.kv_tiles;
       const int column0 = static_cast<int>(rank) * L::kHalf + group * (L::kHalf / 2);
       const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
@@ -927,6 +994,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                             __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
         }
       }
+      g += tiles;
+      r += tiles;
     }
   }
 
@@ -951,7 +1020,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
   const LatentParams& p = ap.in;
   const int row = threadIdx.x % kTileRows;
   const int column = blockIdx.y * 8 + (threadIdx.x / kTileRows) * 4;
-  int64_t all = 0, begin = 0, end = 0;
+  uint32_t all = 0, begin = 0, end = 0;
   int tiles = 0, covered0 = p.rows, covered1 = p.rows;
   size_t out_row = 0;
   bool mine = false, found = false;
@@ -967,13 +1036,13 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
     const int tile = static_cast<int>(blockIdx.x) - tiles;
     if (tile >= 0 && tile < rt) {
       found = true;
-      begin = all + static_cast<int64_t>(tile) * kt;
+      begin = all + static_cast<uint32_t>(tile) * kt;
       end = begin + kt;
       mine = tile * kTileRows + row < r.drafts * p.heads;
       out_row = static_cast<size_t>(r.begin) * p.heads + tile * kTileRows + row;
     }
     tiles += rt;
-    all += static_cast<int64_t>(rt) * kt;
+    all += static_cast<uint32_t>(rt) * kt;
   }
   auto write = [&](size_t at, float4 v) {
     *reinterpret_cast<uint2*>(p.out + at * kLatent + column) =
@@ -995,17 +1064,17 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
   }
   // The clusters that shared the row tile: its pieces', or those whose runs
   // meet it.
-  const int64_t run = piece > 0 ? 1 : run_length(all, ap.clusters);
-  const int c0 = static_cast<int>(begin / run), c1 = static_cast<int>((end - 1) / run);
+  const uint32_t run = piece > 0 ? 1 : run_length(all, ap.clusters);
+  const uint32_t c0 = begin / run, c1 = (end - 1) / run;
   if (c0 == c1) return;  // one cluster wrote the whole
-  auto slot_of = [&](int c) { return 2 * c + (c * run < begin ? 1 : 0); };
+  auto slot_of = [&](uint32_t c) { return 2 * c + (c * run < begin ? 1 : 0); };
   float top = -INFINITY;
-  for (int c = c0; c <= c1; ++c) top = fmaxf(top, ap.stats[slot_of(c) * kTileRows + row].x);
+  for (uint32_t c = c0; c <= c1; ++c) top = fmaxf(top, ap.stats[slot_of(c) * kTileRows + row].x);
   float4 sum = zero;
   float total = 0.0f;
 #pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const int slot = slot_of(c);
+  for (uint32_t c = c0; c <= c1; ++c) {
+    const uint32_t slot = slot_of(c);
     const float2 st = ap.stats[slot * kTileRows + row];
     const float4 v =
         ap.partial[(static_cast<size_t>(slot) * (kLatent / 4) + column / 4) * kTileRows + row];
@@ -1025,8 +1094,8 @@ constexpr int kMaxClusters = 80;
 template <int kLatent>
 constexpr uint32_t smem_bytes() {
   static_assert(MXFP8_MAX_LATENT_ROWS <= 65535, "row numbers fit 16 bits");
-  static_assert(Shape<kLatent>::kMisc + sizeof(Misc) + 1024 <= 232448, "shared memory of a CTA");
-  return Shape<kLatent>::kMisc + sizeof(Misc) + 1024;
+  static_assert(Shape<kLatent>::kMisc + sizeof(Misc) <= 232448, "shared memory of a CTA");
+  return Shape<kLatent>::kMisc + sizeof(Misc);
 }
 
 // Clusters that run at once on the current device, asked once.
@@ -1079,15 +1148,17 @@ CUresult encode_cache(CUtensorMap* map, const LatentParams& p, int first, int co
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// q [rows x heads][latent + 64], boxes of 128 rows.
+// q [rows x heads][latent + 64].
 CUresult encode_queries(CUtensorMap* map, const LatentParams& p, int latent, int first,
-                        int columns, int box_columns, CUtensorMapSwizzle swizzle) {
+                        int columns, int box_columns, int box_rows,
+                        CUtensorMapSwizzle swizzle) {
   const EncodeTiled fn = encode_tiled();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns),
                         static_cast<cuuint64_t>(p.rows) * p.heads};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(latent + kRope) * 2};
-  cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box_columns), kTileRows};
+  cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box_columns),
+                         static_cast<cuuint32_t>(box_rows)};
   cuuint32_t elem[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.q + first), dims,
             strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
@@ -1113,8 +1184,8 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
       encode_cache(&maps.rope, p, kLatent, kRope, ap.box, 32, k64) != CUDA_SUCCESS ||
       encode_cache(&maps.latent_small, p, 0, kLatent, kSmallBox, 64, k128) != CUDA_SUCCESS ||
       encode_cache(&maps.rope_small, p, kLatent, kRope, kSmallBox, 32, k64) != CUDA_SUCCESS ||
-      encode_queries(&maps.q, p, kLatent, 0, kLatent, 64, k128) != CUDA_SUCCESS ||
-      encode_queries(&maps.q_rope, p, kLatent, kLatent, kRope, 32, k64) != CUDA_SUCCESS)
+      encode_queries(&maps.q, p, kLatent, 0, kLatent, 64, kTileRows, k128) != CUDA_SUCCESS ||
+      encode_queries(&maps.q_rope, p, kLatent, kLatent, kRope, 32, kTileRows / 2, k64) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
 
   cudaLaunchAttribute attr;

@@ -47,6 +47,18 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
+// Whether the phase is over, at once (try_wait may suspend the thread).
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -389,6 +401,15 @@ __device__ __forceinline__ void st_async_remote_v2(uint32_t remote_addr, uint32_
           remote_addr),
       "r"(a), "r"(b), "r"(remote_bar)
       : "memory");
+}
+// Store 4 bytes into a peer CTA's shared memory; the byte count completes on
+// the peer's mbarrier.
+__device__ __forceinline__ void st_async_remote(uint32_t remote_addr, uint32_t a,
+                                                uint32_t remote_bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
+                   remote_addr),
+               "r"(a), "r"(remote_bar)
+               : "memory");
 }
 
 // ------------------------------------------------ programmatic dependent launch
