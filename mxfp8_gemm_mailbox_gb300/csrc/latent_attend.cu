@@ -39,8 +39,9 @@
 // joins in a fixed order.
 //
 // Warps of a CTA:
-//   0      producer: TMA boxes into a ring, a lane a box: a row tile's queries
-//          in two places of it, then its token tiles;
+//   0, 3   producers: TMA boxes into a ring, a lane a box: a row tile's queries
+//          in two places of it, then its token tiles; a warp every other place
+//          (a place costs its warp 0.5 to 1.2 us of look-ups and issue);
 //   1      MMA issuer;
 //   2      mender of the tiles that reach the drafts or the length: zeroes the
 //          tokens past the length and drafts that are not finite;
@@ -433,26 +434,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   Segment seg{};
   const Waiter wait{&m.abort, p.flags};
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // -------------------------------------------------------------- producer
-    // A lane a box (one thread's copies are served one after another); the
-    // page of a lane's box is looked up one tile ahead.
+    // A lane a box (one thread's copies are served one after another).  The
+    // page of a lane's box is read one of this warp's tiles ahead.
+    const int which = warp == 3;
     constexpr int kItems = (kTokens / kSmallBox * (L::kAtoms + 1) + 31) / 32;  // of a lane
     const uint64_t keep = ptx::policy_evict_last();
-    auto box_of = [&](int kv) { return special(seg, kv) ? kSmallBox : ap.box; };
-    auto page_of = [&](int kv, int i) {
-      const int box = box_of(kv);
+    // The page of box i of tile kv: in the pool, or past it (then the copy fills
+    // zeros) for what lies past the length.
+    auto read_page = [&](int kv, int i) {
+      const int box = special(seg, kv) ? kSmallBox : ap.box;
       const int token = kv * kTokens + i / (L::kAtoms + 1) * box;
-      // Past the length, and past the pool, the copy fills zeros.
       if (i >= kTokens / box * (L::kAtoms + 1) || token >= seg.length) return p.pages;
-      const int page = p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
-      if (page >= 0 && page < p.pages) return page;
-      raise(p.flags, MXFP8_FLAG_BAD_INDEX);
-      return p.pages;
+      return p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
     };
-    int r = 0;  // places of the ring used
+    int r = 0;  // places of the ring, of both warps
     bool ok = true;
-    auto place = [&](uint32_t& full) {  // the next one, once it is free
+    auto place = [&](uint32_t& full) {  // place r, once it is free
       if (r >= kStages) ok = __all_sync(~0u, wait(m.kv_empty[r % kStages], r / kStages - 1));
       full = bar(m.kv_full[r % kStages]);
       if (ok && lane == 0) ptx::mbar_arrive_expect_tx(full, L::kStageBytes);
@@ -460,13 +459,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       return ok;
     };
     while (ok && next_segment(m, p, cluster, walk, seg)) {
+      // This warp's first token tile.
+      const int first = seg.kv0 + ((r & 1) != which);
       int page[kItems];
 #pragma unroll
-      for (int k = 0; k < kItems; ++k) page[k] = page_of(seg.kv0, lane + 32 * k);
+      for (int k = 0; k < kItems; ++k)
+        page[k] = first < seg.kv1 ? read_page(first, lane + 32 * k) : p.pages;
       uint32_t full;
       // The queries: half of this CTA's columns and half of the rows' rotary
       // part a place.
-      for (int half = 0; half < 2 && place(full); ++half, ++r) {
+      for (int half = 0; half < 2; ++half, ++r) {
+        if ((r & 1) != which) continue;
+        if (!place(full)) break;
         const uint32_t dst = sbase + r % kStages * L::kStageBytes;
         const int row = seg.begin * p.heads + seg.row0;
         if (lane < L::kAtoms / 2)
@@ -480,20 +484,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                            ptx::policy_evict_first());
         __syncwarp();
       }
-      for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++r) {
+      if (!ok) break;
+      const int r0 = r - seg.kv0;
+      for (int kv = first; kv < seg.kv1; kv += 2) {
+        r = r0 + kv;
         int next[kItems];
 #pragma unroll
         for (int k = 0; k < kItems; ++k)
-          next[k] = kv + 1 < seg.kv1 ? page_of(kv + 1, lane + 32 * k) : p.pages;
+          next[k] = kv + 2 < seg.kv1 ? read_page(kv + 2, lane + 32 * k) : p.pages;
         if (!place(full)) break;
         const bool fine = special(seg, kv);
-        const int box = box_of(kv);
+        const int box = fine ? kSmallBox : ap.box;
         const int items = kTokens / box * (L::kAtoms + 1);
         const uint32_t dst = sbase + r % kStages * L::kStageBytes;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
           const int i = lane + 32 * k;
           if (i >= items) continue;
+          if (page[k] < 0 || page[k] > p.pages ||
+              (page[k] == p.pages && kv * kTokens + i / (L::kAtoms + 1) * box < seg.length)) {
+            raise(p.flags, MXFP8_FLAG_BAD_INDEX);
+            page[k] = p.pages;
+          }
           const int at = i / (L::kAtoms + 1) * box, atom = i % (L::kAtoms + 1);
           const int slot = (kv * kTokens + at) % p.page_size;
           if (atom < L::kAtoms)
@@ -510,12 +522,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
 #pragma unroll
         for (int k = 0; k < kItems; ++k) page[k] = next[k];
       }
+      r = r0 + seg.kv1;
     }
-    // Copies in flight land before the CTA leaves (they have, unless a wait
-    // ran out).
-    for (int i = max(0, r - kStages); i < r; ++i)
+    // Copies in flight land before the CTA leaves: each was waited for by the
+    // mender, which passes every place, unless a wait ran out.
+    for (int i = max(0, r - kStages); !ok && i < r; ++i)
       ptx::mbar_wait(bar(m.kv_full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u,
-                     kWaitLimitNs);
+                     kWaitLimitNs / 16);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     // The warp stays converged and one elected lane issues: 32 clocks a
