@@ -54,6 +54,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <mutex>
 
 #include "internal.h"
@@ -109,13 +110,17 @@ struct Shape {
 
 constexpr int kMaxStages = 8;
 struct Misc {
-  // Every barrier but `drained` completes once a use, in order.
-  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages], kv_ready[kMaxStages];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];        // [tile parity]
-  uint64_t recv[2][4], recv_credit[2][4];                      // [group][lane quarter]
+  // Barriers, in four runs by their arrivals a phase.  Every one but `drained`
+  // completes once a use, in order.
+  uint64_t kv_full[kMaxStages], kv_ready[kMaxStages];    // 1 arrival
+  uint64_t s_full[2], pv_done[2];                        // [tile parity]
+  uint64_t recv[2][4], recv_credit[2][4];                // [group][lane quarter]
   uint64_t weights[2][4], weights_credit[2][4], decided[2][4];
-  uint64_t tops[4];                                            // [lane quarter]
-  uint64_t q_ready, drained;
+  uint64_t tops[4];                                      // [lane quarter]
+  uint64_t drained;
+  uint64_t kv_empty[kMaxStages];                         // 2: outputs' commit, mender
+  uint64_t s_free[2], p_full[2];                         // 4: the group's warps
+  uint64_t q_ready;                                      // 8: all softmax warps
   uint64_t bad[kMaxStages];  // non-finite drafts of a stage's tile, one bit a token
   uint32_t tmem;
   int32_t abort;
@@ -349,9 +354,10 @@ __device__ __forceinline__ void deal(Misc& m, const AttendParams& ap, int lane) 
   __syncwarp();
   if (tiles_of_rows <= ap.clusters) {
     int pieces = 0;
-    for (int b = 0; b < p.requests; ++b)
-      pieces += row_tiles(drafts_of(m, b), p.heads) *
-                ((token_tiles(m.length[b]) + run + lane - 1) / (run + lane));
+    if (lane <= kPieceSlack)
+      for (int b = 0; b < p.requests; ++b)
+        pieces += row_tiles(drafts_of(m, b), p.heads) *
+                  ((token_tiles(m.length[b]) + run + lane - 1) / (run + lane));
     const uint32_t fits = __ballot_sync(~0u, lane <= kPieceSlack && pieces <= ap.clusters);
     if (fits != 0u) piece = run + __ffs(fits) - 1;
   }
@@ -392,23 +398,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   }
 
   if (warp == 0) {
-    // Barriers, a lane a kind.
-    auto init = [&](uint64_t* b, int n, uint32_t count) {
-      for (int i = 0; i < n; ++i) ptx::mbar_init(bar(b[i]), count);
-    };
-    if (lane == 0) init(m.kv_full, kStages, 1);
-    if (lane == 1) init(m.kv_empty, kStages, 2);  // the outputs' commit and the mender
-    if (lane == 2) init(m.kv_ready, kStages, 1);
-    if (lane == 3) init(m.s_full, 2, 1), init(m.s_free, 2, 4);
-    if (lane == 4) init(m.p_full, 2, 4), init(m.pv_done, 2, 1);
-    if (lane == 5) init(m.recv[0], 8, 1);
-    if (lane == 6) init(m.recv_credit[0], 8, 1);
-    if (lane == 7) init(m.weights[0], 8, 1);
-    if (lane == 8) init(m.weights_credit[0], 8, 1);
-    if (lane == 9) init(m.decided[0], 8, 1);
-    if (lane == 10) init(&m.q_ready, 1, 8), init(&m.drained, 1, 1);
-    if (lane == 12) init(m.tops, 4, 1);
-    if (lane == 13) m.abort = 0;
+    constexpr int kTwo = offsetof(Misc, kv_empty) / 8, kFour = offsetof(Misc, s_free) / 8;
+    constexpr int kEight = offsetof(Misc, q_ready) / 8;
+    for (int i = lane; i <= kEight; i += 32)
+      ptx::mbar_init(bar(m.kv_full[0]) + 8u * i, i < kTwo ? 1 : i < kFour ? 2 : i < kEight ? 4 : 8);
+    if (lane == 0) m.abort = 0;
     ptx::fence_mbarrier_init();
     ptx::fence_proxy_async_smem();
   }
@@ -459,12 +453,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       return ok;
     };
     while (ok && next_segment(m, p, cluster, walk, seg)) {
-      // This warp's first token tile.
-      const int first = seg.kv0 + ((r & 1) != which);
-      int page[kItems];
-#pragma unroll
-      for (int k = 0; k < kItems; ++k)
-        page[k] = first < seg.kv1 ? read_page(first, lane + 32 * k) : p.pages;
       uint32_t full;
       // The queries: half of this CTA's columns and half of the rows' rotary
       // part a place.
@@ -485,6 +473,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
+      // This warp's first token tile.
+      const int first = seg.kv0 + ((r & 1) != which);
+      int page[kItems];
+#pragma unroll
+      for (int k = 0; k < kItems; ++k)
+        page[k] = first < seg.kv1 ? read_page(first, lane + 32 * k) : p.pages;
       const int r0 = r - seg.kv0;
       for (int kv = first; kv < seg.kv1; kv += 2) {
         r = r0 + kv;
@@ -1033,30 +1027,43 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
   const LatentParams& p = ap.in;
   const int row = threadIdx.x % kTileRows;
   const int column = blockIdx.y * 8 + (threadIdx.x / kTileRows) * 4;
-  uint32_t all = 0, begin = 0, end = 0;
-  int tiles = 0, covered0 = p.rows, covered1 = p.rows;
-  size_t out_row = 0;
-  bool mine = false, found = false;
+  const int lane = threadIdx.x % 32;
   const int piece = *ap.piece;
-  for (int b = 0; b < p.requests; ++b) {
-    const Request r = load_request(p, b);
-    if (b == 0) covered0 = r.begin;
-    if (b == p.requests - 1) covered1 = r.begin + r.drafts;
-    // Runs of the list that a row tile makes up.
+  // Where this block's row tile stands in the list of runs; a lane a request.
+  uint32_t all = 0, begin = 0, end = 0;
+  int tiles = 0, covered0 = p.rows, covered1 = p.rows, row0 = 0, valid = 0;
+  for (int base = 0; base < p.requests; base += 32) {
+    Request r{p.rows, 0, 0, false};
+    if (base + lane < p.requests) r = load_request(p, base + lane);
     const int rt = row_tiles(r.drafts, p.heads);
+    // Runs that a row tile of the request makes up.
     int kt = token_tiles(r.length);
     if (piece > 0) kt = (kt + piece - 1) / piece;
-    const int tile = static_cast<int>(blockIdx.x) - tiles;
-    if (tile >= 0 && tile < rt) {
-      found = true;
-      begin = all + static_cast<uint32_t>(tile) * kt;
-      end = begin + kt;
-      mine = tile * kTileRows + row < r.drafts * p.heads;
-      out_row = static_cast<size_t>(r.begin) * p.heads + tile * kTileRows + row;
+    int tiles_to = rt;
+    uint32_t runs_to = static_cast<uint32_t>(rt) * kt;
+    for (int o = 1; o < 32; o *= 2) {
+      const int t = __shfl_up_sync(~0u, tiles_to, o);
+      const uint32_t n = __shfl_up_sync(~0u, runs_to, o);
+      if (lane >= o) tiles_to += t, runs_to += n;
     }
-    tiles += rt;
-    all += static_cast<uint32_t>(rt) * kt;
+    const int tile = static_cast<int>(blockIdx.x) - (tiles + tiles_to - rt);
+    const uint32_t has = __ballot_sync(~0u, tile >= 0 && tile < rt);
+    if (has != 0u) {
+      const int from = __ffs(has) - 1;
+      const uint32_t at = all + runs_to - static_cast<uint32_t>(rt) * kt +
+                          static_cast<uint32_t>(tile) * kt;
+      begin = __shfl_sync(~0u, at, from);
+      end = begin + __shfl_sync(~0u, kt, from);
+      row0 = __shfl_sync(~0u, r.begin * p.heads + tile * kTileRows, from);
+      valid = __shfl_sync(~0u, r.drafts * p.heads - tile * kTileRows, from);
+    }
+    if (base == 0) covered0 = __shfl_sync(~0u, r.begin, 0);
+    if (base + 32 >= p.requests)
+      covered1 = __shfl_sync(~0u, r.begin + r.drafts, p.requests - 1 - base);
+    tiles += __shfl_sync(~0u, tiles_to, 31);
+    all += __shfl_sync(~0u, runs_to, 31);
   }
+  const size_t out_row = static_cast<size_t>(row0) + row;
   auto write = [&](size_t at, float4 v) {
     *reinterpret_cast<uint2*>(p.out + at * kLatent + column) =
         make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
@@ -1070,7 +1077,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
     for (size_t at = hi + row; at < n; at += kTileRows) write(at, zero);
     return;
   }
-  if (!found || !mine) return;
+  if (row >= valid) return;
   if (begin == end) {
     write(out_row, zero);
     return;
