@@ -1088,20 +1088,36 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Atten
   const uint32_t c0 = begin / run, c1 = (end - 1) / run;
   if (c0 == c1) return;  // one cluster wrote the whole
   auto slot_of = [&](uint32_t c) { return 2 * c + (c * run < begin ? 1 : 0); };
-  float top = -INFINITY;
-  for (uint32_t c = c0; c <= c1; ++c) top = fmaxf(top, ap.stats[slot_of(c) * kTileRows + row].x);
+  // Eight clusters' loads at a time, under the largest reference so far.
+  constexpr uint32_t kBatch = 8;
+  float top = -INFINITY, total = 0.0f;
   float4 sum = zero;
-  float total = 0.0f;
-#pragma unroll 4
-  for (uint32_t c = c0; c <= c1; ++c) {
-    const uint32_t slot = slot_of(c);
-    const float2 st = ap.stats[slot * kTileRows + row];
-    const float4 v =
-        ap.partial[(static_cast<size_t>(slot) * (kLatent / 4) + column / 4) * kTileRows + row];
-    const float f = shift_factor(st.x, top);
-    total = fmaf(f, st.y, total);
-    sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y);
-    sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+  for (uint32_t c = c0; c <= c1; c += kBatch) {
+    float2 st[kBatch];
+    float4 v[kBatch];
+#pragma unroll
+    for (uint32_t k = 0; k < kBatch; ++k) {
+      st[k] = make_float2(-INFINITY, 0.0f);
+      v[k] = zero;
+      if (c + k > c1) continue;
+      const uint32_t slot = slot_of(c + k);
+      st[k] = ap.stats[slot * kTileRows + row];
+      v[k] = ap.partial[(static_cast<size_t>(slot) * (kLatent / 4) + column / 4) * kTileRows + row];
+    }
+    float next = top;
+#pragma unroll
+    for (uint32_t k = 0; k < kBatch; ++k) next = fmaxf(next, st[k].x);
+    const float keep = shift_factor(top, next);
+    top = next;
+    total *= keep;
+    sum = make_float4(sum.x * keep, sum.y * keep, sum.z * keep, sum.w * keep);
+#pragma unroll
+    for (uint32_t k = 0; k < kBatch; ++k) {
+      const float f = shift_factor(st[k].x, top);
+      total = fmaf(f, st[k].y, total);
+      sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
+      sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
+    }
   }
   const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
   write(out_row, make_float4(sum.x * inverse, sum.y * inverse, sum.z * inverse, sum.w * inverse));
