@@ -287,9 +287,15 @@ def test_values_of_zeros_extremes_and_nan(cuda):
     assert codes[0, 0] == 127 and v[0, 0] == 448 and v[0, 1] == -1
     assert codes[0, 3] == 128 and v[0, 64 + 40] == 448
     assert codes[0, 1] == 129 and v[0, 40] == 224
-    assert torch.isnan(v[1, 3]) and v[1, 4] == 256 and codes[1, 0] == 120
+    # 0 x NaN is NaN: every output of the head; blocks of NaN alone take 2^0
+    assert torch.isnan(v[1, :64]).all() and codes[1, :2].eq(127).all() and v[1, 64:].eq(0).all()
     assert codes[2, 0] == 0 and v[2, 0] > 0
     assert codes[3, 0] == 127 + 127 - 8 + 1 and v[3, 0] == 224
+    w[0, 3, 200] = float("nan")  # one output alone: it does not count towards the scale
+    o[4, 0, 4] = 2.0
+    x, scale = mx.latent_values(o, w)
+    v, codes = x.float(), scale.view(torch.uint8)
+    assert torch.isnan(v[4, 3]) and v[4, 4] == 256 and codes[4, 0] == 120
 
 
 def test_the_whole_step_feeds_the_projection(cuda):
