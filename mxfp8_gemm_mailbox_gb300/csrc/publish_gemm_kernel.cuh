@@ -234,6 +234,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   // u + 1 of it before use u completed, while the phase parity it tests still
   // shows the phase before (the parity aliases) and the wait returns at once.
   const int pipes = p.pipes;
+  // With an addend, the kernels right before this one make it, and make nothing
+  // else that is read here: the first of them lets its dependents launch only
+  // past its own grid wait, so whatever came before it is complete when this
+  // grid starts, and only the epilogue waits, for the addend.
+  const bool late_wait = p.addend != nullptr;
 
   const uint32_t bar_full = sbase + L.bars;                     // [stages]
   const uint32_t bar_empty = bar_full + 8u * stages;            // [stages]
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                            static_cast<uint32_t>(nwarm - npre) * kSfChunkBytes);
         }
         // The activations follow the programmatic grid wait.
-        ptx::grid_dependency_wait();
+        if (!late_wait) ptx::grid_dependency_wait();
         for (int i = lane; i < npre; i += producers)
           load_x_tile(sbase + L.x + i * kXStageBytes, kt_begin + i, bar_full + 8u * i);
         // From here every slot is on its second or later use: wait until the
@@ -468,7 +473,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                            static_cast<uint32_t>(warm_end - warm_begin) * kSfChunkBytes);
         }
         // The activations follow the programmatic grid wait.
-        ptx::grid_dependency_wait();
+        if (!late_wait) ptx::grid_dependency_wait();
         for (int i = lane; i < npre; i += producers)
           load_x_stage(i, kt_begin + i * T, bar_full + 8u * i);
         // From here every slot is on its second or later use: wait until the
@@ -514,7 +519,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
       // (about 260 ns per 16 KB stage of 2 copies, 4 MMAs and 2 commits),
       // which caps one thread near 65 GB/s of weight, so issuer j < pipes
       // takes stages j, j + pipes, ...
-      ptx::grid_dependency_wait();
+      if (!late_wait) ptx::grid_dependency_wait();
       bool ok = true;
       if (nkt > 0) {
         ok = ptx::mbar_wait(bar_sfb, 0, p.wait_limit_ns);
@@ -637,7 +642,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     const int warp_piece = F == 1 ? 0 : (quarter * 32) / kTileRows;  // the warp's first piece
     const uint32_t lane_base =
         (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(kRows * warp_piece);
-    ptx::grid_dependency_wait();
+    if (!late_wait) ptx::grid_dependency_wait();
     if (etid == 0) misc[1] = ptx::ld_volatile_u32(p.state + 0);
 
     // x scales of this CTA's K range as one chunk per stage: MMA column r
@@ -835,6 +840,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         red_hi[j] = sh;
         red_lo[j] = sl;
       }
+      if (late_wait) ptx::grid_dependency_wait();
       const float a = p.alpha != nullptr ? *p.alpha : 1.0f;
       // The global scale and the one rounding of a finished token (as below).
       auto finish = [&](int t_local, float sh, float sl) {
@@ -1011,6 +1017,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
       // The rows' low-rank adapters (a BF16 result of the whole sum: the addend
       // joins the compensated pair before its one rounding).
       if (p.addend != nullptr) {
+        ptx::grid_dependency_wait();
 #pragma unroll
         for (int jj = 0; jj < kShard; ++jj) {
           const int t = static_cast<int>(split) * kShard + jj;
