@@ -20,12 +20,13 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 # The current stream's handle without building a Stream object (7 us of a call
 # on a Grace core), where this torch has the call.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -104,10 +105,13 @@ class Mailbox:
         """The consumer: [m][n] BF16 copied out of the active generation."""
         if out is None:
             out = torch.empty((m, self.n), dtype=torch.bfloat16, device=self.words.device)
-        _halves(out, "out", m, self.n)
-        check(_lib.load().mailbox_consume(_ptr(self.words), _ptr(self.state), self.capacity,
-                                          self.n, m, _ptr(out), timeout_ns, _stream(stream)),
-              "mailbox_consume")
+        else:
+            _halves(out, "out", m, self.n)
+        status = _lib.load().mailbox_consume(self.words.data_ptr(), self.state.data_ptr(),
+                                             self.capacity, self.n, m, out.data_ptr(), timeout_ns,
+                                             _stream(stream))
+        if status:
+            check(status, "mailbox_consume")
         return out
 
     def status(self, stream=None):
@@ -239,14 +243,16 @@ class PublishGemm:
         if adapters.n != self.n or adapters.k != self.k:
             raise ValueError(f"the adapters are for N={adapters.n}, K={adapters.k}; the "
                              f"projection has N={self.n}, K={self.k}")
-        if which.dtype != torch.int32 or which.dim() != 1 or which.shape[0] < m:
+        if which.dtype is not torch.int32 or which.dim() != 1 or which.shape[0] < m:
             raise ValueError(f"which must be int32 [>= {m}], got {which.dtype} "
                              f"{tuple(which.shape)}")
         _on_device(which, "which")
-        check(_lib.load().mxfp8_publish_gemm_run_adapted(
-            self._handle, _ptr(x), _ptr(x_scale), m, _ptr(alpha), ctypes.byref(adapters.desc),
-            _ptr(which), _ptr(adapters.workspace), adapters.workspace.nbytes, _ptr(c),
-            _stream(stream)), "mxfp8_publish_gemm_run_adapted")
+        desc, workspace, nbytes = adapters._borrowed
+        status = _lib.load().mxfp8_publish_gemm_run_adapted(
+            self._handle, x.data_ptr(), x_scale.data_ptr(), m, _ptr(alpha), desc,
+            which.data_ptr(), workspace, nbytes, _ptr(c), _stream(stream))
+        if status:
+            check(status, "mxfp8_publish_gemm_run_adapted")
         return c
 
     def run_unfused(self, x: torch.Tensor, x_scale: torch.Tensor, c: torch.Tensor,
@@ -313,6 +319,7 @@ class Adapters:
                                   gain.data_ptr() if gain is not None else None,
                                   ranks.data_ptr() if ranks is not None else None,
                                   self.count, self.rank)
+        self._borrowed = (ctypes.byref(self.desc), self.workspace.data_ptr(), nbytes)
 
 
 class LamportGather:

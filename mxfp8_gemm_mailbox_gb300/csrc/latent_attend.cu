@@ -66,7 +66,7 @@ namespace {
 constexpr int kRope = 64;
 constexpr int kTokens = 64;     // tokens in a tile
 constexpr int kTileRows = 128;  // rows in a tile
-constexpr int kSmallBox = 8;    // tokens of a box in a tile that reaches drafts or length
+constexpr int kMinBox = 8;      // tokens of a TMA box at least: pages are multiples of 8
 constexpr int kAttendThreads = 384;
 constexpr int kSoftmaxWarp = 4;
 constexpr int kMaxRequests = MXFP8_MAX_REQUESTS;
@@ -307,9 +307,8 @@ struct AttendParams {
   int32_t* piece;     // the deal: token tiles of a piece, 0 for equal runs
 };
 struct AttendMaps {
-  CUtensorMap latent, rope;              // boxes of `box` tokens
-  CUtensorMap latent_small, rope_small;  // boxes of 8
-  CUtensorMap q, q_rope;                 // boxes of 128 and of 64 rows
+  CUtensorMap latent, rope;  // boxes of `box` tokens
+  CUtensorMap q, q_rope;     // boxes of 128 and of 64 rows
 };
 
 // Token tiles of a cluster's run in an even deal.
@@ -410,14 +409,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     ptx::tmem_alloc(ptx::smem_addr(&m.tmem), 512);
     ptx::tmem_relinquish();
   }
-  if (warp == 2 && lane < 6)
+  if (warp == 2 && lane < 4)
     ptx::prefetch_tensormap(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   ptx::tc_fence_before();
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = m.tmem;
-  if (tid == 0) ptx::launch_dependents();
   ptx::grid_dependency_wait();
+  // Past the wait: the join may read this kernel's inputs at once.
+  if (tid == 0) ptx::launch_dependents();
   if (warp == 0) deal(m, ap, lane);
   __syncthreads();
 
@@ -433,14 +433,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     // A lane a box (one thread's copies are served one after another).  The
     // page of a lane's box is read one of this warp's tiles ahead.
     const int which = warp == 3;
-    constexpr int kItems = (kTokens / kSmallBox * (L::kAtoms + 1) + 31) / 32;  // of a lane
+    constexpr int kItems = (kTokens / kMinBox * (L::kAtoms + 1) + 31) / 32;  // of a lane
     const uint64_t keep = ptx::policy_evict_last();
-    // The page of box i of tile kv: in the pool, or past it (then the copy fills
-    // zeros) for what lies past the length.
+    // The page of copy i of tile kv (box i / (atoms + 1)): in the pool, or past
+    // it (then the copy fills zeros) for a box past the length.
+    const int items = kTokens / ap.box * (L::kAtoms + 1);
     auto read_page = [&](int kv, int i) {
-      const int box = special(seg, kv) ? kSmallBox : ap.box;
-      const int token = kv * kTokens + i / (L::kAtoms + 1) * box;
-      if (i >= kTokens / box * (L::kAtoms + 1) || token >= seg.length) return p.pages;
+      const int token = kv * kTokens + i / (L::kAtoms + 1) * ap.box;
+      if (i >= items || token >= seg.length) return p.pages;
       return p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
     };
     int r = 0;  // places of the ring, of both warps
@@ -487,30 +487,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         for (int k = 0; k < kItems; ++k)
           next[k] = kv + 2 < seg.kv1 ? read_page(kv + 2, lane + 32 * k) : p.pages;
         if (!place(full)) break;
-        const bool fine = special(seg, kv);
-        const int box = fine ? kSmallBox : ap.box;
-        const int items = kTokens / box * (L::kAtoms + 1);
         const uint32_t dst = sbase + r % kStages * L::kStageBytes;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
           const int i = lane + 32 * k;
           if (i >= items) continue;
-          if (page[k] < 0 || page[k] > p.pages ||
-              (page[k] == p.pages && kv * kTokens + i / (L::kAtoms + 1) * box < seg.length)) {
-            raise(p.flags, MXFP8_FLAG_BAD_INDEX);
+          const int at = i / (L::kAtoms + 1) * ap.box, atom = i % (L::kAtoms + 1);
+          if (page[k] < 0 || page[k] >= p.pages) {
+            if (kv * kTokens + at < seg.length) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
             page[k] = p.pages;
           }
-          const int at = i / (L::kAtoms + 1) * box, atom = i % (L::kAtoms + 1);
           const int slot = (kv * kTokens + at) % p.page_size;
           if (atom < L::kAtoms)
-            ptx::tma_load_3d(dst + atom * kAtomBytes + at * 128,
-                             fine ? &maps.latent_small : &maps.latent,
+            ptx::tma_load_3d(dst + atom * kAtomBytes + at * 128, &maps.latent,
                              static_cast<int>(rank) * L::kHalf + atom * 64, slot, page[k], full,
                              keep);
           else
-            ptx::tma_load_3d(dst + L::kAtoms * kAtomBytes + at * 64,
-                             fine ? &maps.rope_small : &maps.rope, static_cast<int>(rank) * 32,
-                             slot, page[k], full, keep);
+            ptx::tma_load_3d(dst + L::kAtoms * kAtomBytes + at * 64, &maps.rope,
+                             static_cast<int>(rank) * 32, slot, page[k], full, keep);
         }
         __syncwarp();
 #pragma unroll
@@ -640,19 +634,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             }
             if (!__all_sync(~0u, finite)) bad |= 1ull << n;
           }
-          // Boxes of 8 tokens past the length came as zeros; the rest of the
-          // last one is filled here.
-          uint64_t fill = bad | (low_ones((n1 + kSmallBox - 1) / kSmallBox * kSmallBox) &
-                                 ~low_ones(n1));
-          while (fill != 0) {
-            const int n = __ffsll(static_cast<long long>(fill)) - 1;
-            fill &= fill - 1;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            if (lane < L::kAtoms * 8)
-              *reinterpret_cast<uint4*>(kvp + (lane / 8) * kAtomBytes + n * 128 +
-                                        (lane % 8) * 16) = zero;
-            if (lane < 4)
-              *reinterpret_cast<uint4*>(kvp + L::kAtoms * kAtomBytes + n * 64 + lane * 16) = zero;
+          // Boxes past the length came as zeros; the rest of the last one is
+          // filled here.
+          const uint64_t fill =
+              bad | (low_ones((n1 + ap.box - 1) / ap.box * ap.box) & ~low_ones(n1));
+          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+          for (int n = lane / 8; n < kTokens; n += 4) {  // 8 lanes a token's row of 128 bytes
+            if (!(fill >> n & 1)) continue;
+#pragma unroll
+            for (int atom = 0; atom < L::kAtoms; ++atom)
+              *reinterpret_cast<uint4*>(kvp + atom * kAtomBytes + n * 128 + lane % 8 * 16) = zero;
+            if (lane % 8 < 4)
+              *reinterpret_cast<uint4*>(kvp + L::kAtoms * kAtomBytes + n * 64 + lane % 8 * 16) =
+                  zero;
           }
           if (lane == 0) m.bad[stage] = bad;
           ptx::fence_proxy_async_smem();
@@ -681,16 +675,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     auto chunk_at = [&](uint32_t half, int c) { return ((half * 4u + c) ^ (row & 7u)) * 16u; };
     const uint64_t& recv_bar = m.recv[group][quarter];
     const uint64_t& weights_bar = m.weights[group][quarter];
-    const uint32_t to_scores = ptx::map_to_rank(sbase + recv_offset, peer);
-    const uint32_t to_scores_bar = ptx::map_to_rank(bar(recv_bar), peer);
-    const uint32_t to_weights = ptx::map_to_rank(sbase + p_row, peer);
-    const uint32_t to_weights_bar = ptx::map_to_rank(bar(weights_bar), peer);
-    const uint32_t to_sum = ptx::map_to_rank(ptx::smem_addr(&m.peer[group][row]), peer);
-    const uint32_t to_top = ptx::map_to_rank(ptx::smem_addr(&m.peer_top[row]), peer);
-    const uint32_t to_top_bar = ptx::map_to_rank(bar(m.tops[quarter]), peer);
-    const uint32_t to_recv_credit = ptx::map_to_rank(bar(m.recv_credit[group][quarter]), peer);
-    const uint32_t to_weights_credit =
-        ptx::map_to_rank(bar(m.weights_credit[group][quarter]), peer);
+    // The peer's copy of a shared-memory address is this much further.
+    const uint32_t over = ptx::map_to_rank(sbase, peer) - sbase;
+    auto there = [&](const auto& x) { return ptx::smem_addr(&x) + over; };
     uint32_t exchanges = 0;  // tiles this warp exchanged
     uint32_t decisions = 0;  // tiles of this quarter's rows, of both groups
     uint32_t firsts = 0;     // row tiles of this quarter
@@ -698,7 +685,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     int r = 0;               // places of the ring before its first token tile
     // The peer may send this group its scores; after that, a permit follows
     // every tile whose outputs are added (its weights lay where scores land).
-    if (lane == 0) ptx::mbar_arrive_remote_relaxed(to_recv_credit);
+    if (lane == 0) ptx::mbar_arrive_remote_relaxed(there(m.recv_credit[group][quarter]));
     for (uint32_t segments = 0; next_segment(m, p, cluster, walk, seg); ++segments) {
       const size_t q_row = static_cast<size_t>(seg.begin) * p.heads + seg.row0 + row;
       const bool mine = row < seg.valid;
@@ -765,7 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         const uint32_t decision = decisions + i;
         if (i > i0) {
           wait(m.pv_done[group], (g + i - 2) >> 1);
-          if (lane == 0) ptx::mbar_arrive_remote_relaxed(to_recv_credit);
+          if (lane == 0) ptx::mbar_arrive_remote_relaxed(there(m.recv_credit[group][quarter]));
         }
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(bar(recv_bar), 32u * 32u * 4u);
@@ -799,10 +786,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         wait.cluster(m.recv_credit[group][quarter], exchanges);
 #pragma unroll
         for (int c = 0; c < 8; ++c)
-          ptx::st_async_remote_v4(to_scores + c * 512,
+          ptx::st_async_remote_v4(sbase + recv_offset + over + c * 512,
                                   make_uint4(other[4 * c], other[4 * c + 1], other[4 * c + 2],
                                              other[4 * c + 3]),
-                                  to_scores_bar);
+                                  there(recv_bar));
         wait.cluster(recv_bar, exchanges);
         float z[32];
 #pragma unroll
@@ -848,13 +835,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         // would wait for this CTA's own stores to the peer: it cost 60 us of 320
         // on 8 x 64k tokens, 128 heads.)
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_remote_relaxed(to_weights_credit);
+        if (lane == 0) ptx::mbar_arrive_remote_relaxed(there(m.weights_credit[group][quarter]));
         // Weights of this CTA's tokens: under the halves' common maximum in the
         // first tile, then under the last reference this group knows, or one
         // whole steps above it.
         float under;
         if (i == 0) {
-          ptx::st_async_remote(to_top, __float_as_uint(top), to_top_bar);
+          ptx::st_async_remote(there(m.peer_top[row]), __float_as_uint(top),
+                               there(m.tops[quarter]));
           wait.cluster(m.tops[quarter], firsts);
           under = fmaxf(top, m.peer_top[row]);
           m.reference[decision & 1][row] = under;
@@ -887,11 +875,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         wait.cluster(m.weights_credit[group][quarter], exchanges);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          ptx::st_async_remote_v4(to_weights + chunk_at(rank, c),
+          ptx::st_async_remote_v4(sbase + p_row + over + chunk_at(rank, c),
                                   make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]),
-                                  to_weights_bar);
-        ptx::st_async_remote_v2(to_sum, __float_as_uint(base), __float_as_uint(total),
-                                to_weights_bar);
+                                  there(weights_bar));
+        ptx::st_async_remote_v2(there(m.peer[group][row]), __float_as_uint(base),
+                                __float_as_uint(total), there(weights_bar));
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<uint4*>(smem + p_row + chunk_at(rank, c)) =
@@ -966,7 +954,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
       total = sums[0] + sums[32];
       asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-      if (lane == 0 && i0 < tiles) ptx::mbar_arrive_remote_relaxed(to_recv_credit);
+      if (lane == 0 && i0 < tiles) ptx::mbar_arrive_remote_relaxed(there(m.recv_credit[group][quarter]));
       const bool whole = seg.kv0 == 0 && seg.kv1 == seg.kv_tiles;
       const int column0 = static_cast<int>(rank) * L::kHalf + group * (L::kHalf / 2);
       const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
@@ -1023,18 +1011,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
 template <int kLatent>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttendParams ap) {
   ptx::launch_dependents();
-  ptx::grid_dependency_wait();
   const LatentParams& p = ap.in;
   const int row = threadIdx.x % kTileRows;
   const int column = blockIdx.y * 8 + (threadIdx.x / kTileRows) * 4;
   const int lane = threadIdx.x % 32;
+  Request mine{p.rows, 0, 0, false};  // the first 32 requests, a lane each
+  if (lane < p.requests) mine = load_request(p, lane);
+  ptx::grid_dependency_wait();
   const int piece = *ap.piece;
   // Where this block's row tile stands in the list of runs; a lane a request.
   uint32_t all = 0, begin = 0, end = 0;
   int tiles = 0, covered0 = p.rows, covered1 = p.rows, row0 = 0, valid = 0;
   for (int base = 0; base < p.requests; base += 32) {
-    Request r{p.rows, 0, 0, false};
-    if (base + lane < p.requests) r = load_request(p, base + lane);
+    Request r = mine;
+    if (base > 0) {
+      r = Request{p.rows, 0, 0, false};
+      if (base + lane < p.requests) r = load_request(p, base + lane);
+    }
     const int rt = row_tiles(r.drafts, p.heads);
     // Runs that a row tile of the request makes up.
     int kt = token_tiles(r.length);
@@ -1218,8 +1211,6 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
   constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, k64 = CU_TENSOR_MAP_SWIZZLE_64B;
   if (encode_cache(&maps.latent, p, 0, kLatent, ap.box, 64, k128) != CUDA_SUCCESS ||
       encode_cache(&maps.rope, p, kLatent, kRope, ap.box, 32, k64) != CUDA_SUCCESS ||
-      encode_cache(&maps.latent_small, p, 0, kLatent, kSmallBox, 64, k128) != CUDA_SUCCESS ||
-      encode_cache(&maps.rope_small, p, kLatent, kRope, kSmallBox, 32, k64) != CUDA_SUCCESS ||
       encode_queries(&maps.q, p, kLatent, 0, kLatent, 64, kTileRows, k128) != CUDA_SUCCESS ||
       encode_queries(&maps.q_rope, p, kLatent, kLatent, kRope, 32, kTileRows / 2, k64) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;

@@ -17,31 +17,37 @@ import torch
 
 from . import _lib
 from ._lib import LatentDesc, check
-from .api import _ptr, _stream
+from .api import _current_device, _stream
 
 _BF16, _I32, _I64 = torch.bfloat16, torch.int32, torch.int64
 _E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
 _ROPE = _lib.LATENT_ROPE
+_empty = torch.empty
 
 
-def _device_of(t: torch.Tensor, name: str) -> int:
-    """The ordinal of t's device, which must be the current CUDA device."""
-    device = t.get_device()
-    if device < 0:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if device != torch.cuda.current_device():
-        raise ValueError(f"{name} is on device {device}, the current device is "
-                         f"{torch.cuda.current_device()}")
-    return device
-
-
-def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
+def _refuse(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
+    """Raises what is wrong with a tensor that is not dtype, shape, contiguous
+    and on the device."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {str(dtype)[6:]}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on device {device}")
+    if device < 0 or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on device {max(device, 0)}")
+
+
+def _expect(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, device: int) -> None:
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != device
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, device)
+
+
+def _check_device(device: int, name: str) -> None:
+    if device < 0:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if device != _current_device():
+        raise ValueError(f"{name} is on device {device}, the current device is "
+                         f"{_current_device()}")
 
 
 def _matrices(w: torch.Tensor) -> tuple:
@@ -50,7 +56,8 @@ def _matrices(w: torch.Tensor) -> tuple:
         raise TypeError(f"w must be bfloat16, got {w.dtype}")
     if w.dim() != 3:
         raise ValueError(f"w must be [heads][outputs][inputs], got {list(w.shape)}")
-    device = _device_of(w, "w")
+    device = w.get_device()
+    _check_device(device, "w")
     if not w.is_contiguous():
         raise ValueError("w must be a contiguous CUDA tensor")
     return (*w.shape, device)
@@ -64,11 +71,11 @@ def latent_query(q_nope: torch.Tensor, q_rope: torch.Tensor, w: torch.Tensor,
     first.  ``w`` is read before the kernel before this one on the stream has
     finished, so that kernel must not write it."""
     heads, latent, nope, device = _matrices(w)
-    rows = len(q_nope)
+    rows = q_nope.shape[0]
     _expect(q_nope, "q_nope", _BF16, (rows, heads, nope), device)
     _expect(q_rope, "q_rope", _BF16, (rows, heads, _ROPE), device)
     if out is None:
-        out = w.new_empty((rows, heads, latent + _ROPE))
+        out = _empty((rows, heads, latent + _ROPE), dtype=_BF16, device=w.device)
     else:
         _expect(out, "out", _BF16, (rows, heads, latent + _ROPE), device)
     status = _lib.load().mxfp8_latent_query(q_nope.data_ptr(), q_rope.data_ptr(), w.data_ptr(),
@@ -93,14 +100,14 @@ def latent_values(o: torch.Tensor, w: torch.Tensor, x: torch.Tensor | None = Non
     read before the kernel before this one on the stream has finished, so that
     kernel must not write it."""
     heads, value, latent, device = _matrices(w)
-    rows, k = len(o), heads * value
+    rows, k = o.shape[0], heads * value
     _expect(o, "o", _BF16, (rows, heads, latent), device)
     if x is None:
-        x = w.new_empty((rows, k), dtype=_E4M3)
+        x = _empty((rows, k), dtype=_E4M3, device=w.device)
     else:
         _codes_out(x, "x", rows, k, device)
     if x_scale is None:
-        x_scale = w.new_empty((rows, k // 32), dtype=_E8M0)
+        x_scale = _empty((rows, k // 32), dtype=_E8M0, device=w.device)
     else:
         _codes_out(x_scale, "x_scale", rows, k // 32, device)
     status = _lib.load().mxfp8_latent_values(o.data_ptr(), w.data_ptr(), x.data_ptr(),
@@ -126,7 +133,8 @@ class LatentAttention:
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.flags = torch.zeros(1, dtype=torch.int32, device=device)
         self._desc = LatentDesc(heads, latent)
-        self._borrowed = (ctypes.byref(self._desc), self.workspace.data_ptr(), nbytes)
+        self._borrowed = (ctypes.byref(self._desc), self.workspace.data_ptr(), nbytes,
+                          self.flags.data_ptr())
 
     def run(self, q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
             lengths: torch.Tensor, row_begin: torch.Tensor, scale: float,
@@ -143,44 +151,51 @@ class LatentAttention:
         j <= t."""
         heads, latent = self.heads, self.latent
         width = latent + _ROPE
-        if q.dim() != 3:
-            raise ValueError(f"q must be [rows][{heads}][{width}], got {list(q.shape)}")
-        rows = len(q)
-        if q.shape != (rows, heads, width):
-            raise ValueError(f"q must be [rows][{heads}][{width}], got {list(q.shape)}")
-        device = _device_of(q, "q")
-        _expect(q, "q", _BF16, (rows, heads, width), device)
+        shape = q.shape
+        if len(shape) != 3 or shape[1] != heads or shape[2] != width:
+            raise ValueError(f"q must be [rows][{heads}][{width}], got {list(shape)}")
+        rows, device = shape[0], q.get_device()
+        _check_device(device, "q")
+        if q.dtype is not _BF16 or not q.is_contiguous():
+            _refuse(q, "q", _BF16, shape, device)
         if cache.dtype is not _BF16:
             raise TypeError(f"cache must be bfloat16, got {cache.dtype}")
-        shape = cache.shape
-        if len(shape) != 3 or shape[2] != width:
-            raise ValueError(f"cache must be [pages][page_size][{width}], got {list(shape)}")
+        pool = cache.shape
+        if len(pool) != 3 or pool[2] != width:
+            raise ValueError(f"cache must be [pages][page_size][{width}], got {list(pool)}")
         page_stride, token_stride, one = cache.stride()
         if cache.get_device() != device or one != 1:
             raise ValueError(f"cache must be a CUDA tensor on device {device} with contiguous "
                              "tokens")
-        if lengths.dim() != 1 or page_table.dim() != 2:
-            raise ValueError("lengths must be [requests] and page_table [requests][width], got "
-                             f"{list(lengths.shape)} and {list(page_table.shape)}")
-        requests, table_width = page_table.shape
+        table = page_table.shape
+        if len(table) != 2:
+            raise ValueError(f"page_table must be [requests][width], got {list(table)}")
+        requests = table[0]
+        _expect(page_table, "page_table", _I32, table, device)
         _expect(lengths, "lengths", _I32, (requests,), device)
         _expect(row_begin, "row_begin", _I32, (requests + 1,), device)
-        _expect(page_table, "page_table", _I32, (requests, table_width), device)
+        masks = None
         if tree is not None:
             _expect(tree, "tree", _I64, (rows,), device)
+            masks = tree.data_ptr()
         if out is None:
-            out = q.new_empty((rows, heads, latent))
+            out = _empty((rows, heads, latent), dtype=_BF16, device=q.device)
         else:
             _expect(out, "out", _BF16, (rows, heads, latent), device)
         d = self._desc
-        d.rows, d.requests, d.page_size, d.pages = rows, requests, shape[1], shape[0]
-        d.table_width, d.scale, d.token_stride, d.page_stride = (table_width, scale, token_stride,
-                                                                 page_stride)
-        desc, workspace, nbytes = self._borrowed
+        d.rows = rows
+        d.requests = requests
+        d.page_size = pool[1]
+        d.pages = pool[0]
+        d.table_width = table[1]
+        d.scale = scale
+        d.token_stride = token_stride
+        d.page_stride = page_stride
+        desc, workspace, nbytes, flags = self._borrowed
         status = _lib.load().mxfp8_latent_attend(
             desc, q.data_ptr(), cache.data_ptr(), page_table.data_ptr(), lengths.data_ptr(),
-            row_begin.data_ptr(), _ptr(tree), out.data_ptr(), workspace, nbytes,
-            self.flags.data_ptr(), _stream(stream))
+            row_begin.data_ptr(), masks, out.data_ptr(), workspace, nbytes, flags,
+            _stream(stream))
         if status:
             check(status, "mxfp8_latent_attend")
         return out
