@@ -26,6 +26,7 @@ struct mxfp8_publish_gemm {
   uint16_t* mailbox;
   int32_t* state;
   int device;
+  int sms;
   // Set by create, whose re-layout kernels write the scale chunks and the
   // tiled weight that the GEMM's producer reads before its grid wait: the
   // first launch then takes a full stream dependency instead of the
@@ -554,6 +555,7 @@ mxfp8_status mxfp8_publish_gemm_create(const mxfp8_gemm_desc* desc, const void* 
   g->mailbox = static_cast<uint16_t*>(mailbox);
   g->state = stage_state;
   g->device = device;
+  g->sms = lim.sms;
   g->first_launch_pending = true;
   g->k_tiles = k_tiles_for_fold(desc->k, fold);
   g->tiles_per_split = (g->k_tiles + g->desc.split_k - 1) / g->desc.split_k;
@@ -709,7 +711,7 @@ mxfp8_status mxfp8_publish_gemm_run_adapted(mxfp8_publish_gemm* gemm, const void
   p.inner = static_cast<float*>(workspace);
   p.delta = p.inner + adapter_inner_floats(p.k, p.rank);
   p.flags = gemm->state + 3;
-  const cudaError_t e = launch_adapters(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_adapters(p, device, gemm->sms, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the adapters");
   return run_gemm(gemm, x, x_scale, m, c, stream, true, alpha, p.delta);
 }

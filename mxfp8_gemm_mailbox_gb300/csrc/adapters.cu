@@ -10,13 +10,19 @@
 //
 // Both products read their matrix once for one row of activations each: bound
 // by HBM (8 rows with adapters of their own, rank 64, N = 7168, K = 16384: 16.8
-// MB of A, 7.3 MB of B beside the projection's 121 MB).  The first kernel cuts
-// K into pieces of 1024 so that 2048 warps each have 8 KB on its way; the
-// second adds the pieces, in order, while its part of B is on its way, which it
-// asks for before it waits for the first.  The GEMM, launched behind both, has
-// its weight stream started by then.
+// MB of A, 7.3 MB of B beside the projection's 121 MB).  The first, three blocks
+// an SM, has all of A on its way at once and takes 5.3 us of that call.  The
+// second, one block an SM of 4 warps x 72 registers a thread and next to no
+// shared memory, leaves room for two of the GEMM's blocks and runs under the
+// GEMM's weight stream: both let their dependents launch at once, and the GEMM
+// waits for delta in its epilogue alone.  31.3 us a call (21.3 without adapters;
+// 145 MB are 21.2 us at the copy rate); 32.6 with two blocks of the second an SM,
+// 35 with three (the GEMM's come later), 36 with one block of the first.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
+#include <mutex>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -42,10 +48,10 @@ __device__ __forceinline__ int rank_of(const AdapterParams& p, int i) {
   return p.ranks == nullptr ? p.rank : min(max(p.ranks[i], 0), p.rank);
 }
 
-constexpr int kPiece = 1024;       // numbers of a row of x a warp multiplies
-constexpr int kSteps = kPiece / 256;
+constexpr int kSteps = 3;          // loads of a row of A a lane has on its way
+constexpr int kPiece = kSteps * 256;  // numbers of a row of x a warp multiplies
 constexpr int kRowsOfA = 4;        // rows of A a warp takes
-constexpr int kInnerWarps = 4;     // of a block: one piece, 16 rows of A
+constexpr int kInnerThreads = 256;
 
 __host__ __device__ constexpr int pieces_of(int k) { return (k + kPiece - 1) / kPiece; }
 
@@ -63,14 +69,10 @@ __device__ __forceinline__ float high_bf16(uint32_t w) {
 }
 
 // inner[t][piece][j]: lane l of a warp takes numbers 8 l .. 8 l + 7 of every 256
-// of its piece of K, for four rows of A.
-__global__ void __launch_bounds__(32 * kInnerWarps)
-    adapter_inner_kernel(const __grid_constant__ AdapterParams p) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();  // past the wait: the next kernel may read `which` at once
-  const int t = blockIdx.z, piece = blockIdx.y;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int j0 = (blockIdx.x * kInnerWarps + warp) * kRowsOfA;
+// of its piece of K, for four rows of A; a warp's items are (row t, piece, four
+// rows), every gridDim.x x 8 warps.
+__device__ __forceinline__ void inner_item(const AdapterParams& p, int t, int piece, int j0,
+                                           int lane) {
   const int i = adapter_of(p, t);
   if (i < 0) return;
   const int rank = rank_of(p, i);
@@ -118,79 +120,115 @@ __global__ void __launch_bounds__(32 * kInnerWarps)
   }
 }
 
-constexpr int kDeltaThreads = 256;
-constexpr int kDeltaLoads = 4;  // of a thread, at once
+__global__ void __launch_bounds__(kInnerThreads, 3)
+    adapter_inner_kernel(const __grid_constant__ AdapterParams p) {
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();  // past the wait: the next kernels may read the call's inputs at once
+  const int groups = (p.rank + kRowsOfA - 1) / kRowsOfA, pieces = pieces_of(p.k);
+  const int items = p.m * pieces * groups, warps = gridDim.x * (kInnerThreads / 32);
+  for (int at = blockIdx.x * (kInnerThreads / 32) + threadIdx.x / 32; at < items; at += warps)
+    inner_item(p, at / (pieces * groups), at / groups % pieces, at % groups * kRowsOfA,
+               threadIdx.x % 32);
+}
+
+constexpr int kDeltaThreads = 128;
+constexpr int kDeltaLoads = 8;  // of a thread, at once
 
 // delta[t][n]: kLanes lanes share a row of B, 16 bytes (8 numbers) each a turn.
-// A block takes kDeltaLoads x 256 / kLanes outputs of one row.
+// A block's items are (row t, kDeltaLoads x 128 / kLanes outputs), every
+// gridDim.x.
 template <int kLanes>
-__global__ void __launch_bounds__(kDeltaThreads)
+__global__ void __launch_bounds__(kDeltaThreads, 7)
     adapter_delta_kernel(const __grid_constant__ AdapterParams p) {
   __shared__ float inner[MXFP8_MAX_ADAPTER_RANK];
   ptx::launch_dependents();
-  const int t = blockIdx.y, tid = threadIdx.x, sub = tid % kLanes;
   constexpr int kAtOnce = kDeltaThreads / kLanes;  // outputs a turn
-  const int n0 = blockIdx.x * kAtOnce * kDeltaLoads + tid / kLanes;
-  const int i = adapter_of(p, t);
-  const int rank = i < 0 ? 0 : rank_of(p, i);
-  const int rank8 = (p.rank + 7) & ~7;
-  const uint16_t* b = p.b + (static_cast<size_t>(max(i, 0)) * p.n + n0) * rank8 + sub * 8;
-  // The first turn's part of B, before the wait for `inner`.
-  uint4 w[kDeltaLoads];
-  const bool live = sub * 8 < rank;
+  constexpr int kOutputs = kAtOnce * kDeltaLoads;
+  const int tid = threadIdx.x, sub = tid % kLanes;
+  const int blocks = (p.n + kOutputs - 1) / kOutputs, items = p.m * blocks;
+  const int rank8 = (p.rank + 7) & ~7, pieces = pieces_of(p.k);
+  int have = -1;  // the row whose products with A are in `inner`
+  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const int t = item / blocks, n0 = item % blocks * kOutputs + tid / kLanes;
+    const int i = adapter_of(p, t);
+    const int rank = i < 0 ? 0 : rank_of(p, i);
+    const uint16_t* b = p.b + (static_cast<size_t>(max(i, 0)) * p.n + n0) * rank8 + sub * 8;
+    // The first turn's part of B, before the wait for the products with A.
+    uint4 w[kDeltaLoads];
+    const bool live = sub * 8 < rank;
 #pragma unroll
-  for (int l = 0; l < kDeltaLoads; ++l)
-    if (live && n0 + l * kAtOnce < p.n)
-      w[l] = load_once(b + static_cast<size_t>(l) * kAtOnce * rank8);
-  ptx::grid_dependency_wait();
-  const float gain = i < 0 || p.gain == nullptr ? 1.0f : p.gain[i];
-  const int pieces = pieces_of(p.k);
-  for (int j = tid; j < rank; j += kDeltaThreads) {
-    float sum = 0.0f;
-#pragma unroll 16
-    for (int piece = 0; piece < pieces; ++piece)
-      sum += p.inner[(static_cast<size_t>(t) * pieces + piece) * p.rank + j];
-    inner[j] = sum;
-  }
-  __syncthreads();
-  float sum[kDeltaLoads] = {};
-  for (int j0 = sub * 8; j0 < rank; j0 += kLanes * 8) {
-    if (j0 != sub * 8) {
-#pragma unroll
-      for (int l = 0; l < kDeltaLoads; ++l)
-        if (n0 + l * kAtOnce < p.n)
-          w[l] = load_once(b + static_cast<size_t>(l) * kAtOnce * rank8 + j0 - sub * 8);
+    for (int l = 0; l < kDeltaLoads; ++l)
+      if (live && n0 + l * kAtOnce < p.n)
+        w[l] = load_once(b + static_cast<size_t>(l) * kAtOnce * rank8);
+    if (have < 0) ptx::grid_dependency_wait();
+    if (have != t) {
+      if (have >= 0) __syncthreads();
+      for (int j = tid; j < rank; j += kDeltaThreads) {
+        float sum = 0.0f;
+#pragma unroll 8
+        for (int piece = 0; piece < pieces; ++piece)
+          sum += p.inner[(static_cast<size_t>(t) * pieces + piece) * p.rank + j];
+        inner[j] = sum;
+      }
+      __syncthreads();
+      have = t;
     }
-    float v[8];
+    const float gain = i < 0 || p.gain == nullptr ? 1.0f : p.gain[i];
+    float sum[kDeltaLoads] = {};
+    for (int j0 = sub * 8; j0 < rank; j0 += kLanes * 8) {
+      if (j0 != sub * 8) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = j0 + q < rank ? inner[j0 + q] : 0.0f;
-#pragma unroll
-    for (int l = 0; l < kDeltaLoads; ++l) {
-      if (n0 + l * kAtOnce >= p.n) continue;
-      const uint32_t c[4] = {w[l].x, w[l].y, w[l].z, w[l].w};
+        for (int l = 0; l < kDeltaLoads; ++l)
+          if (n0 + l * kAtOnce < p.n)
+            w[l] = load_once(b + static_cast<size_t>(l) * kAtOnce * rank8 + j0 - sub * 8);
+      }
+      // (Columns past the adapter's rank may hold anything.)
+      const int left = rank - j0;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        // (Columns past the adapter's rank may hold anything.)
-        if (j0 + 2 * q < rank) sum[l] = fmaf(low_bf16(c[q]), v[2 * q], sum[l]);
-        if (j0 + 2 * q + 1 < rank) sum[l] = fmaf(high_bf16(c[q]), v[2 * q + 1], sum[l]);
+        const float v0 = inner[min(j0 + 2 * q, rank - 1)];
+        const float v1 = inner[min(j0 + 2 * q + 1, rank - 1)];
+#pragma unroll
+        for (int l = 0; l < kDeltaLoads; ++l) {
+          const uint32_t c = q == 0 ? w[l].x : q == 1 ? w[l].y : q == 2 ? w[l].z : w[l].w;
+          if (2 * q < left) sum[l] = fmaf(low_bf16(c), v0, sum[l]);
+          if (2 * q + 1 < left) sum[l] = fmaf(high_bf16(c), v1, sum[l]);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int l = 0; l < kDeltaLoads; ++l) {
+    for (int l = 0; l < kDeltaLoads; ++l) {
 #pragma unroll
-    for (int o = kLanes / 2; o; o /= 2) sum[l] += __shfl_xor_sync(~0u, sum[l], o);
-    const int n = n0 + l * kAtOnce;
-    if (sub == 0 && n < p.n) p.delta[static_cast<size_t>(t) * p.n + n] = sum[l] * gain;
+      for (int o = kLanes / 2; o; o /= 2) sum[l] += __shfl_xor_sync(~0u, sum[l], o);
+      const int n = n0 + l * kAtOnce;
+      if (sub == 0 && n < p.n) p.delta[static_cast<size_t>(t) * p.n + n] = sum[l] * gain;
+    }
   }
+  if (have < 0) ptx::grid_dependency_wait();
+}
+
+// An SM's split between cache and shared memory changes only while it is idle,
+// so both kernels ask for the GEMM's: its blocks could not join them otherwise.
+template <auto* kKernel>
+cudaError_t share_sm(int device) {
+  static std::mutex mutex;
+  static bool done[64] = {};
+  if (device < 0 || device >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (done[device]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(
+      kKernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  done[device] = e == cudaSuccess;
+  return e;
 }
 
 template <int kLanes>
-cudaError_t launch_delta(const AdapterParams& p, cudaLaunchConfig_t cfg) {
+cudaError_t launch_delta(const AdapterParams& p, cudaLaunchConfig_t cfg, int device, int sms) {
   constexpr int kOutputs = kDeltaThreads / kLanes * kDeltaLoads;
-  cfg.gridDim = dim3(static_cast<unsigned>((p.n + kOutputs - 1) / kOutputs),
-                     static_cast<unsigned>(p.m));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min(p.m * ((p.n + kOutputs - 1) / kOutputs), sms)));
   cfg.blockDim = dim3(kDeltaThreads);
+  const cudaError_t e = share_sm<&adapter_delta_kernel<kLanes>>(device);
+  if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, adapter_delta_kernel<kLanes>, p);
 }
 
@@ -200,7 +238,7 @@ size_t adapter_inner_floats(int k, int rank) {
   return (static_cast<size_t>(kRows) * pieces_of(k) * rank + 3) & ~size_t{3};
 }
 
-cudaError_t launch_adapters(const AdapterParams& p, cudaStream_t stream) {
+cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -208,17 +246,19 @@ cudaError_t launch_adapters(const AdapterParams& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  constexpr int kRowsOfBlock = kInnerWarps * kRowsOfA;
-  cfg.gridDim = dim3(static_cast<unsigned>((p.rank + kRowsOfBlock - 1) / kRowsOfBlock),
-                     static_cast<unsigned>(pieces_of(p.k)), static_cast<unsigned>(p.m));
-  cfg.blockDim = dim3(32 * kInnerWarps);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, adapter_inner_kernel, p);
+  const int items = p.m * pieces_of(p.k) * ((p.rank + kRowsOfA - 1) / kRowsOfA);
+  constexpr int kWarps = kInnerThreads / 32;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min((items + kWarps - 1) / kWarps, 3 * sms)));
+  cfg.blockDim = dim3(kInnerThreads);
+  cudaError_t e = share_sm<&adapter_inner_kernel>(device);
+  if (e != cudaSuccess) return e;
+  e = cudaLaunchKernelEx(&cfg, adapter_inner_kernel, p);
   if (e != cudaSuccess) return e;
   // Lanes to a row of B: what its 16-byte pieces fill, at most 8 (rank 64).
-  if (p.rank <= 8) return launch_delta<1>(p, cfg);
-  if (p.rank <= 16) return launch_delta<2>(p, cfg);
-  if (p.rank <= 32) return launch_delta<4>(p, cfg);
-  return launch_delta<8>(p, cfg);
+  if (p.rank <= 8) return launch_delta<1>(p, cfg, device, sms);
+  if (p.rank <= 16) return launch_delta<2>(p, cfg, device, sms);
+  if (p.rank <= 32) return launch_delta<4>(p, cfg, device, sms);
+  return launch_delta<8>(p, cfg, device, sms);
 }
 
 }  // namespace mxfp8

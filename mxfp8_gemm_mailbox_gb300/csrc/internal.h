@@ -159,7 +159,7 @@ struct AdapterParams {
   int32_t* flags;          // MXFP8_FLAG_BAD_INDEX for an index outside -1..count-1
 };
 size_t adapter_inner_floats(int k, int rank);
-cudaError_t launch_adapters(const AdapterParams& p, cudaStream_t stream);
+cudaError_t launch_adapters(const AdapterParams& p, int device, int sms, cudaStream_t stream);
 
 // Latent attention (latent_project.cu, latent_attend.cu).
 cudaError_t launch_latent_query(const uint16_t* q_nope, const uint16_t* q_rope, const uint16_t* w,
