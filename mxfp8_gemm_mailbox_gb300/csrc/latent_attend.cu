@@ -224,19 +224,22 @@ __device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& 
   s.drafts = drafts_of(m, w.b);
   s.context = max(s.length - s.drafts, 0);
   s.kv_tiles = token_tiles(s.length);
-  const int local = static_cast<int>(w.at - m.first[w.b]);
+  const uint32_t local = w.at - m.first[w.b];
   int tile;
   if (m.piece > 0) {
-    const int pieces = (s.kv_tiles + m.piece - 1) / m.piece;
+    // At most as many pieces as clusters, so the products stay below 2^32.
+    const uint32_t kv = s.kv_tiles, piece = m.piece;
+    const uint32_t pieces = (kv + piece - 1) / piece;
     tile = local / pieces;
-    const int k = local % pieces;
-    s.kv0 = static_cast<int>(static_cast<int64_t>(s.kv_tiles) * k / pieces);
-    s.kv1 = static_cast<int>(static_cast<int64_t>(s.kv_tiles) * (k + 1) / pieces);
+    const uint32_t k = local - tile * pieces;
+    s.kv0 = kv * k / pieces;
+    s.kv1 = kv * (k + 1) / pieces;
     s.slot = 2 * cluster;
     ++w.at;
   } else {
-    tile = local / s.kv_tiles;
-    s.kv0 = local % s.kv_tiles;
+    const uint32_t kv = s.kv_tiles;
+    tile = local / kv;
+    s.kv0 = local - tile * kv;
     s.kv1 = min(s.kv_tiles, s.kv0 + static_cast<int>(w.end - w.at));
     // Only a share's first and last row tiles can be cut.
     s.slot = 2 * cluster + (w.at == w.from ? 0 : 1);
