@@ -15,22 +15,18 @@
 // rows that see it NaN.
 //
 // Mapping.  The T x heads rows of a request are packed into tiles of 128, the
-// MMA's M.  128 rows x 512 FP32 outputs would take all of an SM's tensor
-// memory, so a cluster of two CTAs shares a tile: CTA r holds columns
-// [r latent/2, (r+1) latent/2) of the latent (and half of the rotary key) of
-// every token, as key and as value, so a token crosses from L2 once per
-// cluster.  Per tile of 64 tokens a CTA
-//   1. multiplies its columns: partial scores of all 64 tokens;
-//   2. sends the peer its partials of the peer's 32 tokens (FP32, distributed
-//      shared memory) and adds the peer's partials of its own 32;
-//   3. exponentiates its 32 and sends the peer their weights (BF16), straight
-//      into the peer's MMA operand;
-//   4. multiplies the weights of all 64 into its own output columns.
-// The two halves exchange their maxima in a row tile's first token tile, whose
-// common maximum becomes the row's reference (the exponent subtracted from its
-// scores).  Later each half moves the reference it knows by whole steps alone,
-// and the two agree on the larger afterwards: weights formed under different
-// ones differ by a power of two, so bringing them together rounds nothing.
+// M of a pair's product: a cluster of two CTAs shares the tile, 64 rows each,
+// whose 64 x 512 FP32 outputs take half of an SM's tensor memory (a lane holds
+// half of a row's columns).  Per tile of 64 tokens the pair
+//   1. multiplies queries and keys: each CTA brings 32 of the tokens, whole;
+//   2. exponentiates: each CTA its rows, a thread half of a row's tokens;
+//   3. multiplies weights and values: each CTA brings its half of the latent
+//      columns, of all tokens.
+// Of the values a CTA lacks the peer's tokens; they are fetched (from L2, where
+// the peer has just brought them) over the half of its own tokens that only
+// the keys' product reads, as soon as that product is done.  The two products'
+// operands must lie at the same addresses in both CTAs: with the first half of
+// the columns (and of the tokens) in the first half of a place, they do.
 //
 // Work.  The row tiles' token tiles are dealt to the clusters in runs: whole
 // pieces of one row tile each where that costs little more than an even deal,
@@ -40,13 +36,13 @@
 //
 // Warps of a CTA:
 //   0, 3   producers: TMA boxes into a ring, a lane a box: a row tile's queries
-//          in two places of it, then its token tiles; a warp every other place
-//          (a place costs its warp 0.5 to 1.2 us of look-ups and issue);
-//   1      MMA issuer;
-//   2      mender of the tiles that reach the drafts or the length: zeroes the
-//          tokens past the length and drafts that are not finite;
-//   4-11   softmax, two groups of four that take the token tiles in turn, so
-//          one group's exchanges run under the other's: thread = row.
+//          in two places of it, then its token tiles; a warp every other place;
+//   1      issuer of the pair's products (in the first CTA);
+//   2, 13  menders, of keys and of values: they pass every tile on to the
+//          issuer, after a look at the ones that reach the drafts or the length;
+//   4-11   softmax, two groups of four that take the token tiles in turn;
+//   12     fetches the values of the peer's tokens, and what the shared memory
+//          holds of the queries.
 //
 // Precision: scores, references, sums, outputs and partials FP32; the weights
 // are rounded to BF16, the MMA's operand type (2^-8 relative at most), and the
@@ -65,10 +61,14 @@ namespace {
 
 constexpr int kRope = 64;
 constexpr int kTokens = 64;     // tokens in a tile
+constexpr int kCtaTokens = 32;  // of them, those a CTA brings as keys
 constexpr int kTileRows = 128;  // rows in a tile
+constexpr int kCtaRows = 64;
 constexpr int kMinBox = 8;      // tokens of a TMA box at least: pages are multiples of 8
-constexpr int kAttendThreads = 384;
+constexpr int kAttendThreads = 448;
 constexpr int kSoftmaxWarp = 4;
+constexpr int kFetchWarp = 12;
+constexpr int kValueMender = 13;
 constexpr int kMaxRequests = MXFP8_MAX_REQUESTS;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // A new maximum moves the reference of a row's exponentials only when it
@@ -79,55 +79,55 @@ constexpr float kLazy = 8.0f;
 // even deal's runs: about what a second row tile in a run costs.
 constexpr int kPieceSlack = 5;
 constexpr int kMinRun = 2;
-constexpr uint32_t kAtomBytes = kTokens * 128;  // 64 tokens x 64 columns
-constexpr uint32_t kRopeBytes = kTokens * 64;   // 64 tokens x 32 rotary columns
-constexpr uint32_t kQAtomBytes = kTileRows * 128;
-constexpr uint32_t kQRopeBytes = kTileRows * 64;
-// A group's partial scores from the peer (128 rows x 32 tokens x 4 bytes), then,
-// read out, its weights (128 rows x 64 tokens x 2 bytes, swizzled): either way
-// a quarter of 32 rows keeps to its own 4096 bytes.
-constexpr uint32_t kExchangeBytes = kTileRows * 128;
+constexpr uint32_t kBlockBytes = kCtaTokens * 128;  // 32 tokens x 64 columns
+constexpr uint32_t kQBlockBytes = kCtaRows * 128;   // 64 rows x 64 columns
+constexpr uint32_t kWeightBytes = kCtaRows * kTokens * 2;
 
 template <int kLatent>
 struct Shape {
-  static constexpr int kHalf = kLatent / 2;  // columns of a CTA
-  static constexpr int kAtoms = kHalf / 64;
-  static constexpr uint32_t kStageBytes = kAtoms * kAtomBytes + kRopeBytes;
-  static constexpr int kStages = kLatent == 512 ? 5 : 8;
+  static constexpr int kBlocks = kLatent / 64;
+  static constexpr int kHalf = kBlocks / 2;  // blocks of a CTA's value columns
+  // A place of the ring: a CTA's tokens, blocks of 64 columns, the rotary one
+  // last.
+  static constexpr uint32_t kPlaceBytes = (kBlocks + 1) * kBlockBytes;
+  static constexpr int kStages = kLatent == 512 ? 5 : 9;
+  // Blocks of the queries in tensor memory (in both halves of the lanes); the
+  // rest, the rotary one last, in shared memory.
+  static constexpr int kTmemBlocks = kLatent == 512 ? 6 : 4;
+  static constexpr int kSmemBlocks = kBlocks + 1 - kTmemBlocks;
   // Tensor-memory columns: outputs, queries (two BF16 a column), two score
   // tiles.
-  static constexpr uint32_t kQ = kHalf;
-  static constexpr uint32_t kS = kHalf + kHalf / 2;
-  // Shared memory: the ring; the two groups' exchanges; the rotary part of the
-  // queries.
-  static constexpr uint32_t kX = kStages * kStageBytes;
-  static constexpr uint32_t kQRope = kX + 2 * kExchangeBytes;
-  static constexpr uint32_t kMisc = kQRope + kQRopeBytes;
-  static_assert(kS + 2 * kTokens <= 512, "tensor memory");
-  static_assert(kAtoms / 2 * kQAtomBytes + kQRopeBytes / 2 == kStageBytes,
-                "half of the queries fill a place of the ring");
+  static constexpr int kColumns = kLatent / 2;  // of a lane's outputs
+  static constexpr uint32_t kQ = kColumns;
+  static constexpr uint32_t kS = kQ + kTmemBlocks * 32;
+  // Shared memory: the ring; the two groups' weights; queries.
+  static constexpr uint32_t kP = kStages * kPlaceBytes;
+  static constexpr uint32_t kQSmem = kP + 2 * kWeightBytes;
+  static constexpr uint32_t kMisc = kQSmem + kSmemBlocks * kQBlockBytes;
+  static_assert(kS + 2 * kCtaTokens <= 512, "tensor memory");
+  static_assert(kTmemBlocks / 2 * kQBlockBytes <= kPlaceBytes,
+                "half of tensor memory's queries fit a place of the ring");
 };
 
-constexpr int kMaxStages = 8;
+template <int kStages>
 struct Misc {
-  // Barriers, in four runs by their arrivals a phase.  Every one but `drained`
-  // completes once a use, in order.
-  uint64_t kv_full[kMaxStages], kv_ready[kMaxStages];    // 1 arrival
-  uint64_t s_full[2], pv_done[2];                        // [tile parity]
-  uint64_t recv[2][4], recv_credit[2][4];                // [group][lane quarter]
-  uint64_t weights[2][4], weights_credit[2][4], decided[2][4];
-  uint64_t tops[4];                                      // [lane quarter]
-  uint64_t drained;
-  uint64_t kv_empty[kMaxStages];                         // 2: outputs' commit, mender
-  uint64_t s_free[2], p_full[2];                         // 4: the group's warps
-  uint64_t q_ready;                                      // 8: all softmax warps
-  uint64_t bad[kMaxStages];  // non-finite drafts of a stage's tile, one bit a token
+  // Barriers, in runs by their arrivals a phase.  Every one but `drained`
+  // completes once a use, in order.  The issuer waits on the first CTA's, which
+  // both CTAs arrive on; a commit arrives on both CTAs'.
+  uint64_t kv_full[kStages], kv_empty[kStages];  // 1; [place of the ring]
+  uint64_t qk_done[kStages], v_full[kStages];    // 1; [token tile mod kStages]
+  uint64_t s_full[2], pv_done[2];                // 1; [tile parity]
+  uint64_t decided[2][4];                        // 1; [tile parity][lane quarter]
+  uint64_t q_full, drained;                      // 1
+  uint64_t k_ready[kStages], v_ready[kStages];   // 2: the CTAs' menders
+  uint64_t s_free[2], p_full[2];                 // 8: a group's warps in both CTAs
+  uint64_t q_ready;                              // 16: all softmax warps of both
   uint32_t tmem;
   int32_t abort;
   int32_t piece;  // token tiles of a piece, 0 for an even deal
-  float peer_top[kTileRows];         // the peer's maxima in the first tile
-  float reference[2][kTileRows];     // [tile parity][row], after that tile
-  float2 peer[2][kTileRows];         // [group][row]: (reference, sum) of the peer's tokens
+  float tops[2][2][128];             // [a group's tile parity][group][lane]: maxima
+  float reference[2][128];           // [tile parity][lane], after that tile
+  float sums[4][kCtaRows];           // [group, token half][row]
   uint32_t first[kMaxRequests + 1];  // runs (pieces, or token tiles) before each request
   int32_t length[kMaxRequests];
   uint16_t begin[kMaxRequests + 1];  // rows are at most MXFP8_MAX_LATENT_ROWS
@@ -194,10 +194,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t scale_bf16(uint32_t w, float f) {
-  return pack_bf16(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+__device__ __forceinline__ bool finite_bf16(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool finite = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    finite = finite && (w[i] & 0x7F80u) != 0x7F80u && (w[i] & 0x7F800000u) != 0x7F800000u;
+  return finite;
 }
 
+template <class Misc>
 __device__ __forceinline__ int drafts_of(const Misc& m, int b) {
   return max(m.begin[b + 1] - m.begin[b], 0);
 }
@@ -214,6 +220,7 @@ struct Walk {
   uint32_t at, end, from;  // of the list of runs
   int b;
 };
+template <class Misc>
 __device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& p, int cluster,
                                              Walk& w, Segment& s) {
   if (w.at >= w.end) return false;
@@ -304,14 +311,15 @@ struct Waiter {
 struct AttendParams {
   LatentParams in;
   int32_t clusters;
-  int32_t box;        // tokens of a TMA box: the largest of 64, 32, 16, 8 in a page
+  int32_t box;        // tokens of a TMA box: the largest of 32, 16, 8 in a page
   float4* partial;    // [2 clusters][latent / 4][128 rows] x 4 columns
   float2* stats;      // [2 clusters][128 rows] (reference, sum)
   int32_t* piece;     // the deal: token tiles of a piece, 0 for equal runs
 };
 struct AttendMaps {
-  CUtensorMap latent, rope;  // boxes of `box` tokens
-  CUtensorMap q, q_rope;     // boxes of 128 and of 64 rows
+  // Boxes of 64 columns by `box` tokens (64 rows), by as many blocks of columns
+  // as a copy takes.
+  CUtensorMap keys, values, q;
 };
 
 // Token tiles of a cluster's run in an even deal.
@@ -321,6 +329,7 @@ __device__ __forceinline__ uint32_t run_length(uint32_t tiles, int clusters) {
 
 // The deal, by one warp: fills Misc's lists.  (The host has checked that all
 // token tiles number less than 2^31.)
+template <class Misc>
 __device__ __forceinline__ void deal(Misc& m, const AttendParams& ap, int lane) {
   const LatentParams& p = ap.in;
   uint32_t before = 0;
@@ -385,34 +394,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                   const __grid_constant__ AttendParams ap) {
   using L = Shape<kLatent>;
   constexpr int kStages = L::kStages;
+  using Local = Misc<kStages>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw;
   const uint32_t sbase = ptx::smem_addr(smem);
-  Misc& m = *reinterpret_cast<Misc*>(smem + L::kMisc);
+  Local& m = *reinterpret_cast<Local*>(smem + L::kMisc);
   const LatentParams& p = ap.in;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t rank = ptx::cluster_ctarank();
   const int cluster = blockIdx.x / 2;
   auto bar = [&](const uint64_t& b) { return ptx::smem_addr(&b); };
+  auto first_cta = [&](const uint64_t& b) { return ptx::map_to_rank(ptx::smem_addr(&b), 0); };
   if (sbase % 1024u != 0) {  // the swizzles count from 1024-byte boundaries
     raise(p.flags, MXFP8_FLAG_GEMM_TIMEOUT);
     return;
   }
 
   if (warp == 0) {
-    constexpr int kTwo = offsetof(Misc, kv_empty) / 8, kFour = offsetof(Misc, s_free) / 8;
-    constexpr int kEight = offsetof(Misc, q_ready) / 8;
-    for (int i = lane; i <= kEight; i += 32)
-      ptx::mbar_init(bar(m.kv_full[0]) + 8u * i, i < kTwo ? 1 : i < kFour ? 2 : i < kEight ? 4 : 8);
+    constexpr int kTwo = offsetof(Local, k_ready) / 8, kEight = offsetof(Local, s_free) / 8;
+    constexpr int kLast = offsetof(Local, q_ready) / 8;
+    for (int i = lane; i <= kLast; i += 32)
+      ptx::mbar_init(bar(m.kv_full[0]) + 8u * i, i < kTwo ? 1 : i < kEight ? 2 : i < kLast ? 8 : 16);
     if (lane == 0) m.abort = 0;
     ptx::fence_mbarrier_init();
     ptx::fence_proxy_async_smem();
   }
   if (warp == 1) {
-    ptx::tmem_alloc(ptx::smem_addr(&m.tmem), 512);
-    ptx::tmem_relinquish();
+    ptx::tmem_alloc_pair(ptx::smem_addr(&m.tmem), 512);
+    ptx::tmem_relinquish_pair();
   }
-  if (warp == 2 && lane < 4)
+  if (warp == 2 && lane < 3)
     ptx::prefetch_tensormap(reinterpret_cast<const CUtensorMap*>(&maps) + lane);
   ptx::tc_fence_before();
   ptx::cluster_sync();
@@ -430,49 +441,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   Walk walk{from, min(all, from + run), from, 0};
   Segment seg{};
   const Waiter wait{&m.abort, p.flags};
+  // The page of the box with token `token`: in the pool, or past it (then the
+  // copy fills zeros) for a box past the length.
+  auto read_page = [&](int token) {
+    if (token >= seg.length) return p.pages;
+    return p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
+  };
 
   if (warp == 0 || warp == 3) {
     // -------------------------------------------------------------- producer
-    // A lane a box (one thread's copies are served one after another).  The
-    // page of a lane's box is read one of this warp's tiles ahead.
+    // A tile's part in one copy where a page holds 32 tokens in a row, else a
+    // lane a box of each block.  The page of a lane's box is read one of this
+    // warp's tiles ahead.
     const int which = warp == 3;
-    constexpr int kItems = (kTokens / kMinBox * (L::kAtoms + 1) + 31) / 32;  // of a lane
+    constexpr int kItems = (kCtaTokens / kMinBox * (L::kBlocks + 1) + 31) / 32;  // of a lane
     const uint64_t keep = ptx::policy_evict_last();
-    // The page of copy i of tile kv (box i / (atoms + 1)): in the pool, or past
-    // it (then the copy fills zeros) for a box past the length.
-    const int items = kTokens / ap.box * (L::kAtoms + 1);
-    auto read_page = [&](int kv, int i) {
-      const int token = kv * kTokens + i / (L::kAtoms + 1) * ap.box;
-      if (i >= items || token >= seg.length) return p.pages;
-      return p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
+    const int blocks = ap.box == kCtaTokens ? 1 : L::kBlocks + 1;  // copies of a box
+    const int items = kCtaTokens / ap.box * blocks;
+    // The first token of copy i of this CTA's part of tile kv.
+    auto token_of = [&](int kv, int i) {
+      return kv * kTokens + static_cast<int>(rank) * kCtaTokens + i / blocks * ap.box;
+    };
+    auto page_of = [&](int kv, int i) {
+      return kv < seg.kv1 && i < items ? read_page(token_of(kv, i)) : p.pages;
     };
     int r = 0;  // places of the ring, of both warps
     bool ok = true;
-    auto place = [&](uint32_t& full) {  // place r, once it is free
+    auto place = [&](uint32_t bytes, uint32_t& full) {  // place r, once it is free
       if (r >= kStages) ok = __all_sync(~0u, wait(m.kv_empty[r % kStages], r / kStages - 1));
       full = bar(m.kv_full[r % kStages]);
-      if (ok && lane == 0) ptx::mbar_arrive_expect_tx(full, L::kStageBytes);
+      if (ok && lane == 0) ptx::mbar_arrive_expect_tx(full, bytes);
       __syncwarp();
       return ok;
     };
     while (ok && next_segment(m, p, cluster, walk, seg)) {
       uint32_t full;
-      // The queries: half of this CTA's columns and half of the rows' rotary
-      // part a place.
+      // The queries that go to tensor memory, half of their blocks a place.
       for (int half = 0; half < 2; ++half, ++r) {
         if ((r & 1) != which) continue;
-        if (!place(full)) break;
-        const uint32_t dst = sbase + r % kStages * L::kStageBytes;
-        const int row = seg.begin * p.heads + seg.row0;
-        if (lane < L::kAtoms / 2)
-          ptx::tma_load_2d(dst + lane * kQAtomBytes, &maps.q,
-                           static_cast<int>(rank) * L::kHalf +
-                               (half * (L::kAtoms / 2) + lane) * 64,
-                           row, full, ptx::policy_evict_first());
-        else if (lane == L::kAtoms / 2)
-          ptx::tma_load_2d(dst + L::kAtoms * kAtomBytes, &maps.q_rope,
-                           static_cast<int>(rank) * 32, row + half * 64, full,
-                           ptx::policy_evict_first());
+        if (!place(L::kTmemBlocks / 2 * kQBlockBytes, full)) break;
+        if (lane < L::kTmemBlocks / 2)
+          ptx::tma_load_2d(sbase + r % kStages * L::kPlaceBytes + lane * kQBlockBytes, &maps.q,
+                           (half * (L::kTmemBlocks / 2) + lane) * 64,
+                           seg.begin * p.heads + seg.row0 + static_cast<int>(rank) * kCtaRows,
+                           full, ptx::policy_evict_first());
         __syncwarp();
       }
       if (!ok) break;
@@ -480,34 +492,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       const int first = seg.kv0 + ((r & 1) != which);
       int page[kItems];
 #pragma unroll
-      for (int k = 0; k < kItems; ++k)
-        page[k] = first < seg.kv1 ? read_page(first, lane + 32 * k) : p.pages;
+      for (int k = 0; k < kItems; ++k) page[k] = page_of(first, lane + 32 * k);
       const int r0 = r - seg.kv0;
       for (int kv = first; kv < seg.kv1; kv += 2) {
         r = r0 + kv;
         int next[kItems];
 #pragma unroll
-        for (int k = 0; k < kItems; ++k)
-          next[k] = kv + 2 < seg.kv1 ? read_page(kv + 2, lane + 32 * k) : p.pages;
-        if (!place(full)) break;
-        const uint32_t dst = sbase + r % kStages * L::kStageBytes;
+        for (int k = 0; k < kItems; ++k) next[k] = page_of(kv + 2, lane + 32 * k);
+        if (!place(L::kPlaceBytes, full)) break;
+        const uint32_t dst = sbase + r % kStages * L::kPlaceBytes;
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
           const int i = lane + 32 * k;
           if (i >= items) continue;
-          const int at = i / (L::kAtoms + 1) * ap.box, atom = i % (L::kAtoms + 1);
+          const int block = i % blocks, at = i / blocks * ap.box;
+          const int token = token_of(kv, i);
           if (page[k] < 0 || page[k] >= p.pages) {
-            if (kv * kTokens + at < seg.length) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
+            if (token < seg.length) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
             page[k] = p.pages;
           }
-          const int slot = (kv * kTokens + at) % p.page_size;
-          if (atom < L::kAtoms)
-            ptx::tma_load_3d(dst + atom * kAtomBytes + at * 128, &maps.latent,
-                             static_cast<int>(rank) * L::kHalf + atom * 64, slot, page[k], full,
-                             keep);
-          else
-            ptx::tma_load_3d(dst + L::kAtoms * kAtomBytes + at * 64, &maps.rope,
-                             static_cast<int>(rank) * 32, slot, page[k], full, keep);
+          ptx::tma_load_4d(dst + block * kBlockBytes + at * 128, &maps.keys, 0,
+                           token % p.page_size, block, page[k], full, keep);
         }
         __syncwarp();
 #pragma unroll
@@ -520,81 +525,144 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     for (int i = max(0, r - kStages); !ok && i < r; ++i)
       ptx::mbar_wait(bar(m.kv_full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u,
                      kWaitLimitNs / 16);
+  } else if (warp == kFetchWarp) {
+    // ----------------------------------------------------------------- fetch
+    // This CTA's value columns of the peer's tokens, over the blocks of its own
+    // tokens that only the keys' product reads.
+    const uint64_t keep = ptx::policy_evict_last();
+    const int blocks = ap.box == kCtaTokens ? 1 : L::kHalf;  // copies of a box
+    const int items = kCtaTokens / ap.box * blocks;          // at most 16
+    const int column0 = static_cast<int>(rank) * L::kHalf, theirs = static_cast<int>(rank ^ 1u);
+    auto token_of = [&](int kv) {
+      return kv * kTokens + theirs * kCtaTokens + lane / blocks * ap.box;
+    };
+    auto page_of = [&](int kv) {
+      return kv < seg.kv1 && lane < items ? read_page(token_of(kv)) : p.pages;
+    };
+    int r = 0, j = 0;  // places of the ring, token tiles
+    uint32_t segments = 0;
+    bool ok = true;
+    for (; ok && next_segment(m, p, cluster, walk, seg); ++segments) {
+      // Every product with the last row tile's queries is done.
+      const uint32_t full = bar(m.q_full);
+      if (lane == 0) ptx::mbar_arrive_expect_tx(full, L::kSmemBlocks * kQBlockBytes);
+      __syncwarp();
+      if (lane < L::kSmemBlocks)
+        ptx::tma_load_2d(sbase + L::kQSmem + lane * kQBlockBytes, &maps.q,
+                         (L::kTmemBlocks + lane) * 64,
+                         seg.begin * p.heads + seg.row0 + static_cast<int>(rank) * kCtaRows, full,
+                         ptx::policy_evict_first());
+      __syncwarp();
+      r += 2;
+      int page = page_of(seg.kv0);
+      for (int kv = seg.kv0; kv < seg.kv1; ++kv, ++r, ++j) {
+        const int next = page_of(kv + 1);
+        ok = __all_sync(~0u, wait(m.qk_done[j % kStages], j / kStages));
+        if (!ok) break;
+        const uint32_t done = bar(m.v_full[j % kStages]);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(done, L::kHalf * kBlockBytes);
+        __syncwarp();
+        if (lane < items) {
+          const int block = lane % blocks, at = lane / blocks * ap.box;
+          if (page < 0 || page >= p.pages) page = p.pages;
+          ptx::tma_load_4d(sbase + r % kStages * L::kPlaceBytes +
+                               (theirs * L::kHalf + block) * kBlockBytes + at * 128,
+                           &maps.values, 0, token_of(kv) % p.page_size, column0 + block, page,
+                           done, keep);
+        }
+        __syncwarp();
+        page = next;
+      }
+    }
+    if (!ok) {
+      if (segments > 0) ptx::mbar_wait(bar(m.q_full), (segments - 1) & 1u, kWaitLimitNs / 16);
+      for (int i = max(0, j - kStages); i < j; ++i)
+        ptx::mbar_wait(bar(m.v_full[i % kStages]), static_cast<uint32_t>(i / kStages) & 1u,
+                       kWaitLimitNs / 16);
+    }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // The warp stays converged and one elected lane issues: 32 clocks a
-    // 128 x 64 x 16 product with the queries in tensor memory, the rate of the
-    // tensor core; from a branch on the lane number it took 46.
+    // ---------------------------------------------------------------- issuer
+    // The warp stays converged and one elected lane issues (from a branch on
+    // the lane number a product took half as long again).  A pair's 128 x 64 x
+    // 16 product takes 18 clocks with the queries in tensor memory, 25 with
+    // them in shared memory; 128 x 256 x 16 takes 64, the tensor cores' rate.
     constexpr uint32_t kScores = ptx::idesc_bf16(kTokens, false);
-    constexpr uint32_t kOutputs = ptx::idesc_bf16(L::kHalf, true);
-    const uint32_t q_rope = sbase + L::kQRope;
+    constexpr uint32_t kOutputs = ptx::idesc_bf16(256, true);
     int g = 0;  // token tiles before the segment
     int r = 0;  // places of the ring before its first token tile
     uint32_t segments = 0;
-    bool ok = true;
-    auto tile_bar = [&](int i) -> const uint64_t& {
-      const int stage = (r + i) % kStages;
-      return special(seg, seg.kv0 + i) ? m.kv_ready[stage] : m.kv_full[stage];
-    };
+    bool ok = rank == 0;
     auto scores = [&](int i) {
-      const int j = g + i, stage = (r + i) % kStages;
+      const int j = g + i;
       ptx::tc_fence_after();
-      const uint32_t kvb = sbase + stage * L::kStageBytes;
-      const uint32_t d = tmem + L::kS + (j & 1) * kTokens;
-      const uint32_t done = bar(m.s_full[j & 1]);
+      const uint32_t keys = sbase + (r + i) % kStages * L::kPlaceBytes;
+      const uint32_t d = tmem + L::kS + (j & 1) * kCtaTokens;
+      const uint32_t done = bar(m.s_full[j & 1]), fetch = bar(m.qk_done[j % kStages]);
       if (ptx::elect_one()) {
 #pragma unroll
-        for (int k = 0; k < L::kHalf / 16; ++k)
-          ptx::mma_f16_ts(d, tmem + L::kQ + k * 8,
-                          ptx::desc_kmajor_sw128(kvb + (k / 4) * kAtomBytes + (k % 4) * 32),
-                          kScores, k > 0);
+        for (int k = 0; k < L::kTmemBlocks * 4; ++k)
+          ptx::mma_f16_ts_pair(d, tmem + L::kQ + k * 8,
+                               ptx::desc_kmajor_sw128(keys + (k / 4) * kBlockBytes + (k % 4) * 32),
+                               kScores, k > 0);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-          ptx::mma_f16_ss(d, ptx::desc_kmajor_sw64(q_rope + k * 32),
-                          ptx::desc_kmajor_sw64(kvb + L::kAtoms * kAtomBytes + k * 32), kScores,
-                          1u);
-        ptx::mma_commit(done);
+        for (int k = 0; k < L::kSmemBlocks * 4; ++k)
+          ptx::mma_f16_ss_pair(d,
+                               ptx::desc_kmajor_sw128(sbase + L::kQSmem + (k / 4) * kQBlockBytes +
+                                                      (k % 4) * 32),
+                               ptx::desc_kmajor_sw128(keys + (L::kTmemBlocks + k / 4) * kBlockBytes +
+                                                      (k % 4) * 32),
+                               kScores, 1u);
+        ptx::mma_commit_pair(fetch);
+        ptx::mma_commit_pair(done);
       }
       __syncwarp();
     };
     auto outputs = [&](int i) {
       const int j = g + i, stage = (r + i) % kStages;
       ptx::tc_fence_after();
-      const uint32_t kvb = sbase + stage * L::kStageBytes;
-      const uint32_t weights = sbase + L::kX + (j & 1) * kExchangeBytes;
+      const uint32_t values = sbase + stage * L::kPlaceBytes;
+      const uint32_t weights = sbase + L::kP + (j & 1) * kWeightBytes;
       const uint32_t add = i > 0;
       const uint32_t empty = bar(m.kv_empty[stage]), done = bar(m.pv_done[j & 1]);
       if (ptx::elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTokens / 16; ++k)
-          ptx::mma_f16_ss(tmem, ptx::desc_kmajor_sw128(weights + k * 32),
-                          ptx::desc_mnmajor_sw128(kvb + k * 2048, kAtomBytes), kOutputs,
-                          k > 0 ? 1u : add);
-        ptx::mma_commit(empty);
-        ptx::mma_commit(done);
+#pragma unroll
+          for (int c = 0; c < L::kColumns / 128; ++c)  // 128 of each CTA's columns
+            ptx::mma_f16_ss_pair(
+                tmem + c * 128, ptx::desc_kmajor_sw128(weights + k * 32),
+                ptx::desc_mnmajor_sw128(values + (k / 2 * L::kHalf + 2 * c) * kBlockBytes +
+                                            (k % 2) * 2048,
+                                        kBlockBytes),
+                kOutputs, k > 0 ? 1u : add);
+        ptx::mma_commit_pair(empty);
+        ptx::mma_commit_pair(done);
       }
       __syncwarp();
     };
     while (ok && next_segment(m, p, cluster, walk, seg)) {
       ok = __all_sync(~0u, wait(m.q_ready, segments++));
-      if (lane == 0) {  // every softmax warp has read the queries
-        ptx::mbar_arrive(bar(m.kv_empty[r % kStages]));
-        ptx::mbar_arrive(bar(m.kv_empty[(r + 1) % kStages]));
-      }
+      // Every softmax warp has read the queries.
+      if (lane < 4)
+        ptx::mbar_arrive_remote(
+            ptx::map_to_rank(bar(m.kv_empty[(r + lane / 2) % kStages]), lane % 2));
+      __syncwarp();
       r += 2;
       const int tiles = seg.kv1 - seg.kv0;
       // Whichever is ready: the scores of tile s (its tokens there, and the
       // scores of tile s - 2 read out of their buffer) or the outputs of tile o
-      // (its weights there).  Neither waits behind the other, so a late tile
-      // does not keep an earlier one's place in the ring.
+      // (its weights and values there).  Neither waits behind the other, so a
+      // late tile does not keep an earlier one's place in the ring.
       int s = 0, o = 0, spins = 0;
       uint64_t start = 0;
       while (ok && o < tiles) {
-        if (s < tiles && s <= o + 2 && wait.ready(tile_bar(s), (r + s) / kStages) &&
+        if (s < tiles && s <= o + 2 &&
+            wait.ready(m.k_ready[(g + s) % kStages], (g + s) / kStages) &&
             (s < 2 || wait.ready(m.s_free[(g + s) & 1], (g + s - 2) >> 1))) {
           scores(s++);
           spins = 0;
-        } else if (o < s && wait.ready(m.p_full[(g + o) & 1], (g + o) >> 1)) {
+        } else if (o < s && wait.ready(m.p_full[(g + o) & 1], (g + o) >> 1) &&
+                   wait.ready(m.v_ready[(g + o) % kStages], (g + o) / kStages)) {
           outputs(o++);
           spins = 0;
         } else if (spins++ % 64 == 0) {
@@ -604,208 +672,181 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       g += tiles;
       r += tiles;
     }
-    // Nothing runs on when tensor memory is freed.
-    if (ptx::elect_one()) ptx::mma_commit(bar(m.drained));
-    __syncwarp();
-    ptx::mbar_wait(bar(m.drained), 0, kWaitLimitNs);
+    if (rank == 0) {  // nothing runs on when tensor memory is freed
+      if (ptx::elect_one()) ptx::mma_commit_pair(bar(m.drained));
+      __syncwarp();
+      ptx::mbar_wait(bar(m.drained), 0, kWaitLimitNs);
+    }
   } else if (warp == 2) {
-    // ---------------------------------------------------------------- mender
-    int r = 0;
+    // ---------------------------------------------------------- keys' mender
+    // A draft with a non-finite number in its latent gets NaN for a score from
+    // every row: an infinity alone could come out as a weight of zero.
+    int r = 0, j = 0;
     bool ok = true;
     while (ok && next_segment(m, p, cluster, walk, seg)) {
-      for (int kv = seg.kv0 - 2; ok && kv < seg.kv1; ++kv, ++r) {  // two of queries first
-        const int stage = r % kStages;
-        ok = __all_sync(~0u, wait(m.kv_full[stage], r / kStages));
+      for (int kv = seg.kv0 - 2; kv < seg.kv1; ++kv, ++r) {  // two of queries first
+        ok = __all_sync(~0u, wait(m.kv_full[r % kStages], r / kStages));
         if (!ok) break;
-        if (kv >= seg.kv0 && special(seg, kv)) {
-          uint8_t* kvp = smem + stage * L::kStageBytes;
-          const int n0 = max(seg.context - kv * kTokens, 0);
-          const int n1 = min(seg.length - kv * kTokens, kTokens);
+        if (kv < seg.kv0) continue;
+        if (special(seg, kv)) {
+          uint8_t* keys = smem + r % kStages * L::kPlaceBytes;
+          const int at = kv * kTokens + static_cast<int>(rank) * kCtaTokens;
+          const int n0 = max(seg.context - at, 0), n1 = min(seg.length - at, kCtaTokens);
           // A token's 128-byte rows hold their 16-byte chunks in swizzled order,
-          // which neither a search nor a fill minds.
-          uint64_t bad = 0;
+          // which a search does not mind.
           for (int n = n0; n < n1; ++n) {
             bool finite = true;
-            if (lane < L::kAtoms * 8) {
-              const uint4 v = *reinterpret_cast<const uint4*>(kvp + (lane / 8) * kAtomBytes +
-                                                              n * 128 + (lane % 8) * 16);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                finite = finite && (w[q] & 0x7F80u) != 0x7F80u &&
-                         (w[q] & 0x7F800000u) != 0x7F800000u;
-            }
-            if (!__all_sync(~0u, finite)) bad |= 1ull << n;
+            for (int i = 0; i < L::kBlocks * 8; i += 32)
+              finite = finite && finite_bf16(*reinterpret_cast<const uint4*>(
+                                     keys + (i + lane) / 8 * kBlockBytes + n * 128 + lane % 8 * 16));
+            if (!__all_sync(~0u, finite) && lane == 0)
+              *reinterpret_cast<uint16_t*>(keys + n * 128) = 0x7FC0u;
+          }
+          ptx::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_remote(first_cta(m.k_ready[j % kStages]));
+        ++j;
+      }
+    }
+  } else if (warp == kValueMender) {
+    // -------------------------------------------------------- values' mender
+    // Zeros for the tokens past the length and for drafts that are not finite:
+    // rows that do not see them give them weights of zero.
+    int r = 0, j = 0;
+    bool ok = true;
+    while (ok && next_segment(m, p, cluster, walk, seg)) {
+      r += 2;
+      for (int kv = seg.kv0; kv < seg.kv1; ++kv, ++r, ++j) {
+        ok = __all_sync(~0u, wait(m.v_full[j % kStages], j / kStages));
+        if (!ok) break;
+        if (special(seg, kv)) {
+          wait(m.kv_full[r % kStages], r / kStages);  // (over since the keys' product)
+          uint8_t* values = smem + r % kStages * L::kPlaceBytes;
+          const int n0 = max(seg.context - kv * kTokens, 0);
+          const int n1 = min(seg.length - kv * kTokens, kTokens);
+          auto row_of = [&](int n) {
+            return values + n / kCtaTokens * L::kHalf * kBlockBytes + n % kCtaTokens * 128;
+          };
+          uint64_t fill = 0;
+          for (int n = n0; n < n1; ++n) {
+            bool finite = true;
+            if (lane < L::kHalf * 8)
+              finite = finite_bf16(*reinterpret_cast<const uint4*>(
+                  row_of(n) + lane / 8 * kBlockBytes + lane % 8 * 16));
+            if (!__all_sync(~0u, finite)) fill |= 1ull << n;
           }
           // Boxes past the length came as zeros; the rest of the last one is
           // filled here.
-          const uint64_t fill =
-              bad | (low_ones((n1 + ap.box - 1) / ap.box * ap.box) & ~low_ones(n1));
+          fill |= low_ones((n1 + ap.box - 1) / ap.box * ap.box) & ~low_ones(n1);
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
           for (int n = lane / 8; n < kTokens; n += 4) {  // 8 lanes a token's row of 128 bytes
             if (!(fill >> n & 1)) continue;
 #pragma unroll
-            for (int atom = 0; atom < L::kAtoms; ++atom)
-              *reinterpret_cast<uint4*>(kvp + atom * kAtomBytes + n * 128 + lane % 8 * 16) = zero;
-            if (lane % 8 < 4)
-              *reinterpret_cast<uint4*>(kvp + L::kAtoms * kAtomBytes + n * 64 + lane % 8 * 16) =
-                  zero;
+            for (int block = 0; block < L::kHalf; ++block)
+              *reinterpret_cast<uint4*>(row_of(n) + block * kBlockBytes + lane % 8 * 16) = zero;
           }
-          if (lane == 0) m.bad[stage] = bad;
           ptx::fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(bar(m.kv_ready[stage]));
-          ptx::mbar_arrive(bar(m.kv_empty[stage]));
-        }
+        if (lane == 0) ptx::mbar_arrive_remote(first_cta(m.v_ready[j % kStages]));
       }
     }
-  } else if (warp >= kSoftmaxWarp) {
+  } else {
     // --------------------------------------------------------------- softmax
     const int group = (warp - kSoftmaxWarp) / 4;  // takes the tiles of this parity
     const int quarter = warp & 3;  // the 32 tensor-memory lanes this warp reaches
-    const int row = quarter * 32 + lane;
+    // Quarters 0 and 1 hold the rows' scores of the first half of a tile's
+    // tokens and the outputs' first half of the columns, 2 and 3 the second.
+    const int half = quarter / 2, row = quarter % 2 * 32 + lane;
+    const int place_of_row = quarter * 32 + lane;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t score = lanes + L::kS + group * kTokens;
-    const uint32_t peer = rank ^ 1u;
-    const uint32_t recv_offset =
-        L::kX + group * kExchangeBytes + quarter * 4096u + lane * 16u;
-    const float4* recv = reinterpret_cast<const float4*>(smem + recv_offset);
-    // A row of weights is one 128-byte swizzled row: this CTA's 32 tokens are
-    // chunks 4 rank .. 4 rank + 3, in its own operand and in the peer's.
-    const uint32_t p_row = L::kX + group * kExchangeBytes + row * 128u;
-    auto chunk_at = [&](uint32_t half, int c) { return ((half * 4u + c) ^ (row & 7u)) * 16u; };
-    const uint64_t& recv_bar = m.recv[group][quarter];
-    const uint64_t& weights_bar = m.weights[group][quarter];
-    // The peer's copy of a shared-memory address is this much further.
-    const uint32_t over = ptx::map_to_rank(sbase, peer) - sbase;
-    auto there = [&](const auto& x) { return ptx::smem_addr(&x) + over; };
-    uint32_t exchanges = 0;  // tiles this warp exchanged
+    const uint32_t score = lanes + L::kS + group * kCtaTokens;
+    // A row of weights is one 128-byte swizzled row, this thread's tokens half
+    // of its chunks.
+    uint8_t* weights = smem + L::kP + group * kWeightBytes + row * 128;
     uint32_t decisions = 0;  // tiles of this quarter's rows, of both groups
-    uint32_t firsts = 0;     // row tiles of this quarter
     int g = 0;               // token tiles before the segment
     int r = 0;               // places of the ring before its first token tile
-    // The peer may send this group its scores; after that, a permit follows
-    // every tile whose outputs are added (its weights lay where scores land).
-    if (lane == 0) ptx::mbar_arrive_remote_relaxed(there(m.recv_credit[group][quarter]));
+    // The outputs of tile j are added.  A parity tells a phase from the next
+    // alone: a group waits for its own tile j - 2 before it gives tile j's weights
+    // away, so neither group's barrier is ever more than a phase ahead of a wait
+    // (products, and their commits, are done in order).
+    auto added = [&](int j) { wait(m.pv_done[j & 1], j >> 1); };
+    auto all_added = [&](int tiles) {
+      if (tiles > 1 && ((g + tiles) & 1) == group) added(g + tiles - 2);
+      added(g + tiles - 1);
+    };
     for (uint32_t segments = 0; next_segment(m, p, cluster, walk, seg); ++segments) {
-      const size_t q_row = static_cast<size_t>(seg.begin) * p.heads + seg.row0 + row;
-      const bool mine = row < seg.valid;
-      const bool active = quarter * 32 < seg.valid;  // of the warp
+      const int tile_row = static_cast<int>(rank) * kCtaRows + row;
+      const size_t q_row = static_cast<size_t>(seg.begin) * p.heads + seg.row0 + tile_row;
+      const bool mine = tile_row < seg.valid;
+      const bool active = tile_row - lane < seg.valid;  // of the warp
       const int tiles = seg.kv1 - seg.kv0;
       const int i0 = (g & 1) != group;  // this group's first tile
-      // Queries, from the ring: half of this CTA's columns a group into tensor
-      // memory, and half of a row's rotary part (already swizzled).
+      // Queries, from the ring into tensor memory, half of the blocks a group.
       wait(m.kv_full[r % kStages], r / kStages);
       wait(m.kv_full[(r + 1) % kStages], (r + 1) / kStages);
+      wait(m.q_full, segments);
       if (active) {
-        const uint8_t* src = smem + (r + group) % kStages * L::kStageBytes + row * 128;
+        const uint8_t* src = smem + (r + group) % kStages * L::kPlaceBytes + row * 128;
 #pragma unroll
-        for (int half = 0; half < L::kAtoms / 2; ++half) {
+        for (int block = 0; block < L::kTmemBlocks / 2; ++block) {
           uint32_t v[32];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src + half * kQAtomBytes +
+            const uint4 x = *reinterpret_cast<const uint4*>(src + block * kQBlockBytes +
                                                             ((i ^ (row & 7)) * 16));
             v[4 * i] = x.x, v[4 * i + 1] = x.y, v[4 * i + 2] = x.z, v[4 * i + 3] = x.w;
           }
-          ptx::tmem_st_32x32b_x32(lanes + L::kQ + (group * (L::kAtoms / 2) + half) * 32, v);
+          ptx::tmem_st_32x32b_x32(lanes + L::kQ + (group * (L::kTmemBlocks / 2) + block) * 32, v);
         }
-        const uint8_t* rope = smem + (r + row / 64) % kStages * L::kStageBytes +
-                              L::kAtoms * kAtomBytes + row % 64 * 64;
-#pragma unroll
-        for (int i = 2 * group; i < 2 * group + 2; ++i)
-          *reinterpret_cast<uint4*>(smem + L::kQRope + row * 64 + i * 16) =
-              *reinterpret_cast<const uint4*>(rope + i * 16);
         ptx::tmem_wait_st();
-        ptx::fence_proxy_async_smem();
       }
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(bar(m.q_ready));
+      if (lane == 0) ptx::mbar_arrive_remote(first_cta(m.q_ready));
       r += 2;
       if (!active) {
         for (int i = i0; i < tiles; i += 2) {
           wait(m.s_full[group], (g + i) >> 1);
-          if (lane == 0) {
-            ptx::mbar_arrive(bar(m.s_free[group]));
-            ptx::mbar_arrive(bar(m.p_full[group]));
-          }
           // (The scores two tiles on may come before this tile's weights: no
           // second arrival at one phase.)
-          wait(m.p_full[group], (g + i) >> 1);
+          if (i >= 2) added(g + i - 2);
+          if (lane == 0) {
+            ptx::mbar_arrive_remote(first_cta(m.s_free[group]));
+            ptx::mbar_arrive_remote(first_cta(m.p_full[group]));
+          }
         }
-        // Not on to the next segment before every warp has come to this one.
-        wait(m.q_ready, segments);
+        // Not on to the next segment before this one is done.
+        all_added(tiles);
         g += tiles;
         r += tiles;
         continue;
       }
       // What this row sees of the drafts.
-      const int t = (seg.row0 + row) / p.heads;
+      const int t = (seg.row0 + tile_row) / p.heads;
       const uint64_t tree =
           p.tree != nullptr && mine ? static_cast<uint64_t>(p.tree[seg.begin + t]) : 0;
-      // After this group's last tile: the row's common reference, and this
-      // CTA's tokens' sum under `base`.
-      float known = -INFINITY, base = -INFINITY, total = 0.0f;
+      // After this group's last tile: the reference, and the sum of this
+      // thread's tokens under it.
+      float base = -INFINITY, total = 0.0f;
 
-      for (int i = i0; i < tiles; i += 2, ++exchanges) {
-        const int kv = seg.kv0 + i;
+      for (int i = i0; i < tiles; i += 2) {
+        const int kv = seg.kv0 + i, j = g + i;
         const uint32_t decision = decisions + i;
-        if (i > i0) {
-          wait(m.pv_done[group], (g + i - 2) >> 1);
-          if (lane == 0) ptx::mbar_arrive_remote_relaxed(there(m.recv_credit[group][quarter]));
-        }
-        if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(bar(recv_bar), 32u * 32u * 4u);
-          ptx::mbar_arrive_expect_tx(bar(weights_bar), 32u * (64u + 8u));
-          if (i == 0) ptx::mbar_arrive_expect_tx(bar(m.tops[quarter]), 32u * 4u);
-        }
-        wait(m.s_full[group], (g + i) >> 1);
+        wait(m.s_full[group], j >> 1);
         ptx::tc_fence_after();
-        uint32_t other[32], own[32];
-        ptx::tmem_ld_32x32b_x32(score + peer * 32, other);
-        ptx::tmem_ld_32x32b_x32(score + rank * 32, own);
+        uint32_t raw[32];
+        ptx::tmem_ld_32x32b_x32(score, raw);
         ptx::tmem_wait_ld();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(bar(m.s_free[group]));
-        if (special(seg, kv)) {
-          const int stage = (r + i) % kStages;
-          wait(m.kv_ready[stage], (r + i) / kStages);
-          const uint64_t bad = m.bad[stage];
-          if (bad != 0) {
-            const uint32_t bad_other = static_cast<uint32_t>(bad >> (32 * peer));
-            const uint32_t bad_own = static_cast<uint32_t>(bad >> (32 * rank));
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (bad_other >> c & 1u) other[c] = 0x7FC00000u;
-              if (bad_own >> c & 1u) own[c] = 0x7FC00000u;
-            }
-          }
-        }
-        // Scores: the peer's tokens out, its partials of this CTA's in.
-        wait.cluster(m.recv_credit[group][quarter], exchanges);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-          ptx::st_async_remote_v4(sbase + recv_offset + over + c * 512,
-                                  make_uint4(other[4 * c], other[4 * c + 1], other[4 * c + 2],
-                                             other[4 * c + 3]),
-                                  there(recv_bar));
-        wait.cluster(recv_bar, exchanges);
+        if (lane == 0) ptx::mbar_arrive_remote(first_cta(m.s_free[group]));
         float z[32];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const float4 x = recv[c * 32];
-          const float2 lo = add2(make_float2(__uint_as_float(own[4 * c]),
-                                             __uint_as_float(own[4 * c + 1])),
-                                 make_float2(x.x, x.y));
-          const float2 hi = add2(make_float2(__uint_as_float(own[4 * c + 2]),
-                                             __uint_as_float(own[4 * c + 3])),
-                                 make_float2(x.z, x.w));
-          z[4 * c] = lo.x, z[4 * c + 1] = lo.y, z[4 * c + 2] = hi.x, z[4 * c + 3] = hi.y;
-        }
+        for (int c = 0; c < 32; ++c) z[c] = __uint_as_float(raw[c]);
         if (special(seg, kv)) {
           const int at = kv * kTokens;
           uint64_t sees;
@@ -817,7 +858,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             sees = low_ones(seg.context + t + 1 - at);
           }
           sees &= low_ones(seg.length - at);
-          const uint32_t bits = static_cast<uint32_t>(sees >> (32 * rank));
+          const uint32_t bits = static_cast<uint32_t>(sees >> (32 * half));
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (!(bits >> c & 1u)) z[c] = -INFINITY;
@@ -831,38 +872,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         for (int c = 0; c < 4; ++c) tops[c] = max3(tops[c], z[c + 20], z[c + 24]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tops[c] = fmaxf(tops[c], z[c + 28]);
-        const float top =
-            fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
-        // The received scores have returned their values (each went into the
-        // maximum), so the peer's weights may come over them.  (A release here
-        // would wait for this CTA's own stores to the peer: it cost 60 us of 320
-        // on 8 x 64k tokens, 128 heads.)
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_remote_relaxed(there(m.weights_credit[group][quarter]));
-        // Weights of this CTA's tokens: under the halves' common maximum in the
-        // first tile, then under the last reference this group knows, or one
-        // whole steps above it.
-        float under;
-        if (i == 0) {
-          ptx::st_async_remote(there(m.peer_top[row]), __float_as_uint(top),
-                               there(m.tops[quarter]));
-          wait.cluster(m.tops[quarter], firsts);
-          under = fmaxf(top, m.peer_top[row]);
-          m.reference[decision & 1][row] = under;
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
-        } else {
-          if (i == 1) {
-            wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
-            known = m.reference[(decision - 1) & 1][row];
-          }
-          under = !(top > known + kLazy)  ? known
-                  : known == -INFINITY    ? ceilf(top)
-                                          : known + ceilf(top - known);
+        // The row's maximum, with the thread of its other tokens; the two
+        // decide alike on the row's reference after this tile.
+        float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
+        float* shared = m.tops[(j >> 1) & 1][group];
+        shared[place_of_row] = top;
+        asm volatile("bar.sync %0, 64;" ::"r"(3 + group * 2 + quarter % 2) : "memory");
+        top = fmaxf(top, shared[place_of_row ^ 64]);
+        float before = -INFINITY;
+        if (i > 0) {
+          wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
+          before = m.reference[(decision - 1) & 1][place_of_row];
         }
-        total *= shift_factor(base, under);
-        base = under;
-        const float sub = under == -INFINITY ? 0.0f : under;
+        const float now = top > before + kLazy ? top : before;
+        m.reference[decision & 1][place_of_row] = now;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
+        total *= shift_factor(base, now);
+        base = now;
+        const float sub = now == -INFINITY ? 0.0f : now;
         uint32_t w[16];
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         const float2 by = make_float2(p.scale_log2, p.scale_log2), less = make_float2(-sub, -sub);
@@ -875,98 +903,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         }
         sum[0] = add2(sum[0], sum[1]);
         total += sum[0].x + sum[0].y;
-        wait.cluster(m.weights_credit[group][quarter], exchanges);
+        if (i >= 2) added(j - 2);  // this group's last weights are read
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          ptx::st_async_remote_v4(sbase + p_row + over + chunk_at(rank, c),
-                                  make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]),
-                                  there(weights_bar));
-        ptx::st_async_remote_v2(there(m.peer[group][row]), __float_as_uint(base),
-                                __float_as_uint(total), there(weights_bar));
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          *reinterpret_cast<uint4*>(smem + p_row + chunk_at(rank, c)) =
+          *reinterpret_cast<uint4*>(weights + (((half * 4 + c) ^ (row & 7)) * 16)) =
               make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-        // The row's reference after this tile: the largest of the one before
-        // and the two halves'.
-        float before = -INFINITY;
-        if (i > 0) {
-          wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
-          before = m.reference[(decision - 1) & 1][row];
-        }
-        wait.cluster(weights_bar, exchanges);
-        const float theirs = m.peer[group][row].x;
-        const float now = fmaxf(before, fmaxf(base, theirs));
-        if (i > 0) m.reference[decision & 1][row] = now;
-        // Seldom anything else: all three references are the same.
-        if (__any_sync(~0u, now != base || now != theirs || (i > 0 && now != before))) {
-          const float f_own = shift_factor(base, now), f_peer = shift_factor(theirs, now);
-#pragma unroll
-          for (uint32_t c = 0; c < 8; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(smem + p_row + chunk_at(0, c));
-            const float f = c / 4 == rank ? f_own : f_peer;
-            const uint4 v = *at;
-            *at = make_uint4(scale_bf16(v.x, f), scale_bf16(v.y, f), scale_bf16(v.z, f),
-                             scale_bf16(v.w, f));
-          }
-          if (i > 0) {
-            // The outputs so far, once the tile before has been added.
-            const float f = shift_factor(before, now);
-            wait(m.pv_done[group ^ 1], (g + i - 1) >> 1);
-            ptx::tc_fence_after();
+        if (i > 0 && __any_sync(~0u, now != before)) {
+          // The outputs so far, once the tile before has been added.
+          const float f = shift_factor(before, now);
+          added(j - 1);
+          ptx::tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < L::kHalf; c += 32) {
-              ptx::tmem_ld_32x32b_x32(lanes + c, own);
-              ptx::tmem_wait_ld();
+          for (int c = 0; c < L::kColumns; c += 32) {
+            ptx::tmem_ld_32x32b_x32(lanes + c, raw);
+            ptx::tmem_wait_ld();
 #pragma unroll
-              for (int q = 0; q < 32; ++q) own[q] = __float_as_uint(__uint_as_float(own[q]) * f);
-              ptx::tmem_st_32x32b_x32(lanes + c, own);
-            }
-            ptx::tmem_wait_st();
-            ptx::tc_fence_before();
+            for (int q = 0; q < 32; ++q) raw[q] = __float_as_uint(__uint_as_float(raw[q]) * f);
+            ptx::tmem_st_32x32b_x32(lanes + c, raw);
           }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
         }
-        known = now;
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          if (i > 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
-          ptx::mbar_arrive(bar(m.p_full[group]));
-        }
+        if (lane == 0) ptx::mbar_arrive_remote(first_cta(m.p_full[group]));
       }
 
-      // The row tile's outputs: the last tile is decided, and added (in this
-      // order: then the barrier of the additions is at most one phase ahead of
-      // a look at its parity).
+      // The row tile's outputs: the last tile is decided, and added.
       const uint32_t last = decisions + tiles - 1;
       decisions += tiles;
-      ++firsts;
       wait(m.decided[last & 1][quarter], last >> 1);
-      wait(m.pv_done[(g + tiles - 1) & 1], (g + tiles - 1) >> 1);
+      const float now = m.reference[last & 1][place_of_row];
+      m.sums[group * 2 + half][row] = total * shift_factor(base, now);
+      asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter % 2) : "memory");
+      total = (m.sums[0][row] + m.sums[1][row]) + (m.sums[2][row] + m.sums[3][row]);
+      all_added(tiles);
       ptx::tc_fence_after();
-      const float now = m.reference[last & 1][row];
-      // The sums, of both groups and both halves, under it.  The groups' pass
-      // through the place of the last tile's weights, which its outputs have read
-      // and the peer has no permit for yet.
-      float* sums = reinterpret_cast<float*>(smem + L::kX + ((g + tiles - 1) & 1) * kExchangeBytes +
-                                             quarter * 4096) +
-                    lane;
-      total *= shift_factor(base, now);
-      if (i0 < tiles) total += m.peer[group][row].y * shift_factor(m.peer[group][row].x, now);
-      sums[group * 32] = i0 < tiles ? total : 0.0f;
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-      total = sums[0] + sums[32];
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory");
-      if (lane == 0 && i0 < tiles) ptx::mbar_arrive_remote_relaxed(there(m.recv_credit[group][quarter]));
       const bool whole = seg.kv0 == 0 && seg.kv1 == seg.kv_tiles;
-      const int column0 = static_cast<int>(rank) * L::kHalf + group * (L::kHalf / 2);
+      const int lane_column = group * (L::kColumns / 2);
+      const int column0 = half * L::kColumns + lane_column;
       const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
-      if (!whole && rank == 0 && group == 0 && mine)
-        ap.stats[seg.slot * kTileRows + row] = make_float2(now, total);
+      if (!whole && half == 0 && group == 0 && mine)
+        ap.stats[seg.slot * kTileRows + tile_row] = make_float2(now, total);
 #pragma unroll 1
-      for (int c = 0; c < L::kHalf / 2; c += 32) {
+      for (int c = 0; c < L::kColumns / 2; c += 32) {
         uint32_t v[32];
-        ptx::tmem_ld_32x32b_x32(lanes + group * (L::kHalf / 2) + c, v);
+        ptx::tmem_ld_32x32b_x32(lanes + lane_column + c, v);
         ptx::tmem_wait_ld();
         if (!mine) continue;
         if (whole) {
@@ -984,7 +966,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           float4* part = ap.partial +
                          (static_cast<size_t>(seg.slot) * (kLatent / 4) + (column0 + c) / 4) *
                              kTileRows +
-                         row;
+                         tile_row;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             part[i * kTileRows] =
@@ -1004,7 +986,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   ptx::cluster_sync();  // no CTA leaves while its peer may address it
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    ptx::tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -1126,8 +1108,8 @@ constexpr int kMaxClusters = 80;
 template <int kLatent>
 constexpr uint32_t smem_bytes() {
   static_assert(MXFP8_MAX_LATENT_ROWS <= 65535, "row numbers fit 16 bits");
-  static_assert(Shape<kLatent>::kMisc + sizeof(Misc) <= 232448, "shared memory of a CTA");
-  return Shape<kLatent>::kMisc + sizeof(Misc);
+  static_assert(Shape<kLatent>::kMisc + sizeof(Misc<Shape<kLatent>::kStages>) <= 232448, "shared memory of a CTA");
+  return Shape<kLatent>::kMisc + sizeof(Misc<Shape<kLatent>::kStages>);
 }
 
 // Clusters that run at once on the current device, asked once.
@@ -1164,36 +1146,33 @@ cudaError_t resident_clusters(int* out) {
   return cudaSuccess;
 }
 
-CUresult encode_cache(CUtensorMap* map, const LatentParams& p, int first, int columns, int box,
-                      int box_columns, CUtensorMapSwizzle swizzle) {
+// The cache as [page][block of 64 columns][token][64].
+CUresult encode_cache(CUtensorMap* map, const LatentParams& p, int latent, int box, int blocks) {
   const EncodeTiled fn = encode_tiled();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
   const cuuint64_t page =
       p.pages > 1 ? p.page_stride : static_cast<int64_t>(p.page_size) * p.token_stride;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(p.page_size),
-                        static_cast<cuuint64_t>(p.pages)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.token_stride) * 2, page * 2};
-  cuuint32_t boxes[3] = {static_cast<cuuint32_t>(box_columns), static_cast<cuuint32_t>(box), 1};
-  cuuint32_t elem[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(p.cache + first), dims,
-            strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+  cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(p.page_size),
+                        static_cast<cuuint64_t>(latent / 64 + 1), static_cast<cuuint64_t>(p.pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.token_stride) * 2, 128, page * 2};
+  cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(blocks), 1};
+  cuuint32_t elem[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(p.cache), dims,
+            strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 // q [rows x heads][latent + 64].
-CUresult encode_queries(CUtensorMap* map, const LatentParams& p, int latent, int first,
-                        int columns, int box_columns, int box_rows,
-                        CUtensorMapSwizzle swizzle) {
+CUresult encode_queries(CUtensorMap* map, const LatentParams& p, int latent) {
   const EncodeTiled fn = encode_tiled();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(columns),
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(latent + kRope),
                         static_cast<cuuint64_t>(p.rows) * p.heads};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(latent + kRope) * 2};
-  cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box_columns),
-                         static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t boxes[2] = {64, kCtaRows};
   cuuint32_t elem[2] = {1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.q + first), dims,
-            strides, boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.q), dims, strides,
+            boxes, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
@@ -1203,7 +1182,7 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
   ap.in = p;
   cudaError_t e = resident_clusters<kLatent>(&ap.clusters);
   if (e != cudaSuccess) return e;
-  ap.box = kTokens;
+  ap.box = kCtaTokens;
   while (p.page_size % ap.box) ap.box /= 2;
   ap.partial = static_cast<float4*>(workspace);
   ap.stats = reinterpret_cast<float2*>(ap.partial + static_cast<size_t>(2) * kMaxClusters *
@@ -1211,11 +1190,11 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
   ap.piece = reinterpret_cast<int32_t*>(ap.stats + static_cast<size_t>(2) * kMaxClusters *
                                                        kTileRows);
   AttendMaps maps;
-  constexpr CUtensorMapSwizzle k128 = CU_TENSOR_MAP_SWIZZLE_128B, k64 = CU_TENSOR_MAP_SWIZZLE_64B;
-  if (encode_cache(&maps.latent, p, 0, kLatent, ap.box, 64, k128) != CUDA_SUCCESS ||
-      encode_cache(&maps.rope, p, kLatent, kRope, ap.box, 32, k64) != CUDA_SUCCESS ||
-      encode_queries(&maps.q, p, kLatent, 0, kLatent, 64, kTileRows, k128) != CUDA_SUCCESS ||
-      encode_queries(&maps.q_rope, p, kLatent, kLatent, kRope, 32, kTileRows / 2, k64) != CUDA_SUCCESS)
+  using L = Shape<kLatent>;
+  const bool whole = ap.box == kCtaTokens;
+  if (encode_cache(&maps.keys, p, kLatent, ap.box, whole ? L::kBlocks + 1 : 1) != CUDA_SUCCESS ||
+      encode_cache(&maps.values, p, kLatent, ap.box, whole ? L::kHalf : 1) != CUDA_SUCCESS ||
+      encode_queries(&maps.q, p, kLatent) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
 
   cudaLaunchAttribute attr;
