@@ -37,9 +37,9 @@
 // Warps of a CTA:
 //   0, 3   producers: TMA boxes into a ring, a lane a box: a row tile's queries
 //          in two places of it, then its token tiles; a warp every other place;
-//   1      issuer of the pair's products (in the first CTA);
+//   1, 14  issuers, in the first CTA, of the pair's products: scores, outputs;
 //   2, 13  menders, of keys and of values: they pass every tile on to the
-//          issuer, after a look at the ones that reach the drafts or the length;
+//          issuers, after a look at the ones that reach the drafts or the length;
 //   4-11   softmax, two groups of four that take the token tiles in turn;
 //   12     fetches the values of the peer's tokens, and what the shared memory
 //          holds of the queries.
@@ -65,10 +65,11 @@ constexpr int kCtaTokens = 32;  // of them, those a CTA brings as keys
 constexpr int kTileRows = 128;  // rows in a tile
 constexpr int kCtaRows = 64;
 constexpr int kMinBox = 8;      // tokens of a TMA box at least: pages are multiples of 8
-constexpr int kAttendThreads = 448;
+constexpr int kAttendThreads = 480;
 constexpr int kSoftmaxWarp = 4;
 constexpr int kFetchWarp = 12;
 constexpr int kValueMender = 13;
+constexpr int kOutputWarp = 14;
 constexpr int kMaxRequests = MXFP8_MAX_REQUESTS;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
 // A new maximum moves the reference of a row's exponentials only when it
@@ -118,7 +119,7 @@ struct Misc {
   uint64_t qk_done[kStages], v_full[kStages];    // 1; [token tile mod kStages]
   uint64_t s_full[2], pv_done[2];                // 1; [tile parity]
   uint64_t decided[2][4];                        // 1; [tile parity][lane quarter]
-  uint64_t q_full, drained;                      // 1
+  uint64_t q_full, drained[2];                   // 1
   uint64_t k_ready[kStages], v_ready[kStages];   // 2: the CTAs' menders
   uint64_t s_free[2], p_full[2];                 // 8: a group's warps in both CTAs
   uint64_t q_ready;                              // 16: all softmax warps of both
@@ -271,39 +272,20 @@ struct Waiter {
   __device__ __forceinline__ bool operator()(const uint64_t& b, uint32_t parity) const {
     const uint32_t bar = ptx::smem_addr(&b);
     bool done = ptx::mbar_try_wait(bar, parity & 1u);
-    if (!done) done = slow(bar, parity & 1u, false);
+    if (!done) done = slow(bar, parity & 1u);
     __syncwarp();
     return done;
   }
-  // With acquire over the cluster, for what a peer CTA signals.
-  __device__ __forceinline__ bool cluster(const uint64_t& b, uint32_t parity) const {
-    const uint32_t bar = ptx::smem_addr(&b);
-    bool done = ptx::mbar_try_wait_cluster(bar, parity & 1u);
-    if (!done) done = slow(bar, parity & 1u, true);
-    __syncwarp();
-    return done;
-  }
-  // Whether it is over already.
-  __device__ __forceinline__ bool ready(const uint64_t& b, uint32_t parity) const {
-    return __all_sync(~0u, ptx::mbar_test_wait(ptx::smem_addr(&b), parity & 1u));
-  }
-  // For a loop over ready(): whether it may go on after `spins` empty rounds
-  // since `start` (set at the first).
-  __device__ __noinline__ bool patient(int spins, uint64_t& start) const {
-    const uint64_t now = ptx::globaltimer();
-    if (spins == 0) start = now;
-    if (*reinterpret_cast<volatile int32_t*>(abort) != 0) return false;
-    if (now - start <= kWaitLimitNs) return true;
-    *reinterpret_cast<volatile int32_t*>(abort) = 1;
-    raise(flags, MXFP8_FLAG_GEMM_TIMEOUT);
-    return false;
-  }
-  __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity, bool wide) const {
-    uint64_t start = 0;
+  __device__ __noinline__ bool slow(uint32_t bar, uint32_t parity) const {
+    const uint64_t start = ptx::globaltimer();
     for (int i = 0;; ++i) {
-      if (wide ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity))
-        return true;
-      if (i % 16 == 0 && !patient(i, start)) return false;
+      if (ptx::mbar_try_wait(bar, parity)) return true;
+      if (i % 16 != 0) continue;
+      if (*reinterpret_cast<volatile int32_t*>(abort) != 0) return false;
+      if (ptx::globaltimer() - start <= kWaitLimitNs) continue;
+      *reinterpret_cast<volatile int32_t*>(abort) = 1;
+      raise(flags, MXFP8_FLAG_GEMM_TIMEOUT);
+      return false;
     }
   }
 };
@@ -581,65 +563,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                        kWaitLimitNs / 16);
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------------- issuer
-    // The warp stays converged and one elected lane issues (from a branch on
+    // --------------------------------------------------------- scores' issuer
+    // Both issuers stay converged and one elected lane issues (from a branch on
     // the lane number a product took half as long again).  A pair's 128 x 64 x
     // 16 product takes 18 clocks with the queries in tensor memory, 25 with
     // them in shared memory; 128 x 256 x 16 takes 64, the tensor cores' rate.
+    // One warp for both products left the tensor cores idle while it looked
+    // for the next that was ready: 0.2 us a look.
     constexpr uint32_t kScores = ptx::idesc_bf16(kTokens, false);
-    constexpr uint32_t kOutputs = ptx::idesc_bf16(256, true);
-    int g = 0;  // token tiles before the segment
-    int r = 0;  // places of the ring before its first token tile
+    int j = 0;  // token tiles
+    int r = 0;  // places of the ring
     uint32_t segments = 0;
     bool ok = rank == 0;
-    auto scores = [&](int i) {
-      const int j = g + i;
-      ptx::tc_fence_after();
-      const uint32_t keys = sbase + (r + i) % kStages * L::kPlaceBytes;
-      const uint32_t d = tmem + L::kS + (j & 1) * kCtaTokens;
-      const uint32_t done = bar(m.s_full[j & 1]), fetch = bar(m.qk_done[j % kStages]);
-      if (ptx::elect_one()) {
-#pragma unroll
-        for (int k = 0; k < L::kTmemBlocks * 4; ++k)
-          ptx::mma_f16_ts_pair(d, tmem + L::kQ + k * 8,
-                               ptx::desc_kmajor_sw128(keys + (k / 4) * kBlockBytes + (k % 4) * 32),
-                               kScores, k > 0);
-#pragma unroll
-        for (int k = 0; k < L::kSmemBlocks * 4; ++k)
-          ptx::mma_f16_ss_pair(d,
-                               ptx::desc_kmajor_sw128(sbase + L::kQSmem + (k / 4) * kQBlockBytes +
-                                                      (k % 4) * 32),
-                               ptx::desc_kmajor_sw128(keys + (L::kTmemBlocks + k / 4) * kBlockBytes +
-                                                      (k % 4) * 32),
-                               kScores, 1u);
-        ptx::mma_commit_pair(fetch);
-        ptx::mma_commit_pair(done);
-      }
-      __syncwarp();
-    };
-    auto outputs = [&](int i) {
-      const int j = g + i, stage = (r + i) % kStages;
-      ptx::tc_fence_after();
-      const uint32_t values = sbase + stage * L::kPlaceBytes;
-      const uint32_t weights = sbase + L::kP + (j & 1) * kWeightBytes;
-      const uint32_t add = i > 0;
-      const uint32_t empty = bar(m.kv_empty[stage]), done = bar(m.pv_done[j & 1]);
-      if (ptx::elect_one()) {
-#pragma unroll
-        for (int k = 0; k < kTokens / 16; ++k)
-#pragma unroll
-          for (int c = 0; c < L::kColumns / 128; ++c)  // 128 of each CTA's columns
-            ptx::mma_f16_ss_pair(
-                tmem + c * 128, ptx::desc_kmajor_sw128(weights + k * 32),
-                ptx::desc_mnmajor_sw128(values + (k / 2 * L::kHalf + 2 * c) * kBlockBytes +
-                                            (k % 2) * 2048,
-                                        kBlockBytes),
-                kOutputs, k > 0 ? 1u : add);
-        ptx::mma_commit_pair(empty);
-        ptx::mma_commit_pair(done);
-      }
-      __syncwarp();
-    };
     while (ok && next_segment(m, p, cluster, walk, seg)) {
       ok = __all_sync(~0u, wait(m.q_ready, segments++));
       // Every softmax warp has read the queries.
@@ -648,34 +583,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             ptx::map_to_rank(bar(m.kv_empty[(r + lane / 2) % kStages]), lane % 2));
       __syncwarp();
       r += 2;
-      const int tiles = seg.kv1 - seg.kv0;
-      // Whichever is ready: the scores of tile s (its tokens there, and the
-      // scores of tile s - 2 read out of their buffer) or the outputs of tile o
-      // (its weights and values there).  Neither waits behind the other, so a
-      // late tile does not keep an earlier one's place in the ring.
-      int s = 0, o = 0, spins = 0;
-      uint64_t start = 0;
-      while (ok && o < tiles) {
-        if (s < tiles && s <= o + 2 &&
-            wait.ready(m.k_ready[(g + s) % kStages], (g + s) / kStages) &&
-            (s < 2 || wait.ready(m.s_free[(g + s) & 1], (g + s - 2) >> 1))) {
-          scores(s++);
-          spins = 0;
-        } else if (o < s && wait.ready(m.p_full[(g + o) & 1], (g + o) >> 1) &&
-                   wait.ready(m.v_ready[(g + o) % kStages], (g + o) / kStages)) {
-          outputs(o++);
-          spins = 0;
-        } else if (spins++ % 64 == 0) {
-          ok = __all_sync(~0u, wait.patient(spins - 1, start));
+      for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++r, ++j) {
+        // The tile's tokens are there, and the scores of the one before the
+        // last are read out of their buffer.
+        ok = wait(m.k_ready[j % kStages], j / kStages);
+        if (kv >= seg.kv0 + 2) ok = wait(m.s_free[j & 1], (j - 2) >> 1) && ok;
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t keys = sbase + r % kStages * L::kPlaceBytes;
+        const uint32_t d = tmem + L::kS + (j & 1) * kCtaTokens;
+        const uint32_t done = bar(m.s_full[j & 1]), fetch = bar(m.qk_done[j % kStages]);
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < L::kTmemBlocks * 4; ++k)
+            ptx::mma_f16_ts_pair(
+                d, tmem + L::kQ + k * 8,
+                ptx::desc_kmajor_sw128(keys + (k / 4) * kBlockBytes + (k % 4) * 32), kScores, k > 0);
+#pragma unroll
+          for (int k = 0; k < L::kSmemBlocks * 4; ++k)
+            ptx::mma_f16_ss_pair(
+                d,
+                ptx::desc_kmajor_sw128(sbase + L::kQSmem + (k / 4) * kQBlockBytes + (k % 4) * 32),
+                ptx::desc_kmajor_sw128(keys + (L::kTmemBlocks + k / 4) * kBlockBytes +
+                                       (k % 4) * 32),
+                kScores, 1u);
+          ptx::mma_commit_pair(fetch);
+          ptx::mma_commit_pair(done);
         }
+        __syncwarp();
       }
-      g += tiles;
-      r += tiles;
     }
     if (rank == 0) {  // nothing runs on when tensor memory is freed
-      if (ptx::elect_one()) ptx::mma_commit_pair(bar(m.drained));
+      if (ptx::elect_one()) ptx::mma_commit_pair(bar(m.drained[0]));
       __syncwarp();
-      ptx::mbar_wait(bar(m.drained), 0, kWaitLimitNs);
+      ptx::mbar_wait(bar(m.drained[0]), 0, kWaitLimitNs);
+    }
+  } else if (warp == kOutputWarp) {
+    // -------------------------------------------------------- outputs' issuer
+    constexpr uint32_t kOutputs = ptx::idesc_bf16(256, true);
+    int j = 0, r = 0;
+    bool ok = rank == 0;
+    while (ok && next_segment(m, p, cluster, walk, seg)) {
+      r += 2;
+      for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++r, ++j) {
+        ok = wait(m.v_ready[j % kStages], j / kStages);
+        ok = wait(m.p_full[j & 1], j >> 1) && ok;
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const int stage = r % kStages;
+        const uint32_t values = sbase + stage * L::kPlaceBytes;
+        const uint32_t weights = sbase + L::kP + (j & 1) * kWeightBytes;
+        const uint32_t add = kv > seg.kv0;
+        const uint32_t empty = bar(m.kv_empty[stage]), done = bar(m.pv_done[j & 1]);
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < kTokens / 16; ++k)
+#pragma unroll
+            for (int c = 0; c < L::kColumns / 128; ++c)  // 128 of each CTA's columns
+              ptx::mma_f16_ss_pair(
+                  tmem + c * 128, ptx::desc_kmajor_sw128(weights + k * 32),
+                  ptx::desc_mnmajor_sw128(values + (k / 2 * L::kHalf + 2 * c) * kBlockBytes +
+                                              (k % 2) * 2048,
+                                          kBlockBytes),
+                  kOutputs, k > 0 ? 1u : add);
+          ptx::mma_commit_pair(empty);
+          ptx::mma_commit_pair(done);
+        }
+        __syncwarp();
+      }
+    }
+    if (rank == 0) {
+      if (ptx::elect_one()) ptx::mma_commit_pair(bar(m.drained[1]));
+      __syncwarp();
+      ptx::mbar_wait(bar(m.drained[1]), 0, kWaitLimitNs);
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------- keys' mender
