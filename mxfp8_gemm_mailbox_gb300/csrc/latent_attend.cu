@@ -79,7 +79,8 @@ constexpr float kLazy = 8.0f;
 // Pieces of one row tile a cluster may be this many token tiles longer than an
 // even deal's runs: about what a second row tile in a run costs.
 constexpr int kPieceSlack = 5;
-constexpr int kMinRun = 2;
+constexpr int kMinRun = 4;
+constexpr int kMaxClusters = 80;  // whose partials the workspace holds
 constexpr uint32_t kBlockBytes = kCtaTokens * 128;  // 32 tokens x 64 columns
 constexpr uint32_t kQBlockBytes = kCtaRows * 128;   // 64 rows x 64 columns
 constexpr uint32_t kWeightBytes = kCtaRows * kTokens * 2;
@@ -225,7 +226,14 @@ template <class Misc>
 __device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& p, int cluster,
                                              Walk& w, Segment& s) {
   if (w.at >= w.end) return false;
-  while (w.at >= m.first[w.b + 1]) ++w.b;
+  // The request of run `at`: a lane looks at one of 32.
+  for (;; w.b += 32) {
+    const int b = w.b + threadIdx.x % 32;
+    const uint32_t past = __ballot_sync(~0u, b < p.requests && m.first[b + 1] <= w.at);
+    if (past == ~0u) continue;
+    w.b += __popc(past);
+    break;
+  }
   s.b = w.b;
   s.length = m.length[w.b];
   s.begin = m.begin[w.b];
@@ -262,9 +270,15 @@ __device__ __forceinline__ bool special(const Segment& s, int kv) {
   return (kv + 1) * kTokens > s.context;
 }
 
-// Bounded waits of a warp's lanes, which come out together.  One that runs out sets `abort`,
-// after which every wait of the CTA returns at once and the kernel ends with
-// its flag set.  (The softmax warps then run their loops out on whatever the
+// Tokens that one row tile alone reads leave L2 first (8 x 64k tokens: 126 us,
+// 132 when they are kept or treated as any other); those of several stay.
+__device__ __forceinline__ uint64_t cache_policy(const LatentParams& p, const Segment& s) {
+  return s.drafts * p.heads > kTileRows ? ptx::policy_evict_last() : ptx::policy_evict_first();
+}
+
+// Bounded waits of a warp's lanes, which come out together.  One that runs out
+// sets `abort`, after which every wait of the CTA returns at once and the
+// kernel ends with its flag set.  (The softmax warps then run their loops out on whatever the
 // buffers hold, so that none is missing at their barriers.)
 struct Waiter {
   int32_t* abort;
@@ -290,13 +304,19 @@ struct Waiter {
   }
 };
 
+// A row tile that begins in a cluster's share and ends in another's: its slot
+// there, the last cluster (whose slot is its first, as are those between), its
+// first row of all (rows x heads) and how many; 0 rows: none.
+struct Cut {
+  int32_t slot, last, row0, rows;
+};
 struct AttendParams {
   LatentParams in;
   int32_t clusters;
   int32_t box;        // tokens of a TMA box: the largest of 32, 16, 8 in a page
   float4* partial;    // [2 clusters][latent / 4][128 rows] x 4 columns
   float2* stats;      // [2 clusters][128 rows] (reference, sum)
-  int32_t* piece;     // the deal: token tiles of a piece, 0 for equal runs
+  Cut* cuts;          // [clusters]
 };
 struct AttendMaps {
   // Boxes of 64 columns by `box` tokens (64 rows), by as many blocks of columns
@@ -309,64 +329,103 @@ __device__ __forceinline__ uint32_t run_length(uint32_t tiles, int clusters) {
   return max(static_cast<uint32_t>(kMinRun), (tiles + clusters - 1) / clusters);
 }
 
-// The deal, by one warp: fills Misc's lists.  (The host has checked that all
-// token tiles number less than 2^31.)
+// The deal's terms: all token tiles, and the token tiles of a piece (0 for an
+// even deal in runs), by a warp whose lane asks `at(b)` for request b's row
+// tiles and token tiles.  (The host has checked that all token tiles number
+// less than 2^31.)
+struct Terms {
+  uint32_t all;
+  int piece;
+};
+template <class At>
+__device__ __forceinline__ Terms terms_of(int requests, int clusters, int lane, At at) {
+  uint32_t all = 0;
+  int tiles_of_rows = 0;
+  for (int b = lane; b < requests + lane; b += 32) {
+    const int2 t = b < requests ? at(b) : make_int2(0, 0);
+    all += __reduce_add_sync(~0u, static_cast<uint32_t>(t.x) * t.y);
+    tiles_of_rows += __reduce_add_sync(~0u, t.x);
+  }
+  if (tiles_of_rows > clusters) return {all, 0};
+  // Pieces: the shortest length, from that of the even deal on, at which all
+  // pieces fit the clusters, one a cluster.
+  const uint32_t run = run_length(all, clusters);
+  uint32_t pieces[kPieceSlack + 1] = {};
+  for (int b = lane; b < requests; b += 32) {
+    const int2 t = at(b);
+#pragma unroll
+    for (int k = 0; k <= kPieceSlack; ++k) pieces[k] += t.x * ((t.y + run + k - 1) / (run + k));
+  }
+  int piece = 0;
+#pragma unroll
+  for (int k = kPieceSlack; k >= 0; --k)
+    if (__reduce_add_sync(~0u, pieces[k]) <= static_cast<uint32_t>(clusters)) piece = run + k;
+  return {all, piece};
+}
+
+// The deal, by one warp: fills Misc's lists.
 template <class Misc>
 __device__ __forceinline__ void deal(Misc& m, const AttendParams& ap, int lane) {
   const LatentParams& p = ap.in;
+  auto load = [&](int b) {
+    const Request r = load_request(p, b);
+    if (r.cut && blockIdx.x == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
+    m.length[b] = r.length;
+    m.begin[b] = static_cast<uint16_t>(r.begin);
+    if (b == p.requests - 1) m.begin[b + 1] = static_cast<uint16_t>(r.begin + r.drafts);
+    return make_int2(r.length > 0 ? row_tiles(r.drafts, p.heads) : 0, token_tiles(r.length));
+  };
+  // The first 32 requests stay in registers.
+  const int2 mine = lane < p.requests ? load(lane) : make_int2(0, 0);
+  for (int b = lane + 32; b < p.requests; b += 32) load(b);
+  __syncwarp();
+  auto at = [&](int b) {
+    if (b < 32) return mine;
+    const int n = m.length[b];
+    return make_int2(n > 0 ? row_tiles(drafts_of(m, b), p.heads) : 0, token_tiles(n));
+  };
+  const Terms terms = terms_of(p.requests, ap.clusters, lane, at);
+  const int piece = terms.piece;
   uint32_t before = 0;
-  int tiles_of_rows = 0;
-  auto list = [&](int b, uint32_t runs) {  // sums of `runs` over the requests up to b
+  for (int b = lane; b < p.requests + lane; b += 32) {
+    const int2 t = b < p.requests ? at(b) : make_int2(0, 0);
+    uint32_t runs = t.x * (piece > 0 ? static_cast<uint32_t>(t.y + piece - 1) / piece : t.y);
     for (int o = 1; o < 32; o *= 2) {
       const uint32_t v = __shfl_up_sync(~0u, runs, o);
       if (lane >= o) runs += v;
     }
     if (b < p.requests) m.first[b + 1] = before + runs;
     before += __shfl_sync(~0u, runs, 31);
-  };
-  for (int base = 0; base < p.requests; base += 32) {
-    const int b = base + lane;
-    uint32_t tiles = 0;
-    int rt = 0;
-    if (b < p.requests) {
-      const Request r = load_request(p, b);
-      if (r.cut && blockIdx.x == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
-      m.length[b] = r.length;
-      m.begin[b] = static_cast<uint16_t>(r.begin);
-      if (b == p.requests - 1) m.begin[b + 1] = static_cast<uint16_t>(r.begin + r.drafts);
-      rt = r.length > 0 ? row_tiles(r.drafts, p.heads) : 0;
-      tiles = static_cast<uint32_t>(rt) * token_tiles(r.length);
-    }
-    tiles_of_rows += __reduce_add_sync(~0u, rt);
-    list(b, tiles);
-  }
-  // Pieces: the shortest length, from that of the even deal on, at which all
-  // pieces fit the clusters, one a cluster; a lane a length.
-  const int run = static_cast<int>(run_length(before, ap.clusters));
-  int piece = 0;
-  __syncwarp();
-  if (tiles_of_rows <= ap.clusters) {
-    int pieces = 0;
-    if (lane <= kPieceSlack)
-      for (int b = 0; b < p.requests; ++b)
-        pieces += row_tiles(drafts_of(m, b), p.heads) *
-                  ((token_tiles(m.length[b]) + run + lane - 1) / (run + lane));
-    const uint32_t fits = __ballot_sync(~0u, lane <= kPieceSlack && pieces <= ap.clusters);
-    if (fits != 0u) piece = run + __ffs(fits) - 1;
-  }
-  if (piece > 0) {
-    before = 0;
-    for (int base = 0; base < p.requests; base += 32) {
-      const int b = base + lane;
-      list(b, b < p.requests ? row_tiles(drafts_of(m, b), p.heads) *
-                                   ((token_tiles(m.length[b]) + piece - 1) / piece)
-                             : 0);
-    }
   }
   if (lane == 0) {
     m.first[0] = 0;
     m.piece = piece;
-    if (blockIdx.x == 0) *ap.piece = piece;
+  }
+}
+
+// Zeros for the rows before the first request, past the last and of requests
+// without tokens; a warp of every cluster, in turn.
+template <class Misc>
+__device__ __forceinline__ void zero_rows(const Misc& m, const LatentParams& p, int lane,
+                                          int latent) {
+  auto zero = [&](int from, int to) {
+    const int row_bytes = p.heads * latent * 2;  // a multiple of 512
+    for (int t = from + blockIdx.x / 2; t < to; t += gridDim.x / 2) {
+      uint4* row = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) +
+                                            static_cast<size_t>(t) * row_bytes);
+      for (int i = lane; i < row_bytes / 16; i += 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  zero(0, p.requests > 0 ? m.begin[0] : 0);
+  zero(p.requests > 0 ? m.begin[p.requests] : 0, p.rows);
+  for (int base = 0; base < p.requests; base += 32) {
+    const int b = base + lane;
+    uint32_t empty =
+        __ballot_sync(~0u, b < p.requests && m.length[b] == 0 && drafts_of(m, b) > 0);
+    for (; empty != 0u; empty &= empty - 1u) {
+      const int e = base + __ffs(empty) - 1;
+      zero(m.begin[e], m.begin[e + 1]);
+    }
   }
 }
 
@@ -412,8 +471,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = m.tmem;
   ptx::grid_dependency_wait();
-  // Past the wait: the join may read this kernel's inputs at once.
-  if (tid == 0) ptx::launch_dependents();
   if (warp == 0) deal(m, ap, lane);
   __syncthreads();
 
@@ -437,7 +494,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     // warp's tiles ahead.
     const int which = warp == 3;
     constexpr int kItems = (kCtaTokens / kMinBox * (L::kBlocks + 1) + 31) / 32;  // of a lane
-    const uint64_t keep = ptx::policy_evict_last();
     const int blocks = ap.box == kCtaTokens ? 1 : L::kBlocks + 1;  // copies of a box
     const int items = kCtaTokens / ap.box * blocks;
     // The first token of copy i of this CTA's part of tile kv.
@@ -457,6 +513,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       return ok;
     };
     while (ok && next_segment(m, p, cluster, walk, seg)) {
+      const uint64_t keep = cache_policy(p, seg);
       uint32_t full;
       // The queries that go to tensor memory, half of their blocks a place.
       for (int half = 0; half < 2; ++half, ++r) {
@@ -511,7 +568,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     // ----------------------------------------------------------------- fetch
     // This CTA's value columns of the peer's tokens, over the blocks of its own
     // tokens that only the keys' product reads.
-    const uint64_t keep = ptx::policy_evict_last();
     const int blocks = ap.box == kCtaTokens ? 1 : L::kHalf;  // copies of a box
     const int items = kCtaTokens / ap.box * blocks;          // at most 16
     const int column0 = static_cast<int>(rank) * L::kHalf, theirs = static_cast<int>(rank ^ 1u);
@@ -536,6 +592,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                          ptx::policy_evict_first());
       __syncwarp();
       r += 2;
+      const uint64_t keep = cache_policy(p, seg);
       int page = page_of(seg.kv0);
       for (int kv = seg.kv0; kv < seg.kv1; ++kv, ++r, ++j) {
         const int next = page_of(kv + 1);
@@ -621,6 +678,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     }
   } else if (warp == kOutputWarp) {
     // -------------------------------------------------------- outputs' issuer
+    if (rank == 1) {  // nothing to issue
+      zero_rows(m, p, lane, kLatent);
+      // For the join.
+      Cut cut{0, 0, 0, 0};
+      Walk ahead = walk;
+      for (;;) {
+        const uint32_t at = ahead.at;
+        if (!next_segment(m, p, cluster, ahead, seg)) break;
+        if (seg.kv0 != 0 || seg.kv1 == seg.kv_tiles) continue;
+        const uint32_t runs =
+            m.piece > 0 ? (seg.kv_tiles + m.piece - 1) / m.piece : seg.kv_tiles;
+        cut = Cut{seg.slot, static_cast<int>((at + runs - 1) / run),
+                  seg.begin * p.heads + seg.row0, seg.valid};
+      }
+      if (lane == 0) ap.cuts[cluster] = cut;
+    }
     constexpr uint32_t kOutputs = ptx::idesc_bf16(256, true);
     int j = 0, r = 0;
     bool ok = rank == 0;
@@ -692,6 +765,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         ++j;
       }
     }
+    // The join may come: it reads this kernel's inputs, which are past the wait.
+    // (With the first tiles it would take issue slots from them.)
+    ptx::launch_dependents();
   } else if (warp == kValueMender) {
     // -------------------------------------------------------- values' mender
     // Zeros for the tokens past the length and for drafts that are not finite:
@@ -973,119 +1049,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
 }
 
 // Joins the partial outputs of the row tiles that several clusters shared, in
-// the order of their tokens, and writes the zeros of rows without tokens.
-// Block (tile, 8 columns): thread = row x 4 columns.
+// the order of their tokens.  An item is a row tile's 8 columns, a thread a row
+// by 4 of them.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinColumns = kJoinThreads / kTileRows * 4;
 template <int kLatent>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ AttendParams ap) {
+__global__ void __launch_bounds__(kJoinThreads, 4)
+    join_kernel(const __grid_constant__ AttendParams ap) {
   ptx::launch_dependents();
   const LatentParams& p = ap.in;
   const int row = threadIdx.x % kTileRows;
-  const int column = blockIdx.y * 8 + (threadIdx.x / kTileRows) * 4;
-  const int lane = threadIdx.x % 32;
-  Request mine{p.rows, 0, 0, false};  // the first 32 requests, a lane each
-  if (lane < p.requests) mine = load_request(p, lane);
+  constexpr int kItems = kLatent / kJoinColumns;  // of a row tile
   ptx::grid_dependency_wait();
-  const int piece = *ap.piece;
-  // Where this block's row tile stands in the list of runs; a lane a request.
-  uint32_t all = 0, begin = 0, end = 0;
-  int tiles = 0, covered0 = p.rows, covered1 = p.rows, row0 = 0, valid = 0;
-  for (int base = 0; base < p.requests; base += 32) {
-    Request r = mine;
-    if (base > 0) {
-      r = Request{p.rows, 0, 0, false};
-      if (base + lane < p.requests) r = load_request(p, base + lane);
-    }
-    const int rt = row_tiles(r.drafts, p.heads);
-    // Runs that a row tile of the request makes up.
-    int kt = token_tiles(r.length);
-    if (piece > 0) kt = (kt + piece - 1) / piece;
-    int tiles_to = rt;
-    uint32_t runs_to = static_cast<uint32_t>(rt) * kt;
-    for (int o = 1; o < 32; o *= 2) {
-      const int t = __shfl_up_sync(~0u, tiles_to, o);
-      const uint32_t n = __shfl_up_sync(~0u, runs_to, o);
-      if (lane >= o) tiles_to += t, runs_to += n;
-    }
-    const int tile = static_cast<int>(blockIdx.x) - (tiles + tiles_to - rt);
-    const uint32_t has = __ballot_sync(~0u, tile >= 0 && tile < rt);
-    if (has != 0u) {
-      const int from = __ffs(has) - 1;
-      const uint32_t at = all + runs_to - static_cast<uint32_t>(rt) * kt +
-                          static_cast<uint32_t>(tile) * kt;
-      begin = __shfl_sync(~0u, at, from);
-      end = begin + __shfl_sync(~0u, kt, from);
-      row0 = __shfl_sync(~0u, r.begin * p.heads + tile * kTileRows, from);
-      valid = __shfl_sync(~0u, r.drafts * p.heads - tile * kTileRows, from);
-    }
-    if (base == 0) covered0 = __shfl_sync(~0u, r.begin, 0);
-    if (base + 32 >= p.requests)
-      covered1 = __shfl_sync(~0u, r.begin + r.drafts, p.requests - 1 - base);
-    tiles += __shfl_sync(~0u, tiles_to, 31);
-    all += __shfl_sync(~0u, runs_to, 31);
-  }
-  const size_t out_row = static_cast<size_t>(row0) + row;
-  auto write = [&](size_t at, float4 v) {
-    *reinterpret_cast<uint2*>(p.out + at * kLatent + column) =
-        make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-  };
-  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (blockIdx.x == gridDim.x - 1) {  // rows before the first request or past the last
-    const size_t lo = static_cast<size_t>(covered0) * p.heads;
-    const size_t hi = static_cast<size_t>(covered1) * p.heads;
-    const size_t n = static_cast<size_t>(p.rows) * p.heads;
-    for (size_t at = row; at < lo; at += kTileRows) write(at, zero);
-    for (size_t at = hi + row; at < n; at += kTileRows) write(at, zero);
-    return;
-  }
-  if (row >= valid) return;
-  if (begin == end) {
-    write(out_row, zero);
-    return;
-  }
-  // The clusters that shared the row tile: its pieces', or those whose runs
-  // meet it.
-  const uint32_t run = piece > 0 ? 1 : run_length(all, ap.clusters);
-  const uint32_t c0 = begin / run, c1 = (end - 1) / run;
-  if (c0 == c1) return;  // one cluster wrote the whole
-  auto slot_of = [&](uint32_t c) { return 2 * c + (c * run < begin ? 1 : 0); };
-  // Eight clusters' loads at a time, under the largest reference so far.
-  constexpr uint32_t kBatch = 8;
-  float top = -INFINITY, total = 0.0f;
-  float4 sum = zero;
-  for (uint32_t c = c0; c <= c1; c += kBatch) {
-    float2 st[kBatch];
-    float4 v[kBatch];
+  // The cut row tiles, at most one a cluster, a lane each of 32 clusters.
+  constexpr int kWords = (kMaxClusters + 31) / 32;
+  Cut mine[kWords];
+  uint32_t there[kWords];
+  int cuts = 0;
 #pragma unroll
-    for (uint32_t k = 0; k < kBatch; ++k) {
-      st[k] = make_float2(-INFINITY, 0.0f);
-      v[k] = zero;
-      if (c + k > c1) continue;
-      const uint32_t slot = slot_of(c + k);
-      st[k] = ap.stats[slot * kTileRows + row];
-      v[k] = ap.partial[(static_cast<size_t>(slot) * (kLatent / 4) + column / 4) * kTileRows + row];
-    }
-    float next = top;
-#pragma unroll
-    for (uint32_t k = 0; k < kBatch; ++k) next = fmaxf(next, st[k].x);
-    const float keep = shift_factor(top, next);
-    top = next;
-    total *= keep;
-    sum = make_float4(sum.x * keep, sum.y * keep, sum.z * keep, sum.w * keep);
-#pragma unroll
-    for (uint32_t k = 0; k < kBatch; ++k) {
-      const float f = shift_factor(st[k].x, top);
-      total = fmaf(f, st[k].y, total);
-      sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
-      sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
-    }
+  for (int w = 0; w < kWords; ++w) {
+    const int c = w * 32 + threadIdx.x % 32;
+    mine[w] = c < ap.clusters ? ap.cuts[c] : Cut{0, 0, 0, 0};
+    there[w] = __ballot_sync(~0u, mine[w].rows > 0);
+    cuts += __popc(there[w]);
   }
-  const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
-  write(out_row, make_float4(sum.x * inverse, sum.y * inverse, sum.z * inverse, sum.w * inverse));
+  for (int item = blockIdx.x; item < cuts * kItems; item += gridDim.x) {
+    int n = item / kItems;
+    Cut cut{};
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      uint32_t left = there[w];
+      if (n >= 0 && n < __popc(left)) {
+        for (int k = 0; k < n; ++k) left &= left - 1u;
+        const int from = __ffs(left) - 1;
+        cut.slot = __shfl_sync(~0u, mine[w].slot, from);
+        cut.last = __shfl_sync(~0u, mine[w].last, from);
+        cut.row0 = __shfl_sync(~0u, mine[w].row0, from);
+        cut.rows = __shfl_sync(~0u, mine[w].rows, from);
+      }
+      n -= __popc(there[w]);
+    }
+    if (row >= cut.rows) continue;
+    const int column = item % kItems * kJoinColumns + threadIdx.x / kTileRows * 4;
+    const int c0 = cut.slot / 2;
+    // Eight clusters' loads at a time, under the largest reference so far.
+    constexpr int kBatch = 8;
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float top = -INFINITY, total = 0.0f;
+    float4 sum = zero;
+    for (int c = c0; c <= cut.last; c += kBatch) {
+      float2 st[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        st[k] = make_float2(-INFINITY, 0.0f);
+        v[k] = zero;
+        if (c + k > cut.last) continue;
+        const int slot = c + k == c0 ? cut.slot : 2 * (c + k);
+        st[k] = ap.stats[slot * kTileRows + row];
+        v[k] =
+            ap.partial[(static_cast<size_t>(slot) * (kLatent / 4) + column / 4) * kTileRows + row];
+      }
+      float next = top;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) next = fmaxf(next, st[k].x);
+      const float keep = shift_factor(top, next);
+      top = next;
+      total *= keep;
+      sum = make_float4(sum.x * keep, sum.y * keep, sum.z * keep, sum.w * keep);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float f = shift_factor(st[k].x, top);
+        total = fmaf(f, st[k].y, total);
+        sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
+        sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
+      }
+    }
+    const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
+    *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(cut.row0) + row) * kLatent + column) =
+        make_uint2(pack_bf16(sum.x * inverse, sum.y * inverse),
+                   pack_bf16(sum.z * inverse, sum.w * inverse));
+  }
 }
 
 constexpr int kMaxDevicesTracked = 64;
-// Clusters whose partials the workspace holds.
-constexpr int kMaxClusters = 80;
 
 template <int kLatent>
 constexpr uint32_t smem_bytes() {
@@ -1169,8 +1216,7 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
   ap.partial = static_cast<float4*>(workspace);
   ap.stats = reinterpret_cast<float2*>(ap.partial + static_cast<size_t>(2) * kMaxClusters *
                                                         (kLatent / 4) * kTileRows);
-  ap.piece = reinterpret_cast<int32_t*>(ap.stats + static_cast<size_t>(2) * kMaxClusters *
-                                                       kTileRows);
+  ap.cuts = reinterpret_cast<Cut*>(ap.stats + static_cast<size_t>(2) * kMaxClusters * kTileRows);
   AttendMaps maps;
   using L = Shape<kLatent>;
   const bool whole = ap.box == kCtaTokens;
@@ -1191,11 +1237,17 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
   cfg.dynamicSmemBytes = smem_bytes<kLatent>();
   e = cudaLaunchKernelEx(&cfg, attend_kernel<kLatent>, maps, ap);
   if (e != cudaSuccess) return e;
-  // Row tiles of all requests at most, and one block for the rows of none.
+  // Row tiles of all requests at most.  None is cut where each fits the shortest
+  // run and there is a cluster for each.
   const int tiles = static_cast<int>(static_cast<int64_t>(p.rows) * p.heads / kTileRows) +
-                    std::min(p.requests, p.rows) + 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles), kLatent / 8);
-  cfg.blockDim = dim3(256);
+                    std::min(p.requests, p.rows);
+  if (tiles == 0 || (tiles <= ap.clusters &&
+                     static_cast<int64_t>(p.table_width) * p.page_size <= kMinRun * kTokens))
+    return cudaSuccess;
+  // (Four blocks an SM.)
+  cfg.gridDim = dim3(static_cast<unsigned>(
+      std::min(std::min(tiles, ap.clusters) * (kLatent / kJoinColumns), 8 * ap.clusters)));
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join_kernel<kLatent>, ap);
 }
@@ -1205,7 +1257,7 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
 size_t latent_workspace_bytes(int latent) {
   return static_cast<size_t>(2) * kMaxClusters * kTileRows *
              (static_cast<size_t>(latent) * sizeof(float) + sizeof(float2)) +
-         256;
+         kMaxClusters * sizeof(Cut);
 }
 
 cudaError_t launch_latent_attend(const LatentParams& p, int latent, void* workspace,
