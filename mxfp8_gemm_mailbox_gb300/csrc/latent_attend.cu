@@ -111,6 +111,29 @@ struct Shape {
                 "half of tensor memory's queries fit a place of the ring");
 };
 
+// One row tile's run of token tiles inside a cluster's share.
+struct Segment {
+  int b, kv0, kv1, kv_tiles;
+  int length, context, drafts, begin;
+  int row0;   // first row of the tile within the request (drafts x heads rows)
+  int valid;  // rows of the tile, at most 128
+  int slot;   // of its partial outputs
+};
+struct Walk {
+  uint32_t at, end, from;  // of the list of runs
+  int b;                   // -1 before the share's first segment
+};
+// The deal.
+struct Lists {
+  uint32_t first[kMaxRequests + 1];  // runs (pieces, or token tiles) before each request
+  int32_t length[kMaxRequests];
+  uint16_t begin[kMaxRequests + 1];  // rows are at most MXFP8_MAX_LATENT_ROWS
+  int32_t piece;                     // token tiles of a piece, 0 for an even deal
+  uint32_t run;                      // runs of the list a cluster has
+  Segment head;                      // this cluster's first segment
+  Walk walk;                         // past it
+};
+
 template <int kStages>
 struct Misc {
   // Barriers, in runs by their arrivals a phase.  Every one but `drained`
@@ -126,13 +149,10 @@ struct Misc {
   uint64_t q_ready;                              // 16: all softmax warps of both
   uint32_t tmem;
   int32_t abort;
-  int32_t piece;  // token tiles of a piece, 0 for an even deal
   float tops[2][2][128];             // [a group's tile parity][group][lane]: maxima
   float reference[2][128];           // [tile parity][lane], after that tile
   float sums[4][kCtaRows];           // [group, token half][row]
-  uint32_t first[kMaxRequests + 1];  // runs (pieces, or token tiles) before each request
-  int32_t length[kMaxRequests];
-  uint16_t begin[kMaxRequests + 1];  // rows are at most MXFP8_MAX_LATENT_ROWS
+  Lists lists;
 };
 
 // The device-side inputs of one request, cut to what the buffers hold.
@@ -205,46 +225,37 @@ __device__ __forceinline__ bool finite_bf16(uint4 v) {
   return finite;
 }
 
-template <class Misc>
-__device__ __forceinline__ int drafts_of(const Misc& m, int b) {
-  return max(m.begin[b + 1] - m.begin[b], 0);
+__device__ __forceinline__ int drafts_of(const Lists& l, int b) {
+  return max(l.begin[b + 1] - l.begin[b], 0);
 }
 
-// One row tile's run of token tiles inside a cluster's share.
-struct Segment {
-  int b, kv0, kv1, kv_tiles;
-  int length, context, drafts, begin;
-  int row0;   // first row of the tile within the request (drafts x heads rows)
-  int valid;  // rows of the tile, at most 128
-  int slot;   // of its partial outputs
+// The segment at a place of a cluster's share, by a whole warp.
+struct Next {
+  Segment s;
+  Walk w;
 };
-struct Walk {
-  uint32_t at, end, from;  // of the list of runs
-  int b;
-};
-template <class Misc>
-__device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& p, int cluster,
-                                             Walk& w, Segment& s) {
-  if (w.at >= w.end) return false;
+__device__ __forceinline__ Next segment_at(const Lists& l, int requests, int heads, int cluster,
+                                           Walk w) {
   // The request of run `at`: a lane looks at one of 32.
   for (;; w.b += 32) {
     const int b = w.b + threadIdx.x % 32;
-    const uint32_t past = __ballot_sync(~0u, b < p.requests && m.first[b + 1] <= w.at);
+    const uint32_t past = __ballot_sync(~0u, b < requests && l.first[b + 1] <= w.at);
     if (past == ~0u) continue;
     w.b += __popc(past);
     break;
   }
+  Segment s;
   s.b = w.b;
-  s.length = m.length[w.b];
-  s.begin = m.begin[w.b];
-  s.drafts = drafts_of(m, w.b);
+  s.length = l.length[w.b];
+  s.begin = l.begin[w.b];
+  s.drafts = drafts_of(l, w.b);
   s.context = max(s.length - s.drafts, 0);
   s.kv_tiles = token_tiles(s.length);
-  const uint32_t local = w.at - m.first[w.b];
+  const uint32_t local = w.at - l.first[w.b];
   int tile;
-  if (m.piece > 0) {
+  if (l.piece > 0) {
     // At most as many pieces as clusters, so the products stay below 2^32.
-    const uint32_t kv = s.kv_tiles, piece = m.piece;
+    const uint32_t kv = s.kv_tiles, piece = l.piece;
     const uint32_t pieces = (kv + piece - 1) / piece;
     tile = local / pieces;
     const uint32_t k = local - tile * pieces;
@@ -262,7 +273,25 @@ __device__ __forceinline__ bool next_segment(const Misc& m, const LatentParams& 
     w.at += s.kv1 - s.kv0;
   }
   s.row0 = tile * kTileRows;
-  s.valid = min(kTileRows, s.drafts * p.heads - s.row0);
+  s.valid = min(kTileRows, s.drafts * heads - s.row0);
+  return {s, w};
+}
+// The first segment is found once, with the deal: with a copy of that code a
+// role, the warps waited for it to come from far, 0.7 to 1.4 us.
+__device__ __noinline__ Next step(const Lists& l, int requests, int heads, int cluster, Walk w) {
+  return segment_at(l, requests, heads, cluster, w);
+}
+__device__ __forceinline__ bool next_segment(const Lists& l, const LatentParams& p, int cluster,
+                                             Walk& w, Segment& s) {
+  if (w.b < 0) {
+    s = l.head;
+    w = l.walk;
+    return s.kv1 > s.kv0;
+  }
+  if (w.at >= w.end) return false;
+  const Next next = step(l, p.requests, p.heads, cluster, w);
+  s = next.s;
+  w = next.w;
   return true;
 }
 // Whether a token tile reaches the drafts or the length.
@@ -329,84 +358,81 @@ __device__ __forceinline__ uint32_t run_length(uint32_t tiles, int clusters) {
   return max(static_cast<uint32_t>(kMinRun), (tiles + clusters - 1) / clusters);
 }
 
-// The deal's terms: all token tiles, and the token tiles of a piece (0 for an
-// even deal in runs), by a warp whose lane asks `at(b)` for request b's row
-// tiles and token tiles.  (The host has checked that all token tiles number
+// The deal, by one warp.  (The host has checked that all token tiles number
 // less than 2^31.)
-struct Terms {
-  uint32_t all;
-  int piece;
-};
-template <class At>
-__device__ __forceinline__ Terms terms_of(int requests, int clusters, int lane, At at) {
-  uint32_t all = 0;
-  int tiles_of_rows = 0;
-  for (int b = lane; b < requests + lane; b += 32) {
-    const int2 t = b < requests ? at(b) : make_int2(0, 0);
-    all += __reduce_add_sync(~0u, static_cast<uint32_t>(t.x) * t.y);
-    tiles_of_rows += __reduce_add_sync(~0u, t.x);
-  }
-  if (tiles_of_rows > clusters) return {all, 0};
-  // Pieces: the shortest length, from that of the even deal on, at which all
-  // pieces fit the clusters, one a cluster.
-  const uint32_t run = run_length(all, clusters);
-  uint32_t pieces[kPieceSlack + 1] = {};
-  for (int b = lane; b < requests; b += 32) {
-    const int2 t = at(b);
-#pragma unroll
-    for (int k = 0; k <= kPieceSlack; ++k) pieces[k] += t.x * ((t.y + run + k - 1) / (run + k));
-  }
-  int piece = 0;
-#pragma unroll
-  for (int k = kPieceSlack; k >= 0; --k)
-    if (__reduce_add_sync(~0u, pieces[k]) <= static_cast<uint32_t>(clusters)) piece = run + k;
-  return {all, piece};
-}
-
-// The deal, by one warp: fills Misc's lists.
-template <class Misc>
-__device__ __forceinline__ void deal(Misc& m, const AttendParams& ap, int lane) {
+__device__ __forceinline__ void deal(Lists& l, const AttendParams& ap, int cluster, int lane) {
   const LatentParams& p = ap.in;
-  auto load = [&](int b) {
-    const Request r = load_request(p, b);
-    if (r.cut && blockIdx.x == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
-    m.length[b] = r.length;
-    m.begin[b] = static_cast<uint16_t>(r.begin);
-    if (b == p.requests - 1) m.begin[b + 1] = static_cast<uint16_t>(r.begin + r.drafts);
-    return make_int2(r.length > 0 ? row_tiles(r.drafts, p.heads) : 0, token_tiles(r.length));
-  };
-  // The first 32 requests stay in registers.
-  const int2 mine = lane < p.requests ? load(lane) : make_int2(0, 0);
-  for (int b = lane + 32; b < p.requests; b += 32) load(b);
+  uint32_t all = 0;  // token tiles
+  int tiles = 0;     // row tiles
+  for (int base = 0; base < p.requests; base += 32) {
+    const int b = base + lane;
+    int rt = 0, tt = 0;
+    if (b < p.requests) {
+      const Request r = load_request(p, b);
+      if (r.cut && blockIdx.x == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
+      l.length[b] = r.length;
+      l.begin[b] = static_cast<uint16_t>(r.begin);
+      if (b == p.requests - 1) l.begin[b + 1] = static_cast<uint16_t>(r.begin + r.drafts);
+      rt = r.length > 0 ? row_tiles(r.drafts, p.heads) : 0;
+      tt = token_tiles(r.length);
+    }
+    all += __reduce_add_sync(~0u, static_cast<uint32_t>(rt) * tt);
+    tiles += __reduce_add_sync(~0u, rt);
+  }
   __syncwarp();
-  auto at = [&](int b) {
-    if (b < 32) return mine;
-    const int n = m.length[b];
-    return make_int2(n > 0 ? row_tiles(drafts_of(m, b), p.heads) : 0, token_tiles(n));
+  auto row_tiles_of = [&](int b) {
+    return l.length[b] > 0 ? row_tiles(drafts_of(l, b), p.heads) : 0;
   };
-  const Terms terms = terms_of(p.requests, ap.clusters, lane, at);
-  const int piece = terms.piece;
+  // Pieces: the shortest length, from that of the even deal on, at which all
+  // pieces fit the clusters, one a cluster; a lane a length and every fourth
+  // request.
+  static_assert(kPieceSlack < 8, "");
+  const uint32_t run = run_length(all, ap.clusters), slack = lane % 8;
+  uint32_t piece = 0;
+  if (tiles <= ap.clusters) {
+    uint32_t pieces = 0;
+    for (int b = lane / 8; b < p.requests; b += 4)
+      pieces += row_tiles_of(b) * ((token_tiles(l.length[b]) + run + slack - 1) / (run + slack));
+    pieces += __shfl_xor_sync(~0u, pieces, 8);
+    pieces += __shfl_xor_sync(~0u, pieces, 16);
+    const uint32_t fits = __ballot_sync(
+        ~0u, slack <= kPieceSlack && pieces <= static_cast<uint32_t>(ap.clusters));
+    if (fits != 0u) piece = run + __ffs(fits) - 1;
+  }
   uint32_t before = 0;
-  for (int b = lane; b < p.requests + lane; b += 32) {
-    const int2 t = b < p.requests ? at(b) : make_int2(0, 0);
-    uint32_t runs = t.x * (piece > 0 ? static_cast<uint32_t>(t.y + piece - 1) / piece : t.y);
+  for (int base = 0; base < p.requests; base += 32) {
+    const int b = base + lane;
+    uint32_t runs = 0;
+    if (b < p.requests) {
+      const uint32_t tt = token_tiles(l.length[b]);
+      runs = row_tiles_of(b) * (piece > 0 ? (tt + piece - 1) / piece : tt);
+    }
     for (int o = 1; o < 32; o *= 2) {
       const uint32_t v = __shfl_up_sync(~0u, runs, o);
       if (lane >= o) runs += v;
     }
-    if (b < p.requests) m.first[b + 1] = before + runs;
+    if (b < p.requests) l.first[b + 1] = before + runs;
     before += __shfl_sync(~0u, runs, 31);
   }
   if (lane == 0) {
-    m.first[0] = 0;
-    m.piece = piece;
+    l.first[0] = 0;
+    l.piece = static_cast<int>(piece);
+    l.run = piece > 0 ? 1 : run;
+  }
+  __syncwarp();
+  const uint32_t share = piece > 0 ? 1 : run;
+  const uint32_t from = min(before, cluster * share), end = min(before, from + share);
+  Next next{{}, {from, end, from, 0}};
+  if (from < end) next = segment_at(l, p.requests, p.heads, cluster, next.w);
+  if (lane == 0) {
+    l.head = next.s;
+    l.walk = next.w;
   }
 }
 
 // Zeros for the rows before the first request, past the last and of requests
 // without tokens; a warp of every cluster, in turn.
-template <class Misc>
-__device__ __forceinline__ void zero_rows(const Misc& m, const LatentParams& p, int lane,
+__device__ __forceinline__ void zero_rows(const Lists& l, const LatentParams& p, int lane,
                                           int latent) {
   auto zero = [&](int from, int to) {
     const int row_bytes = p.heads * latent * 2;  // a multiple of 512
@@ -416,15 +442,15 @@ __device__ __forceinline__ void zero_rows(const Misc& m, const LatentParams& p, 
       for (int i = lane; i < row_bytes / 16; i += 32) row[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  zero(0, p.requests > 0 ? m.begin[0] : 0);
-  zero(p.requests > 0 ? m.begin[p.requests] : 0, p.rows);
+  zero(0, p.requests > 0 ? l.begin[0] : 0);
+  zero(p.requests > 0 ? l.begin[p.requests] : 0, p.rows);
   for (int base = 0; base < p.requests; base += 32) {
     const int b = base + lane;
     uint32_t empty =
-        __ballot_sync(~0u, b < p.requests && m.length[b] == 0 && drafts_of(m, b) > 0);
+        __ballot_sync(~0u, b < p.requests && l.length[b] == 0 && drafts_of(l, b) > 0);
     for (; empty != 0u; empty &= empty - 1u) {
       const int e = base + __ffs(empty) - 1;
-      zero(m.begin[e], m.begin[e + 1]);
+      zero(l.begin[e], l.begin[e + 1]);
     }
   }
 }
@@ -470,14 +496,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   ptx::cluster_sync();
   ptx::tc_fence_after();
   const uint32_t tmem = m.tmem;
-  ptx::grid_dependency_wait();
-  if (warp == 0) deal(m, ap, lane);
-  __syncthreads();
+  // The wait for the kernel before and for the deal.  Every role makes it at its
+  // own start: the code that follows is then at hand when it is over.
+  auto begin = [&] {
+    ptx::grid_dependency_wait();
+    asm volatile("bar.sync 0;" ::: "memory");
+  };
 
-  const uint32_t all = m.first[p.requests];
-  const uint32_t run = m.piece > 0 ? 1 : run_length(all, ap.clusters);
-  const uint32_t from = min(all, cluster * run);
-  Walk walk{from, min(all, from + run), from, 0};
+  Walk walk{0, 0, 0, -1};
   Segment seg{};
   const Waiter wait{&m.abort, p.flags};
   // The page of the box with token `token`: in the pool, or past it (then the
@@ -489,6 +515,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
 
   if (warp == 0 || warp == 3) {
     // -------------------------------------------------------------- producer
+    if (warp == 0) {
+      ptx::grid_dependency_wait();
+      deal(m.lists, ap, cluster, lane);
+    }
+    begin();
     // A tile's part in one copy where a page holds 32 tokens in a row, else a
     // lane a box of each block.  The page of a lane's box is read one of this
     // warp's tiles ahead.
@@ -512,8 +543,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       __syncwarp();
       return ok;
     };
-    while (ok && next_segment(m, p, cluster, walk, seg)) {
+    while (ok && next_segment(m.lists, p, cluster, walk, seg)) {
       const uint64_t keep = cache_policy(p, seg);
+      // This warp's first token tile.
+      const int first = seg.kv0 + ((r & 1) != which);  // (the queries take two places)
+      int page[kItems];
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) page[k] = page_of(first, lane + 32 * k);
       uint32_t full;
       // The queries that go to tensor memory, half of their blocks a place.
       for (int half = 0; half < 2; ++half, ++r) {
@@ -527,11 +563,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         __syncwarp();
       }
       if (!ok) break;
-      // This warp's first token tile.
-      const int first = seg.kv0 + ((r & 1) != which);
-      int page[kItems];
-#pragma unroll
-      for (int k = 0; k < kItems; ++k) page[k] = page_of(first, lane + 32 * k);
       const int r0 = r - seg.kv0;
       for (int kv = first; kv < seg.kv1; kv += 2) {
         r = r0 + kv;
@@ -566,6 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                      kWaitLimitNs / 16);
   } else if (warp == kFetchWarp) {
     // ----------------------------------------------------------------- fetch
+    begin();
     // This CTA's value columns of the peer's tokens, over the blocks of its own
     // tokens that only the keys' product reads.
     const int blocks = ap.box == kCtaTokens ? 1 : L::kHalf;  // copies of a box
@@ -580,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     int r = 0, j = 0;  // places of the ring, token tiles
     uint32_t segments = 0;
     bool ok = true;
-    for (; ok && next_segment(m, p, cluster, walk, seg); ++segments) {
+    for (; ok && next_segment(m.lists, p, cluster, walk, seg); ++segments) {
       // Every product with the last row tile's queries is done.
       const uint32_t full = bar(m.q_full);
       if (lane == 0) ptx::mbar_arrive_expect_tx(full, L::kSmemBlocks * kQBlockBytes);
@@ -621,6 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     }
   } else if (warp == 1) {
     // --------------------------------------------------------- scores' issuer
+    begin();
     // Both issuers stay converged and one elected lane issues (from a branch on
     // the lane number a product took half as long again).  A pair's 128 x 64 x
     // 16 product takes 18 clocks with the queries in tensor memory, 25 with
@@ -632,7 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     int r = 0;  // places of the ring
     uint32_t segments = 0;
     bool ok = rank == 0;
-    while (ok && next_segment(m, p, cluster, walk, seg)) {
+    while (ok && next_segment(m.lists, p, cluster, walk, seg)) {
       ok = __all_sync(~0u, wait(m.q_ready, segments++));
       // Every softmax warp has read the queries.
       if (lane < 4)
@@ -678,26 +711,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     }
   } else if (warp == kOutputWarp) {
     // -------------------------------------------------------- outputs' issuer
+    begin();
     if (rank == 1) {  // nothing to issue
-      zero_rows(m, p, lane, kLatent);
+      zero_rows(m.lists, p, lane, kLatent);
       // For the join.
       Cut cut{0, 0, 0, 0};
       Walk ahead = walk;
       for (;;) {
-        const uint32_t at = ahead.at;
-        if (!next_segment(m, p, cluster, ahead, seg)) break;
+        if (!next_segment(m.lists, p, cluster, ahead, seg)) break;
         if (seg.kv0 != 0 || seg.kv1 == seg.kv_tiles) continue;
-        const uint32_t runs =
-            m.piece > 0 ? (seg.kv_tiles + m.piece - 1) / m.piece : seg.kv_tiles;
-        cut = Cut{seg.slot, static_cast<int>((at + runs - 1) / run),
-                  seg.begin * p.heads + seg.row0, seg.valid};
+        // The clusters of its other runs follow this one.
+        const int piece = m.lists.piece, left = seg.kv_tiles - seg.kv1;
+        const int more = piece > 0 ? (seg.kv_tiles + piece - 1) / piece - 1
+                                   : (left + m.lists.run - 1) / m.lists.run;
+        cut = Cut{seg.slot, cluster + more, seg.begin * p.heads + seg.row0, seg.valid};
       }
       if (lane == 0) ap.cuts[cluster] = cut;
     }
     constexpr uint32_t kOutputs = ptx::idesc_bf16(256, true);
     int j = 0, r = 0;
     bool ok = rank == 0;
-    while (ok && next_segment(m, p, cluster, walk, seg)) {
+    while (ok && next_segment(m.lists, p, cluster, walk, seg)) {
       r += 2;
       for (int kv = seg.kv0; ok && kv < seg.kv1; ++kv, ++r, ++j) {
         ok = wait(m.v_ready[j % kStages], j / kStages);
@@ -734,11 +768,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------- keys' mender
+    begin();
     // A draft with a non-finite number in its latent gets NaN for a score from
     // every row: an infinity alone could come out as a weight of zero.
     int r = 0, j = 0;
     bool ok = true;
-    while (ok && next_segment(m, p, cluster, walk, seg)) {
+    while (ok && next_segment(m.lists, p, cluster, walk, seg)) {
       for (int kv = seg.kv0 - 2; kv < seg.kv1; ++kv, ++r) {  // two of queries first
         ok = __all_sync(~0u, wait(m.kv_full[r % kStages], r / kStages));
         if (!ok) break;
@@ -770,11 +805,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     ptx::launch_dependents();
   } else if (warp == kValueMender) {
     // -------------------------------------------------------- values' mender
+    begin();
     // Zeros for the tokens past the length and for drafts that are not finite:
     // rows that do not see them give them weights of zero.
     int r = 0, j = 0;
     bool ok = true;
-    while (ok && next_segment(m, p, cluster, walk, seg)) {
+    while (ok && next_segment(m.lists, p, cluster, walk, seg)) {
       r += 2;
       for (int kv = seg.kv0; kv < seg.kv1; ++kv, ++r, ++j) {
         ok = __all_sync(~0u, wait(m.v_full[j % kStages], j / kStages));
@@ -813,6 +849,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     }
   } else {
     // --------------------------------------------------------------- softmax
+    begin();
     const int group = (warp - kSoftmaxWarp) / 4;  // takes the tiles of this parity
     const int quarter = warp & 3;  // the 32 tensor-memory lanes this warp reaches
     // Quarters 0 and 1 hold the rows' scores of the first half of a tile's
@@ -836,7 +873,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       if (tiles > 1 && ((g + tiles) & 1) == group) added(g + tiles - 2);
       added(g + tiles - 1);
     };
-    for (uint32_t segments = 0; next_segment(m, p, cluster, walk, seg); ++segments) {
+    for (uint32_t segments = 0; next_segment(m.lists, p, cluster, walk, seg); ++segments) {
       const int tile_row = static_cast<int>(rank) * kCtaRows + row;
       const size_t q_row = static_cast<size_t>(seg.begin) * p.heads + seg.row0 + tile_row;
       const bool mine = tile_row < seg.valid;
