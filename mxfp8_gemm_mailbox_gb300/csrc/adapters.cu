@@ -55,14 +55,6 @@ constexpr int kInnerThreads = 256;
 
 __host__ __device__ constexpr int pieces_of(int k) { return (k + kPiece - 1) / kPiece; }
 
-__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ float low_bf16(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float high_bf16(uint32_t w) {
   return __uint_as_float(w & 0xFFFF0000u);
@@ -85,7 +77,7 @@ __device__ __forceinline__ void inner_item(const AdapterParams& p, int t, int pi
     for (int r = 0; r < kRowsOfA; ++r) {
       a[r][s] = make_uint4(0u, 0u, 0u, 0u);
       if (j0 + r < rank && k0 + s * 256 < p.k)
-        a[r][s] = load_once(p.a + (static_cast<size_t>(i) * p.rank + j0 + r) * p.k + k0 + s * 256);
+        a[r][s] = ptx::ld_once_v4(p.a + (static_cast<size_t>(i) * p.rank + j0 + r) * p.k + k0 + s * 256);
     }
   float sum[kRowsOfA] = {};
 #pragma unroll
@@ -159,7 +151,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 7)
 #pragma unroll
     for (int l = 0; l < kDeltaLoads; ++l)
       if (live && n0 + l * kAtOnce < p.n)
-        w[l] = load_once(b + static_cast<size_t>(l) * kAtOnce * rank8);
+        w[l] = ptx::ld_once_v4(b + static_cast<size_t>(l) * kAtOnce * rank8);
     if (have < 0) ptx::grid_dependency_wait();
     if (have != t) {
       if (have >= 0) __syncthreads();
@@ -180,7 +172,7 @@ __global__ void __launch_bounds__(kDeltaThreads, 7)
 #pragma unroll
         for (int l = 0; l < kDeltaLoads; ++l)
           if (n0 + l * kAtOnce < p.n)
-            w[l] = load_once(b + static_cast<size_t>(l) * kAtOnce * rank8 + j0 - sub * 8);
+            w[l] = ptx::ld_once_v4(b + static_cast<size_t>(l) * kAtOnce * rank8 + j0 - sub * 8);
       }
       // (Columns past the adapter's rank may hold anything.)
       const int left = rank - j0;

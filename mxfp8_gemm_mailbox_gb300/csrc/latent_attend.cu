@@ -78,7 +78,7 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 constexpr float kLazy = 8.0f;
 // Pieces of one row tile a cluster may be this many token tiles longer than an
 // even deal's runs: about what a second row tile in a run costs.
-constexpr int kPieceSlack = 5;
+constexpr int kPieceSlack = 7;
 constexpr int kMinRun = 4;
 constexpr int kMaxClusters = 80;  // whose partials the workspace holds
 constexpr uint32_t kBlockBytes = kCtaTokens * 128;  // 32 tokens x 64 columns
@@ -380,8 +380,12 @@ __device__ __forceinline__ void deal(Lists& l, const AttendParams& ap, int clust
     tiles += __reduce_add_sync(~0u, rt);
   }
   __syncwarp();
+  // Rows given to several requests could make up more tiles than the host
+  // counted: such a list is not dealt at all.
+  const bool sound = tiles <= p.rows * p.heads / kTileRows + p.requests;
+  if (!sound && blockIdx.x == 0 && lane == 0) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
   auto row_tiles_of = [&](int b) {
-    return l.length[b] > 0 ? row_tiles(drafts_of(l, b), p.heads) : 0;
+    return sound && l.length[b] > 0 ? row_tiles(drafts_of(l, b), p.heads) : 0;
   };
   // Pieces: the shortest length, from that of the even deal on, at which all
   // pieces fit the clusters, one a cluster; a lane a length and every fourth

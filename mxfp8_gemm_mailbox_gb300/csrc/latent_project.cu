@@ -60,16 +60,6 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 16 bytes read once, in program order with the wait for the kernel before.
-__device__ __forceinline__ uint4 load_once(const uint16_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-
 // Warps that share an output's sum over `inner` numbers.
 __host__ __device__ constexpr int sum_warps(int inner) {
   const int steps = inner / 32;
@@ -99,7 +89,7 @@ __device__ __forceinline__ void products(const uint16_t* __restrict__ w,
     for (int k = 0; k < kBatch; ++k)
       if (k0 + k < kSteps)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) a[r][k] = load_once(wp + r * 8 * kInner + (k0 + k) * 32);
+        for (int r = 0; r < 4; ++r) a[r][k] = ptx::ld_once_v4(wp + r * 8 * kInner + (k0 + k) * 32);
     // The weights do not depend on the kernel before; the activations do.
     if (k0 == 0) ptx::grid_dependency_wait();
     uint4 b[kBatch];

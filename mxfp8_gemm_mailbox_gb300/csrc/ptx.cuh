@@ -47,18 +47,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// Whether the phase is over, at once (try_wait may suspend the thread).
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -290,29 +278,10 @@ __device__ __forceinline__ bool elect_one() {
       : "=r"(r));
   return r != 0;
 }
-// BF16 MMA (kind::f16), D[tmem] (+)= A B^T, one elected thread; A in shared
-// memory (`a_desc`) or in tensor memory (lane = row, a 32-bit column = two
-// consecutive K elements).
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// The same by a pair of CTAs (M = 128: 64 rows of A each), issued by the even
-// one for both.  Each holds its own rows of A and half of B's N rows at the
+// BF16 MMA (kind::f16), D[tmem] (+)= A B^T, by a pair of CTAs (M = 128: 64 rows
+// of A each), issued by one elected thread of the even one; A in shared memory
+// (`a_desc`) or in tensor memory (lane = row, a 32-bit column = two consecutive
+// K elements).  Each holds its own rows of A and half of B's N rows at the
 // same addresses, and its rows of D: lanes 0-63 the first N / 2 columns, lanes
 // 64-127 the rest.  A in tensor memory lies in both halves of the lanes.
 __device__ __forceinline__ void mma_f16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -361,13 +330,6 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn_major ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
-// K-major operand in the 64-byte swizzle: rows of 64 bytes, 8-row groups 512
-// bytes apart.
-__device__ __forceinline__ uint64_t desc_kmajor_sw64(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
-         (static_cast<uint64_t>(512 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(4) << 61);
-}
 // MN-major operand in the 128-byte swizzle: a row of 128 bytes is 64
 // consecutive M or N elements of one k, 8-k groups 1024 bytes apart, the next
 // 64 elements `mn_bytes` apart.
@@ -376,14 +338,6 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr, uint32_t 
          (static_cast<uint64_t>(mn_bytes >> 4) << 16) |
          (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
-}
-__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
 }
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
@@ -423,13 +377,6 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-// Arrive on a peer CTA's mbarrier (`remote_bar` from map_to_rank), ordering
-// nothing: for a caller whose reads have returned their values already.  (The
-// release form waits for the thread's earlier remote stores.)
-__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t remote_bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
-               : "memory");
-}
 // Arrive on an mbarrier of any CTA of the cluster (an address from map_to_rank),
 // after what this thread did to its own CTA's memories: for a waiter that lets
 // the pair's products read them there.  (Released to the cluster, an arrival
@@ -464,16 +411,6 @@ __device__ __forceinline__ void st_async_remote_v2(uint32_t remote_addr, uint32_
       "r"(a), "r"(b), "r"(remote_bar)
       : "memory");
 }
-// Store 4 bytes into a peer CTA's shared memory; the byte count completes on
-// the peer's mbarrier.
-__device__ __forceinline__ void st_async_remote(uint32_t remote_addr, uint32_t a,
-                                                uint32_t remote_bar) {
-  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
-                   remote_addr),
-               "r"(a), "r"(remote_bar)
-               : "memory");
-}
-
 // ------------------------------------------------ programmatic dependent launch
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -483,6 +420,15 @@ __device__ __forceinline__ void launch_dependents() {
 }
 
 // --------------------------------------------------------- global memory
+// 16 bytes read once, in program order with the wait for the kernel before.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ uint32_t ld_volatile_u32(const int32_t* p) {
   uint32_t v;
   asm volatile("ld.volatile.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");

@@ -350,3 +350,51 @@ def test_the_whole_step_feeds_the_projection(cuda):
     err = (eager.double() - want).abs()
     assert (err <= 2.0 ** -8 * want.abs() + 2.0 ** -18 * size).all()
     assert mailbox.status()[0] == mx.OK
+
+
+@pytest.mark.parametrize("latent,page", [(256, 8), (512, 64)])
+@pytest.mark.parametrize("heads", [3, 100])
+@pytest.mark.parametrize("contexts", [(30, 150), (150, 30), (300, 30)])
+def test_several_row_tiles_in_a_share(cuda, latent, page, heads, contexts):
+    # More row tiles than the GPU takes at once: each share holds parts of several.
+    attend(cuda, Paged(contexts * 60, [1] * 120, latent, page), heads)
+
+
+@pytest.mark.parametrize("latent", [256, 512])
+def test_long_shares_of_one_and_of_several_row_tiles(cuda, latent):
+    attend(cuda, Paged([30011, 29000], [1, 2], latent, 64), 128)
+    attend(cuda, Paged([700 + 13 * b for b in range(90)], [1] * 90, latent, 32), 128)
+
+
+def test_short_tables_are_never_cut_long_ones_are(cuda):
+    # 256 tokens at most: one kernel; the same lengths under a table of more pages: two.
+    short = Paged([200, 0, 256], [2, 1, 0], 512, 64)
+    attend(cuda, short, 70)
+    short.table = torch.cat([short.table, torch.full_like(short.table, -7)], 1)
+    attend(cuda, short, 70)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf")])
+def test_an_infinite_draft_is_nan_whatever_its_scores(cuda, value):
+    # q . c is -inf or +inf by the sign of q there: NaN for the rows that see it either way.
+    for column in (0, 255, 256, 511):
+        paged = Paged([70], [2], 512, 32)
+        paged.cache[int(paged.table[0, 70 // 32]), 70 % 32, column] = value
+        q = normal(4, 2, 32, 576)
+        q[:, ::2, column], q[:, 1::2, column] = 1.0, -1.0
+        at = mx.LatentAttention(32)
+        got = at.run(q, paged.cache, paged.table, paged.lengths, paged.begin, SCALE,
+                     tree=masks_tensor([1, 2]))
+        assert torch.isnan(got[0]).all() and at.status() == 0
+        want, weight = paged.expected(q, SCALE, [1, 2])
+        close(got[1], want[1], weight[1])
+
+
+def test_rows_given_twice_are_refused_on_the_device(cuda):
+    # Descending row ranges would be more rows than the call has.
+    paged = Paged([30] * 8, [1] * 8, 256, 16)
+    begin = torch.tensor([0, 8] * 4 + [0], dtype=torch.int32, device="cuda")
+    at = mx.LatentAttention(128, 256)
+    out = at.run(normal(1, 8, 128, 320), paged.cache, paged.table, paged.lengths, begin, SCALE)
+    assert out.shape == (8, 128, 256)
+    assert at.status() & mx.FLAG_BAD_INDEX

@@ -89,6 +89,12 @@ def test_attend_refusals(lib):
     assert attend(lib, rows=0, q=0) == mx.OK
 
 
+def test_attend_refuses_more_tiles_than_it_numbers(lib):
+    # 65535 x 256 / 128 + 1 row tiles of 2^20 / 64 token tiles: past 2^31
+    assert attend(lib, rows=65535, heads=256, table_width=1 << 14) == mx.ERR_UNSUPPORTED
+    assert "tiles" in text(lib)
+
+
 def test_run_adapted_needs_a_handle(lib):
     d = _lib.Adapters(0x1000, 0x1000, None, None, 1, 8)
     assert lib.mxfp8_publish_gemm_run_adapted(None, P(0x1000), P(0x1000), 1, None, ctypes.byref(d),
