@@ -90,8 +90,8 @@ def test_attend_refusals(lib):
 
 
 def test_attend_refuses_more_tiles_than_it_numbers(lib):
-    # 65535 x 256 / 128 + 1 row tiles of 2^20 / 64 token tiles: past 2^31
-    assert attend(lib, rows=65535, heads=256, table_width=1 << 14) == mx.ERR_UNSUPPORTED
+    # 65535 x 256 / 128 + 1 row tiles of 2^21 / 64 token tiles: past 2^31
+    assert attend(lib, rows=65535, heads=256, table_width=1 << 15) == mx.ERR_UNSUPPORTED
     assert "tiles" in text(lib)
 
 
