@@ -299,12 +299,6 @@ __device__ __forceinline__ bool special(const Segment& s, int kv) {
   return (kv + 1) * kTokens > s.context;
 }
 
-// Tokens that one row tile alone reads leave L2 first (8 x 64k tokens: 126 us,
-// 132 when they are kept or treated as any other); those of several stay.
-__device__ __forceinline__ uint64_t cache_policy(const LatentParams& p, const Segment& s) {
-  return s.drafts * p.heads > kTileRows ? ptx::policy_evict_last() : ptx::policy_evict_first();
-}
-
 // Bounded waits of a warp's lanes, which come out together.  One that runs out
 // sets `abort`, after which every wait of the CTA returns at once and the
 // kernel ends with its flag set.  (The softmax warps then run their loops out on whatever the
@@ -548,7 +542,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       return ok;
     };
     while (ok && next_segment(m.lists, p, cluster, walk, seg)) {
-      const uint64_t keep = cache_policy(p, seg);
       // This warp's first token tile.
       const int first = seg.kv0 + ((r & 1) != which);  // (the queries take two places)
       int page[kItems];
@@ -586,7 +579,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             page[k] = p.pages;
           }
           ptx::tma_load_4d(dst + block * kBlockBytes + at * 128, &maps.keys, 0,
-                           token % p.page_size, block, page[k], full, keep);
+                           token % p.page_size, block, page[k], full);
         }
         __syncwarp();
 #pragma unroll
@@ -628,7 +621,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                          ptx::policy_evict_first());
       __syncwarp();
       r += 2;
-      const uint64_t keep = cache_policy(p, seg);
       int page = page_of(seg.kv0);
       for (int kv = seg.kv0; kv < seg.kv1; ++kv, ++r, ++j) {
         const int next = page_of(kv + 1);
@@ -643,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           ptx::tma_load_4d(sbase + r % kStages * L::kPlaceBytes +
                                (theirs * L::kHalf + block) * kBlockBytes + at * 128,
                            &maps.values, 0, token_of(kv) % p.page_size, column0 + block, page,
-                           done, keep);
+                           done);
         }
         __syncwarp();
         page = next;

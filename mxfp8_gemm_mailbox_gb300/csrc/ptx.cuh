@@ -112,14 +112,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int3
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
 }
+// 4-D tiled TMA load into this CTA's shared memory, completing on `bar`; no
+// cache hint.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int32_t c0,
-                                            int32_t c1, int32_t c2, int32_t c3, uint32_t bar,
-                                            uint64_t policy) {
+                                            int32_t c1, int32_t c2, int32_t c3, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar),
-      "l"(policy)
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
 // Untiled bulk copy global -> shared (16-byte aligned, size a multiple of 16).
