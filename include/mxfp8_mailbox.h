@@ -455,8 +455,11 @@ size_t mxfp8_adapters_workspace_bytes(int32_t n, int32_t k, int32_t rank);
  * mxfp8_adapters_workspace_bytes(N, K, rank) bytes, written by every call, so
  * calls that share one must be ordered on one stream.  Nothing is kept of
  * *adapters beyond the call.  Three kernels, programmatically serialised: the
- * GEMM's weight stream starts beside the adapters' products.  As after
- * mxfp8_publish_gemm_run, one mailbox_consume must follow. */
+ * GEMM's weight stream starts beside the adapters' products.  The adapters, x,
+ * x_scale, which and alpha are read after the kernel before the call has
+ * finished, so it may write them; the projection's own weight is read earlier,
+ * as in mxfp8_publish_gemm_run.  As after that call, one mailbox_consume must
+ * follow. */
 mxfp8_status mxfp8_publish_gemm_run_adapted(mxfp8_publish_gemm* gemm, const void* x,
                                             const void* x_scale, int32_t m, const float* alpha,
                                             const mxfp8_adapters* adapters, const int32_t* which,
@@ -485,7 +488,11 @@ mxfp8_status mxfp8_publish_gemm_run_adapted(mxfp8_publish_gemm* gemm, const void
  * (w [heads][latent][nope] BF16 times q_nope [rows][heads][nope] BF16, summed
  * in FP32, rounded once) with q_rope [rows][heads][64] BF16 behind it.  nope:
  * a multiple of 32 in 32..512; latent: 256 or 512; all pointers device,
- * 16-byte aligned.  rows = 0 launches nothing. */
+ * 16-byte aligned.  rows = 0 launches nothing.
+ * Launched with programmatic stream serialisation: w is read before the kernel
+ * before this one on the stream has finished, so w must not be written by that
+ * kernel, nor by one still running when it starts (the rule of
+ * mxfp8_publish_gemm_run's weight); q_nope and q_rope are read after it has. */
 mxfp8_status mxfp8_latent_query(const void* q_nope, const void* q_rope, const void* w, void* q,
                                 int32_t rows, int32_t heads, int32_t nope, int32_t latent,
                                 void* stream);
@@ -495,7 +502,9 @@ mxfp8_status mxfp8_latent_query(const void* q_nope, const void* q_rope, const vo
  * [rows][heads][latent] BF16, summed in FP32) in MXFP8: a block of 32 takes
  * the smallest power of two under which no element passes 448, then rounds to
  * nearest even (a block of zeros takes 2^0; NaN elements stay NaN and do not
- * count towards a block's scale).  value: a multiple of 32 in 32..512. */
+ * count towards a block's scale).  value: a multiple of 32 in 32..512.  w is
+ * read before the kernel before this one has finished, as for
+ * mxfp8_latent_query; o is read after it has. */
 mxfp8_status mxfp8_latent_values(const void* o, const void* w, void* x, void* x_scale,
                                  int32_t rows, int32_t heads, int32_t latent, int32_t value,
                                  void* stream);
@@ -529,8 +538,12 @@ size_t mxfp8_latent_workspace_bytes(int32_t latent);
  * non-finite number in the latent of a draft makes the rows that see it NaN.
  * lengths, row_begin and page_table are read on the device; a page outside the
  * pool (read as zeros), a length past the table (cut) or rows outside q (cut)
- * raise MXFP8_FLAG_BAD_INDEX in *flags (device int32, may be NULL), and a wait
- * of the pipeline that runs out raises MXFP8_FLAG_GEMM_TIMEOUT.  workspace:
+ * raise MXFP8_FLAG_BAD_INDEX in *flags (device int32, may be NULL), as do
+ * row_begin that give rows to several requests (then the rows' results mean
+ * nothing), and a wait of the pipeline that runs out raises
+ * MXFP8_FLAG_GEMM_TIMEOUT.  A call whose rows, heads and page table could make
+ * up 2^31 or more tiles of 128 rows x 64 tokens is MXFP8_ERR_UNSUPPORTED.
+ * Every input is read after the kernel before this one has finished.  workspace:
  * device, 256-byte aligned; calls that share one must be ordered on one
  * stream. */
 mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* desc, const void* q, const void* cache,

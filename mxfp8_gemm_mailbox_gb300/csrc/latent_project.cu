@@ -19,7 +19,12 @@
 // 32 k + 8 q for both operands, and the products take them as they lie.  Long
 // sums are cut over two or four warps of a block (128 numbers a warp where that
 // divides them), so that every weight a warp needs is on its way at once, before
-// the wait for the kernel that makes the activations.
+// the wait for the kernel that makes the activations.  (The legacy product
+// instruction suffices: 8 rows are 3 % of the tensor cores' time.)
+//
+// Measured, 8 rows and 128 heads, one call after another: query 128 -> 512 3.6
+// us = 5.2 TB/s (19 MB), values 512 -> 128 4.1 us = 4.4 TB/s (18 MB); 1 row,
+// 16 and 32 heads: 1.4 and 2.2 us, launch and two round trips to memory.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
