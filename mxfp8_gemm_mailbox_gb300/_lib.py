@@ -117,6 +117,21 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+_calls = None
+
+
+def calls():
+    """The module ``_calls``: the C ABI's calls that take tensors as they are
+    (``csrc/calls.cpp``); raises if it has not been built."""
+    global _calls
+    if _calls is None:
+        load()
+        from . import _calls as module
+
+        _calls = module
+    return _calls
+
+
 class Mxfp8Error(RuntimeError):
     def __init__(self, status: int, where: str, message: str):
         self.status = status

@@ -237,23 +237,11 @@ class PublishGemm:
         the device, -1 for none) before its one rounding.  An index outside
         ``-1 .. count - 1`` counts as none and sets FLAG_BAD_INDEX, which
         ``mailbox.status`` reports."""
-        if alpha is not None and (alpha.dtype != torch.float32 or not alpha.is_cuda):
-            raise TypeError("alpha must be a float32 CUDA tensor")
-        m = self._rows(x, x_scale, c)
         if adapters.n != self.n or adapters.k != self.k:
             raise ValueError(f"the adapters are for N={adapters.n}, K={adapters.k}; the "
                              f"projection has N={self.n}, K={self.k}")
-        if which.dtype is not torch.int32 or which.dim() != 1 or which.shape[0] < m:
-            raise ValueError(f"which must be int32 [>= {m}], got {which.dtype} "
-                             f"{tuple(which.shape)}")
-        _on_device(which, "which")
-        desc, workspace, nbytes = adapters._borrowed
-        status = _lib.load().mxfp8_publish_gemm_run_adapted(
-            self._handle, x.data_ptr(), x_scale.data_ptr(), m, _ptr(alpha), desc,
-            which.data_ptr(), workspace, nbytes, _ptr(c), _stream(stream))
-        if status:
-            check(status, "mxfp8_publish_gemm_run_adapted")
-        return c
+        return _lib.calls().run_adapted(self._handle.value, self.n, self.k, *adapters._borrowed,
+                                        x, x_scale, which, alpha, c, stream)
 
     def run_unfused(self, x: torch.Tensor, x_scale: torch.Tensor, c: torch.Tensor,
                     stream=None) -> torch.Tensor:
@@ -319,7 +307,7 @@ class Adapters:
                                   gain.data_ptr() if gain is not None else None,
                                   ranks.data_ptr() if ranks is not None else None,
                                   self.count, self.rank)
-        self._borrowed = (ctypes.byref(self.desc), self.workspace.data_ptr(), nbytes)
+        self._borrowed = (ctypes.addressof(self.desc), self.workspace.data_ptr(), nbytes)
 
 
 class LamportGather:
