@@ -103,16 +103,8 @@ class Mailbox:
     def consume(self, m: int, out: torch.Tensor | None = None, timeout_ns: int = 0,
                 stream=None) -> torch.Tensor:
         """The consumer: [m][n] BF16 copied out of the active generation."""
-        if out is None:
-            out = torch.empty((m, self.n), dtype=torch.bfloat16, device=self.words.device)
-        else:
-            _halves(out, "out", m, self.n)
-        status = _lib.load().mailbox_consume(self.words.data_ptr(), self.state.data_ptr(),
-                                             self.capacity, self.n, m, out.data_ptr(), timeout_ns,
-                                             _stream(stream))
-        if status:
-            check(status, "mailbox_consume")
-        return out
+        return _lib.calls().mailbox_consume(self.words, self.state, self.capacity, self.n, m, out,
+                                            timeout_ns, stream)
 
     def status(self, stream=None):
         """(status code, [4] state words); synchronises the stream."""

@@ -84,6 +84,18 @@ int64_t codes(const at::Tensor& t, const char* name, int64_t cols, int64_t min_r
     refuse(PyExc_ValueError, std::string(name) + " must be a contiguous CUDA tensor");
   return t.size(0);
 }
+// A matrix of two-byte values [rows >= min_rows][cols].
+void halves(const at::Tensor& t, const char* name, int64_t cols, int64_t min_rows) {
+  if (t.element_size() != 2)
+    refuse(PyExc_TypeError, std::string(name) +
+                                " must hold two-byte values (bfloat16 / int16), got " +
+                                name_of(t.scalar_type()));
+  if (t.dim() != 2 || t.size(1) != cols || t.size(0) < min_rows)
+    refuse(PyExc_ValueError, std::string(name) + " must be [rows >= " + std::to_string(min_rows) +
+                                 "][" + std::to_string(cols) + "], got " + text_of(t.sizes()));
+  if (!t.is_cuda() || !t.is_contiguous())
+    refuse(PyExc_ValueError, std::string(name) + " must be a contiguous CUDA tensor");
+}
 at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType dtype, int device) {
   return at::empty(shape,
                    at::TensorOptions().dtype(dtype).device(at::Device(at::kCUDA, device)));
@@ -295,14 +307,7 @@ PyObject* run_adapted(PyObject*, PyObject* const* args, Py_ssize_t n) {
   codes(scale, "x_scale", k / 32, m);
   if (args[10] != Py_None) {
     const at::Tensor& t = tensor(args[10], "c");
-    if (t.element_size() != 2)
-      refuse(PyExc_TypeError, std::string("c must hold two-byte values (bfloat16 / int16), got ") +
-                                  name_of(t.scalar_type()));
-    if (t.dim() != 2 || t.size(1) != outputs || t.size(0) < m)
-      refuse(PyExc_ValueError, "c must be [rows >= " + std::to_string(m) + "][" +
-                                   std::to_string(outputs) + "], got " + text_of(t.sizes()));
-    if (!t.is_cuda() || !t.is_contiguous())
-      refuse(PyExc_ValueError, "c must be a contiguous CUDA tensor");
+    halves(t, "c", outputs, m);
     c = t.data_ptr();
   }
   if (which.scalar_type() != at::kInt || which.dim() != 1 || which.size(0) < m)
@@ -322,6 +327,32 @@ PyObject* run_adapted(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// (words, state, capacity, n, m, out | None, timeout_ns, stream | None) -> out; words and state
+// are tensors.
+PyObject* mailbox_consume(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  arguments(count, 8);
+  const at::Tensor &words = tensor(args[0], "words"), &state = tensor(args[1], "state");
+  const int64_t capacity = integer(args[2]), n = integer(args[3]), m = integer(args[4]);
+  if (m < INT32_MIN || m > INT32_MAX) refuse(PyExc_ValueError, "m is past 32 bits");
+  at::Tensor out;
+  if (args[5] == Py_None) {
+    out = new_tensor({m, n}, at::kBFloat16, gpu_of(words));
+  } else {
+    out = tensor(args[5], "out");
+    halves(out, "out", n, m);
+  }
+  const uint64_t timeout = PyLong_AsUnsignedLongLong(args[6]);
+  if (PyErr_Occurred()) throw python_error();
+  check(::mailbox_consume(words.data_ptr(), static_cast<int32_t*>(state.data_ptr()),
+                          static_cast<int32_t>(capacity), static_cast<int32_t>(n),
+                          static_cast<int32_t>(m), out.data_ptr(), timeout,
+                          stream_of(args[7], c10::cuda::current_device())),
+        "mailbox_consume");
+  return args[5] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[5]);
+  END_HANDLE_TH_ERRORS
+}
+
 PyCFunction fast(PyObject* (*call)(PyObject*, PyObject* const*, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call));
 }
@@ -329,6 +360,7 @@ PyMethodDef methods[] = {{"latent_query", fast(latent_query), METH_FASTCALL, nul
                          {"latent_values", fast(latent_values), METH_FASTCALL, nullptr},
                          {"latent_attend", fast(latent_attend), METH_FASTCALL, nullptr},
                          {"run_adapted", fast(run_adapted), METH_FASTCALL, nullptr},
+                         {"mailbox_consume", fast(mailbox_consume), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
                       nullptr,               nullptr,  nullptr, nullptr};
