@@ -1186,8 +1186,13 @@ constexpr int kMaxDevicesTracked = 64;
 template <int kLatent>
 constexpr uint32_t smem_bytes() {
   static_assert(MXFP8_MAX_LATENT_ROWS <= 65535, "row numbers fit 16 bits");
-  static_assert(Shape<kLatent>::kMisc + sizeof(Misc<Shape<kLatent>::kStages>) <= 232448, "shared memory of a CTA");
-  return Shape<kLatent>::kMisc + sizeof(Misc<Shape<kLatent>::kStages>);
+  constexpr uint32_t kBytes = Shape<kLatent>::kMisc + sizeof(Misc<Shape<kLatent>::kStages>);
+  static_assert(kBytes <= 232448, "shared memory of a CTA");
+  // The pair allocates all of tensor memory, which waits for whoever holds some;
+  // no CTA that in turn waits for another (the projection's clusters ask for a
+  // third of an SM's shared memory) may be on its SM.
+  static_assert(kBytes > 233472 / 3 * 2, "an SM to itself");
+  return kBytes;
 }
 
 // Clusters that run at once on the current device, asked once.
