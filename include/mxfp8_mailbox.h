@@ -542,7 +542,7 @@ size_t mxfp8_latent_workspace_bytes(int32_t latent);
  * row_begin that give rows to several requests (then the rows' results mean
  * nothing), and a wait of the pipeline that runs out raises
  * MXFP8_FLAG_GEMM_TIMEOUT.  A call whose rows, heads and page table could make
- * up 2^31 or more tiles of 128 rows x 64 tokens is MXFP8_ERR_UNSUPPORTED.
+ * up more than 2^30 tiles of 128 rows x 64 tokens is MXFP8_ERR_UNSUPPORTED.
  * Every input is read after the kernel before this one has finished.  workspace:
  * device, 256-byte aligned; calls that share one must be ordered on one
  * stream. */

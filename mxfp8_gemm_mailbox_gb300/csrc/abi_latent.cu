@@ -110,11 +110,11 @@ mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* d, const void* q, cons
     return fail(MXFP8_ERR_INVALID, "pages and table_width must be positive");
   if (static_cast<int64_t>(d->table_width) * d->page_size > INT32_MAX - 128)
     return fail(MXFP8_ERR_UNSUPPORTED, "a page table spans at most 2^31 - 129 tokens");
-  // Token tiles of all row tiles at most (64 tokens, 128 rows), numbered in 32 bits.
+  // Token tiles of all row tiles at most (64 tokens, 128 rows), numbered in 31 bits.
   if ((static_cast<int64_t>(d->rows) * d->heads / 128 + d->requests) *
           ((static_cast<int64_t>(d->table_width) * d->page_size + 63) / 64) >
-      INT32_MAX)
-    return fail(MXFP8_ERR_UNSUPPORTED, "rows x heads x tokens is past 2^31 tiles of 128 x 64");
+      1 << 30)
+    return fail(MXFP8_ERR_UNSUPPORTED, "rows x heads x tokens is past 2^30 tiles of 128 x 64");
   if (d->token_stride < width || d->token_stride % 8 || d->page_stride % 8 ||
       (d->pages > 1 && d->page_stride < width))
     return fail(MXFP8_ERR_UNSUPPORTED,

@@ -241,6 +241,35 @@ __device__ __forceinline__ bool finite_bf16(uint4 v) {
   return finite;
 }
 
+// Divisions, which stand in the way of a call's first copies (a 32-bit one by a
+// variable is some 200 clocks).  By a number that the host knows, of n < 2^31:
+struct Divisor {
+  uint32_t magic;  // ceil(2^shift / d)
+  int32_t shift;   // 31 + ceil(log2 d): the quotient's error n (magic d - 2^shift) / (d 2^shift)
+                   // stays below 1 / d
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(n)) * magic >> shift);
+  }
+};
+Divisor divisor_of(int d) {
+  int log = 0;
+  while ((int64_t{1} << log) < d) ++log;
+  const uint64_t power = uint64_t{1} << (31 + log);
+  return {static_cast<uint32_t>((power + d - 1) / d), 31 + log};
+}
+// By a variable: the approximate quotient (2 units in the last place) of n < 2^21
+// is off by one at most.
+__device__ __forceinline__ uint32_t quotient(uint32_t n, uint32_t d) {
+  if (n >= 1u << 21) return n / d;
+  uint32_t q = static_cast<uint32_t>(__fdividef(static_cast<float>(n), static_cast<float>(d)));
+  const int32_t rest = static_cast<int32_t>(n - q * d);
+  if (rest < 0)
+    --q;
+  else if (rest >= static_cast<int32_t>(d))
+    ++q;
+  return q;
+}
+
 __device__ __forceinline__ int drafts_of(const Lists& l, int b) {
   return max(l.begin[b + 1] - l.begin[b], 0);
 }
@@ -272,16 +301,16 @@ __device__ __forceinline__ Next segment_at(const Lists& l, int requests, int hea
   if (l.piece > 0) {
     // At most as many pieces as clusters, so the products stay below 2^32.
     const uint32_t kv = s.kv_tiles, piece = l.piece;
-    const uint32_t pieces = (kv + piece - 1) / piece;
-    tile = local / pieces;
+    const uint32_t pieces = quotient(kv + piece - 1, piece);
+    tile = quotient(local, pieces);
     const uint32_t k = local - tile * pieces;
-    s.kv0 = kv * k / pieces;
-    s.kv1 = kv * (k + 1) / pieces;
+    s.kv0 = quotient(kv * k, pieces);
+    s.kv1 = quotient(kv * (k + 1), pieces);
     s.slot = 2 * cluster;
     ++w.at;
   } else {
     const uint32_t kv = s.kv_tiles;
-    tile = local / kv;
+    tile = quotient(local, kv);
     s.kv0 = local - tile * kv;
     s.kv1 = min(s.kv_tiles, s.kv0 + static_cast<int>(w.end - w.at));
     // Only a share's first and last row tiles can be cut.
@@ -353,6 +382,8 @@ struct AttendParams {
   LatentParams in;
   int32_t clusters;
   int32_t box;        // tokens of a TMA box: the largest of 32, 16, 8 in a page
+  int32_t box_log2;
+  Divisor by_page, by_clusters;  // page_size, clusters
   float4* partial;    // [2 clusters][latent / 4][128 rows] x 4 columns
   float2* stats;      // [2 clusters][128 rows] (reference, sum)
   Cut* cuts;          // [clusters]
@@ -364,8 +395,8 @@ struct AttendMaps {
 };
 
 // Token tiles of a cluster's run in an even deal.
-__device__ __forceinline__ uint32_t run_length(uint32_t tiles, int clusters) {
-  return max(static_cast<uint32_t>(kMinRun), (tiles + clusters - 1) / clusters);
+__device__ __forceinline__ uint32_t run_length(uint32_t tiles, const AttendParams& ap) {
+  return max(kMinRun, ap.by_clusters(tiles + ap.clusters - 1));
 }
 
 // The deal, by one warp.  (The host has checked that all token tiles number
@@ -401,12 +432,12 @@ __device__ __forceinline__ void deal(Lists& l, const AttendParams& ap, int clust
   // pieces fit the clusters, one a cluster; a lane a length and every fourth
   // request.
   static_assert(kPieceSlack < 8, "");
-  const uint32_t run = run_length(all, ap.clusters), slack = lane % 8;
+  const uint32_t run = run_length(all, ap), slack = lane % 8;
   uint32_t piece = 0;
   if (tiles <= ap.clusters) {
     uint32_t pieces = 0;
     for (int b = lane / 8; b < p.requests; b += 4)
-      pieces += row_tiles_of(b) * ((token_tiles(l.length[b]) + run + slack - 1) / (run + slack));
+      pieces += row_tiles_of(b) * quotient(token_tiles(l.length[b]) + run + slack - 1, run + slack);
     pieces += __shfl_xor_sync(~0u, pieces, 8);
     pieces += __shfl_xor_sync(~0u, pieces, 16);
     const uint32_t fits = __ballot_sync(
@@ -419,7 +450,7 @@ __device__ __forceinline__ void deal(Lists& l, const AttendParams& ap, int clust
     uint32_t runs = 0;
     if (b < p.requests) {
       const uint32_t tt = token_tiles(l.length[b]);
-      runs = row_tiles_of(b) * (piece > 0 ? (tt + piece - 1) / piece : tt);
+      runs = row_tiles_of(b) * (piece > 0 ? quotient(tt + piece - 1, piece) : tt);
     }
     for (int o = 1; o < 32; o *= 2) {
       const uint32_t v = __shfl_up_sync(~0u, runs, o);
@@ -524,8 +555,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   // copy fills zeros) for a box past the length.
   auto read_page = [&](int token) {
     if (token >= seg.length) return p.pages;
-    return p.table[static_cast<size_t>(seg.b) * p.table_width + token / p.page_size];
+    return p.table[static_cast<size_t>(seg.b) * p.table_width + ap.by_page(token)];
   };
+
+  auto slot_of = [&](int token) { return token - ap.by_page(token) * p.page_size; };
 
   if (warp == 0 || warp == 3) {
     // -------------------------------------------------------------- producer
@@ -539,11 +572,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     // warp's tiles ahead.
     const int which = warp == 3;
     constexpr int kItems = (kCtaTokens / kMinBox * (L::kBlocks + 1) + 31) / 32;  // of a lane
-    const int blocks = ap.box == kCtaTokens ? 1 : L::kBlocks + 1;  // copies of a box
-    const int items = kCtaTokens / ap.box * blocks;
+    const bool whole = ap.box == kCtaTokens;
+    const int items = whole ? 1 : (kCtaTokens >> ap.box_log2) * (L::kBlocks + 1);
+    auto box_of = [&](int i) { return whole ? 0 : i / (L::kBlocks + 1) << ap.box_log2; };
     // The first token of copy i of this CTA's part of tile kv.
     auto token_of = [&](int kv, int i) {
-      return kv * kTokens + static_cast<int>(rank) * kCtaTokens + i / blocks * ap.box;
+      return kv * kTokens + static_cast<int>(rank) * kCtaTokens + box_of(i);
     };
     auto page_of = [&](int kv, int i) {
       return kv < seg.kv1 && i < items ? read_page(token_of(kv, i)) : p.pages;
@@ -588,14 +622,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         for (int k = 0; k < kItems; ++k) {
           const int i = lane + 32 * k;
           if (i >= items) continue;
-          const int block = i % blocks, at = i / blocks * ap.box;
+          const int block = whole ? 0 : i % (L::kBlocks + 1), at = box_of(i);
           const int token = token_of(kv, i);
           if (page[k] < 0 || page[k] >= p.pages) {
             if (token < seg.length) raise(p.flags, MXFP8_FLAG_BAD_INDEX);
             page[k] = p.pages;
           }
           ptx::tma_load_4d(dst + block * kBlockBytes + at * 128, &maps.keys, 0,
-                           token % p.page_size, block, page[k], full);
+                           slot_of(token), block, page[k], full);
         }
         __syncwarp();
 #pragma unroll
@@ -613,11 +647,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     begin();
     // This CTA's value columns of the peer's tokens, over the blocks of its own
     // tokens that only the keys' product reads.
-    const int blocks = ap.box == kCtaTokens ? 1 : L::kHalf;  // copies of a box
-    const int items = kCtaTokens / ap.box * blocks;          // at most 16
+    const bool whole = ap.box == kCtaTokens;
+    const int items = whole ? 1 : (kCtaTokens >> ap.box_log2) * L::kHalf;  // at most 16
+    const int block = whole ? 0 : lane % L::kHalf;
+    const int at = whole ? 0 : lane / L::kHalf << ap.box_log2;
     const int column0 = static_cast<int>(rank) * L::kHalf, theirs = static_cast<int>(rank ^ 1u);
     auto token_of = [&](int kv) {
-      return kv * kTokens + theirs * kCtaTokens + lane / blocks * ap.box;
+      return kv * kTokens + theirs * kCtaTokens + at;
     };
     auto page_of = [&](int kv) {
       return kv < seg.kv1 && lane < items ? read_page(token_of(kv)) : p.pages;
@@ -646,11 +682,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         if (lane == 0) ptx::mbar_arrive_expect_tx(done, L::kHalf * kBlockBytes);
         __syncwarp();
         if (lane < items) {
-          const int block = lane % blocks, at = lane / blocks * ap.box;
           if (page < 0 || page >= p.pages) page = p.pages;
           ptx::tma_load_4d(sbase + r % kStages * L::kPlaceBytes +
                                (theirs * L::kHalf + block) * kBlockBytes + at * 128,
-                           &maps.values, 0, token_of(kv) % p.page_size, column0 + block, page,
+                           &maps.values, 0, slot_of(token_of(kv)), column0 + block, page,
                            done);
         }
         __syncwarp();
@@ -845,7 +880,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           }
           // Boxes past the length came as zeros; the rest of the last one is
           // filled here.
-          fill |= low_ones((n1 + ap.box - 1) / ap.box * ap.box) & ~low_ones(n1);
+          fill |= low_ones((n1 + ap.box - 1) & -ap.box) & ~low_ones(n1);
           const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
           for (int n = lane / 8; n < kTokens; n += 4) {  // 8 lanes a token's row of 128 bytes
             if (!(fill >> n & 1)) continue;
@@ -1090,7 +1125,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
-  ptx::cluster_sync();  // no CTA leaves while its peer may address it
+  // No CTA leaves while its peer may address it.  (Nothing is handed over: a
+  // release would wait for the outputs' stores, 0.5 us.)
+  ptx::cluster_sync_relaxed();
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, 512);
@@ -1267,6 +1304,9 @@ cudaError_t launch_impl(const LatentParams& p, void* workspace, cudaStream_t str
   if (e != cudaSuccess) return e;
   ap.box = kCtaTokens;
   while (p.page_size % ap.box) ap.box /= 2;
+  while (1 << ap.box_log2 < ap.box) ++ap.box_log2;
+  ap.by_page = divisor_of(p.page_size);
+  ap.by_clusters = divisor_of(ap.clusters);
   ap.partial = static_cast<float4*>(workspace);
   ap.stats = reinterpret_cast<float2*>(ap.partial + static_cast<size_t>(2) * kMaxClusters *
                                                         (kLatent / 4) * kTileRows);

@@ -364,6 +364,13 @@ __device__ __forceinline__ void cluster_sync() {
       "barrier.cluster.wait.acquire.aligned;" ::
           : "memory");
 }
+// The same, ordering no memory.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile(
+      "barrier.cluster.arrive.relaxed.aligned;\n\t"
+      "barrier.cluster.wait.aligned;" ::
+          : "memory");
+}
 // The two halves of a cluster barrier, for a wait placed well after the
 // arrival (every thread of every CTA of the cluster arrives once per phase).
 __device__ __forceinline__ void cluster_arrive() {
