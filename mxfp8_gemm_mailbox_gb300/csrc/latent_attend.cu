@@ -45,14 +45,14 @@
 //          holds of the queries.
 //
 // Bounds, measured (latent 512, contexts spread so that none lies in L2):
-//   8 x 64k tokens, 128 heads: 123 us = 4.9 TB/s, 1.19 PFLOP/s; 16 heads 118 us.
+//   8 x 64k tokens, 128 heads: 121 us = 5.0 TB/s, 1.21 PFLOP/s; 16 heads 117 us.
 //     The stream of tokens: 111 us without the values' second fetch, 104
 //     without products either.
-//   8 drafts in a tree on 16k tokens, 128 heads: 40 us = 0.90 PFLOP/s.  29
-//     token tiles of 0.83 us (their products fill 0.65), 5 us before the first
-//     scores, 8 in which 20 MB of partial outputs go to L2 and are joined.
-//   8 x 4k tokens, 128 heads: 27 us, 8 tiles and the same ends.
-//   1 x 100 tokens, 16 heads: 8.8 us, a chain of latencies.
+//   8 drafts in a tree on 16k tokens, 128 heads: 39 us = 0.93 PFLOP/s.  29
+//     token tiles of 0.83 us (their products fill 0.65), 4.5 us before the
+//     first scores, 7 in which 20 MB of partial outputs go to L2 and are joined.
+//   8 x 4k tokens, 128 heads: 26 us, 8 tiles and the same ends.
+//   1 x 100 tokens, 16 heads: 8.3 us, a chain of latencies.
 // Two CTAs that share a row tile by columns and exchange partial scores took
 // 1.3 to 1.5 us a tile (174, 57 and 28.5 us for the first three).
 //
@@ -94,7 +94,8 @@ constexpr float kLazy = 8.0f;
 // tiles a cluster, 129 with even runs of 108).
 constexpr int kPieceSlack = 7;
 // Token tiles of a run at least: four take about as long as the join of two
-// halves (3 x 2.5k tokens, latent 256: 14.0 us, 15.7 with runs of 2).
+// halves (3 x 2.5k tokens, latent 256: 14.0 us, 15.7 with runs of 2; one request
+// of 4k tokens, 128 heads: 16.2 us, 16.7 with 3, 17.6 with 6).
 constexpr int kMinRun = 4;
 constexpr int kMaxClusters = 80;  // whose partials the workspace holds
 constexpr uint32_t kBlockBytes = kCtaTokens * 128;  // 32 tokens x 64 columns
@@ -400,7 +401,7 @@ __device__ __forceinline__ uint32_t run_length(uint32_t tiles, const AttendParam
 }
 
 // The deal, by one warp.  (The host has checked that all token tiles number
-// less than 2^31.)
+// at most 2^30.)
 __device__ __forceinline__ void deal(Lists& l, const AttendParams& ap, int cluster, int lane) {
   const LatentParams& p = ap.in;
   uint32_t all = 0;  // token tiles
