@@ -15,9 +15,11 @@
 // second, one block an SM of 4 warps x 72 registers a thread and next to no
 // shared memory, leaves room for two of the GEMM's blocks and runs under the
 // GEMM's weight stream: both let their dependents launch at once, and the GEMM
-// waits for delta in its epilogue alone.  31.3 us a call (21.3 without adapters;
-// 145 MB are 21.2 us at the copy rate); 32.6 with two blocks of the second an SM,
-// 35 with three (the GEMM's come later), 36 with one block of the first.
+// waits for delta in its epilogue alone.  30.6 us a call (21.2 without adapters;
+// 145 MB are 21.2 us at the copy rate): the GEMM's blocks come when the first
+// kernel's leave.  35 with two or three blocks of the second an SM (they come
+// after the first kernel, and the GEMM's after them), 30.9 with smaller blocks of
+// the first that the GEMM's fit beside.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -127,8 +129,10 @@ constexpr int kDeltaThreads = 128;
 constexpr int kDeltaLoads = 8;  // of a thread, at once
 
 // delta[t][n]: kLanes lanes share a row of B, 16 bytes (8 numbers) each a turn.
-// A block's items are (row t, kDeltaLoads x 128 / kLanes outputs), every
-// gridDim.x.
+// A block's items are (row t, kDeltaLoads x 128 / kLanes outputs), in a row: it
+// gathers the products with A once, for mostly one t.  (Beside the GEMM's weight
+// stream such a round trip takes 2 to 3 us; with every gridDim.x-th item this
+// kernel outlasted the GEMM by 1 us at 8 rows of rank 64.)
 template <int kLanes>
 __global__ void __launch_bounds__(kDeltaThreads, 7)
     adapter_delta_kernel(const __grid_constant__ AdapterParams p) {
@@ -140,7 +144,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 7)
   const int blocks = (p.n + kOutputs - 1) / kOutputs, items = p.m * blocks;
   const int rank8 = (p.rank + 7) & ~7, pieces = pieces_of(p.k);
   int have = -1;  // the row whose products with A are in `inner`
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
+  const int last = (blockIdx.x + 1) * items / gridDim.x;
+  for (int item = blockIdx.x * items / gridDim.x; item < last; ++item) {
     const int t = item / blocks, n0 = item % blocks * kOutputs + tid / kLanes;
     const int i = adapter_of(p, t);
     const int rank = i < 0 ? 0 : rank_of(p, i);

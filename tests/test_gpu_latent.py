@@ -398,3 +398,41 @@ def test_rows_given_twice_are_refused_on_the_device(cuda):
     out = at.run(normal(1, 8, 128, 320), paged.cache, paged.table, paged.lengths, begin, SCALE)
     assert out.shape == (8, 128, 256)
     assert at.status() & mx.FLAG_BAD_INDEX
+
+
+def test_streams_outputs_and_refusals_of_the_calls(cuda):
+    paged = Paged([100], [2], 256, 16)
+    at = mx.LatentAttention(8, 256)
+    q = normal(1, 2, 8, 320)
+    args = (q, paged.cache, paged.table, paged.lengths, paged.begin, SCALE)
+    first = at.run(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = torch.empty_like(first)
+    assert at.run(*args, out=out, stream=side.cuda_stream) is out  # a handle in place of a Stream
+    side.synchronize()
+    assert torch.equal(out, first)
+    with pytest.raises(TypeError):
+        at.run(*args, stream=object())
+    with pytest.raises(TypeError, match="int32"):
+        at.run(q, paged.cache, paged.table, paged.lengths.long(), paged.begin, SCALE)
+    with pytest.raises(ValueError, match="row_begin"):
+        at.run(q, paged.cache, paged.table, paged.lengths, paged.begin[:1], SCALE)
+    with pytest.raises(ValueError, match="contiguous"):
+        at.run(q.transpose(0, 1).contiguous().transpose(0, 1), *args[1:])
+    with pytest.raises(ValueError, match="cache"):
+        at.run(q, paged.cache.transpose(1, 2).contiguous().transpose(1, 2), *args[2:])
+    with pytest.raises(ValueError, match="out"):
+        at.run(*args, out=out[:1])
+    with pytest.raises(mx.Mxfp8Error, match="scale"):
+        at.run(*args[:5], 0.0)
+    w = normal(2, 8, 64, 256)
+    x, scale = mx.latent_values(first, w)
+    x2, scale2 = torch.empty_like(x), torch.empty_like(scale)
+    got = mx.latent_values(first, w, x2, scale2)
+    assert got[0] is x2 and got[1] is scale2
+    assert torch.equal(x.view(torch.uint8), x2.view(torch.uint8))
+    assert torch.equal(scale.view(torch.uint8), scale2.view(torch.uint8))
+    with pytest.raises(TypeError, match="one-byte"):
+        mx.latent_values(first, w, x2.float(), scale2)
+    assert at.status() == 0

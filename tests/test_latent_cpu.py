@@ -117,6 +117,12 @@ def test_binding_refuses_wrong_tensors():
         at.run(z(1, 5, 320), z(2, 8, 320), z(1, 1), z(1), z(2), 1.0)
     with pytest.raises(ValueError, match="CUDA"):
         at.run(z(1, 4, 320), z(2, 8, 320), z(1, 1), z(1), z(2), 1.0)
+    for args in ((1, z(1, 4, 64), z(4, 512, 64)), (z(1, 4, 64), None, z(4, 512, 64)),
+                 (z(1, 4, 64), z(1, 4, 64), "w")):
+        with pytest.raises((TypeError, ValueError)):
+            mx.latent_query(*args)
+    with pytest.raises(TypeError, match="must be a tensor"):
+        mx.latent_values(z(1, 4, 512), [1.0])
     for a, b, error in ((z(2, 8, 64), z(2, 128, 7), ValueError),
                         (z(2, 8, 64), z(1, 128, 8), ValueError),
                         (z(2, 8, 64, dtype=torch.float32), z(2, 128, 8), TypeError),
