@@ -49,8 +49,12 @@
 //     The stream of tokens: 111 us without the values' second fetch, 104
 //     without products either.
 //   8 drafts in a tree on 16k tokens, 128 heads: 39 us = 0.93 PFLOP/s.  29
-//     token tiles of 0.83 us (their products fill 0.65), 4.5 us before the
-//     first scores, 7 in which 20 MB of partial outputs go to L2 and are joined.
+//     token tiles of 0.8 us, 4.5 us before the first scores, 7 in which 20 MB of
+//     partial outputs go to L2 and are joined.  A tile is bound by shared memory:
+//     per CTA 53 KB of tokens come in, the products read 37 + 25 KB (keys, the
+//     queries outside tensor memory) and 32 + 16 KB (values, weights twice), the
+//     softmax writes 8: 171 KB, 1340 of some 1450 clocks at 128 bytes each.  (The
+//     products alone take 1250.)
 //   8 x 4k tokens, 128 heads: 26 us, 8 tiles and the same ends.
 //   1 x 100 tokens, 16 heads: 8.3 us, a chain of latencies.
 // Two CTAs that share a row tile by columns and exchange partial scores took
