@@ -50,11 +50,9 @@
 //     without products either.
 //   8 drafts in a tree on 16k tokens, 128 heads: 39 us = 0.93 PFLOP/s.  29
 //     token tiles of 0.8 us, 4.5 us before the first scores, 7 in which 20 MB of
-//     partial outputs go to L2 and are joined.  A tile is bound by shared memory:
-//     per CTA 53 KB of tokens come in, the products read 37 + 25 KB (keys, the
-//     queries outside tensor memory) and 32 + 16 KB (values, weights twice), the
-//     softmax writes 8: 171 KB, 1340 of some 1450 clocks at 128 bytes each.  (The
-//     products alone take 1250.)
+//     partial outputs go to L2 and are joined.  The products fill 1250 of a
+//     tile's 1450 clocks: 24 of the scores' at 18 and 12 at 25 (these read their
+//     queries from shared memory, 128 bytes a clock), 8 of the outputs' at 64.
 //   8 x 4k tokens, 128 heads: 26 us, 8 tiles and the same ends.
 //   1 x 100 tokens, 16 heads: 8.3 us, a chain of latencies.
 // Two CTAs that share a row tile by columns and exchange partial scores took
