@@ -640,6 +640,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       }
       r = r0 + seg.kv1;
     }
+    // The first CTA's last release of each place has landed.
+    for (int i = max(0, r - kStages); ok && i < r; ++i)
+      if ((i & 1) == which) ok = __all_sync(~0u, wait(m.kv_empty[i % kStages], i / kStages));
     // Copies in flight land before the CTA leaves: each was waited for by the
     // mender, which passes every place, unless a wait ran out.
     for (int i = max(0, r - kStages); !ok && i < r; ++i)
@@ -754,10 +757,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         __syncwarp();
       }
     }
-    if (rank == 0) {  // nothing runs on when tensor memory is freed
+    if (rank == 0) {
+      // The softmax warps' last arrivals, which no product waits for.
+      for (int i = max(0, j - 2); ok && i < j; ++i)
+        ok = __all_sync(~0u, wait(m.s_free[i & 1], i >> 1));
       if (ptx::elect_one()) ptx::mma_commit_pair(bar(m.drained[0]));
-      __syncwarp();
-      ptx::mbar_wait(bar(m.drained[0]), 0, kWaitLimitNs);
     }
   } else if (warp == kOutputWarp) {
     // -------------------------------------------------------- outputs' issuer
@@ -811,11 +815,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         __syncwarp();
       }
     }
-    if (rank == 0) {
-      if (ptx::elect_one()) ptx::mma_commit_pair(bar(m.drained[1]));
-      __syncwarp();
-      ptx::mbar_wait(bar(m.drained[1]), 0, kWaitLimitNs);
-    }
+    if (rank == 0 && ptx::elect_one()) ptx::mma_commit_pair(bar(m.drained[1]));
   } else if (warp == 2) {
     // ---------------------------------------------------------- keys' mender
     begin();
@@ -1128,8 +1128,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
   __syncwarp();
   ptx::tc_fence_before();
   __syncthreads();
-  // No CTA leaves while its peer may address it.  (Nothing is handed over: a
-  // release would wait for the outputs' stores, 0.5 us.)
+  // Nothing runs on when tensor memory is freed, and no CTA leaves while its peer
+  // may address it: each waits here for the issuers' last commits, which arrive
+  // on both CTAs' barriers and are not shown to have reached the second one by
+  // what the first one sees; every other arrival from the peer a role has waited
+  // for.  (Nothing is handed over by the cluster's barrier: a release would wait
+  // for the outputs' stores, 0.5 us.)
+  if (warp == 1) {
+    ptx::mbar_wait(bar(m.drained[0]), 0, kWaitLimitNs);
+    ptx::mbar_wait(bar(m.drained[1]), 0, kWaitLimitNs);
+  }
+  __syncwarp();
   ptx::cluster_sync_relaxed();
   if (warp == 1) {
     ptx::tc_fence_after();

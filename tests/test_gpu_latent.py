@@ -436,3 +436,34 @@ def test_streams_outputs_and_refusals_of_the_calls(cuda):
     with pytest.raises(TypeError, match="one-byte"):
         mx.latent_values(first, w, x2.float(), scale2)
     assert at.status() == 0
+
+
+def test_calls_in_a_row_share_the_sms_with_the_projections_clusters(cuda):
+    """The next kernels' CTAs take an SM as soon as one of a pair has left it: nothing of the
+    pair may still be on its way to that shared memory."""
+    paged = Paged([900, 130], [3, 1], 512, 64)
+    at, q = mx.LatentAttention(64), normal(1, 4, 64, 576)
+    narrow = Paged([300], [2], 256, 32, seed=3)
+    at2, q2 = mx.LatentAttention(16, 256), normal(2, 2, 16, 320)
+    n, k = 4096, 1024
+    mailbox = mx.Mailbox(8, n)
+    gemm = mx.PublishGemm(torch.randint(0, 0x78, (n, k), dtype=torch.uint8, device="cuda"),
+                          torch.full((n, k // 32), 120, dtype=torch.uint8, device="cuda"), mailbox,
+                          split_k=4)
+    x = torch.randint(0, 0x78, (8, k), dtype=torch.uint8, device="cuda")
+    xs = torch.full((8, k // 32), 120, dtype=torch.uint8, device="cuda")
+
+    def step():
+        a = at.run(q, paged.cache, paged.table, paged.lengths, paged.begin, SCALE)
+        gemm.run(x, xs)
+        b = mailbox.consume(8)
+        return a, b, at2.run(q2, narrow.cache, narrow.table, narrow.lengths, narrow.begin, SCALE)
+
+    first = step()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        for got, want in zip(step(), first):
+            differ += (got.view(torch.int16) != want.view(torch.int16)).sum()
+    assert differ.item() == 0
+    close(first[0], *paged.expected(q, SCALE))
+    assert at.status() == 0 and at2.status() == 0 and mailbox.status()[0] == mx.OK
