@@ -527,7 +527,8 @@ size_t mxfp8_latent_workspace_bytes(int32_t latent);
 
 /* out [rows][heads][latent] BF16 of q [rows][heads][latent + 64] BF16 over
  * cache [pages][page_size][latent + 64] BF16 (strided; page_table
- * int32[requests][table_width] names each request's pages in order).  Request
+ * int32[requests][table_width] names each request's pages in order), all three
+ * 16-byte aligned (tree 8, the int32 inputs 4).  Request
  * b's query rows are row_begin[b] .. row_begin[b + 1] - 1 (ascending; a row in
  * no request gives zeros) and its tokens 0 .. lengths[b] - 1, of which the last
  * T = row_begin[b + 1] - row_begin[b] are the rows' own, the drafts.  Every row sees

@@ -1085,6 +1085,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       all_added(tiles);
       ptx::tc_fence_after();
       const bool whole = seg.kv0 == 0 && seg.kv1 == seg.kv_tiles;
+      const bool sectors = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
       const int lane_column = group * (L::kColumns / 2);
       const int column0 = half * L::kColumns + lane_column;
       const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
@@ -1105,7 +1106,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             for (int q = 0; q < 8; ++q)
               w[q] = pack_bf16(__uint_as_float(v[16 * i + 2 * q]) * inverse,
                                __uint_as_float(v[16 * i + 2 * q + 1]) * inverse);
-            ptx::st_v8(out + 16 * i, w);
+            // A sector at once where the output begins on one (rows and columns
+            // keep to it), which the C interface does not ask for.
+            if (sectors) {
+              ptx::st_v8(out + 16 * i, w);
+            } else {
+              uint4* chunk = reinterpret_cast<uint4*>(out + 16 * i);
+              chunk[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              chunk[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         } else {
           float4* part = ap.partial +

@@ -467,3 +467,22 @@ def test_calls_in_a_row_share_the_sms_with_the_projections_clusters(cuda):
     assert differ.item() == 0
     close(first[0], *paged.expected(q, SCALE))
     assert at.status() == 0 and at2.status() == 0 and mailbox.status()[0] == mx.OK
+
+
+@pytest.mark.parametrize("latent", [256, 512])
+@pytest.mark.parametrize("offset", [8, 16, 24])
+def test_outputs_on_any_16_byte_boundary(cuda, latent, offset):
+    # Uncut row tiles (a short table), cut ones, and rows of zeros.
+    for contexts, heads in (([60, 0, 200], 40), ([9000, 30], 70)):
+        drafts = [2, 0, 1][:len(contexts)]
+        paged = Paged(contexts, drafts, latent, 16, seed=offset)
+        at, q = mx.LatentAttention(heads, latent), normal(5, paged.rows + 1, heads, latent + ROPE)
+        args = (paged.cache, paged.table, paged.lengths, paged.begin, SCALE)
+        want = at.run(q, *args)
+        pool = torch.full((want.numel() + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = pool[offset:offset + want.numel()].view(want.shape)
+        assert out.data_ptr() % 32 == offset * 2 % 32
+        at.run(q, *args, out=out)
+        assert torch.equal(out, want) and (want[-1] == 0).all()
+        assert (pool[:offset] == 7).all() and (pool[offset + want.numel():] == 7).all()
+        assert at.status() == 0
