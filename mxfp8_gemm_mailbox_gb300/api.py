@@ -31,6 +31,19 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """An output, of the call's stream's own memory.  (From the current stream's, it could be a
+    block that work queued there still reads.)"""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        # 0 and 1 are the legacy default stream.
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _synchronize(stream, device) -> None:
     """Waits for the work issued so far on ``stream`` (as ``_stream`` reads it)."""
     if stream is None:
@@ -324,9 +337,9 @@ class LamportGather:
 
     def __call__(self, inp: torch.Tensor, out: torch.Tensor | None = None, timeout_ns: int = 0,
                  stream=None) -> torch.Tensor:
-        if out is None:
-            out = torch.empty_like(inp)
         _on_device(inp, "inp")
+        if out is None:
+            out = _empty(inp.shape, inp.dtype, inp.device, stream)
         _on_device(out, "out")
         if out.nbytes < inp.nbytes:
             raise ValueError(f"out holds {out.nbytes} bytes, fewer than the input's {inp.nbytes}")
@@ -367,7 +380,7 @@ class TaggedMailbox:
     def consume(self, m: int, tag: int, out: torch.Tensor | None = None, timeout_ns: int = 0,
                 stream=None) -> torch.Tensor:
         if out is None:
-            out = torch.empty((m, self.n), dtype=torch.bfloat16, device=self.pairs.device)
+            out = _empty((m, self.n), torch.bfloat16, self.pairs.device, stream)
         _halves(out, "out", m, self.n)
         check(_lib.load().tagged_consume(_ptr(self.pairs), self.capacity, self.n, m, tag,
                                          _ptr(out), timeout_ns, _ptr(self.flags),

@@ -7,6 +7,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -100,8 +101,7 @@ at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType dtype, int device) {
   return at::empty(shape,
                    at::TensorOptions().dtype(dtype).device(at::Device(at::kCUDA, device)));
 }
-void* stream_of(PyObject* s, int device) {
-  if (s == Py_None) return c10::cuda::getCurrentCUDAStream(device).stream();
+void* handle_of(PyObject* s) {
   THPObjectPtr handle(PyObject_GetAttrString(s, "cuda_stream"));
   if (!handle) {
     PyErr_Clear();
@@ -112,6 +112,30 @@ void* stream_of(PyObject* s, int device) {
   if (PyErr_Occurred()) throw python_error();
   return p;
 }
+// A call's stream, which is torch's current one while this lives: an output made
+// here is that stream's memory.  (From the current stream's, it could be a block
+// that work queued there still reads, and on its release be given to work there
+// before the kernel has written it.)
+class CallStream {
+ public:
+  CallStream(PyObject* s, int device) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device);
+    handle_ = current.stream();
+    if (s == Py_None) return;
+    handle_ = static_cast<cudaStream_t>(handle_of(s));
+    if (handle_ == current.stream()) return;
+    // (Torch's default stream is the legacy one; its numbers of streams hold odd
+    // values for others than handles.)
+    guard_.reset_stream(handle_ == nullptr || handle_ == cudaStreamLegacy
+                            ? c10::cuda::getDefaultCUDAStream(device)
+                            : c10::cuda::getStreamFromExternal(handle_, device));
+  }
+  operator void*() const { return handle_; }
+
+ private:
+  cudaStream_t handle_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 int64_t integer(PyObject* o) {
   const int64_t v = PyLong_AsLongLong(o);
   if (v == -1 && PyErr_Occurred()) throw python_error();
@@ -166,6 +190,7 @@ PyObject* latent_query(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const int32_t rows = rows_of(q, "q_nope");
   expect(q, "q_nope", at::kBFloat16, {rows, heads, nope}, device);
   expect(rope, "q_rope", at::kBFloat16, {rows, heads, kRope}, device);
+  const CallStream stream(args[4], device);
   at::Tensor out;
   if (args[3] == Py_None) {
     out = new_tensor({rows, heads, latent + kRope}, at::kBFloat16, device);
@@ -175,7 +200,7 @@ PyObject* latent_query(PyObject*, PyObject* const* args, Py_ssize_t n) {
   }
   check(mxfp8_latent_query(q.data_ptr(), rope.data_ptr(), w.data_ptr(), out.data_ptr(), rows,
                            static_cast<int32_t>(heads), static_cast<int32_t>(nope),
-                           static_cast<int32_t>(latent), stream_of(args[4], device)),
+                           static_cast<int32_t>(latent), stream),
         "mxfp8_latent_query");
   return args[3] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[3]);
   END_HANDLE_TH_ERRORS
@@ -191,6 +216,7 @@ PyObject* latent_values(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const at::Tensor& o = tensor(args[0], "o");
   const int32_t rows = rows_of(o, "o");
   expect(o, "o", at::kBFloat16, {rows, heads, latent}, device);
+  const CallStream stream(args[4], device);
   auto result = [&](PyObject* t, const char* name, at::ScalarType dtype, int64_t cols) {
     if (t == Py_None) return new_tensor({rows, cols}, dtype, device);
     const at::Tensor& x = tensor(t, name);
@@ -202,7 +228,7 @@ PyObject* latent_values(PyObject*, PyObject* const* args, Py_ssize_t n) {
   at::Tensor scale = result(args[3], "x_scale", at::kFloat8_e8m0fnu, k / 32);
   check(mxfp8_latent_values(o.data_ptr(), w.data_ptr(), x.data_ptr(), scale.data_ptr(), rows,
                             static_cast<int32_t>(heads), static_cast<int32_t>(latent),
-                            static_cast<int32_t>(value), stream_of(args[4], device)),
+                            static_cast<int32_t>(value), stream),
         "mxfp8_latent_values");
   THPObjectPtr a(args[2] == Py_None ? THPVariable_Wrap(std::move(x)) : given(args[2]));
   THPObjectPtr b(args[3] == Py_None ? THPVariable_Wrap(std::move(scale)) : given(args[3]));
@@ -255,6 +281,7 @@ PyObject* latent_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (rows > limit || requests > limit || cache.size(0) > limit || cache.size(1) > limit ||
       table.size(1) > limit)
     refuse(PyExc_ValueError, "a size is past 2^31 - 1");
+  const CallStream stream(args[13], device);
   at::Tensor out;
   if (args[12] == Py_None) {
     out = new_tensor({rows, heads, latent}, at::kBFloat16, device);
@@ -281,7 +308,7 @@ PyObject* latent_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
                             static_cast<const int64_t*>(masks), out.data_ptr(),
                             workspace.data_ptr(), static_cast<size_t>(integer(args[3])),
                             static_cast<int32_t*>(tensor(args[4], "flags").data_ptr()),
-                            stream_of(args[13], device)),
+                            stream),
         "mxfp8_latent_attend");
   return args[12] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[12]);
   END_HANDLE_TH_ERRORS
@@ -321,7 +348,7 @@ PyObject* run_adapted(PyObject*, PyObject* const* args, Py_ssize_t n) {
             static_cast<const float*>(alpha),
             static_cast<const mxfp8_adapters*>(address(args[3])),
             static_cast<const int32_t*>(which.data_ptr()), address(args[4]),
-            static_cast<size_t>(integer(args[5])), c, stream_of(args[11], x.get_device())),
+            static_cast<size_t>(integer(args[5])), c, CallStream(args[11], x.get_device())),
         "mxfp8_publish_gemm_run_adapted");
   return given(args[10]);
   END_HANDLE_TH_ERRORS
@@ -335,6 +362,7 @@ PyObject* mailbox_consume(PyObject*, PyObject* const* args, Py_ssize_t count) {
   const at::Tensor &words = tensor(args[0], "words"), &state = tensor(args[1], "state");
   const int64_t capacity = integer(args[2]), n = integer(args[3]), m = integer(args[4]);
   if (m < INT32_MIN || m > INT32_MAX) refuse(PyExc_ValueError, "m is past 32 bits");
+  const CallStream stream(args[7], c10::cuda::current_device());
   at::Tensor out;
   if (args[5] == Py_None) {
     out = new_tensor({m, n}, at::kBFloat16, gpu_of(words));
@@ -346,8 +374,7 @@ PyObject* mailbox_consume(PyObject*, PyObject* const* args, Py_ssize_t count) {
   if (PyErr_Occurred()) throw python_error();
   check(::mailbox_consume(words.data_ptr(), static_cast<int32_t*>(state.data_ptr()),
                           static_cast<int32_t>(capacity), static_cast<int32_t>(n),
-                          static_cast<int32_t>(m), out.data_ptr(), timeout,
-                          stream_of(args[7], c10::cuda::current_device())),
+                          static_cast<int32_t>(m), out.data_ptr(), timeout, stream),
         "mailbox_consume");
   return args[5] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[5]);
   END_HANDLE_TH_ERRORS

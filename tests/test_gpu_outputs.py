@@ -1,0 +1,84 @@
+"""Outputs that the calls make: they belong to the call's stream."""
+import pytest
+import torch
+
+import mxfp8_gemm_mailbox_gb300 as mx
+from tests.latent_cases import ROPE, Paged, normal
+
+pytestmark = pytest.mark.gpu
+
+
+def _latent():
+    paged = Paged([300, 20], [3, 1], 512, 32)
+    at, q = mx.LatentAttention(32), normal(1, 4, 32, 512 + ROPE)
+    return lambda stream: at.run(q, paged.cache, paged.table, paged.lengths, paged.begin, 0.07,
+                                 stream=stream)
+
+
+def _query():
+    q, rope, w = normal(1, 4, 32, 64), normal(2, 4, 32, ROPE), normal(3, 32, 512, 64)
+    return lambda stream: mx.latent_query(q, rope, w, stream=stream)
+
+
+def _values():
+    o, w = normal(1, 4, 32, 512), normal(2, 32, 128, 512)
+    return lambda stream: mx.latent_values(o, w, stream=stream)[0]
+
+
+def _mailbox():
+    mailbox, c = mx.Mailbox(8, 4096), normal(1, 4, 4096)
+
+    def call(stream):
+        mailbox.publish(c, stream=stream)
+        return mailbox.consume(4, stream=stream)
+    return call
+
+
+def _tagged():
+    mailbox, c = mx.TaggedMailbox(8, 4096), normal(1, 4, 4096)
+
+    def call(stream):
+        mailbox.publish(c, 5, stream=stream)
+        return mailbox.consume(4, 5, stream=stream)
+    return call
+
+
+def _gather():
+    gather, c = mx.LamportGather(1 << 16), normal(1, 4, 4096)
+    return lambda stream: gather(c, stream=stream)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("make", [_latent, _query, _values, _mailbox, _tagged, _gather])
+def test_an_output_is_not_memory_that_the_current_stream_still_reads(cuda, make, handle):
+    call, side = make(), torch.cuda.Stream()
+    want = call(None).clone()
+    torch.cuda.synchronize()
+    before = torch.full_like(want.view(torch.uint8), 7)
+    kept, at = torch.empty_like(before), before.data_ptr()
+    torch.cuda._sleep(20_000_000)  # some 10 ms
+    kept.copy_(before)  # waits behind it
+    del before  # its block is the current stream's next of that size
+    got = call(side.cuda_stream if handle else side)
+    assert got.data_ptr() != at
+    side.synchronize()
+    assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+    torch.cuda.synchronize()
+    assert (kept == 7).all()
+    # And on its release the block is the side stream's, not the current one's.
+    at = got.data_ptr()
+    del got
+    assert torch.empty_like(kept).data_ptr() != at
+    with torch.cuda.stream(side):
+        assert call(None).data_ptr() == at
+
+
+def test_the_default_streams_handles(cuda):
+    call = _query()
+    want = call(None)
+    for handle in (0, 1):  # both the legacy default stream, torch's own
+        assert torch.equal(call(handle), want)
+    call = _tagged()
+    want = call(None)
+    for handle in (0, 1):
+        assert torch.equal(call(handle), want)
