@@ -5,6 +5,7 @@ library's CUDA kernels.  Names follow the C ABI (``include/mxfp8_mailbox.h``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -31,17 +32,16 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """An output, of the call's stream's own memory.  (From the current stream's, it could be a
-    block that work queued there still reads.)"""
+def _memory_of(stream, device):
+    """Within it, new tensors are the call's stream's own memory.  (From the current stream's, a
+    block could be one that work queued there still reads.)"""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return contextlib.nullcontext()
     if not hasattr(stream, "cuda_stream"):
         # 0 and 1 are the legacy default stream.
         stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1
                   else torch.cuda.default_stream(device))
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+    return torch.cuda.stream(stream)
 
 
 def _synchronize(stream, device) -> None:
@@ -98,8 +98,9 @@ class Mailbox:
         device = torch.device(device or "cuda")
         self.capacity = capacity_m
         self.n = n
-        self.words = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
-        self.state = torch.zeros(4, dtype=torch.int32, device=device)
+        with _memory_of(stream, device):
+            self.words = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
+            self.state = torch.zeros(4, dtype=torch.int32, device=device)
         self.init(stream)
 
     def init(self, stream=None) -> None:
@@ -187,7 +188,8 @@ class PublishGemm:
         ws_bytes = lib.mxfp8_publish_gemm_workspace_bytes(ctypes.byref(self.desc))
         if ws_bytes == 0:
             raise ValueError(f"invalid GEMM shape N={n}, K={k}")
-        self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=w.device)
+        with _memory_of(stream, w.device):
+            self.workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=w.device)
         self.w = w
         self.mailbox = mailbox
         self.n, self.k = n, k
@@ -327,8 +329,9 @@ class LamportGather:
             raise ValueError(f"invalid gather capacity {capacity_bytes}")
         device = torch.device(device or "cuda")
         self.capacity = capacity_bytes
-        self.words = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
-        self.state = torch.zeros(4, dtype=torch.int32, device=device)
+        with _memory_of(stream, device):
+            self.words = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
+            self.state = torch.zeros(4, dtype=torch.int32, device=device)
         check(lib.lamport_gather_init(_ptr(self.words), _ptr(self.state), capacity_bytes,
                                       _stream(stream)), "lamport_gather_init")
 
@@ -339,7 +342,8 @@ class LamportGather:
                  stream=None) -> torch.Tensor:
         _on_device(inp, "inp")
         if out is None:
-            out = _empty(inp.shape, inp.dtype, inp.device, stream)
+            with _memory_of(stream, inp.device):
+                out = torch.empty_like(inp)
         _on_device(out, "out")
         if out.nbytes < inp.nbytes:
             raise ValueError(f"out holds {out.nbytes} bytes, fewer than the input's {inp.nbytes}")
@@ -367,8 +371,9 @@ class TaggedMailbox:
             raise ValueError(f"invalid tagged mailbox shape capacity_m={capacity_m}, n={n}")
         device = torch.device(device or "cuda")
         self.capacity, self.n = capacity_m, n
-        self.pairs = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
-        self.flags = torch.zeros(1, dtype=torch.int32, device=device)
+        with _memory_of(stream, device):
+            self.pairs = torch.empty(nbytes // 4, dtype=torch.int32, device=device)
+            self.flags = torch.zeros(1, dtype=torch.int32, device=device)
         check(lib.tagged_mailbox_init(_ptr(self.pairs), capacity_m, n, _stream(stream)),
               "tagged_mailbox_init")
 
@@ -380,7 +385,8 @@ class TaggedMailbox:
     def consume(self, m: int, tag: int, out: torch.Tensor | None = None, timeout_ns: int = 0,
                 stream=None) -> torch.Tensor:
         if out is None:
-            out = _empty((m, self.n), torch.bfloat16, self.pairs.device, stream)
+            with _memory_of(stream, self.pairs.device):
+                out = torch.empty((m, self.n), dtype=torch.bfloat16, device=self.pairs.device)
         _halves(out, "out", m, self.n)
         check(_lib.load().tagged_consume(_ptr(self.pairs), self.capacity, self.n, m, tag,
                                          _ptr(out), timeout_ns, _ptr(self.flags),

@@ -82,3 +82,29 @@ def test_the_default_streams_handles(cuda):
     want = call(None)
     for handle in (0, 1):
         assert torch.equal(call(handle), want)
+
+
+def _weights():
+    w = torch.randint(0, 0x78, (256, 512), dtype=torch.uint8, device="cuda")
+    return w, torch.full((256, 16), 120, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("make,buffer", [
+    (lambda stream: mx.Mailbox(8, 4096, stream=stream), "words"),
+    (lambda stream: mx.TaggedMailbox(8, 4096, stream=stream), "pairs"),
+    (lambda stream: mx.LamportGather(1 << 16, stream=stream), "words"),
+    (lambda stream: mx.PublishGemm(*_weights(), mx.Mailbox(8, 256), stream=stream), "workspace")])
+def test_an_objects_buffers_are_not_memory_that_the_current_stream_still_reads(cuda, make, buffer):
+    side = torch.cuda.Stream()
+    size = getattr(make(None), buffer).nbytes
+    _weights()
+    torch.cuda.synchronize()
+    before = torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+    kept, at = torch.empty_like(before), before.data_ptr()
+    torch.cuda._sleep(20_000_000)
+    kept.copy_(before)
+    del before
+    made = make(side)
+    assert getattr(made, buffer).data_ptr() != at
+    torch.cuda.synchronize()
+    assert (kept == 7).all()
