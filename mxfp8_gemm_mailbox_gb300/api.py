@@ -282,8 +282,10 @@ class Adapters:
     ``b [count][N][rank]`` BF16, with an optional FP32 ``gain [count]`` and each
     adapter's own rank, int32 ``ranks [count]`` (at most ``rank``; what lies
     past it is not used).  The tensors stay borrowed; ``b`` is copied once, its
-    rows padded, where ``rank`` is not a multiple of 8.  The workspace of the
-    calls lives here, so calls with one object are ordered on one stream."""
+    rows padded, where ``rank`` is not a multiple of 8; the constructor waits
+    for that copy.  The workspace of the calls lives here, so calls with one
+    object are ordered on one stream, and the object outlives what they have
+    queued on another stream than the one it was made on."""
 
     def __init__(self, a: torch.Tensor, b: torch.Tensor, gain: torch.Tensor | None = None,
                  ranks: torch.Tensor | None = None):
@@ -308,6 +310,7 @@ class Adapters:
                 _on_device(t, name)
         if self.rank % 8:
             b = torch.nn.functional.pad(b, (0, 8 - self.rank % 8))
+            _synchronize(None, b.device)  # the copy is there for a run on any stream
         self.a, self.b, self.gain, self.ranks = a, b, gain, ranks
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=a.device)
         self.desc = _lib.Adapters(a.data_ptr(), b.data_ptr(),

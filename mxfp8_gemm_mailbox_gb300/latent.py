@@ -40,7 +40,8 @@ class LatentAttention:
     """Attention of ``heads`` query heads over a paged cache of latents.
 
     Holds the workspace and the flags word, so calls on one object are ordered
-    on one stream and made by one host thread at a time."""
+    on one stream and made by one host thread at a time, and the object outlives
+    what they have queued on another stream than the one it was made on."""
 
     def __init__(self, heads: int, latent: int = 512, device=None):
         nbytes = _lib.load().mxfp8_latent_workspace_bytes(latent)

@@ -181,3 +181,22 @@ def test_same_bits_again_and_from_a_graph(cuda):
     torch.cuda.synchronize()
     p.gemm.run(x, xs)
     assert torch.equal(out, p.mailbox.consume(8))
+
+
+def test_a_padded_copy_is_there_for_a_run_on_any_stream(cuda):
+    p = Projection(256, 512)
+    x, xs = codes(1, 3, 512)
+    a, b = normal(2, 2, 12, 512, std=0.05), normal(3, 2, 256, 12)
+    which = torch.tensor([1, 0, 1], dtype=torch.int32, device="cuda")
+    p.gemm.run_adapted(x, xs, mx.Adapters(a, b), which)
+    want = p.mailbox.consume(3)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    junk = torch.full((2, 256, 16), float("nan"), dtype=torch.bfloat16, device="cuda")
+    del junk  # what the copy's block holds before it
+    torch.cuda._sleep(20_000_000)  # the copy waits behind it
+    adapters = mx.Adapters(a, b)
+    p.gemm.run_adapted(x, xs, adapters, which, stream=side)
+    got = p.mailbox.consume(3, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
