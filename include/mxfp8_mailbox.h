@@ -501,8 +501,9 @@ mxfp8_status mxfp8_latent_query(const void* q_nope, const void* q_rope, const vo
  * each head's values (w [heads][value][latent] BF16 times o
  * [rows][heads][latent] BF16, summed in FP32) in MXFP8: a block of 32 takes
  * the smallest power of two under which no element passes 448, then rounds to
- * nearest even (a block of zeros takes 2^0; NaN elements stay NaN and do not
- * count towards a block's scale).  value: a multiple of 32 in 32..512.  w is
+ * nearest even (a block of zeros takes 2^0; NaN elements stay NaN, infinite
+ * ones, which E4M3 has no code for, become NaN, and neither counts towards a
+ * block's scale).  value: a multiple of 32 in 32..512.  w is
  * read before the kernel before this one has finished, as for
  * mxfp8_latent_query; o is read after it has. */
 mxfp8_status mxfp8_latent_values(const void* o, const void* w, void* x, void* x_scale,

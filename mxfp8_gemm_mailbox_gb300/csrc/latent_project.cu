@@ -7,7 +7,8 @@
 //
 // Sums in FP32.  A block's scale is the smallest power of two under which no
 // element passes 448, E4M3's largest, so none saturates; the elements are
-// rounded to nearest, ties to even.
+// rounded to nearest, ties to even.  An element that is not finite is NaN and
+// no part of its block's scale.
 //
 // Few rows against many matrices: bound by reading W once (16.8 MB at 128
 // heads, 512 x 128).  A warp owns 32 outputs of one head and holds their rows
@@ -202,6 +203,12 @@ __global__ void __launch_bounds__(32 * kWarps)
       }
     }
   } else {
+    // An infinity has no E4M3 code, and the conversion would make 448 of it.
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (!isfinite(acc[half][e])) acc[half][e] = __uint_as_float(0x7FC00000u);
     // One scale block is a warp's 32 outputs of a row: its largest magnitude
     // over the lanes of equal q.  (fmaxf passes over NaN.)
 #pragma unroll

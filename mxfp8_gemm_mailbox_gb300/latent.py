@@ -30,9 +30,9 @@ def latent_values(o: torch.Tensor, w: torch.Tensor, x: torch.Tensor | None = Non
                   x_scale: torch.Tensor | None = None, stream=None):
     """(x, x_scale): ``w [heads][value][latent]`` times ``o [rows][heads][latent]``
     in MXFP8, E4M3 elements ``[rows][heads * value]`` and E8M0 scales
-    ``[rows][heads * value / 32]``, which ``PublishGemm.run`` takes.  ``w`` is
-    read before the kernel before this one on the stream has finished, so that
-    kernel must not write it."""
+    ``[rows][heads * value / 32]``, which ``PublishGemm.run`` takes.  What is
+    not finite becomes NaN.  ``w`` is read before the kernel before this one on
+    the stream has finished, so that kernel must not write it."""
     return _lib.calls().latent_values(o, w, x, x_scale, stream)
 
 

@@ -486,3 +486,33 @@ def test_outputs_on_any_16_byte_boundary(cuda, latent, offset):
         assert torch.equal(out, want) and (want[-1] == 0).all()
         assert (pool[:offset] == 7).all() and (pool[offset + want.numel():] == 7).all()
         assert at.status() == 0
+
+
+def test_infinite_values_become_nan(cuda):
+    # An infinity has no E4M3 code: it is NaN, and as little part of its block's scale.
+    w = torch.zeros((2, 64, 256), dtype=torch.bfloat16, device="cuda")
+    w[:, torch.arange(64), torch.arange(64)] = 1.0  # y = o's first 64 numbers
+    o = normal(1, 3, 2, 256)
+    want, want_scale = mx.latent_values(o, w)
+    want, want_scale = want.float(), want_scale.view(torch.uint8)
+    for value in (float("inf"), float("-inf")):
+        w[0, 5, 5], w[1, 40, 7] = value, value  # o[t][0][5] x inf, o[t][1][7] x inf
+        x, scale = mx.latent_values(o, w)
+        v, codes = x.float(), scale.view(torch.uint8)
+        assert torch.isnan(v[:, 5]).all() and torch.isnan(v[:, 64 + 40]).all()
+        # The rest of a block as if that number were not there.
+        rest = o.clone()
+        rest[:, 0, 5] = 0
+        clean = torch.zeros_like(w)
+        clean[:, torch.arange(64), torch.arange(64)] = 1.0
+        clean[1, 40] = 0
+        y, y_scale = mx.latent_values(rest, clean)
+        y, keep = y.float(), torch.ones(128, dtype=torch.bool, device="cuda")
+        keep[[5, 64 + 40]] = False
+        assert torch.equal(v[:, keep], y[:, keep])
+        assert torch.equal(codes, y_scale.view(torch.uint8))
+    # A sum past FP32 is such an infinity too.
+    w.zero_()
+    w[0, 3, :2] = 3e38
+    o[:, 0, :2] = 3.0
+    assert torch.isnan(mx.latent_values(o, w)[0].float()[:, 3]).all()
