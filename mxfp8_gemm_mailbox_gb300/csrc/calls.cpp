@@ -146,6 +146,15 @@ void* address(PyObject* o) {
   if (!p && PyErr_Occurred()) throw python_error();
   return p;
 }
+// `call` without the interpreter's lock: a launch blocks where the GPU's queue is
+// full, and what would empty it may be another thread's to issue.
+template <typename Call>
+mxfp8_status unlocked(Call&& call) {
+  PyThreadState* const state = PyEval_SaveThread();
+  const mxfp8_status status = call();
+  PyEval_RestoreThread(state);
+  return status;
+}
 // What the package raises for a status that is not OK.
 void check(mxfp8_status status, const char* where) {
   if (status == MXFP8_OK) return;
@@ -198,9 +207,13 @@ PyObject* latent_query(PyObject*, PyObject* const* args, Py_ssize_t n) {
     out = tensor(args[3], "out");
     expect(out, "out", at::kBFloat16, {rows, heads, latent + kRope}, device);
   }
-  check(mxfp8_latent_query(q.data_ptr(), rope.data_ptr(), w.data_ptr(), out.data_ptr(), rows,
-                           static_cast<int32_t>(heads), static_cast<int32_t>(nope),
-                           static_cast<int32_t>(latent), stream),
+  const void *const qp = q.data_ptr(), *const rp = rope.data_ptr(), *const wp = w.data_ptr();
+  void* const op = out.data_ptr();
+  check(unlocked([&] {
+          return mxfp8_latent_query(qp, rp, wp, op, rows, static_cast<int32_t>(heads),
+                                    static_cast<int32_t>(nope), static_cast<int32_t>(latent),
+                                    stream);
+        }),
         "mxfp8_latent_query");
   return args[3] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[3]);
   END_HANDLE_TH_ERRORS
@@ -226,9 +239,13 @@ PyObject* latent_values(PyObject*, PyObject* const* args, Py_ssize_t n) {
   };
   at::Tensor x = result(args[2], "x", at::kFloat8_e4m3fn, k);
   at::Tensor scale = result(args[3], "x_scale", at::kFloat8_e8m0fnu, k / 32);
-  check(mxfp8_latent_values(o.data_ptr(), w.data_ptr(), x.data_ptr(), scale.data_ptr(), rows,
-                            static_cast<int32_t>(heads), static_cast<int32_t>(latent),
-                            static_cast<int32_t>(value), stream),
+  const void *const op = o.data_ptr(), *const wp = w.data_ptr();
+  void *const xp = x.data_ptr(), *const sp = scale.data_ptr();
+  check(unlocked([&] {
+          return mxfp8_latent_values(op, wp, xp, sp, rows, static_cast<int32_t>(heads),
+                                     static_cast<int32_t>(latent), static_cast<int32_t>(value),
+                                     stream);
+        }),
         "mxfp8_latent_values");
   THPObjectPtr a(args[2] == Py_None ? THPVariable_Wrap(std::move(x)) : given(args[2]));
   THPObjectPtr b(args[3] == Py_None ? THPVariable_Wrap(std::move(scale)) : given(args[3]));
@@ -301,14 +318,17 @@ PyObject* latent_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                   static_cast<float>(scale),
                                   cache.stride(1),
                                   cache.stride(0)};
-  check(mxfp8_latent_attend(&desc, q.data_ptr(), cache.data_ptr(),
-                            static_cast<const int32_t*>(table.data_ptr()),
-                            static_cast<const int32_t*>(lengths.data_ptr()),
-                            static_cast<const int32_t*>(begin.data_ptr()),
-                            static_cast<const int64_t*>(masks), out.data_ptr(),
-                            workspace.data_ptr(), static_cast<size_t>(integer(args[3])),
-                            static_cast<int32_t*>(tensor(args[4], "flags").data_ptr()),
-                            stream),
+  const void *const qp = q.data_ptr(), *const kp = cache.data_ptr();
+  const auto *const tp = static_cast<const int32_t*>(table.data_ptr()),
+             *const lp = static_cast<const int32_t*>(lengths.data_ptr()),
+             *const bp = static_cast<const int32_t*>(begin.data_ptr());
+  void *const op = out.data_ptr(), *const sp = workspace.data_ptr();
+  const auto bytes = static_cast<size_t>(integer(args[3]));
+  auto* const flags = static_cast<int32_t*>(tensor(args[4], "flags").data_ptr());
+  check(unlocked([&] {
+          return mxfp8_latent_attend(&desc, qp, kp, tp, lp, bp, static_cast<const int64_t*>(masks),
+                                     op, sp, bytes, flags, stream);
+        }),
         "mxfp8_latent_attend");
   return args[12] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[12]);
   END_HANDLE_TH_ERRORS
@@ -342,13 +362,18 @@ PyObject* run_adapted(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                  name_of(which.scalar_type()) + " " + text_of(which.sizes()));
   if (!which.is_cuda() || !which.is_contiguous())
     refuse(PyExc_ValueError, "which must be a contiguous CUDA tensor");
-  check(mxfp8_publish_gemm_run_adapted(
-            static_cast<mxfp8_publish_gemm*>(address(args[0])), x.data_ptr(), scale.data_ptr(),
-            static_cast<int32_t>(std::min<int64_t>(m, INT32_MAX)),
-            static_cast<const float*>(alpha),
-            static_cast<const mxfp8_adapters*>(address(args[3])),
-            static_cast<const int32_t*>(which.data_ptr()), address(args[4]),
-            static_cast<size_t>(integer(args[5])), c, CallStream(args[11], x.get_device())),
+  const CallStream stream(args[11], x.get_device());
+  auto* const gemm = static_cast<mxfp8_publish_gemm*>(address(args[0]));
+  const auto* const adapters = static_cast<const mxfp8_adapters*>(address(args[3]));
+  void* const workspace = address(args[4]);
+  const auto bytes = static_cast<size_t>(integer(args[5]));
+  const void *const xp = x.data_ptr(), *const sp = scale.data_ptr();
+  const auto* const ip = static_cast<const int32_t*>(which.data_ptr());
+  check(unlocked([&] {
+          return mxfp8_publish_gemm_run_adapted(
+              gemm, xp, sp, static_cast<int32_t>(std::min<int64_t>(m, INT32_MAX)),
+              static_cast<const float*>(alpha), adapters, ip, workspace, bytes, c, stream);
+        }),
         "mxfp8_publish_gemm_run_adapted");
   return given(args[10]);
   END_HANDLE_TH_ERRORS
@@ -372,9 +397,12 @@ PyObject* mailbox_consume(PyObject*, PyObject* const* args, Py_ssize_t count) {
   }
   const uint64_t timeout = PyLong_AsUnsignedLongLong(args[6]);
   if (PyErr_Occurred()) throw python_error();
-  check(::mailbox_consume(words.data_ptr(), static_cast<int32_t*>(state.data_ptr()),
-                          static_cast<int32_t>(capacity), static_cast<int32_t>(n),
-                          static_cast<int32_t>(m), out.data_ptr(), timeout, stream),
+  void *const wp = words.data_ptr(), *const op = out.data_ptr();
+  auto* const sp = static_cast<int32_t*>(state.data_ptr());
+  check(unlocked([&] {
+          return ::mailbox_consume(wp, sp, static_cast<int32_t>(capacity), static_cast<int32_t>(n),
+                                   static_cast<int32_t>(m), op, timeout, stream);
+        }),
         "mailbox_consume");
   return args[5] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[5]);
   END_HANDLE_TH_ERRORS

@@ -1,4 +1,7 @@
 """Outputs that the calls make: they belong to the call's stream."""
+import threading
+import time
+
 import pytest
 import torch
 
@@ -108,3 +111,32 @@ def test_an_objects_buffers_are_not_memory_that_the_current_stream_still_reads(c
     assert getattr(made, buffer).data_ptr() != at
     torch.cuda.synchronize()
     assert (kept == 7).all()
+
+
+@pytest.mark.parametrize("make", [_latent, _query, _values])
+def test_other_threads_run_while_a_launch_waits_for_its_turn(cuda, make):
+    """A launch blocks its thread where the GPU's queue is full."""
+    call, gaps, stop = make(), [], threading.Event()
+    call(None)
+    torch.cuda.synchronize()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps.append(now - last)
+            last = now
+
+    thread = threading.Thread(target=tick)
+    thread.start()
+    start = time.perf_counter()
+    torch.cuda._sleep(1_000_000_000)  # some 500 ms
+    for _ in range(3000):
+        call(None)
+    issued = time.perf_counter() - start
+    stop.set()
+    thread.join()
+    torch.cuda.synchronize()
+    assert issued > 0.3, "the queue was never full"
+    assert max(gaps) < 0.15
