@@ -395,7 +395,7 @@ PyObject* mailbox_consume(PyObject*, PyObject* const* args, Py_ssize_t count) {
     out = tensor(args[5], "out");
     halves(out, "out", n, m);
   }
-  const uint64_t timeout = PyLong_AsUnsignedLongLong(args[6]);
+  const uint64_t timeout = PyLong_AsUnsignedLongLongMask(args[6]);  // -1: no limit
   if (PyErr_Occurred()) throw python_error();
   void *const wp = words.data_ptr(), *const op = out.data_ptr();
   auto* const sp = static_cast<int32_t*>(state.data_ptr());

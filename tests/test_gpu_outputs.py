@@ -140,3 +140,11 @@ def test_other_threads_run_while_a_launch_waits_for_its_turn(cuda, make):
     torch.cuda.synchronize()
     assert issued > 0.3, "the queue was never full"
     assert max(gaps) < 0.15
+
+
+def test_a_consume_without_a_limit(cuda):
+    mailbox, c = mx.Mailbox(8, 256), normal(1, 4, 256)
+    for limit in (-1, 2 ** 64 - 1, 0):
+        mailbox.publish(c)
+        assert torch.equal(mailbox.consume(4, timeout_ns=limit), c)
+    assert mailbox.status()[0] == mx.OK
