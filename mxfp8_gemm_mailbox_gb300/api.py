@@ -229,6 +229,8 @@ class PublishGemm:
         """``run`` with C = alpha * (W x); alpha a one-element float32 CUDA tensor."""
         if alpha is not None and (alpha.dtype != torch.float32 or not alpha.is_cuda):
             raise TypeError("alpha must be a float32 CUDA tensor")
+        if alpha is not None and alpha.numel() == 0:  # without an address it would count as none
+            raise ValueError("alpha must hold one number")
         m = self._rows(x, x_scale, c)
         check(_lib.load().mxfp8_publish_gemm_run_scaled(self._handle, _ptr(x), _ptr(x_scale),
                                                         m, _ptr(alpha), _ptr(c),
@@ -301,6 +303,9 @@ class Adapters:
             raise ValueError(f"invalid adapters: count={self.count}, rank={self.rank} (at most "
                              f"{_lib.MAX_ADAPTER_RANK}), N={self.n}, K={self.k}")
         _on_device(a, "a")
+        for t, name in ((b, "b"), (gain, "gain"), (ranks, "ranks")):
+            if t is not None and t.is_cuda and t.device != a.device:
+                raise ValueError(f"{name} is on {t.device}, a on {a.device}")
         _on_device(b, "b")
         for t, name, dtype in ((gain, "gain", torch.float32), (ranks, "ranks", torch.int32)):
             if t is not None:
@@ -317,7 +322,7 @@ class Adapters:
                                   gain.data_ptr() if gain is not None else None,
                                   ranks.data_ptr() if ranks is not None else None,
                                   self.count, self.rank)
-        self._borrowed = (ctypes.addressof(self.desc), self.workspace.data_ptr(), nbytes)
+        self._borrowed = (ctypes.addressof(self.desc), self.workspace, nbytes)
 
 
 class LamportGather:

@@ -335,7 +335,8 @@ PyObject* latent_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
 }
 
 // (handle, n, k, adapters' descriptor, workspace, its bytes, x, x_scale, which, alpha | None,
-//  c | None, stream | None) -> c; the first ones as addresses and numbers.
+//  c | None, stream | None) -> c; the handle and the descriptor as addresses, the workspace, which
+//  is where the adapters are, a tensor.
 PyObject* run_adapted(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   arguments(n, 12);
@@ -348,10 +349,16 @@ PyObject* run_adapted(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const at::Tensor& t = tensor(args[9], "alpha");
     if (t.scalar_type() != at::kFloat || !t.is_cuda())
       refuse(PyExc_TypeError, "alpha must be a float32 CUDA tensor");
+    if (t.numel() != 1)
+      refuse(PyExc_ValueError, "alpha must hold one number, got " + text_of(t.sizes()));
     alpha = t.data_ptr();
   }
   const int64_t m = codes(x, "x", k, 0);
   codes(scale, "x_scale", k / 32, m);
+  const int device = on_current_device(x, "x");
+  const at::Tensor& workspace = tensor(args[4], "workspace");
+  if (gpu_of(workspace) != device)
+    refuse(PyExc_ValueError, "x is on device " + std::to_string(device) + ", the adapters are not");
   if (args[10] != Py_None) {
     const at::Tensor& t = tensor(args[10], "c");
     halves(t, "c", outputs, m);
@@ -362,17 +369,24 @@ PyObject* run_adapted(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                  name_of(which.scalar_type()) + " " + text_of(which.sizes()));
   if (!which.is_cuda() || !which.is_contiguous())
     refuse(PyExc_ValueError, "which must be a contiguous CUDA tensor");
-  const CallStream stream(args[11], x.get_device());
+  for (const int i : {7, 8, 9, 10})
+    if (args[i] != Py_None && gpu_of(THPVariable_Unpack(args[i])) != device)
+      refuse(PyExc_ValueError, std::string(i == 7   ? "x_scale"
+                                           : i == 8 ? "which"
+                                           : i == 9 ? "alpha"
+                                                    : "c") +
+                                   " must be on device " + std::to_string(device));
+  const CallStream stream(args[11], device);
   auto* const gemm = static_cast<mxfp8_publish_gemm*>(address(args[0]));
   const auto* const adapters = static_cast<const mxfp8_adapters*>(address(args[3]));
-  void* const workspace = address(args[4]);
+  void* const space = workspace.data_ptr();
   const auto bytes = static_cast<size_t>(integer(args[5]));
   const void *const xp = x.data_ptr(), *const sp = scale.data_ptr();
   const auto* const ip = static_cast<const int32_t*>(which.data_ptr());
   check(unlocked([&] {
           return mxfp8_publish_gemm_run_adapted(
               gemm, xp, sp, static_cast<int32_t>(std::min<int64_t>(m, INT32_MAX)),
-              static_cast<const float*>(alpha), adapters, ip, workspace, bytes, c, stream);
+              static_cast<const float*>(alpha), adapters, ip, space, bytes, c, stream);
         }),
         "mxfp8_publish_gemm_run_adapted");
   return given(args[10]);

@@ -200,3 +200,37 @@ def test_a_padded_copy_is_there_for_a_run_on_any_stream(cuda):
     got = p.mailbox.consume(3, stream=side)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_refusals_of_the_binding(cuda):
+    p = Projection(256, 512)
+    x, xs = codes(1, 3, 512)
+    adapters = mx.Adapters(normal(2, 2, 8, 512), normal(3, 2, 256, 8))
+    which = torch.zeros(3, dtype=torch.int32, device="cuda")
+    alpha = torch.ones(1, device="cuda")
+    c = torch.empty((3, 256), dtype=torch.bfloat16, device="cuda")
+    run = p.gemm.run_adapted
+    for error, text, args, more in (
+            (ValueError, "CUDA", (x.cpu(), xs, adapters, which), {}),
+            (ValueError, "CUDA", (x, xs.cpu(), adapters, which), {}),
+            (ValueError, "CUDA", (x, xs, adapters, which.cpu()), {}),
+            (ValueError, "which", (x, xs, adapters, which.long()), {}),
+            (ValueError, "which", (x, xs, adapters, which[:2]), {}),
+            (ValueError, "x_scale", (x, xs[:2], adapters, which), {}),
+            (ValueError, r"x must be", (x[:, :256].contiguous(), xs, adapters, which), {}),
+            (TypeError, "one-byte", (x.float(), xs, adapters, which), {}),
+            (TypeError, "alpha", (x, xs, adapters, which), dict(alpha=alpha.cpu())),
+            (TypeError, "alpha", (x, xs, adapters, which), dict(alpha=alpha.double())),
+            (ValueError, "alpha", (x, xs, adapters, which), dict(alpha=alpha[:0])),
+            (ValueError, "alpha", (x, xs, adapters, which), dict(alpha=alpha.repeat(2))),
+            (ValueError, "c must be", (x, xs, adapters, which), dict(c=c[:2])),
+            (TypeError, "two-byte", (x, xs, adapters, which), dict(c=c.float())),
+            (ValueError, "adapters are for",
+             (x, xs, mx.Adapters(normal(2, 2, 8, 256), normal(3, 2, 256, 8)), which), {})):
+        with pytest.raises(error, match=text):
+            run(*args, **more)
+    with pytest.raises(ValueError, match="alpha"):
+        p.gemm.run_scaled(x, xs, alpha[:0])
+    # Nothing was launched: the mailbox still takes a call.
+    run(x, xs, adapters, which, alpha=alpha[0])  # a scalar tensor is one number too
+    assert torch.isfinite(p.mailbox.consume(3)).all() and p.mailbox.status()[0] == mx.OK
