@@ -7,8 +7,8 @@
 //   out = sum_p e_p c_p[0 : latent] / sum_p e_p        over the visible p.
 //
 // Request b has T = row_begin[b+1] - row_begin[b] query rows, its drafts, whose
-// latents are the last T of its lengths[b] tokens.  Every row sees the tokens
-// before them; among the drafts, row t sees draft j iff bit j of tree[t] is
+// latents are the last T of its lengths[b] tokens (of fewer than T, the first
+// drafts have none).  Every row sees the tokens before them; among the drafts, row t sees draft j iff bit j of tree[t] is
 // set (without a tree: iff j <= t).  A row that sees nothing gives zeros.
 // Tokens past the length, and drafts that a row does not see, may hold
 // anything, NaN included; a non-finite number in a draft's latent makes the
@@ -133,7 +133,8 @@ struct Shape {
 // One row tile's run of token tiles inside a cluster's share.
 struct Segment {
   int b, kv0, kv1, kv_tiles;
-  int length, context, drafts, begin;
+  int length, drafts, begin;
+  int context;  // tokens before the drafts; below 0 where the first drafts have no token
   int row0;   // first row of the tile within the request (drafts x heads rows)
   int valid;  // rows of the tile, at most 128
   int slot;   // of its partial outputs
@@ -297,7 +298,7 @@ __device__ __forceinline__ Next segment_at(const Lists& l, int requests, int hea
   s.length = l.length[w.b];
   s.begin = l.begin[w.b];
   s.drafts = drafts_of(l, w.b);
-  s.context = max(s.length - s.drafts, 0);
+  s.context = s.length - s.drafts;
   s.kv_tiles = token_tiles(s.length);
   const uint32_t local = w.at - l.first[w.b];
   int tile;

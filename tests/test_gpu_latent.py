@@ -516,3 +516,27 @@ def test_infinite_values_become_nan(cuda):
     w[0, 3, :2] = 3e38
     o[:, 0, :2] = 3.0
     assert torch.isnan(mx.latent_values(o, w)[0].float()[:, 3]).all()
+
+
+@pytest.mark.parametrize("drafts,length", [(2, 1), (6, 4), (70, 65), (70, 3)])
+def test_fewer_tokens_than_drafts(cuda, drafts, length):
+    # Token p is draft p - (length - drafts): the first drafts have no token.
+    first = drafts - length
+    paged = Paged([0], [drafts], 512, 16)
+    q, heads = normal(7, drafts, 9, 576), 9
+    at = mx.LatentAttention(heads)
+    lengths = torch.full_like(paged.lengths, length)
+    masks = [(0x9E3779B97F4A7C15 * (t + 1)) & (1 << 64) - 1 for t in range(drafts)]
+    for tree in (None, masks):
+        got = at.run(q, paged.cache, paged.table, lengths, paged.begin, SCALE,
+                     tree=None if tree is None else masks_tensor(tree))
+        for t in range(drafts):
+            sees = [p for p in range(length)
+                    if (p + first <= t if tree is None
+                        else p + first < 64 and tree[t] >> (p + first) & 1)]
+            if not sees:
+                assert (got[t] == 0).all()
+                continue
+            mine = paged.tokens[0][torch.tensor(sees, device="cuda")].double()
+            p = torch.softmax(q[t].double() @ mine.t() * SCALE, -1)
+            close(got[t], p @ mine[:, :512], p @ mine[:, :512].abs())
