@@ -86,8 +86,8 @@ constexpr int kValueMender = 13;
 constexpr int kOutputWarp = 14;
 constexpr int kMaxRequests = MXFP8_MAX_REQUESTS;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-// A new maximum moves the reference of a row's exponentials only when it
-// passes it by this many powers of two: the weights then stay below 2^9, far
+// A new maximum moves the reference of a row's exponentials (a score before its
+// scale) only when it passes it by this many powers of two: the weights then stay below 2^9, far
 // inside FP32 and BF16, and the outputs in tensor memory are seldom rescaled.
 constexpr float kLazy = 8.0f;
 // Pieces of one row tile a cluster may be this many token tiles longer than an
@@ -206,9 +206,9 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 2^(from - to) for references from <= to; equal infinities give 1.
-__device__ __forceinline__ float shift_factor(float from, float to) {
-  return from == to ? 1.0f : exp2_approx(from - to);
+// 2^((from - to) scale) for references from <= to; equal infinities give 1.
+__device__ __forceinline__ float shift_factor(float from, float to, float scale) {
+  return from == to ? 1.0f : exp2_approx((from - to) * scale);
 }
 // Pairs of FP32 numbers in one instruction, each as the single one rounds.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -219,12 +219,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
       : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -1020,7 +1020,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         for (int c = 0; c < 4; ++c) tops[c] = fmaxf(tops[c], z[c + 28]);
         // The row's maximum, with the thread of its other tokens; the two
         // decide alike on the row's reference after this tile.
-        float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * p.scale_log2;
+        float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
         float* shared = m.tops[(j >> 1) & 1][group];
         shared[place_of_row] = top;
         asm volatile("bar.sync %0, 64;" ::"r"(3 + group * 2 + quarter % 2) : "memory");
@@ -1030,19 +1030,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           wait(m.decided[(decision - 1) & 1][quarter], (decision - 1) >> 1);
           before = m.reference[(decision - 1) & 1][place_of_row];
         }
-        const float now = top > before + kLazy ? top : before;
+        const float now = (top - before) * p.scale_log2 > kLazy ? top : before;
         m.reference[decision & 1][place_of_row] = now;
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(bar(m.decided[decision & 1][quarter]));
-        total *= shift_factor(base, now);
+        total *= shift_factor(base, now, p.scale_log2);
         base = now;
         const float sub = now == -INFINITY ? 0.0f : now;
         uint32_t w[16];
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        // (The reference in the scores' own units, subtracted before the scale: a
+        // fused z scale - reference would leave of a great score what the
+        // rounding of its product with the scale has left out, past 2^31 more
+        // than the exponential takes.)
         const float2 by = make_float2(p.scale_log2, p.scale_log2), less = make_float2(-sub, -sub);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float2 x = fma2(make_float2(z[2 * c], z[2 * c + 1]), by, less);
+          const float2 x = mul2(add2(make_float2(z[2 * c], z[2 * c + 1]), less), by);
           w[c] = pack_bf16(exp2_approx(x.x), exp2_approx(x.y));
           sum[c % 2] = add2(sum[c % 2], make_float2(__uint_as_float(w[c] << 16),
                                                     __uint_as_float(w[c] & 0xFFFF0000u)));
@@ -1056,7 +1060,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
               make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
         if (i > 0 && __any_sync(~0u, now != before)) {
           // The outputs so far, once the tile before has been added.
-          const float f = shift_factor(before, now);
+          const float f = shift_factor(before, now, p.scale_log2);
           added(j - 1);
           ptx::tc_fence_after();
 #pragma unroll 1
@@ -1080,7 +1084,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       decisions += tiles;
       wait(m.decided[last & 1][quarter], last >> 1);
       const float now = m.reference[last & 1][place_of_row];
-      m.sums[group * 2 + half][row] = total * shift_factor(base, now);
+      m.sums[group * 2 + half][row] = total * shift_factor(base, now, p.scale_log2);
       asm volatile("bar.sync %0, 128;" ::"r"(1 + quarter % 2) : "memory");
       total = (m.sums[0][row] + m.sums[1][row]) + (m.sums[2][row] + m.sums[3][row]);
       all_added(tiles);
@@ -1222,13 +1226,13 @@ __global__ void __launch_bounds__(kJoinThreads, 3)
       float next = top;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) next = fmaxf(next, st[k].x);
-      const float keep = shift_factor(top, next);
+      const float keep = shift_factor(top, next, p.scale_log2);
       top = next;
       total *= keep;
       sum = make_float4(sum.x * keep, sum.y * keep, sum.z * keep, sum.w * keep);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float f = shift_factor(st[k].x, top);
+        const float f = shift_factor(st[k].x, top, p.scale_log2);
         total = fmaf(f, st[k].y, total);
         sum.x = fmaf(f, v[k].x, sum.x), sum.y = fmaf(f, v[k].y, sum.y);
         sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);

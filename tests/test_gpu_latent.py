@@ -540,3 +540,20 @@ def test_fewer_tokens_than_drafts(cuda, drafts, length):
             mine = paged.tokens[0][torch.tensor(sees, device="cuda")].double()
             p = torch.softmax(q[t].double() @ mine.t() * SCALE, -1)
             close(got[t], p @ mine[:, :512], p @ mine[:, :512].abs())
+
+
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 20, 2.0 ** 40])
+@pytest.mark.parametrize("context", [30, 5000])
+def test_scores_far_past_the_exponentials_range(cuda, size, context):
+    # Spreads of 1e5 and more, so that one token has all of the weight: the errors of an FP32
+    # score do not reach the next.
+    def keys(b, n, width):
+        k = normal(8, n, width) * 2.0 ** -9
+        k[:, 0] = torch.randperm(n, generator=torch.Generator().manual_seed(1)).to("cuda") % 256
+        k[(k[:, 0] == 255).nonzero()[1:, 0], 0] = 0.0
+        return k.to(torch.bfloat16)
+
+    paged = Paged([context], [1], 512, 64, keys=keys)
+    q = normal(9, 1, 20, 576) * 2.0 ** -9
+    q[:, :, 0] = torch.where(torch.arange(20, device="cuda") % 2 == 0, size, size * 1.5)
+    attend(cuda, paged, 20, q=q.to(torch.bfloat16), scale=1.0)
