@@ -536,19 +536,19 @@ size_t mxfp8_latent_workspace_bytes(int32_t latent);
  * token p is draft p + T - lengths[b] and the first drafts have none).  Every
  * row sees the tokens before the drafts; row t sees draft j iff bit j of
  * tree[row_begin[b] + t] is set (j < 64), or without a tree (NULL) iff j <= t.
- * A row that sees nothing gives zeros.  What lies in pages past a request's
- * length, or in drafts that a row does not see, has no effect on it, NaN
- * included.  A non-finite number in the latent of a draft makes the rows that
- * see it NaN. lengths, row_begin and page_table are read on the device; a page
- * outside the pool (read as zeros), a length past the table (cut) or rows
- * outside q (cut) raise MXFP8_FLAG_BAD_INDEX in *flags (device int32, may be
- * NULL), as do row_begin that give rows to several requests (then the rows'
- * results mean nothing), and a wait of the pipeline that runs out raises
- * MXFP8_FLAG_GEMM_TIMEOUT.  A call whose rows, heads and page table could make
- * up more than 2^30 tiles of 128 rows x 64 tokens is MXFP8_ERR_UNSUPPORTED.
- * Every input is read after the kernel before this one has finished.
- * workspace: device, 256-byte aligned; calls that share one must be ordered on
- * one stream. */
+ * A row that sees nothing gives zeros, one whose scores are all -infinity NaN.
+ * What lies in pages past a request's length, or in drafts that a row does not
+ * see, has no effect on it, NaN included.  A non-finite number in the latent
+ * of a draft makes the rows that see it NaN. lengths, row_begin and page_table
+ * are read on the device; a page outside the pool (read as zeros), a length
+ * past the table (cut) or rows outside q (cut) raise MXFP8_FLAG_BAD_INDEX in
+ * *flags (device int32, may be NULL), as do row_begin that give rows to
+ * several requests (then the rows' results mean nothing), and a wait of the
+ * pipeline that runs out raises MXFP8_FLAG_GEMM_TIMEOUT.  A call whose rows,
+ * heads and page table could make up more than 2^30 tiles of 128 rows x 64
+ * tokens is MXFP8_ERR_UNSUPPORTED. Every input is read after the kernel before
+ * this one has finished. workspace: device, 256-byte aligned; calls that share
+ * one must be ordered on one stream. */
 mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* desc, const void* q, const void* cache,
                                  const int32_t* page_table, const int32_t* lengths,
                                  const int32_t* row_begin, const int64_t* tree, void* out,

@@ -9,7 +9,8 @@
 // Request b has T = row_begin[b+1] - row_begin[b] query rows, its drafts, whose
 // latents are the last T of its lengths[b] tokens (of fewer than T, the first
 // drafts have none).  Every row sees the tokens before them; among the drafts, row t sees draft j iff bit j of tree[t] is
-// set (without a tree: iff j <= t).  A row that sees nothing gives zeros.
+// set (without a tree: iff j <= t).  A row that sees nothing gives zeros, one whose
+// scores are all -infinity NaN.
 // Tokens past the length, and drafts that a row does not see, may hold
 // anything, NaN included; a non-finite number in a draft's latent makes the
 // rows that see it NaN.
@@ -209,6 +210,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
 // 2^((from - to) scale) for references from <= to; equal infinities give 1.
 __device__ __forceinline__ float shift_factor(float from, float to, float scale) {
   return from == to ? 1.0f : exp2_approx((from - to) * scale);
+}
+// The sum of a row's weights so far where every score that it sees is -infinity:
+// the formula's -infinity + infinity, if none comes that is not.  (A row that
+// sees nothing has 0; a later reference shifts either away.)
+constexpr float kAllInfinite = -1.0f;
+__device__ __forceinline__ float inverse_of(float total) {
+  return total == 0.0f ? 0.0f : total < 0.0f ? NAN : 1.0f / total;
 }
 // Pairs of FP32 numbers in one instruction, each as the single one rounds.
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -993,6 +1001,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         float z[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) z[c] = __uint_as_float(raw[c]);
+        bool any = true;  // of this thread's tokens is visible
         if (special(seg, kv)) {
           const int at = kv * kTokens;
           uint64_t sees;
@@ -1005,6 +1014,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
           }
           sees &= low_ones(seg.length - at);
           const uint32_t bits = static_cast<uint32_t>(sees >> (32 * half));
+          any = bits != 0u;
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (!(bits >> c & 1u)) z[c] = -INFINITY;
@@ -1053,6 +1063,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         }
         sum[0] = add2(sum[0], sum[1]);
         total += sum[0].x + sum[0].y;
+        if (now == -INFINITY && any && total == 0.0f) total = kAllInfinite;
         if (i >= 2) added(j - 2);  // this group's last weights are read
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -1093,7 +1104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
       const bool sectors = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;
       const int lane_column = group * (L::kColumns / 2);
       const int column0 = half * L::kColumns + lane_column;
-      const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
+      const float inverse = inverse_of(total);
       if (!whole && half == 0 && group == 0 && mine)
         ap.stats[seg.slot * kTileRows + tile_row] = make_float2(now, total);
 #pragma unroll 1
@@ -1238,7 +1249,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3)
         sum.z = fmaf(f, v[k].z, sum.z), sum.w = fmaf(f, v[k].w, sum.w);
       }
     }
-    const float inverse = total == 0.0f ? 0.0f : 1.0f / total;
+    const float inverse = inverse_of(total);
     *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(cut.row0) + row) * kLatent + column) =
         make_uint2(pack_bf16(sum.x * inverse, sum.y * inverse),
                    pack_bf16(sum.z * inverse, sum.w * inverse));

@@ -557,3 +557,33 @@ def test_scores_far_past_the_exponentials_range(cuda, size, context):
     q = normal(9, 1, 20, 576) * 2.0 ** -9
     q[:, :, 0] = torch.where(torch.arange(20, device="cuda") % 2 == 0, size, size * 1.5)
     attend(cuda, paged, 20, q=q.to(torch.bfloat16), scale=1.0)
+
+
+@pytest.mark.parametrize("context", [40, 700, 9000])
+def test_scores_of_minus_infinity(cuda, context):
+    # Infinite keys under a positive query: those tokens alone drop out.
+    paged = Paged([context], [2], 512, 32)
+    q = normal(3, 2, 40, 576)
+    q[:, :, 570] = 1.0
+    page = paged.table[0].long()
+    keys = paged.tokens[0].clone()
+    keys[:context * 3 // 4, 570] = float("-inf")
+    for i in range(len(page)):
+        part = keys[i * 32:(i + 1) * 32]
+        paged.cache[page[i], :part.shape[0]] = part
+    paged.tokens[0] = keys
+    attend(cuda, paged, 40, q=q)
+    # Every key: the formula is inf - inf, which must not pass for a row that sees nothing.
+    keys[:, 570] = float("-inf")
+    for i in range(len(page)):
+        part = keys[i * 32:(i + 1) * 32]
+        paged.cache[page[i], :part.shape[0]] = part
+    at = mx.LatentAttention(40)
+    masks = masks_tensor([0, 0b11])
+    got = at.run(q, paged.cache, paged.table, paged.lengths, paged.begin, SCALE, tree=masks)
+    assert torch.isnan(got).all()
+    short = Paged([0], [2], 512, 32)
+    short.cache[short.table[0, 0], :, 570] = float("-inf")
+    got = at.run(q, short.cache, short.table, short.lengths, short.begin, SCALE, tree=masks)
+    assert (got[0] == 0).all() and torch.isnan(got[1]).all()
+    assert at.status() == 0
