@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "even_share.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -144,8 +145,8 @@ __global__ void __launch_bounds__(kDeltaThreads, 7)
   const int blocks = (p.n + kOutputs - 1) / kOutputs, items = p.m * blocks;
   const int rank8 = (p.rank + 7) & ~7, pieces = pieces_of(p.k);
   int have = -1;  // the row whose products with A are in `inner`
-  const int last = (blockIdx.x + 1) * items / gridDim.x;
-  for (int item = blockIdx.x * items / gridDim.x; item < last; ++item) {
+  const EvenShare share = even_share(items, blockIdx.x, gridDim.x);
+  for (int item = share.first; item < share.last; ++item) {
     const int t = item / blocks, n0 = item % blocks * kOutputs + tid / kLanes;
     const int i = adapter_of(p, t);
     const int rank = i < 0 ? 0 : rank_of(p, i);
