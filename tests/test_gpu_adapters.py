@@ -234,3 +234,64 @@ def test_refusals_of_the_binding(cuda):
     # Nothing was launched: the mailbox still takes a call.
     run(x, xs, adapters, which, alpha=alpha[0])  # a scalar tensor is one number too
     assert torch.isfinite(p.mailbox.consume(3)).all() and p.mailbox.status()[0] == mx.OK
+
+
+@pytest.mark.parametrize("n,heads,rank,which,tactic", [
+    (4096, 32, 16, [0], dict(split_k=1)),
+    (1024, 64, 40, [0, 1, 2, 3, -1, 2, 1, 0], dict(split_k=2)),
+    (512, 16, 8, [-1, -1, -1], dict(split_k=4)),
+    (256, 128, 200, [3, 2, 1, 0], dict(fold=4))])
+def test_the_projection_reads_the_activations_made_right_before_it(cuda, n, heads, rank, which,
+                                                                   tactic):
+    """The projection waits for its adapters in its epilogue alone: nothing it reads before that
+    may be of the call before.  Steps in a row with other queries each, through the same x,
+    x_scale, which and alpha, that their kernels write right before the call."""
+    value, latent, rows, steps = 128, 512, len(which), 8
+    p = Projection(n, heads * value, **tactic)
+    wv = normal(1, heads, value, latent, std=latent ** -0.5)
+    outputs = [normal(20 + i, rows, heads, latent) for i in range(steps)]
+    adapters = mx.Adapters(normal(2, 4, rank, p.k, std=p.k ** -0.5), normal(3, 4, n, rank))
+    lists = [torch.tensor(which[i % rows:] + which[:i % rows], dtype=torch.int32, device="cuda")
+             for i in range(steps)]
+    alphas = [torch.full((1,), 0.5 + i, device="cuda") for i in range(steps)]
+    x, xs = mx.latent_values(outputs[0], wv)
+    index, alpha = torch.empty_like(lists[0]), torch.empty_like(alphas[0])
+
+    def step(i, out, wait):
+        index.copy_(lists[i])
+        alpha.copy_(alphas[i])
+        wait()
+        mx.latent_values(outputs[i], wv, x, xs)
+        wait()
+        p.gemm.run_adapted(x, xs, adapters, index, alpha=alpha)
+        wait()
+        p.mailbox.consume(rows, out)
+        wait()
+
+    want = torch.empty((steps, rows, n), dtype=torch.bfloat16, device="cuda")
+    for i in range(steps):
+        step(i, want[i], torch.cuda.synchronize)
+    assert not any(torch.equal(want[i], want[i - 1]) for i in range(1, steps))
+    got = torch.empty_like(want)
+    for _ in range(5):
+        got.fill_(float("nan"))
+        for i in range(steps):
+            step(i, got[i], lambda: None)
+        assert torch.equal(got, want)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        for i in range(steps):
+            step(i, got[i], lambda: None)
+    for turn in range(20):
+        # Other queries at each replay as well.
+        outputs[0].copy_(outputs[1 + turn % (steps - 1)])
+        got.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got[1:], want[1:])
+        first = torch.empty_like(want[0])
+        step(0, first, torch.cuda.synchronize)
+        assert torch.equal(got[0], first)
+    assert p.mailbox.status()[0] == mx.OK
