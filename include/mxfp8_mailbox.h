@@ -488,7 +488,8 @@ mxfp8_status mxfp8_publish_gemm_run_adapted(mxfp8_publish_gemm* gemm, const void
  * (w [heads][latent][nope] BF16 times q_nope [rows][heads][nope] BF16, summed
  * in FP32, rounded once) with q_rope [rows][heads][64] BF16 behind it.  nope:
  * a multiple of 32 in 32..512; latent: 256 or 512; all pointers device,
- * 16-byte aligned.  rows = 0 launches nothing.
+ * 16-byte aligned.  rows = 0 launches nothing.  Made for the projection's few
+ * rows: w is read again for every 8 of them.
  * Launched with programmatic stream serialisation: w is read before the kernel
  * before this one on the stream has finished, so w must not be written by that
  * kernel, nor by one still running when it starts (the rule of
@@ -503,9 +504,10 @@ mxfp8_status mxfp8_latent_query(const void* q_nope, const void* q_rope, const vo
  * the smallest power of two under which no element passes 448, then rounds to
  * nearest even (a block of zeros takes 2^0; NaN elements stay NaN, infinite
  * ones, which E4M3 has no code for, become NaN, and neither counts towards a
- * block's scale).  value: a multiple of 32 in 32..512.  w is
- * read before the kernel before this one has finished, as for
- * mxfp8_latent_query; o is read after it has. */
+ * block's scale).  value: a multiple of 32 in 32..512.  Made for the
+ * projection's few rows: w is read again for every 8 of them.  w is read
+ * before the kernel before this one has finished, as for mxfp8_latent_query; o
+ * is read after it has. */
 mxfp8_status mxfp8_latent_values(const void* o, const void* w, void* x, void* x_scale,
                                  int32_t rows, int32_t heads, int32_t latent, int32_t value,
                                  void* stream);
@@ -523,7 +525,8 @@ typedef struct mxfp8_latent_desc {
   int64_t page_stride;   /* elements between pages: a multiple of 8                        */
 } mxfp8_latent_desc;
 
-/* Workspace bytes of mxfp8_latent_attend; 0 for an unsupported latent. */
+/* Workspace bytes of mxfp8_latent_attend (42 MB for 512, 21 MB for 256, whatever
+ * the call; one serves every layer of a stream); 0 for an unsupported latent. */
 size_t mxfp8_latent_workspace_bytes(int32_t latent);
 
 /* out [rows][heads][latent] BF16 of q [rows][heads][latent + 64] BF16 over
@@ -546,9 +549,10 @@ size_t mxfp8_latent_workspace_bytes(int32_t latent);
  * several requests (then the rows' results mean nothing), and a wait of the
  * pipeline that runs out raises MXFP8_FLAG_GEMM_TIMEOUT.  A call whose rows,
  * heads and page table could make up more than 2^30 tiles of 128 rows x 64
- * tokens is MXFP8_ERR_UNSUPPORTED. Every input is read after the kernel before
- * this one has finished. workspace: device, 256-byte aligned; calls that share
- * one must be ordered on one stream. */
+ * tokens is MXFP8_ERR_UNSUPPORTED. Any number of drafts a request works; the
+ * call is made for a decode step's few against long contexts.  Every input is
+ * read after the kernel before this one has finished. workspace: device,
+ * 256-byte aligned; calls that share one must be ordered on one stream. */
 mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* desc, const void* q, const void* cache,
                                  const int32_t* page_table, const int32_t* lengths,
                                  const int32_t* row_begin, const int64_t* tree, void* out,

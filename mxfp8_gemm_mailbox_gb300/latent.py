@@ -7,7 +7,8 @@ matrix and rounds it to MXFP8, the activations ``PublishGemm`` takes.
 
 A decode step makes these calls once a layer, and the smallest take a few
 microseconds on the GPU, so their checks and outputs are made in the module
-``_calls``.
+``_calls``.  The products are made for the projection's few rows: they read
+their matrices again for every 8 of them.
 """
 from __future__ import annotations
 
@@ -39,9 +40,10 @@ def latent_values(o: torch.Tensor, w: torch.Tensor, x: torch.Tensor | None = Non
 class LatentAttention:
     """Attention of ``heads`` query heads over a paged cache of latents.
 
-    Holds the workspace and the flags word, so calls on one object are ordered
-    on one stream and made by one host thread at a time, and the object outlives
-    what they have queued on another stream than the one it was made on."""
+    Holds the workspace (42 MB at latent 512, 21 MB at 256) and the flags word,
+    so calls on one object are ordered on one stream and made by one host thread
+    at a time, and the object outlives what they have queued on another stream
+    than the one it was made on.  One object serves every layer of a stream."""
 
     def __init__(self, heads: int, latent: int = 512, device=None):
         nbytes = _lib.load().mxfp8_latent_workspace_bytes(latent)
