@@ -3,7 +3,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
+#include <limits>
 
 #include "internal.h"
 
@@ -145,7 +147,11 @@ mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* d, const void* q, cons
   p.table_width = d->table_width;
   p.token_stride = d->token_stride;
   p.page_stride = d->page_stride;
-  p.scale_log2 = static_cast<float>(static_cast<double>(d->scale) * 1.4426950408889634);
+  // Finite still where the product with log2(e) is not: a difference of scores is then
+  // past what the exponential takes either way, and equal ones stay equal.
+  p.scale_log2 = static_cast<float>(
+      std::min(static_cast<double>(d->scale) * 1.4426950408889634,
+               static_cast<double>(std::numeric_limits<float>::max())));
   p.q = static_cast<const uint16_t*>(q);
   p.cache = static_cast<const uint16_t*>(cache);
   p.table = page_table;

@@ -587,3 +587,18 @@ def test_scores_of_minus_infinity(cuda, context):
     got = at.run(q, short.cache, short.table, short.lengths, short.begin, SCALE, tree=masks)
     assert (got[0] == 0).all() and torch.isnan(got[1]).all()
     assert at.status() == 0
+
+
+@pytest.mark.parametrize("scale", [3e38, 1e38, 1e-38, 1e-44])
+def test_the_scale_over_its_whole_range(cuda, scale):
+    # Scores of small integers: exact, with ties, which share the weight at a great scale.
+    def keys(b, n, width):
+        k = torch.zeros((n, width), device="cuda")
+        k[:, 0] = torch.arange(n, device="cuda") % 7 - 3
+        k[:, 1:100] = normal(8, n, 99)
+        return k.to(torch.bfloat16)
+
+    paged = Paged([300, 40], [1, 2], 512, 64, keys=keys)
+    q = torch.zeros((3, 12, 576), dtype=torch.bfloat16, device="cuda")
+    q[:, ::2, 0], q[:, 1::2, 0] = 1.0, -2.0
+    attend(cuda, paged, 12, q=q, scale=scale)
