@@ -20,11 +20,13 @@ def _latent():
 
 def _query():
     q, rope, w = normal(1, 4, 32, 64), normal(2, 4, 32, ROPE), normal(3, 32, 512, 64)
+    torch.cuda.synchronize()  # w may not be written by the kernel right before the call
     return lambda stream: mx.latent_query(q, rope, w, stream=stream)
 
 
 def _values():
     o, w = normal(1, 4, 32, 512), normal(2, 32, 128, 512)
+    torch.cuda.synchronize()  # as above
     return lambda stream: mx.latent_values(o, w, stream=stream)[0]
 
 
