@@ -559,6 +559,135 @@ mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* desc, const void* q, c
                                  void* workspace, size_t workspace_bytes, int32_t* flags,
                                  void* stream);
 
+/* ------------------------------------------------------------------------
+ * A layer of routed experts, what follows the projection in a model that has
+ * them: route, quantize (the tokens' rows, in the experts' order), the experts'
+ * first product with its gate, their second product, combine.  Any number of
+ * tokens, from one of a decode step to a prompt's.  Every call is launched with
+ * programmatic stream serialisation and reads all of its inputs after the kernel
+ * before it has finished.  Element types:
+ * ------------------------------------------------------------------------ */
+#define MXFP8_BF16 0
+#define MXFP8_FP16 1
+#define MXFP8_FP32 2
+/* Formats of matrices: BF16; MXFP8 (E4M3 codes [rows][K], E8M0 codes
+ * [rows][K/32]); MXFP4 (E2M1 codes [rows][K/2], the even element in a byte's low
+ * half, E8M0 codes [rows][K/32]). */
+#define MXFP8_FORMAT_BF16 0
+#define MXFP8_FORMAT_MXFP8 1
+#define MXFP8_FORMAT_MXFP4 2
+#define MXFP8_MAX_EXPERTS 512
+#define MXFP8_MAX_CHOICES 32
+
+/* Workspace bytes of mxfp8_route (0 where it needs none, as for up to 128 tokens;
+ * also for invalid sizes). */
+size_t mxfp8_route_workspace_bytes(int64_t tokens, int32_t experts);
+
+/* Each token's k experts, their weights, and the tokens in the experts' order.
+ *  logits: device, [tokens][experts], `stride` elements between tokens; type
+ *          MXFP8_BF16, _FP16 or _FP32; experts 1..MXFP8_MAX_EXPERTS; k in
+ *          1..min(experts, MXFP8_MAX_CHOICES); tokens x k below 2^31.
+ *  expert: int32 [tokens][k], the indexes of the k largest logits, largest first,
+ *          the lowest index first among equals (NaN counts as the largest);
+ *  weight: FP32 [tokens][k], exp(z - z_max) over the sum of those of the k chosen
+ *          (normalize) or of all experts (not);
+ *  slot:   int32 [tokens][k], the row that this choice has in the experts'
+ *          products: rows are numbered by expert, then by token;
+ *  begin:  int32 [experts + 1], where each expert's rows begin; the last is the
+ *          number of rows;
+ *  row:    int32 [tokens k], the token of each row, -1 from begin[experts] on.
+ * A logit of -infinity is not chosen: such an entry has expert -1, slot -1 and
+ * weight 0 (a token all of whose logits are, a padded one, goes nowhere).
+ * workspace: device, 4-byte aligned, mxfp8_route_workspace_bytes; calls that share
+ * one must be ordered on one stream.  tokens = 0 writes begin alone. */
+mxfp8_status mxfp8_route(const void* logits, int32_t type, int64_t stride, int64_t tokens,
+                         int32_t experts, int32_t k, int32_t normalize, float* weight,
+                         int32_t* expert, int32_t* slot, int32_t* row, int32_t* begin,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* codes and scales (out_rows rows of K) in `format` (MXFP8 or MXFP4) of x
+ * [x_rows][K] (device, `stride` elements between rows, type as above; address
+ * and row stride multiples of 16 bytes).  Output row r is made of row rows[r]
+ * (device int32), or of row r without rows (NULL; then out_rows = x_rows).  An
+ * output row whose index is -1 is left as it was; another index outside x does
+ * the same and raises MXFP8_FLAG_BAD_INDEX in *flags (device int32, may be NULL).
+ * A block of 32 takes the smallest power of two under which no element passes 448
+ * (E4M3) or 6 (E2M1), at least 2^-127; elements are rounded to nearest, ties to
+ * even; a block of zeros takes 2^0.  What is not finite becomes NaN: in MXFP8
+ * that element, which does not count towards its block's scale, in MXFP4, whose
+ * elements have no NaN, its block, by the scale code 255.  K: a multiple of 32;
+ * codes 16-byte aligned; out_rows x K at most 2^35. */
+mxfp8_status mxfp8_quantize(const void* x, int32_t type, int64_t stride, int64_t x_rows, int32_t k,
+                            const int32_t* rows, int64_t out_rows, int32_t format, void* codes,
+                            void* scales, int32_t* flags, void* stream);
+
+/* The values of [rows][K] codes, K a multiple of 32, in `type`: FP32 holds them all;
+ * BF16 and FP16 take them rounded to nearest.  out 16-byte aligned. */
+mxfp8_status mxfp8_dequantize(const void* codes, const void* scales, int64_t rows, int32_t k,
+                              int32_t format, int32_t type, void* out, void* stream);
+
+typedef struct mxfp8_expert_desc {
+  int32_t experts;    /* 1..MXFP8_MAX_EXPERTS                                             */
+  int32_t n;          /* outputs: a multiple of 8; of 32 where gated or rounded to blocks */
+  int32_t k;          /* a multiple of 128                                                */
+  int32_t gated;      /* 1: W holds n gate rows, then n up rows, an expert               */
+  int32_t w_format;   /* MXFP8_FORMAT_MXFP8 or MXFP8_FORMAT_MXFP4                         */
+  int32_t x_format;   /* the same                                                         */
+  int32_t out_format; /* any of the three                                                 */
+  int32_t rows;       /* of x and of the result                                           */
+} mxfp8_expert_desc;
+
+/* Bytes of the matrices' scales as the product reads them; 0 for an invalid shape
+ * (x_format, out_format and rows do not count here). */
+size_t mxfp8_expert_scales_bytes(const mxfp8_expert_desc* desc);
+
+/* laid (device, 16-byte aligned, mxfp8_expert_scales_bytes) = the matrices' scales
+ * (device, 4-byte aligned, E8M0 [experts][n, or 2 n gated][K/32]) in the products'
+ * order; once a set of matrices. */
+mxfp8_status mxfp8_expert_lay_scales(const mxfp8_expert_desc* desc, const void* w_scale, void* laid,
+                                     void* stream);
+
+/* Workspace bytes of the product, whatever the call: 21 MB. */
+size_t mxfp8_expert_workspace_bytes(void);
+#define MXFP8_EXPERT_WORKSPACE_ZEROS 1024
+
+/* Every expert's matrix times its rows:
+ *
+ *   y[r] = W[e] x[r]  for begin[e] <= r < begin[e + 1],
+ *
+ * y = silu(gate) up of it where gated; sums in FP32 (the tensor core's), rounded
+ * once, to BF16 or as mxfp8_quantize does.
+ *  w:      device, [experts][n or 2 n] rows of K codes, 32-byte aligned; laid: its
+ *          scales, by mxfp8_expert_lay_scales;
+ *  x, x_scale: device, [rows] of K codes (32-byte aligned) and K/32 scales (4);
+ *  begin:  device int32 [experts + 1], ascending from 0 to at most rows; NULL with
+ *          one expert, which then has all rows.  Rows in no expert are left as
+ *          they were.  An index outside 0..rows or below the one before is cut
+ *          and raises MXFP8_FLAG_BAD_INDEX.
+ *  out:    device, 16-byte aligned, [rows][n] BF16 or codes; out_scale: device,
+ *          [rows][n/32], where codes are asked for.
+ *  workspace: device, 16-byte aligned, mxfp8_expert_workspace_bytes, whose first
+ *          MXFP8_EXPERT_WORKSPACE_ZEROS bytes are zero before the first call (each
+ *          call leaves them zero); calls that share one must be ordered on one
+ *          stream; any number of sets of matrices may share one.
+ *  flags:  device int32 or NULL; a wait of the pipeline that runs out raises
+ *          MXFP8_FLAG_GEMM_TIMEOUT.
+ * Results have the same bits every time.  rows = 0 launches nothing. */
+mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* desc, const void* w, const void* laid,
+                                  const void* x, const void* x_scale, const int32_t* begin,
+                                  void* out, void* out_scale, void* workspace,
+                                  size_t workspace_bytes, int32_t* flags, void* stream);
+
+/* out [tokens][n] BF16 = add[t] + sum_j weight[t][j] y[slot[t][j]], in FP32, j
+ * ascending, rounded once.  y: device, BF16, `slots` rows of n, `stride` elements
+ * apart (a multiple of 8); weight FP32 and slot int32 [tokens][k]; add BF16
+ * [tokens][n] or NULL.  A slot of -1 adds nothing, whatever its weight; another
+ * one outside y neither, and raises MXFP8_FLAG_BAD_INDEX in *flags (may be NULL).
+ * n: a multiple of 8; y, add and out 16-byte aligned; out may be add. */
+mxfp8_status mxfp8_combine(const void* y, int64_t stride, int32_t slots, const float* weight,
+                           const int32_t* slot, int64_t tokens, int32_t k, int32_t n,
+                           const void* add, void* out, int32_t* flags, void* stream);
+
 /* Text of the calling thread's last error ("" if none). */
 const char* mxfp8_last_error(void);
 

@@ -27,12 +27,18 @@ MAX_ROWS = 8
 NOALLOC_SCRATCH_BYTES = 4 << 20
 LATENT_ROPE = 64
 MAX_ADAPTER_RANK = 256
+BF16, FP16, FP32 = range(3)
+FORMAT_BF16, FORMAT_MXFP8, FORMAT_MXFP4 = range(3)
+MAX_EXPERTS = 512
+MAX_CHOICES = 32
+EXPERT_WORKSPACE_ZEROS = 1024
 
 # Every symbol the header declares, with (restype, argtypes).
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _sz = ctypes.c_size_t
 _u64 = ctypes.c_uint64
+_i64 = ctypes.c_int64
 
 
 class GemmDesc(ctypes.Structure):
@@ -52,6 +58,11 @@ class LatentDesc(ctypes.Structure):
                 ("page_size", _i32), ("pages", _i32), ("table_width", _i32),
                 ("scale", ctypes.c_float), ("token_stride", ctypes.c_int64),
                 ("page_stride", ctypes.c_int64)]
+
+
+class ExpertDesc(ctypes.Structure):
+    _fields_ = [("experts", _i32), ("n", _i32), ("k", _i32), ("gated", _i32), ("w_format", _i32),
+                ("x_format", _i32), ("out_format", _i32), ("rows", _i32)]
 
 
 SIGNATURES = {
@@ -79,6 +90,19 @@ SIGNATURES = {
     "mxfp8_latent_workspace_bytes": (_sz, [_i32]),
     "mxfp8_latent_attend": (ctypes.c_int, [ctypes.POINTER(LatentDesc), _vp, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _sz, _vp, _vp]),
+    "mxfp8_route_workspace_bytes": (_sz, [_i64, _i32]),
+    "mxfp8_route": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _sz, _vp]),
+    "mxfp8_quantize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _vp,
+                                      _vp]),
+    "mxfp8_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),
+    "mxfp8_expert_lay_scales": (ctypes.c_int, [ctypes.POINTER(ExpertDesc), _vp, _vp, _vp]),
+    "mxfp8_expert_product": (ctypes.c_int, [ctypes.POINTER(ExpertDesc), _vp, _vp, _vp, _vp, _vp,
+                                            _vp, _vp, _vp, _sz, _vp, _vp]),
+    "mxfp8_combine": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp,
+                                     _vp]),
+    "mxfp8_expert_scales_bytes": (_sz, [ctypes.POINTER(ExpertDesc)]),
+    "mxfp8_expert_workspace_bytes": (_sz, []),
     "mailbox_publish": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp]),
     "mailbox_consume": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _u64, _vp]),
     "mxfp8_mailbox_status": (ctypes.c_int, [_vp, ctypes.POINTER(_i32), _vp]),

@@ -24,7 +24,8 @@ BUILD_DIR = PACKAGE / "_build"
 LIBRARY = PACKAGE / "libmxfp8_mailbox.so"
 SOURCES = ("publish_gemm.cu", "publish_gemm_fold.cu", "publish_gemm_k256.cu", "mailbox.cu",
            "lamport_gather.cu", "tagged_mailbox.cu", "adapters.cu", "latent_project.cu",
-           "latent_attend.cu", "abi_latent.cu", "abi.cu")
+           "latent_attend.cu", "abi_latent.cu", "experts_route.cu", "quantize.cu",
+           "experts_product.cu", "abi_experts.cu", "abi.cu")
 CALLS = PACKAGE / ("_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -16,6 +16,7 @@
 
 #include <algorithm>
 #include <string>
+#include <vector>
 
 #include "mxfp8_mailbox.h"
 
@@ -423,6 +424,325 @@ PyObject* mailbox_consume(PyObject*, PyObject* const* args, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------------------ a layer of routed experts
+
+// MXFP8_BF16, _FP16 or _FP32.
+int32_t type_of(const at::Tensor& t, const char* name) {
+  switch (t.scalar_type()) {
+    case at::kBFloat16: return MXFP8_BF16;
+    case at::kHalf: return MXFP8_FP16;
+    case at::kFloat: return MXFP8_FP32;
+    default:
+      refuse(PyExc_TypeError, std::string(name) + " must be bfloat16, float16 or float32, got " +
+                                  name_of(t.scalar_type()));
+  }
+}
+// A matrix whose rows are contiguous and may be strided; returns the stride.
+int64_t strided_rows(const at::Tensor& t, const char* name, const char* shape) {
+  if (t.dim() != 2)
+    refuse(PyExc_ValueError, std::string(name) + " must be " + shape + ", got " + text_of(t.sizes()));
+  if (!t.is_cuda() || (t.size(1) > 1 && t.stride(1) != 1))
+    refuse(PyExc_ValueError, std::string(name) + " must be a CUDA tensor with contiguous rows");
+  return t.stride(0);
+}
+int32_t narrowed(int64_t v, const char* what) {
+  if (v > INT32_MAX) refuse(PyExc_ValueError, std::string(what) + " is past 2^31 - 1");
+  return static_cast<int32_t>(v);
+}
+int32_t* flags_of(PyObject* o, int device) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = tensor(o, "flags");
+  expect(t, "flags", at::kInt, {1}, device);
+  return static_cast<int32_t*>(t.data_ptr());
+}
+// What a format is called, as a number.
+int32_t format_of(PyObject* o, bool none_is_bf16) {
+  if (none_is_bf16 && o == Py_None) return MXFP8_FORMAT_BF16;
+  if (PyUnicode_Check(o)) {
+    if (PyUnicode_CompareWithASCIIString(o, "mxfp8") == 0) return MXFP8_FORMAT_MXFP8;
+    if (PyUnicode_CompareWithASCIIString(o, "mxfp4") == 0) return MXFP8_FORMAT_MXFP4;
+  }
+  refuse(PyExc_ValueError, none_is_bf16 ? "format must be None, \"mxfp8\" or \"mxfp4\""
+                                        : "format must be \"mxfp8\" or \"mxfp4\"");
+}
+// One-byte codes of exactly this shape, contiguous, on the device.
+void exact_codes(const at::Tensor& t, const char* name, at::IntArrayRef shape, int device) {
+  if (t.element_size() != 1)
+    refuse(PyExc_TypeError, std::string(name) + " must hold one-byte codes (uint8 / float8), got " +
+                                name_of(t.scalar_type()));
+  expect(t, name, t.scalar_type(), shape, device);
+}
+
+// (logits, k, normalize, stream | None) -> (weight, expert, slot, row, begin)
+PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 4);
+  const at::Tensor& logits = tensor(args[0], "logits");
+  const int32_t type = type_of(logits, "logits");
+  const int64_t stride = strided_rows(logits, "logits", "[tokens][experts]");
+  const int device = on_current_device(logits, "logits");
+  const int64_t tokens = logits.size(0), experts = logits.size(1), k = integer(args[1]);
+  const int normalize = PyObject_IsTrue(args[2]);
+  if (normalize < 0) throw python_error();
+  // Sizes that no output could be made for; the others the library refuses.
+  if (k < 1 || k > MXFP8_MAX_CHOICES || k > experts)
+    refuse(PyExc_ValueError, "k must be in 1..min(experts, " + std::to_string(MXFP8_MAX_CHOICES) +
+                                 "), got " + std::to_string(k) + " of " + std::to_string(experts));
+  if (tokens > INT32_MAX / k) refuse(PyExc_ValueError, "tokens x k must be below 2^31");
+  const CallStream stream(args[3], device);
+  at::Tensor weight = new_tensor({tokens, k}, at::kFloat, device);
+  at::Tensor expert = new_tensor({tokens, k}, at::kInt, device);
+  at::Tensor slot = new_tensor({tokens, k}, at::kInt, device);
+  at::Tensor row = new_tensor({tokens * k}, at::kInt, device);
+  at::Tensor begin = new_tensor({experts + 1}, at::kInt, device);
+  const auto space = static_cast<int64_t>(
+      mxfp8_route_workspace_bytes(tokens, narrowed(experts, "the number of experts")));
+  at::Tensor workspace;
+  if (space) workspace = new_tensor({space}, at::kByte, device);
+  const void* const lp = logits.data_ptr();
+  auto* const wp = static_cast<float*>(weight.data_ptr());
+  const auto ints = [](const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
+  int32_t *const ep = ints(expert), *const sp = ints(slot), *const rp = ints(row),
+                 *const bp = ints(begin);
+  void* const space_p = space ? workspace.data_ptr() : nullptr;
+  check(unlocked([&] {
+          return mxfp8_route(lp, type, stride, tokens, static_cast<int32_t>(experts),
+                             static_cast<int32_t>(k), normalize, wp, ep, sp, rp, bp, space_p,
+                             static_cast<size_t>(space), stream);
+        }),
+        "mxfp8_route");
+  PyObject* out = PyTuple_New(5);
+  if (!out) throw python_error();
+  at::Tensor* const all[5] = {&weight, &expert, &slot, &row, &begin};
+  for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(out, i, THPVariable_Wrap(std::move(*all[i])));
+  return out;
+  END_HANDLE_TH_ERRORS
+}
+
+// (x, format, rows | None, codes | None, scale | None, flags | None, stream | None) -> (codes,
+// scale)
+PyObject* quantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 7);
+  const at::Tensor& x = tensor(args[0], "x");
+  const int32_t type = type_of(x, "x"), format = format_of(args[1], false);
+  if (x.dim() < 1) refuse(PyExc_ValueError, "x must be [...][K], got " + text_of(x.sizes()));
+  const int device = on_current_device(x, "x");
+  const int64_t k = x.size(-1);
+  if (k < 32 || k % 32)
+    refuse(PyExc_ValueError, "K must be a positive multiple of 32, got " + std::to_string(k));
+  int64_t x_rows = 1, stride = k;
+  if (x.dim() == 2) {
+    stride = strided_rows(x, "x", "[rows][K]");
+    x_rows = x.size(0);
+  } else {
+    if (!x.is_contiguous())
+      refuse(PyExc_ValueError, "x of other than two axes must be contiguous");
+    x_rows = x.numel() / k;
+  }
+  std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end());
+  const int32_t* index = nullptr;
+  int64_t out_rows = x_rows;
+  if (args[2] != Py_None) {
+    const at::Tensor& rows = tensor(args[2], "rows");
+    if (x.dim() != 2) refuse(PyExc_ValueError, "x must be [rows][K] to be indexed");
+    if (rows.dim() != 1)
+      refuse(PyExc_ValueError, "rows must have one axis, got " + text_of(rows.sizes()));
+    expect(rows, "rows", at::kInt, rows.sizes(), device);
+    shape[0] = out_rows = rows.size(0);
+    index = static_cast<const int32_t*>(rows.data_ptr());
+    // (An empty tensor has no address, and without one every row would be taken.)
+    if (out_rows == 0) index = reinterpret_cast<const int32_t*>(uintptr_t{4});
+  }
+  int32_t* const flags = flags_of(args[5], device);
+  const CallStream stream(args[6], device);
+  const bool wide = format == MXFP8_FORMAT_MXFP8;
+  const auto result = [&](PyObject* t, const char* name, at::ScalarType dtype, int64_t last) {
+    shape.back() = last;
+    if (t == Py_None) return new_tensor(shape, dtype, device);
+    exact_codes(tensor(t, name), name, shape, device);
+    return tensor(t, name);
+  };
+  at::Tensor codes = result(args[3], "codes", wide ? at::kFloat8_e4m3fn : at::kByte,
+                            wide ? k : k / 2);
+  at::Tensor scale = result(args[4], "scale", at::kFloat8_e8m0fnu, k / 32);
+  const int32_t k32 = narrowed(k, "K");
+  const void* const xp = x.data_ptr();
+  void *const cp = codes.data_ptr(), *const sp = scale.data_ptr();
+  check(unlocked([&] {
+          return mxfp8_quantize(xp, type, stride, x_rows, k32, index, out_rows, format, cp, sp, flags,
+                                stream);
+        }),
+        "mxfp8_quantize");
+  THPObjectPtr a(args[3] == Py_None ? THPVariable_Wrap(std::move(codes)) : given(args[3]));
+  THPObjectPtr b(args[4] == Py_None ? THPVariable_Wrap(std::move(scale)) : given(args[4]));
+  if (!a || !b) throw python_error();
+  return PyTuple_Pack(2, a.get(), b.get());
+  END_HANDLE_TH_ERRORS
+}
+
+// (codes, scale, type as a number, stream | None) -> values
+PyObject* dequantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  arguments(n, 4);
+  const at::Tensor &codes = tensor(args[0], "codes"), &scale = tensor(args[1], "scale");
+  if (scale.dim() < 1)
+    refuse(PyExc_ValueError, "scale must be [...][K / 32], got " + text_of(scale.sizes()));
+  const int device = on_current_device(scale, "scale");
+  exact_codes(scale, "scale", scale.sizes(), device);
+  const int64_t k = scale.size(-1) * 32;
+  if (k == 0) refuse(PyExc_ValueError, "K must be a positive multiple of 32, got 0");
+  const bool wide = codes.dim() == scale.dim() && codes.size(-1) == k;
+  std::vector<int64_t> shape(scale.sizes().begin(), scale.sizes().end());
+  shape.back() = wide ? k : k / 2;
+  exact_codes(codes, "codes", shape, device);
+  shape.back() = k;
+  const int32_t type = static_cast<int32_t>(integer(args[2]));
+  const CallStream stream(args[3], device);
+  at::Tensor out = new_tensor(
+      shape, type == MXFP8_BF16 ? at::kBFloat16 : type == MXFP8_FP16 ? at::kHalf : at::kFloat,
+      device);
+  const void *const cp = codes.data_ptr(), *const sp = scale.data_ptr();
+  void* const op = out.data_ptr();
+  const int64_t rows = scale.numel() / (k / 32);
+  const int32_t k32 = narrowed(k, "K");
+  check(unlocked([&] {
+          return mxfp8_dequantize(cp, sp, rows, k32,
+                                  wide ? MXFP8_FORMAT_MXFP8 : MXFP8_FORMAT_MXFP4, type, op, stream);
+        }),
+        "mxfp8_dequantize");
+  return THPVariable_Wrap(std::move(out));
+  END_HANDLE_TH_ERRORS
+}
+
+// (experts, n, k, gated, w_format, w, laid scales, workspace, flags, x, x_scale, begin | None,
+//  format | None, out | None, out_scale | None, stream | None) -> out or (out, out_scale)
+PyObject* expert_product(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  arguments(count, 16);
+  mxfp8_expert_desc desc{};
+  desc.experts = static_cast<int32_t>(integer(args[0]));
+  desc.n = static_cast<int32_t>(integer(args[1]));
+  desc.k = static_cast<int32_t>(integer(args[2]));
+  desc.gated = static_cast<int32_t>(integer(args[3]));
+  desc.w_format = static_cast<int32_t>(integer(args[4]));
+  const at::Tensor &w = tensor(args[5], "w"), &laid = tensor(args[6], "scales");
+  const at::Tensor &workspace = tensor(args[7], "workspace"), &x = tensor(args[9], "x");
+  const at::Tensor& x_scale = tensor(args[10], "x_scale");
+  const int64_t n = desc.n, k = desc.k;
+  const int device = on_current_device(x, "x");
+  if (gpu_of(w) != device)
+    refuse(PyExc_ValueError,
+           "x is on device " + std::to_string(device) + ", this object's matrices are not");
+  if (x.dim() != 2 || (x.size(1) != k && x.size(1) != k / 2))
+    refuse(PyExc_ValueError, "x must be [rows][" + std::to_string(k) + "] (MXFP8) or [rows][" +
+                                 std::to_string(k / 2) + "] (MXFP4), got " + text_of(x.sizes()));
+  const int64_t rows = x.size(0);
+  exact_codes(x, "x", x.sizes(), device);
+  exact_codes(x_scale, "x_scale", {rows, k / 32}, device);
+  desc.x_format = x.size(1) == k ? MXFP8_FORMAT_MXFP8 : MXFP8_FORMAT_MXFP4;
+  desc.out_format = format_of(args[12], true);
+  desc.rows = narrowed(rows, "the number of rows");
+  const int32_t* begin = nullptr;
+  if (args[11] != Py_None) {
+    const at::Tensor& b = tensor(args[11], "begin");
+    expect(b, "begin", at::kInt, {desc.experts + 1}, device);
+    begin = static_cast<const int32_t*>(b.data_ptr());
+  }
+  int32_t* const flags = flags_of(args[8], device);
+  const bool codes = desc.out_format != MXFP8_FORMAT_BF16;
+  if (codes && n % 32)
+    refuse(PyExc_ValueError, "N must be a multiple of 32 to be rounded to blocks, got " +
+                                 std::to_string(n));
+  if (!codes && args[14] != Py_None) refuse(PyExc_ValueError, "out_scale goes with a format");
+  const CallStream stream(args[15], device);
+  const int64_t width = desc.out_format == MXFP8_FORMAT_MXFP4 ? n / 2 : n;
+  at::Tensor out, scale;
+  if (args[13] == Py_None) {
+    out = new_tensor({rows, width},
+                     desc.out_format == MXFP8_FORMAT_BF16    ? at::kBFloat16
+                     : desc.out_format == MXFP8_FORMAT_MXFP8 ? at::kFloat8_e4m3fn
+                                                             : at::kByte,
+                     device);
+  } else {
+    out = tensor(args[13], "out");
+    if (codes)
+      exact_codes(out, "out", {rows, width}, device);
+    else
+      expect(out, "out", at::kBFloat16, {rows, width}, device);
+  }
+  if (codes) {
+    if (args[14] == Py_None) {
+      scale = new_tensor({rows, n / 32}, at::kFloat8_e8m0fnu, device);
+    } else {
+      scale = tensor(args[14], "out_scale");
+      exact_codes(scale, "out_scale", {rows, n / 32}, device);
+    }
+  }
+  const void *const wp = w.data_ptr(), *const lp = laid.data_ptr(), *const xp = x.data_ptr(),
+                    *const sp = x_scale.data_ptr();
+  void *const op = out.data_ptr(), *const tp = codes ? scale.data_ptr() : nullptr,
+              *const space = workspace.data_ptr();
+  const auto bytes = static_cast<size_t>(workspace.numel());
+  check(unlocked([&] {
+          return mxfp8_expert_product(&desc, wp, lp, xp, sp, begin, op, tp, space, bytes, flags,
+                                      stream);
+        }),
+        "mxfp8_expert_product");
+  THPObjectPtr a(args[13] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[13]));
+  if (!a) throw python_error();
+  if (!codes) return a.release();
+  THPObjectPtr b(args[14] == Py_None ? THPVariable_Wrap(std::move(scale)) : given(args[14]));
+  if (!b) throw python_error();
+  return PyTuple_Pack(2, a.get(), b.get());
+  END_HANDLE_TH_ERRORS
+}
+
+// (y, weight, slot, add | None, out | None, flags | None, stream | None) -> out
+PyObject* combine(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  arguments(count, 7);
+  const at::Tensor &y = tensor(args[0], "y"), &weight = tensor(args[1], "weight");
+  const at::Tensor& slot = tensor(args[2], "slot");
+  if (y.scalar_type() != at::kBFloat16)
+    refuse(PyExc_TypeError, std::string("y must be bfloat16, got ") + name_of(y.scalar_type()));
+  const int64_t stride = strided_rows(y, "y", "[rows][N]");
+  const int device = on_current_device(y, "y");
+  const int64_t n = y.size(1);
+  if (slot.dim() != 2)
+    refuse(PyExc_ValueError, "slot must be [tokens][k], got " + text_of(slot.sizes()));
+  const int64_t tokens = slot.size(0), k = slot.size(1);
+  expect(slot, "slot", at::kInt, {tokens, k}, device);
+  expect(weight, "weight", at::kFloat, {tokens, k}, device);
+  const void* add = nullptr;
+  if (args[3] != Py_None) {
+    const at::Tensor& t = tensor(args[3], "add");
+    expect(t, "add", at::kBFloat16, {tokens, n}, device);
+    add = t.data_ptr();
+  }
+  int32_t* const flags = flags_of(args[5], device);
+  const CallStream stream(args[6], device);
+  at::Tensor out;
+  if (args[4] == Py_None) {
+    out = new_tensor({tokens, n}, at::kBFloat16, device);
+  } else {
+    out = tensor(args[4], "out");
+    expect(out, "out", at::kBFloat16, {tokens, n}, device);
+  }
+  const int32_t slots = narrowed(y.size(0), "the number of rows"), k32 = narrowed(k, "k"),
+                n32 = narrowed(n, "N");
+  const void* const yp = y.data_ptr();
+  const auto* const wp = static_cast<const float*>(weight.data_ptr());
+  const auto* const sp = static_cast<const int32_t*>(slot.data_ptr());
+  void* const op = out.data_ptr();
+  check(unlocked([&] {
+          return mxfp8_combine(yp, stride, slots, wp, sp, tokens, k32, n32, add, op, flags, stream);
+        }),
+        "mxfp8_combine");
+  return args[4] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[4]);
+  END_HANDLE_TH_ERRORS
+}
+
 PyCFunction fast(PyObject* (*call)(PyObject*, PyObject* const*, Py_ssize_t)) {
   return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(call));
 }
@@ -431,6 +751,11 @@ PyMethodDef methods[] = {{"latent_query", fast(latent_query), METH_FASTCALL, nul
                          {"latent_attend", fast(latent_attend), METH_FASTCALL, nullptr},
                          {"run_adapted", fast(run_adapted), METH_FASTCALL, nullptr},
                          {"mailbox_consume", fast(mailbox_consume), METH_FASTCALL, nullptr},
+                         {"route", fast(route), METH_FASTCALL, nullptr},
+                         {"quantize", fast(quantize), METH_FASTCALL, nullptr},
+                         {"dequantize", fast(dequantize), METH_FASTCALL, nullptr},
+                         {"expert_product", fast(expert_product), METH_FASTCALL, nullptr},
+                         {"combine", fast(combine), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
                       nullptr,               nullptr,  nullptr, nullptr};

@@ -1,0 +1,613 @@
+// Products grouped by expert in microscaled formats, for sm_103a:
+//
+//   y[r][n] = sum_k W[e][n][k] x[r][k],   begin[e] <= r < begin[e + 1]
+//
+// W MXFP8 or MXFP4, x MXFP8 or MXFP4, FP32 sums; the result BF16, or rounded
+// to MXFP8 / MXFP4 along n.  Gated: W[e] holds n gate rows, then n up rows, and
+// the result is silu(gate) up.
+//
+// W is the MMA's A operand (a tile of 128 of its rows), the expert's rows its B
+// operand (a tile of up to kCols), the products kind::mxf8f6f4 with one scale
+// a block of 32: elements of 4 bits lie in shared memory as 16 in 16 bytes, the
+// latter 8 unused, which is how the tensor copies lay them.  A tile of a gated
+// product takes 32 gate rows, their 32 up rows, 32 gate rows, 32 up rows, so a
+// block of 32 outputs is one warp's lanes and its partner's.
+//
+// Work.  begin is read on the device, so the grid is one CTA an SM, and each
+// finds its share: tiles are numbered expert by expert, tiles of rows inside
+// those of W (neighbouring CTAs read the same W at the same time); as many
+// whole rounds as there are go one tile a CTA, and what is left is cut along k
+// into equal runs.  A tile that several CTAs share leaves FP32 partials; the
+// last to arrive adds them in the order of k, so results have the same bits
+// every time.
+//
+// Warp roles: warp 0 copies (kLanes lanes take stages in turn), warp 1 lays the
+// rows' scales, warps 2-5 read the sums back, warps 6.. issue the products
+// (kPipes, each with an accumulator of its own, added at the end).
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "mx_format.cuh"
+#include "ptx.cuh"
+
+namespace mxfp8 {
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kTileRows = 128;  // rows of W
+constexpr uint32_t kWStage = kTileRows * 128;
+constexpr uint32_t kChunk = 512;  // scales of 128 rows, 4 blocks each
+
+template <int kCols_, int kStages_, int kPipes_, int kLanes_, int kBox_, int kMinRun_>
+struct Shape {
+  static constexpr int kCols = kCols_;      // expert rows of a tile
+  static constexpr int kStages = kStages_;  // of the ring
+  static constexpr int kPipes = kPipes_;    // issuing warps
+  static constexpr int kLanes = kLanes_;    // copying lanes
+  static constexpr int kBox = kBox_;        // rows of a copy of x
+  static constexpr int kMinRun = kMinRun_;  // k tiles of a run at least
+  static constexpr int kChunks = (kCols + 127) / 128;  // scale chunks of the rows
+  static constexpr int kRowsALane = (kCols + 31) / 32;
+  static constexpr uint32_t kXStage = kCols * 128;
+  static constexpr int kThreads = 192 + 32 * kPipes;
+  static constexpr uint32_t kAccSlot = kCols < 32 ? 32 : kCols;
+  static constexpr uint32_t kAcc = 2 * kPipes * kAccSlot;
+  static constexpr uint32_t kSf = 4 + 4 * kChunks;  // columns of a stage's scales
+  static constexpr uint32_t kColumns = kAcc + kStages * kSf <= 256 ? 256 : 512;
+  static_assert(kAcc + kStages * kSf <= 512, "tensor memory");
+  // Each barrier is waited on by one thread in use order.
+  static_assert(kStages % kPipes == 0 && kStages % kLanes == 0, "slots keep their threads");
+  static_assert(kCols % kBox == 0 && kBox % 8 == 0, "copies of whole swizzled groups");
+  // Shared memory, from a 1024-byte boundary.
+  static constexpr uint32_t kX = kStages * kWStage;
+  static constexpr uint32_t kSfa = kX + kStages * kXStage;
+  static constexpr uint32_t kSfb = kSfa + kStages * kChunk;
+  static constexpr uint32_t kExchange = kSfb + kStages * kChunk * kChunks;
+  static constexpr uint32_t kStaging = kExchange + 2 * 2 * 8 * 32 * 4;
+  static constexpr uint32_t kTables = kStaging + 4 * 8 * 80;
+  static constexpr uint32_t kBars = kTables + 2 * 4 * ((MXFP8_MAX_EXPERTS + 8) / 4 * 4);
+  static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 4);
+  static constexpr uint32_t kBytes = kMisc + 32 + 1024;
+  static_assert(kBytes <= 232448, "shared memory");
+};
+// Few rows an expert: bound by the stream of W.  Many: by the products.
+using Narrow = Shape<32, 8, 4, 4, 8, 4>;
+using Wide = Shape<128, 6, 1, 2, 32, 8>;
+
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void pair_barrier(int pair) {
+  asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
+}
+
+// A run of k tiles of one tile.
+struct Segment {
+  int expert, row, rows, w_tile;  // rows: of the tile
+  int kt0, kt1;
+  int left;  // which of the tiles that are cut into runs, -1: a whole round's
+};
+
+// The segments of a CTA, in order; every role walks the same list.
+struct Share {
+  const int* rows;   // [experts + 1] each expert's first row
+  const int* tiles;  // [experts + 1] ... first tile
+  int experts, cols, k_tiles;
+  int grid, cta, rounds, round;
+  int units, runs, at, end;  // k tiles of the cut tiles; this CTA's run
+
+  __device__ __forceinline__ int run_begin(int c) const {
+    return static_cast<int>(static_cast<int64_t>(c) * units / runs);
+  }
+  __device__ __forceinline__ int owner(int unit) const {
+    return static_cast<int>(((static_cast<int64_t>(unit) + 1) * runs - 1) / units);
+  }
+  __device__ __forceinline__ Share(const int* r, const int* t, int e, int c, int kt, int min_run)
+      : rows(r), tiles(t), experts(e), cols(c), k_tiles(kt) {
+    grid = gridDim.x;
+    cta = blockIdx.x;
+    const int all = tiles[e];
+    rounds = all / grid;
+    round = 0;
+    units = (all - rounds * grid) * kt;
+    runs = max(1, min(grid, units / min_run));
+    at = end = 0;
+    if (units > 0 && cta < runs) {
+      at = run_begin(cta);
+      end = run_begin(cta + 1);
+    }
+  }
+  __device__ __forceinline__ bool next(Segment& s) {
+    int tile;
+    if (round < rounds) {
+      tile = cta + grid * round++;
+      s.kt0 = 0;
+      s.kt1 = k_tiles;
+      s.left = -1;
+    } else if (at < end) {
+      s.left = at / k_tiles;
+      tile = rounds * grid + s.left;
+      s.kt0 = at - s.left * k_tiles;
+      s.kt1 = min(k_tiles, s.kt0 + end - at);
+      at += s.kt1 - s.kt0;
+    } else {
+      return false;
+    }
+    int lo = 0, hi = experts - 1;  // the last expert whose first tile is not past this one
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (tiles[mid] <= tile)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    s.expert = lo;
+    const int count = rows[lo + 1] - rows[lo], row_tiles = (count + cols - 1) / cols;
+    const int local = tile - tiles[lo];
+    s.w_tile = local / row_tiles;
+    // Equal tiles of rows, in eights.
+    const int size = ((count + row_tiles - 1) / row_tiles + 7) / 8 * 8;
+    const int first = (local - s.w_tile * row_tiles) * size;
+    s.row = rows[lo] + first;
+    s.rows = max(0, min(size, count - first));
+    return true;
+  }
+};
+
+// The experts' first rows and first tiles, by one warp.  Rows outside 0 .. rows
+// or that go back are cut and raise the flag.
+__device__ __forceinline__ void deal(const ExpertParams& p, int cols, int* rows, int* tiles) {
+  const int lane = threadIdx.x % 32;
+  int top = 0, sum = 0;
+  bool bad = false;
+  for (int e0 = 0; e0 <= p.experts; e0 += 32) {
+    const int e = e0 + lane;
+    int b = 0;
+    if (e <= p.experts) {
+      const int given = p.begin ? p.begin[e] : e * p.rows;  // without begin: one expert
+      b = min(max(given, 0), p.rows);
+      bad |= given != b;
+    }
+    int m = b;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int up = __shfl_up_sync(~0u, m, o);
+      if (lane >= o) m = max(m, up);
+    }
+    m = max(m, top);
+    bad |= e <= p.experts && m != b;
+    if (e <= p.experts) rows[e] = m;
+    top = __shfl_sync(~0u, m, 31);
+  }
+  __syncwarp();
+  for (int e0 = 0; e0 < p.experts; e0 += 32) {
+    const int e = e0 + lane;
+    const int own = e < p.experts ? (rows[e + 1] - rows[e] + cols - 1) / cols * p.w_tiles : 0;
+    int inc = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int up = __shfl_up_sync(~0u, inc, o);
+      if (lane >= o) inc += up;
+    }
+    if (e < p.experts) tiles[e] = sum + inc - own;
+    sum += __shfl_sync(~0u, inc, 31);
+  }
+  if (lane == 0) tiles[p.experts] = sum;
+  if (bad && blockIdx.x == 0 && p.flags) atomicOr(p.flags, MXFP8_FLAG_BAD_INDEX);
+}
+
+// kTokens rows' results of 32 outputs (one a lane) to memory.  `staging`: 640
+// bytes of the warp's own.
+template <int kTokens>
+__device__ __forceinline__ void store_block(const ExpertParams& p, const float (&v)[kTokens],
+                                            int row, int live, int n0, uint8_t* staging) {
+  const int lane = threadIdx.x % 32;
+  __syncwarp();
+  if (p.format == MXFP8_FORMAT_BF16) {
+#pragma unroll
+    for (int t = 0; t < kTokens; ++t)
+      reinterpret_cast<__nv_bfloat16*>(staging + t * 80)[lane] = __float2bfloat16_rn(v[t]);
+    __syncwarp();
+    const int t = lane / 4, c = lane % 4 * 8;
+    if (t < kTokens && t < live && n0 + c < p.n)
+      ptx::st_v4(static_cast<uint16_t*>(p.out) + static_cast<size_t>(row + t) * p.n + n0 + c,
+                 *reinterpret_cast<const uint4*>(staging + t * 80 + c * 2));
+    return;
+  }
+  const bool wide = p.format == MXFP8_FORMAT_MXFP8;
+  uint32_t codes[kTokens];
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) {
+    const uint32_t bits = __float_as_uint(v[t]) & 0x7FFFFFFFu;
+    const bool finite = bits < 0x7F800000u;
+    const float top = __uint_as_float(__reduce_max_sync(~0u, finite ? bits : 0u));
+    if (wide) {
+      codes[t] = scale_code(top);
+      staging[t * 32 + lane] = static_cast<uint8_t>(
+          to_e4m3(finite ? v[t] : __uint_as_float(0x7FC00000u), 0.0f, codes[t]));
+    } else {
+      const uint32_t code = scale_code_e2m1(top);
+      const bool all = __all_sync(~0u, finite);
+      const float next = __shfl_down_sync(~0u, v[t], 1);
+      codes[t] = all ? code : 255u;
+      if (lane % 2 == 0)
+        staging[t * 16 + lane / 2] = all ? static_cast<uint8_t>(to_e2m1(v[t], next, code)) : 0;
+    }
+  }
+  __syncwarp();
+  if (n0 >= p.n) return;  // past the last block: n is whole blocks
+  const int bytes = wide ? 32 : 16;  // of a row's block
+  for (int i = lane; i < live * bytes / 4; i += 32) {
+    const int t = i / (bytes / 4), w = i % (bytes / 4);
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) +
+                                 (static_cast<size_t>(row + t) * p.n + n0) * bytes / 32 + w * 4) =
+        *reinterpret_cast<const uint32_t*>(staging + t * bytes + w * 4);
+  }
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t)
+    if (t < live && lane == t)
+      p.out_scale[static_cast<size_t>(row + t) * (p.n / 32) + n0 / 32] =
+          static_cast<uint8_t>(codes[t]);
+}
+
+template <class S, bool kGated>
+__global__ void __launch_bounds__(S::kThreads, 1)
+    expert_kernel(const __grid_constant__ CUtensorMap tmap_w,
+                  const __grid_constant__ CUtensorMap tmap_x,
+                  const __grid_constant__ ExpertParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  uint8_t* const smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+  const uint32_t sbase = ptx::smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const uint32_t bar_full = sbase + S::kBars, bar_empty = bar_full + 8 * S::kStages;
+  const uint32_t bar_acc_full = bar_empty + 8 * S::kStages, bar_acc_empty = bar_acc_full + 16;
+  uint32_t* const misc = reinterpret_cast<uint32_t*>(smem + S::kMisc);
+  int* const rows = reinterpret_cast<int*>(smem + S::kTables);
+  int* const tiles = rows + (MXFP8_MAX_EXPERTS + 8) / 4 * 4;
+
+  if (tid == 0) {
+    ptx::prefetch_tensormap(&tmap_w);
+    ptx::prefetch_tensormap(&tmap_x);
+    for (int s = 0; s < S::kStages; ++s) {
+      ptx::mbar_init(bar_full + 8 * s, 33);  // the copies and the scales' warp
+      ptx::mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(bar_acc_full + 8 * b, S::kPipes);
+      ptx::mbar_init(bar_acc_empty + 8 * b, 128);
+    }
+    ptx::fence_mbarrier_init();
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 6) {
+    ptx::tmem_alloc(sbase + S::kMisc, S::kColumns);
+    ptx::tmem_relinquish();
+    // Not before: a CTA of the next kernel must not hold what this one waits for.
+    ptx::launch_dependents();
+  }
+  ptx::grid_dependency_wait();
+  if (warp == 0) deal(p, S::kCols, rows, tiles);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const auto timed_out = [&] {
+    if (p.flags) atomicOr(p.flags, MXFP8_FLAG_GEMM_TIMEOUT);
+  };
+  Share share(rows, tiles, p.experts, S::kCols, p.k_tiles, S::kMinRun);
+  Segment s;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- copies
+    if (lane < S::kLanes) {
+      uint32_t stage = lane;  // of all this CTA's stages; the slot's use: stage / kStages
+      uint32_t before = 0;    // stages of the segments before
+      bool ok = true;
+      while (ok && share.next(s)) {
+        const uint32_t count = s.kt1 - s.kt0;
+        const int boxes = (s.rows + S::kBox - 1) / S::kBox;
+        const uint32_t bytes = p.w_bytes + kChunk + static_cast<uint32_t>(boxes) * p.x_bytes;
+        const uint8_t* sf = p.w_sf + (static_cast<size_t>(s.expert) * p.w_tiles + s.w_tile) *
+                                         p.k_tiles * kChunk;
+        for (; stage < before + count; stage += S::kLanes) {
+          const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
+          if (!ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs)) {
+            timed_out();
+            ok = false;
+            break;
+          }
+          const uint32_t full = bar_full + 8 * slot;
+          const int kt = s.kt0 + static_cast<int>(stage - before);
+          ptx::mbar_arrive_expect_tx(full, bytes);
+          const uint32_t w = sbase + slot * kWStage;
+          if constexpr (kGated) {
+            ptx::tma_load_4d(w, &tmap_w, kt * 128, s.w_tile * 64, 0, s.expert, full);
+            ptx::tma_load_4d(w + kWStage / 2, &tmap_w, kt * 128, s.w_tile * 64 + 32, 0, s.expert,
+                             full);
+          } else {
+            ptx::tma_load_4d(w, &tmap_w, kt * 128, s.w_tile * kTileRows, 0, s.expert, full);
+          }
+          ptx::bulk_load(sbase + S::kSfa + slot * kChunk, sf + static_cast<size_t>(kt) * kChunk,
+                         kChunk, full);
+          for (int b = 0; b < boxes; ++b)
+            ptx::tma_load_4d(sbase + S::kX + slot * S::kXStage + b * S::kBox * 128, &tmap_x,
+                             kt * 128, s.row + b * S::kBox, 0, 0, full);
+        }
+        before += count;
+      }
+      // The products that read this lane's last stages are done before the CTA
+      // leaves, and with them the copies.
+      for (int i = 0; i < S::kStages / S::kLanes; ++i, stage += S::kLanes)
+        ptx::mbar_wait(bar_empty + 8 * (stage % S::kStages), ((stage / S::kStages) & 1) ^ 1,
+                       kWaitNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------- the rows' scales, laid for the copy
+    // Row r's four codes of a k tile at (r % 32) 16 + (r / 32 % 4) 4 of its chunk.
+    // Four k tiles' loads are under way while the four before are stored.
+    constexpr int kAhead = 4;
+    uint32_t stage = 0;
+    bool ok = true;
+    const size_t stride = static_cast<size_t>(p.k_tiles) * 4;
+    while (ok && share.next(s)) {
+      const uint8_t* at[S::kRowsALane];
+#pragma unroll
+      for (int i = 0; i < S::kRowsALane; ++i)
+        at[i] = p.x_scale + min(s.row + min(lane + 32 * i, s.rows - 1), p.rows - 1) * stride;
+      uint32_t next[kAhead][S::kRowsALane];
+      const auto load = [&](int kt) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int i = 0; i < S::kRowsALane; ++i)
+            next[j][i] = kt + j < s.kt1 && 32 * i < s.rows
+                             ? *reinterpret_cast<const uint32_t*>(at[i] + 4 * (kt + j))
+                             : 0u;
+      };
+      load(s.kt0);
+      for (int kt = s.kt0; ok && kt < s.kt1; kt += kAhead) {
+        uint32_t now[kAhead][S::kRowsALane];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int i = 0; i < S::kRowsALane; ++i) now[j][i] = next[j][i];
+        load(kt + kAhead);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (kt + j >= s.kt1) break;
+          const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
+          ok = ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs);
+          if (!ok) {
+            timed_out();
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < S::kRowsALane; ++i)
+            *reinterpret_cast<uint32_t*>(smem + S::kSfb + (slot * S::kChunks + i / 4) * kChunk +
+                                         lane * 16 + i % 4 * 4) = now[j][i];
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(bar_full + 8 * slot);
+          ++stage;
+        }
+      }
+    }
+  } else if (warp >= 6) {
+    // -------------------------------------------------------------- products
+    if (lane == 0) {
+      const uint32_t pipe = warp - 6;
+      uint32_t stage = pipe, before = 0, use = 0;  // use: segments so far
+      bool ok = true;
+      while (ok && share.next(s)) {
+        const uint32_t count = s.kt1 - s.kt0, buffer = use & 1;
+        const uint32_t columns = static_cast<uint32_t>((s.rows + 7) / 8 * 8);
+        const uint32_t idesc = p.idesc | columns >> 3 << 17;
+        const uint32_t acc = tmem + (buffer * S::kPipes + pipe) * S::kAccSlot;
+        if (!ptx::mbar_wait(bar_acc_empty + 8 * buffer, ((use >> 1) & 1) ^ 1, kWaitNs)) {
+          timed_out();
+          break;
+        }
+        ptx::tc_fence_after();
+        uint32_t accumulate = 0;
+        for (; stage < before + count; stage += S::kPipes) {
+          const uint32_t slot = stage % S::kStages;
+          if (!ptx::mbar_wait(bar_full + 8 * slot, (stage / S::kStages) & 1, kWaitNs)) {
+            timed_out();
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t sfa = tmem + S::kAcc + slot * S::kSf, sfb = sfa + 4;
+          ptx::tmem_cp_32x128b_warpx4(sfa, ptx::desc_rows16(sbase + S::kSfa + slot * kChunk));
+#pragma unroll
+          for (int c = 0; c < S::kChunks; ++c)
+            ptx::tmem_cp_32x128b_warpx4(
+                sfb + 4 * c,
+                ptx::desc_rows16(sbase + S::kSfb + (slot * S::kChunks + c) * kChunk));
+          const uint32_t a = sbase + slot * kWStage, b = sbase + S::kX + slot * S::kXStage;
+#pragma unroll
+          for (uint32_t kb = 0; kb < 4; ++kb) {
+            ptx::mma_mxf8(acc, ptx::desc_kmajor_sw128(a + 32 * kb),
+                          ptx::desc_kmajor_sw128(b + 32 * kb), idesc | kb << 4 | kb << 29,
+                          accumulate, sfa, sfb);
+            accumulate = 1;
+          }
+          ptx::mma_commit(bar_empty + 8 * slot);
+        }
+        before += count;
+        ++use;
+        if (ok) ptx::mma_commit(bar_acc_full + 8 * buffer);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp % 4;  // the tensor memory lanes this warp reaches
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    uint8_t* const staging = smem + S::kStaging + (warp - 2) * 640;
+    // Gated: an even quarter has the gates, the odd one after it the ups.
+    const int pair = quarter / 2;
+    const bool gates = quarter % 2 == 0;
+    float* const exchange = reinterpret_cast<float*>(smem + S::kExchange) + pair * 512 + lane;
+    int flip = 0;
+    // Eight rows' sums of this lane's row of W.
+    const auto finish = [&](const Segment& s, int c, const float (&v)[8]) {
+      const int row = s.row + c, live = s.rows - c;
+      if constexpr (kGated) {
+        float* const box = exchange + flip * 256;
+        flip ^= 1;  // the other half is read until the next barrier at most
+#pragma unroll
+        for (int j = 0; j < 4; ++j) box[(gates ? 4 + j : j) * 32] = v[gates ? 4 + j : j];
+        pair_barrier(pair);
+        float h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float other = box[(gates ? j : 4 + j) * 32];
+          const float g = gates ? v[j] : other, u = gates ? other : v[4 + j];
+          h[j] = g / (1.0f + __expf(-g)) * u;
+        }
+        const int first = gates ? 0 : 4;
+        store_block<4>(p, h, row + first, min(4, live - first), s.w_tile * 64 + pair * 32, staging);
+      } else {
+        store_block<8>(p, v, row, min(8, live), s.w_tile * kTileRows + quarter * 32, staging);
+      }
+    };
+    uint32_t before = 0, use = 0;
+    while (share.next(s)) {
+      const uint32_t count = s.kt1 - s.kt0, buffer = use & 1;
+      if (!ptx::mbar_wait(bar_acc_full + 8 * buffer, (use >> 1) & 1, kWaitNs)) {
+        timed_out();
+        break;
+      }
+      ptx::tc_fence_after();
+      const bool whole = s.kt0 == 0 && s.kt1 == p.k_tiles;
+      const int lo = whole ? 0 : share.owner(s.left * p.k_tiles);
+      const int hi = whole ? 0 : share.owner((s.left + 1) * p.k_tiles - 1);
+      // A CTA's run has two cut tiles at most: its first and its last.
+      const auto place = [&](int cta) {
+        const int second = share.run_begin(cta) < s.left * p.k_tiles ? 1 : 0;
+        return p.partial + static_cast<size_t>(2 * cta + second) * kTileRows * S::kCols +
+               quarter * 32 + lane;
+      };
+      for (int c = 0; c < s.rows; c += 8) {
+        float v[8] = {};
+#pragma unroll
+        for (uint32_t q = 0; q < S::kPipes; ++q) {
+          if ((q - before) % S::kPipes >= count) continue;  // an issuer without a stage
+          uint32_t r[8];
+          ptx::tmem_ld_32x32b_x8(tmem + lanes + (buffer * S::kPipes + q) * S::kAccSlot + c, r);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(r[j]);
+        }
+        if (whole) {
+          finish(s, c, v);
+        } else {
+          float* const to = place(share.cta);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) __stcg(to + (c + j) * kTileRows, v[j]);
+        }
+      }
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(bar_acc_empty + 8 * buffer);
+      if (!whole) {
+        __threadfence();
+        epilogue_barrier();
+        if (tid == 64) {
+          const uint32_t arrived = ptx::atom_add_acq_rel(p.tickets + s.left, 1u);
+          misc[1] = arrived == static_cast<uint32_t>(hi - lo);
+          if (misc[1]) p.tickets[s.left] = 0;  // for the next call
+        }
+        epilogue_barrier();
+        if (misc[1]) {
+          __threadfence();
+          for (int c = 0; c < s.rows; c += 8) {
+            float v[8] = {};
+            for (int cta = lo; cta <= hi; ++cta) {
+              const float* from = place(cta);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] += __ldcg(from + (c + j) * kTileRows);
+            }
+            finish(s, c, v);
+          }
+        }
+      }
+      before += count;
+      ++use;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 6) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, S::kColumns);
+  }
+}
+
+// The row of an expert's W (of `n` or 2 n) that lane a of tile j holds.
+__host__ __device__ constexpr int w_row(bool gated, int n, int j, int a) {
+  return gated ? a / 32 % 2 * n + j * 64 + a / 64 * 32 + a % 32 : j * kTileRows + a;
+}
+
+// W's scales as the tensor-memory copies read them: [expert][tile][k tile], a
+// chunk of 512 bytes each, lane a's four codes at (a % 32) 16 + (a / 32) 4.
+__global__ void __launch_bounds__(128) lay_scales_kernel(const uint8_t* scale, uint8_t* laid, int n,
+                                                         bool gated, int w_tiles, int k_tiles) {
+  ptx::launch_dependents();
+  ptx::grid_dependency_wait();
+  const int a = threadIdx.x, kt = blockIdx.x, j = blockIdx.y, e = blockIdx.z;
+  const int output = gated ? j * 64 + a / 64 * 32 + a % 32 : j * kTileRows + a;
+  uint32_t codes = 0x7F7F7F7Fu;
+  if (output < n) {
+    const size_t row = static_cast<size_t>(e) * (gated ? 2 * n : n) + w_row(gated, n, j, a);
+    codes = *reinterpret_cast<const uint32_t*>(scale + (row * k_tiles + kt) * 4);
+  }
+  uint8_t* chunk = laid + ((static_cast<size_t>(e) * w_tiles + j) * k_tiles + kt) * kChunk;
+  *reinterpret_cast<uint32_t*>(chunk + a % 32 * 16 + a / 32 * 4) = codes;
+}
+
+template <class S, bool kGated>
+cudaError_t launch_as(const CUtensorMap& w, const CUtensorMap& x, const ExpertParams& p, int sms,
+                      cudaStream_t stream) {
+  const auto kernel = expert_kernel<S, kGated>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(S::kBytes));
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.dynamicSmemBytes = S::kBytes;
+  return cudaLaunchKernelEx(&cfg, kernel, w, x, p);
+}
+
+}  // namespace
+
+size_t expert_partial_bytes(int sms) {
+  return static_cast<size_t>(sms) * 2 * kTileRows * std::max(Narrow::kCols, Wide::kCols) * 4;
+}
+bool expert_wide(int rows, int experts) { return rows > Narrow::kCols * experts; }
+int expert_cols(bool wide) { return wide ? Wide::kCols : Narrow::kCols; }
+int expert_x_box(bool wide) { return wide ? Wide::kBox : Narrow::kBox; }
+
+cudaError_t launch_expert_product(const CUtensorMap& w, const CUtensorMap& x, const ExpertParams& p,
+                                  bool wide, int sms, cudaStream_t stream) {
+  if (wide)
+    return p.gated ? launch_as<Wide, true>(w, x, p, sms, stream)
+                   : launch_as<Wide, false>(w, x, p, sms, stream);
+  return p.gated ? launch_as<Narrow, true>(w, x, p, sms, stream)
+                 : launch_as<Narrow, false>(w, x, p, sms, stream);
+}
+
+cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,
+                              int w_tiles, int k_tiles, cudaStream_t stream) {
+  lay_scales_kernel<<<dim3(k_tiles, w_tiles, experts), 128, 0, stream>>>(scale, laid, n, gated,
+                                                                         w_tiles, k_tiles);
+  return cudaGetLastError();
+}
+
+}  // namespace mxfp8

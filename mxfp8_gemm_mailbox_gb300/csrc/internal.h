@@ -185,4 +185,68 @@ size_t latent_workspace_bytes(int latent);
 cudaError_t launch_latent_attend(const LatentParams& p, int latent, void* workspace,
                                  cudaStream_t stream);
 
+// A layer of routed experts (experts_route.cu, quantize.cu, experts_product.cu).
+constexpr int kRouteTokens = 128;  // of a block
+struct RouteParams {
+  int64_t tokens, stride;  // elements between tokens' logits
+  int32_t experts, k, type, normalize;
+  const void* logits;
+  float* weight;    // [tokens][k]
+  int32_t* expert;  // [tokens][k], -1: none
+  int32_t* slot;    // [tokens][k], -1: none
+  int32_t* row;     // [tokens k] the token of a slot, -1: none
+  int32_t* begin;   // [experts + 1]
+  int32_t* counts;  // [blocks][experts], of more than one block
+};
+cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);
+struct CombineParams {
+  int32_t n, k, slots;
+  uint32_t items;  // eights of the result
+  int64_t y_stride;
+  const uint16_t* y;
+  const float* weight;
+  const int32_t* slot;
+  const uint16_t* add;  // or nullptr
+  uint16_t* out;
+  int32_t* flags;  // or nullptr
+};
+cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
+struct QuantizeParams {
+  int32_t k, format, type;
+  uint32_t items;  // sixteens of the result
+  int64_t x_rows, x_stride;
+  const void* x;
+  const int32_t* rows;  // or nullptr
+  uint8_t* codes;
+  uint8_t* scales;
+  int32_t* flags;  // or nullptr
+};
+cudaError_t launch_quantize(const QuantizeParams& p, cudaStream_t stream);
+cudaError_t launch_dequantize(const uint8_t* codes, const uint8_t* scales, void* out, int format,
+                              int type, uint32_t items, cudaStream_t stream);
+struct ExpertParams {
+  int32_t experts, n, rows;   // n: outputs
+  int32_t w_tiles, k_tiles;   // tiles of 128 rows of an expert's W, of 128 k
+  int32_t gated, format;      // of the result
+  uint32_t idesc;             // the products', without their columns
+  uint32_t w_bytes, x_bytes;  // what a tile of W, a copy of x count
+  const uint8_t* w_sf;        // laid by launch_lay_scales
+  const uint8_t* x_scale;     // [rows][4 k_tiles]
+  const int32_t* begin;       // [experts + 1], or nullptr: one expert has all rows
+  void* out;
+  uint8_t* out_scale;
+  float* partial;
+  int32_t* tickets;  // zero between calls
+  int32_t* flags;    // or nullptr
+};
+constexpr int kMaxExpertCtas = 160;
+size_t expert_partial_bytes(int ctas);
+bool expert_wide(int rows, int experts);  // which kernel
+int expert_cols(bool wide);               // rows of a tile
+int expert_x_box(bool wide);              // rows of a copy of x
+cudaError_t launch_expert_product(const CUtensorMap& w, const CUtensorMap& x, const ExpertParams& p,
+                                  bool wide, int ctas, cudaStream_t stream);
+cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,
+                              int w_tiles, int k_tiles, cudaStream_t stream);
+
 }  // namespace mxfp8

@@ -27,9 +27,9 @@
 // us = 5.2 TB/s (19 MB), values 512 -> 128 4.1 us = 4.4 TB/s (18 MB); 1 row,
 // 16 and 32 heads: 1.4 and 2.2 us, launch and two round trips to memory.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "internal.h"
+#include "mx_format.cuh"
 #include "ptx.cuh"
 
 namespace mxfp8 {
@@ -37,24 +37,6 @@ namespace {
 
 constexpr int kRope = 64;
 constexpr int kRowsPerBlock = 8;  // the B operand's columns
-
-// The E8M0 code of a block whose largest magnitude is `top`: 127 for a block
-// of zeros; top = f 2^E (1 <= f < 2) takes E - 8 for f <= 1.75, else E - 7.
-__device__ __forceinline__ uint32_t scale_code(float top) {
-  const uint32_t bits = __float_as_uint(top);
-  if (bits == 0u) return 127u;
-  const int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return static_cast<uint32_t>(min(max(e, 0), 254));
-}
-
-// Two E4M3 codes of v 2^(127 - code), the power in two exact halves (one may
-// be past FP32's range).
-__device__ __forceinline__ uint32_t to_e4m3(float a, float b, uint32_t code) {
-  const int e = 127 - static_cast<int>(code);
-  const float s = __uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23);
-  const float r = __uint_as_float(static_cast<uint32_t>(127 + e - e / 2) << 23);
-  return __nv_cvt_float2_to_fp8x2(make_float2(a * s * r, b * s * r), __NV_SATFINITE, __NV_E4M3);
-}
 
 // D (16 x 8, FP32) += A (16 x 16) B (16 x 8), BF16.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
