@@ -50,6 +50,8 @@ mxfp8_status check_matrices(const mxfp8_expert_desc* d) {
   if (d->k < 128 || d->k % 128 || d->k > 1 << 20)
     return fail(MXFP8_ERR_UNSUPPORTED,
                 "k must be a multiple of 128 up to 2^20, got " + std::to_string(d->k));
+  if (static_cast<int64_t>(d->experts) * ((d->n + 63) / 64) * (d->k / 128) > INT32_MAX)
+    return fail(MXFP8_ERR_UNSUPPORTED, "experts x n x k is past 2^31 tiles");
   return check_codes("w_format", d->w_format);
 }
 int w_tiles(const mxfp8_expert_desc& d) {
@@ -245,13 +247,14 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return cuda_fail(e, "reading the device's SM count");
-  CUtensorMap map_w, map_x;
+  ExpertMaps maps{};
   const uint32_t box = static_cast<uint32_t>(expert_x_box(wide));
   if (d->gated)
-    CHECK(encode_codes(&map_w, w, d->w_format, d->k, d->n, 2, d->experts, 32));
+    CHECK(encode_codes(&maps.w, w, d->w_format, d->k, d->n, 2, d->experts, 32));
   else
-    CHECK(encode_codes(&map_w, w, d->w_format, d->k, d->n, 1, d->experts, 128));
-  CHECK(encode_codes(&map_x, x, d->x_format, d->k, d->rows, 1, 1, box));
+    CHECK(encode_codes(&maps.w, w, d->w_format, d->k, d->n, 1, d->experts, 128));
+  CHECK(encode_codes(&maps.x, x, d->x_format, d->k, d->rows, 1, 1, box));
+  if (wide) CHECK(encode_codes(&maps.x_half, x, d->x_format, d->k, d->rows, 1, 1, box / 2));
   constexpr uint32_t kE2M1 = 5;  // the products' type codes; E4M3 is 0
   ExpertParams p{};
   p.experts = d->experts;
@@ -261,7 +264,7 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   p.k_tiles = d->k / 128;
   p.gated = d->gated;
   p.format = d->out_format;
-  p.idesc = 1u << 23 | 128u >> 4 << 24 | (d->w_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 7 : 0u) |
+  p.idesc = 1u << 23 | (wide ? 256u : 128u) >> 4 << 24 | (d->w_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 7 : 0u) |
             (d->x_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 10 : 0u);
   // A copy counts the bytes that it reads, not the places that 4-bit elements take.
   p.w_bytes = d->w_format == MXFP8_FORMAT_MXFP4 ? 128 * 64 : 128 * 128;
@@ -275,7 +278,7 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                        MXFP8_EXPERT_WORKSPACE_ZEROS);
   p.flags = flags;
-  e = launch_expert_product(map_w, map_x, p, wide, std::min(sms, kMaxExpertCtas),
+  e = launch_expert_product(maps, p, wide, std::min(sms, kMaxExpertCtas),
                             static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the experts' product");
   return MXFP8_OK;

@@ -40,8 +40,11 @@ constexpr int kTileRows = 128;  // rows of W
 constexpr uint32_t kWStage = kTileRows * 128;
 constexpr uint32_t kChunk = 512;  // scales of 128 rows, 4 blocks each
 
-template <int kCols_, int kStages_, int kPipes_, int kLanes_, int kBox_, int kMinRun_>
+template <bool kPair_, int kCols_, int kStages_, int kPipes_, int kLanes_, int kBox_, int kMinRun_,
+          int kAtOnce_>
 struct Shape {
+  static constexpr int kAtOnce = kAtOnce_;  // columns that an epilogue's warp reads together
+  static constexpr bool kPair = kPair_;     // two CTAs a tile
   static constexpr int kCols = kCols_;      // expert rows of a tile
   static constexpr int kStages = kStages_;  // of the ring
   static constexpr int kPipes = kPipes_;    // issuing warps
@@ -50,8 +53,10 @@ struct Shape {
   static constexpr int kMinRun = kMinRun_;  // k tiles of a run at least
   static constexpr int kChunks = (kCols + 127) / 128;  // scale chunks of the rows
   static constexpr int kRowsALane = (kCols + 31) / 32;
-  static constexpr uint32_t kXStage = kCols * 128;
-  static constexpr int kThreads = 192 + 32 * kPipes;
+  static constexpr int kStep = kPair ? 16 : 8;  // of a product's columns
+  static constexpr int kXRows = kPair ? kCols / 2 : kCols;  // of a CTA
+  static constexpr uint32_t kXStage = kXRows * 128;
+  static constexpr int kThreads = kPair ? 384 : 192 + 32 * kPipes;
   static constexpr uint32_t kAccSlot = kCols < 32 ? 32 : kCols;
   static constexpr uint32_t kAcc = 2 * kPipes * kAccSlot;
   static constexpr uint32_t kSf = 4 + 4 * kChunks;  // columns of a stage's scales
@@ -59,22 +64,25 @@ struct Shape {
   static_assert(kAcc + kStages * kSf <= 512, "tensor memory");
   // Each barrier is waited on by one thread in use order.
   static_assert(kStages % kPipes == 0 && kStages % kLanes == 0, "slots keep their threads");
-  static_assert(kCols % kBox == 0 && kBox % 8 == 0, "copies of whole swizzled groups");
+  static_assert(kXRows % kBox == 0 && kBox % 8 == 0, "copies of whole swizzled groups");
+  static_assert(kPair || kChunks == 1, "one chunk of scales");
+  static_assert(kCols % kAtOnce == 0, "whole reads");
+  static_assert(!kPair || (kPipes == 1 && kLanes == 1), "one issuer a pair, a copier of W, one of x");
   // Shared memory, from a 1024-byte boundary.
   static constexpr uint32_t kX = kStages * kWStage;
   static constexpr uint32_t kSfa = kX + kStages * kXStage;
   static constexpr uint32_t kSfb = kSfa + kStages * kChunk;
-  static constexpr uint32_t kExchange = kSfb + kStages * kChunk * kChunks;
-  static constexpr uint32_t kStaging = kExchange + 2 * 2 * 8 * 32 * 4;
-  static constexpr uint32_t kTables = kStaging + 4 * 8 * 80;
+  static constexpr uint32_t kExchange = kPair ? kSfa : kSfb + kStages * kChunk;
+  static constexpr uint32_t kStaging = kExchange + 2 * 2 * kAtOnce * 32 * 4;
+  static constexpr uint32_t kTables = kStaging + 4 * kAtOnce * 80;
   static constexpr uint32_t kBars = kTables + 2 * 4 * ((MXFP8_MAX_EXPERTS + 8) / 4 * 4);
   static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 4);
   static constexpr uint32_t kBytes = kMisc + 32 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
 };
 // Few rows an expert: bound by the stream of W.  Many: by the products.
-using Narrow = Shape<32, 8, 4, 4, 8, 4>;
-using Wide = Shape<128, 6, 1, 2, 32, 8>;
+using Narrow = Shape<false, 32, 8, 4, 4, 8, 4, 8>;
+using Wide = Shape<true, 224, 5, 1, 1, 112, 8, 32>;
 
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ void pair_barrier(int pair) {
@@ -92,9 +100,9 @@ struct Segment {
 struct Share {
   const int* rows;   // [experts + 1] each expert's first row
   const int* tiles;  // [experts + 1] ... first tile
-  int experts, cols, k_tiles;
-  int grid, cta, rounds, round;
-  int units, runs, at, end;  // k tiles of the cut tiles; this CTA's run
+  int experts, cols, step, k_tiles;
+  int grid, cta, rounds, round;  // in pairs where they share a tile
+  int units, runs, at, end;      // k tiles of the cut tiles; this CTA's run
 
   __device__ __forceinline__ int run_begin(int c) const {
     return static_cast<int>(static_cast<int64_t>(c) * units / runs);
@@ -102,15 +110,24 @@ struct Share {
   __device__ __forceinline__ int owner(int unit) const {
     return static_cast<int>(((static_cast<int64_t>(unit) + 1) * runs - 1) / units);
   }
-  __device__ __forceinline__ Share(const int* r, const int* t, int e, int c, int kt, int min_run)
-      : rows(r), tiles(t), experts(e), cols(c), k_tiles(kt) {
-    grid = gridDim.x;
-    cta = blockIdx.x;
+  __device__ __forceinline__ Share(const int* r, const int* t, int e, int c, int st, int kt,
+                                   int min_run, int sharers)
+      : rows(r), tiles(t), experts(e), cols(c), step(st), k_tiles(kt) {
+    grid = gridDim.x / sharers;
+    cta = blockIdx.x / sharers;
     const int all = tiles[e];
     rounds = all / grid;
     round = 0;
-    units = (all - rounds * grid) * kt;
-    runs = max(1, min(grid, units / min_run));
+    const int left = all - rounds * grid;
+    units = left * kt;
+    // A tile's pieces are runs of whole tiles' parts where two or more CTAs fit a
+    // tile, else runs of equal length where they are shorter by enough to pay for
+    // the joining, else whole tiles.
+    if (2 * left <= grid)
+      runs = left * max(1, min(grid / max(left, 1), kt / min_run));
+    else
+      runs = kt - units / grid >= 2 * min_run ? grid : left;
+    runs = max(runs, 1);
     at = end = 0;
     if (units > 0 && cta < runs) {
       at = run_begin(cta);
@@ -145,8 +162,8 @@ struct Share {
     const int count = rows[lo + 1] - rows[lo], row_tiles = (count + cols - 1) / cols;
     const int local = tile - tiles[lo];
     s.w_tile = local / row_tiles;
-    // Equal tiles of rows, in eights.
-    const int size = ((count + row_tiles - 1) / row_tiles + 7) / 8 * 8;
+    // Equal tiles of rows, in whole steps of a product.
+    const int size = ((count + row_tiles - 1) / row_tiles + step - 1) / step * step;
     const int first = (local - s.w_tile * row_tiles) * size;
     s.row = rows[lo] + first;
     s.rows = max(0, min(size, count - first));
@@ -156,7 +173,8 @@ struct Share {
 
 // The experts' first rows and first tiles, by one warp.  Rows outside 0 .. rows
 // or that go back are cut and raise the flag.
-__device__ __forceinline__ void deal(const ExpertParams& p, int cols, int* rows, int* tiles) {
+__device__ __forceinline__ void deal(const ExpertParams& p, int cols, int w_tiles, int* rows,
+                                     int* tiles) {
   const int lane = threadIdx.x % 32;
   int top = 0, sum = 0;
   bool bad = false;
@@ -182,7 +200,7 @@ __device__ __forceinline__ void deal(const ExpertParams& p, int cols, int* rows,
   __syncwarp();
   for (int e0 = 0; e0 < p.experts; e0 += 32) {
     const int e = e0 + lane;
-    const int own = e < p.experts ? (rows[e + 1] - rows[e] + cols - 1) / cols * p.w_tiles : 0;
+    const int own = e < p.experts ? (rows[e + 1] - rows[e] + cols - 1) / cols * w_tiles : 0;
     int inc = own;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -196,8 +214,8 @@ __device__ __forceinline__ void deal(const ExpertParams& p, int cols, int* rows,
   if (bad && blockIdx.x == 0 && p.flags) atomicOr(p.flags, MXFP8_FLAG_BAD_INDEX);
 }
 
-// kTokens rows' results of 32 outputs (one a lane) to memory.  `staging`: 640
-// bytes of the warp's own.
+// kTokens rows' results of 32 outputs (one a lane) to memory.  `staging`: 80 bytes a
+// row, the warp's own.
 template <int kTokens>
 __device__ __forceinline__ void store_block(const ExpertParams& p, const float (&v)[kTokens],
                                             int row, int live, int n0, uint8_t* staging) {
@@ -208,53 +226,65 @@ __device__ __forceinline__ void store_block(const ExpertParams& p, const float (
     for (int t = 0; t < kTokens; ++t)
       reinterpret_cast<__nv_bfloat16*>(staging + t * 80)[lane] = __float2bfloat16_rn(v[t]);
     __syncwarp();
-    const int t = lane / 4, c = lane % 4 * 8;
-    if (t < kTokens && t < live && n0 + c < p.n)
-      ptx::st_v4(static_cast<uint16_t*>(p.out) + static_cast<size_t>(row + t) * p.n + n0 + c,
-                 *reinterpret_cast<const uint4*>(staging + t * 80 + c * 2));
+    const int c = lane % 4 * 8;
+#pragma unroll
+    for (int t0 = 0; t0 < kTokens; t0 += 8) {
+      const int t = t0 + lane / 4;
+      if (t < kTokens && t < live && n0 + c < p.n)
+        ptx::st_v4(static_cast<uint16_t*>(p.out) + static_cast<size_t>(row + t) * p.n + n0 + c,
+                   *reinterpret_cast<const uint4*>(staging + t * 80 + c * 2));
+    }
     return;
   }
+  // Magnitudes as integers keep their order, and what is not finite lies above.
   const bool wide = p.format == MXFP8_FORMAT_MXFP8;
-  uint32_t codes[kTokens];
+  uint32_t top[kTokens];
 #pragma unroll
   for (int t = 0; t < kTokens; ++t) {
     const uint32_t bits = __float_as_uint(v[t]) & 0x7FFFFFFFu;
-    const bool finite = bits < 0x7F800000u;
-    const float top = __uint_as_float(__reduce_max_sync(~0u, finite ? bits : 0u));
+    top[t] = __reduce_max_sync(~0u, wide && bits >= 0x7F800000u ? 0u : bits);
+  }
+  uint32_t mine = 0;  // lane t: row t's scale
+#pragma unroll
+  for (int t = 0; t < kTokens; ++t) {
     if (wide) {
-      codes[t] = scale_code(top);
+      const uint32_t code = scale_code(__uint_as_float(top[t]));
+      const bool finite = (__float_as_uint(v[t]) & 0x7FFFFFFFu) < 0x7F800000u;
       staging[t * 32 + lane] = static_cast<uint8_t>(
-          to_e4m3(finite ? v[t] : __uint_as_float(0x7FC00000u), 0.0f, codes[t]));
+          to_e4m3(finite ? v[t] : __uint_as_float(0x7FC00000u), 0.0f, code));
+      if (lane == t) mine = code;
     } else {
-      const uint32_t code = scale_code_e2m1(top);
-      const bool all = __all_sync(~0u, finite);
+      const bool all = top[t] < 0x7F800000u;
+      const uint32_t code = all ? scale_code_e2m1(__uint_as_float(top[t])) : 255u;
       const float next = __shfl_down_sync(~0u, v[t], 1);
-      codes[t] = all ? code : 255u;
       if (lane % 2 == 0)
         staging[t * 16 + lane / 2] = all ? static_cast<uint8_t>(to_e2m1(v[t], next, code)) : 0;
+      if (lane == t) mine = code;
     }
   }
   __syncwarp();
   if (n0 >= p.n) return;  // past the last block: n is whole blocks
   const int bytes = wide ? 32 : 16;  // of a row's block
-  for (int i = lane; i < live * bytes / 4; i += 32) {
-    const int t = i / (bytes / 4), w = i % (bytes / 4);
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) +
-                                 (static_cast<size_t>(row + t) * p.n + n0) * bytes / 32 + w * 4) =
-        *reinterpret_cast<const uint32_t*>(staging + t * bytes + w * 4);
-  }
 #pragma unroll
-  for (int t = 0; t < kTokens; ++t)
-    if (t < live && lane == t)
-      p.out_scale[static_cast<size_t>(row + t) * (p.n / 32) + n0 / 32] =
-          static_cast<uint8_t>(codes[t]);
+  for (int i0 = 0; i0 < kTokens * 2; i0 += 32) {
+    const int t = (i0 + lane) * 16 / bytes, at = (i0 + lane) * 16 % bytes;
+    if (t < kTokens && t < live)
+      ptx::st_v4(static_cast<uint8_t*>(p.out) +
+                     (static_cast<size_t>(row + t) * p.n + n0) * bytes / 32 + at,
+                 *reinterpret_cast<const uint4*>(staging + t * bytes + at));
+  }
+  if (lane < kTokens && lane < live)
+    p.out_scale[static_cast<size_t>(row + lane) * (p.n / 32) + n0 / 32] =
+        static_cast<uint8_t>(mine);
 }
 
 template <class S, bool kGated>
 __global__ void __launch_bounds__(S::kThreads, 1)
     expert_kernel(const __grid_constant__ CUtensorMap tmap_w,
                   const __grid_constant__ CUtensorMap tmap_x,
+                  const __grid_constant__ CUtensorMap tmap_x_half,
                   const __grid_constant__ ExpertParams p) {
+  constexpr int kSharers = S::kPair ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = ptx::smem_addr(smem_raw);
   uint8_t* const smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -266,50 +296,79 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   int* const rows = reinterpret_cast<int*>(smem + S::kTables);
   int* const tiles = rows + (MXFP8_MAX_EXPERTS + 8) / 4 * 4;
 
+  const uint32_t rank = S::kPair ? ptx::cluster_ctarank() : 0;
+  // At a barrier of the CTA that issues the products.
+  const auto arrive = [&](uint32_t bar) {
+    if constexpr (S::kPair)
+      ptx::mbar_arrive_remote(ptx::map_to_rank(bar, 0));
+    else
+      ptx::mbar_arrive(bar);
+  };
+
   if (tid == 0) {
     ptx::prefetch_tensormap(&tmap_w);
     ptx::prefetch_tensormap(&tmap_x);
+    if (S::kPair) ptx::prefetch_tensormap(&tmap_x_half);
     for (int s = 0; s < S::kStages; ++s) {
-      ptx::mbar_init(bar_full + 8 * s, 33);  // the copies and the scales' warp
+      // The copies, and the warps of the scales.
+      ptx::mbar_init(bar_full + 8 * s, S::kPair ? 2 + 2 * 4 : 2);
       ptx::mbar_init(bar_empty + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(bar_acc_full + 8 * b, S::kPipes);
-      ptx::mbar_init(bar_acc_empty + 8 * b, 128);
+      ptx::mbar_init(bar_acc_empty + 8 * b, 4 * kSharers);  // the warps that read them
     }
     ptx::fence_mbarrier_init();
     ptx::fence_proxy_async_smem();
   }
   if (warp == 6) {
-    ptx::tmem_alloc(sbase + S::kMisc, S::kColumns);
-    ptx::tmem_relinquish();
+    if constexpr (S::kPair) {
+      ptx::tmem_alloc_pair(sbase + S::kMisc, S::kColumns);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(sbase + S::kMisc, S::kColumns);
+      ptx::tmem_relinquish();
+    }
     // Not before: a CTA of the next kernel must not hold what this one waits for.
     ptx::launch_dependents();
   }
   ptx::grid_dependency_wait();
-  if (warp == 0) deal(p, S::kCols, rows, tiles);
+  if (warp == 0) deal(p, S::kCols, (p.w_tiles + kSharers - 1) / kSharers, rows, tiles);
   ptx::tc_fence_before();
-  __syncthreads();
+  if constexpr (S::kPair)
+    ptx::cluster_sync();  // the pair's barriers exist
+  else
+    __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = misc[0];
   const auto timed_out = [&] {
     if (p.flags) atomicOr(p.flags, MXFP8_FLAG_GEMM_TIMEOUT);
   };
-  Share share(rows, tiles, p.experts, S::kCols, p.k_tiles, S::kMinRun);
+  Share share(rows, tiles, p.experts, S::kCols, S::kStep, p.k_tiles, S::kMinRun, kSharers);
   Segment s;
 
-  if (warp == 0) {
+  if (warp == 0 || (S::kPair && warp == 1)) {
     // ---------------------------------------------------------------- copies
     if (lane < S::kLanes) {
+      const bool of_w = warp == 0, of_x = !S::kPair || !of_w;
       uint32_t stage = lane;  // of all this CTA's stages; the slot's use: stage / kStages
       uint32_t before = 0;    // stages of the segments before
       bool ok = true;
       while (ok && share.next(s)) {
         const uint32_t count = s.kt1 - s.kt0;
-        const int boxes = (s.rows + S::kBox - 1) / S::kBox;
-        const uint32_t bytes = p.w_bytes + kChunk + static_cast<uint32_t>(boxes) * p.x_bytes;
-        const uint8_t* sf = p.w_sf + (static_cast<size_t>(s.expert) * p.w_tiles + s.w_tile) *
-                                         p.k_tiles * kChunk;
+        // A pair's CTAs have a tile of W each (the last may have none: zeros, that are not
+        // stored) and half of the columns.
+        const int w_tile = s.w_tile * kSharers + static_cast<int>(rank);
+        const int columns = (s.rows + S::kStep - 1) / S::kStep * S::kStep / kSharers;
+        const int row = s.row + static_cast<int>(rank) * columns;
+        // A pair's rows come in one copy, of all a tile may have or half of them; others by
+        // the box.
+        const bool half = S::kPair && columns <= S::kBox / 2;
+        const int boxes = S::kPair ? 1 : (columns + S::kBox - 1) / S::kBox;
+        const uint32_t x_bytes = half ? p.x_bytes / 2 : static_cast<uint32_t>(boxes) * p.x_bytes;
+        const uint32_t bytes = kSharers * ((of_w ? p.w_bytes : 0) + (of_x ? x_bytes : 0)) +
+                               (S::kPair ? 0 : kChunk);
+        const size_t chunk = static_cast<size_t>(s.expert * p.w_tiles + w_tile) * p.k_tiles;
         for (; stage < before + count; stage += S::kLanes) {
           const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
           if (!ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs)) {
@@ -319,20 +378,33 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           const uint32_t full = bar_full + 8 * slot;
           const int kt = s.kt0 + static_cast<int>(stage - before);
-          ptx::mbar_arrive_expect_tx(full, bytes);
-          const uint32_t w = sbase + slot * kWStage;
-          if constexpr (kGated) {
-            ptx::tma_load_4d(w, &tmap_w, kt * 128, s.w_tile * 64, 0, s.expert, full);
-            ptx::tma_load_4d(w + kWStage / 2, &tmap_w, kt * 128, s.w_tile * 64 + 32, 0, s.expert,
-                             full);
-          } else {
-            ptx::tma_load_4d(w, &tmap_w, kt * 128, s.w_tile * kTileRows, 0, s.expert, full);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(full, bytes);
+          const uint32_t w = sbase + slot * kWStage, x = sbase + S::kX + slot * S::kXStage;
+          const uint32_t done = S::kPair ? ptx::map_to_rank(full, 0) : full;
+          const auto load = [&](uint32_t dst, const CUtensorMap* map, int c1, int c3) {
+            if constexpr (S::kPair)
+              ptx::tma_load_4d_pair(dst, map, kt * 128, c1, 0, c3, done);
+            else
+              ptx::tma_load_4d(dst, map, kt * 128, c1, 0, c3, done);
+          };
+          if (of_w) {
+            if constexpr (kGated) {
+              load(w, &tmap_w, w_tile * 64, s.expert);
+              load(w + kWStage / 2, &tmap_w, w_tile * 64 + 32, s.expert);
+            } else {
+              load(w, &tmap_w, w_tile * kTileRows, s.expert);
+            }
+            if constexpr (!S::kPair)
+              ptx::bulk_load(sbase + S::kSfa + slot * kChunk, p.w_sf + (chunk + kt) * kChunk,
+                             kChunk, full);
           }
-          ptx::bulk_load(sbase + S::kSfa + slot * kChunk, sf + static_cast<size_t>(kt) * kChunk,
-                         kChunk, full);
-          for (int b = 0; b < boxes; ++b)
-            ptx::tma_load_4d(sbase + S::kX + slot * S::kXStage + b * S::kBox * 128, &tmap_x,
-                             kt * 128, s.row + b * S::kBox, 0, 0, full);
+          if (of_x) {
+            if (half)
+              load(x, &tmap_x_half, row, 0);
+            else
+              for (int b = 0; b < boxes; ++b)
+                load(x + b * S::kBox * 128, &tmap_x, row + b * S::kBox, 0);
+          }
         }
         before += count;
       }
@@ -342,7 +414,89 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         ptx::mbar_wait(bar_empty + 8 * (stage % S::kStages), ((stage / S::kStages) & 1) ^ 1,
                        kWaitNs);
     }
-  } else if (warp == 1) {
+  } else if (S::kPair && warp >= 8) {
+    // ------------------------- scales, from registers into tensor memory (a warp a quarter
+    // of its lanes, which all hold the same)
+    if constexpr (S::kPair) {
+      constexpr int kAhead = 4;  // k tiles loaded while those before are stored
+      const uint32_t lanes = static_cast<uint32_t>((warp - 8) * 32) << 16;
+      uint32_t stage = 0;
+      bool ok = true;
+      while (ok && share.next(s)) {
+        const int w_tile = min(s.w_tile * kSharers + static_cast<int>(rank), p.w_tiles - 1);
+        const uint8_t* const of_w =
+            p.w_sf + static_cast<size_t>(s.expert * p.w_tiles + w_tile) * p.k_tiles * kChunk +
+            lane * 16;
+        const uint8_t* of_x[S::kRowsALane];
+#pragma unroll
+        for (int i = 0; i < S::kRowsALane; ++i)
+          of_x[i] = p.x_scale + static_cast<size_t>(s.row + min(lane + 32 * i, s.rows - 1)) *
+                                    p.k_tiles * 4;
+        // Rows of scales on 16-byte boundaries give four k tiles a load.
+        const bool wide = (p.k_tiles | s.kt0) % 4 == 0;
+        uint4 a[kAhead], a_next[kAhead];
+        uint32_t b[S::kRowsALane][kAhead], b_next[S::kRowsALane][kAhead];
+        const auto load = [&](int kt) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            if (kt + j < s.kt1)
+              a_next[j] = *reinterpret_cast<const uint4*>(of_w + (kt + j) * static_cast<int>(kChunk));
+#pragma unroll
+          for (int i = 0; i < S::kRowsALane; ++i) {
+            if (32 * i >= s.rows || kt >= s.kt1) continue;
+            if (wide) {
+              const uint4 v = *reinterpret_cast<const uint4*>(of_x[i] + 4 * kt);
+              b_next[i][0] = v.x, b_next[i][1] = v.y, b_next[i][2] = v.z, b_next[i][3] = v.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < kAhead; ++j)
+                if (kt + j < s.kt1)
+                  b_next[i][j] = *reinterpret_cast<const uint32_t*>(of_x[i] + 4 * (kt + j));
+            }
+          }
+        };
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          a_next[j] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int i = 0; i < S::kRowsALane; ++i) b_next[i][j] = 0u;
+        }
+        load(s.kt0);
+        for (int kt = s.kt0; ok && kt < s.kt1; kt += kAhead) {
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            a[j] = a_next[j];
+#pragma unroll
+            for (int i = 0; i < S::kRowsALane; ++i) b[i][j] = b_next[i][j];
+          }
+          load(kt + kAhead);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            if (kt + j >= s.kt1) break;
+            const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
+            ok = __all_sync(~0u, ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs));
+            if (!ok) {
+              timed_out();
+              break;
+            }
+            const uint32_t to = tmem + lanes + S::kAcc + slot * S::kSf;
+            const uint32_t ra[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+            uint32_t rb[8] = {};
+#pragma unroll
+            for (int i = 0; i < S::kRowsALane; ++i) rb[i] = b[i][j];
+            ptx::tc_fence_after();
+            ptx::tmem_st_32x32b_x4(to, ra);
+            ptx::tmem_st_32x32b_x8(to + 4, rb);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(bar_full + 8 * slot);
+            ++stage;
+          }
+        }
+      }
+    }
+  } else if (!S::kPair && warp == 1) {
     // ------------------------------------------- the rows' scales, laid for the copy
     // Row r's four codes of a k tile at (r % 32) 16 + (r / 32 % 4) 4 of its chunk.
     // Four k tiles' loads are under way while the four before are stored.
@@ -377,30 +531,39 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         for (int j = 0; j < kAhead; ++j) {
           if (kt + j >= s.kt1) break;
           const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
-          ok = ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs);
+          ok = __all_sync(~0u, ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs));
           if (!ok) {
             timed_out();
             break;
           }
 #pragma unroll
           for (int i = 0; i < S::kRowsALane; ++i)
-            *reinterpret_cast<uint32_t*>(smem + S::kSfb + (slot * S::kChunks + i / 4) * kChunk +
-                                         lane * 16 + i % 4 * 4) = now[j][i];
+            *reinterpret_cast<uint32_t*>(smem + S::kSfb + slot * kChunk + lane * 16 + i * 4) =
+                now[j][i];
           ptx::fence_proxy_async_smem();
-          ptx::mbar_arrive(bar_full + 8 * slot);
+          __syncwarp();
+          if (lane == 0) arrive(bar_full + 8 * slot);
           ++stage;
         }
       }
     }
   } else if (warp >= 6) {
     // -------------------------------------------------------------- products
-    if (lane == 0) {
+    // (Of a pair's twelve warps the eighth has nothing to do.)
+    if (lane == 0 && rank == 0 && warp < 6 + S::kPipes) {
       const uint32_t pipe = warp - 6;
       uint32_t stage = pipe, before = 0, use = 0;  // use: segments so far
       bool ok = true;
+      const auto commit = [&](uint32_t bar) {
+        if constexpr (S::kPair)
+          ptx::mma_commit_pair(bar);
+        else
+          ptx::mma_commit(bar);
+      };
       while (ok && share.next(s)) {
         const uint32_t count = s.kt1 - s.kt0, buffer = use & 1;
-        const uint32_t columns = static_cast<uint32_t>((s.rows + 7) / 8 * 8);
+        const uint32_t columns =
+            static_cast<uint32_t>((s.rows + S::kStep - 1) / S::kStep * S::kStep);
         const uint32_t idesc = p.idesc | columns >> 3 << 17;
         const uint32_t acc = tmem + (buffer * S::kPipes + pipe) * S::kAccSlot;
         if (!ptx::mbar_wait(bar_acc_empty + 8 * buffer, ((use >> 1) & 1) ^ 1, kWaitNs)) {
@@ -418,66 +581,75 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           }
           ptx::tc_fence_after();
           const uint32_t sfa = tmem + S::kAcc + slot * S::kSf, sfb = sfa + 4;
-          ptx::tmem_cp_32x128b_warpx4(sfa, ptx::desc_rows16(sbase + S::kSfa + slot * kChunk));
-#pragma unroll
-          for (int c = 0; c < S::kChunks; ++c)
-            ptx::tmem_cp_32x128b_warpx4(
-                sfb + 4 * c,
-                ptx::desc_rows16(sbase + S::kSfb + (slot * S::kChunks + c) * kChunk));
+          if constexpr (!S::kPair) {
+            ptx::tmem_cp_32x128b_warpx4(sfa, ptx::desc_rows16(sbase + S::kSfa + slot * kChunk));
+            ptx::tmem_cp_32x128b_warpx4(sfb, ptx::desc_rows16(sbase + S::kSfb + slot * kChunk));
+          }
           const uint32_t a = sbase + slot * kWStage, b = sbase + S::kX + slot * S::kXStage;
 #pragma unroll
           for (uint32_t kb = 0; kb < 4; ++kb) {
-            ptx::mma_mxf8(acc, ptx::desc_kmajor_sw128(a + 32 * kb),
-                          ptx::desc_kmajor_sw128(b + 32 * kb), idesc | kb << 4 | kb << 29,
-                          accumulate, sfa, sfb);
+            const uint64_t ad = ptx::desc_kmajor_sw128(a + 32 * kb);
+            const uint64_t bd = ptx::desc_kmajor_sw128(b + 32 * kb);
+            if constexpr (S::kPair)
+              ptx::mma_mxf8_pair(acc, ad, bd, idesc | kb << 4 | kb << 29, accumulate, sfa, sfb);
+            else
+              ptx::mma_mxf8(acc, ad, bd, idesc | kb << 4 | kb << 29, accumulate, sfa, sfb);
             accumulate = 1;
           }
-          ptx::mma_commit(bar_empty + 8 * slot);
+          commit(bar_empty + 8 * slot);
         }
         before += count;
         ++use;
-        if (ok) ptx::mma_commit(bar_acc_full + 8 * buffer);
+        if (ok) commit(bar_acc_full + 8 * buffer);
       }
     }
   } else {
     // -------------------------------------------------------------- epilogue
     const int quarter = warp % 4;  // the tensor memory lanes this warp reaches
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    uint8_t* const staging = smem + S::kStaging + (warp - 2) * 640;
+    constexpr int kC = S::kAtOnce, kHalf = kC / 2;
+    uint8_t* const staging = smem + S::kStaging + (warp - 2) * kC * 80;
     // Gated: an even quarter has the gates, the odd one after it the ups.
     const int pair = quarter / 2;
     const bool gates = quarter % 2 == 0;
-    float* const exchange = reinterpret_cast<float*>(smem + S::kExchange) + pair * 512 + lane;
+    float* const exchange =
+        reinterpret_cast<float*>(smem + S::kExchange) + pair * 2 * kC * 32 + lane;
     int flip = 0;
-    // Eight rows' sums of this lane's row of W.
-    const auto finish = [&](const Segment& s, int c, const float (&v)[8]) {
+    // kC rows' sums of this lane's row of W.
+    const auto finish = [&](const Segment& s, int c, const float (&v)[kC]) {
       const int row = s.row + c, live = s.rows - c;
+      const int w_tile = s.w_tile * kSharers + static_cast<int>(rank);
       if constexpr (kGated) {
-        float* const box = exchange + flip * 256;
+        // Each of the pair's warps takes half of the rows: it gives the others'.
+        float* const box = exchange + flip * kC * 32;
         flip ^= 1;  // the other half is read until the next barrier at most
 #pragma unroll
-        for (int j = 0; j < 4; ++j) box[(gates ? 4 + j : j) * 32] = v[gates ? 4 + j : j];
+        for (int j = 0; j < kHalf; ++j)
+          box[(gates ? kHalf + j : j) * 32] = gates ? v[kHalf + j] : v[j];
         pair_barrier(pair);
-        float h[4];
+        float h[kHalf];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float other = box[(gates ? j : 4 + j) * 32];
-          const float g = gates ? v[j] : other, u = gates ? other : v[4 + j];
-          h[j] = g / (1.0f + __expf(-g)) * u;
+        for (int j = 0; j < kHalf; ++j) {
+          const float other = box[(gates ? j : kHalf + j) * 32];
+          const float g = gates ? v[j] : other, u = gates ? other : v[kHalf + j];
+          h[j] = __fdividef(g, 1.0f + __expf(-g)) * u;
         }
-        const int first = gates ? 0 : 4;
-        store_block<4>(p, h, row + first, min(4, live - first), s.w_tile * 64 + pair * 32, staging);
+        const int first = gates ? 0 : kHalf;
+        store_block<kHalf>(p, h, row + first, min(kHalf, live - first), w_tile * 64 + pair * 32,
+                           staging);
       } else {
-        store_block<8>(p, v, row, min(8, live), s.w_tile * kTileRows + quarter * 32, staging);
+        store_block<kC>(p, v, row, min(kC, live), w_tile * kTileRows + quarter * 32, staging);
       }
     };
     uint32_t before = 0, use = 0;
+    bool ok = true;  // else the walk goes on without waiting: all warps meet at its barriers
     while (share.next(s)) {
       const uint32_t count = s.kt1 - s.kt0, buffer = use & 1;
-      if (!ptx::mbar_wait(bar_acc_full + 8 * buffer, (use >> 1) & 1, kWaitNs)) {
+      if (ok && !ptx::mbar_wait(bar_acc_full + 8 * buffer, (use >> 1) & 1, kWaitNs)) {
         timed_out();
-        break;
+        ok = false;
       }
+      __syncwarp();
       ptx::tc_fence_after();
       const bool whole = s.kt0 == 0 && s.kt1 == p.k_tiles;
       const int lo = whole ? 0 : share.owner(s.left * p.k_tiles);
@@ -485,47 +657,58 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       // A CTA's run has two cut tiles at most: its first and its last.
       const auto place = [&](int cta) {
         const int second = share.run_begin(cta) < s.left * p.k_tiles ? 1 : 0;
-        return p.partial + static_cast<size_t>(2 * cta + second) * kTileRows * S::kCols +
+        return p.partial +
+               (static_cast<size_t>(2 * cta + second) * kSharers + rank) * kTileRows * S::kCols +
                quarter * 32 + lane;
       };
-      for (int c = 0; c < s.rows; c += 8) {
-        float v[8] = {};
+      for (int c = 0; c < s.rows; c += kC) {
+        float v[kC];
+#pragma unroll
+        for (int j = 0; j < kC; ++j) v[j] = 0.0f;
+        __syncwarp();  // the reads are a converged warp's
 #pragma unroll
         for (uint32_t q = 0; q < S::kPipes; ++q) {
           if ((q - before) % S::kPipes >= count) continue;  // an issuer without a stage
-          uint32_t r[8];
-          ptx::tmem_ld_32x32b_x8(tmem + lanes + (buffer * S::kPipes + q) * S::kAccSlot + c, r);
+          uint32_t r[kC];
+          const uint32_t from = tmem + lanes + (buffer * S::kPipes + q) * S::kAccSlot + c;
+          if constexpr (kC == 32)
+            ptx::tmem_ld_32x32b_x32(from, r);
+          else
+            ptx::tmem_ld_32x32b_x8(from, r);
           ptx::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += __uint_as_float(r[j]);
+          for (int j = 0; j < kC; ++j) v[j] += __uint_as_float(r[j]);
         }
         if (whole) {
           finish(s, c, v);
         } else {
           float* const to = place(share.cta);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) __stcg(to + (c + j) * kTileRows, v[j]);
+          for (int j = 0; j < kC; ++j) __stcg(to + (c + j) * kTileRows, v[j]);
         }
       }
       ptx::tc_fence_before();
-      ptx::mbar_arrive(bar_acc_empty + 8 * buffer);
+      __syncwarp();
+      if (lane == 0) arrive(bar_acc_empty + 8 * buffer);
       if (!whole) {
         __threadfence();
         epilogue_barrier();
         if (tid == 64) {
-          const uint32_t arrived = ptx::atom_add_acq_rel(p.tickets + s.left, 1u);
-          misc[1] = arrived == static_cast<uint32_t>(hi - lo);
-          if (misc[1]) p.tickets[s.left] = 0;  // for the next call
+          int32_t* const ticket = p.tickets + s.left * kSharers + rank;
+          misc[1] = ptx::atom_add_acq_rel(ticket, 1u) == static_cast<uint32_t>(hi - lo);
+          if (misc[1]) *ticket = 0;  // for the next call
         }
         epilogue_barrier();
         if (misc[1]) {
           __threadfence();
-          for (int c = 0; c < s.rows; c += 8) {
-            float v[8] = {};
+          for (int c = 0; c < s.rows; c += kC) {
+            float v[kC];
+#pragma unroll
+            for (int j = 0; j < kC; ++j) v[j] = 0.0f;
             for (int cta = lo; cta <= hi; ++cta) {
               const float* from = place(cta);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) v[j] += __ldcg(from + (c + j) * kTileRows);
+              for (int j = 0; j < kC; ++j) v[j] += __ldcg(from + (c + j) * kTileRows);
             }
             finish(s, c, v);
           }
@@ -535,11 +718,18 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       ++use;
     }
   }
+  __syncwarp();
   ptx::tc_fence_before();
-  __syncthreads();
+  if constexpr (S::kPair)
+    ptx::cluster_sync();  // the pair's products read both CTAs' memories
+  else
+    __syncthreads();
   if (warp == 6) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, S::kColumns);
+    if constexpr (S::kPair)
+      ptx::tmem_dealloc_pair(tmem, S::kColumns);
+    else
+      ptx::tmem_dealloc(tmem, S::kColumns);
   }
 }
 
@@ -566,41 +756,44 @@ __global__ void __launch_bounds__(128) lay_scales_kernel(const uint8_t* scale, u
 }
 
 template <class S, bool kGated>
-cudaError_t launch_as(const CUtensorMap& w, const CUtensorMap& x, const ExpertParams& p, int sms,
+cudaError_t launch_as(const ExpertMaps& maps, const ExpertParams& p, int ctas,
                       cudaStream_t stream) {
   const auto kernel = expert_kernel<S, kGated>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(S::kBytes));
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = S::kPair ? 2 : 1;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   cfg.blockDim = dim3(S::kThreads);
-  cfg.gridDim = dim3(static_cast<unsigned>(sms));
+  cfg.gridDim = dim3(static_cast<unsigned>(S::kPair ? ctas / 2 * 2 : ctas));
   cfg.dynamicSmemBytes = S::kBytes;
-  return cudaLaunchKernelEx(&cfg, kernel, w, x, p);
+  return cudaLaunchKernelEx(&cfg, kernel, maps.w, maps.x, maps.x_half, p);
 }
 
 }  // namespace
 
-size_t expert_partial_bytes(int sms) {
-  return static_cast<size_t>(sms) * 2 * kTileRows * std::max(Narrow::kCols, Wide::kCols) * 4;
+size_t expert_partial_bytes(int ctas) {
+  return static_cast<size_t>(ctas) * 2 * kTileRows * std::max(Narrow::kCols, Wide::kCols) * 4;
 }
 bool expert_wide(int rows, int experts) { return rows > Narrow::kCols * experts; }
 int expert_cols(bool wide) { return wide ? Wide::kCols : Narrow::kCols; }
 int expert_x_box(bool wide) { return wide ? Wide::kBox : Narrow::kBox; }
 
-cudaError_t launch_expert_product(const CUtensorMap& w, const CUtensorMap& x, const ExpertParams& p,
-                                  bool wide, int sms, cudaStream_t stream) {
+cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p, bool wide,
+                                  int ctas, cudaStream_t stream) {
   if (wide)
-    return p.gated ? launch_as<Wide, true>(w, x, p, sms, stream)
-                   : launch_as<Wide, false>(w, x, p, sms, stream);
-  return p.gated ? launch_as<Narrow, true>(w, x, p, sms, stream)
-                 : launch_as<Narrow, false>(w, x, p, sms, stream);
+    return p.gated ? launch_as<Wide, true>(maps, p, ctas, stream)
+                   : launch_as<Wide, false>(maps, p, ctas, stream);
+  return p.gated ? launch_as<Narrow, true>(maps, p, ctas, stream)
+                 : launch_as<Narrow, false>(maps, p, ctas, stream);
 }
 
 cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,

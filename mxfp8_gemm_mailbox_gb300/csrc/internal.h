@@ -239,13 +239,18 @@ struct ExpertParams {
   int32_t* tickets;  // zero between calls
   int32_t* flags;    // or nullptr
 };
-constexpr int kMaxExpertCtas = 160;
+constexpr int kMaxExpertCtas = 160;  // a ticket each: 640 bytes of the workspace's zeros
+static_assert(kMaxExpertCtas * 4 <= MXFP8_EXPERT_WORKSPACE_ZEROS, "tickets");
 size_t expert_partial_bytes(int ctas);
 bool expert_wide(int rows, int experts);  // which kernel
 int expert_cols(bool wide);               // rows of a tile
 int expert_x_box(bool wide);              // rows of a copy of x
-cudaError_t launch_expert_product(const CUtensorMap& w, const CUtensorMap& x, const ExpertParams& p,
-                                  bool wide, int ctas, cudaStream_t stream);
+struct ExpertMaps {
+  CUtensorMap w, x;
+  CUtensorMap x_half;  // of the wide kernel: half as many rows
+};
+cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p, bool wide,
+                                  int ctas, cudaStream_t stream);
 cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,
                               int w_tiles, int k_tiles, cudaStream_t stream);
 
