@@ -50,8 +50,8 @@ mxfp8_status check_matrices(const mxfp8_expert_desc* d) {
   if (d->k < 128 || d->k % 128 || d->k > 1 << 20)
     return fail(MXFP8_ERR_UNSUPPORTED,
                 "k must be a multiple of 128 up to 2^20, got " + std::to_string(d->k));
-  if (static_cast<int64_t>(d->experts) * ((d->n + 63) / 64) * (d->k / 128) > INT32_MAX)
-    return fail(MXFP8_ERR_UNSUPPORTED, "experts x n x k is past 2^31 tiles");
+  if (static_cast<int64_t>(d->experts) * ((d->n + 63) / 64) * d->k > INT32_MAX)
+    return fail(MXFP8_ERR_UNSUPPORTED, "experts x n x k is past 2^37");
   return check_codes("w_format", d->w_format);
 }
 int w_tiles(const mxfp8_expert_desc& d) {
@@ -59,27 +59,46 @@ int w_tiles(const mxfp8_expert_desc& d) {
   return (d.n + outputs - 1) / outputs;
 }
 
-// Codes [outermost][halves][rows][k], read in boxes of 128 x box_rows x halves;
-// those of 4 bits land as 16 in 16 bytes.
-mxfp8_status encode_codes(CUtensorMap* map, const void* base, int32_t format, int32_t k, int64_t rows,
-                          int64_t halves, int64_t outermost, uint32_t box_rows) {
+// 8-bit or 4-bit codes, the latter landing as 16 in 16 bytes: rows of `width`, `pitch`
+// bytes apart, and `depth` planes of them, in boxes of 128 x box_rows x box_depth.
+mxfp8_status encode_codes(CUtensorMap* map, const void* base, int32_t format, int64_t width,
+                          int64_t rows, int64_t pitch, int64_t depth, int64_t plane, int box_rows,
+                          int box_depth) {
   EncodeTiled fn = encode_tiled();
   if (!fn) return fail(MXFP8_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const bool narrow = format == MXFP8_FORMAT_MXFP4;
-  const cuuint64_t row = static_cast<cuuint64_t>(narrow ? k / 2 : k);
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(halves), static_cast<cuuint64_t>(outermost)};
-  const cuuint64_t strides[3] = {row, row * rows, row * rows * halves};
-  const cuuint32_t box[4] = {128, box_rows, static_cast<cuuint32_t>(halves), 1};
-  const cuuint32_t elem[4] = {1, 1, 1, 1};
-  const CUresult r =
-      fn(map, narrow ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
-         const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(depth)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(plane)};
+  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(box_depth)};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  const CUresult r = fn(
+      map,
+      format == MXFP8_FORMAT_MXFP4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
+                                   : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+      depth ? 3 : 2, const_cast<void*>(base), dims, strides, box, elem,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(MXFP8_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(r));
   return MXFP8_OK;
+}
+int row_bytes(int32_t format, int32_t k) { return format == MXFP8_FORMAT_MXFP4 ? k / 2 : k; }
+// x's rows, k_tiles of 128 k a copy: the k tiles of more than one are planes.
+mxfp8_status encode_x(CUtensorMap* map, const void* x, const mxfp8_expert_desc& d, int rows,
+                      int k_tiles) {
+  const int64_t pitch = row_bytes(d.x_format, d.k);
+  if (k_tiles == 1)
+    return encode_codes(map, x, d.x_format, d.k, d.rows, pitch, 1, pitch * d.rows, rows, 1);
+  return encode_codes(map, x, d.x_format, 128, d.rows, pitch, d.k / 128,
+                      row_bytes(d.x_format, 128), rows, k_tiles);
+}
+// k tiles of all tiles of W.
+int64_t blocks_of(const mxfp8_expert_desc& d) {
+  return static_cast<int64_t>(d.experts) * w_tiles(d) * (d.k / 128);
+}
+size_t codes_bytes(const mxfp8_expert_desc& d) {
+  return static_cast<size_t>(blocks_of(d)) * 128 * row_bytes(d.w_format, 128);
 }
 
 }  // namespace
@@ -189,20 +208,24 @@ mxfp8_status mxfp8_dequantize(const void* codes, const void* scales, int64_t row
   return MXFP8_OK;
 }
 
-size_t mxfp8_expert_scales_bytes(const mxfp8_expert_desc* d) {
+size_t mxfp8_expert_bytes(const mxfp8_expert_desc* d) {
   if (check_matrices(d) != MXFP8_OK) return 0;
-  return static_cast<size_t>(d->experts) * w_tiles(*d) * (d->k / 128) * 512;
+  return codes_bytes(*d) + static_cast<size_t>(blocks_of(*d)) * 512;
 }
 
-mxfp8_status mxfp8_expert_lay_scales(const mxfp8_expert_desc* d, const void* w_scale, void* laid,
-                                     void* stream) {
+mxfp8_status mxfp8_expert_lay(const mxfp8_expert_desc* d, const void* w, const void* w_scale,
+                              void* laid, void* stream) {
   CHECK(check_matrices(d));
+  CHECK(check_pointer("w", w, 16));
   CHECK(check_pointer("w_scale", w_scale, 4));
-  CHECK(check_pointer("laid", laid, 16));
-  const cudaError_t e = launch_lay_scales(static_cast<const uint8_t*>(w_scale),
-                                          static_cast<uint8_t*>(laid), d->experts, d->n, d->gated,
-                                          w_tiles(*d), d->k / 128, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "laying the scales");
+  CHECK(check_pointer("laid", laid, 32));
+  uint8_t* const codes = static_cast<uint8_t*>(laid);
+  const cudaError_t e =
+      launch_lay(static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(w_scale), codes,
+                 codes + codes_bytes(*d), d->experts, d->n, d->gated,
+                 d->w_format == MXFP8_FORMAT_MXFP4, w_tiles(*d), d->k / 128,
+                 static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "laying the matrices");
   return MXFP8_OK;
 }
 
@@ -210,8 +233,8 @@ size_t mxfp8_expert_workspace_bytes(void) {
   return MXFP8_EXPERT_WORKSPACE_ZEROS + expert_partial_bytes(kMaxExpertCtas);
 }
 
-mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, const void* laid,
-                                  const void* x, const void* x_scale, const int32_t* begin,
+mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, const void* x,
+                                  const void* x_scale, const int32_t* begin,
                                   void* out, void* out_scale, void* workspace,
                                   size_t workspace_bytes, int32_t* flags, void* stream) {
   CHECK(check_matrices(d));
@@ -227,12 +250,12 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   if (!begin && d->experts != 1)
     return fail(MXFP8_ERR_INVALID, "begin is NULL, and there is more than one expert");
   const bool wide = expert_wide(d->rows, d->experts);
+  const ExpertTile tile = expert_tile(wide);
   // Tiles are numbered in 31 bits, and what is left of a round in k tiles.
-  if ((static_cast<int64_t>(d->rows) / expert_cols(wide) + d->experts) * w_tiles(*d) > 1 << 30)
+  if ((static_cast<int64_t>(d->rows) / tile.rows + d->experts) * w_tiles(*d) > 1 << 30)
     return fail(MXFP8_ERR_UNSUPPORTED, "rows x n is past 2^30 tiles");
   if (d->rows == 0) return MXFP8_OK;
-  CHECK(check_pointer("w", w, 32));
-  CHECK(check_pointer("laid", laid, 16));
+  CHECK(check_pointer("laid", laid, 32));
   CHECK(check_pointer("x", x, 32));
   CHECK(check_pointer("x_scale", x_scale, 4));
   if (begin) CHECK(check_pointer("begin", begin, 4));
@@ -248,13 +271,10 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return cuda_fail(e, "reading the device's SM count");
   ExpertMaps maps{};
-  const uint32_t box = static_cast<uint32_t>(expert_x_box(wide));
-  if (d->gated)
-    CHECK(encode_codes(&maps.w, w, d->w_format, d->k, d->n, 2, d->experts, 32));
-  else
-    CHECK(encode_codes(&maps.w, w, d->w_format, d->k, d->n, 1, d->experts, 128));
-  CHECK(encode_codes(&maps.x, x, d->x_format, d->k, d->rows, 1, 1, box));
-  if (wide) CHECK(encode_codes(&maps.x_half, x, d->x_format, d->k, d->rows, 1, 1, box / 2));
+  CHECK(encode_codes(&maps.w, laid, d->w_format, 128, blocks_of(*d) * 128,
+                     row_bytes(d->w_format, 128), 0, 0, 128 * tile.k_tiles, 1));
+  CHECK(encode_x(&maps.x, x, *d, tile.x_rows, tile.k_tiles));
+  CHECK(encode_x(&maps.x_small, x, *d, tile.x_small, tile.k_tiles));
   constexpr uint32_t kE2M1 = 5;  // the products' type codes; E4M3 is 0
   ExpertParams p{};
   p.experts = d->experts;
@@ -267,9 +287,11 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   p.idesc = 1u << 23 | (wide ? 256u : 128u) >> 4 << 24 | (d->w_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 7 : 0u) |
             (d->x_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 10 : 0u);
   // A copy counts the bytes that it reads, not the places that 4-bit elements take.
-  p.w_bytes = d->w_format == MXFP8_FORMAT_MXFP4 ? 128 * 64 : 128 * 128;
-  p.x_bytes = d->x_format == MXFP8_FORMAT_MXFP4 ? box * 64 : box * 128;
-  p.w_sf = static_cast<const uint8_t*>(laid);
+  const uint32_t x_row = tile.k_tiles * (d->x_format == MXFP8_FORMAT_MXFP4 ? 64 : 128);
+  p.w_bytes = 128 * tile.k_tiles * (d->w_format == MXFP8_FORMAT_MXFP4 ? 64 : 128);
+  p.x_bytes = tile.x_rows * x_row;
+  p.x_small_bytes = tile.x_small * x_row;
+  p.w_sf = static_cast<const uint8_t*>(laid) + codes_bytes(*d);
   p.x_scale = static_cast<const uint8_t*>(x_scale);
   p.begin = begin;
   p.out = out;

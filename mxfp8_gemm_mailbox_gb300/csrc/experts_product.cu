@@ -37,42 +37,42 @@ namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kTileRows = 128;  // rows of W
-constexpr uint32_t kWStage = kTileRows * 128;
+constexpr uint32_t kWTile = kTileRows * 128;  // in shared memory, of 128 k
 constexpr uint32_t kChunk = 512;  // scales of 128 rows, 4 blocks each
 
-template <bool kPair_, int kCols_, int kStages_, int kPipes_, int kLanes_, int kBox_, int kMinRun_,
+template <bool kPair_, int kCols_, int kTiles_, int kStages_, int kPipes_, int kSmall_, int kMinRun_,
           int kAtOnce_>
 struct Shape {
-  static constexpr int kAtOnce = kAtOnce_;  // columns that an epilogue's warp reads together
   static constexpr bool kPair = kPair_;     // two CTAs a tile
   static constexpr int kCols = kCols_;      // expert rows of a tile
+  static constexpr int kTiles = kTiles_;    // k tiles of a stage
   static constexpr int kStages = kStages_;  // of the ring
   static constexpr int kPipes = kPipes_;    // issuing warps
-  static constexpr int kLanes = kLanes_;    // copying lanes
-  static constexpr int kBox = kBox_;        // rows of a copy of x
-  static constexpr int kMinRun = kMinRun_;  // k tiles of a run at least
+  static constexpr int kMinRun = kMinRun_;  // stages of a run at least
+  static constexpr int kAtOnce = kAtOnce_;  // columns that an epilogue's warp reads together
   static constexpr int kChunks = (kCols + 127) / 128;  // scale chunks of the rows
   static constexpr int kRowsALane = (kCols + 31) / 32;
   static constexpr int kStep = kPair ? 16 : 8;  // of a product's columns
-  static constexpr int kXRows = kPair ? kCols / 2 : kCols;  // of a CTA
-  static constexpr uint32_t kXStage = kXRows * 128;
+  static constexpr int kXRows = kPair ? kCols / 2 : kCols;  // rows of a copy of x: all of a CTA's,
+  static constexpr int kSmall = kSmall_;                    // or where there are no more than these
+  static constexpr uint32_t kXTile = kXRows * 128;
   static constexpr int kThreads = kPair ? 384 : 192 + 32 * kPipes;
   static constexpr uint32_t kAccSlot = kCols < 32 ? 32 : kCols;
   static constexpr uint32_t kAcc = 2 * kPipes * kAccSlot;
-  static constexpr uint32_t kSf = 4 + 4 * kChunks;  // columns of a stage's scales
-  static constexpr uint32_t kColumns = kAcc + kStages * kSf <= 256 ? 256 : 512;
-  static_assert(kAcc + kStages * kSf <= 512, "tensor memory");
+  static constexpr uint32_t kSf = 4 + 4 * kChunks;  // columns of a k tile's scales
+  static constexpr uint32_t kUsed = kAcc + kStages * kTiles * kSf;
+  static constexpr uint32_t kColumns = kUsed <= 256 ? 256 : 512;
+  static_assert(kUsed <= 512, "tensor memory");
   // Each barrier is waited on by one thread in use order.
-  static_assert(kStages % kPipes == 0 && kStages % kLanes == 0, "slots keep their threads");
-  static_assert(kXRows % kBox == 0 && kBox % 8 == 0, "copies of whole swizzled groups");
-  static_assert(kPair || kChunks == 1, "one chunk of scales");
+  static_assert(kStages % kPipes == 0, "slots keep their issuers");
+  static_assert(kXRows % 8 == 0 && kSmall % 8 == 0, "copies of whole swizzled groups");
+  static_assert(kPair ? kPipes == 1 && kTiles == 1 : kChunks == 1, "scales");
   static_assert(kCols % kAtOnce == 0, "whole reads");
-  static_assert(!kPair || (kPipes == 1 && kLanes == 1), "one issuer a pair, a copier of W, one of x");
   // Shared memory, from a 1024-byte boundary.
-  static constexpr uint32_t kX = kStages * kWStage;
-  static constexpr uint32_t kSfa = kX + kStages * kXStage;
-  static constexpr uint32_t kSfb = kSfa + kStages * kChunk;
-  static constexpr uint32_t kExchange = kPair ? kSfa : kSfb + kStages * kChunk;
+  static constexpr uint32_t kX = kStages * kTiles * kWTile;
+  static constexpr uint32_t kSfa = kX + kStages * kTiles * kXTile;
+  static constexpr uint32_t kSfb = kSfa + kStages * kTiles * kChunk;
+  static constexpr uint32_t kExchange = kPair ? kSfa : kSfb + kStages * kTiles * kChunk;
   static constexpr uint32_t kStaging = kExchange + 2 * 2 * kAtOnce * 32 * 4;
   static constexpr uint32_t kTables = kStaging + 4 * kAtOnce * 80;
   static constexpr uint32_t kBars = kTables + 2 * 4 * ((MXFP8_MAX_EXPERTS + 8) / 4 * 4);
@@ -81,8 +81,8 @@ struct Shape {
   static_assert(kBytes <= 232448, "shared memory");
 };
 // Few rows an expert: bound by the stream of W.  Many: by the products.
-using Narrow = Shape<false, 32, 8, 4, 4, 8, 4, 8>;
-using Wide = Shape<true, 224, 5, 1, 1, 112, 8, 32>;
+using Narrow = Shape<false, 32, 2, 5, 5, 8, 2, 8>;
+using Wide = Shape<true, 224, 1, 5, 1, 56, 8, 32>;
 
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ void pair_barrier(int pair) {
@@ -92,44 +92,48 @@ __device__ __forceinline__ void pair_barrier(int pair) {
 // A run of k tiles of one tile.
 struct Segment {
   int expert, row, rows, w_tile;  // rows: of the tile
-  int kt0, kt1;
+  int kt0, kt1;  // whole stages, but for the last of a tile
   int left;  // which of the tiles that are cut into runs, -1: a whole round's
 };
 
-// The segments of a CTA, in order; every role walks the same list.
+// The segments of a CTA, in order; every role walks the same list.  (Divisions of 32
+// bits: a run's end is below 160 x 160 x 8192.)
+template <class S>
 struct Share {
   const int* rows;   // [experts + 1] each expert's first row
   const int* tiles;  // [experts + 1] ... first tile
-  int experts, cols, step, k_tiles;
+  int experts, k_tiles, stages;  // stages of a tile
   int grid, cta, rounds, round;  // in pairs where they share a tile
-  int units, runs, at, end;      // k tiles of the cut tiles; this CTA's run
+  uint32_t units, runs;          // stages of the cut tiles
+  int at, end;                   // this CTA's run
 
   __device__ __forceinline__ int run_begin(int c) const {
-    return static_cast<int>(static_cast<int64_t>(c) * units / runs);
+    return static_cast<int>(static_cast<uint32_t>(c) * units / runs);
   }
   __device__ __forceinline__ int owner(int unit) const {
-    return static_cast<int>(((static_cast<int64_t>(unit) + 1) * runs - 1) / units);
+    return static_cast<int>((static_cast<uint32_t>(unit + 1) * runs - 1) / units);
   }
-  __device__ __forceinline__ Share(const int* r, const int* t, int e, int c, int st, int kt,
-                                   int min_run, int sharers)
-      : rows(r), tiles(t), experts(e), cols(c), step(st), k_tiles(kt) {
-    grid = gridDim.x / sharers;
-    cta = blockIdx.x / sharers;
-    const int all = tiles[e];
-    rounds = all / grid;
+  __device__ __forceinline__ Share(const int* r, const int* t, int e, int kt)
+      : rows(r), tiles(t), experts(e), k_tiles(kt) {
+    constexpr int kSharers = S::kPair ? 2 : 1;
+    stages = (kt + S::kTiles - 1) / S::kTiles;
+    grid = gridDim.x / kSharers;
+    cta = blockIdx.x / kSharers;
+    const uint32_t all = static_cast<uint32_t>(tiles[e]);
+    rounds = static_cast<int>(all / static_cast<uint32_t>(grid));
     round = 0;
-    const int left = all - rounds * grid;
-    units = left * kt;
+    const int left = static_cast<int>(all) - rounds * grid;
+    units = static_cast<uint32_t>(left * stages);
     // A tile's pieces are runs of whole tiles' parts where two or more CTAs fit a
     // tile, else runs of equal length where they are shorter by enough to pay for
     // the joining, else whole tiles.
     if (2 * left <= grid)
-      runs = left * max(1, min(grid / max(left, 1), kt / min_run));
+      runs = left * max(1, min(grid / max(left, 1), stages / S::kMinRun));
     else
-      runs = kt - units / grid >= 2 * min_run ? grid : left;
-    runs = max(runs, 1);
+      runs = stages - static_cast<int>(units / grid) >= 2 * S::kMinRun ? grid : left;
+    runs = max(runs, 1u);
     at = end = 0;
-    if (units > 0 && cta < runs) {
+    if (units > 0 && cta < static_cast<int>(runs)) {
       at = run_begin(cta);
       end = run_begin(cta + 1);
     }
@@ -142,75 +146,100 @@ struct Share {
       s.kt1 = k_tiles;
       s.left = -1;
     } else if (at < end) {
-      s.left = at / k_tiles;
+      s.left = static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(stages));
       tile = rounds * grid + s.left;
-      s.kt0 = at - s.left * k_tiles;
-      s.kt1 = min(k_tiles, s.kt0 + end - at);
-      at += s.kt1 - s.kt0;
+      const int from = at - s.left * stages, to = min(stages, from + end - at);
+      s.kt0 = from * S::kTiles;
+      s.kt1 = min(k_tiles, to * S::kTiles);
+      at += to - from;
     } else {
       return false;
     }
-    int lo = 0, hi = experts - 1;  // the last expert whose first tile is not past this one
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) / 2;
-      if (tiles[mid] <= tile)
-        lo = mid;
-      else
-        hi = mid - 1;
+    // The last expert whose first tile is not past this one: eight at a time, whose loads
+    // do not wait for one another.
+    int lo = 0;
+    static_assert(MXFP8_MAX_EXPERTS <= 512, "three steps of eight");
+#pragma unroll
+    for (int step = 64; step > 0; step /= 8) {
+      if (step >= experts) continue;
+      int past = 0;
+#pragma unroll
+      for (int i = 1; i < 8; ++i) {
+        const int e = lo + i * step;
+        past += e < experts && tiles[min(e, experts)] <= tile;
+      }
+      lo += past * step;
     }
     s.expert = lo;
-    const int count = rows[lo + 1] - rows[lo], row_tiles = (count + cols - 1) / cols;
-    const int local = tile - tiles[lo];
-    s.w_tile = local / row_tiles;
-    // Equal tiles of rows, in whole steps of a product.
-    const int size = ((count + row_tiles - 1) / row_tiles + step - 1) / step * step;
-    const int first = (local - s.w_tile * row_tiles) * size;
+    const uint32_t count = rows[lo + 1] - rows[lo];
+    const uint32_t row_tiles = (count + S::kCols - 1) / S::kCols;
+    const uint32_t local = tile - tiles[lo];
+    s.w_tile = local;
+    int first = 0, size = count;
+    if (row_tiles > 1) {  // equal tiles of rows, in whole steps of a product
+      s.w_tile = local / row_tiles;
+      size = ((count + row_tiles - 1) / row_tiles + S::kStep - 1) / S::kStep * S::kStep;
+      first = (local - s.w_tile * row_tiles) * size;
+    }
     s.row = rows[lo] + first;
-    s.rows = max(0, min(size, count - first));
+    s.rows = min(size, static_cast<int>(count) - first);
     return true;
+  }
+  __device__ __forceinline__ uint32_t count(const Segment& s) const {  // stages
+    return static_cast<uint32_t>((s.kt1 - s.kt0 + S::kTiles - 1) / S::kTiles);
   }
 };
 
-// The experts' first rows and first tiles, by one warp.  Rows outside 0 .. rows
-// or that go back are cut and raise the flag.
+// The experts' first rows and first tiles.  Rows outside 0 .. rows or that go back are
+// cut and raise the flag.  All threads load (one latency), one warp adds, a run of
+// consecutive experts a lane.
 __device__ __forceinline__ void deal(const ExpertParams& p, int cols, int w_tiles, int* rows,
                                      int* tiles) {
-  const int lane = threadIdx.x % 32;
-  int top = 0, sum = 0;
   bool bad = false;
-  for (int e0 = 0; e0 <= p.experts; e0 += 32) {
-    const int e = e0 + lane;
-    int b = 0;
-    if (e <= p.experts) {
-      const int given = p.begin ? p.begin[e] : e * p.rows;  // without begin: one expert
-      b = min(max(given, 0), p.rows);
-      bad |= given != b;
-    }
-    int m = b;
+  for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) {
+    const int given = p.begin ? p.begin[e] : e * p.rows;  // without begin: one expert
+    const int b = min(max(given, 0), p.rows);
+    bad |= given != b;
+    rows[e] = b;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x, per = (p.experts + 32) / 32;
+    const int from = min(lane * per, p.experts + 1), to = min(from + per, p.experts + 1);
+    int top = 0;
+    for (int e = from; e < to; ++e) top = max(top, rows[e]);
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const int up = __shfl_up_sync(~0u, m, o);
-      if (lane >= o) m = max(m, up);
+      const int up = __shfl_up_sync(~0u, top, o);
+      if (lane >= o) top = max(top, up);
     }
-    m = max(m, top);
-    bad |= e <= p.experts && m != b;
-    if (e <= p.experts) rows[e] = m;
-    top = __shfl_sync(~0u, m, 31);
-  }
-  __syncwarp();
-  for (int e0 = 0; e0 < p.experts; e0 += 32) {
-    const int e = e0 + lane;
-    const int own = e < p.experts ? (rows[e + 1] - rows[e] + cols - 1) / cols * w_tiles : 0;
-    int inc = own;
+    int last = __shfl_up_sync(~0u, top, 1);  // the largest before this lane's
+    if (lane == 0) last = 0;
+    int sum = 0;
+    const int before = last;
+    for (int e = from; e < to; ++e) {
+      const int b = rows[e], m = max(b, last);
+      bad |= m != b;
+      rows[e] = m;
+      if (e > 0) sum += (m - last + cols - 1) / cols * w_tiles;
+      last = m;
+    }
+    int inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int up = __shfl_up_sync(~0u, inc, o);
       if (lane >= o) inc += up;
     }
-    if (e < p.experts) tiles[e] = sum + inc - own;
-    sum += __shfl_sync(~0u, inc, 31);
+    // tiles[e]: of the experts before e.
+    int at = inc - sum;
+    last = before;
+    for (int e = from; e < to; ++e) {
+      const int m = rows[e];
+      if (e > 0) at += (m - last + cols - 1) / cols * w_tiles;
+      tiles[e] = at;
+      last = m;
+    }
   }
-  if (lane == 0) tiles[p.experts] = sum;
   if (bad && blockIdx.x == 0 && p.flags) atomicOr(p.flags, MXFP8_FLAG_BAD_INDEX);
 }
 
@@ -282,7 +311,7 @@ template <class S, bool kGated>
 __global__ void __launch_bounds__(S::kThreads, 1)
     expert_kernel(const __grid_constant__ CUtensorMap tmap_w,
                   const __grid_constant__ CUtensorMap tmap_x,
-                  const __grid_constant__ CUtensorMap tmap_x_half,
+                  const __grid_constant__ CUtensorMap tmap_x_small,
                   const __grid_constant__ ExpertParams p) {
   constexpr int kSharers = S::kPair ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -308,7 +337,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   if (tid == 0) {
     ptx::prefetch_tensormap(&tmap_w);
     ptx::prefetch_tensormap(&tmap_x);
-    if (S::kPair) ptx::prefetch_tensormap(&tmap_x_half);
+    ptx::prefetch_tensormap(&tmap_x_small);
     for (int s = 0; s < S::kStages; ++s) {
       // The copies, and the warps of the scales.
       ptx::mbar_init(bar_full + 8 * s, S::kPair ? 2 + 2 * 4 : 2);
@@ -333,7 +362,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     ptx::launch_dependents();
   }
   ptx::grid_dependency_wait();
-  if (warp == 0) deal(p, S::kCols, (p.w_tiles + kSharers - 1) / kSharers, rows, tiles);
+  deal(p, S::kCols, (p.w_tiles + kSharers - 1) / kSharers, rows, tiles);
   ptx::tc_fence_before();
   if constexpr (S::kPair)
     ptx::cluster_sync();  // the pair's barriers exist
@@ -344,32 +373,26 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   const auto timed_out = [&] {
     if (p.flags) atomicOr(p.flags, MXFP8_FLAG_GEMM_TIMEOUT);
   };
-  Share share(rows, tiles, p.experts, S::kCols, S::kStep, p.k_tiles, S::kMinRun, kSharers);
+  Share<S> share(rows, tiles, p.experts, p.k_tiles);
   Segment s;
 
   if (warp == 0 || (S::kPair && warp == 1)) {
     // ---------------------------------------------------------------- copies
-    if (lane < S::kLanes) {
+    // (A copy costs its thread some 90 clocks, whatever its size.)
+    if (lane == 0) {
       const bool of_w = warp == 0, of_x = !S::kPair || !of_w;
-      uint32_t stage = lane;  // of all this CTA's stages; the slot's use: stage / kStages
-      uint32_t before = 0;    // stages of the segments before
+      uint32_t stage = 0;  // of all this CTA's stages; the slot's use: stage / kStages
       bool ok = true;
       while (ok && share.next(s)) {
-        const uint32_t count = s.kt1 - s.kt0;
-        // A pair's CTAs have a tile of W each (the last may have none: zeros, that are not
-        // stored) and half of the columns.
+        // A pair's CTAs have a tile of W each (the last may have none: what comes of the one
+        // it takes then is not stored) and half of the columns.
         const int w_tile = s.w_tile * kSharers + static_cast<int>(rank);
         const int columns = (s.rows + S::kStep - 1) / S::kStep * S::kStep / kSharers;
         const int row = s.row + static_cast<int>(rank) * columns;
-        // A pair's rows come in one copy, of all a tile may have or half of them; others by
-        // the box.
-        const bool half = S::kPair && columns <= S::kBox / 2;
-        const int boxes = S::kPair ? 1 : (columns + S::kBox - 1) / S::kBox;
-        const uint32_t x_bytes = half ? p.x_bytes / 2 : static_cast<uint32_t>(boxes) * p.x_bytes;
-        const uint32_t bytes = kSharers * ((of_w ? p.w_bytes : 0) + (of_x ? x_bytes : 0)) +
-                               (S::kPair ? 0 : kChunk);
-        const size_t chunk = static_cast<size_t>(s.expert * p.w_tiles + w_tile) * p.k_tiles;
-        for (; stage < before + count; stage += S::kLanes) {
+        const bool small = columns <= S::kSmall;
+        const uint32_t x_bytes = small ? p.x_small_bytes : p.x_bytes;
+        const int w = (s.expert * p.w_tiles + min(w_tile, p.w_tiles - 1)) * p.k_tiles;
+        for (int kt = s.kt0; kt < s.kt1; kt += S::kTiles, ++stage) {
           const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
           if (!ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs)) {
             timed_out();
@@ -377,40 +400,28 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             break;
           }
           const uint32_t full = bar_full + 8 * slot;
-          const int kt = s.kt0 + static_cast<int>(stage - before);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(full, bytes);
-          const uint32_t w = sbase + slot * kWStage, x = sbase + S::kX + slot * S::kXStage;
+          const uint32_t chunks = S::kPair ? 0 : min(S::kTiles, s.kt1 - kt) * kChunk;
+          if (rank == 0)
+            ptx::mbar_arrive_expect_tx(
+                full, kSharers * ((of_w ? p.w_bytes : 0) + (of_x ? x_bytes : 0)) + chunks);
           const uint32_t done = S::kPair ? ptx::map_to_rank(full, 0) : full;
-          const auto load = [&](uint32_t dst, const CUtensorMap* map, int c1, int c3) {
-            if constexpr (S::kPair)
-              ptx::tma_load_4d_pair(dst, map, kt * 128, c1, 0, c3, done);
-            else
-              ptx::tma_load_4d(dst, map, kt * 128, c1, 0, c3, done);
-          };
           if (of_w) {
-            if constexpr (kGated) {
-              load(w, &tmap_w, w_tile * 64, s.expert);
-              load(w + kWStage / 2, &tmap_w, w_tile * 64 + 32, s.expert);
-            } else {
-              load(w, &tmap_w, w_tile * kTileRows, s.expert);
-            }
+            ptx::tma_load_2d<S::kPair>(sbase + slot * S::kTiles * kWTile, &tmap_w, 0,
+                                       (w + kt) * kTileRows, done);
             if constexpr (!S::kPair)
-              ptx::bulk_load(sbase + S::kSfa + slot * kChunk, p.w_sf + (chunk + kt) * kChunk,
-                             kChunk, full);
+              ptx::bulk_load(sbase + S::kSfa + slot * S::kTiles * kChunk,
+                             p.w_sf + static_cast<size_t>(w + kt) * kChunk, chunks, full);
           }
-          if (of_x) {
-            if (half)
-              load(x, &tmap_x_half, row, 0);
-            else
-              for (int b = 0; b < boxes; ++b)
-                load(x + b * S::kBox * 128, &tmap_x, row + b * S::kBox, 0);
-          }
+          if (of_x)
+            ptx::tma_load_3d<S::kPair>(sbase + S::kX + slot * S::kTiles * S::kXTile,
+                                       small ? &tmap_x_small : &tmap_x,
+                                       S::kTiles == 1 ? kt * 128 : 0, row,
+                                       S::kTiles == 1 ? 0 : kt, done);
         }
-        before += count;
       }
-      // The products that read this lane's last stages are done before the CTA
-      // leaves, and with them the copies.
-      for (int i = 0; i < S::kStages / S::kLanes; ++i, stage += S::kLanes)
+      // The products that read the last stages are done before the CTA leaves, and
+      // with them the copies.
+      for (int i = 0; i < S::kStages; ++i, ++stage)
         ptx::mbar_wait(bar_empty + 8 * (stage % S::kStages), ((stage / S::kStages) & 1) ^ 1,
                        kWaitNs);
     }
@@ -498,17 +509,18 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
   } else if (!S::kPair && warp == 1) {
     // ------------------------------------------- the rows' scales, laid for the copy
-    // Row r's four codes of a k tile at (r % 32) 16 + (r / 32 % 4) 4 of its chunk.
-    // Four k tiles' loads are under way while the four before are stored.
+    // Row r's four codes of a k tile at (r % 32) 16 + (r / 32) 4 of its chunk.  Four k
+    // tiles' loads are under way while the four before are stored.
     constexpr int kAhead = 4;
+    static_assert(kAhead % S::kTiles == 0, "whole stages");
     uint32_t stage = 0;
     bool ok = true;
-    const size_t stride = static_cast<size_t>(p.k_tiles) * 4;
     while (ok && share.next(s)) {
       const uint8_t* at[S::kRowsALane];
 #pragma unroll
       for (int i = 0; i < S::kRowsALane; ++i)
-        at[i] = p.x_scale + min(s.row + min(lane + 32 * i, s.rows - 1), p.rows - 1) * stride;
+        at[i] = p.x_scale +
+                static_cast<size_t>(s.row + min(lane + 32 * i, s.rows - 1)) * p.k_tiles * 4;
       uint32_t next[kAhead][S::kRowsALane];
       const auto load = [&](int kt) {
 #pragma unroll
@@ -528,8 +540,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           for (int i = 0; i < S::kRowsALane; ++i) now[j][i] = next[j][i];
         load(kt + kAhead);
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (kt + j >= s.kt1) break;
+        for (int j0 = 0; j0 < kAhead; j0 += S::kTiles) {
+          if (kt + j0 >= s.kt1) break;
           const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
           ok = __all_sync(~0u, ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs));
           if (!ok) {
@@ -537,9 +549,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             break;
           }
 #pragma unroll
-          for (int i = 0; i < S::kRowsALane; ++i)
-            *reinterpret_cast<uint32_t*>(smem + S::kSfb + slot * kChunk + lane * 16 + i * 4) =
-                now[j][i];
+          for (int j = 0; j < S::kTiles; ++j)
+#pragma unroll
+            for (int i = 0; i < S::kRowsALane; ++i)
+              *reinterpret_cast<uint32_t*>(smem + S::kSfb + (slot * S::kTiles + j) * kChunk +
+                                           lane * 16 + i * 4) = now[j0 + j][i];
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) arrive(bar_full + 8 * slot);
@@ -561,10 +575,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           ptx::mma_commit(bar);
       };
       while (ok && share.next(s)) {
-        const uint32_t count = s.kt1 - s.kt0, buffer = use & 1;
+        const uint32_t count = share.count(s), buffer = use & 1;
         const uint32_t columns =
             static_cast<uint32_t>((s.rows + S::kStep - 1) / S::kStep * S::kStep);
         const uint32_t idesc = p.idesc | columns >> 3 << 17;
+        const uint32_t x_tile = (columns / kSharers <= S::kSmall ? S::kSmall : S::kXRows) * 128;
         const uint32_t acc = tmem + (buffer * S::kPipes + pipe) * S::kAccSlot;
         if (!ptx::mbar_wait(bar_acc_empty + 8 * buffer, ((use >> 1) & 1) ^ 1, kWaitNs)) {
           timed_out();
@@ -580,21 +595,28 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             break;
           }
           ptx::tc_fence_after();
-          const uint32_t sfa = tmem + S::kAcc + slot * S::kSf, sfb = sfa + 4;
-          if constexpr (!S::kPair) {
-            ptx::tmem_cp_32x128b_warpx4(sfa, ptx::desc_rows16(sbase + S::kSfa + slot * kChunk));
-            ptx::tmem_cp_32x128b_warpx4(sfb, ptx::desc_rows16(sbase + S::kSfb + slot * kChunk));
-          }
-          const uint32_t a = sbase + slot * kWStage, b = sbase + S::kX + slot * S::kXStage;
+          const int left = s.kt1 - s.kt0 - static_cast<int>(stage - before) * S::kTiles;
 #pragma unroll
-          for (uint32_t kb = 0; kb < 4; ++kb) {
-            const uint64_t ad = ptx::desc_kmajor_sw128(a + 32 * kb);
-            const uint64_t bd = ptx::desc_kmajor_sw128(b + 32 * kb);
-            if constexpr (S::kPair)
-              ptx::mma_mxf8_pair(acc, ad, bd, idesc | kb << 4 | kb << 29, accumulate, sfa, sfb);
-            else
-              ptx::mma_mxf8(acc, ad, bd, idesc | kb << 4 | kb << 29, accumulate, sfa, sfb);
-            accumulate = 1;
+          for (int t = 0; t < S::kTiles; ++t) {
+            if (t >= left) break;
+            const uint32_t tile = slot * S::kTiles + t;
+            const uint32_t sfa = tmem + S::kAcc + tile * S::kSf, sfb = sfa + 4;
+            if constexpr (!S::kPair) {
+              ptx::tmem_cp_32x128b_warpx4(sfa, ptx::desc_rows16(sbase + S::kSfa + tile * kChunk));
+              ptx::tmem_cp_32x128b_warpx4(sfb, ptx::desc_rows16(sbase + S::kSfb + tile * kChunk));
+            }
+            const uint32_t a = sbase + tile * kWTile;
+            const uint32_t b = sbase + S::kX + slot * S::kTiles * S::kXTile + t * x_tile;
+#pragma unroll
+            for (uint32_t kb = 0; kb < 4; ++kb) {
+              const uint64_t ad = ptx::desc_kmajor_sw128(a + 32 * kb);
+              const uint64_t bd = ptx::desc_kmajor_sw128(b + 32 * kb);
+              if constexpr (S::kPair)
+                ptx::mma_mxf8_pair(acc, ad, bd, idesc | kb << 4 | kb << 29, accumulate, sfa, sfb);
+              else
+                ptx::mma_mxf8(acc, ad, bd, idesc | kb << 4 | kb << 29, accumulate, sfa, sfb);
+              accumulate = 1;
+            }
           }
           commit(bar_empty + 8 * slot);
         }
@@ -644,7 +666,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     uint32_t before = 0, use = 0;
     bool ok = true;  // else the walk goes on without waiting: all warps meet at its barriers
     while (share.next(s)) {
-      const uint32_t count = s.kt1 - s.kt0, buffer = use & 1;
+      const uint32_t count = share.count(s), buffer = use & 1;
       if (ok && !ptx::mbar_wait(bar_acc_full + 8 * buffer, (use >> 1) & 1, kWaitNs)) {
         timed_out();
         ok = false;
@@ -652,11 +674,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       __syncwarp();
       ptx::tc_fence_after();
       const bool whole = s.kt0 == 0 && s.kt1 == p.k_tiles;
-      const int lo = whole ? 0 : share.owner(s.left * p.k_tiles);
-      const int hi = whole ? 0 : share.owner((s.left + 1) * p.k_tiles - 1);
+      const int lo = whole ? 0 : share.owner(s.left * share.stages);
+      const int hi = whole ? 0 : share.owner((s.left + 1) * share.stages - 1);
       // A CTA's run has two cut tiles at most: its first and its last.
       const auto place = [&](int cta) {
-        const int second = share.run_begin(cta) < s.left * p.k_tiles ? 1 : 0;
+        const int second = share.run_begin(cta) < s.left * share.stages ? 1 : 0;
         return p.partial +
                (static_cast<size_t>(2 * cta + second) * kSharers + rank) * kTileRows * S::kCols +
                quarter * 32 + lane;
@@ -666,18 +688,22 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 #pragma unroll
         for (int j = 0; j < kC; ++j) v[j] = 0.0f;
         __syncwarp();  // the reads are a converged warp's
+        uint32_t r[S::kPipes][kC];
 #pragma unroll
         for (uint32_t q = 0; q < S::kPipes; ++q) {
-          if ((q - before) % S::kPipes >= count) continue;  // an issuer without a stage
-          uint32_t r[kC];
           const uint32_t from = tmem + lanes + (buffer * S::kPipes + q) * S::kAccSlot + c;
           if constexpr (kC == 32)
-            ptx::tmem_ld_32x32b_x32(from, r);
+            ptx::tmem_ld_32x32b_x32(from, r[q]);
           else
-            ptx::tmem_ld_32x32b_x8(from, r);
-          ptx::tmem_wait_ld();
+            ptx::tmem_ld_32x32b_x8(from, r[q]);
+        }
+        ptx::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < kC; ++j) v[j] += __uint_as_float(r[j]);
+        for (uint32_t q = 0; q < S::kPipes; ++q) {
+          if ((q + S::kPipes - before % S::kPipes) % S::kPipes >= count)
+            continue;  // an issuer without a stage
+#pragma unroll
+          for (int j = 0; j < kC; ++j) v[j] += __uint_as_float(r[q][j]);
         }
         if (whole) {
           finish(s, c, v);
@@ -691,7 +717,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       __syncwarp();
       if (lane == 0) arrive(bar_acc_empty + 8 * buffer);
       if (!whole) {
-        __threadfence();
+        // The barrier hands the warps' partials to one thread, whose arrival releases
+        // them; the last one's acquires the others' for its warps the same way.
         epilogue_barrier();
         if (tid == 64) {
           int32_t* const ticket = p.tickets + s.left * kSharers + rank;
@@ -700,7 +727,6 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         }
         epilogue_barrier();
         if (misc[1]) {
-          __threadfence();
           for (int c = 0; c < s.rows; c += kC) {
             float v[kC];
 #pragma unroll
@@ -733,26 +759,39 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   }
 }
 
-// The row of an expert's W (of `n` or 2 n) that lane a of tile j holds.
-__host__ __device__ constexpr int w_row(bool gated, int n, int j, int a) {
-  return gated ? a / 32 % 2 * n + j * 64 + a / 64 * 32 + a % 32 : j * kTileRows + a;
-}
-
-// W's scales as the tensor-memory copies read them: [expert][tile][k tile], a
-// chunk of 512 bytes each, lane a's four codes at (a % 32) 16 + (a / 32) 4.
-__global__ void __launch_bounds__(128) lay_scales_kernel(const uint8_t* scale, uint8_t* laid, int n,
-                                                         bool gated, int w_tiles, int k_tiles) {
-  ptx::launch_dependents();
-  ptx::grid_dependency_wait();
-  const int a = threadIdx.x, kt = blockIdx.x, j = blockIdx.y, e = blockIdx.z;
-  const int output = gated ? j * 64 + a / 64 * 32 + a % 32 : j * kTileRows + a;
-  uint32_t codes = 0x7F7F7F7Fu;
-  if (output < n) {
-    const size_t row = static_cast<size_t>(e) * (gated ? 2 * n : n) + w_row(gated, n, j, a);
-    codes = *reinterpret_cast<const uint32_t*>(scale + (row * k_tiles + kt) * 4);
+// W as the copies read it, [expert][tile][k tile] of 128 rows of 128 codes, and its
+// scales in the same order, 512 bytes a k tile: row a's four codes at (a % 32) 16 +
+// (a / 32) 4.  Rows past the last are zeros.  (Read in place, a copy's rows of 64 or
+// 128 bytes lie K apart: 89 us in place of NN for the gated step of 64 rows.)
+template <bool kNarrow>
+__global__ void __launch_bounds__(256)
+    lay_kernel(const uint8_t* w, const uint8_t* scale, uint8_t* laid, uint8_t* laid_scale, int n,
+               bool gated, int w_tiles, int k_tiles) {
+  constexpr int kRowBytes = kNarrow ? 64 : 128, kShares = kRowBytes / 16;
+  const int kt = blockIdx.x, j = blockIdx.y, e = blockIdx.z;
+  const size_t block = (static_cast<size_t>(e) * w_tiles + j) * k_tiles + kt;
+  const int rows = gated ? 2 * n : n;  // of an expert
+  const auto row_of = [&](int a) {     // lane a's, or -1
+    const int output = gated ? j * 64 + a / 64 * 32 + a % 32 : j * kTileRows + a;
+    return output < n ? (gated ? a / 32 % 2 * n : 0) + output : -1;
+  };
+  for (int i = threadIdx.x; i < kTileRows * kShares; i += 256) {
+    const int row = row_of(i / kShares);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (row >= 0)
+      v = *reinterpret_cast<const uint4*>(
+          w + ((static_cast<size_t>(e) * rows + row) * k_tiles + kt) * kRowBytes +
+          i % kShares * 16);
+    *reinterpret_cast<uint4*>(laid + block * kTileRows * kRowBytes + i * 16) = v;
   }
-  uint8_t* chunk = laid + ((static_cast<size_t>(e) * w_tiles + j) * k_tiles + kt) * kChunk;
-  *reinterpret_cast<uint32_t*>(chunk + a % 32 * 16 + a / 32 * 4) = codes;
+  if (threadIdx.x < kTileRows) {
+    const int a = threadIdx.x, row = row_of(a);
+    uint32_t codes = 0x7F7F7F7Fu;
+    if (row >= 0)
+      codes = *reinterpret_cast<const uint32_t*>(
+          scale + ((static_cast<size_t>(e) * rows + row) * k_tiles + kt) * 4);
+    *reinterpret_cast<uint32_t*>(laid_scale + block * kChunk + a % 32 * 16 + a / 32 * 4) = codes;
+  }
 }
 
 template <class S, bool kGated>
@@ -775,7 +814,7 @@ cudaError_t launch_as(const ExpertMaps& maps, const ExpertParams& p, int ctas,
   cfg.blockDim = dim3(S::kThreads);
   cfg.gridDim = dim3(static_cast<unsigned>(S::kPair ? ctas / 2 * 2 : ctas));
   cfg.dynamicSmemBytes = S::kBytes;
-  return cudaLaunchKernelEx(&cfg, kernel, maps.w, maps.x, maps.x_half, p);
+  return cudaLaunchKernelEx(&cfg, kernel, maps.w, maps.x, maps.x_small, p);
 }
 
 }  // namespace
@@ -784,8 +823,10 @@ size_t expert_partial_bytes(int ctas) {
   return static_cast<size_t>(ctas) * 2 * kTileRows * std::max(Narrow::kCols, Wide::kCols) * 4;
 }
 bool expert_wide(int rows, int experts) { return rows > Narrow::kCols * experts; }
-int expert_cols(bool wide) { return wide ? Wide::kCols : Narrow::kCols; }
-int expert_x_box(bool wide) { return wide ? Wide::kBox : Narrow::kBox; }
+ExpertTile expert_tile(bool wide) {
+  return wide ? ExpertTile{Wide::kCols, Wide::kTiles, Wide::kXRows, Wide::kSmall}
+              : ExpertTile{Narrow::kCols, Narrow::kTiles, Narrow::kXRows, Narrow::kSmall};
+}
 
 cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p, bool wide,
                                   int ctas, cudaStream_t stream) {
@@ -796,10 +837,16 @@ cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p,
                  : launch_as<Narrow, false>(maps, p, ctas, stream);
 }
 
-cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,
-                              int w_tiles, int k_tiles, cudaStream_t stream) {
-  lay_scales_kernel<<<dim3(k_tiles, w_tiles, experts), 128, 0, stream>>>(scale, laid, n, gated,
-                                                                         w_tiles, k_tiles);
+cudaError_t launch_lay(const uint8_t* w, const uint8_t* scale, uint8_t* laid, uint8_t* laid_scale,
+                       int experts, int n, bool gated, bool narrow, int w_tiles, int k_tiles,
+                       cudaStream_t stream) {
+  const dim3 grid(k_tiles, w_tiles, experts);
+  if (narrow)
+    lay_kernel<true><<<grid, 256, 0, stream>>>(w, scale, laid, laid_scale, n, gated, w_tiles,
+                                               k_tiles);
+  else
+    lay_kernel<false><<<grid, 256, 0, stream>>>(w, scale, laid, laid_scale, n, gated, w_tiles,
+                                                k_tiles);
   return cudaGetLastError();
 }
 

@@ -229,8 +229,9 @@ struct ExpertParams {
   int32_t w_tiles, k_tiles;   // tiles of 128 rows of an expert's W, of 128 k
   int32_t gated, format;      // of the result
   uint32_t idesc;             // the products', without their columns
-  uint32_t w_bytes, x_bytes;  // what a tile of W, a copy of x count
-  const uint8_t* w_sf;        // laid by launch_lay_scales
+  uint32_t w_bytes;           // what a stage's copies of W, of x, of fewer rows of x count
+  uint32_t x_bytes, x_small_bytes;
+  const uint8_t* w_sf;        // laid by launch_lay
   const uint8_t* x_scale;     // [rows][4 k_tiles]
   const int32_t* begin;       // [experts + 1], or nullptr: one expert has all rows
   void* out;
@@ -243,15 +244,20 @@ constexpr int kMaxExpertCtas = 160;  // a ticket each: 640 bytes of the workspac
 static_assert(kMaxExpertCtas * 4 <= MXFP8_EXPERT_WORKSPACE_ZEROS, "tickets");
 size_t expert_partial_bytes(int ctas);
 bool expert_wide(int rows, int experts);  // which kernel
-int expert_cols(bool wide);               // rows of a tile
-int expert_x_box(bool wide);              // rows of a copy of x
+struct ExpertTile {
+  int rows;             // of a tile
+  int k_tiles;          // of a stage
+  int x_rows, x_small;  // rows of the two copies of x
+};
+ExpertTile expert_tile(bool wide);
 struct ExpertMaps {
   CUtensorMap w, x;
-  CUtensorMap x_half;  // of the wide kernel: half as many rows
+  CUtensorMap x_small;  // of fewer rows
 };
 cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p, bool wide,
                                   int ctas, cudaStream_t stream);
-cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,
-                              int w_tiles, int k_tiles, cudaStream_t stream);
+cudaError_t launch_lay(const uint8_t* w, const uint8_t* scale, uint8_t* laid, uint8_t* laid_scale,
+                       int experts, int n, bool gated, bool narrow, int w_tiles, int k_tiles,
+                       cudaStream_t stream);
 
 }  // namespace mxfp8
