@@ -108,7 +108,8 @@ extern "C" {
 size_t mxfp8_route_workspace_bytes(int64_t tokens, int32_t experts) {
   if (tokens <= kRouteTokens || experts < 1 || experts > MXFP8_MAX_EXPERTS || tokens > INT32_MAX)
     return 0;
-  return static_cast<size_t>((tokens + kRouteTokens - 1) / kRouteTokens) * experts * 4;
+  const int64_t block = route_block_tokens(tokens);
+  return static_cast<size_t>((tokens + block - 1) / block + 1) * experts * 4;
 }
 
 mxfp8_status mxfp8_route(const void* logits, int32_t type, int64_t stride, int64_t tokens,
@@ -144,9 +145,10 @@ mxfp8_status mxfp8_route(const void* logits, int32_t type, int64_t stride, int64
       return fail(MXFP8_ERR_INVALID,
                   "the workspace must hold " + std::to_string(need) + " bytes");
   }
-  const RouteParams p{tokens, stride, experts, k,    type, normalize ? 1 : 0,
-                      logits, weight, expert,  slot, row,  begin,
-                      static_cast<int32_t*>(workspace)};
+  const bool pairs = experts % 2 == 0 && stride % 2 == 0 && aligned(logits, 4);
+  const RouteParams p{tokens,        stride, experts, k,      type, normalize ? 1 : 0,
+                      pairs ? 1 : 0, logits, weight,  expert, slot, row,
+                      begin,         static_cast<int32_t*>(workspace)};
   const cudaError_t e = launch_route(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the routing");
   return MXFP8_OK;

@@ -6,19 +6,22 @@
 // A slot is a row of the experts' products: slots are numbered by expert, then
 // by token.  A logit of -infinity is not chosen: such an entry has no slot.
 //
-// A warp takes a token, its logits in registers.  A value's order is that of an
-// integer made of its bits, so a step of the choice is two warp reductions: the
-// largest key, and the lowest index that has it.  An expert appears once at
-// most among a token's, so a block of 128 tokens is, for each expert, a mask of
-// 128 bits: its population is the block's count, and that of the bits below a
-// token the token's place.  Nothing depends on the order of atomics.  One block
-// does all of up to 128 tokens; for more a second kernel adds the counts of the
-// blocks before.
+// A warp takes a token, its logits in registers as integers of the same order with the
+// index below them (32 bits for logits of 16, else 64), each lane's sorted once.  A step
+// of the choice is then a warp reduction over the lanes' first keys (for FP32 a second
+// one, over the indexes of the lanes that have the largest), and the lane that gave it
+// moves its keys up.  An expert appears once at most among a token's, so a block of tokens is, for
+// each expert, a bit mask: its population is the block's count, and that of the bits
+// below a token the token's place.  Nothing depends on the order of atomics.  One block
+// does all of up to 128 tokens; for more a second kernel adds up the blocks' counts, and
+// a third gives the places.  (Each block adding up those before it: all read the same
+// lines at the same time, 20 us at 16k tokens in place of 2.)
 //
 // Combine.  out[t] = add[t] + sum_j weight[t][j] y[slot[t][j]], in FP32, j
 // ascending, rounded once; a thread has 8 numbers of a row, and its loads are
 // all under way at once.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -28,8 +31,6 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTokens = kRouteTokens;  // of a block
-constexpr int kMaskWords = kTokens / 32;
 static_assert(kThreads >= MXFP8_MAX_EXPERTS, "a thread an expert");
 
 // Larger values have larger keys; +0 and -0 one; NaN the largest of all.
@@ -38,14 +39,31 @@ __device__ __forceinline__ uint32_t order_key(float z) {
   if ((b & 0x7FFFFFFFu) > 0x7F800000u) return ~0u;
   return (b >> 31) ? ~b : b | 0x80000000u;
 }
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key >> 31) ? key & 0x7FFFFFFFu : ~key);
+}
 constexpr uint32_t kNothing = 0x007FFFFFu;  // order_key(-infinity)
 
-__device__ __forceinline__ float logit(const RouteParams& p, int64_t t, int e) {
-  const int64_t at = t * p.stride + e;
-  if (p.type == MXFP8_FP32) return static_cast<const float*>(p.logits)[at];
-  const uint16_t h = static_cast<const uint16_t*>(p.logits)[at];
-  if (p.type == MXFP8_BF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
-  return __half2float(__ushort_as_half(h));
+// Two keys of 16 bits from two numbers of a 16-bit type, in order: adding zero makes
+// +0 of -0 and one NaN, the largest, of all; then negative ones are turned over.
+template <int kType>
+__device__ __forceinline__ uint32_t short_keys(uint32_t w) {
+  if constexpr (kType == MXFP8_BF16) {
+    const __nv_bfloat162 v =
+        __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&w), __float2bfloat162_rn(0.0f));
+    w = *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __hadd2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(0.0f));
+    w = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const uint32_t negative = w >> 15 & 0x00010001u;
+  return w ^ (negative * 0xFFFFu | 0x80008000u);
+}
+template <int kType>
+__device__ __forceinline__ float short_value(uint32_t key) {
+  const uint32_t h = (key >> 15) ? key & 0x7FFFu : ~key & 0xFFFFu;
+  if constexpr (kType == MXFP8_BF16) return __uint_as_float(h << 16);
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -54,54 +72,110 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Token t's experts and weights; the chosen experts' bits in `mask`.
-template <int kEach>
-__device__ void choose(const RouteParams& p, int64_t t, int bit, uint32_t (*mask)[MXFP8_MAX_EXPERTS]) {
+// A key and below it the index, smaller for a higher one.
+template <int kType>
+struct KeyOf {
+  using T = uint32_t;
+};
+template <>
+struct KeyOf<MXFP8_FP32> {
+  using T = uint64_t;
+};
+
+// Descending, by Batcher's odd-even merges.
+template <int kEach, typename T>
+__device__ __forceinline__ void sort_down(T (&k)[kEach]) {
+#pragma unroll
+  for (int p = 1; p < kEach; p *= 2)
+#pragma unroll
+    for (int q = p; q > 0; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < kEach; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (j + i + q < kEach && (j + i) / (2 * p) == (j + i + q) / (2 * p)) {
+            const T a = k[j + i], b = k[j + i + q];
+            k[j + i] = a > b ? a : b;
+            k[j + i + q] = a > b ? b : a;
+          }
+}
+
+// A lane's logits are neighbours in pairs.
+template <int kType, int kEach>
+__device__ __forceinline__ void load_keys(const RouteParams& p, int64_t t,
+                                          typename KeyOf<kType>::T (&key)[kEach]) {
   const int lane = threadIdx.x % 32;
-  float z[kEach];
-  uint32_t key[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int e = lane + 32 * i;
-    z[i] = e < p.experts ? logit(p, t, e) : -INFINITY;
-    key[i] = e < p.experts ? order_key(z[i]) : 0u;
-  }
-  float first = 0.0f, mine = 0.0f;  // lane j: the j-th chosen logit
-  int expert = -1;
-  for (int j = 0; j < p.k; ++j) {
-    uint32_t best = 0u;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) best = max(best, key[i]);
-    const uint32_t top = __reduce_max_sync(~0u, best);
-    if (top <= kNothing) break;  // -infinity from here on
-    uint32_t at = ~0u;
-#pragma unroll
-    for (int i = kEach - 1; i >= 0; --i)
-      if (key[i] == top) at = lane + 32 * i;
-    at = __reduce_min_sync(~0u, at);
-    float value = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (lane + 32 * i == at) {
-        value = z[i];
-        key[i] = 0u;
-      }
-    value = __shfl_sync(~0u, value, at % 32);
-    if (j == 0) first = value;
-    if (lane == j) {
-      mine = value;
-      expert = static_cast<int>(at);
+  for (int i = 0; i < kEach; i += 2) {
+    const int e = 2 * lane + 32 * i;
+    key[i] = key[i + 1] = 0u;
+    if (e >= p.experts) continue;
+    const bool both = e + 1 < p.experts;
+    if constexpr (kType != MXFP8_FP32) {
+      const uint16_t* const at = static_cast<const uint16_t*>(p.logits) + t * p.stride + e;
+      const uint32_t w = p.pairs ? *reinterpret_cast<const uint32_t*>(at)
+                                 : at[0] | (both ? static_cast<uint32_t>(at[1]) << 16 : 0u);
+      const uint32_t keys = short_keys<kType>(w);
+      key[i] = keys << 16 | (0xFFFFu - e);
+      if (both) key[i + 1] = (keys & 0xFFFF0000u) | (0xFFFFu - (e + 1));
+    } else {
+      const float* const at = static_cast<const float*>(p.logits) + t * p.stride + e;
+      key[i] = static_cast<uint64_t>(order_key(at[0])) << 32 | (0xFFFFu - e);
+      if (both) key[i + 1] = static_cast<uint64_t>(order_key(at[1])) << 32 | (0xFFFFu - (e + 1));
     }
   }
-  float e = expert >= 0 ? expf(mine - first) : 0.0f;
-  float total = e;
-  if (!p.normalize) {
-    total = 0.0f;
+}
+
+// Token t's experts and weights, from its keys; the chosen experts' bits in `mask`.
+template <int kType, int kEach>
+__device__ __forceinline__ void choose(const RouteParams& p, int64_t t,
+                                       typename KeyOf<kType>::T (&key)[kEach], int bit,
+                                       uint32_t (*mask)[MXFP8_MAX_EXPERTS]) {
+  constexpr bool kShort = kType != MXFP8_FP32;
+  using Key = typename KeyOf<kType>::T;
+  const int lane = threadIdx.x % 32;
+  const auto value = [&](Key k) {
+    if constexpr (kShort)
+      return short_value<kType>(k >> 16);
+    else
+      return key_value(static_cast<uint32_t>(k >> 32));
+  };
+  const auto nothing = [&](Key k) {  // -infinity, or none
+    if constexpr (kShort)
+      return k >> 16 <= (kType == MXFP8_BF16 ? 0x007Fu : 0x03FFu);
+    else
+      return static_cast<uint32_t>(k >> 32) <= kNothing;
+  };
+  sort_down(key);
+  float total = 0.0f;
+  Key first = 0u, mine = 0u;  // lane j: the j-th chosen key
+  for (int j = 0; j < p.k; ++j) {
+    Key top;
+    if constexpr (kShort) {
+      top = __reduce_max_sync(~0u, key[0]);
+    } else {
+      const uint32_t high = __reduce_max_sync(~0u, static_cast<uint32_t>(key[0] >> 32));
+      const uint32_t low = static_cast<uint32_t>(key[0] >> 32) == high ? key[0] & 0xFFFFu : 0u;
+      top = static_cast<uint64_t>(high) << 32 | __reduce_max_sync(~0u, low);
+    }
+    if (nothing(top)) break;
+    if (j == 0) {
+      first = top;
+      if (!p.normalize)
 #pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (lane + 32 * i < p.experts) total += expf(z[i] - first);
+        for (int i = 0; i < kEach; ++i)
+          if (key[i] != 0u) total += expf(value(key[i]) - value(first));
+    }
+    if (lane == j) mine = top;
+    if (key[0] == top) {  // one lane: keys are all different
+#pragma unroll
+      for (int i = 0; i + 1 < kEach; ++i) key[i] = key[i + 1];
+      key[kEach - 1] = 0u;
+    }
   }
-  total = warp_sum(total);
+  const int expert = mine != 0u ? static_cast<int>(0xFFFFu - (mine & 0xFFFFu)) : -1;
+  const float e = expert >= 0 ? expf(value(mine) - value(first)) : 0.0f;
+  total = warp_sum(p.normalize ? e : total);
   if (lane < p.k) {
     p.weight[t * p.k + lane] = expert >= 0 ? e / total : 0.0f;
     p.expert[t * p.k + lane] = expert;
@@ -125,10 +199,11 @@ __device__ __forceinline__ int before_in_block(int v, int* sums) {
   return base + inc - v;
 }
 
-// kStep 0: all of a call with one block.  1: the choice, and each block's
-// counts.  2: the places.
-template <int kStep, int kEach>
+// kStep 0: all of a call with one block.  1: the choice, and each block's counts.  2:
+// the places, from the counts of the blocks before.
+template <int kStep, int kTokens, int kType, int kEach>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p) {
+  constexpr int kMaskWords = kTokens / 32;
   __shared__ uint32_t mask[kMaskWords][MXFP8_MAX_EXPERTS];
   __shared__ int base[MXFP8_MAX_EXPERTS];
   __shared__ int sums[kWarps];
@@ -140,43 +215,48 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
   for (int i = tid; i < kMaskWords * MXFP8_MAX_EXPERTS; i += kThreads) (&mask[0][0])[i] = 0u;
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  __syncthreads();
+  int count = 0, earlier = 0;  // thread e: expert e's rows (kStep 2: of all blocks, of those before)
   if constexpr (kStep != 2) {
-    for (int i = warp; i < tokens; i += kWarps) choose<kEach>(p, t0 + i, i, mask);
+    // A token's logits are on their way while the one before is chosen from.
+    using Key = typename KeyOf<kType>::T;
+    Key next[kEach];
+    if (warp < tokens) load_keys<kType, kEach>(p, t0 + warp, next);
+    __syncthreads();
+    for (int i = warp; i < tokens; i += kWarps) {
+      Key key[kEach];
+#pragma unroll
+      for (int q = 0; q < kEach; ++q) key[q] = next[q];
+      if (i + kWarps < tokens) load_keys<kType, kEach>(p, t0 + i + kWarps, next);
+      choose<kType, kEach>(p, t0 + i, key, i, mask);
+    }
   } else {
+    if (tid < p.experts) {
+      count = p.counts[static_cast<size_t>(gridDim.x) * p.experts + tid];
+      earlier = p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid];
+    }
+    __syncthreads();
     for (int i = tid; i < entries; i += kThreads) {
       const int e = p.expert[t0 * p.k + i];
       if (e >= 0) atomicOr(&mask[i / p.k / 32][e], 1u << (i / p.k % 32));
     }
   }
   __syncthreads();
-  int count = 0;
-  if (tid < p.experts)
-#pragma unroll
-    for (int w = 0; w < kMaskWords; ++w) count += __popc(mask[w][tid]);
-  if constexpr (kStep == 1) {
-    if (tid < p.experts) p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid] = count;
-    return;
-  }
-  int all = count, earlier = 0;
-  if constexpr (kStep == 2) {
-    all = 0;
-    const int blocks = gridDim.x, mine = blockIdx.x;
+  if constexpr (kStep != 2) {
     if (tid < p.experts)
-#pragma unroll 8
-      for (int b = 0; b < blocks; ++b) {
-        const int c = p.counts[static_cast<size_t>(b) * p.experts + tid];
-        all += c;
-        if (b < mine) earlier += c;
-      }
+#pragma unroll
+      for (int w = 0; w < kMaskWords; ++w) count += __popc(mask[w][tid]);
+    if constexpr (kStep == 1) {
+      if (tid < p.experts) p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid] = count;
+      return;
+    }
   }
-  const int begin = before_in_block(all, sums);
+  const int begin = before_in_block(count, sums);
   if (tid < p.experts) {
     base[tid] = begin + earlier;
     if (blockIdx.x == 0) p.begin[tid] = begin;
     if (tid == p.experts - 1) {
-      routed = begin + all;
-      if (blockIdx.x == 0) p.begin[p.experts] = begin + all;
+      routed = begin + count;
+      if (blockIdx.x == 0) p.begin[p.experts] = begin + count;
     }
   }
   __syncthreads();
@@ -186,14 +266,42 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     int slot = -1;
     if (e >= 0) {
       slot = base[e] + __popc(mask[bit / 32][e] & ((1u << (bit % 32)) - 1u));
-#pragma unroll
-      for (int w = 0; w < kMaskWords; ++w)
-        if (w < bit / 32) slot += __popc(mask[w][e]);
+      for (int w = 0; w < bit / 32; ++w) slot += __popc(mask[w][e]);
       p.row[slot] = static_cast<int32_t>(t0 + bit);
     }
     p.slot[flat] = slot;
     if (flat >= routed) p.row[flat] = -1;  // a slot that nothing was routed to
   }
+}
+
+// Each expert's counts become those of the blocks before, in place, and the row after
+// the last block's the sum.  A block of 32 x 32: 32 experts, whose blocks the 32 rows of
+// threads take in turn.
+__global__ void __launch_bounds__(1024) route_sum_kernel(int32_t* counts, int experts, int blocks) {
+  __shared__ int sums[32][33];
+  ptx::launch_dependents();
+  ptx::grid_dependency_wait();
+  const int lane = threadIdx.x % 32, part = threadIdx.x / 32, e = blockIdx.x * 32 + lane;
+  const int each = (blocks + 31) / 32, from = min(part * each, blocks), to = min(from + each, blocks);
+  int sum = 0;
+  if (e < experts)
+#pragma unroll 8
+    for (int b = from; b < to; ++b) sum += counts[static_cast<size_t>(b) * experts + e];
+  sums[part][lane] = sum;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int q = 0; q < 31; ++q)
+    if (q < part) before += sums[q][lane];
+  if (e >= experts) return;
+#pragma unroll 8
+  for (int b = from; b < to; ++b) {
+    int32_t* const at = counts + static_cast<size_t>(b) * experts + e;
+    const int c = *at;
+    *at = before;
+    before += c;
+  }
+  if (part == 31) counts[static_cast<size_t>(blocks) * experts + e] = before;
 }
 
 constexpr int kCombineThreads = 256;
@@ -255,9 +363,9 @@ __global__ void __launch_bounds__(kCombineThreads)
   ptx::st_v4(p.out + static_cast<size_t>(t) * p.n + c, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-template <typename Params>
-cudaError_t launch(void (*kernel)(Params), uint32_t blocks, int threads, const Params& p,
-                   cudaStream_t stream) {
+template <typename... Args>
+cudaError_t launch(void (*kernel)(Args...), uint32_t blocks, int threads, cudaStream_t stream,
+                   Args... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -267,30 +375,47 @@ cudaError_t launch(void (*kernel)(Params), uint32_t blocks, int threads, const P
   cfg.numAttrs = 1;
   cfg.blockDim = dim3(threads);
   cfg.gridDim = dim3(blocks);
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int kEach>
-cudaError_t route_as(const RouteParams& p, cudaStream_t stream) {
+template <int kTokens, int kType, int kEach>
+cudaError_t route_blocks(const RouteParams& p, cudaStream_t stream) {
   const uint32_t blocks = static_cast<uint32_t>((p.tokens + kTokens - 1) / kTokens);
-  if (blocks <= 1) return launch(route_kernel<0, kEach>, 1, kThreads, p, stream);
-  const cudaError_t e = launch(route_kernel<1, kEach>, blocks, kThreads, p, stream);
+  cudaError_t e = launch(route_kernel<1, kTokens, kType, kEach>, blocks, kThreads, stream, p);
   if (e != cudaSuccess) return e;
-  return launch(route_kernel<2, 1>, blocks, kThreads, p, stream);
+  e = launch(route_sum_kernel, static_cast<uint32_t>((p.experts + 31) / 32), 1024, stream, p.counts,
+             p.experts, static_cast<int>(blocks));
+  if (e != cudaSuccess) return e;
+  return launch(route_kernel<2, kTokens, MXFP8_FP32, 1>, blocks, kThreads, stream, p);
+}
+template <int kType, int kEach>
+cudaError_t route_as(const RouteParams& p, cudaStream_t stream) {
+  if (p.tokens <= kRouteTokens)
+    return launch(route_kernel<0, kRouteTokens, kType, kEach>, 1, kThreads, stream, p);
+  return route_block_tokens(p.tokens) == kRouteFew ? route_blocks<kRouteFew, kType, kEach>(p, stream)
+                                                   : route_blocks<kRouteMany, kType, kEach>(p, stream);
+}
+template <int kType>
+cudaError_t route_for(const RouteParams& p, cudaStream_t stream) {
+  if (p.experts <= 64) return route_as<kType, 2>(p, stream);
+  if (p.experts <= 256) return route_as<kType, 8>(p, stream);
+  return route_as<kType, 16>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream) {
-  if (p.experts <= 64) return route_as<2>(p, stream);
-  if (p.experts <= 256) return route_as<8>(p, stream);
-  return route_as<16>(p, stream);
+  switch (p.type) {
+    case MXFP8_BF16: return route_for<MXFP8_BF16>(p, stream);
+    case MXFP8_FP16: return route_for<MXFP8_FP16>(p, stream);
+    default: return route_for<MXFP8_FP32>(p, stream);
+  }
 }
 
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream) {
   const uint32_t blocks = (p.items + kCombineThreads - 1) / kCombineThreads;
-  return p.k <= 4 ? launch(combine_kernel<4>, blocks, kCombineThreads, p, stream)
-                  : launch(combine_kernel<8>, blocks, kCombineThreads, p, stream);
+  return p.k <= 4 ? launch(combine_kernel<4>, blocks, kCombineThreads, stream, p)
+                  : launch(combine_kernel<8>, blocks, kCombineThreads, stream, p);
 }
 
 }  // namespace mxfp8

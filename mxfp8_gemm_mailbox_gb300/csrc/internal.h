@@ -186,17 +186,22 @@ cudaError_t launch_latent_attend(const LatentParams& p, int latent, void* worksp
                                  cudaStream_t stream);
 
 // A layer of routed experts (experts_route.cu, quantize.cu, experts_product.cu).
-constexpr int kRouteTokens = 128;  // of a block
+constexpr int kRouteTokens = 128;  // of a call with one block
+// Of a block of more: small ones fill the GPU; past the second's capacity for some 500 of
+// them, larger ones.
+constexpr int kRouteFew = 64, kRouteMany = 512;
+constexpr int route_block_tokens(int64_t tokens) { return tokens <= 32768 ? kRouteFew : kRouteMany; }
 struct RouteParams {
   int64_t tokens, stride;  // elements between tokens' logits
   int32_t experts, k, type, normalize;
+  int32_t pairs;  // logits of 16 bits lie on 4-byte boundaries two by two
   const void* logits;
   float* weight;    // [tokens][k]
   int32_t* expert;  // [tokens][k], -1: none
   int32_t* slot;    // [tokens][k], -1: none
   int32_t* row;     // [tokens k] the token of a slot, -1: none
   int32_t* begin;   // [experts + 1]
-  int32_t* counts;  // [blocks][experts], of more than one block
+  int32_t* counts;  // [blocks + 1][experts], of more than one block
 };
 cudaError_t launch_route(const RouteParams& p, cudaStream_t stream);
 struct CombineParams {

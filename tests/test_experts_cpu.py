@@ -33,7 +33,7 @@ def test_route_refusals(lib):
     for bad in (dict(type=3), dict(type=-1), dict(tokens=-1), dict(stride=63), dict(logits=0),
                 dict(logits=A + 1), dict(type=2, logits=A + 2), dict(weight=A + 2), dict(expert=0),
                 dict(slot=A + 1), dict(row=0), dict(begin=0), dict(tokens=129),
-                dict(tokens=129, workspace=A, nbytes=511)):
+                dict(tokens=129, workspace=A, nbytes=1023)):
         assert route(lib, **bad) == mx.ERR_INVALID, bad
         assert text(lib)
     for bad in (dict(experts=0), dict(experts=513, stride=600), dict(k=0), dict(k=33),
@@ -44,7 +44,8 @@ def test_route_refusals(lib):
 def test_route_workspace(lib):
     size = lib.mxfp8_route_workspace_bytes
     assert size(0, 64) == size(128, 64) == size(-5, 64) == size(200, 0) == size(200, 513) == 0
-    assert size(129, 64) == 2 * 64 * 4 and size(16384, 256) == 128 * 256 * 4
+    assert size(129, 63) == 4 * 63 * 4 and size(16384, 256) == 257 * 256 * 4
+    assert size(1 << 20, 512) == 2049 * 512 * 4
 
 
 def quantize(lib, x=A, type=0, stride=64, x_rows=4, k=64, rows=None, out_rows=4, format=1, codes=A,

@@ -155,7 +155,8 @@ def routed(logits, k, normalize):
     z = logits.double().cpu()
     weight, expert, entries = [], [], []
     for t, row in enumerate(z.tolist()):
-        key = lambda e: (-float("inf") if row[e] != row[e] else -row[e], e)  # noqa: E731
+        # NaN before all numbers, infinity among them.
+        key = lambda e: (0, 0.0, e) if row[e] != row[e] else (1, -row[e], e)  # noqa: E731
         chosen = sorted(range(len(row)), key=key)[:k]
         chosen = [e for e in chosen if row[e] != -float("inf")]
         first = row[chosen[0]] if chosen else 0.0
@@ -207,6 +208,15 @@ def test_route_types(cuda, experts, k, dtype, normalize):
     check_route(z.to(dtype)[:, 8:], k, normalize)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_route_unaligned_pairs(cuda, dtype):
+    z = torch.randn(40, 71, generator=generator(2), device="cuda").to(dtype)
+    for part in (z, z[:, 1:], z[:, 1:70], z[:, 2:], torch.cat((z, z), 1)[:, 3:85]):
+        check_route(part, 6)
+    every = torch.arange(65536, device="cuda").to(torch.uint16).view(dtype).view(-1, 512)
+    check_route(every, 32)
+
+
 def test_route_ties_infinities_and_nan(cuda):
     inf, nan = float("inf"), float("nan")
     z = torch.zeros(10, 40, device="cuda")  # all equal: the lowest indexes
@@ -221,6 +231,27 @@ def test_route_ties_infinities_and_nan(cuda):
     z[9] = torch.finfo(torch.float32).max
     check_route(z, 8)
     check_route(z.to(torch.bfloat16), 3, normalize=False)
+
+
+@pytest.mark.parametrize("tokens", [5000, 32769, 40000])
+def test_route_many_tokens(cuda, tokens):
+    """Against the definition in sorts: the lowest index first among equal logits."""
+    experts, k = 37, 3
+    z = torch.randn(tokens, experts, generator=generator(tokens), device="cuda").to(torch.bfloat16)
+    z[::7] = -float("inf")
+    got = mx.route(z, k)
+    top, expert = torch.sort(z.double(), dim=1, descending=True, stable=True)
+    expert = torch.where(top > -float("inf"), expert, -1)[:, :k]
+    assert torch.equal(got.expert.long(), expert)
+    key = torch.where(expert >= 0, expert, experts).flatten()
+    order = torch.sort(key, stable=True)[1]
+    begin = torch.tensor([0] + torch.bincount(key, minlength=experts + 1).tolist()).cumsum(0)
+    assert got.begin.tolist() == begin[:experts + 1].tolist()
+    total = int(got.begin[-1])
+    assert torch.equal(got.row[:total].long(), order[:total] // k)
+    assert (got.row[total:] == -1).all()
+    assert torch.equal(got.slot.flatten()[order[:total]].long(), torch.arange(total, device="cuda"))
+    assert (got.slot.flatten()[order[total:]] == -1).all()
 
 
 def test_route_one_expert_for_all(cuda):
