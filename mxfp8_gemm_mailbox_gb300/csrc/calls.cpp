@@ -7,6 +7,8 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/ScalarTypeToTypeMeta.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -99,9 +101,32 @@ void halves(const at::Tensor& t, const char* name, int64_t cols, int64_t min_row
   if (!t.is_cuda() || !t.is_contiguous())
     refuse(PyExc_ValueError, std::string(name) + " must be a contiguous CUDA tensor");
 }
+// New memory of the current stream, as torch's own outputs have it, without its
+// dispatcher (1 us of a call on a Grace core).  The device is the current one.
+c10::Storage new_storage(int64_t bytes) {
+  c10::Allocator* const allocator = c10::cuda::CUDACachingAllocator::get();
+  const auto size = static_cast<size_t>(bytes);
+  return c10::Storage(c10::Storage::use_byte_size_t(), size, allocator->allocate(size), allocator,
+                      /*resizable=*/true);
+}
+// A contiguous tensor at a place of a storage (in elements).
+at::Tensor tensor_of(c10::Storage storage, int64_t at, at::IntArrayRef shape,
+                     at::ScalarType dtype) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+      c10::scalarTypeToTypeMeta(dtype));
+  c10::TensorImpl* const impl = t.unsafeGetTensorImpl();
+  impl->set_sizes_contiguous(shape);
+  impl->set_storage_offset(at);
+  return t;
+}
 at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType dtype, int device) {
-  return at::empty(shape,
-                   at::TensorOptions().dtype(dtype).device(at::Device(at::kCUDA, device)));
+  if (device != c10::cuda::current_device())  // an object's of another device
+    return at::empty(shape,
+                     at::TensorOptions().dtype(dtype).device(at::Device(at::kCUDA, device)));
+  int64_t bytes = static_cast<int64_t>(c10::elementSize(dtype));
+  for (const int64_t n : shape) bytes *= n;
+  return tensor_of(new_storage(bytes), 0, shape, dtype);
 }
 void* handle_of(PyObject* s) {
   THPObjectPtr handle(PyObject_GetAttrString(s, "cuda_stream"));
@@ -490,21 +515,18 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                  "), got " + std::to_string(k) + " of " + std::to_string(experts));
   if (tokens > INT32_MAX / k) refuse(PyExc_ValueError, "tokens x k must be below 2^31");
   const CallStream stream(args[3], device);
-  at::Tensor weight = new_tensor({tokens, k}, at::kFloat, device);
-  at::Tensor expert = new_tensor({tokens, k}, at::kInt, device);
-  at::Tensor slot = new_tensor({tokens, k}, at::kInt, device);
-  at::Tensor row = new_tensor({tokens * k}, at::kInt, device);
-  at::Tensor begin = new_tensor({experts + 1}, at::kInt, device);
   const auto space = static_cast<int64_t>(
       mxfp8_route_workspace_bytes(tokens, narrowed(experts, "the number of experts")));
-  at::Tensor workspace;
-  if (space) workspace = new_tensor({space}, at::kByte, device);
+  // All five in one piece of memory, and the workspace behind them, each on a boundary of
+  // 16 bytes (places in words of 4).
+  const auto rounded = [](int64_t words) { return (words + 3) / 4 * 4; };
+  const int64_t each = rounded(tokens * k), begins = rounded(experts + 1);
+  c10::Storage memory = new_storage(4 * (4 * each + begins) + space);
+  auto* const ep = static_cast<int32_t*>(memory.mutable_data()) + each;
+  auto* const wp = reinterpret_cast<float*>(ep - each);
+  int32_t *const sp = ep + each, *const rp = sp + each, *const bp = rp + each;
+  void* const space_p = space ? bp + begins : nullptr;
   const void* const lp = logits.data_ptr();
-  auto* const wp = static_cast<float*>(weight.data_ptr());
-  const auto ints = [](const at::Tensor& t) { return static_cast<int32_t*>(t.data_ptr()); };
-  int32_t *const ep = ints(expert), *const sp = ints(slot), *const rp = ints(row),
-                 *const bp = ints(begin);
-  void* const space_p = space ? workspace.data_ptr() : nullptr;
   check(unlocked([&] {
           return mxfp8_route(lp, type, stride, tokens, static_cast<int32_t>(experts),
                              static_cast<int32_t>(k), normalize, wp, ep, sp, rp, bp, space_p,
@@ -513,8 +535,11 @@ PyObject* route(PyObject*, PyObject* const* args, Py_ssize_t n) {
         "mxfp8_route");
   PyObject* out = PyTuple_New(5);
   if (!out) throw python_error();
-  at::Tensor* const all[5] = {&weight, &expert, &slot, &row, &begin};
-  for (int i = 0; i < 5; ++i) PyTuple_SET_ITEM(out, i, THPVariable_Wrap(std::move(*all[i])));
+  PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(tensor_of(memory, 0, {tokens, k}, at::kFloat)));
+  PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(tensor_of(memory, each, {tokens, k}, at::kInt)));
+  PyTuple_SET_ITEM(out, 2, THPVariable_Wrap(tensor_of(memory, 2 * each, {tokens, k}, at::kInt)));
+  PyTuple_SET_ITEM(out, 3, THPVariable_Wrap(tensor_of(memory, 3 * each, {tokens * k}, at::kInt)));
+  PyTuple_SET_ITEM(out, 4, THPVariable_Wrap(tensor_of(memory, 4 * each, {experts + 1}, at::kInt)));
   return out;
   END_HANDLE_TH_ERRORS
 }
