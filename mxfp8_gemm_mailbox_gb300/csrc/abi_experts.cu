@@ -178,12 +178,19 @@ mxfp8_status mxfp8_quantize(const void* x, int32_t type, int64_t stride, int64_t
   CHECK(check_pointer("codes", codes, 16));
   CHECK(check_pointer("scales", scales, 1));
   if (flags) CHECK(check_pointer("flags", flags, 4));
-  const QuantizeParams p{k,      format, type,
-                         static_cast<uint32_t>(out_rows * per_row),
-                         x_rows, stride, x,
-                         rows,   static_cast<uint8_t*>(codes),
-                         static_cast<uint8_t*>(scales),
-                         flags};
+  QuantizeParams p{};
+  p.format = format;
+  p.type = type;
+  p.items = static_cast<uint32_t>(out_rows * per_row);
+  p.sectors = aligned(x, 32) && (x_rows <= 1 || stride % (2 * step) == 0);
+  p.x_rows = x_rows;
+  p.x_stride = stride;
+  p.k = k;
+  p.x = x;
+  p.rows = rows;
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scales = static_cast<uint8_t*>(scales);
+  p.flags = flags;
   const cudaError_t e = launch_quantize(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the quantisation");
   return MXFP8_OK;

@@ -219,6 +219,7 @@ cudaError_t launch_combine(const CombineParams& p, cudaStream_t stream);
 struct QuantizeParams {
   int32_t k, format, type;
   uint32_t items;  // sixteens of the result
+  int32_t sectors;  // x's rows lie on 32-byte boundaries
   int64_t x_rows, x_stride;
   const void* x;
   const int32_t* rows;  // or nullptr

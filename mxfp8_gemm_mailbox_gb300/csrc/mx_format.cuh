@@ -28,26 +28,25 @@ __device__ __forceinline__ uint32_t scale_code_e2m1(float top) {
   return static_cast<uint32_t>(min(max(e, 0), 254));
 }
 
-// 2^(127 - code) as two exact factors (one power may be past FP32's range).
-// Their product with an element is exact wherever the element type's codes
+// 2^(127 - code), code up to 254 (for which it is subnormal), and 2^(code - 127), NaN for
+// the code 255.  An element times the first is exact wherever the element type's codes
 // tell values apart.
-__device__ __forceinline__ float2 inverse_scale(uint32_t code) {
-  const int e = 127 - static_cast<int>(code);
-  return make_float2(__uint_as_float(static_cast<uint32_t>(127 + e / 2) << 23),
-                     __uint_as_float(static_cast<uint32_t>(127 + e - e / 2) << 23));
+__device__ __forceinline__ float inverse_scale(uint32_t code) {
+  return __uint_as_float(code < 254u ? (254u - code) << 23 : 0x00400000u);
+}
+__device__ __forceinline__ float scale_of(uint32_t code) {
+  return __uint_as_float(code == 0u ? 0x00400000u : code == 255u ? 0x7FC00000u : code << 23);
 }
 
 // Two E4M3 codes of v 2^(127 - code).
 __device__ __forceinline__ uint32_t to_e4m3(float a, float b, uint32_t code) {
-  const float2 s = inverse_scale(code);
-  return __nv_cvt_float2_to_fp8x2(make_float2(a * s.x * s.y, b * s.x * s.y), __NV_SATFINITE,
-                                  __NV_E4M3);
+  const float s = inverse_scale(code);
+  return __nv_cvt_float2_to_fp8x2(make_float2(a * s, b * s), __NV_SATFINITE, __NV_E4M3);
 }
 // Two E2M1 codes in a byte, a's in its low half.
 __device__ __forceinline__ uint32_t to_e2m1(float a, float b, uint32_t code) {
-  const float2 s = inverse_scale(code);
-  return __nv_cvt_float2_to_fp4x2(make_float2(a * s.x * s.y, b * s.x * s.y), __NV_E2M1,
-                                  cudaRoundNearest);
+  const float s = inverse_scale(code);
+  return __nv_cvt_float2_to_fp4x2(make_float2(a * s, b * s), __NV_E2M1, cudaRoundNearest);
 }
 
 }  // namespace mxfp8

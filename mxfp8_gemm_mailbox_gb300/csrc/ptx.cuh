@@ -503,6 +503,14 @@ __device__ __forceinline__ uint4 ld_once_v4(const void* p) {
                : "memory");
   return v;
 }
+// 32 bytes read once (32-byte aligned), one sector, in program order likewise.
+__device__ __forceinline__ void ld_once_v8(const void* p, uint32_t (&r)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t ld_volatile_u32(const int32_t* p) {
   uint32_t v;
   asm volatile("ld.volatile.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
