@@ -39,6 +39,8 @@ constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kTileRows = 128;  // rows of W
 constexpr uint32_t kWTile = kTileRows * 128;  // in shared memory, of 128 k
 constexpr uint32_t kChunk = 512;  // scales of 128 rows, 4 blocks each
+constexpr int kTurnPitch = 36;    // floats of an expert row in the epilogue's turn: a quarter-warp's
+                                  // 16-byte reads meet no bank twice
 
 template <bool kPair_, int kCols_, int kTiles_, int kStages_, int kPipes_, int kSmall_, int kMinRun_,
           int kAtOnce_>
@@ -72,9 +74,8 @@ struct Shape {
   static constexpr uint32_t kX = kStages * kTiles * kWTile;
   static constexpr uint32_t kSfa = kX + kStages * kTiles * kXTile;
   static constexpr uint32_t kSfb = kSfa + kStages * kTiles * kChunk;
-  static constexpr uint32_t kExchange = kPair ? kSfa : kSfb + kStages * kTiles * kChunk;
-  static constexpr uint32_t kStaging = kExchange + 2 * 2 * kAtOnce * 32 * 4;
-  static constexpr uint32_t kTables = kStaging + 4 * kAtOnce * 80;
+  static constexpr uint32_t kTurns = kPair ? kSfa : kSfb + kStages * kTiles * kChunk;
+  static constexpr uint32_t kTables = kTurns + 2 * 4 * kAtOnce * kTurnPitch * 4;
   static constexpr uint32_t kBars = kTables + 2 * 4 * ((MXFP8_MAX_EXPERTS + 8) / 4 * 4);
   static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 4);
   static constexpr uint32_t kBytes = kMisc + 32 + 1024;
@@ -243,68 +244,92 @@ __device__ __forceinline__ void deal(const ExpertParams& p, int cols, int w_tile
   if (bad && blockIdx.x == 0 && p.flags) atomicOr(p.flags, MXFP8_FLAG_BAD_INDEX);
 }
 
-// kTokens rows' results of 32 outputs (one a lane) to memory.  `staging`: 80 bytes a
-// row, the warp's own.
-template <int kTokens>
-__device__ __forceinline__ void store_block(const ExpertParams& p, const float (&v)[kTokens],
-                                            int row, int live, int n0, uint8_t* staging) {
-  const int lane = threadIdx.x % 32;
-  __syncwarp();
+// kOut consecutive outputs from n on of one expert row to memory, where they are `live`;
+// 32 / kOut neighbouring lanes have a block of 32.
+template <int kOut>
+__device__ __forceinline__ void store_outputs(const ExpertParams& p, const float (&v)[kOut],
+                                              int row, bool live, int n) {
   if (p.format == MXFP8_FORMAT_BF16) {
+    uint32_t w[kOut / 2];
 #pragma unroll
-    for (int t = 0; t < kTokens; ++t)
-      reinterpret_cast<__nv_bfloat16*>(staging + t * 80)[lane] = __float2bfloat16_rn(v[t]);
-    __syncwarp();
-    const int c = lane % 4 * 8;
+    for (int i = 0; i < kOut / 2; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    uint16_t* const to = static_cast<uint16_t*>(p.out) + static_cast<size_t>(row) * p.n + n;
+    if constexpr (kOut == 4) {
+      if (live && n < p.n) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+    } else {
 #pragma unroll
-    for (int t0 = 0; t0 < kTokens; t0 += 8) {
-      const int t = t0 + lane / 4;
-      if (t < kTokens && t < live && n0 + c < p.n)
-        ptx::st_v4(static_cast<uint16_t*>(p.out) + static_cast<size_t>(row + t) * p.n + n0 + c,
-                   *reinterpret_cast<const uint4*>(staging + t * 80 + c * 2));
+      for (int i = 0; i < kOut; i += 8)
+        if (live && n + i < p.n)
+          ptx::st_v4(to + i, make_uint4(w[i / 2], w[i / 2 + 1], w[i / 2 + 2], w[i / 2 + 3]));
     }
     return;
   }
   // Magnitudes as integers keep their order, and what is not finite lies above.
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < kOut; ++i) top = max(top, __float_as_uint(v[i]) & 0x7FFFFFFFu);
   const bool wide = p.format == MXFP8_FORMAT_MXFP8;
-  uint32_t top[kTokens];
+  bool finite = top < 0x7F800000u;
+  if (wide && !finite) {  // the scale is that of the finite ones
+    top = 0u;
 #pragma unroll
-  for (int t = 0; t < kTokens; ++t) {
-    const uint32_t bits = __float_as_uint(v[t]) & 0x7FFFFFFFu;
-    top[t] = __reduce_max_sync(~0u, wide && bits >= 0x7F800000u ? 0u : bits);
-  }
-  uint32_t mine = 0;  // lane t: row t's scale
-#pragma unroll
-  for (int t = 0; t < kTokens; ++t) {
-    if (wide) {
-      const uint32_t code = scale_code(__uint_as_float(top[t]));
-      const bool finite = (__float_as_uint(v[t]) & 0x7FFFFFFFu) < 0x7F800000u;
-      staging[t * 32 + lane] = static_cast<uint8_t>(
-          to_e4m3(finite ? v[t] : __uint_as_float(0x7FC00000u), 0.0f, code));
-      if (lane == t) mine = code;
-    } else {
-      const bool all = top[t] < 0x7F800000u;
-      const uint32_t code = all ? scale_code_e2m1(__uint_as_float(top[t])) : 255u;
-      const float next = __shfl_down_sync(~0u, v[t], 1);
-      if (lane % 2 == 0)
-        staging[t * 16 + lane / 2] = all ? static_cast<uint8_t>(to_e2m1(v[t], next, code)) : 0;
-      if (lane == t) mine = code;
+    for (int i = 0; i < kOut; ++i) {
+      const uint32_t m = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+      if (m < 0x7F800000u) top = max(top, m);
     }
   }
-  __syncwarp();
-  if (n0 >= p.n) return;  // past the last block: n is whole blocks
-  const int bytes = wide ? 32 : 16;  // of a row's block
 #pragma unroll
-  for (int i0 = 0; i0 < kTokens * 2; i0 += 32) {
-    const int t = (i0 + lane) * 16 / bytes, at = (i0 + lane) * 16 % bytes;
-    if (t < kTokens && t < live)
-      ptx::st_v4(static_cast<uint8_t*>(p.out) +
-                     (static_cast<size_t>(row + t) * p.n + n0) * bytes / 32 + at,
-                 *reinterpret_cast<const uint4*>(staging + t * bytes + at));
+  for (int o = 1; o < 32 / kOut; o *= 2) top = max(top, __shfl_xor_sync(~0u, top, o));
+  live = live && n < p.n;  // n is whole blocks
+  const size_t first = static_cast<size_t>(row) * p.n + n;
+  uint8_t* const codes = static_cast<uint8_t*>(p.out);
+  uint32_t code;
+  if (wide) {
+    code = scale_code(__uint_as_float(top));
+    const float s = inverse_scale(code);
+    uint32_t w[kOut / 4];
+#pragma unroll
+    for (int i = 0; i < kOut; i += 2) {
+      float a = v[i] * s, b = v[i + 1] * s;
+      if (!finite) {
+        if (!isfinite(v[i])) a = __uint_as_float(0x7FC00000u);
+        if (!isfinite(v[i + 1])) b = __uint_as_float(0x7FC00000u);
+      }
+      const uint32_t both = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+      w[i / 4] = i % 4 ? w[i / 4] | both << 16 : both;
+    }
+    if (live) {
+      if constexpr (kOut == 16)
+        ptx::st_v4(codes + first, make_uint4(w[0], w[1], w[2], w[3]));
+      else if constexpr (kOut == 8)
+        *reinterpret_cast<uint2*>(codes + first) = make_uint2(w[0], w[1]);
+      else
+        *reinterpret_cast<uint32_t*>(codes + first) = w[0];
+    }
+  } else {
+    finite = top < 0x7F800000u;  // of the whole block
+    code = finite ? scale_code_e2m1(__uint_as_float(top)) : 255u;
+    const float s = inverse_scale(code);
+    uint64_t w = 0u;
+#pragma unroll
+    for (int i = 0; i < kOut; i += 2)
+      w |= static_cast<uint64_t>(__nv_cvt_float2_to_fp4x2(make_float2(v[i] * s, v[i + 1] * s),
+                                                          __NV_E2M1, cudaRoundNearest))
+           << 4 * i;
+    if (!finite) w = 0u;
+    if (live) {
+      if constexpr (kOut == 16)
+        *reinterpret_cast<uint64_t*>(codes + first / 2) = w;
+      else if constexpr (kOut == 8)
+        *reinterpret_cast<uint32_t*>(codes + first / 2) = static_cast<uint32_t>(w);
+      else
+        *reinterpret_cast<uint16_t*>(codes + first / 2) = static_cast<uint16_t>(w);
+    }
   }
-  if (lane < kTokens && lane < live)
-    p.out_scale[static_cast<size_t>(row + lane) * (p.n / 32) + n0 / 32] =
-        static_cast<uint8_t>(mine);
+  if (live && n % 32 == 0) p.out_scale[first / 32] = static_cast<uint8_t>(code);
 }
 
 template <class S, bool kGated>
@@ -629,38 +654,53 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     // -------------------------------------------------------------- epilogue
     const int quarter = warp % 4;  // the tensor memory lanes this warp reaches
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    constexpr int kC = S::kAtOnce, kHalf = kC / 2;
-    uint8_t* const staging = smem + S::kStaging + (warp - 2) * kC * 80;
-    // Gated: an even quarter has the gates, the odd one after it the ups.
+    constexpr int kC = S::kAtOnce;
+    // The turn: a lane has one row of W's sums of kC expert rows; it takes several outputs
+    // of one expert row instead, through shared memory.  Gated: an even quarter of the
+    // lanes has the gates, the odd one after it the ups, and each of their warps takes half
+    // of the expert rows.  Two places in turn: a place is read until the next barrier at
+    // most.
+    constexpr int kRows = kGated ? kC / 2 : kC < 16 ? kC : 16;  // expert rows at a time
+    constexpr int kShare = 32 / kRows;                          // lanes of one
     const int pair = quarter / 2;
     const bool gates = quarter % 2 == 0;
-    float* const exchange =
-        reinterpret_cast<float*>(smem + S::kExchange) + pair * 2 * kC * 32 + lane;
+    float* const turns = reinterpret_cast<float*>(smem + S::kTurns);
+    const int t = lane / kShare, n_lane = lane % kShare * kRows;
     int flip = 0;
     // kC rows' sums of this lane's row of W.
     const auto finish = [&](const Segment& s, int c, const float (&v)[kC]) {
-      const int row = s.row + c, live = s.rows - c;
+      float* const turn = turns + (flip * 4 + quarter) * kC * kTurnPitch;
+      flip ^= 1;
+#pragma unroll
+      for (int j = 0; j < kC; ++j) turn[j * kTurnPitch + lane] = v[j];
       const int w_tile = s.w_tile * kSharers + static_cast<int>(rank);
-      if constexpr (kGated) {
-        // Each of the pair's warps takes half of the rows: it gives the others'.
-        float* const box = exchange + flip * kC * 32;
-        flip ^= 1;  // the other half is read until the next barrier at most
+      const auto read = [&](const float* from, float (&x)[kRows]) {
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j)
-          box[(gates ? kHalf + j : j) * 32] = gates ? v[kHalf + j] : v[j];
-        pair_barrier(pair);
-        float h[kHalf];
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-          const float other = box[(gates ? j : kHalf + j) * 32];
-          const float g = gates ? v[j] : other, u = gates ? other : v[kHalf + j];
-          h[j] = __fdividef(g, 1.0f + __expf(-g)) * u;
+        for (int i = 0; i < kRows; i += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(from + i);
+          x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
         }
-        const int first = gates ? 0 : kHalf;
-        store_block<kHalf>(p, h, row + first, min(kHalf, live - first), w_tile * 64 + pair * 32,
-                           staging);
+      };
+      if constexpr (kGated) {
+        pair_barrier(pair);
+        const int at = (gates ? 0 : kRows) + t;
+        const float* const mine = turn + at * kTurnPitch + n_lane;
+        const int other = gates ? kC * kTurnPitch : -kC * kTurnPitch;
+        float g[kRows], u[kRows];
+        read(gates ? mine : mine + other, g);
+        read(gates ? mine + other : mine, u);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) u[i] *= __fdividef(g[i], 1.0f + __expf(-g[i]));
+        store_outputs<kRows>(p, u, s.row + c + at, c + at < s.rows, w_tile * 64 + pair * 32 + n_lane);
       } else {
-        store_block<kC>(p, v, row, min(kC, live), w_tile * kTileRows + quarter * 32, staging);
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < kC; r += kRows) {
+          float x[kRows];
+          read(turn + (r + t) * kTurnPitch + n_lane, x);
+          store_outputs<kRows>(p, x, s.row + c + r + t, c + r + t < s.rows,
+                               w_tile * kTileRows + quarter * 32 + n_lane);
+        }
       }
     };
     uint32_t before = 0, use = 0;
