@@ -258,10 +258,8 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, 
   if (d->rows < 0) return fail(MXFP8_ERR_INVALID, "rows must not be negative");
   if (!begin && d->experts != 1)
     return fail(MXFP8_ERR_INVALID, "begin is NULL, and there is more than one expert");
-  const bool wide = expert_wide(d->rows, d->experts);
-  const ExpertTile tile = expert_tile(wide);
-  // Tiles are numbered in 31 bits, and what is left of a round in k tiles.
-  if ((static_cast<int64_t>(d->rows) / tile.rows + d->experts) * w_tiles(*d) > 1 << 30)
+  // Tiles are numbered in 31 bits (32 rows the smallest).
+  if ((static_cast<int64_t>(d->rows) / 32 + d->experts) * w_tiles(*d) > 1 << 30)
     return fail(MXFP8_ERR_UNSUPPORTED, "rows x n is past 2^30 tiles");
   if (d->rows == 0) return MXFP8_OK;
   CHECK(check_pointer("laid", laid, 32));
@@ -279,6 +277,8 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, 
   cudaError_t e = cudaGetDevice(&device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return cuda_fail(e, "reading the device's SM count");
+  const int ctas = std::min(sms, kMaxExpertCtas);
+  const ExpertTile tile = expert_tile(d->rows, d->experts, w_tiles(*d), ctas);
   ExpertMaps maps{};
   CHECK(encode_codes(&maps.w, laid, d->w_format, 128, blocks_of(*d) * 128,
                      row_bytes(d->w_format, 128), 0, 0, 128 * tile.k_tiles, 1));
@@ -293,7 +293,7 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, 
   p.k_tiles = d->k / 128;
   p.gated = d->gated;
   p.format = d->out_format;
-  p.idesc = 1u << 23 | (wide ? 256u : 128u) >> 4 << 24 | (d->w_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 7 : 0u) |
+  p.idesc = 1u << 23 | (tile.kind == ExpertTile::kWide ? 256u : 128u) >> 4 << 24 | (d->w_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 7 : 0u) |
             (d->x_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 10 : 0u);
   // A copy counts the bytes that it reads, not the places that 4-bit elements take.
   const uint32_t x_row = tile.k_tiles * (d->x_format == MXFP8_FORMAT_MXFP4 ? 64 : 128);
@@ -309,8 +309,7 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, 
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                        MXFP8_EXPERT_WORKSPACE_ZEROS);
   p.flags = flags;
-  e = launch_expert_product(maps, p, wide, std::min(sms, kMaxExpertCtas),
-                            static_cast<cudaStream_t>(stream));
+  e = launch_expert_product(maps, p, tile.kind, ctas, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the experts' product");
   return MXFP8_OK;
 }

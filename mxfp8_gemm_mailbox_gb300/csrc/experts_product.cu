@@ -75,7 +75,7 @@ struct Shape {
   static constexpr uint32_t kSfa = kX + kStages * kTiles * kXTile;
   static constexpr uint32_t kSfb = kSfa + kStages * kTiles * kChunk;
   static constexpr uint32_t kTurns = kPair ? kSfa : kSfb + kStages * kTiles * kChunk;
-  static constexpr uint32_t kTables = kTurns + 2 * 4 * kAtOnce * kTurnPitch * 4;
+  static constexpr uint32_t kTables = kTurns + 4 * kAtOnce * kTurnPitch * 4;
   static constexpr uint32_t kBars = kTables + 2 * 4 * ((MXFP8_MAX_EXPERTS + 8) / 4 * 4);
   static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 4);
   static constexpr uint32_t kBytes = kMisc + 32 + 1024;
@@ -83,6 +83,7 @@ struct Shape {
 };
 // Few rows an expert: bound by the stream of W.  Many: by the products.
 using Narrow = Shape<false, 32, 2, 5, 5, 8, 2, 8>;
+using Middle = Shape<false, 64, 2, 4, 2, 32, 2, 16>;
 using Wide = Shape<true, 224, 1, 5, 1, 56, 8, 32>;
 
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -658,19 +659,16 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     // The turn: a lane has one row of W's sums of kC expert rows; it takes several outputs
     // of one expert row instead, through shared memory.  Gated: an even quarter of the
     // lanes has the gates, the odd one after it the ups, and each of their warps takes half
-    // of the expert rows.  Two places in turn: a place is read until the next barrier at
-    // most.
+    // of the expert rows.
     constexpr int kRows = kGated ? kC / 2 : kC < 16 ? kC : 16;  // expert rows at a time
     constexpr int kShare = 32 / kRows;                          // lanes of one
     const int pair = quarter / 2;
     const bool gates = quarter % 2 == 0;
     float* const turns = reinterpret_cast<float*>(smem + S::kTurns);
     const int t = lane / kShare, n_lane = lane % kShare * kRows;
-    int flip = 0;
     // kC rows' sums of this lane's row of W.
     const auto finish = [&](const Segment& s, int c, const float (&v)[kC]) {
-      float* const turn = turns + (flip * 4 + quarter) * kC * kTurnPitch;
-      flip ^= 1;
+      float* const turn = turns + quarter * kC * kTurnPitch;
 #pragma unroll
       for (int j = 0; j < kC; ++j) turn[j * kTurnPitch + lane] = v[j];
       const int w_tile = s.w_tile * kSharers + static_cast<int>(rank);
@@ -689,6 +687,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         float g[kRows], u[kRows];
         read(gates ? mine : mine + other, g);
         read(gates ? mine + other : mine, u);
+        pair_barrier(pair);  // both have read; the next rows may come
 #pragma unroll
         for (int i = 0; i < kRows; ++i) u[i] *= __fdividef(g[i], 1.0f + __expf(-g[i]));
         store_outputs<kRows>(p, u, s.row + c + at, c + at < s.rows, w_tile * 64 + pair * 32 + n_lane);
@@ -701,6 +700,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           store_outputs<kRows>(p, x, s.row + c + r + t, c + r + t < s.rows,
                                w_tile * kTileRows + quarter * 32 + n_lane);
         }
+        __syncwarp();
       }
     };
     uint32_t before = 0, use = 0;
@@ -734,6 +734,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           const uint32_t from = tmem + lanes + (buffer * S::kPipes + q) * S::kAccSlot + c;
           if constexpr (kC == 32)
             ptx::tmem_ld_32x32b_x32(from, r[q]);
+          else if constexpr (kC == 16)
+            ptx::tmem_ld_32x32b_x16(from, r[q]);
           else
             ptx::tmem_ld_32x32b_x8(from, r[q]);
         }
@@ -771,10 +773,21 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             float v[kC];
 #pragma unroll
             for (int j = 0; j < kC; ++j) v[j] = 0.0f;
-            for (int cta = lo; cta <= hi; ++cta) {
-              const float* from = place(cta);
+            // Several pieces' loads at a time, added in the order of k.
+            constexpr int kPieces = 64 / kC;
+            for (int cta = lo; cta <= hi; cta += kPieces) {
+              float x[kPieces][kC];
 #pragma unroll
-              for (int j = 0; j < kC; ++j) v[j] += __ldcg(from + (c + j) * kTileRows);
+              for (int i = 0; i < kPieces; ++i) {
+                const float* const from = place(min(cta + i, hi));
+#pragma unroll
+                for (int j = 0; j < kC; ++j)
+                  x[i][j] = cta + i <= hi ? __ldcg(from + (c + j) * kTileRows) : 0.0f;
+              }
+#pragma unroll
+              for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+                for (int j = 0; j < kC; ++j) v[j] += x[i][j];
             }
             finish(s, c, v);
           }
@@ -860,21 +873,35 @@ cudaError_t launch_as(const ExpertMaps& maps, const ExpertParams& p, int ctas,
 }  // namespace
 
 size_t expert_partial_bytes(int ctas) {
-  return static_cast<size_t>(ctas) * 2 * kTileRows * std::max(Narrow::kCols, Wide::kCols) * 4;
-}
-bool expert_wide(int rows, int experts) { return rows > Narrow::kCols * experts; }
-ExpertTile expert_tile(bool wide) {
-  return wide ? ExpertTile{Wide::kCols, Wide::kTiles, Wide::kXRows, Wide::kSmall}
-              : ExpertTile{Narrow::kCols, Narrow::kTiles, Narrow::kXRows, Narrow::kSmall};
+  return static_cast<size_t>(ctas) * 2 * kTileRows * Wide::kCols * 4;
 }
 
-cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p, bool wide,
-                                  int ctas, cudaStream_t stream) {
-  if (wide)
-    return p.gated ? launch_as<Wide, true>(maps, p, ctas, stream)
-                   : launch_as<Wide, false>(maps, p, ctas, stream);
-  return p.gated ? launch_as<Narrow, true>(maps, p, ctas, stream)
-                 : launch_as<Narrow, false>(maps, p, ctas, stream);
+ExpertTile expert_tile(int rows, int experts, int w_tiles, int ctas) {
+  const auto of = [](auto s, ExpertTile::Kind kind) {
+    using S = decltype(s);
+    static_assert(S::kCols <= Wide::kCols, "partials");
+    return ExpertTile{kind, S::kCols, S::kTiles, S::kXRows, S::kSmall};
+  };
+  const int64_t all = static_cast<int64_t>(experts) * w_tiles;
+  if (rows <= 12 * static_cast<int64_t>(experts)) return of(Narrow{}, ExpertTile::kNarrow);
+  if (rows <= (all > 2 * ctas ? 96 : 48) * static_cast<int64_t>(experts))
+    return of(Middle{}, ExpertTile::kMiddle);
+  return of(Wide{}, ExpertTile::kWide);
+}
+
+cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p,
+                                  ExpertTile::Kind kind, int ctas, cudaStream_t stream) {
+  switch (kind) {
+    case ExpertTile::kNarrow:
+      return p.gated ? launch_as<Narrow, true>(maps, p, ctas, stream)
+                     : launch_as<Narrow, false>(maps, p, ctas, stream);
+    case ExpertTile::kMiddle:
+      return p.gated ? launch_as<Middle, true>(maps, p, ctas, stream)
+                     : launch_as<Middle, false>(maps, p, ctas, stream);
+    default:
+      return p.gated ? launch_as<Wide, true>(maps, p, ctas, stream)
+                     : launch_as<Wide, false>(maps, p, ctas, stream);
+  }
 }
 
 cudaError_t launch_lay(const uint8_t* w, const uint8_t* scale, uint8_t* laid, uint8_t* laid_scale,

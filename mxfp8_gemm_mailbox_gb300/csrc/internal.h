@@ -249,19 +249,19 @@ struct ExpertParams {
 constexpr int kMaxExpertCtas = 160;  // a ticket each: 640 bytes of the workspace's zeros
 static_assert(kMaxExpertCtas * 4 <= MXFP8_EXPERT_WORKSPACE_ZEROS, "tickets");
 size_t expert_partial_bytes(int ctas);
-bool expert_wide(int rows, int experts);  // which kernel
 struct ExpertTile {
+  enum Kind { kNarrow, kMiddle, kWide } kind;
   int rows;             // of a tile
   int k_tiles;          // of a stage
   int x_rows, x_small;  // rows of the two copies of x
 };
-ExpertTile expert_tile(bool wide);
+ExpertTile expert_tile(int rows, int experts, int w_tiles, int ctas);
 struct ExpertMaps {
   CUtensorMap w, x;
   CUtensorMap x_small;  // of fewer rows
 };
-cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p, bool wide,
-                                  int ctas, cudaStream_t stream);
+cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p,
+                                  ExpertTile::Kind kind, int ctas, cudaStream_t stream);
 cudaError_t launch_lay(const uint8_t* w, const uint8_t* scale, uint8_t* laid, uint8_t* laid_scale,
                        int experts, int n, bool gated, bool narrow, int w_tiles, int k_tiles,
                        cudaStream_t stream);
