@@ -278,7 +278,7 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, 
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (e != cudaSuccess) return cuda_fail(e, "reading the device's SM count");
   const int ctas = std::min(sms, kMaxExpertCtas);
-  const ExpertTile tile = expert_tile(d->rows, d->experts, w_tiles(*d), ctas);
+  const ExpertTile tile = expert_tile(d->rows, d->experts, w_tiles(*d), d->k / 128, ctas);
   ExpertMaps maps{};
   CHECK(encode_codes(&maps.w, laid, d->w_format, 128, blocks_of(*d) * 128,
                      row_bytes(d->w_format, 128), 0, 0, 128 * tile.k_tiles, 1));

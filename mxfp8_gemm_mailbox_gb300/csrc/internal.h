@@ -251,11 +251,10 @@ static_assert(kMaxExpertCtas * 4 <= MXFP8_EXPERT_WORKSPACE_ZEROS, "tickets");
 size_t expert_partial_bytes(int ctas);
 struct ExpertTile {
   enum Kind { kNarrow, kMiddle, kWide } kind;
-  int rows;             // of a tile
   int k_tiles;          // of a stage
   int x_rows, x_small;  // rows of the two copies of x
 };
-ExpertTile expert_tile(int rows, int experts, int w_tiles, int ctas);
+ExpertTile expert_tile(int rows, int experts, int w_tiles, int k_tiles, int ctas);
 struct ExpertMaps {
   CUtensorMap w, x;
   CUtensorMap x_small;  // of fewer rows
