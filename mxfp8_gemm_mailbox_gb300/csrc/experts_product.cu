@@ -351,6 +351,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   int* const rows = reinterpret_cast<int*>(smem + S::kTables);
   int* const tiles = rows + (MXFP8_MAX_EXPERTS + 8) / 4 * 4;
 
+  // What the deal reads first, while the kernel before still runs.
+  if (p.begin && tid * 32 <= p.experts) ptx::prefetch_l2_line(p.begin + tid * 32);
   const uint32_t rank = S::kPair ? ptx::cluster_ctarank() : 0;
   // At a barrier of the CTA that issues the products.
   const auto arrive = [&](uint32_t bar) {

@@ -147,6 +147,10 @@ __device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
                "r"(bytes)
                : "memory");
 }
+// Warm L2 with the line of an address, whoever may still write it.
+__device__ __forceinline__ void prefetch_l2_line(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
 // Warm L2 with one 2-D TMA box.
 __device__ __forceinline__ void prefetch_l2_tile(const void* tmap, int32_t c0, int32_t c1) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
