@@ -637,16 +637,15 @@ typedef struct mxfp8_expert_desc {
   int32_t rows;       /* of x and of the result                                           */
 } mxfp8_expert_desc;
 
-/* Bytes of the matrices and their scales as the product reads them; 0 for an invalid
- * shape (x_format, out_format and rows do not count here). */
-size_t mxfp8_expert_bytes(const mxfp8_expert_desc* desc);
+/* Bytes of the matrices' scales as the product reads them; 0 for an invalid shape
+ * (x_format, out_format and rows do not count here). */
+size_t mxfp8_expert_scales_bytes(const mxfp8_expert_desc* desc);
 
-/* laid (device, 32-byte aligned, mxfp8_expert_bytes) = the matrices w (device, 16-byte
- * aligned, [experts][n, or 2 n gated] rows of K codes) and their scales (device, 4-byte
- * aligned, E8M0 [experts][n, or 2 n][K/32]) in the products' order: tiles of 128 rows x
- * 128 k, each contiguous.  Once a set of matrices; neither is read again. */
-mxfp8_status mxfp8_expert_lay(const mxfp8_expert_desc* desc, const void* w, const void* w_scale,
-                              void* laid, void* stream);
+/* laid (device, 16-byte aligned, mxfp8_expert_scales_bytes) = the matrices' scales
+ * (device, 4-byte aligned, E8M0 [experts][n, or 2 n gated][K/32]) in the products'
+ * order; once a set of matrices. */
+mxfp8_status mxfp8_expert_lay_scales(const mxfp8_expert_desc* desc, const void* w_scale, void* laid,
+                                     void* stream);
 
 /* Workspace bytes of the product, whatever the call: 37 MB. */
 size_t mxfp8_expert_workspace_bytes(void);
@@ -658,7 +657,9 @@ size_t mxfp8_expert_workspace_bytes(void);
  *
  * y = silu(gate) up of it where gated; sums in FP32 (the tensor core's), rounded
  * once, to BF16 or as mxfp8_quantize does.
- *  laid:   by mxfp8_expert_lay, with the same desc but for x_format, out_format and rows;
+ *  w:      device, [experts][n or 2 n] rows of K codes, 32-byte aligned; laid: its
+ *          scales, by mxfp8_expert_lay_scales with the same desc (but for x_format,
+ *          out_format and rows);
  *  x, x_scale: device, [rows] of K codes (32-byte aligned) and K/32 scales (4);
  *  begin:  device int32 [experts + 1], ascending from 0 to at most rows; NULL with
  *          one expert, which then has all rows.  Rows in no expert are left as
@@ -673,10 +674,10 @@ size_t mxfp8_expert_workspace_bytes(void);
  *  flags:  device int32 or NULL; a wait of the pipeline that runs out raises
  *          MXFP8_FLAG_GEMM_TIMEOUT.
  * Results have the same bits every time.  rows = 0 launches nothing. */
-mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* desc, const void* laid, const void* x,
-                                  const void* x_scale, const int32_t* begin, void* out,
-                                  void* out_scale, void* workspace, size_t workspace_bytes,
-                                  int32_t* flags, void* stream);
+mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* desc, const void* w, const void* laid,
+                                  const void* x, const void* x_scale, const int32_t* begin,
+                                  void* out, void* out_scale, void* workspace,
+                                  size_t workspace_bytes, int32_t* flags, void* stream);
 
 /* out [tokens][n] BF16 = add[t] + sum_j weight[t][j] y[slot[t][j]], in FP32, j
  * ascending, rounded once.  y: device, BF16, `slots` rows of n, `stride` elements

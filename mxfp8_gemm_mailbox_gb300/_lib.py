@@ -96,12 +96,12 @@ SIGNATURES = {
     "mxfp8_quantize": (ctypes.c_int, [_vp, _i32, _i64, _i64, _i32, _vp, _i64, _i32, _vp, _vp, _vp,
                                       _vp]),
     "mxfp8_dequantize": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp]),
-    "mxfp8_expert_lay": (ctypes.c_int, [ctypes.POINTER(ExpertDesc), _vp, _vp, _vp, _vp]),
+    "mxfp8_expert_lay_scales": (ctypes.c_int, [ctypes.POINTER(ExpertDesc), _vp, _vp, _vp]),
     "mxfp8_expert_product": (ctypes.c_int, [ctypes.POINTER(ExpertDesc), _vp, _vp, _vp, _vp, _vp,
-                                            _vp, _vp, _sz, _vp, _vp]),
+                                            _vp, _vp, _vp, _sz, _vp, _vp]),
     "mxfp8_combine": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _i64, _i32, _i32, _vp, _vp, _vp,
                                      _vp]),
-    "mxfp8_expert_bytes": (_sz, [ctypes.POINTER(ExpertDesc)]),
+    "mxfp8_expert_scales_bytes": (_sz, [ctypes.POINTER(ExpertDesc)]),
     "mxfp8_expert_workspace_bytes": (_sz, []),
     "mailbox_publish": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _vp]),
     "mailbox_consume": (ctypes.c_int, [_vp, _vp, _i32, _i32, _i32, _vp, _u64, _vp]),

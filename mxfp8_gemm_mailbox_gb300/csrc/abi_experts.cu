@@ -59,46 +59,66 @@ int w_tiles(const mxfp8_expert_desc& d) {
   return (d.n + outputs - 1) / outputs;
 }
 
-// 8-bit or 4-bit codes, the latter landing as 16 in 16 bytes: rows of `width`, `pitch`
-// bytes apart, and `depth` planes of them, in boxes of 128 x box_rows x box_depth.
+int row_bytes(int32_t format, int32_t k) { return format == MXFP8_FORMAT_MXFP4 ? k / 2 : k; }
+
+// An axis of a tensor map past the first: its size, how far apart its elements lie in
+// bytes, and how many a copy takes.
+struct Axis {
+  int64_t size, stride;
+  int box;
+};
+// Codes of 8 bits, or of 4, which land as 16 in 16 bytes; a copy takes 128 along the first
+// axis.
+template <int kAxes>
 mxfp8_status encode_codes(CUtensorMap* map, const void* base, int32_t format, int64_t width,
-                          int64_t rows, int64_t pitch, int64_t depth, int64_t plane, int box_rows,
-                          int box_depth) {
+                          const Axis (&axes)[kAxes]) {
   EncodeTiled fn = encode_tiled();
   if (!fn) return fail(MXFP8_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(depth)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch), static_cast<cuuint64_t>(plane)};
-  const cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_rows),
-                             static_cast<cuuint32_t>(box_depth)};
-  const cuuint32_t elem[3] = {1, 1, 1};
+  cuuint64_t dims[kAxes + 1], strides[kAxes];
+  cuuint32_t box[kAxes + 1], elem[kAxes + 1];
+  dims[0] = static_cast<cuuint64_t>(width);
+  box[0] = 128;
+  for (int i = 0; i < kAxes; ++i) {
+    dims[i + 1] = static_cast<cuuint64_t>(axes[i].size);
+    strides[i] = static_cast<cuuint64_t>(axes[i].stride);
+    box[i + 1] = static_cast<cuuint32_t>(axes[i].box);
+  }
+  for (cuuint32_t& e : elem) e = 1;
   const CUresult r = fn(
       map,
       format == MXFP8_FORMAT_MXFP4 ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B
                                    : CU_TENSOR_MAP_DATA_TYPE_UINT8,
-      depth ? 3 : 2, const_cast<void*>(base), dims, strides, box, elem,
-      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+      kAxes + 1, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail(MXFP8_ERR_CUDA, "cuTensorMapEncodeTiled failed with CUresult " + std::to_string(r));
   return MXFP8_OK;
 }
-int row_bytes(int32_t format, int32_t k) { return format == MXFP8_FORMAT_MXFP4 ? k / 2 : k; }
-// x's rows, k_tiles of 128 k a copy: the k tiles of more than one are planes.
+// A tile of W along k_tiles k tiles: 128 rows of an expert; gated 32 rows of the gate, theirs
+// of the up half, twice.  Gated, blocks of 32 rows are numbered through all experts, and the
+// halves lie n rows apart (the last expert's up blocks are reached as the other half of its
+// gate's, so that axis ends before them).
+mxfp8_status encode_w(CUtensorMap* map, const void* w, const mxfp8_expert_desc& d, int k_tiles) {
+  const int64_t row = row_bytes(d.w_format, d.k), n = d.n;
+  const Axis k{d.k / 128, row_bytes(d.w_format, 128), k_tiles};
+  if (d.gated)
+    return encode_codes(map, w, d.w_format, 128,
+                        {{32, row, 32},
+                         {2, n * row, 2},
+                         {(static_cast<int64_t>(d.experts) * 2 - 1) * (n / 32), 32 * row, 2},
+                         k});
+  return encode_codes(map, w, d.w_format, 128,
+                      {{n, row, 128}, {1, n * row, 1}, {d.experts, n * row, 1}, k});
+}
+// x's rows; the k tiles of more than one a copy are planes.
 mxfp8_status encode_x(CUtensorMap* map, const void* x, const mxfp8_expert_desc& d, int rows,
                       int k_tiles) {
-  const int64_t pitch = row_bytes(d.x_format, d.k);
+  const int64_t row = row_bytes(d.x_format, d.k);
   if (k_tiles == 1)
-    return encode_codes(map, x, d.x_format, d.k, d.rows, pitch, 1, pitch * d.rows, rows, 1);
-  return encode_codes(map, x, d.x_format, 128, d.rows, pitch, d.k / 128,
-                      row_bytes(d.x_format, 128), rows, k_tiles);
-}
-// k tiles of all tiles of W.
-int64_t blocks_of(const mxfp8_expert_desc& d) {
-  return static_cast<int64_t>(d.experts) * w_tiles(d) * (d.k / 128);
-}
-size_t codes_bytes(const mxfp8_expert_desc& d) {
-  return static_cast<size_t>(blocks_of(d)) * 128 * row_bytes(d.w_format, 128);
+    return encode_codes(map, x, d.x_format, d.k, {{d.rows, row, rows}, {1, row * d.rows, 1}});
+  return encode_codes(map, x, d.x_format, 128,
+                      {{d.rows, row, rows}, {d.k / 128, row_bytes(d.x_format, 128), k_tiles}});
 }
 
 }  // namespace
@@ -217,24 +237,20 @@ mxfp8_status mxfp8_dequantize(const void* codes, const void* scales, int64_t row
   return MXFP8_OK;
 }
 
-size_t mxfp8_expert_bytes(const mxfp8_expert_desc* d) {
+size_t mxfp8_expert_scales_bytes(const mxfp8_expert_desc* d) {
   if (check_matrices(d) != MXFP8_OK) return 0;
-  return codes_bytes(*d) + static_cast<size_t>(blocks_of(*d)) * 512;
+  return static_cast<size_t>(d->experts) * w_tiles(*d) * (d->k / 128) * 512;
 }
 
-mxfp8_status mxfp8_expert_lay(const mxfp8_expert_desc* d, const void* w, const void* w_scale,
-                              void* laid, void* stream) {
+mxfp8_status mxfp8_expert_lay_scales(const mxfp8_expert_desc* d, const void* w_scale, void* laid,
+                                     void* stream) {
   CHECK(check_matrices(d));
-  CHECK(check_pointer("w", w, 16));
   CHECK(check_pointer("w_scale", w_scale, 4));
-  CHECK(check_pointer("laid", laid, 32));
-  uint8_t* const codes = static_cast<uint8_t*>(laid);
-  const cudaError_t e =
-      launch_lay(static_cast<const uint8_t*>(w), static_cast<const uint8_t*>(w_scale), codes,
-                 codes + codes_bytes(*d), d->experts, d->n, d->gated,
-                 d->w_format == MXFP8_FORMAT_MXFP4, w_tiles(*d), d->k / 128,
-                 static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "laying the matrices");
+  CHECK(check_pointer("laid", laid, 16));
+  const cudaError_t e = launch_lay_scales(static_cast<const uint8_t*>(w_scale),
+                                          static_cast<uint8_t*>(laid), d->experts, d->n, d->gated,
+                                          w_tiles(*d), d->k / 128, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "laying the scales");
   return MXFP8_OK;
 }
 
@@ -242,8 +258,8 @@ size_t mxfp8_expert_workspace_bytes(void) {
   return MXFP8_EXPERT_WORKSPACE_ZEROS + expert_partial_bytes(kMaxExpertCtas);
 }
 
-mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, const void* x,
-                                  const void* x_scale, const int32_t* begin,
+mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, const void* laid,
+                                  const void* x, const void* x_scale, const int32_t* begin,
                                   void* out, void* out_scale, void* workspace,
                                   size_t workspace_bytes, int32_t* flags, void* stream) {
   CHECK(check_matrices(d));
@@ -262,7 +278,8 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, 
   if ((static_cast<int64_t>(d->rows) / 32 + d->experts) * w_tiles(*d) > 1 << 30)
     return fail(MXFP8_ERR_UNSUPPORTED, "rows x n is past 2^30 tiles");
   if (d->rows == 0) return MXFP8_OK;
-  CHECK(check_pointer("laid", laid, 32));
+  CHECK(check_pointer("w", w, 32));
+  CHECK(check_pointer("laid", laid, 16));
   CHECK(check_pointer("x", x, 32));
   CHECK(check_pointer("x_scale", x_scale, 4));
   if (begin) CHECK(check_pointer("begin", begin, 4));
@@ -280,8 +297,7 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, 
   const int ctas = std::min(sms, kMaxExpertCtas);
   const ExpertTile tile = expert_tile(d->rows, d->experts, w_tiles(*d), d->k / 128, ctas);
   ExpertMaps maps{};
-  CHECK(encode_codes(&maps.w, laid, d->w_format, 128, blocks_of(*d) * 128,
-                     row_bytes(d->w_format, 128), 0, 0, 128 * tile.k_tiles, 1));
+  CHECK(encode_w(&maps.w, w, *d, tile.k_tiles));
   CHECK(encode_x(&maps.x, x, *d, tile.x_rows, tile.k_tiles));
   CHECK(encode_x(&maps.x_small, x, *d, tile.x_small, tile.k_tiles));
   constexpr uint32_t kE2M1 = 5;  // the products' type codes; E4M3 is 0
@@ -300,7 +316,7 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* laid, 
   p.w_bytes = 128 * tile.k_tiles * (d->w_format == MXFP8_FORMAT_MXFP4 ? 64 : 128);
   p.x_bytes = tile.x_rows * x_row;
   p.x_small_bytes = tile.x_small * x_row;
-  p.w_sf = static_cast<const uint8_t*>(laid) + codes_bytes(*d);
+  p.w_sf = static_cast<const uint8_t*>(laid);
   p.x_scale = static_cast<const uint8_t*>(x_scale);
   p.begin = begin;
   p.out = out;

@@ -640,22 +640,23 @@ PyObject* dequantize(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
-// (experts, n, k, gated, w_format, laid, workspace, flags, x, x_scale, begin | None, format | None,
-//  out | None, out_scale | None, stream | None) -> out or (out, out_scale)
+// (experts, n, k, gated, w_format, w, laid scales, workspace, flags, x, x_scale, begin | None,
+//  format | None, out | None, out_scale | None, stream | None) -> out or (out, out_scale)
 PyObject* expert_product(PyObject*, PyObject* const* args, Py_ssize_t count) {
   HANDLE_TH_ERRORS
-  arguments(count, 15);
+  arguments(count, 16);
   mxfp8_expert_desc desc{};
   desc.experts = static_cast<int32_t>(integer(args[0]));
   desc.n = static_cast<int32_t>(integer(args[1]));
   desc.k = static_cast<int32_t>(integer(args[2]));
   desc.gated = static_cast<int32_t>(integer(args[3]));
   desc.w_format = static_cast<int32_t>(integer(args[4]));
-  const at::Tensor &laid = tensor(args[5], "laid"), &workspace = tensor(args[6], "workspace");
-  const at::Tensor &x = tensor(args[8], "x"), &x_scale = tensor(args[9], "x_scale");
+  const at::Tensor &w = tensor(args[5], "w"), &laid = tensor(args[6], "laid");
+  const at::Tensor& workspace = tensor(args[7], "workspace");
+  const at::Tensor &x = tensor(args[9], "x"), &x_scale = tensor(args[10], "x_scale");
   const int64_t n = desc.n, k = desc.k;
   const int device = on_current_device(x, "x");
-  if (gpu_of(laid) != device)
+  if (gpu_of(w) != device)
     refuse(PyExc_ValueError,
            "x is on device " + std::to_string(device) + ", this object's matrices are not");
   if (x.dim() != 2 || (x.size(1) != k && x.size(1) != k / 2))
@@ -665,56 +666,57 @@ PyObject* expert_product(PyObject*, PyObject* const* args, Py_ssize_t count) {
   exact_codes(x, "x", x.sizes(), device);
   exact_codes(x_scale, "x_scale", {rows, k / 32}, device);
   desc.x_format = x.size(1) == k ? MXFP8_FORMAT_MXFP8 : MXFP8_FORMAT_MXFP4;
-  desc.out_format = format_of(args[11], true);
+  desc.out_format = format_of(args[12], true);
   desc.rows = narrowed(rows, "the number of rows");
   const int32_t* begin = nullptr;
-  if (args[10] != Py_None) {
-    const at::Tensor& b = tensor(args[10], "begin");
+  if (args[11] != Py_None) {
+    const at::Tensor& b = tensor(args[11], "begin");
     expect(b, "begin", at::kInt, {desc.experts + 1}, device);
     begin = static_cast<const int32_t*>(b.data_ptr());
   }
-  int32_t* const flags = flags_of(args[7], device);
+  int32_t* const flags = flags_of(args[8], device);
   const bool codes = desc.out_format != MXFP8_FORMAT_BF16;
   if (codes && n % 32)
     refuse(PyExc_ValueError, "N must be a multiple of 32 to be rounded to blocks, got " +
                                  std::to_string(n));
-  if (!codes && args[13] != Py_None) refuse(PyExc_ValueError, "out_scale goes with a format");
-  const CallStream stream(args[14], device);
+  if (!codes && args[14] != Py_None) refuse(PyExc_ValueError, "out_scale goes with a format");
+  const CallStream stream(args[15], device);
   const int64_t width = desc.out_format == MXFP8_FORMAT_MXFP4 ? n / 2 : n;
   at::Tensor out, scale;
-  if (args[12] == Py_None) {
+  if (args[13] == Py_None) {
     out = new_tensor({rows, width},
                      desc.out_format == MXFP8_FORMAT_BF16    ? at::kBFloat16
                      : desc.out_format == MXFP8_FORMAT_MXFP8 ? at::kFloat8_e4m3fn
                                                              : at::kByte,
                      device);
   } else {
-    out = tensor(args[12], "out");
+    out = tensor(args[13], "out");
     if (codes)
       exact_codes(out, "out", {rows, width}, device);
     else
       expect(out, "out", at::kBFloat16, {rows, width}, device);
   }
   if (codes) {
-    if (args[13] == Py_None) {
+    if (args[14] == Py_None) {
       scale = new_tensor({rows, n / 32}, at::kFloat8_e8m0fnu, device);
     } else {
-      scale = tensor(args[13], "out_scale");
+      scale = tensor(args[14], "out_scale");
       exact_codes(scale, "out_scale", {rows, n / 32}, device);
     }
   }
-  const void *const lp = laid.data_ptr(), *const xp = x.data_ptr(), *const sp = x_scale.data_ptr();
+  const void *const wp = w.data_ptr(), *const lp = laid.data_ptr(), *const xp = x.data_ptr(),
+                    *const sp = x_scale.data_ptr();
   void *const op = out.data_ptr(), *const tp = codes ? scale.data_ptr() : nullptr,
               *const space = workspace.data_ptr();
   const auto bytes = static_cast<size_t>(workspace.numel());
   check(unlocked([&] {
-          return mxfp8_expert_product(&desc, lp, xp, sp, begin, op, tp, space, bytes, flags, stream);
+          return mxfp8_expert_product(&desc, wp, lp, xp, sp, begin, op, tp, space, bytes, flags, stream);
         }),
         "mxfp8_expert_product");
-  THPObjectPtr a(args[12] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[12]));
+  THPObjectPtr a(args[13] == Py_None ? THPVariable_Wrap(std::move(out)) : given(args[13]));
   if (!a) throw python_error();
   if (!codes) return a.release();
-  THPObjectPtr b(args[13] == Py_None ? THPVariable_Wrap(std::move(scale)) : given(args[13]));
+  THPObjectPtr b(args[14] == Py_None ? THPVariable_Wrap(std::move(scale)) : given(args[14]));
   if (!b) throw python_error();
   return PyTuple_Pack(2, a.get(), b.get());
   END_HANDLE_TH_ERRORS

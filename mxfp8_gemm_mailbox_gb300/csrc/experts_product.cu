@@ -412,14 +412,18 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       uint32_t stage = 0;  // of all this CTA's stages; the slot's use: stage / kStages
       bool ok = true;
       while (ok && share.next(s)) {
-        // A pair's CTAs have a tile of W each (the last may have none: what comes of the one
-        // it takes then is not stored) and half of the columns.
+        // A pair's CTAs have a tile of W each (the last may have none: what is copied then
+        // is not stored) and half of the columns.
         const int w_tile = s.w_tile * kSharers + static_cast<int>(rank);
         const int columns = (s.rows + S::kStep - 1) / S::kStep * S::kStep / kSharers;
         const int row = s.row + static_cast<int>(rank) * columns;
         const bool small = columns <= S::kSmall;
         const uint32_t x_bytes = small ? p.x_small_bytes : p.x_bytes;
-        const int w = (s.expert * p.w_tiles + min(w_tile, p.w_tiles - 1)) * p.k_tiles;
+        // Gated: blocks of 32 rows are numbered through all experts' halves.
+        const int w1 = kGated ? 0 : w_tile * kTileRows;
+        const int w3 = kGated ? s.expert * (p.n / 16) + w_tile * 2 : s.expert;
+        const uint8_t* const sf =
+            p.w_sf + static_cast<size_t>(s.expert * p.w_tiles + w_tile) * p.k_tiles * kChunk;
         for (int kt = s.kt0; kt < s.kt1; kt += S::kTiles, ++stage) {
           const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
           if (!ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs)) {
@@ -434,11 +438,11 @@ __global__ void __launch_bounds__(S::kThreads, 1)
                 full, kSharers * ((of_w ? p.w_bytes : 0) + (of_x ? x_bytes : 0)) + chunks);
           const uint32_t done = S::kPair ? ptx::map_to_rank(full, 0) : full;
           if (of_w) {
-            ptx::tma_load_2d<S::kPair>(sbase + slot * S::kTiles * kWTile, &tmap_w, 0,
-                                       (w + kt) * kTileRows, done);
+            ptx::tma_load_5d<S::kPair>(sbase + slot * S::kTiles * kWTile, &tmap_w, 0, w1, 0, w3, kt,
+                                       done);
             if constexpr (!S::kPair)
               ptx::bulk_load(sbase + S::kSfa + slot * S::kTiles * kChunk,
-                             p.w_sf + static_cast<size_t>(w + kt) * kChunk, chunks, full);
+                             sf + static_cast<size_t>(kt) * kChunk, chunks, full);
           }
           if (of_x)
             ptx::tma_load_3d<S::kPair>(sbase + S::kX + slot * S::kTiles * S::kXTile,
@@ -814,39 +818,23 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   }
 }
 
-// W as the copies read it, [expert][tile][k tile] of 128 rows of 128 codes, and its
-// scales in the same order, 512 bytes a k tile: row a's four codes at (a % 32) 16 +
-// (a / 32) 4.  Rows past the last are zeros.  (Read in place, a copy's rows of 64 or
-// 128 bytes lie K apart: 89 us in place of NN for the gated step of 64 rows.)
-template <bool kNarrow>
-__global__ void __launch_bounds__(256)
-    lay_kernel(const uint8_t* w, const uint8_t* scale, uint8_t* laid, uint8_t* laid_scale, int n,
-               bool gated, int w_tiles, int k_tiles) {
-  constexpr int kRowBytes = kNarrow ? 64 : 128, kShares = kRowBytes / 16;
-  const int kt = blockIdx.x, j = blockIdx.y, e = blockIdx.z;
-  const size_t block = (static_cast<size_t>(e) * w_tiles + j) * k_tiles + kt;
-  const int rows = gated ? 2 * n : n;  // of an expert
-  const auto row_of = [&](int a) {     // lane a's, or -1
-    const int output = gated ? j * 64 + a / 64 * 32 + a % 32 : j * kTileRows + a;
-    return output < n ? (gated ? a / 32 % 2 * n : 0) + output : -1;
-  };
-  for (int i = threadIdx.x; i < kTileRows * kShares; i += 256) {
-    const int row = row_of(i / kShares);
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= 0)
-      v = *reinterpret_cast<const uint4*>(
-          w + ((static_cast<size_t>(e) * rows + row) * k_tiles + kt) * kRowBytes +
-          i % kShares * 16);
-    *reinterpret_cast<uint4*>(laid + block * kTileRows * kRowBytes + i * 16) = v;
+// W's scales as the tensor-memory copies read them: [expert][tile][k tile], a chunk of
+// 512 bytes each, lane a's four codes at (a % 32) 16 + (a / 32) 4.  Lane a of tile j holds
+// row 128 j + a, or gated output 64 j + 32 (a / 64) + a % 32 of the half a / 32 % 2.
+__global__ void __launch_bounds__(128) lay_scales_kernel(const uint8_t* scale, uint8_t* laid, int n,
+                                                         bool gated, int w_tiles, int k_tiles) {
+  ptx::launch_dependents();
+  ptx::grid_dependency_wait();
+  const int a = threadIdx.x, kt = blockIdx.x, j = blockIdx.y, e = blockIdx.z;
+  const int output = gated ? j * 64 + a / 64 * 32 + a % 32 : j * kTileRows + a;
+  uint32_t codes = 0x7F7F7F7Fu;
+  if (output < n) {
+    const size_t row = static_cast<size_t>(e) * (gated ? 2 * n : n) +
+                       (gated ? a / 32 % 2 * n : 0) + output;
+    codes = *reinterpret_cast<const uint32_t*>(scale + (row * k_tiles + kt) * 4);
   }
-  if (threadIdx.x < kTileRows) {
-    const int a = threadIdx.x, row = row_of(a);
-    uint32_t codes = 0x7F7F7F7Fu;
-    if (row >= 0)
-      codes = *reinterpret_cast<const uint32_t*>(
-          scale + ((static_cast<size_t>(e) * rows + row) * k_tiles + kt) * 4);
-    *reinterpret_cast<uint32_t*>(laid_scale + block * kChunk + a % 32 * 16 + a / 32 * 4) = codes;
-  }
+  uint8_t* chunk = laid + ((static_cast<size_t>(e) * w_tiles + j) * k_tiles + kt) * kChunk;
+  *reinterpret_cast<uint32_t*>(chunk + a % 32 * 16 + a / 32 * 4) = codes;
 }
 
 template <class S, bool kGated>
@@ -923,16 +911,10 @@ cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p,
   }
 }
 
-cudaError_t launch_lay(const uint8_t* w, const uint8_t* scale, uint8_t* laid, uint8_t* laid_scale,
-                       int experts, int n, bool gated, bool narrow, int w_tiles, int k_tiles,
-                       cudaStream_t stream) {
-  const dim3 grid(k_tiles, w_tiles, experts);
-  if (narrow)
-    lay_kernel<true><<<grid, 256, 0, stream>>>(w, scale, laid, laid_scale, n, gated, w_tiles,
-                                               k_tiles);
-  else
-    lay_kernel<false><<<grid, 256, 0, stream>>>(w, scale, laid, laid_scale, n, gated, w_tiles,
-                                                k_tiles);
+cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,
+                              int w_tiles, int k_tiles, cudaStream_t stream) {
+  lay_scales_kernel<<<dim3(k_tiles, w_tiles, experts), 128, 0, stream>>>(scale, laid, n, gated,
+                                                                         w_tiles, k_tiles);
   return cudaGetLastError();
 }
 

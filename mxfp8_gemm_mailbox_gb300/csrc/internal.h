@@ -237,7 +237,7 @@ struct ExpertParams {
   uint32_t idesc;             // the products', without their columns
   uint32_t w_bytes;           // what a stage's copies of W, of x, of fewer rows of x count
   uint32_t x_bytes, x_small_bytes;
-  const uint8_t* w_sf;        // laid by launch_lay
+  const uint8_t* w_sf;        // laid by launch_lay_scales
   const uint8_t* x_scale;     // [rows][4 k_tiles]
   const int32_t* begin;       // [experts + 1], or nullptr: one expert has all rows
   void* out;
@@ -261,8 +261,7 @@ struct ExpertMaps {
 };
 cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p,
                                   ExpertTile::Kind kind, int ctas, cudaStream_t stream);
-cudaError_t launch_lay(const uint8_t* w, const uint8_t* scale, uint8_t* laid, uint8_t* laid_scale,
-                       int experts, int n, bool gated, bool narrow, int w_tiles, int k_tiles,
-                       cudaStream_t stream);
+cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,
+                              int w_tiles, int k_tiles, cudaStream_t stream);
 
 }  // namespace mxfp8

@@ -77,12 +77,11 @@ class ExpertProduct:
     ``gated``: N holds a gate's rows, then as many of an up matrix, and the result is
     silu(gate) x up, N / 2 wide.
 
-    Both are copied, once, into the products' order (``laid``): tiles that are read in
-    one piece.  The constructor waits for that, and neither is used afterwards.  The
-    workspace (37 MB) and the flags word live here; ``workspace``: another product's, to
-    be shared.  Calls that share one are ordered on one stream, made by one host thread at
-    a time, and the object outlives what they have queued on another stream than the one
-    it was made on."""
+    The codes stay borrowed; the scales are copied, once, into the products' order, and
+    the constructor waits for that.  The workspace (37 MB) and the flags word live here;
+    ``workspace``: another product's, to be shared.  Calls that share one are ordered on
+    one stream, made by one host thread at a time, and the object outlives what they have
+    queued on another stream than the one it was made on."""
 
     def __init__(self, w: torch.Tensor, w_scale: torch.Tensor, gated: bool = False,
                  workspace: torch.Tensor | None = None):
@@ -111,7 +110,7 @@ class ExpertProduct:
         self.n, self.k, self.gated = outputs // 2 if gated else outputs, k, bool(gated)
         w_format = _lib.FORMAT_MXFP8 if w.shape[-1] == k else _lib.FORMAT_MXFP4
         desc = _lib.ExpertDesc(self.experts, self.n, k, self.gated, w_format)
-        nbytes = lib.mxfp8_expert_bytes(ctypes.byref(desc))
+        nbytes = lib.mxfp8_expert_scales_bytes(ctypes.byref(desc))
         if nbytes == 0:
             raise ValueError(lib.mxfp8_last_error().decode())
         need = lib.mxfp8_expert_workspace_bytes()
@@ -121,16 +120,16 @@ class ExpertProduct:
         elif (workspace.dtype != torch.uint8 or workspace.numel() < need
               or workspace.device != w.device or not workspace.is_contiguous()):
             raise ValueError(f"workspace must be another product's on {w.device}")
-        self.workspace = workspace
-        self.laid = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
+        self.w, self.workspace = w, workspace
+        self.scales = torch.empty(nbytes, dtype=torch.uint8, device=w.device)
         self.flags = torch.zeros(1, dtype=torch.int32, device=w.device)
         with torch.cuda.device(w.device):
-            check(lib.mxfp8_expert_lay(ctypes.byref(desc), w.data_ptr(), w_scale.data_ptr(),
-                                       self.laid.data_ptr(),
-                                       torch.cuda.current_stream().cuda_stream),
-                  "mxfp8_expert_lay")
+            check(lib.mxfp8_expert_lay_scales(ctypes.byref(desc), w_scale.data_ptr(),
+                                              self.scales.data_ptr(),
+                                              torch.cuda.current_stream().cuda_stream),
+                  "mxfp8_expert_lay_scales")
         _synchronize(None, w.device)
-        self._own = (self.experts, self.n, k, int(self.gated), w_format, self.laid, workspace,
+        self._own = (self.experts, self.n, k, int(self.gated), w_format, w, self.scales, workspace,
                      self.flags)
 
     def run(self, x: torch.Tensor, x_scale: torch.Tensor, begin: torch.Tensor | None = None,

@@ -85,16 +85,16 @@ def desc(**kw):
     return _lib.ExpertDesc(**d)
 
 
-def product(lib, laid=A, x=A, x_scale=A, begin=A, out=A, out_scale=A, workspace=A, nbytes=None,
+def product(lib, w=A, laid=A, x=A, x_scale=A, begin=A, out=A, out_scale=A, workspace=A, nbytes=None,
             flags=A, **kw):
     nbytes = lib.mxfp8_expert_workspace_bytes() if nbytes is None else nbytes
-    return lib.mxfp8_expert_product(ctypes.byref(desc(**kw)), P(laid), P(x), P(x_scale),
+    return lib.mxfp8_expert_product(ctypes.byref(desc(**kw)), P(w), P(laid), P(x), P(x_scale),
                                     P(begin), P(out), P(out_scale), P(workspace), nbytes, P(flags),
                                     None)
 
 
 def test_product_refusals(lib):
-    for bad in (dict(laid=A + 16), dict(x=A + 16), dict(x_scale=A + 2), dict(begin=0),
+    for bad in (dict(w=A + 16), dict(laid=A + 8), dict(x=A + 16), dict(x_scale=A + 2), dict(begin=0),
                 dict(begin=A + 2), dict(out=A + 8), dict(out_format=1, out_scale=0),
                 dict(workspace=A + 8), dict(nbytes=1024), dict(flags=A + 2), dict(gated=2),
                 dict(w_format=0), dict(x_format=3), dict(out_format=3), dict(rows=-1)):
@@ -105,21 +105,18 @@ def test_product_refusals(lib):
                 dict(rows=2 ** 31 - 1, n=1 << 20)):
         assert product(lib, **bad) == mx.ERR_UNSUPPORTED, bad
     assert product(lib, rows=0, x=0, out=0) == mx.OK
-    assert lib.mxfp8_expert_product(None, *[None] * 7, 0, None, None) == mx.ERR_INVALID
+    assert lib.mxfp8_expert_product(None, *[None] * 8, 0, None, None) == mx.ERR_INVALID
 
 
-def test_laid_matrices(lib):
-    size = lambda **kw: lib.mxfp8_expert_bytes(ctypes.byref(desc(**kw)))  # noqa: E731
-    tile = 128 * 64 + 512  # codes and scales of 128 rows x 128 k
-    assert size() == 4 * 1 * 2 * tile
-    assert size(n=136) == 4 * 2 * 2 * tile
-    assert size(n=96, gated=1) == 4 * 2 * 2 * tile
-    assert size(w_format=1) == 4 * 1 * 2 * (tile + 128 * 64)
+def test_scales(lib):
+    size = lambda **kw: lib.mxfp8_expert_scales_bytes(ctypes.byref(desc(**kw)))  # noqa: E731
+    assert size() == 4 * 1 * 2 * 512
+    assert size(n=136) == 4 * 2 * 2 * 512
+    assert size(n=96, gated=1) == 4 * 2 * 2 * 512
     assert size(k=100) == size(n=4) == size(experts=-1) == size(w_format=0) == 0
     assert size(experts=512, n=1 << 20, k=1 << 20) == 0
-    lay = lambda *a: lib.mxfp8_expert_lay(ctypes.byref(desc()), *map(P, a), None)  # noqa: E731
-    assert lay(A + 8, A, A) == lay(A, A + 2, A) == lay(A, A, A + 16) == mx.ERR_INVALID
-    assert lay(0, A, A) == lay(A, 0, A) == lay(A, A, 0) == mx.ERR_INVALID
+    lay = lambda a, b: lib.mxfp8_expert_lay_scales(ctypes.byref(desc()), P(a), P(b), None)  # noqa: E731
+    assert lay(A + 2, A) == lay(A, A + 8) == lay(0, A) == lay(A, 0) == mx.ERR_INVALID
     assert lib.mxfp8_expert_workspace_bytes() < 1 << 26
 
 
