@@ -406,8 +406,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 
   if (warp == 0 || (S::kPair && warp == 1)) {
     // ---------------------------------------------------------------- copies
-    // (A copy costs its thread some 90 clocks, whatever its size.)
-    if (lane == 0) {
+    // (The warp stays converged and one elected lane copies, as in the products below.)
+    {
       const bool of_w = warp == 0, of_x = !S::kPair || !of_w;
       uint32_t stage = 0;  // of all this CTA's stages; the slot's use: stage / kStages
       bool ok = true;
@@ -426,13 +426,14 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             p.w_sf + static_cast<size_t>(s.expert * p.w_tiles + w_tile) * p.k_tiles * kChunk;
         for (int kt = s.kt0; kt < s.kt1; kt += S::kTiles, ++stage) {
           const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
-          if (!ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs)) {
+          ok = __all_sync(~0u, ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs));
+          if (!ok) {
             timed_out();
-            ok = false;
             break;
           }
           const uint32_t full = bar_full + 8 * slot;
           const uint32_t chunks = S::kPair ? 0 : min(S::kTiles, s.kt1 - kt) * kChunk;
+          if (!ptx::elect_one()) continue;
           if (rank == 0)
             ptx::mbar_arrive_expect_tx(
                 full, kSharers * ((of_w ? p.w_bytes : 0) + (of_x ? x_bytes : 0)) + chunks);
@@ -596,7 +597,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   } else if (warp >= 6) {
     // -------------------------------------------------------------- products
     // (Of a pair's twelve warps the eighth has nothing to do.)
-    if (lane == 0 && rank == 0 && warp < 6 + S::kPipes) {
+    // The warp stays converged and one elected lane issues: from a branch on the lane number
+    // NN.
+    if (rank == 0 && warp < 6 + S::kPipes) {
       const uint32_t pipe = warp - 6;
       uint32_t stage = pipe, before = 0, use = 0;  // use: segments so far
       bool ok = true;
@@ -613,21 +616,25 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         const uint32_t idesc = p.idesc | columns >> 3 << 17;
         const uint32_t x_tile = (columns / kSharers <= S::kSmall ? S::kSmall : S::kXRows) * 128;
         const uint32_t acc = tmem + (buffer * S::kPipes + pipe) * S::kAccSlot;
-        if (!ptx::mbar_wait(bar_acc_empty + 8 * buffer, ((use >> 1) & 1) ^ 1, kWaitNs)) {
+        ok = __all_sync(~0u,
+                        ptx::mbar_wait(bar_acc_empty + 8 * buffer, ((use >> 1) & 1) ^ 1, kWaitNs));
+        if (!ok) {
           timed_out();
           break;
         }
         ptx::tc_fence_after();
-        uint32_t accumulate = 0;
+        uint32_t more = 0u;  // onto the sums of the stages before
         for (; stage < before + count; stage += S::kPipes) {
           const uint32_t slot = stage % S::kStages;
-          if (!ptx::mbar_wait(bar_full + 8 * slot, (stage / S::kStages) & 1, kWaitNs)) {
+          ok = __all_sync(~0u,
+                          ptx::mbar_wait(bar_full + 8 * slot, (stage / S::kStages) & 1, kWaitNs));
+          if (!ok) {
             timed_out();
-            ok = false;
             break;
           }
           ptx::tc_fence_after();
           const int left = s.kt1 - s.kt0 - static_cast<int>(stage - before) * S::kTiles;
+          if (ptx::elect_one()) {
 #pragma unroll
           for (int t = 0; t < S::kTiles; ++t) {
             if (t >= left) break;
@@ -644,17 +651,22 @@ __global__ void __launch_bounds__(S::kThreads, 1)
               const uint64_t ad = ptx::desc_kmajor_sw128(a + 32 * kb);
               const uint64_t bd = ptx::desc_kmajor_sw128(b + 32 * kb);
               if constexpr (S::kPair)
-                ptx::mma_mxf8_pair(acc, ad, bd, idesc | kb << 4 | kb << 29, accumulate, sfa, sfb);
+                ptx::mma_mxf8_pair(acc, ad, bd, idesc | kb << 4 | kb << 29,
+                                   t + kb > 0 ? 1u : more, sfa, sfb);
               else
-                ptx::mma_mxf8(acc, ad, bd, idesc | kb << 4 | kb << 29, accumulate, sfa, sfb);
-              accumulate = 1;
+                ptx::mma_mxf8(acc, ad, bd, idesc | kb << 4 | kb << 29,
+                                   t + kb > 0 ? 1u : more, sfa, sfb);
             }
           }
-          commit(bar_empty + 8 * slot);
+            commit(bar_empty + 8 * slot);
+          }
+          __syncwarp();
+          more = 1u;
         }
         before += count;
         ++use;
-        if (ok) commit(bar_acc_full + 8 * buffer);
+        if (ok && ptx::elect_one()) commit(bar_acc_full + 8 * buffer);
+        __syncwarp();
       }
     }
   } else {
