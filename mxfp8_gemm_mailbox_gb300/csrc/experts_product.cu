@@ -74,10 +74,14 @@ struct Shape {
   static constexpr uint32_t kX = kStages * kTiles * kWTile;
   static constexpr uint32_t kSfa = kX + kStages * kTiles * kXTile;
   static constexpr uint32_t kSfb = kSfa + kStages * kTiles * kChunk;
-  static constexpr uint32_t kTurns = kPair ? kSfa : kSfb + kStages * kTiles * kChunk;
+  // A pair's scales come four k tiles at a time: W's chunks, then the rows' codes by k tile.
+  static constexpr int kQuads = 3;
+  static constexpr uint32_t kQuad = 4 * (kChunk + kRowsALane * 128);
+  static constexpr uint32_t kTurns =
+      kPair ? kSfa + kQuads * kQuad : kSfb + kStages * kTiles * kChunk;
   static constexpr uint32_t kTables = kTurns + 4 * kAtOnce * kTurnPitch * 4;
   static constexpr uint32_t kBars = kTables + 2 * 4 * ((MXFP8_MAX_EXPERTS + 8) / 4 * 4);
-  static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 4);
+  static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 4 + 2 * kQuads);
   static constexpr uint32_t kBytes = kMisc + 32 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
 };
@@ -347,6 +351,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t bar_full = sbase + S::kBars, bar_empty = bar_full + 8 * S::kStages;
   const uint32_t bar_acc_full = bar_empty + 8 * S::kStages, bar_acc_empty = bar_acc_full + 16;
+  const uint32_t bar_quad_full = bar_acc_empty + 16, bar_quad_empty = bar_quad_full + 8 * S::kQuads;
   uint32_t* const misc = reinterpret_cast<uint32_t*>(smem + S::kMisc);
   int* const rows = reinterpret_cast<int*>(smem + S::kTables);
   int* const tiles = rows + (MXFP8_MAX_EXPERTS + 8) / 4 * 4;
@@ -370,6 +375,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       // The copies, and the warps of the scales.
       ptx::mbar_init(bar_full + 8 * s, S::kPair ? 2 + 2 * 4 : 2);
       ptx::mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int q = 0; S::kPair && q < S::kQuads; ++q) {
+      ptx::mbar_init(bar_quad_full + 8 * q, 1);
+      ptx::mbar_init(bar_quad_empty + 8 * q, 4);
     }
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(bar_acc_full + 8 * b, S::kPipes);
@@ -458,76 +467,87 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         ptx::mbar_wait(bar_empty + 8 * (stage % S::kStages), ((stage / S::kStages) & 1) ^ 1,
                        kWaitNs);
     }
+  } else if (S::kPair && warp == 7) {
+    // ------------------------------------------------ a pair's scales, into shared memory
+    uint32_t quad = 0;  // of all this CTA's; the place's use: quad / kQuads
+    bool ok = true;
+    while (ok && share.next(s)) {
+      const int w_tile = min(s.w_tile * kSharers + static_cast<int>(rank), p.w_tiles - 1);
+      const uint8_t* const of_w =
+          p.w_sf + static_cast<size_t>(s.expert * p.w_tiles + w_tile) * p.k_tiles * kChunk;
+      // Rows of codes on 16-byte boundaries give four k tiles a load.
+      const bool wide = (p.k_tiles | s.kt0) % 4 == 0;
+      for (int kt = s.kt0; kt < s.kt1; kt += 4, ++quad) {
+        const uint32_t place = quad % S::kQuads, use = quad / S::kQuads;
+        const int count = min(4, s.kt1 - kt);
+        uint32_t v[S::kRowsALane][4];
+#pragma unroll
+        for (int i = 0; i < S::kRowsALane; ++i) {
+          const uint8_t* const from =
+              p.x_scale +
+              (static_cast<size_t>(s.row + min(lane + 32 * i, s.rows - 1)) * p.k_tiles + kt) * 4;
+          if (32 * i >= s.rows) {
+            v[i][0] = v[i][1] = v[i][2] = v[i][3] = 0u;
+          } else if (wide) {
+            const uint4 u = *reinterpret_cast<const uint4*>(from);
+            v[i][0] = u.x, v[i][1] = u.y, v[i][2] = u.z, v[i][3] = u.w;
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              v[i][j] = j < count ? *reinterpret_cast<const uint32_t*>(from + 4 * j) : 0u;
+          }
+        }
+        ok = __all_sync(~0u, ptx::mbar_wait(bar_quad_empty + 8 * place, (use & 1) ^ 1, kWaitNs));
+        if (!ok) {
+          timed_out();
+          break;
+        }
+        uint8_t* const to = smem + S::kSfa + place * S::kQuad;
+        uint32_t* const codes = reinterpret_cast<uint32_t*>(to + 4 * kChunk);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < S::kRowsALane; ++i)
+            codes[(j * S::kRowsALane + i) * 32 + lane] = v[i][j];
+        __syncwarp();
+        if (ptx::elect_one()) {
+          const uint32_t full = bar_quad_full + 8 * place;
+          ptx::mbar_arrive_expect_tx(full, count * kChunk);
+          ptx::bulk_load(ptx::smem_addr(to), of_w + static_cast<size_t>(kt) * kChunk,
+                         count * kChunk, full);
+        }
+      }
+    }
+    // (The last copies land before the scales' warps read them, and those before the end.)
   } else if (S::kPair && warp >= 8) {
-    // ------------------------- scales, from registers into tensor memory (a warp a quarter
-    // of its lanes, which all hold the same)
+    // ---------------- and on into tensor memory (a warp a quarter of its lanes, which all
+    // hold the same)
     if constexpr (S::kPair) {
-      constexpr int kAhead = 4;  // k tiles loaded while those before are stored
       const uint32_t lanes = static_cast<uint32_t>((warp - 8) * 32) << 16;
-      uint32_t stage = 0;
+      uint32_t stage = 0, quad = 0;
       bool ok = true;
       while (ok && share.next(s)) {
-        const int w_tile = min(s.w_tile * kSharers + static_cast<int>(rank), p.w_tiles - 1);
-        const uint8_t* const of_w =
-            p.w_sf + static_cast<size_t>(s.expert * p.w_tiles + w_tile) * p.k_tiles * kChunk +
-            lane * 16;
-        const uint8_t* of_x[S::kRowsALane];
-#pragma unroll
-        for (int i = 0; i < S::kRowsALane; ++i)
-          of_x[i] = p.x_scale + static_cast<size_t>(s.row + min(lane + 32 * i, s.rows - 1)) *
-                                    p.k_tiles * 4;
-        // Rows of scales on 16-byte boundaries give four k tiles a load.
-        const bool wide = (p.k_tiles | s.kt0) % 4 == 0;
-        uint4 a[kAhead], a_next[kAhead];
-        uint32_t b[S::kRowsALane][kAhead], b_next[S::kRowsALane][kAhead];
-        const auto load = [&](int kt) {
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j)
-            if (kt + j < s.kt1)
-              a_next[j] = *reinterpret_cast<const uint4*>(of_w + (kt + j) * static_cast<int>(kChunk));
-#pragma unroll
-          for (int i = 0; i < S::kRowsALane; ++i) {
-            if (32 * i >= s.rows || kt >= s.kt1) continue;
-            if (wide) {
-              const uint4 v = *reinterpret_cast<const uint4*>(of_x[i] + 4 * kt);
-              b_next[i][0] = v.x, b_next[i][1] = v.y, b_next[i][2] = v.z, b_next[i][3] = v.w;
-            } else {
-#pragma unroll
-              for (int j = 0; j < kAhead; ++j)
-                if (kt + j < s.kt1)
-                  b_next[i][j] = *reinterpret_cast<const uint32_t*>(of_x[i] + 4 * (kt + j));
-            }
-          }
-        };
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          a_next[j] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int i = 0; i < S::kRowsALane; ++i) b_next[i][j] = 0u;
-        }
-        load(s.kt0);
-        for (int kt = s.kt0; ok && kt < s.kt1; kt += kAhead) {
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            a[j] = a_next[j];
-#pragma unroll
-            for (int i = 0; i < S::kRowsALane; ++i) b[i][j] = b_next[i][j];
-          }
-          load(kt + kAhead);
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            if (kt + j >= s.kt1) break;
-            const uint32_t slot = stage % S::kStages, use = stage / S::kStages;
-            ok = __all_sync(~0u, ptx::mbar_wait(bar_empty + 8 * slot, (use & 1) ^ 1, kWaitNs));
-            if (!ok) {
-              timed_out();
-              break;
-            }
-            const uint32_t to = tmem + lanes + S::kAcc + slot * S::kSf;
-            const uint32_t ra[4] = {a[j].x, a[j].y, a[j].z, a[j].w};
+        for (int kt = s.kt0; ok && kt < s.kt1; kt += 4, ++quad) {
+          const uint32_t place = quad % S::kQuads, use = quad / S::kQuads;
+          const int count = min(4, s.kt1 - kt);
+          ok = __all_sync(~0u, ptx::mbar_wait(bar_quad_full + 8 * place, use & 1, kWaitNs));
+          const uint8_t* const from = smem + S::kSfa + place * S::kQuad;
+          const uint32_t* const codes = reinterpret_cast<const uint32_t*>(from + 4 * kChunk);
+          for (int j = 0; ok && j < count; ++j, ++stage) {
+            const uint4 a = *reinterpret_cast<const uint4*>(from + j * kChunk + lane * 16);
+            const uint32_t ra[4] = {a.x, a.y, a.z, a.w};
             uint32_t rb[8] = {};
 #pragma unroll
-            for (int i = 0; i < S::kRowsALane; ++i) rb[i] = b[i][j];
+            for (int i = 0; i < S::kRowsALane; ++i)
+              rb[i] = codes[(j * S::kRowsALane + i) * 32 + lane];
+            if (j == count - 1) {
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive(bar_quad_empty + 8 * place);
+            }
+            const uint32_t slot = stage % S::kStages;
+            ok = __all_sync(~0u, ptx::mbar_wait(bar_empty + 8 * slot,
+                                                (stage / S::kStages & 1) ^ 1, kWaitNs));
+            const uint32_t to = tmem + lanes + S::kAcc + slot * S::kSf;
             ptx::tc_fence_after();
             ptx::tmem_st_32x32b_x4(to, ra);
             ptx::tmem_st_32x32b_x8(to + 4, rb);
@@ -535,8 +555,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive(bar_full + 8 * slot);
-            ++stage;
           }
+          if (!ok) timed_out();
         }
       }
     }
@@ -596,10 +616,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
     }
   } else if (warp >= 6) {
     // -------------------------------------------------------------- products
-    // (Of a pair's twelve warps the eighth has nothing to do.)
     // The warp stays converged and one elected lane issues: from a branch on the lane number
     // NN.
-    if (rank == 0 && warp < 6 + S::kPipes) {
+    if (rank == 0) {
       const uint32_t pipe = warp - 6;
       uint32_t stage = pipe, before = 0, use = 0;  // use: segments so far
       bool ok = true;
