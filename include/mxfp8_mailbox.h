@@ -647,7 +647,7 @@ size_t mxfp8_expert_scales_bytes(const mxfp8_expert_desc* desc);
 mxfp8_status mxfp8_expert_lay_scales(const mxfp8_expert_desc* desc, const void* w_scale, void* laid,
                                      void* stream);
 
-/* Workspace bytes of the product, whatever the call: 37 MB. */
+/* Workspace bytes of the product, whatever the call: 5 MB. */
 size_t mxfp8_expert_workspace_bytes(void);
 #define MXFP8_EXPERT_WORKSPACE_ZEROS 1024
 

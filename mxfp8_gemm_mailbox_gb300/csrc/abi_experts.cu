@@ -325,7 +325,7 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
                                        MXFP8_EXPERT_WORKSPACE_ZEROS);
   p.flags = flags;
-  e = launch_expert_product(maps, p, tile.kind, ctas, static_cast<cudaStream_t>(stream));
+  e = launch_expert_product(maps, p, tile, ctas, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the experts' product");
   return MXFP8_OK;
 }

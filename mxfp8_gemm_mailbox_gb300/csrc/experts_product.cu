@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 #include "mx_format.cuh"
@@ -42,15 +43,13 @@ constexpr uint32_t kChunk = 512;  // scales of 128 rows, 4 blocks each
 constexpr int kTurnPitch = 36;    // floats of an expert row in the epilogue's turn: a quarter-warp's
                                   // 16-byte reads meet no bank twice
 
-template <bool kPair_, int kCols_, int kTiles_, int kStages_, int kPipes_, int kSmall_, int kMinRun_,
-          int kAtOnce_>
+template <bool kPair_, int kCols_, int kTiles_, int kStages_, int kPipes_, int kSmall_, int kAtOnce_>
 struct Shape {
   static constexpr bool kPair = kPair_;     // two CTAs a tile
   static constexpr int kCols = kCols_;      // expert rows of a tile
   static constexpr int kTiles = kTiles_;    // k tiles of a stage
   static constexpr int kStages = kStages_;  // of the ring
   static constexpr int kPipes = kPipes_;    // issuing warps
-  static constexpr int kMinRun = kMinRun_;  // stages of a run at least
   static constexpr int kAtOnce = kAtOnce_;  // columns that an epilogue's warp reads together
   static constexpr int kChunks = (kCols + 127) / 128;  // scale chunks of the rows
   static constexpr int kRowsALane = (kCols + 31) / 32;
@@ -86,81 +85,70 @@ struct Shape {
   static_assert(kBytes <= 232448, "shared memory");
 };
 // Few rows an expert: bound by the stream of W.  Many: by the products.
-using Narrow = Shape<false, 32, 2, 5, 5, 8, 2, 8>;
-using Middle = Shape<false, 64, 2, 4, 2, 32, 2, 16>;
-using Wide = Shape<true, 224, 1, 5, 1, 56, 8, 32>;
+using Narrow = Shape<false, 32, 2, 5, 5, 8, 8>;
+using Middle = Shape<false, 64, 2, 4, 2, 32, 16>;
+using Wide = Shape<true, 224, 1, 5, 1, 56, 32>;
+constexpr int kMinPiece = 16;  // k tiles of a piece of a cut tile
 
 __device__ __forceinline__ void epilogue_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ void pair_barrier(int pair) {
   asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
 }
 
-// A run of k tiles of one tile.
+// The k tiles of one tile, or a piece of them.
 struct Segment {
   int expert, row, rows, w_tile;  // rows: of the tile
   int kt0, kt1;  // whole stages, but for the last of a tile
-  int left;  // which of the tiles that are cut into runs, -1: a whole round's
+  int cut;       // which of the tiles that are cut
 };
 
-// The segments of a CTA, in order; every role walks the same list.  (Divisions of 32
-// bits: a run's end is below 160 x 160 x 8192.)
-template <class S>
+// The segments of a CTA, in order; every role walks the same list.  Tiles go round by
+// round, one a CTA; with kCuts those of a round that fills half of the CTAs or less are
+// cut along k into as many equal pieces as there are CTAs a tile.
+template <class S, bool kCuts>
 struct Share {
   const int* rows;   // [experts + 1] each expert's first row
   const int* tiles;  // [experts + 1] ... first tile
   int experts, k_tiles, stages;  // stages of a tile
-  int grid, cta, rounds, round;  // in pairs where they share a tile
-  uint32_t units, runs;          // stages of the cut tiles
-  int at, end;                   // this CTA's run
+  int grid, cta, round;          // in pairs where they share a tile
+  int all;                       // tiles
+  int rounds, pieces, piece, of; // kCuts: whole rounds; a cut tile's pieces, this CTA's piece and tile
 
-  __device__ __forceinline__ int run_begin(int c) const {
-    return static_cast<int>(static_cast<uint32_t>(c) * units / runs);
-  }
-  __device__ __forceinline__ int owner(int unit) const {
-    return static_cast<int>((static_cast<uint32_t>(unit + 1) * runs - 1) / units);
-  }
   __device__ __forceinline__ Share(const int* r, const int* t, int e, int kt)
       : rows(r), tiles(t), experts(e), k_tiles(kt) {
     constexpr int kSharers = S::kPair ? 2 : 1;
     stages = (kt + S::kTiles - 1) / S::kTiles;
     grid = gridDim.x / kSharers;
     cta = blockIdx.x / kSharers;
-    const uint32_t all = static_cast<uint32_t>(tiles[e]);
-    rounds = static_cast<int>(all / static_cast<uint32_t>(grid));
+    all = tiles[e];
     round = 0;
-    const int left = static_cast<int>(all) - rounds * grid;
-    units = static_cast<uint32_t>(left * stages);
-    // A tile's pieces are runs of whole tiles' parts where two or more CTAs fit a
-    // tile, else runs of equal length where they are shorter by enough to pay for
-    // the joining, else whole tiles.
-    if (2 * left <= grid)
-      runs = left * max(1, min(grid / max(left, 1), stages / S::kMinRun));
-    else
-      runs = stages - static_cast<int>(units / grid) >= 2 * S::kMinRun ? grid : left;
-    runs = max(runs, 1u);
-    at = end = 0;
-    if (units > 0 && cta < static_cast<int>(runs)) {
-      at = run_begin(cta);
-      end = run_begin(cta + 1);
+    if constexpr (kCuts) {
+      rounds = static_cast<int>(static_cast<uint32_t>(all) / static_cast<uint32_t>(grid));
+      const int left = all - rounds * grid;
+      pieces = left == 0 ? 1
+                         : max(1, min(static_cast<int>(static_cast<uint32_t>(grid) /
+                                                       static_cast<uint32_t>(left)),
+                                      stages * S::kTiles / kMinPiece));
+      of = static_cast<int>(static_cast<uint32_t>(cta) / static_cast<uint32_t>(pieces));
+      piece = cta - of * pieces;
     }
   }
   __device__ __forceinline__ bool next(Segment& s) {
-    int tile;
-    if (round < rounds) {
-      tile = cta + grid * round++;
-      s.kt0 = 0;
-      s.kt1 = k_tiles;
-      s.left = -1;
-    } else if (at < end) {
-      s.left = static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(stages));
-      tile = rounds * grid + s.left;
-      const int from = at - s.left * stages, to = min(stages, from + end - at);
-      s.kt0 = from * S::kTiles;
-      s.kt1 = min(k_tiles, to * S::kTiles);
-      at += to - from;
-    } else {
-      return false;
+    int tile = cta + grid * round;
+    s.kt0 = 0;
+    s.kt1 = k_tiles;
+    if constexpr (kCuts) {
+      s.cut = of;
+      if (round == rounds) {
+        tile = rounds * grid + of;
+        s.kt0 = piece * stages / pieces * S::kTiles;
+        s.kt1 = min(k_tiles, (piece + 1) * stages / pieces * S::kTiles);
+      } else if (round > rounds) {
+        return false;
+      }
     }
+    ++round;
+    if (tile >= all) return false;
     // The last expert whose first tile is not past this one: eight at a time, whose loads
     // do not wait for one another.
     int lo = 0;
@@ -337,7 +325,7 @@ __device__ __forceinline__ void store_outputs(const ExpertParams& p, const float
   if (live && n % 32 == 0) p.out_scale[first / 32] = static_cast<uint8_t>(code);
 }
 
-template <class S, bool kGated>
+template <class S, bool kGated, bool kCuts>
 __global__ void __launch_bounds__(S::kThreads, 1)
     expert_kernel(const __grid_constant__ CUtensorMap tmap_w,
                   const __grid_constant__ CUtensorMap tmap_x,
@@ -410,7 +398,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
   const auto timed_out = [&] {
     if (p.flags) atomicOr(p.flags, MXFP8_FLAG_GEMM_TIMEOUT);
   };
-  Share<S> share(rows, tiles, p.experts, p.k_tiles);
+  Share<S, kCuts> share(rows, tiles, p.experts, p.k_tiles);
   Segment s;
 
   if (warp == 0 || (S::kPair && warp == 1)) {
@@ -750,15 +738,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       }
       __syncwarp();
       ptx::tc_fence_after();
-      const bool whole = s.kt0 == 0 && s.kt1 == p.k_tiles;
-      const int lo = whole ? 0 : share.owner(s.left * share.stages);
-      const int hi = whole ? 0 : share.owner((s.left + 1) * share.stages - 1);
-      // A CTA's run has two cut tiles at most: its first and its last.
+      const bool whole = !kCuts || (s.kt0 == 0 && s.kt1 == p.k_tiles);
+      // A piece's partials: a CTA has one cut tile at most.
       const auto place = [&](int cta) {
-        const int second = share.run_begin(cta) < s.left * share.stages ? 1 : 0;
-        return p.partial +
-               (static_cast<size_t>(2 * cta + second) * kSharers + rank) * kTileRows * S::kCols +
-               quarter * 32 + lane;
+        return p.partial + static_cast<size_t>(cta) * kTileRows * S::kCols + quarter * 32 + lane;
       };
       for (int c = 0; c < s.rows; c += kC) {
         float v[kC];
@@ -795,38 +778,42 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive(bar_acc_empty + 8 * buffer);
-      if (!whole) {
-        // The barrier hands the warps' partials to one thread, whose arrival releases
-        // them; the last one's acquires the others' for its warps the same way.
-        epilogue_barrier();
-        if (tid == 64) {
-          int32_t* const ticket = p.tickets + s.left * kSharers + rank;
-          misc[1] = ptx::atom_add_acq_rel(ticket, 1u) == static_cast<uint32_t>(hi - lo);
-          if (misc[1]) *ticket = 0;  // for the next call
-        }
-        epilogue_barrier();
-        if (misc[1]) {
-          for (int c = 0; c < s.rows; c += kC) {
-            float v[kC];
+      if constexpr (kCuts) {
+        if (!whole) {
+          // The barrier hands the warps' partials to one thread, whose arrival releases
+          // them; the last one's acquires the others' for its warps the same way.
+          epilogue_barrier();
+          if (tid == 64) {
+            int32_t* const ticket = p.tickets + s.cut;
+            misc[1] =
+                ptx::atom_add_acq_rel(ticket, 1u) == static_cast<uint32_t>(share.pieces - 1);
+            if (misc[1]) *ticket = 0;  // for the next call
+          }
+          epilogue_barrier();
+          if (misc[1]) {
+            for (int c = 0; c < s.rows; c += kC) {
+              float v[kC];
 #pragma unroll
-            for (int j = 0; j < kC; ++j) v[j] = 0.0f;
-            // Several pieces' loads at a time, added in the order of k.
-            constexpr int kPieces = 64 / kC;
-            for (int cta = lo; cta <= hi; cta += kPieces) {
-              float x[kPieces][kC];
+              for (int j = 0; j < kC; ++j) v[j] = 0.0f;
+              // Several pieces' loads at a time, added in the order of k.
+              constexpr int kPieces = 64 / kC;
+              const int lo = s.cut * share.pieces, hi = lo + share.pieces - 1;
+              for (int cta = lo; cta <= hi; cta += kPieces) {
+                float x[kPieces][kC];
 #pragma unroll
-              for (int i = 0; i < kPieces; ++i) {
-                const float* const from = place(min(cta + i, hi));
+                for (int i = 0; i < kPieces; ++i) {
+                  const float* const from = place(min(cta + i, hi));
 #pragma unroll
-                for (int j = 0; j < kC; ++j)
-                  x[i][j] = cta + i <= hi ? __ldcg(from + (c + j) * kTileRows) : 0.0f;
+                  for (int j = 0; j < kC; ++j)
+                    x[i][j] = cta + i <= hi ? __ldcg(from + (c + j) * kTileRows) : 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+#pragma unroll
+                  for (int j = 0; j < kC; ++j) v[j] += x[i][j];
               }
-#pragma unroll
-              for (int i = 0; i < kPieces; ++i)
-#pragma unroll
-                for (int j = 0; j < kC; ++j) v[j] += x[i][j];
+              finish(s, c, v);
             }
-            finish(s, c, v);
           }
         }
       }
@@ -868,10 +855,10 @@ __global__ void __launch_bounds__(128) lay_scales_kernel(const uint8_t* scale, u
   *reinterpret_cast<uint32_t*>(chunk + a % 32 * 16 + a / 32 * 4) = codes;
 }
 
-template <class S, bool kGated>
+template <class S, bool kGated, bool kCuts>
 cudaError_t launch_as(const ExpertMaps& maps, const ExpertParams& p, int ctas,
                       cudaStream_t stream) {
-  const auto kernel = expert_kernel<S, kGated>;
+  const auto kernel = expert_kernel<S, kGated, kCuts>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(S::kBytes));
   if (e != cudaSuccess) return e;
@@ -894,7 +881,7 @@ cudaError_t launch_as(const ExpertMaps& maps, const ExpertParams& p, int ctas,
 }  // namespace
 
 size_t expert_partial_bytes(int ctas) {
-  return static_cast<size_t>(ctas) * 2 * kTileRows * Wide::kCols * 4;
+  return static_cast<size_t>(ctas) * kTileRows * Middle::kCols * 4;
 }
 
 // By what the host knows, the mean of an expert's rows.  A rule found on some 100 shapes of
@@ -909,37 +896,41 @@ size_t expert_partial_bytes(int ctas) {
 //   22 experts x 697 rows, 112 x 128            10.3  8.3 11.3   (half of the pairs' second tile)
 //   64 experts x 512 rows, gated 2048 x 4096    1147  718  496
 ExpertTile expert_tile(int rows, int experts, int w_tiles, int k_tiles, int ctas) {
-  const auto of = [](auto s, ExpertTile::Kind kind) {
-    using S = decltype(s);
-    static_assert(S::kCols <= Wide::kCols, "partials");
-    return ExpertTile{kind, S::kTiles, S::kXRows, S::kSmall};
-  };
   const int active = std::max(1, std::min(rows, experts));
   const int each = (rows + experts - 1) / experts;
   const auto tiles = [&](int cols) {
     return static_cast<int64_t>(active) * ((each + cols - 1) / cols) * w_tiles;
   };
-  if (rows <= 12 * static_cast<int64_t>(experts) || (tiles(Narrow::kCols) <= ctas && k_tiles <= 32))
+  // Whether cutting the few tiles there are saves more than the joining costs.
+  const auto cuts = [&](int cols) {
+    const int64_t pieces = std::min<int64_t>(ctas / tiles(cols), k_tiles / kMinPiece);
+    return pieces > 1 && k_tiles - k_tiles / pieces >= (cols > 32 ? 40 : 24);
+  };
+  const auto of = [&](auto s, ExpertTile::Kind kind) {
+    using S = decltype(s);
+    return ExpertTile{kind, !S::kPair && cuts(S::kCols), S::kTiles, S::kXRows, S::kSmall};
+  };
+  const auto mean = [&](int64_t r) { return rows > r * experts; };
+  if (!mean(8) || (mean(100) && tiles(Narrow::kCols) <= ctas))
     return of(Narrow{}, ExpertTile::kNarrow);
-  const bool paired = w_tiles % 2 == 0 || w_tiles >= 8;
-  if (rows > 64 * static_cast<int64_t>(experts) && 2 * tiles(Middle::kCols) > 3 * ctas && paired)
+  // (An odd tile of W leaves half a pair without one.)
+  if (mean(64) &&
+      2 * tiles(Middle::kCols) * w_tiles > 3 * ctas * static_cast<int64_t>(w_tiles + w_tiles % 2))
     return of(Wide{}, ExpertTile::kWide);
   return of(Middle{}, ExpertTile::kMiddle);
 }
 
 cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p,
-                                  ExpertTile::Kind kind, int ctas, cudaStream_t stream) {
-  switch (kind) {
-    case ExpertTile::kNarrow:
-      return p.gated ? launch_as<Narrow, true>(maps, p, ctas, stream)
-                     : launch_as<Narrow, false>(maps, p, ctas, stream);
-    case ExpertTile::kMiddle:
-      return p.gated ? launch_as<Middle, true>(maps, p, ctas, stream)
-                     : launch_as<Middle, false>(maps, p, ctas, stream);
-    default:
-      return p.gated ? launch_as<Wide, true>(maps, p, ctas, stream)
-                     : launch_as<Wide, false>(maps, p, ctas, stream);
-  }
+                                  const ExpertTile& tile, int ctas, cudaStream_t stream) {
+  const auto as = [&](auto s, auto cuts) {
+    using S = decltype(s);
+    return p.gated ? launch_as<S, true, decltype(cuts)::value>(maps, p, ctas, stream)
+                   : launch_as<S, false, decltype(cuts)::value>(maps, p, ctas, stream);
+  };
+  if (tile.kind == ExpertTile::kWide) return as(Wide{}, std::false_type{});
+  if (tile.kind == ExpertTile::kMiddle)
+    return tile.cuts ? as(Middle{}, std::true_type{}) : as(Middle{}, std::false_type{});
+  return tile.cuts ? as(Narrow{}, std::true_type{}) : as(Narrow{}, std::false_type{});
 }
 
 cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,

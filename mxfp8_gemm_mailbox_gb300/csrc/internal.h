@@ -251,6 +251,7 @@ static_assert(kMaxExpertCtas * 4 <= MXFP8_EXPERT_WORKSPACE_ZEROS, "tickets");
 size_t expert_partial_bytes(int ctas);
 struct ExpertTile {
   enum Kind { kNarrow, kMiddle, kWide } kind;
+  bool cuts;            // along k, the tiles of a round that few CTAs would have
   int k_tiles;          // of a stage
   int x_rows, x_small;  // rows of the two copies of x
 };
@@ -260,7 +261,7 @@ struct ExpertMaps {
   CUtensorMap x_small;  // of fewer rows
 };
 cudaError_t launch_expert_product(const ExpertMaps& maps, const ExpertParams& p,
-                                  ExpertTile::Kind kind, int ctas, cudaStream_t stream);
+                                  const ExpertTile& tile, int ctas, cudaStream_t stream);
 cudaError_t launch_lay_scales(const uint8_t* scale, uint8_t* laid, int experts, int n, bool gated,
                               int w_tiles, int k_tiles, cudaStream_t stream);
 

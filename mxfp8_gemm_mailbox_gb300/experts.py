@@ -78,7 +78,7 @@ class ExpertProduct:
     silu(gate) x up, N / 2 wide.
 
     The codes stay borrowed; the scales are copied, once, into the products' order, and
-    the constructor waits for that.  The workspace (37 MB) and the flags word live here;
+    the constructor waits for that.  The workspace (5 MB) and the flags word live here;
     ``workspace``: another product's, to be shared.  Calls that share one are ordered on
     one stream, made by one host thread at a time, and the object outlives what they have
     queued on another stream than the one it was made on."""
