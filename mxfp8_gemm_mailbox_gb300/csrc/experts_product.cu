@@ -7,23 +7,43 @@
 // the result is silu(gate) up.
 //
 // W is the MMA's A operand (a tile of 128 of its rows), the expert's rows its B
-// operand (a tile of up to kCols), the products kind::mxf8f6f4 with one scale
-// a block of 32: elements of 4 bits lie in shared memory as 16 in 16 bytes, the
-// latter 8 unused, which is how the tensor copies lay them.  A tile of a gated
-// product takes 32 gate rows, their 32 up rows, 32 gate rows, 32 up rows, so a
-// block of 32 outputs is one warp's lanes and its partner's.
+// operand, the products kind::mxf8f6f4 with one scale a block of 32: elements of
+// 4 bits lie in shared memory as 16 in 16 bytes, the latter 8 unused, which is
+// how the tensor copies lay them.  A tile of a gated product takes 32 gate rows,
+// their 32 up rows, 32 gate rows, 32 up rows, so a block of 32 outputs is one
+// warp's lanes and its partner's.
+//
+// Three kernels by the rows an expert has (expert_tile, below): tiles of up to 32
+// rows, bound by the stream of W (two k tiles a stage, five issuers that add up
+// at the end: one issued too slowly for the memory, 57.4 us for 56.2 on the step
+// below); of up to 64; and pairs of CTAs on tiles of 256 rows of W x 224, bound by
+// the products.  A pair's product reads 4 KB of W and 7 KB of x in each SM for 112
+// clocks' work while the copies write 7.5 KB: shared memory's rate, 128 bytes a
+// clock, is what there is (a stage of 4 products took 553 clocks in place of 448),
+// and over milliseconds the power limit (1.6 to 1.8 GHz).
 //
 // Work.  begin is read on the device, so the grid is one CTA an SM, and each
 // finds its share: tiles are numbered expert by expert, tiles of rows inside
-// those of W (neighbouring CTAs read the same W at the same time); as many
-// whole rounds as there are go one tile a CTA, and what is left is cut along k
-// into equal runs.  A tile that several CTAs share leaves FP32 partials; the
-// last to arrive adds them in the order of k, so results have the same bits
-// every time.
+// those of W (neighbouring CTAs read the same W at the same time), and go round
+// by round.  Where the call's few tiles are long, they are cut along k: the pieces
+// leave FP32 partials, and the last to arrive adds them in the order of k, so
+// results have the same bits every time.  The tickets that tell it are zero between
+// calls.
 //
-// Warp roles: warp 0 copies (kLanes lanes take stages in turn), warp 1 lays the
-// rows' scales, warps 2-5 read the sums back, warps 6.. issue the products
-// (kPipes, each with an accumulator of its own, added at the end).
+// Warp roles: warp 0 copies W, and x (a pair's x: warp 1); warp 1 lays the rows'
+// scales for the tensor-memory copies; warps 2-5 read the sums back; warps 6..
+// issue the products.  A scale copy in the products' queue costs them 60 clocks,
+// three a stage of a pair: there warp 7 fetches the scales and warps 8-11 store
+// them into tensor memory from registers (375 us -> 331 at the prompt below).  One
+// elected lane of a converged warp copies and issues: from a branch on the lane
+// number a product took a third longer.
+//
+// Measured (graphs of calls, inputs alternating): a token's 8 experts, N 4096, K
+// 2048, MXFP4: 10.6 us, of which 5.3 are the matrices at the memory's rate and some
+// 5 the launch's wait, begin's latency, the deal and the first copies; 64 rows on 36
+// experts, gated, N 2048, K 4096: 51.8 us, 6.2 TB/s; 4096 rows at N 7168, K 16384,
+// MXFP8: 305 us, 3.15 PFLOP/s (both in 4 bits 246 us); 32768 rows on 64 experts,
+// gated, N 2048, K 4096: 386 us, 2.85 PFLOP/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -884,17 +904,19 @@ size_t expert_partial_bytes(int ctas) {
   return static_cast<size_t>(ctas) * kTileRows * Middle::kCols * 4;
 }
 
-// By what the host knows, the mean of an expert's rows.  A rule found on some 100 shapes of
-// 1 to 16384 rows, 1 to 64 experts, N and K up to 7168 x 8192, each timed as all three; its
-// choice takes 2 % longer than the best on average, 13 % at a few.  Narrow, middle, wide in us:
-//   24 experts x 14 rows, 1000 x 640             7.6  7.5 10.5
-//   8 experts x 24 rows, 2048 x 2048            12.8  8.5 12.1   (more than 32 rows are two tiles)
-//   one expert x 256 rows, 2048 x 2048           7.8 11.6 14.5   (one round, nothing to join)
-//   one expert x 256 rows, 7168 x 8192          35.8 29.4 35.6
-//   64 experts x 64 rows, 1024 x 2048           35.7 24.8 35.6
-//   7 experts x 143 rows, gated 736 x 896       12.8 15.2 12.7
-//   22 experts x 697 rows, 112 x 128            10.3  8.3 11.3   (half of the pairs' second tile)
-//   64 experts x 512 rows, gated 2048 x 4096    1147  718  496
+// By what the host knows, the mean of an expert's rows.  A rule found on 161 shapes of 1 to
+// 16384 rows, 1 to 64 experts, N and K up to 7168 x 8192, each timed as all three; its choice
+// takes 1 % longer than the best on average, 17 % at the most.  Narrow, middle, wide in us:
+//   8 experts x 8 rows, 2048 x 2048               6.4  6.7  8.9
+//   8 experts x 24 rows, 2048 x 2048              8.6  7.2  9.1   (past 32 rows two tiles)
+//   64 experts x 64 rows, 1024 x 2048            27.9 22.0 25.6
+//   one expert x 64 rows, 2048 x 2048             5.6  6.0  8.2   (few tiles)
+//   one expert x 256 rows, 7168 x 8192           30.8 27.2 23.2
+//   22 experts x 697 rows, 112 x 128              8.0  6.5  9.5   (half of the pairs' CTAs idle)
+//   9 experts x 860 rows, gated 1728 x 2688     136.2 89.1 59.0
+// and cutting (by 24 k tiles saved, 40 where there are more partials), one matrix,
+// whole and cut, at 1 row and K = 4096, 8192, 16384: N = 128 6.1 6.6, 9.0 6.8, 14.9 7.0; N =
+// 4096 6.6 7.5, 11.3 8.6, 21.0 12.9; at 64 rows N = 2048 7.9 10.3, 11.6 11.4, 24.4 16.2.
 ExpertTile expert_tile(int rows, int experts, int w_tiles, int k_tiles, int ctas) {
   const int active = std::max(1, std::min(rows, experts));
   const int each = (rows + experts - 1) / experts;
@@ -911,11 +933,11 @@ ExpertTile expert_tile(int rows, int experts, int w_tiles, int k_tiles, int ctas
     return ExpertTile{kind, !S::kPair && cuts(S::kCols), S::kTiles, S::kXRows, S::kSmall};
   };
   const auto mean = [&](int64_t r) { return rows > r * experts; };
-  if (!mean(8) || (mean(100) && tiles(Narrow::kCols) <= ctas))
+  if (!mean(16) || (2 * tiles(Narrow::kCols) <= ctas && k_tiles <= 32))
     return of(Narrow{}, ExpertTile::kNarrow);
   // (An odd tile of W leaves half a pair without one.)
   if (mean(64) &&
-      2 * tiles(Middle::kCols) * w_tiles > 3 * ctas * static_cast<int64_t>(w_tiles + w_tiles % 2))
+      tiles(Middle::kCols) * w_tiles > 2 * ctas * static_cast<int64_t>(w_tiles + w_tiles % 2))
     return of(Wide{}, ExpertTile::kWide);
   return of(Middle{}, ExpertTile::kMiddle);
 }

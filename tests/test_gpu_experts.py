@@ -329,6 +329,10 @@ def test_product_long_sums(cuda):
     Case([3, 9], 512, 16384, 8, 8).check()
     Case([20], 160 * 128, 1024).check()
     Case([600], 1280, 7168).check()
+    Case([40], 256, 8192).check()
+    Case([40], 264, 8192 + 128, 8, 4).check()
+    # More tiles than the means suggest: all rows on one expert.
+    Case([0] * 30 + [64] + [0] * 33, 64, 8192).check()
 
 
 @pytest.mark.parametrize("bits,x_bits", [(4, 8), (8, 8), (4, 4)])
@@ -347,6 +351,7 @@ def test_gated_widths(cuda, n, rows):
 def test_gated_cut_tiles(cuda):
     Case([4], 64, 8192, gated=True).check("mxfp8")
     Case([300], 192, 8192, gated=True).check("mxfp4")
+    Case([33, 50], 96, 8192, gated=True).check("mxfp8")
 
 
 @pytest.mark.parametrize("format", ["mxfp8", "mxfp4"])
@@ -379,10 +384,13 @@ def test_rows_of_no_expert_are_left(cuda):
 
 
 def test_same_bits_every_time(cuda):
-    for c in (Case([3, 9], 512, 16384), Case([260, 77], 320, 4096, gated=True)):
+    for c in (Case([3, 9], 512, 16384), Case([50], 256, 16384, gated=True),
+              Case([260, 77], 320, 4096, gated=True)):
         first = c.product.run(c.x, c.x_scale, c.begin)
         for _ in range(5):
             assert torch.equal(c.product.run(c.x, c.x_scale, c.begin), first)
+        zeros = c.product.workspace[:1024]  # as a call finds them, so it leaves them
+        assert not zeros.any()
 
 
 def test_non_finite_operands_stay_in_their_rows_and_outputs(cuda):
