@@ -13,9 +13,10 @@
 // moves its keys up.  An expert appears once at most among a token's, so a block of tokens is, for
 // each expert, a bit mask: its population is the block's count, and that of the bits
 // below a token the token's place.  Nothing depends on the order of atomics.  One block
-// does all of up to 128 tokens; for more a second kernel adds up the blocks' counts, and
-// a third gives the places.  (Each block adding up those before it: all read the same
-// lines at the same time, 20 us at 16k tokens in place of 2.)
+// does all of up to 128 tokens; for more a second kernel gives the places, each block
+// adding up the counts of those before it; past 32 blocks a kernel between the two adds
+// them (all blocks reading the same lines at the same time took 20 us at 16k tokens, in
+// place of 2).
 //
 // Combine.  out[t] = add[t] + sum_j weight[t][j] y[slot[t][j]], in FP32, j
 // ascending, rounded once; a thread has 8 numbers of a row, and its loads are
@@ -200,7 +201,7 @@ __device__ __forceinline__ int before_in_block(int v, int* sums) {
 }
 
 // kStep 0: all of a call with one block.  1: the choice, and each block's counts.  2:
-// the places, from the counts of the blocks before.
+// the places, from the counts of all blocks; 3: from the sums of those before.
 template <int kStep, int kTokens, int kType, int kEach>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kMaskWords = kTokens / 32;
@@ -215,8 +216,8 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
   for (int i = tid; i < kMaskWords * MXFP8_MAX_EXPERTS; i += kThreads) (&mask[0][0])[i] = 0u;
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  int count = 0, earlier = 0;  // thread e: expert e's rows (kStep 2: of all blocks, of those before)
-  if constexpr (kStep != 2) {
+  int count = 0, earlier = 0;  // thread e: expert e's rows (places: of all blocks, of those before)
+  if constexpr (kStep < 2) {
     // A token's logits are on their way while the one before is chosen from.
     using Key = typename KeyOf<kType>::T;
     Key next[kEach];
@@ -231,8 +232,18 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     }
   } else {
     if (tid < p.experts) {
-      count = p.counts[static_cast<size_t>(gridDim.x) * p.experts + tid];
-      earlier = p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid];
+      if constexpr (kStep == 2) {
+        const int blocks = gridDim.x, mine = blockIdx.x;
+#pragma unroll 8
+        for (int b = 0; b < blocks; ++b) {
+          const int c = p.counts[b * p.experts + tid];
+          count += c;
+          if (b < mine) earlier += c;
+        }
+      } else {
+        count = p.counts[static_cast<size_t>(gridDim.x) * p.experts + tid];
+        earlier = p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid];
+      }
     }
     __syncthreads();
     for (int i = tid; i < entries; i += kThreads) {
@@ -241,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     }
   }
   __syncthreads();
-  if constexpr (kStep != 2) {
+  if constexpr (kStep < 2) {
     if (tid < p.experts)
 #pragma unroll
       for (int w = 0; w < kMaskWords; ++w) count += __popc(mask[w][tid]);
@@ -383,10 +394,12 @@ cudaError_t route_blocks(const RouteParams& p, cudaStream_t stream) {
   const uint32_t blocks = static_cast<uint32_t>((p.tokens + kTokens - 1) / kTokens);
   cudaError_t e = launch(route_kernel<1, kTokens, kType, kEach>, blocks, kThreads, stream, p);
   if (e != cudaSuccess) return e;
+  if (blocks <= 32)
+    return launch(route_kernel<2, kTokens, MXFP8_FP32, 2>, blocks, kThreads, stream, p);
   e = launch(route_sum_kernel, static_cast<uint32_t>((p.experts + 31) / 32), 1024, stream, p.counts,
              p.experts, static_cast<int>(blocks));
   if (e != cudaSuccess) return e;
-  return launch(route_kernel<2, kTokens, MXFP8_FP32, 1>, blocks, kThreads, stream, p);
+  return launch(route_kernel<3, kTokens, MXFP8_FP32, 2>, blocks, kThreads, stream, p);
 }
 template <int kType, int kEach>
 cudaError_t route_as(const RouteParams& p, cudaStream_t stream) {

@@ -233,7 +233,7 @@ def test_route_ties_infinities_and_nan(cuda):
     check_route(z.to(torch.bfloat16), 3, normalize=False)
 
 
-@pytest.mark.parametrize("tokens", [5000, 32769, 40000])
+@pytest.mark.parametrize("tokens", [2048, 2049, 5000, 32769, 40000])
 def test_route_many_tokens(cuda, tokens):
     """Against the definition in sorts: the lowest index first among equal logits."""
     experts, k = 37, 3
