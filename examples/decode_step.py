@@ -3,9 +3,10 @@
 Latent attention over a paged cache (requests with a few drafted tokens each, in
 a tree), the absorbed products around it, and the publishing MXFP8 projection
 with a low-rank adapter per request, captured in one CUDA graph and replayed.
+With --experts a layer of routed experts in MXFP4 follows on the projection's rows.
 Synthetic weights and activations.
 
-    python examples/decode_step.py [--context 4096] [--heads 128] [--steps 50]
+    python examples/decode_step.py [--context 4096] [--heads 128] [--experts 64] [--steps 50]
 """
 import argparse
 import sys
@@ -29,6 +30,12 @@ def mxfp8(rows, k):
     return x, torch.randint(123, 130, (rows, k // 32), dtype=torch.uint8, device="cuda")
 
 
+def mxfp4(experts, rows, k):
+    """Random MXFP4 matrices of outputs of the order of one."""
+    x = torch.randn(experts, rows, k, device="cuda") * k ** -0.5
+    return mx.quantize(x, "mxfp4")
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--context", type=int, default=4096)
@@ -37,6 +44,9 @@ def main():
     ap.add_argument("--drafts", type=int, default=4)
     ap.add_argument("--hidden", type=int, default=7168)
     ap.add_argument("--rank", type=int, default=32)
+    ap.add_argument("--experts", type=int, default=0)
+    ap.add_argument("--choices", type=int, default=4)
+    ap.add_argument("--inner", type=int, default=1024)
     ap.add_argument("--steps", type=int, default=50)
     args = ap.parse_args()
     torch.manual_seed(0)
@@ -51,6 +61,11 @@ def main():
     adapters = mx.Adapters(bf16(args.requests, args.rank, heads * value, std=0.01),
                            bf16(args.requests, args.hidden, args.rank))
     attention = mx.LatentAttention(heads, latent)
+    if args.experts:
+        w_route = bf16(args.hidden, args.experts, std=args.hidden ** -0.5)
+        first = mx.ExpertProduct(*mxfp4(args.experts, 2 * args.inner, args.hidden), gated=True)
+        second = mx.ExpertProduct(*mxfp4(args.experts, args.hidden, args.inner),
+                                  workspace=first.workspace)
 
     # What a serving loop holds: the pool of pages, who owns which, the lengths.
     pages = -(-(args.context + args.drafts + args.steps) // PAGE)
@@ -83,6 +98,12 @@ def main():
         x, x_scale = mx.latent_values(o, w_value)
         gemm.run_adapted(x, x_scale, adapters, which)
         mailbox.consume(rows, out)
+        if args.experts:
+            routing = mx.route(out @ w_route, args.choices)
+            h, h_scale = mx.quantize(out, "mxfp8", rows=routing.row)
+            h, h_scale = first.run(h, h_scale, routing.begin, format="mxfp8")
+            y = second.run(h, h_scale, routing.begin)
+            mx.combine(y, routing.weight, routing.slot, add=out, out=out)
 
     step()  # once outside the capture
     stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
@@ -102,8 +123,11 @@ def main():
     status, words = mailbox.status()
     assert status == mx.OK and attention.status() == 0, (status, words)
     assert torch.isfinite(out).all()
+    if args.experts:
+        assert first.status() == 0 and second.status() == 0
+    layer = f", {args.choices} of {args.experts} experts" if args.experts else ""
     print(f"{args.requests} requests x {args.drafts} drafts, {heads} heads, context "
-          f"{args.context}: {start.elapsed_time(end) / args.steps * 1e3:.1f} us a step")
+          f"{args.context}{layer}: {start.elapsed_time(end) / args.steps * 1e3:.1f} us a step")
 
 
 if __name__ == "__main__":

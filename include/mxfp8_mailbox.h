@@ -579,7 +579,7 @@ mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* desc, const void* q, c
 #define MXFP8_MAX_EXPERTS 512
 #define MXFP8_MAX_CHOICES 32
 
-/* Workspace bytes of mxfp8_route (0 where it needs none, as for up to 128 tokens;
+/* Workspace bytes of mxfp8_route (0 where it needs none, as for up to 32 tokens;
  * also for invalid sizes). */
 size_t mxfp8_route_workspace_bytes(int64_t tokens, int32_t experts);
 

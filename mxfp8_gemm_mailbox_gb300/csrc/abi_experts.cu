@@ -126,7 +126,7 @@ mxfp8_status encode_x(CUtensorMap* map, const void* x, const mxfp8_expert_desc& 
 extern "C" {
 
 size_t mxfp8_route_workspace_bytes(int64_t tokens, int32_t experts) {
-  if (tokens <= kRouteTokens || experts < 1 || experts > MXFP8_MAX_EXPERTS || tokens > INT32_MAX)
+  if (tokens <= kRouteFew || experts < 1 || experts > MXFP8_MAX_EXPERTS || tokens > INT32_MAX)
     return 0;
   const int64_t block = route_block_tokens(tokens);
   return static_cast<size_t>((tokens + block - 1) / block + 1) * experts * 4;

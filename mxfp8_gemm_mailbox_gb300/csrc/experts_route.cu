@@ -13,7 +13,7 @@
 // moves its keys up.  An expert appears once at most among a token's, so a block of tokens is, for
 // each expert, a bit mask: its population is the block's count, and that of the bits
 // below a token the token's place.  Nothing depends on the order of atomics.  One block
-// does all of up to 128 tokens; for more a second kernel gives the places, each block
+// does all of up to 32 tokens; for more a second kernel gives the places, each block
 // adding up the counts of those before it; past 32 blocks a kernel between the two adds
 // them (all blocks reading the same lines at the same time took 20 us at 16k tokens, in
 // place of 2).
@@ -127,10 +127,11 @@ __device__ __forceinline__ void load_keys(const RouteParams& p, int64_t t,
   }
 }
 
-// Token t's experts and weights, from its keys; the chosen experts' bits in `mask`.
-template <int kType, int kEach>
-__device__ __forceinline__ void choose(const RouteParams& p, int64_t t,
-                                       typename KeyOf<kType>::T (&key)[kEach], int bit,
+// The experts and weights of kAtOnce tokens (bits bit, bit + kWarps of the block's masks),
+// from their keys; the tokens' steps, 150 clocks each, do not wait for one another.
+template <int kType, int kEach, int kAtOnce>
+__device__ __forceinline__ void choose(const RouteParams& p, int64_t t0, int tokens, int bit,
+                                       typename KeyOf<kType>::T (&key)[kAtOnce][kEach],
                                        uint32_t (*mask)[MXFP8_MAX_EXPERTS]) {
   constexpr bool kShort = kType != MXFP8_FP32;
   using Key = typename KeyOf<kType>::T;
@@ -147,40 +148,55 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t,
     else
       return static_cast<uint32_t>(k >> 32) <= kNothing;
   };
-  sort_down(key);
-  float total = 0.0f;
-  Key first = 0u, mine = 0u;  // lane j: the j-th chosen key
+  Key first[kAtOnce], mine[kAtOnce];  // lane j: the j-th chosen key
+  float total[kAtOnce];
+#pragma unroll
+  for (int n = 0; n < kAtOnce; ++n) {
+    sort_down(key[n]);
+    first[n] = mine[n] = 0u;
+    total[n] = 0.0f;
+  }
   for (int j = 0; j < p.k; ++j) {
-    Key top;
-    if constexpr (kShort) {
-      top = __reduce_max_sync(~0u, key[0]);
-    } else {
-      const uint32_t high = __reduce_max_sync(~0u, static_cast<uint32_t>(key[0] >> 32));
-      const uint32_t low = static_cast<uint32_t>(key[0] >> 32) == high ? key[0] & 0xFFFFu : 0u;
-      top = static_cast<uint64_t>(high) << 32 | __reduce_max_sync(~0u, low);
-    }
-    if (nothing(top)) break;
-    if (j == 0) {
-      first = top;
-      if (!p.normalize)
+    Key top[kAtOnce];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
-          if (key[i] != 0u) total += expf(value(key[i]) - value(first));
+    for (int n = 0; n < kAtOnce; ++n) {
+      if constexpr (kShort) {
+        top[n] = __reduce_max_sync(~0u, key[n][0]);
+      } else {
+        const uint32_t high = __reduce_max_sync(~0u, static_cast<uint32_t>(key[n][0] >> 32));
+        const uint32_t low =
+            static_cast<uint32_t>(key[n][0] >> 32) == high ? key[n][0] & 0xFFFFu : 0u;
+        top[n] = static_cast<uint64_t>(high) << 32 | __reduce_max_sync(~0u, low);
+      }
     }
-    if (lane == j) mine = top;
-    if (key[0] == top) {  // one lane: keys are all different
 #pragma unroll
-      for (int i = 0; i + 1 < kEach; ++i) key[i] = key[i + 1];
-      key[kEach - 1] = 0u;
+    for (int n = 0; n < kAtOnce; ++n) {
+      const bool live = !nothing(top[n]);  // else -infinity from here on
+      if (j == 0) {
+        first[n] = top[n];
+        if (!p.normalize && live)
+#pragma unroll
+          for (int i = 0; i < kEach; ++i)
+            if (key[n][i] != 0u) total[n] += expf(value(key[n][i]) - value(first[n]));
+      }
+      if (lane == j && live) mine[n] = top[n];
+      const bool pops = key[n][0] == top[n];  // one lane's: keys are all different
+#pragma unroll
+      for (int i = 0; i + 1 < kEach; ++i) key[n][i] = pops ? key[n][i + 1] : key[n][i];
+      key[n][kEach - 1] = pops ? Key{0u} : key[n][kEach - 1];
     }
   }
-  const int expert = mine != 0u ? static_cast<int>(0xFFFFu - (mine & 0xFFFFu)) : -1;
-  const float e = expert >= 0 ? expf(value(mine) - value(first)) : 0.0f;
-  total = warp_sum(p.normalize ? e : total);
-  if (lane < p.k) {
-    p.weight[t * p.k + lane] = expert >= 0 ? e / total : 0.0f;
-    p.expert[t * p.k + lane] = expert;
-    if (expert >= 0) atomicOr(&mask[bit / 32][expert], 1u << (bit % 32));
+#pragma unroll
+  for (int n = 0; n < kAtOnce; ++n) {
+    const int at = bit + n * kWarps;
+    const int expert = mine[n] != 0u ? static_cast<int>(0xFFFFu - (mine[n] & 0xFFFFu)) : -1;
+    const float e = expert >= 0 ? expf(value(mine[n]) - value(first[n])) : 0.0f;
+    const float sum = warp_sum(p.normalize ? e : total[n]);
+    if (lane < p.k && at < tokens) {
+      p.weight[(t0 + at) * p.k + lane] = expert >= 0 ? e / sum : 0.0f;
+      p.expert[(t0 + at) * p.k + lane] = expert;
+      if (expert >= 0) atomicOr(&mask[at / 32][expert], 1u << (at % 32));
+    }
   }
 }
 
@@ -218,17 +234,31 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
   ptx::grid_dependency_wait();
   int count = 0, earlier = 0;  // thread e: expert e's rows (places: of all blocks, of those before)
   if constexpr (kStep < 2) {
-    // A token's logits are on their way while the one before is chosen from.
+    // Two tokens at a time, whose logits are on their way while those before are chosen from.
     using Key = typename KeyOf<kType>::T;
-    Key next[kEach];
-    if (warp < tokens) load_keys<kType, kEach>(p, t0 + warp, next);
-    __syncthreads();
-    for (int i = warp; i < tokens; i += kWarps) {
-      Key key[kEach];
+    constexpr int kAtOnce = kType == MXFP8_FP32 && kEach > 8 ? 1 : 2;  // (registers)
+    Key next[kAtOnce][kEach];
+    const auto load = [&](int i) {
 #pragma unroll
-      for (int q = 0; q < kEach; ++q) key[q] = next[q];
-      if (i + kWarps < tokens) load_keys<kType, kEach>(p, t0 + i + kWarps, next);
-      choose<kType, kEach>(p, t0 + i, key, i, mask);
+      for (int n = 0; n < kAtOnce; ++n) {
+        if (i + n * kWarps < tokens) {
+          load_keys<kType, kEach>(p, t0 + i + n * kWarps, next[n]);
+        } else {
+#pragma unroll
+          for (int q = 0; q < kEach; ++q) next[n][q] = 0u;
+        }
+      }
+    };
+    load(warp);
+    __syncthreads();
+    for (int i = warp; i < tokens; i += kAtOnce * kWarps) {
+      Key key[kAtOnce][kEach];
+#pragma unroll
+      for (int n = 0; n < kAtOnce; ++n)
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) key[n][q] = next[n][q];
+      load(i + kAtOnce * kWarps);
+      choose<kType, kEach, kAtOnce>(p, t0, tokens, i, key, mask);
     }
   } else {
     if (tid < p.experts) {
@@ -403,10 +433,13 @@ cudaError_t route_blocks(const RouteParams& p, cudaStream_t stream) {
 }
 template <int kType, int kEach>
 cudaError_t route_as(const RouteParams& p, cudaStream_t stream) {
-  if (p.tokens <= kRouteTokens)
-    return launch(route_kernel<0, kRouteTokens, kType, kEach>, 1, kThreads, stream, p);
-  return route_block_tokens(p.tokens) == kRouteFew ? route_blocks<kRouteFew, kType, kEach>(p, stream)
-                                                   : route_blocks<kRouteMany, kType, kEach>(p, stream);
+  if (p.tokens <= kRouteFew)
+    return launch(route_kernel<0, kRouteFew, kType, kEach>, 1, kThreads, stream, p);
+  switch (route_block_tokens(p.tokens)) {
+    case kRouteFew: return route_blocks<kRouteFew, kType, kEach>(p, stream);
+    case kRouteSome: return route_blocks<kRouteSome, kType, kEach>(p, stream);
+    default: return route_blocks<kRouteMany, kType, kEach>(p, stream);
+  }
 }
 template <int kType>
 cudaError_t route_for(const RouteParams& p, cudaStream_t stream) {

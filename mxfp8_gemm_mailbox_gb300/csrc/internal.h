@@ -186,11 +186,13 @@ cudaError_t launch_latent_attend(const LatentParams& p, int latent, void* worksp
                                  cudaStream_t stream);
 
 // A layer of routed experts (experts_route.cu, quantize.cu, experts_product.cu).
-constexpr int kRouteTokens = 128;  // of a call with one block
-// Of a block of more: small ones fill the GPU; past the second's capacity for some 500 of
-// them, larger ones.
-constexpr int kRouteFew = 64, kRouteMany = 512;
-constexpr int route_block_tokens(int64_t tokens) { return tokens <= 32768 ? kRouteFew : kRouteMany; }
+// Tokens of a block: a call of up to 32 is one block's (two tokens a warp, side by side);
+// of more, small blocks while there are few tokens, larger ones for many, so that some 500
+// blocks' counts at the most are added up for 256k tokens.
+constexpr int kRouteFew = 32, kRouteSome = 64, kRouteMany = 512;
+constexpr int route_block_tokens(int64_t tokens) {
+  return tokens <= 8192 ? kRouteFew : tokens <= 32768 ? kRouteSome : kRouteMany;
+}
 struct RouteParams {
   int64_t tokens, stride;  // elements between tokens' logits
   int32_t experts, k, type, normalize;

@@ -32,8 +32,8 @@ def route(lib, logits=A, type=0, stride=64, tokens=4, experts=64, k=8, weight=A,
 def test_route_refusals(lib):
     for bad in (dict(type=3), dict(type=-1), dict(tokens=-1), dict(stride=63), dict(logits=0),
                 dict(logits=A + 1), dict(type=2, logits=A + 2), dict(weight=A + 2), dict(expert=0),
-                dict(slot=A + 1), dict(row=0), dict(begin=0), dict(tokens=129),
-                dict(tokens=129, workspace=A, nbytes=1023)):
+                dict(slot=A + 1), dict(row=0), dict(begin=0), dict(tokens=33),
+                dict(tokens=129, workspace=A, nbytes=1535)):
         assert route(lib, **bad) == mx.ERR_INVALID, bad
         assert text(lib)
     for bad in (dict(experts=0), dict(experts=513, stride=600), dict(k=0), dict(k=33),
@@ -43,8 +43,8 @@ def test_route_refusals(lib):
 
 def test_route_workspace(lib):
     size = lib.mxfp8_route_workspace_bytes
-    assert size(0, 64) == size(128, 64) == size(-5, 64) == size(200, 0) == size(200, 513) == 0
-    assert size(129, 63) == 4 * 63 * 4 and size(16384, 256) == 257 * 256 * 4
+    assert size(0, 64) == size(32, 64) == size(-5, 64) == size(200, 0) == size(200, 513) == 0
+    assert size(33, 63) == 3 * 63 * 4 and size(129, 64) == 6 * 64 * 4 and size(16384, 256) == 257 * 256 * 4
     assert size(1 << 20, 512) == 2049 * 512 * 4
 
 

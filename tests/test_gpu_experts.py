@@ -9,6 +9,10 @@ route's weights: 2^-20 of the value (an exponential of 2 ulps, a sum, a quotient
 2^-24 of it for each unit of z_max - z, whose rounding the exponential turns into a
 relative error of that size (the sum's own such error is the mean of z_max - z under the
 weights, at most the logarithm of their number: 6.3 units, within the 2^-20)."""
+import subprocess
+import sys
+from pathlib import Path
+
 import pytest
 import torch
 
@@ -194,7 +198,7 @@ def check_route(logits, k, normalize=True):
     return got
 
 
-@pytest.mark.parametrize("tokens", [0, 1, 2, 31, 127, 128, 129, 256, 300, 1025])
+@pytest.mark.parametrize("tokens", [0, 1, 2, 31, 32, 33, 128, 300, 1024, 1025])
 @pytest.mark.parametrize("experts,k", [(1, 1), (2, 2), (33, 5), (64, 8), (256, 8)])
 def test_route_sizes(cuda, tokens, experts, k):
     check_route(torch.randn(tokens, experts, generator=generator(tokens), device="cuda"), k)
@@ -233,7 +237,7 @@ def test_route_ties_infinities_and_nan(cuda):
     check_route(z.to(torch.bfloat16), 3, normalize=False)
 
 
-@pytest.mark.parametrize("tokens", [2048, 2049, 5000, 32769, 40000])
+@pytest.mark.parametrize("tokens", [2048, 8192, 8193, 32769, 40000])
 def test_route_many_tokens(cuda, tokens):
     """Against the definition in sorts: the lowest index first among equal logits."""
     experts, k = 37, 3
@@ -523,3 +527,12 @@ def test_quantized_rows_into_the_projection(cuda):
     got = mailbox.consume(5)
     want, size = products(w, w_scale, codes, scale, [5])
     close_bf16(got, want, sum_error(size, 512))
+
+
+def test_the_example_with_experts(cuda):
+    root = Path(__file__).resolve().parents[1]
+    res = subprocess.run([sys.executable, str(root / "examples" / "decode_step.py"), "--steps", "5",
+                          "--context", "100", "--heads", "16", "--hidden", "2048", "--experts", "16",
+                          "--inner", "512"], capture_output=True, text=True, timeout=300, cwd=root)
+    assert res.returncode == 0, res.stderr[-2000:]
+    assert "4 of 16 experts" in res.stdout
