@@ -47,6 +47,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "internal.h"
@@ -103,6 +104,10 @@ struct Shape {
   static constexpr uint32_t kMisc = kBars + 8 * (2 * kStages + 4 + 2 * kQuads);
   static constexpr uint32_t kBytes = kMisc + 32 + 1024;
   static_assert(kBytes <= 232448, "shared memory");
+  // The allocation of tensor memory waits for whoever holds some; no CTA that in turn waits
+  // for another (the projection's clusters ask for a third of an SM's shared memory) may be
+  // on its SM.
+  static_assert(kBytes > 233472 / 3 * 2, "an SM to itself");
 };
 // Few rows an expert: bound by the stream of W.  Many: by the products.
 using Narrow = Shape<false, 32, 2, 5, 5, 8, 8>;
@@ -879,9 +884,17 @@ template <class S, bool kGated, bool kCuts>
 cudaError_t launch_as(const ExpertMaps& maps, const ExpertParams& p, int ctas,
                       cudaStream_t stream) {
   const auto kernel = expert_kernel<S, kGated, kCuts>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(S::kBytes));
+  static std::atomic<uint64_t> asked{0};  // a bit a device
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = device < 64 ? uint64_t{1} << device : 0u;
+  if (!(asked.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(S::kBytes));
+    if (e != cudaSuccess) return e;
+    asked.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -18,9 +18,14 @@
 // them (all blocks reading the same lines at the same time took 20 us at 16k tokens, in
 // place of 2).
 //
+// Bound by the steps' latency, 150 clocks each, so two tokens a warp go side by side, and by
+// instructions where there are many tokens: 16384 tokens, 256 experts, k 8 18 us (the logits
+// are 1.2 us' reading); a token 3.0 us, 500 tokens 6.7.
+//
 // Combine.  out[t] = add[t] + sum_j weight[t][j] y[slot[t][j]], in FP32, j
 // ascending, rounded once; a thread has 8 numbers of a row, and its loads are
-// all under way at once.
+// all under way at once.  Bound by the memory: 4096 tokens, 8 rows of 4096 each, 46.5 us for
+// 302 MB (6.5 TB/s); one token 2.5 us, the launch and two round trips.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -8,8 +8,15 @@
 // in E4M3 and no part of its block's scale; E2M1 has no NaN, so there the block
 // takes the scale NaN (255).
 //
-// Bound by the memory: two lanes take a block of 32, each 16 numbers, so that a
-// lane's loads and its store of codes are 16 bytes wide (8 of E2M1).
+// Bound by the memory: two lanes take a block of 32, each 16 numbers (a 32-byte sector of
+// 16-bit ones), twice, so that 64 bytes a thread are under way; the largest magnitude of
+// 16-bit numbers is found two at a time and a scale is one factor, which leaves some four
+// instructions a number (with a comparison and two factors each the arithmetic took longer
+// than the memory: 139 us below).
+//
+// Measured: 16384 x 8192 BF16 to MXFP4 and back 103 us for 687 MB, 6.7 TB/s (the copy rate is
+// 6.78); one share a thread 106, four 105.  64 gathered rows of 7168: 1.8 us, the launch and
+// two round trips.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
