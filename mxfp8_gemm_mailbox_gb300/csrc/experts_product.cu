@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(S::kThreads, 1)
       const uint8_t* const of_w =
           p.w_sf + static_cast<size_t>(s.expert * p.w_tiles + w_tile) * p.k_tiles * kChunk;
       // Rows of codes on 16-byte boundaries give four k tiles a load.
-      const bool wide = (p.k_tiles | s.kt0) % 4 == 0;
+      const bool wide = p.k_tiles % 4 == 0 && reinterpret_cast<uintptr_t>(p.x_scale) % 16 == 0;
       for (int kt = s.kt0; kt < s.kt1; kt += 4, ++quad) {
         const uint32_t place = quad % S::kQuads, use = quad / S::kQuads;
         const int count = min(4, s.kt1 - kt);

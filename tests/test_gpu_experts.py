@@ -369,6 +369,20 @@ def test_one_matrix_without_begin(cuda):
     close_bf16(one.run(c.x, c.x_scale), *c.expected())
 
 
+@pytest.mark.parametrize("rows,n", [(5, 136), (100, 2560), (1000, 2560)])
+@pytest.mark.parametrize("words", [1, 2, 3])
+def test_scales_between_16_byte_boundaries(cuda, rows, n, words):
+    w, w_scale = random_codes(90, (n,), 512, 4)
+    x, x_scale = random_codes(91, (rows,), 512, 8)
+    product = mx.ExpertProduct(w, w_scale)
+    moved = torch.empty(x_scale.numel() + 16, dtype=torch.uint8, device="cuda")
+    moved = moved[4 * words:][:x_scale.numel()].view_as(x_scale)
+    moved.copy_(x_scale)
+    assert moved.data_ptr() % 16 == 4 * words
+    assert torch.equal(product.run(x, moved), product.run(x, x_scale))
+    assert product.status() == 0
+
+
 def test_rows_of_no_expert_are_left(cuda):
     for counts, total in (([5, 3], 12), ([100, 90], 260)):
         c = Case(counts, 128, 256)
