@@ -309,7 +309,8 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   p.k_tiles = d->k / 128;
   p.gated = d->gated;
   p.format = d->out_format;
-  p.idesc = 1u << 23 | (tile.kind == ExpertTile::kWide ? 256u : 128u) >> 4 << 24 | (d->w_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 7 : 0u) |
+  p.idesc = 1u << 23 | (tile.kind == ExpertTile::kWide ? 256u : 128u) >> 4 << 24 |
+            (d->w_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 7 : 0u) |
             (d->x_format == MXFP8_FORMAT_MXFP4 ? kE2M1 << 10 : 0u);
   // A copy counts the bytes that it reads, not the places that 4-bit elements take.
   const uint32_t x_row = tile.k_tiles * (d->x_format == MXFP8_FORMAT_MXFP4 ? 64 : 128);

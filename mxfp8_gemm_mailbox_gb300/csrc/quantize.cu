@@ -106,12 +106,9 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
     const uint32_t i = first + n * kThreads;
     live[n] = i < p.items;
     if (!live[n]) continue;
-    int64_t from = 0, at = static_cast<int64_t>(i) * kShare;
-    if (per_row != p.items) {  // else one row, as of a matrix without gaps
-      const uint32_t row = i / per_row;
-      from = row;
-      at = (i - row * per_row) * kShare;
-    }
+    const uint32_t row = i / per_row;
+    const int64_t at = static_cast<int64_t>(i - row * per_row) * kShare;
+    int64_t from = row;
     if (p.rows) {
       from = p.rows[from];
       if (from < 0 || from >= p.x_rows) {

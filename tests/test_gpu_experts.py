@@ -352,6 +352,29 @@ def test_gated_widths(cuda, n, rows):
     Case([rows, 4], n, 256, gated=True, seed=n).check("mxfp8")
 
 
+@pytest.mark.parametrize("power", [-60, 0, 60, 120])
+@pytest.mark.parametrize("rows", [3, 40])
+def test_gated_far_from_zero(cuda, power, rows):
+    """Gates from -240 to 240, ups of 2^power, up to 0.94 of BF16's largest.  y is exact (one product each): what remains is
+    the exponential's error, 2 ulps and 1.2 for each unit of its argument, and some roundings."""
+    n, k = 64, 128
+    w = torch.zeros(2 * n, k, dtype=torch.uint8, device="cuda")
+    gates = torch.linspace(-240.0, 240.0, n, device="cuda").to(torch.float8_e4m3fn)
+    w[:n, 0], w[n:, 0] = gates.view(torch.uint8), 0x38
+    w_scale = torch.full((2 * n, k // 32), 127, dtype=torch.uint8, device="cuda")
+    w_scale[n:] = 127 + power
+    x = torch.zeros(rows, k, dtype=torch.uint8, device="cuda")
+    x[:, 0] = 0x38
+    x_scale = torch.full((rows, k // 32), 127, dtype=torch.uint8, device="cuda")
+    product = mx.ExpertProduct(w, w_scale, gated=True)
+    g = gates.double()
+    h = g * torch.sigmoid(g) * 2.0 ** power
+    want = h.expand(rows, n)
+    got = product.run(x, x_scale)
+    assert product.status() == 0
+    close_bf16(got, want, want.abs() * ((4 + 1.2 * g.abs()) * 2.0 ** -23 + 2.0 ** -21))
+
+
 def test_gated_cut_tiles(cuda):
     Case([4], 64, 8192, gated=True).check("mxfp8")
     Case([300], 192, 8192, gated=True).check("mxfp4")
