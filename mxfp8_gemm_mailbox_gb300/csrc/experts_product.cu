@@ -120,6 +120,18 @@ __device__ __forceinline__ void pair_barrier(int pair) {
   asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
 }
 
+// To some 2^-22 of the value; below 2^-126 zero.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float reciprocal_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The k tiles of one tile, or a piece of them.
 struct Segment {
   int expert, row, rows, w_tile;  // rows: of the tile
@@ -743,9 +755,8 @@ __global__ void __launch_bounds__(S::kThreads, 1)
           // g / (1 + e^-g) u, for g < 0 as g e^g / (1 + e^g) u, with the root of the exponential
           // on both factors: nothing on the way overflows, or underflows where the result does
           // not, and the divisor is in 1 .. 2.
-          const float root = __expf(-0.5f * fabsf(g[i]));
-          const float both = g[i] < 0.0f ? (u[i] * root) * (g[i] * root) : u[i] * g[i];
-          u[i] = __fdividef(both, fmaf(root, root, 1.0f));
+          const float root = exp2_approx(-0.72134752f * fabsf(g[i])), f = g[i] < 0.0f ? root : 1.0f;
+          u[i] = (u[i] * f) * (g[i] * f) * reciprocal_approx(fmaf(root, root, 1.0f));
         }
         store_outputs<kRows>(p, u, s.row + c + at, c + at < s.rows, w_tile * 64 + pair * 32 + n_lane);
       } else {
