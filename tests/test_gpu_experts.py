@@ -566,6 +566,56 @@ def test_quantized_rows_into_the_projection(cuda):
     close_bf16(got, want, sum_error(size, 512))
 
 
+FAR = (1 << 30) + 16  # elements between three rows: the last lies past 2^31
+
+
+def test_rows_past_31_bits(cuda):
+    far = torch.empty(2 * FAR + 1024, dtype=torch.bfloat16, device="cuda")
+    gen = generator(95)
+    for columns in (256, 1024):
+        view = far.as_strided((3, columns), (FAR, 1))
+        near = torch.randn(3, columns, generator=gen, device="cuda").bfloat16()
+        view.copy_(near)
+        for got, want in zip(mx.quantize(view, "mxfp8"), mx.quantize(near, "mxfp8")):
+            assert torch.equal(got.view(torch.uint8), want.view(torch.uint8))
+        slot = torch.tensor([[2, 0], [1, 2]], dtype=torch.int32, device="cuda")
+        weight = torch.rand(2, 2, generator=gen, device="cuda")
+        assert torch.equal(mx.combine(view, weight, slot), mx.combine(near, weight, slot))
+        if columns == 256:
+            for got, want in zip(mx.route(view, 8), mx.route(near, 8)):
+                assert torch.equal(got, want)
+
+
+def test_codes_past_31_bits(cuda):
+    rows, k = (1 << 16) + 33, 1 << 15
+    x = torch.empty(rows, k, dtype=torch.bfloat16, device="cuda").normal_(generator=generator(96))
+    codes, scale = mx.quantize(x, "mxfp8")
+    back = mx.dequantize(codes, scale)
+    for at in (0, rows - 40):
+        want, want_scale = rounded(x[at:at + 40], 8)
+        assert torch.equal(codes[at:at + 40].view(torch.uint8), want)
+        assert torch.equal(scale[at:at + 40].view(torch.uint8), want_scale)
+        assert torch.equal(back[at:at + 40].double(), values(want, want_scale))
+
+
+@pytest.mark.parametrize("gated", [False, True])
+def test_products_past_31_bits(cuda, gated):
+    """4 GB of results (codes where gated), their last rows against their own product."""
+    rows, n, k = (1 << 18) + 100, 8192, 128
+    w, w_scale = random_codes(97, ((2 if gated else 1) * n,), k, 4, -6, -3)
+    x, x_scale = random_codes(98, (rows,), k, 8)
+    product = mx.ExpertProduct(w, w_scale, gated=gated)
+    format = "mxfp8" if gated else None
+    got = product.run(x, x_scale, format=format)
+    assert product.status() == 0
+    for at in (0, rows - 50):
+        y, size = products(w, w_scale, x[at:at + 50], x_scale[at:at + 50], [50])
+        if gated:
+            close_codes(got[0][at:at + 50], got[1][at:at + 50], *gate(y, sum_error(size, k)))
+        else:
+            close_bf16(got[at:at + 50], y, sum_error(size, k))
+
+
 def test_the_example_with_experts(cuda):
     root = Path(__file__).resolve().parents[1]
     res = subprocess.run([sys.executable, str(root / "examples" / "decode_step.py"), "--steps", "5",
