@@ -165,10 +165,23 @@ mxfp8_status mxfp8_route(const void* logits, int32_t type, int64_t stride, int64
       return fail(MXFP8_ERR_INVALID,
                   "the workspace must hold " + std::to_string(need) + " bytes");
   }
-  const bool pairs = experts % 2 == 0 && stride % 2 == 0 && aligned(logits, 4);
-  const RouteParams p{tokens,        stride, experts, k,      type, normalize ? 1 : 0,
-                      pairs ? 1 : 0, logits, weight,  expert, slot, row,
-                      begin,         static_cast<int32_t*>(workspace)};
+  const int64_t step = type == MXFP8_FP32 ? 4 : 8;  // elements of 16 bytes
+  RouteParams p{};
+  p.tokens = tokens;
+  p.stride = stride;
+  p.experts = experts;
+  p.k = k;
+  p.type = type;
+  p.normalize = normalize ? 1 : 0;
+  p.pairs = experts % 2 == 0 && stride % 2 == 0 && aligned(logits, 4);
+  p.wide = aligned(logits, 16) && (tokens <= 1 || stride % step == 0);
+  p.logits = logits;
+  p.weight = weight;
+  p.expert = expert;
+  p.slot = slot;
+  p.row = row;
+  p.begin = begin;
+  p.counts = static_cast<int32_t*>(workspace);
   const cudaError_t e = launch_route(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "launching the routing");
   return MXFP8_OK;

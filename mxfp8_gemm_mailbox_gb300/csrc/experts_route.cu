@@ -88,6 +88,22 @@ struct KeyOf<MXFP8_FP32> {
   using T = uint64_t;
 };
 
+// A key's logit, and whether that is -infinity (or the key none).
+template <int kType>
+__device__ __forceinline__ float value_of(typename KeyOf<kType>::T key) {
+  if constexpr (kType == MXFP8_FP32)
+    return key_value(static_cast<uint32_t>(key >> 32));
+  else
+    return short_value<kType>(key >> 16);
+}
+template <int kType>
+__device__ __forceinline__ bool is_nothing(typename KeyOf<kType>::T key) {
+  if constexpr (kType == MXFP8_FP32)
+    return static_cast<uint32_t>(key >> 32) <= kNothing;
+  else
+    return key >> 16 <= (kType == MXFP8_BF16 ? 0x007Fu : 0x03FFu);
+}
+
 // Descending, by Batcher's odd-even merges.
 template <int kEach, typename T>
 __device__ __forceinline__ void sort_down(T (&k)[kEach]) {
@@ -141,18 +157,6 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t0, int tok
   constexpr bool kShort = kType != MXFP8_FP32;
   using Key = typename KeyOf<kType>::T;
   const int lane = threadIdx.x % 32;
-  const auto value = [&](Key k) {
-    if constexpr (kShort)
-      return short_value<kType>(k >> 16);
-    else
-      return key_value(static_cast<uint32_t>(k >> 32));
-  };
-  const auto nothing = [&](Key k) {  // -infinity, or none
-    if constexpr (kShort)
-      return k >> 16 <= (kType == MXFP8_BF16 ? 0x007Fu : 0x03FFu);
-    else
-      return static_cast<uint32_t>(k >> 32) <= kNothing;
-  };
   Key first[kAtOnce], mine[kAtOnce];  // lane j: the j-th chosen key
   float total[kAtOnce];
 #pragma unroll
@@ -176,13 +180,13 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t0, int tok
     }
 #pragma unroll
     for (int n = 0; n < kAtOnce; ++n) {
-      const bool live = !nothing(top[n]);  // else -infinity from here on
+      const bool live = !is_nothing<kType>(top[n]);  // else -infinity from here on
       if (j == 0) {
         first[n] = top[n];
         if (!p.normalize && live)
 #pragma unroll
           for (int i = 0; i < kEach; ++i)
-            if (key[n][i] != 0u) total[n] += expf(value(key[n][i]) - value(first[n]));
+            if (key[n][i] != 0u) total[n] += expf(value_of<kType>(key[n][i]) - value_of<kType>(first[n]));
       }
       if (lane == j && live) mine[n] = top[n];
       const bool pops = key[n][0] == top[n];  // one lane's: keys are all different
@@ -195,13 +199,143 @@ __device__ __forceinline__ void choose(const RouteParams& p, int64_t t0, int tok
   for (int n = 0; n < kAtOnce; ++n) {
     const int at = bit + n * kWarps;
     const int expert = mine[n] != 0u ? static_cast<int>(0xFFFFu - (mine[n] & 0xFFFFu)) : -1;
-    const float e = expert >= 0 ? expf(value(mine[n]) - value(first[n])) : 0.0f;
+    const float e = expert >= 0 ? expf(value_of<kType>(mine[n]) - value_of<kType>(first[n])) : 0.0f;
     const float sum = warp_sum(p.normalize ? e : total[n]);
     if (lane < p.k && at < tokens) {
       p.weight[(t0 + at) * p.k + lane] = expert >= 0 ? e / sum : 0.0f;
       p.expert[(t0 + at) * p.k + lane] = expert;
       if (expert >= 0) atomicOr(&mask[at / 32][expert], 1u << (at % 32));
     }
+  }
+}
+
+// ------------------------------------------------------- up to eight choices: kList of them
+constexpr int kList = 8;
+constexpr int kLanes = 8;  // of a token
+
+// The larger eight of two descending lists, descending (keys are all different).
+template <typename T>
+__device__ __forceinline__ void merge_down(T (&a)[kList], const T (&b)[kList]) {
+#pragma unroll
+  for (int i = 0; i < kList; ++i) a[i] = a[i] > b[kList - 1 - i] ? a[i] : b[kList - 1 - i];
+#pragma unroll
+  for (int d = kList / 2; d > 0; d /= 2)  // what goes up, then down, in order
+#pragma unroll
+    for (int i = 0; i < kList; ++i)
+      if (!(i & d)) {
+        const T x = a[i], y = a[i + d];
+        a[i] = x > y ? x : y;
+        a[i + d] = x > y ? y : x;
+      }
+}
+
+// Eight neighbouring logits, the first `left` of them, as they lie in memory.
+template <int kType>
+struct Eight {
+  static constexpr int kWords = kType == MXFP8_FP32 ? 8 : 4;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const RouteParams& p, int64_t t, int e, int left) {
+    const int64_t at = t * p.stride + e;
+    if (left >= 8 && p.wide) {
+      const uint4* const from =
+          kType == MXFP8_FP32
+              ? reinterpret_cast<const uint4*>(static_cast<const float*>(p.logits) + at)
+              : reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.logits) + at);
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 u = from[i / 4];
+        w[i] = u.x, w[i + 1] = u.y, w[i + 2] = u.z, w[i + 3] = u.w;
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (kType == MXFP8_FP32) {
+        w[i] = i < left ? static_cast<const uint32_t*>(p.logits)[at + i] : 0u;
+      } else {
+        const uint16_t* const from = static_cast<const uint16_t*>(p.logits) + at;
+        w[i] = (2 * i < left ? from[2 * i] : 0u) |
+               (2 * i + 1 < left ? static_cast<uint32_t>(from[2 * i + 1]) << 16 : 0u);
+      }
+    }
+  }
+  __device__ __forceinline__ void keys(int e, int left, typename KeyOf<kType>::T (&key)[8]) const {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (kType == MXFP8_FP32) {
+        key[i] = static_cast<uint64_t>(order_key(__uint_as_float(w[i]))) << 32 | (0xFFFFu - (e + i));
+      } else {
+        const uint32_t both = short_keys<kType>(w[i]);
+        key[2 * i] = both << 16 | (0xFFFFu - (e + 2 * i));
+        key[2 * i + 1] = (both & 0xFFFF0000u) | (0xFFFFu - (e + 2 * i + 1));
+      }
+    }
+    if (left < 8)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i >= left) key[i] = 0u;
+  }
+};
+
+// The experts and weights of the block's token `at`, by eight lanes (past the last token
+// they go along).  All of a warp.
+template <int kType, int kEights>
+__device__ __forceinline__ void choose_few(const RouteParams& p, int64_t t0, int tokens, int at,
+                                           uint32_t (*mask)[MXFP8_MAX_EXPERTS]) {
+  using Key = typename KeyOf<kType>::T;
+  const int lane = threadIdx.x % kLanes;
+  const int64_t t = t0 + at;
+  const bool live = at < tokens;
+  const auto first = [&](int c) { return (c * kLanes + lane) * 8; };
+  const auto left = [&](int c) { return live ? p.experts - first(c) : 0; };
+  Eight<kType> eight[kEights];
+#pragma unroll
+  for (int c = 0; c < kEights; ++c) eight[c].load(p, t, first(c), left(c));
+  Key list[kList];
+  eight[0].keys(first(0), left(0), list);
+  sort_down(list);
+#pragma unroll
+  for (int c = 1; c < kEights; ++c) {
+    Key more[kList];
+    eight[c].keys(first(c), left(c), more);
+    sort_down(more);
+    merge_down(list, more);
+  }
+#pragma unroll
+  for (int o = 1; o < kLanes; o *= 2) {
+    Key other[kList];
+#pragma unroll
+    for (int i = 0; i < kList; ++i) other[i] = __shfl_xor_sync(~0u, list[i], o);
+    merge_down(list, other);
+  }
+  Key mine = list[0];  // lane j: the j-th
+#pragma unroll
+  for (int i = 1; i < kList; ++i) mine = lane == i ? list[i] : mine;
+  const bool chosen = lane < p.k && !is_nothing<kType>(mine);
+  const float top = value_of<kType>(list[0]);
+  const float e = chosen ? expf(value_of<kType>(mine) - top) : 0.0f;
+  float sum = e;
+  if (!p.normalize) {
+    sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < kEights; ++c) {
+      Key key[8];
+      Eight<kType> again;
+      again.load(p, t, first(c), left(c));
+      again.keys(first(c), left(c), key);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (key[i] != 0u) sum += expf(value_of<kType>(key[i]) - top);
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < kLanes; o *= 2) sum += __shfl_xor_sync(~0u, sum, o);
+  if (live && lane < p.k) {
+    const int expert = chosen ? static_cast<int>(0xFFFFu - (mine & 0xFFFFu)) : -1;
+    p.weight[t * p.k + lane] = chosen ? e / sum : 0.0f;
+    p.expert[t * p.k + lane] = expert;
+    if (chosen) atomicOr(&mask[at / 32][expert], 1u << (at % 32));
   }
 }
 
@@ -223,7 +357,7 @@ __device__ __forceinline__ int before_in_block(int v, int* sums) {
 
 // kStep 0: all of a call with one block.  1: the choice, and each block's counts.  2:
 // the places, from the counts of all blocks; 3: from the sums of those before.
-template <int kStep, int kTokens, int kType, int kEach>
+template <int kStep, int kTokens, int kType, int kEach, bool kFew>
 __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p) {
   constexpr int kMaskWords = kTokens / 32;
   __shared__ uint32_t mask[kMaskWords][MXFP8_MAX_EXPERTS];
@@ -235,10 +369,14 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
   const int tokens = static_cast<int>(min(static_cast<int64_t>(kTokens), p.tokens - t0));
   const int entries = max(tokens, 0) * p.k;
   for (int i = tid; i < kMaskWords * MXFP8_MAX_EXPERTS; i += kThreads) (&mask[0][0])[i] = 0u;
+  __syncthreads();
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
   int count = 0, earlier = 0;  // thread e: expert e's rows (places: of all blocks, of those before)
-  if constexpr (kStep < 2) {
+  if constexpr (kStep < 2 && kFew) {
+    for (int i = warp * (32 / kLanes); i < tokens; i += kThreads / kLanes)
+      choose_few<kType, kEach>(p, t0, tokens, i + tid % 32 / kLanes, mask);
+  } else if constexpr (kStep < 2) {
     // Two tokens at a time, whose logits are on their way while those before are chosen from.
     using Key = typename KeyOf<kType>::T;
     constexpr int kAtOnce = kType == MXFP8_FP32 && kEach > 8 ? 1 : 2;  // (registers)
@@ -255,7 +393,6 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
       }
     };
     load(warp);
-    __syncthreads();
     for (int i = warp; i < tokens; i += kAtOnce * kWarps) {
       Key key[kAtOnce][kEach];
 #pragma unroll
@@ -280,7 +417,6 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
         earlier = p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid];
       }
     }
-    __syncthreads();
     for (int i = tid; i < entries; i += kThreads) {
       const int e = p.expert[t0 * p.k + i];
       if (e >= 0) atomicOr(&mask[i / p.k / 32][e], 1u << (i / p.k % 32));
@@ -424,33 +560,40 @@ cudaError_t launch(void (*kernel)(Args...), uint32_t blocks, int threads, cudaSt
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int kTokens, int kType, int kEach>
+// kEach: keys a lane has, or where there are few choices eights of them.
+template <int kTokens, int kType, int kEach, bool kFew>
 cudaError_t route_blocks(const RouteParams& p, cudaStream_t stream) {
   const uint32_t blocks = static_cast<uint32_t>((p.tokens + kTokens - 1) / kTokens);
-  cudaError_t e = launch(route_kernel<1, kTokens, kType, kEach>, blocks, kThreads, stream, p);
+  cudaError_t e = launch(route_kernel<1, kTokens, kType, kEach, kFew>, blocks, kThreads, stream, p);
   if (e != cudaSuccess) return e;
   if (blocks <= 32)
-    return launch(route_kernel<2, kTokens, MXFP8_FP32, 2>, blocks, kThreads, stream, p);
+    return launch(route_kernel<2, kTokens, MXFP8_FP32, 2, false>, blocks, kThreads, stream, p);
   e = launch(route_sum_kernel, static_cast<uint32_t>((p.experts + 31) / 32), 1024, stream, p.counts,
              p.experts, static_cast<int>(blocks));
   if (e != cudaSuccess) return e;
-  return launch(route_kernel<3, kTokens, MXFP8_FP32, 2>, blocks, kThreads, stream, p);
+  return launch(route_kernel<3, kTokens, MXFP8_FP32, 2, false>, blocks, kThreads, stream, p);
 }
-template <int kType, int kEach>
+template <int kType, int kEach, bool kFew>
 cudaError_t route_as(const RouteParams& p, cudaStream_t stream) {
   if (p.tokens <= kRouteFew)
-    return launch(route_kernel<0, kRouteFew, kType, kEach>, 1, kThreads, stream, p);
+    return launch(route_kernel<0, kRouteFew, kType, kEach, kFew>, 1, kThreads, stream, p);
   switch (route_block_tokens(p.tokens)) {
-    case kRouteFew: return route_blocks<kRouteFew, kType, kEach>(p, stream);
-    case kRouteSome: return route_blocks<kRouteSome, kType, kEach>(p, stream);
-    default: return route_blocks<kRouteMany, kType, kEach>(p, stream);
+    case kRouteFew: return route_blocks<kRouteFew, kType, kEach, kFew>(p, stream);
+    case kRouteSome: return route_blocks<kRouteSome, kType, kEach, kFew>(p, stream);
+    default: return route_blocks<kRouteMany, kType, kEach, kFew>(p, stream);
   }
 }
 template <int kType>
 cudaError_t route_for(const RouteParams& p, cudaStream_t stream) {
-  if (p.experts <= 64) return route_as<kType, 2>(p, stream);
-  if (p.experts <= 256) return route_as<kType, 8>(p, stream);
-  return route_as<kType, 16>(p, stream);
+  if (p.k <= kList) {
+    if (p.experts <= 64) return route_as<kType, 1, true>(p, stream);
+    if (p.experts <= 128) return route_as<kType, 2, true>(p, stream);
+    if (p.experts <= 256) return route_as<kType, 4, true>(p, stream);
+    return route_as<kType, 8, true>(p, stream);
+  }
+  if (p.experts <= 64) return route_as<kType, 2, false>(p, stream);
+  if (p.experts <= 256) return route_as<kType, 8, false>(p, stream);
+  return route_as<kType, 16, false>(p, stream);
 }
 
 }  // namespace

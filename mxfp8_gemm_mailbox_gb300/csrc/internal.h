@@ -197,6 +197,7 @@ struct RouteParams {
   int64_t tokens, stride;  // elements between tokens' logits
   int32_t experts, k, type, normalize;
   int32_t pairs;  // logits of 16 bits lie on 4-byte boundaries two by two
+  int32_t wide;   // rows of logits lie on 16-byte boundaries
   const void* logits;
   float* weight;    // [tokens][k]
   int32_t* expert;  // [tokens][k], -1: none

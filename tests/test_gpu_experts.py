@@ -221,6 +221,23 @@ def test_route_unaligned_pairs(cuda, dtype):
     check_route(every, 32)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("experts,k", [(7, 7), (71, 8), (128, 8), (129, 9), (250, 7), (257, 8), (512, 8)])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_route_up_to_eight_and_more(cuda, dtype, experts, k, normalize):
+    """Rows on 16-byte boundaries and between them, with ties among them."""
+    z = torch.randn(70, experts, generator=generator(k), device="cuda") * 3
+    z[10:20] = torch.round(z[10:20])
+    z[20, ::3] = -float("inf")
+    z = z.to(dtype)
+    wide = torch.zeros(70, 528, dtype=dtype, device="cuda")[:, 8:8 + experts]
+    odd = torch.zeros(70, 531, dtype=dtype, device="cuda")[:, 1:1 + experts]
+    for part in (wide, odd):
+        part.copy_(z)
+        check_route(part, k, normalize)
+    check_route(wide[3:4], k, normalize)
+
+
 def test_route_ties_infinities_and_nan(cuda):
     inf, nan = float("inf"), float("nan")
     z = torch.zeros(10, 40, device="cuda")  # all equal: the lowest indexes
