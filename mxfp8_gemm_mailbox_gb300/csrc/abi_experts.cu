@@ -169,6 +169,7 @@ mxfp8_status mxfp8_route(const void* logits, int32_t type, int64_t stride, int64
   RouteParams p{};
   p.tokens = tokens;
   p.stride = stride;
+  p.block = route_block_tokens(tokens);
   p.experts = experts;
   p.k = k;
   p.type = type;

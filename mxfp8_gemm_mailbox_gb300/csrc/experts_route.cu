@@ -6,21 +6,27 @@
 // A slot is a row of the experts' products: slots are numbered by expert, then
 // by token.  A logit of -infinity is not chosen: such an entry has no slot.
 //
-// A warp takes a token, its logits in registers as integers of the same order with the
-// index below them (32 bits for logits of 16, else 64), each lane's sorted once.  A step
-// of the choice is then a warp reduction over the lanes' first keys (for FP32 a second
-// one, over the indexes of the lanes that have the largest), and the lane that gave it
-// moves its keys up.  An expert appears once at most among a token's, so a block of tokens is, for
-// each expert, a bit mask: its population is the block's count, and that of the bits
-// below a token the token's place.  Nothing depends on the order of atomics.  One block
-// does all of up to 32 tokens; for more a second kernel gives the places, each block
-// adding up the counts of those before it; past 32 blocks a kernel between the two adds
-// them (all blocks reading the same lines at the same time took 20 us at 16k tokens, in
-// place of 2).
+// Logits become integers of the same order with the index below them (32 bits for logits of
+// 16, else 64), no two alike.  Up to eight choices: eight lanes take a token, each sorts its
+// keys by eights and merges the larger eight of two lists until it has one, and three
+// exchanges merge the lanes'; lane j then has the j-th choice.  Past eight a warp takes a
+// token, each lane's keys sorted once; a step of the choice is a warp reduction over the
+// lanes' first keys (for FP32 a second one, over the indexes of the lanes that have the
+// largest), and the lane that gave it moves its keys up: 150 clocks each, so two tokens a
+// warp go side by side.  (By such steps alone, 32 tokens, 128 experts, k 8 took 4.5 us in
+// place of 2.6, 16384 tokens, 256 experts 18.2 in place of 12.5.)
 //
-// Bound by the steps' latency, 150 clocks each, so two tokens a warp go side by side, and by
-// instructions where there are many tokens: 16384 tokens, 256 experts, k 8 18 us (the logits
-// are 1.2 us' reading); a token 3.0 us, 500 tokens 6.7.
+// An expert appears once at most among a token's, so a block of tokens is, for each expert,
+// a bit mask: its population is the block's count, and that of the bits below a token the
+// token's place.  Nothing depends on the order of atomics.  One block does all of up to 32
+// tokens; for more a second kernel gives the places, each block adding up the counts of
+// those before it; past 64 blocks a kernel between the two adds them (63 blocks 6.9 us so,
+// 6.6 without; 94 blocks 7.7 and 8.1).
+//
+// Bound by instructions where there are many tokens (a lane's compares and exchanges, which
+// issue at half rate, are most of them) and by the launches where there are few: 16384
+// tokens, 256 experts, k 8 12.5 us (the logits are 1.2 us' reading); a token 2.9 us, 500
+// tokens of 128 experts 4.5, 100000 31.
 //
 // Combine.  out[t] = add[t] + sum_j weight[t][j] y[slot[t][j]], in FP32, j
 // ascending, rounded once; a thread has 8 numbers of a row, and its loads are
@@ -37,7 +43,7 @@ namespace {
 
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-static_assert(kThreads >= MXFP8_MAX_EXPERTS, "a thread an expert");
+static_assert(kThreads == MXFP8_MAX_EXPERTS, "a thread an expert");
 
 // Larger values have larger keys; +0 and -0 one; NaN the largest of all.
 __device__ __forceinline__ uint32_t order_key(float z) {
@@ -278,10 +284,21 @@ struct Eight {
   }
 };
 
+// A lane's logits of the block's token `at`; none past the last token.
+template <int kType, int kEights>
+__device__ __forceinline__ void load_few(const RouteParams& p, int64_t t0, int tokens, int at,
+                                         Eight<kType> (&eight)[kEights]) {
+#pragma unroll
+  for (int c = 0; c < kEights; ++c) {
+    const int first = (c * kLanes + static_cast<int>(threadIdx.x) % kLanes) * 8;
+    eight[c].load(p, t0 + at, first, at < tokens ? p.experts - first : 0);
+  }
+}
 // The experts and weights of the block's token `at`, by eight lanes (past the last token
 // they go along).  All of a warp.
 template <int kType, int kEights>
 __device__ __forceinline__ void choose_few(const RouteParams& p, int64_t t0, int tokens, int at,
+                                           const Eight<kType> (&eight)[kEights],
                                            uint32_t (*mask)[MXFP8_MAX_EXPERTS]) {
   using Key = typename KeyOf<kType>::T;
   const int lane = threadIdx.x % kLanes;
@@ -289,9 +306,6 @@ __device__ __forceinline__ void choose_few(const RouteParams& p, int64_t t0, int
   const bool live = at < tokens;
   const auto first = [&](int c) { return (c * kLanes + lane) * 8; };
   const auto left = [&](int c) { return live ? p.experts - first(c) : 0; };
-  Eight<kType> eight[kEights];
-#pragma unroll
-  for (int c = 0; c < kEights; ++c) eight[c].load(p, t, first(c), left(c));
   Key list[kList];
   eight[0].keys(first(0), left(0), list);
   sort_down(list);
@@ -355,28 +369,72 @@ __device__ __forceinline__ int before_in_block(int v, int* sums) {
   return base + inc - v;
 }
 
-// kStep 0: all of a call with one block.  1: the choice, and each block's counts.  2:
-// the places, from the counts of all blocks; 3: from the sums of those before.
-template <int kStep, int kTokens, int kType, int kEach, bool kFew>
-__global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ RouteParams p) {
-  constexpr int kMaskWords = kTokens / 32;
-  __shared__ uint32_t mask[kMaskWords][MXFP8_MAX_EXPERTS];
-  __shared__ int base[MXFP8_MAX_EXPERTS];
-  __shared__ int sums[kWarps];
-  __shared__ int routed;
-  const int tid = threadIdx.x, warp = tid / 32;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
-  const int tokens = static_cast<int>(min(static_cast<int64_t>(kTokens), p.tokens - t0));
-  const int entries = max(tokens, 0) * p.k;
-  for (int i = tid; i < kMaskWords * MXFP8_MAX_EXPERTS; i += kThreads) (&mask[0][0])[i] = 0u;
+// A block's tokens, for each expert as bits.
+struct Masks {
+  uint32_t bits[kRouteMany / 32][MXFP8_MAX_EXPERTS];
+  int base[MXFP8_MAX_EXPERTS];
+  int sums[kWarps];
+  int routed;
+};
+
+// The slots of a block's `entries`, from the masks and, thread e, the rows of expert e (`count`:
+// of all blocks, `earlier`: of those before).
+__device__ __forceinline__ void place(const RouteParams& p, Masks& m, int64_t t0, int entries,
+                                      int count, int earlier) {
+  const int tid = threadIdx.x;
+  const int begin = before_in_block(count, m.sums);
+  if (tid < p.experts) {
+    m.base[tid] = begin + earlier;
+    if (blockIdx.x == 0) p.begin[tid] = begin;
+    if (tid == p.experts - 1) {
+      m.routed = begin + count;
+      if (blockIdx.x == 0) p.begin[p.experts] = begin + count;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < entries; i += kThreads) {
+    const int64_t flat = t0 * p.k + i;
+    const int bit = i / p.k, e = p.expert[flat];
+    int slot = -1;
+    if (e >= 0) {
+      slot = m.base[e] + __popc(m.bits[bit / 32][e] & ((1u << (bit % 32)) - 1u));
+      for (int w = 0; w < bit / 32; ++w) slot += __popc(m.bits[w][e]);
+      p.row[slot] = static_cast<int32_t>(t0 + bit);
+    }
+    p.slot[flat] = slot;
+    if (flat >= m.routed) p.row[flat] = -1;  // a slot that nothing was routed to
+  }
+}
+
+// The choice; with one block the places too, else each block's counts.
+template <int kType, int kEach, bool kFew>
+__global__ void __launch_bounds__(kThreads)
+    route_choose_kernel(const __grid_constant__ RouteParams p) {
+  __shared__ Masks m;
+  const int tid = threadIdx.x, warp = tid / 32, words = p.block / 32;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.block;
+  const int tokens = static_cast<int>(min(static_cast<int64_t>(p.block), p.tokens - t0));
+  for (int w = 0; w < words; ++w) m.bits[w][tid] = 0u;
   __syncthreads();
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
-  int count = 0, earlier = 0;  // thread e: expert e's rows (places: of all blocks, of those before)
-  if constexpr (kStep < 2 && kFew) {
-    for (int i = warp * (32 / kLanes); i < tokens; i += kThreads / kLanes)
-      choose_few<kType, kEach>(p, t0, tokens, i + tid % 32 / kLanes, mask);
-  } else if constexpr (kStep < 2) {
+  if constexpr (kFew) {
+    // Several times in a block of many tokens: the next logits are on their way meanwhile.
+    constexpr int kEvery = kThreads / kLanes;
+    constexpr bool kAhead = kEach * Eight<kType>::kWords <= 16;  // (registers)
+    Eight<kType> eight[kEach];
+    int at = tid / kLanes;
+    load_few<kType, kEach>(p, t0, tokens, at, eight);
+    for (int i = warp * (32 / kLanes); i < tokens; i += kEvery, at += kEvery) {
+      Eight<kType> next[kEach];
+      const bool more = i + kEvery < tokens;
+      if (kAhead && more) load_few<kType, kEach>(p, t0, tokens, at + kEvery, next);
+      choose_few<kType, kEach>(p, t0, tokens, at, eight, m.bits);
+      if (!kAhead && more) load_few<kType, kEach>(p, t0, tokens, at + kEvery, next);
+#pragma unroll
+      for (int c = 0; c < kEach; ++c) eight[c] = next[c];
+    }
+  } else {
     // Two tokens at a time, whose logits are on their way while those before are chosen from.
     using Key = typename KeyOf<kType>::T;
     constexpr int kAtOnce = kType == MXFP8_FP32 && kEach > 8 ? 1 : 2;  // (registers)
@@ -400,60 +458,57 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
 #pragma unroll
         for (int q = 0; q < kEach; ++q) key[n][q] = next[n][q];
       load(i + kAtOnce * kWarps);
-      choose<kType, kEach, kAtOnce>(p, t0, tokens, i, key, mask);
+      choose<kType, kEach, kAtOnce>(p, t0, tokens, i, key, m.bits);
     }
-  } else {
-    if (tid < p.experts) {
-      if constexpr (kStep == 2) {
-        const int blocks = gridDim.x, mine = blockIdx.x;
-#pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-          const int c = p.counts[b * p.experts + tid];
-          count += c;
-          if (b < mine) earlier += c;
+  }
+  __syncthreads();
+  int count = 0;
+  for (int w = 0; w < words; ++w) count += __popc(m.bits[w][tid]);
+  if (gridDim.x > 1) {
+    if (tid < p.experts) p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid] = count;
+    return;
+  }
+  place(p, m, t0, max(tokens, 0) * p.k, count, 0);
+}
+
+// The places: kSums from the sums of the counts before each block, else from the counts.
+template <bool kSums>
+__global__ void __launch_bounds__(kThreads)
+    route_place_kernel(const __grid_constant__ RouteParams p) {
+  __shared__ Masks m;
+  const int tid = threadIdx.x;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * p.block;
+  const int entries =
+      static_cast<int>(min(static_cast<int64_t>(p.block), p.tokens - t0)) * p.k;
+  for (int w = 0; w < p.block / 32; ++w) m.bits[w][tid] = 0u;
+  __syncthreads();
+  ptx::launch_dependents();
+  ptx::grid_dependency_wait();
+  int count = 0, earlier = 0;
+  if (tid < p.experts) {
+    if constexpr (kSums) {
+      count = p.counts[static_cast<size_t>(gridDim.x) * p.experts + tid];
+      earlier = p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid];
+    } else {
+      const int blocks = gridDim.x, mine = blockIdx.x;
+      for (int b = 0; b < blocks; b += 16) {  // all under way together
+        int c[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) c[i] = b + i < blocks ? p.counts[(b + i) * p.experts + tid] : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          count += c[i];
+          if (b + i < mine) earlier += c[i];
         }
-      } else {
-        count = p.counts[static_cast<size_t>(gridDim.x) * p.experts + tid];
-        earlier = p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid];
       }
     }
-    for (int i = tid; i < entries; i += kThreads) {
-      const int e = p.expert[t0 * p.k + i];
-      if (e >= 0) atomicOr(&mask[i / p.k / 32][e], 1u << (i / p.k % 32));
-    }
   }
-  __syncthreads();
-  if constexpr (kStep < 2) {
-    if (tid < p.experts)
-#pragma unroll
-      for (int w = 0; w < kMaskWords; ++w) count += __popc(mask[w][tid]);
-    if constexpr (kStep == 1) {
-      if (tid < p.experts) p.counts[static_cast<size_t>(blockIdx.x) * p.experts + tid] = count;
-      return;
-    }
-  }
-  const int begin = before_in_block(count, sums);
-  if (tid < p.experts) {
-    base[tid] = begin + earlier;
-    if (blockIdx.x == 0) p.begin[tid] = begin;
-    if (tid == p.experts - 1) {
-      routed = begin + count;
-      if (blockIdx.x == 0) p.begin[p.experts] = begin + count;
-    }
-  }
-  __syncthreads();
   for (int i = tid; i < entries; i += kThreads) {
-    const int64_t flat = t0 * p.k + i;
-    const int bit = i / p.k, e = p.expert[flat];
-    int slot = -1;
-    if (e >= 0) {
-      slot = base[e] + __popc(mask[bit / 32][e] & ((1u << (bit % 32)) - 1u));
-      for (int w = 0; w < bit / 32; ++w) slot += __popc(mask[w][e]);
-      p.row[slot] = static_cast<int32_t>(t0 + bit);
-    }
-    p.slot[flat] = slot;
-    if (flat >= routed) p.row[flat] = -1;  // a slot that nothing was routed to
+    const int e = p.expert[t0 * p.k + i];
+    if (e >= 0) atomicOr(&m.bits[i / p.k / 32][e], 1u << (i / p.k % 32));
   }
+  __syncthreads();
+  place(p, m, t0, entries, count, earlier);
 }
 
 // Each expert's counts become those of the blocks before, in place, and the row after
@@ -465,10 +520,17 @@ __global__ void __launch_bounds__(1024) route_sum_kernel(int32_t* counts, int ex
   ptx::grid_dependency_wait();
   const int lane = threadIdx.x % 32, part = threadIdx.x / 32, e = blockIdx.x * 32 + lane;
   const int each = (blocks + 31) / 32, from = min(part * each, blocks), to = min(from + each, blocks);
-  int sum = 0;
-  if (e < experts)
-#pragma unroll 8
-    for (int b = from; b < to; ++b) sum += counts[static_cast<size_t>(b) * experts + e];
+  const auto load = [&](int b, int (&c)[8]) {  // eight at a time, all under way together
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      c[i] = e < experts && b + i < to ? counts[static_cast<size_t>(b + i) * experts + e] : 0;
+  };
+  int c[8], sum = 0;
+  for (int b = from; b < to; b += 8) {
+    load(b, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += c[i];
+  }
   sums[part][lane] = sum;
   __syncthreads();
   int before = 0;
@@ -476,12 +538,14 @@ __global__ void __launch_bounds__(1024) route_sum_kernel(int32_t* counts, int ex
   for (int q = 0; q < 31; ++q)
     if (q < part) before += sums[q][lane];
   if (e >= experts) return;
-#pragma unroll 8
-  for (int b = from; b < to; ++b) {
-    int32_t* const at = counts + static_cast<size_t>(b) * experts + e;
-    const int c = *at;
-    *at = before;
-    before += c;
+  for (int b = from; b < to; b += 8) {
+    if (each > 8) load(b, c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (b + i < to) {
+        counts[static_cast<size_t>(b + i) * experts + e] = before;
+        before += c[i];
+      }
   }
   if (part == 31) counts[static_cast<size_t>(blocks) * experts + e] = before;
 }
@@ -561,27 +625,17 @@ cudaError_t launch(void (*kernel)(Args...), uint32_t blocks, int threads, cudaSt
 }
 
 // kEach: keys a lane has, or where there are few choices eights of them.
-template <int kTokens, int kType, int kEach, bool kFew>
-cudaError_t route_blocks(const RouteParams& p, cudaStream_t stream) {
-  const uint32_t blocks = static_cast<uint32_t>((p.tokens + kTokens - 1) / kTokens);
-  cudaError_t e = launch(route_kernel<1, kTokens, kType, kEach, kFew>, blocks, kThreads, stream, p);
-  if (e != cudaSuccess) return e;
-  if (blocks <= 32)
-    return launch(route_kernel<2, kTokens, MXFP8_FP32, 2, false>, blocks, kThreads, stream, p);
+template <int kType, int kEach, bool kFew>
+cudaError_t route_as(const RouteParams& p, cudaStream_t stream) {
+  const uint32_t blocks =
+      static_cast<uint32_t>(p.tokens <= p.block ? 1 : (p.tokens + p.block - 1) / p.block);
+  cudaError_t e = launch(route_choose_kernel<kType, kEach, kFew>, blocks, kThreads, stream, p);
+  if (e != cudaSuccess || blocks == 1) return e;
+  if (blocks <= 64) return launch(route_place_kernel<false>, blocks, kThreads, stream, p);
   e = launch(route_sum_kernel, static_cast<uint32_t>((p.experts + 31) / 32), 1024, stream, p.counts,
              p.experts, static_cast<int>(blocks));
   if (e != cudaSuccess) return e;
-  return launch(route_kernel<3, kTokens, MXFP8_FP32, 2, false>, blocks, kThreads, stream, p);
-}
-template <int kType, int kEach, bool kFew>
-cudaError_t route_as(const RouteParams& p, cudaStream_t stream) {
-  if (p.tokens <= kRouteFew)
-    return launch(route_kernel<0, kRouteFew, kType, kEach, kFew>, 1, kThreads, stream, p);
-  switch (route_block_tokens(p.tokens)) {
-    case kRouteFew: return route_blocks<kRouteFew, kType, kEach, kFew>(p, stream);
-    case kRouteSome: return route_blocks<kRouteSome, kType, kEach, kFew>(p, stream);
-    default: return route_blocks<kRouteMany, kType, kEach, kFew>(p, stream);
-  }
+  return launch(route_place_kernel<true>, blocks, kThreads, stream, p);
 }
 template <int kType>
 cudaError_t route_for(const RouteParams& p, cudaStream_t stream) {
@@ -591,9 +645,8 @@ cudaError_t route_for(const RouteParams& p, cudaStream_t stream) {
     if (p.experts <= 256) return route_as<kType, 4, true>(p, stream);
     return route_as<kType, 8, true>(p, stream);
   }
-  if (p.experts <= 64) return route_as<kType, 2, false>(p, stream);
-  if (p.experts <= 256) return route_as<kType, 8, false>(p, stream);
-  return route_as<kType, 16, false>(p, stream);
+  return p.experts <= 256 ? route_as<kType, 8, false>(p, stream)
+                          : route_as<kType, 16, false>(p, stream);
 }
 
 }  // namespace

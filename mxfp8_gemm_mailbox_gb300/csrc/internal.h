@@ -186,15 +186,17 @@ cudaError_t launch_latent_attend(const LatentParams& p, int latent, void* worksp
                                  cudaStream_t stream);
 
 // A layer of routed experts (experts_route.cu, quantize.cu, experts_product.cu).
-// Tokens of a block: a call of up to 32 is one block's (two tokens a warp, side by side);
-// of more, small blocks while there are few tokens, larger ones for many, so that some 500
-// blocks' counts at the most are added up for 256k tokens.
-constexpr int kRouteFew = 32, kRouteSome = 64, kRouteMany = 512;
+// Tokens of a block: a call of up to 32 is one block's; of more, small blocks while there
+// are few tokens, larger ones for many, so that fewer blocks' counts are added up.  Blocks of
+// 32, 64, 128 and 256 in us, 128 experts: 500 tokens 4.5 5.1 - -, 5000 8.5 9.6 10.9 12.4,
+// 16000 11.9 11.7 13.2 19.3, 32000 21 14.8 15.3 21, 100000 56 38 33.3 31.2 (512: 39).
+constexpr int kRouteFew = 32, kRouteSome = 64, kRouteMany = 256;
 constexpr int route_block_tokens(int64_t tokens) {
   return tokens <= 8192 ? kRouteFew : tokens <= 32768 ? kRouteSome : kRouteMany;
 }
 struct RouteParams {
   int64_t tokens, stride;  // elements between tokens' logits
+  int32_t block;  // tokens of a block
   int32_t experts, k, type, normalize;
   int32_t pairs;  // logits of 16 bits lie on 4-byte boundaries two by two
   int32_t wide;   // rows of logits lie on 16-byte boundaries

@@ -254,10 +254,8 @@ def test_route_ties_infinities_and_nan(cuda):
     check_route(z.to(torch.bfloat16), 3, normalize=False)
 
 
-@pytest.mark.parametrize("tokens", [2048, 8192, 8193, 32769, 40000])
-def test_route_many_tokens(cuda, tokens):
+def check_many(tokens, experts, k):
     """Against the definition in sorts: the lowest index first among equal logits."""
-    experts, k = 37, 3
     z = torch.randn(tokens, experts, generator=generator(tokens), device="cuda").to(torch.bfloat16)
     z[::7] = -float("inf")
     got = mx.route(z, k)
@@ -273,6 +271,17 @@ def test_route_many_tokens(cuda, tokens):
     assert (got.row[total:] == -1).all()
     assert torch.equal(got.slot.flatten()[order[:total]].long(), torch.arange(total, device="cuda"))
     assert (got.slot.flatten()[order[total:]] == -1).all()
+
+
+@pytest.mark.parametrize("tokens", [2048, 8192, 8193, 32769, 40000])
+def test_route_many_tokens(cuda, tokens):
+    check_many(tokens, 37, 3)
+
+
+@pytest.mark.parametrize("tokens,experts,k", [(2049, 100, 8), (9000, 300, 9), (33000, 260, 8),
+                                              (33001, 64, 12), (70000, 128, 6)])
+def test_route_many_tokens_and_choices(cuda, tokens, experts, k):
+    check_many(tokens, experts, k)
 
 
 def test_route_one_expert_for_all(cuda):
