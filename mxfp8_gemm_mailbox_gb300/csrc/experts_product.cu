@@ -753,10 +753,10 @@ __global__ void __launch_bounds__(S::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           // g / (1 + e^-g) u, for g < 0 as g e^g / (1 + e^g) u, with the root of the exponential
-          // on both factors: nothing on the way overflows, or underflows where the result does
-          // not, and the divisor is in 1 .. 2.
+          // on both factors and the divisor, in 1 .. 2, on g alone: nothing on the way overflows
+          // where the result does not (u g before the divisor did, in the last 27 % below 2^128).
           const float root = exp2_approx(-0.72134752f * fabsf(g[i])), f = g[i] < 0.0f ? root : 1.0f;
-          u[i] = (u[i] * f) * (g[i] * f) * reciprocal_approx(fmaf(root, root, 1.0f));
+          u[i] = (u[i] * f) * ((g[i] * f) * reciprocal_approx(fmaf(root, root, 1.0f)));
         }
         store_outputs<kRows>(p, u, s.row + c + at, c + at < s.rows, w_tile * 64 + pair * 32 + n_lane);
       } else {

@@ -401,6 +401,38 @@ def test_gated_far_from_zero(cuda, power, rows):
     close_bf16(got, want, want.abs() * ((4 + 1.2 * g.abs()) * 2.0 ** -23 + 2.0 ** -21))
 
 
+@pytest.mark.parametrize("format", [None, "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("rows,n", [(3, 64), (40, 64), (3000, 512)])
+def test_gated_next_to_the_largest(cuda, format, rows, n):
+    """Results just below 2^128, of either sign, whose g u is past it for many gates.  The error as
+    in test_gated_far_from_zero."""
+    k = 128
+    gates = torch.cat([torch.arange(1.0, 2.0, 0.125) * p for p in (1, 2, 4, 8)]).double()
+    most = 0.99 * 2.0 ** 128 / (gates * torch.sigmoid(gates))  # of the ups, in steps of E4M3's
+    power = torch.floor(torch.log2(most)).clamp(max=127)
+    ups = torch.floor(most / torch.exp2(power) * 8).clamp(max=15) / 8
+    assert (gates * ups * torch.exp2(power) >= 2.0 ** 128).sum() >= 8
+    gates, power = gates.repeat(n // 32).cuda(), power.repeat(n // 32).cuda()
+    ups = torch.cat((ups, -ups)).repeat(n // 64).cuda()
+    w = torch.zeros(2 * n, k, dtype=torch.uint8, device="cuda")
+    w[:n, 0] = gates.to(torch.float8_e4m3fn).view(torch.uint8)
+    w[n:, 0] = ups.to(torch.float8_e4m3fn).view(torch.uint8)
+    w_scale = torch.full((2 * n, k // 32), 127, dtype=torch.uint8, device="cuda")
+    w_scale[n:] = (127 + power).to(torch.uint8)[:, None]
+    x = torch.zeros(rows, k, dtype=torch.uint8, device="cuda")
+    x[:, 0] = 0x38
+    x_scale = torch.full((rows, k // 32), 127, dtype=torch.uint8, device="cuda")
+    product = mx.ExpertProduct(w, w_scale, gated=True)
+    want = (gates * torch.sigmoid(gates) * ups * torch.exp2(power)).expand(rows, n)
+    error = want.abs() * ((4 + 1.2 * gates) * 2.0 ** -23 + 2.0 ** -21)
+    got = product.run(x, x_scale, format=format)
+    assert product.status() == 0
+    if format is None:
+        close_bf16(got, want, error)
+    else:
+        close_codes(*got, want, error)
+
+
 def test_gated_cut_tiles(cuda):
     Case([4], 64, 8192, gated=True).check("mxfp8")
     Case([300], 192, 8192, gated=True).check("mxfp4")
