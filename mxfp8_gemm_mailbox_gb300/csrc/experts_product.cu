@@ -120,12 +120,13 @@ __device__ __forceinline__ void pair_barrier(int pair) {
   asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
 }
 
-// To some 2^-22 of the value; below 2^-126 zero.
+// To some 2^-22 of the value, subnormal ones too (to their steps).
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The same, of a number in 1 .. 2.
 __device__ __forceinline__ float reciprocal_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -754,7 +755,9 @@ __global__ void __launch_bounds__(S::kThreads, 1)
         for (int i = 0; i < kRows; ++i) {
           // g / (1 + e^-g) u, for g < 0 as g e^g / (1 + e^g) u, with the root of the exponential
           // on both factors and the divisor, in 1 .. 2, on g alone: nothing on the way overflows
-          // where the result does not (u g before the divisor did, in the last 27 % below 2^128).
+          // where the result does not (u g before the divisor did, in the last 27 % below 2^128),
+          // and the root, subnormal from g = -175 on, is zero only where the result is less than
+          // every format's smallest.
           const float root = exp2_approx(-0.72134752f * fabsf(g[i])), f = g[i] < 0.0f ? root : 1.0f;
           u[i] = (u[i] * f) * ((g[i] * f) * reciprocal_approx(fmaf(root, root, 1.0f)));
         }

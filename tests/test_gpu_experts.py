@@ -433,6 +433,40 @@ def test_gated_next_to_the_largest(cuda, format, rows, n):
         close_codes(*got, want, error)
 
 
+@pytest.mark.parametrize("format", [None, "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("rows", [3, 40])
+def test_gated_far_below_zero(cuda, format, rows):
+    """Gates from -160 to -191, a block each, times ups near 2^128: results down to FP32's and the
+    scales' smallest, while the exponential's root is subnormal from -175 on.  The error as in
+    test_gated_far_from_zero; a step (2^-149) of the root, which stands squared, and of what is
+    subnormal after it."""
+    gates = -torch.arange(160, 192, dtype=torch.float64)
+    n, k = 32 * len(gates), 128
+    w = torch.zeros(2 * n, k, dtype=torch.uint8, device="cuda")
+    code = lambda v: v.to(torch.float8_e4m3fn).view(torch.uint8).cuda()  # noqa: E731
+    most = 16 * torch.ceil(gates / 16)  # E4M3 takes -160 and -176, and the rest
+    w[:n, 0] = code(most).repeat_interleave(32)
+    w[:n, 1] = code(gates - most).repeat_interleave(32)
+    ups = (1 + torch.arange(32) % 8 / 8) * torch.where(torch.arange(32) < 16, 1.0, -1.0)
+    w[n:, 0] = code(ups).repeat(len(gates))
+    w_scale = torch.full((2 * n, k // 32), 127, dtype=torch.uint8, device="cuda")
+    w_scale[n:] = 254
+    x = torch.zeros(rows, k, dtype=torch.uint8, device="cuda")
+    x[:, :2] = 0x38
+    x_scale = torch.full((rows, k // 32), 127, dtype=torch.uint8, device="cuda")
+    product = mx.ExpertProduct(w, w_scale, gated=True)
+    g = gates.cuda().repeat_interleave(32)
+    want = g * torch.sigmoid(g) * ups.double().cuda().repeat(len(gates)) * 2.0 ** 127
+    relative = (4 + 1.2 * g.abs()) * 2.0 ** -23 + 2.0 ** -21 + 2.0 ** -148 / torch.exp(g / 2)
+    error = want.abs() * relative + 2.0 ** -148
+    got = product.run(x, x_scale, format=format)
+    assert product.status() == 0
+    if format is None:
+        close_bf16(got, want.expand(rows, n), error.expand(rows, n))
+    else:
+        close_codes(*got, want.expand(rows, n), error.expand(rows, n))
+
+
 def test_gated_cut_tiles(cuda):
     Case([4], 64, 8192, gated=True).check("mxfp8")
     Case([300], 192, 8192, gated=True).check("mxfp4")
