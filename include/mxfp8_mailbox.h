@@ -578,6 +578,7 @@ mxfp8_status mxfp8_latent_attend(const mxfp8_latent_desc* desc, const void* q, c
 #define MXFP8_FORMAT_MXFP4 2
 #define MXFP8_MAX_EXPERTS 512
 #define MXFP8_MAX_CHOICES 32
+#define MXFP8_MAX_EXPERT_ROWS 0x7FFFFBFF
 
 /* Workspace bytes of mxfp8_route (0 where it needs none, as for up to 32 tokens;
  * also for invalid sizes). */
@@ -635,7 +636,7 @@ typedef struct mxfp8_expert_desc {
   int32_t w_format;   /* MXFP8_FORMAT_MXFP8 or MXFP8_FORMAT_MXFP4                         */
   int32_t x_format;   /* the same                                                         */
   int32_t out_format; /* any of the three                                                 */
-  int32_t rows;       /* of x and of the result                                           */
+  int32_t rows;       /* of x and of the result: 0..MXFP8_MAX_EXPERT_ROWS (2^31 - 1025)   */
 } mxfp8_expert_desc;
 
 /* Bytes of the matrices' scales as the product reads them; 0 for an invalid shape

@@ -288,6 +288,11 @@ mxfp8_status mxfp8_expert_product(const mxfp8_expert_desc* d, const void* w, con
   if (d->rows < 0) return fail(MXFP8_ERR_INVALID, "rows must not be negative");
   if (!begin && d->experts != 1)
     return fail(MXFP8_ERR_INVALID, "begin is NULL, and there is more than one expert");
+  // Rows past the last by a tile's, and by the experts, are still counted in 31 bits.
+  if (d->rows > MXFP8_MAX_EXPERT_ROWS)
+    return fail(MXFP8_ERR_UNSUPPORTED, "rows must be at most " +
+                                           std::to_string(MXFP8_MAX_EXPERT_ROWS) + ", got " +
+                                           std::to_string(d->rows));
   // Tiles are numbered in 31 bits (32 rows the smallest).
   if ((static_cast<int64_t>(d->rows) / 32 + d->experts) * w_tiles(*d) > 1 << 30)
     return fail(MXFP8_ERR_UNSUPPORTED, "rows x n is past 2^30 tiles");

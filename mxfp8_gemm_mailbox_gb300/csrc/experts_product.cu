@@ -90,6 +90,7 @@ struct Shape {
   static_assert(kXRows % 8 == 0 && kSmall % 8 == 0, "copies of whole swizzled groups");
   static_assert(kPair ? kPipes == 1 && kTiles == 1 : kChunks == 1, "scales");
   static_assert(kCols % kAtOnce == 0, "whole reads");
+  static_assert(0x7FFFFFFF - MXFP8_MAX_EXPERT_ROWS >= kCols + MXFP8_MAX_EXPERTS, "31 bits");
   // Shared memory, from a 1024-byte boundary.
   static constexpr uint32_t kX = kStages * kTiles * kWTile;
   static constexpr uint32_t kSfa = kX + kStages * kTiles * kXTile;

@@ -108,6 +108,16 @@ def test_product_refusals(lib):
     assert lib.mxfp8_expert_product(None, *[None] * 8, 0, None, None) == mx.ERR_INVALID
 
 
+def test_product_most_rows(lib):
+    """Rows whose count with a tile's or the experts' would pass 31 bits, in one tile of W (past
+    the check of tiles); the largest count allowed reaches the pointers' checks."""
+    for rows in (2 ** 31 - 1, 2 ** 31 - 1024):
+        assert product(lib, rows=rows, n=8, k=128, experts=1) == mx.ERR_UNSUPPORTED, rows
+        assert product(lib, rows=rows, n=8, k=128, experts=512) == mx.ERR_UNSUPPORTED, rows
+        assert "rows must be at most" in text(lib)
+    assert product(lib, rows=2 ** 31 - 1025, n=8, k=128, experts=1, x=A + 16) == mx.ERR_INVALID
+
+
 def test_scales(lib):
     size = lambda **kw: lib.mxfp8_expert_scales_bytes(ctypes.byref(desc(**kw)))  # noqa: E731
     assert size() == 4 * 1 * 2 * 512
