@@ -120,12 +120,18 @@ at::Tensor tensor_of(c10::Storage storage, int64_t at, at::IntArrayRef shape,
   impl->set_storage_offset(at);
   return t;
 }
+// Torch makes it where there is more to do than to take memory: an object of another device;
+// a size below zero, which it refuses.
 at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType dtype, int device) {
-  if (device != c10::cuda::current_device())  // an object's of another device
+  bool plain = device == c10::cuda::current_device();
+  int64_t bytes = static_cast<int64_t>(c10::elementSize(dtype));
+  for (const int64_t n : shape) {
+    plain = plain && n >= 0;
+    bytes *= n;
+  }
+  if (!plain)
     return at::empty(shape,
                      at::TensorOptions().dtype(dtype).device(at::Device(at::kCUDA, device)));
-  int64_t bytes = static_cast<int64_t>(c10::elementSize(dtype));
-  for (const int64_t n : shape) bytes *= n;
   return tensor_of(new_storage(bytes), 0, shape, dtype);
 }
 void* handle_of(PyObject* s) {

@@ -150,3 +150,9 @@ def test_a_consume_without_a_limit(cuda):
         mailbox.publish(c)
         assert torch.equal(mailbox.consume(4, timeout_ns=limit), c)
     assert mailbox.status()[0] == mx.OK
+
+
+def test_a_negative_size_is_refused(cuda):
+    mailbox = mx.Mailbox(8, 256)
+    with pytest.raises(RuntimeError, match="negative"):
+        mailbox.consume(-1)
