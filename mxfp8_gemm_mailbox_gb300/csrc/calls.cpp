@@ -5,6 +5,7 @@
 // kernel's call on a Grace core.)
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/core/ScalarTypeToTypeMeta.h>
@@ -121,9 +122,12 @@ at::Tensor tensor_of(c10::Storage storage, int64_t at, at::IntArrayRef shape,
   return t;
 }
 // Torch makes it where there is more to do than to take memory: an object of another device;
-// a size below zero, which it refuses.
+// a size below zero, which it refuses; its deterministic mode, where it fills the memory (rows
+// that a call leaves as they were hold NaN or a type's largest, the same every time).
 at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType dtype, int device) {
-  bool plain = device == c10::cuda::current_device();
+  const at::Context& context = at::globalContext();
+  bool plain = device == c10::cuda::current_device() &&
+               !(context.deterministicAlgorithms() && context.deterministicFillUninitializedMemory());
   int64_t bytes = static_cast<int64_t>(c10::elementSize(dtype));
   for (const int64_t n : shape) {
     plain = plain && n >= 0;

@@ -108,3 +108,32 @@ def test_two_products_on_two_streams_at_once(cuda):
     torch.cuda.synchronize()
     for g, v in zip(got, want):
         assert all(torch.equal(t.view(torch.uint8), v.view(torch.uint8)) for t in g)
+
+
+def test_rows_that_are_left_in_deterministic_mode(cuda):
+    """What torch fills new memory with there: NaN, a type's largest where it has none."""
+    w, w_scale = random_codes(3, (1, 512), 256, 4, -6, -4)
+    x, x_scale = random_codes(4, (40,), 256, 8)
+    begin = begin_of([10])
+    product = mx.ExpertProduct(w, w_scale)
+    rows = torch.full((40,), -1, dtype=torch.int32, device="cuda")
+    rows[:10] = torch.arange(10, device="cuda")
+    calls = [lambda: [product.run(x, x_scale, begin)]]
+    for format in ("mxfp8", "mxfp4"):
+        calls.append(lambda f=format: product.run(x, x_scale, begin, format=f))
+        calls.append(lambda f=format: mx.quantize(_rows(), f, rows=rows))
+    was = torch.are_deterministic_algorithms_enabled(), torch.is_deterministic_algorithms_warn_only_enabled()
+    for call in calls:
+        plain = call()
+        for t in plain:  # (what the next outputs' memory holds)
+            t.view(torch.uint8).fill_(0x11)
+        plain = [t.clone() for t in call()]
+        torch.use_deterministic_algorithms(True, warn_only=True)
+        try:
+            got = call()
+        finally:
+            torch.use_deterministic_algorithms(was[0], warn_only=was[1])
+        for a, b in zip(got, plain):
+            assert torch.equal(a[:10].view(torch.uint8), b[:10].view(torch.uint8))
+            rest = a[10:]
+            assert torch.isnan(rest.float()).all() if rest.is_floating_point() else (rest == 255).all()
