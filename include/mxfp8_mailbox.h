@@ -622,9 +622,10 @@ mxfp8_status mxfp8_quantize(const void* x, int32_t type, int64_t stride, int64_t
                             const int32_t* rows, int64_t out_rows, int32_t format, void* codes,
                             void* scales, int32_t* flags, void* stream);
 
-/* The values of [rows][K] codes, K a multiple of 32, in `type`: FP32 holds them all (but
- * those of scales that mxfp8_quantize does not make, past its range: infinite); BF16 and
- * FP16 take them rounded to nearest.  out 16-byte aligned. */
+/* The values of [rows][K] codes, K a multiple of 32, in `type`: FP32 holds all below 2^128;
+ * what is larger becomes infinite.  (A finite number may: one within half a step of 2^128,
+ * as BF16's largest, is rounded to 256 x 2^120 or 4 x 2^126.)  BF16 and FP16 take the values
+ * rounded to nearest.  out 16-byte aligned. */
 mxfp8_status mxfp8_dequantize(const void* codes, const void* scales, int64_t rows, int32_t k,
                               int32_t format, int32_t type, void* out, void* stream);
 

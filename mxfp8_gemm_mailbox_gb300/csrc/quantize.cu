@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const __grid_constan
   }
 }
 
-// Values of 16 numbers: exact in FP32; rounded once where the type is narrower
-// than a value's exponent.
+// Values of 16 numbers: exact in FP32 below 2^128, infinite from there on; rounded once
+// where the type is narrower than a value's exponent.
 template <int kType, int kBits>
 __global__ void __launch_bounds__(kThreads)
     dequantize_kernel(const uint8_t* codes, const uint8_t* scales, void* out, uint32_t items) {

@@ -64,8 +64,9 @@ _TYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.FP16, torch.float32: _l
 
 def dequantize(codes: torch.Tensor, scale: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
                stream=None) -> torch.Tensor:
-    """The values ``[...][K]`` of codes as ``quantize`` makes them; FP32 holds every
-    value, BF16 and FP16 (``dtype``) what rounds to them."""
+    """The values ``[...][K]`` of codes as ``quantize`` makes them; FP32 holds every value
+    below 2^128 (numbers within half a step of it are rounded up to it, and come back
+    infinite), BF16 and FP16 (``dtype``) what rounds to them."""
     if dtype not in _TYPES:
         raise TypeError(f"dtype must be bfloat16, float16 or float32, got {dtype}")
     return _lib.calls().dequantize(codes, scale, _TYPES[dtype], stream)

@@ -141,6 +141,41 @@ def test_quantize_gathers_strided_rows_and_leaves_others(cuda):
     assert int(flags) == mx.FLAG_BAD_INDEX
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_dequantize_every_code_and_scale(cuda, bits, dtype):
+    """Every code under every scale: the value rounded once to the type, infinite past its largest,
+    NaN under 255.  (FP32 is wider than E2M1 and E4M3 by their own digits, so that rounding its
+    value rounds once.)"""
+    codes = torch.arange(256, device="cuda").to(torch.uint8).repeat(256, 1)
+    scale = torch.arange(256, device="cuda").to(torch.uint8)[:, None]
+    scale = scale.expand(256, 256 * 8 // bits // 32).contiguous()
+    got = mx.dequantize(codes, scale, dtype)
+    exact = values(codes, scale)
+    assert got.dtype == dtype and got.shape == exact.shape
+    if bits == 4:
+        assert torch.equal(torch.isnan(exact), (scale == 255).repeat_interleave(32, 1))
+    want = exact.float().to(dtype)  # 4 digits down to 2^-136: exact in FP32 below its largest
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got.double(), nan=0.0, posinf=1e300, neginf=-1e300),
+                       torch.nan_to_num(want.double(), nan=0.0, posinf=1e300, neginf=-1e300))
+    assert torch.equal(torch.signbit(got)[~torch.isnan(got)], torch.signbit(want)[~torch.isnan(want)])
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_quantize_and_back_next_to_the_largest(cuda, bits):
+    """Finite numbers that a block rounds up past FP32's largest come back infinite; all others
+    within half a step of the element type."""
+    top = torch.finfo(torch.bfloat16).max
+    x = top * torch.linspace(0.25, 1.0, 64, device="cuda")
+    x = torch.stack((x, -x)).bfloat16()
+    back = mx.dequantize(*mx.quantize(x, "mxfp%d" % bits), torch.float32).double()
+    past = x.double().abs() >= 2.0 ** 128 * (1 - 2.0 ** -5 if bits == 8 else 7 / 8)
+    assert past.any() and torch.equal(torch.isinf(back), past)
+    near = (back - x.double()).abs() <= x.double().abs() * 2.0 ** -(4 if bits == 8 else 2)
+    assert (near | past).all() and torch.equal(torch.signbit(back), torch.signbit(x))
+
+
 def test_quantize_shapes(cuda):
     x = torch.randn(2, 3, 5, 64, generator=generator(5), device="cuda")
     codes, scale = mx.quantize(x, "mxfp4")
