@@ -10,8 +10,6 @@
 
 namespace mxfp8 {
 
-constexpr int kMxBlock = 32;
-
 // The E8M0 code of a block whose largest magnitude is `top`: 127 for a block
 // of zeros; top = f 2^E (1 <= f < 2) takes E - 8 for f <= 1.75, else E - 7.
 __device__ __forceinline__ uint32_t scale_code(float top) {
