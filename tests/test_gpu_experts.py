@@ -319,6 +319,31 @@ def test_route_many_tokens_and_choices(cuda, tokens, experts, k):
     check_many(tokens, experts, k)
 
 
+@pytest.mark.parametrize("tokens,experts,k", [(8193, 33, 4), (9000, 300, 8), (33000, 260, 8),
+                                              (40000, 100, 5), (9000, 64, 9), (33001, 64, 12),
+                                              (34000, 500, 10)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_route_weights_of_many_tokens(cuda, tokens, experts, k, dtype, normalize):
+    """Blocks of 64 and 256 tokens, whose logits are loaded while those before are chosen from.
+    The tolerance of the file's head, and of all experts' sum a rounding for each of a lane's
+    experts (an eighth, or fewer) and of its reduction's steps."""
+    z = (torch.randn(tokens, experts, generator=generator(k), device="cuda") * 3).to(dtype)
+    z[::7] = -float("inf")
+    z[1::7, k - 1:] = -float("inf")  # fewer than k
+    got = mx.route(z, k, normalize)
+    top, expert = torch.sort(z.double(), dim=1, descending=True, stable=True)
+    chosen = top[:, :k] > -float("inf")
+    assert torch.equal(got.expert.long(), torch.where(chosen, expert[:, :k], -1))
+    exps = torch.exp(torch.where(top > -float("inf"), top - top[:, :1], top))
+    total = (exps[:, :k] if normalize else exps).sum(1, keepdim=True)
+    weight = torch.where(chosen, exps[:, :k] / total, 0.0)
+    distance = torch.where(chosen, top[:, :1] - top[:, :k], 0.0)
+    sums = 0.0 if normalize else (experts / 8 + 5) * 2.0 ** -24
+    off = (got.weight.double() - weight).abs()
+    assert (off <= (2.0 ** -20 + sums + 2.0 ** -24 * distance) * weight + 1e-37).all()
+
+
 def test_route_one_expert_for_all(cuda):
     z = torch.zeros(700, 16, device="cuda")
     z[:, 5] = 4.0
