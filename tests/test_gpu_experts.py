@@ -558,6 +558,17 @@ def test_scales_between_16_byte_boundaries(cuda, rows, n, words):
     assert product.status() == 0
 
 
+@pytest.mark.parametrize("rows", [5, 50, 1000])
+def test_codes_written_in_place_are_read(cuda, rows):
+    """By the kernel right before the call, too."""
+    c = Case([rows], 2560, 512)
+    c.check()
+    other, _ = random_codes(92, (1, 2560), 512, 4)
+    c.w.copy_(other)
+    got = c.product.run(c.x, c.x_scale, c.begin)
+    close_bf16(got, *c.expected())
+
+
 def test_rows_of_no_expert_are_left(cuda):
     for counts, total in (([5, 3], 12), ([100, 90], 260)):
         c = Case(counts, 128, 256)
