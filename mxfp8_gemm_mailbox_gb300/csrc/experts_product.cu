@@ -38,12 +38,15 @@
 // elected lane of a converged warp copies and issues: from a branch on the lane
 // number a product took a third longer.
 //
-// Measured (graphs of calls, inputs alternating): a token's 8 experts, N 4096, K
-// 2048, MXFP4: 10.6 us, of which 5.3 are the matrices at the memory's rate and some
-// 5 the launch's wait, begin's latency, the deal and the first copies; 64 rows on 36
-// experts, gated, N 2048, K 4096: 51.8 us, 6.2 TB/s; 4096 rows at N 7168, K 16384,
-// MXFP8: 305 us, 3.15 PFLOP/s (both in 4 bits 246 us); 32768 rows on 64 experts,
-// gated, N 2048, K 4096: 386 us, 2.85 PFLOP/s.
+// Measured (graphs of calls with inputs and outputs of their own, past twice L2
+// together; comparisons in these comments alternate up to four sets, which L2 holds
+// where they are small): a token's 8 experts, N 4096, K 2048, MXFP4: 10.9 us, of
+// which 5.3 are the matrices at the memory's rate and some 5 the launch's wait,
+// begin's latency, the deal and the first copies; 64 rows on 36 experts, gated, N
+// 2048, K 4096: 52 us, 6.2 TB/s; 4096 rows at N 7168, K 16384, MXFP8: 334 us, 2.88
+// PFLOP/s (297 in the first 20 ms, before the power limit; both in 4 bits 261);
+// 32768 rows on 64 experts, gated, N 2048, K 4096: 414 us, 2.66 PFLOP/s (379 at
+// first); 999 rows on 7 experts, gated, N 736, K 896: 10.0 us.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -952,6 +955,9 @@ size_t expert_partial_bytes(int ctas) {
 // and cutting (by 24 k tiles saved, 40 where there are more partials), one matrix,
 // whole and cut, at 1 row and K = 4096, 8192, 16384: N = 128 6.1 6.6, 9.0 6.8, 14.9 7.0; N =
 // 4096 6.6 7.5, 11.3 8.6, 21.0 12.9; at 64 rows N = 2048 7.9 10.3, 11.6 11.4, 24.4 16.2.
+// Rows in no expert count as others do, and where one expert has them all the mean says
+// little (gated, 2048 x 4096, one expert of 64 with all rows, and its matrix by itself):
+// 512 rows 21.0 14.7, 4096 rows 71.0 46.3, 16384 rows 180 185.
 ExpertTile expert_tile(int rows, int experts, int w_tiles, int k_tiles, int ctas) {
   const int active = std::max(1, std::min(rows, experts));
   const int each = (rows + experts - 1) / experts;

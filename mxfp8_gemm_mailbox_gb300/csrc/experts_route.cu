@@ -24,14 +24,15 @@
 // 6.6 without; 94 blocks 7.7 and 8.1).
 //
 // Bound by instructions where there are many tokens (a lane's compares and exchanges, which
-// issue at half rate, are most of them) and by the launches where there are few: 16384
-// tokens, 256 experts, k 8 12.5 us (the logits are 1.2 us' reading); a token 2.9 us, 500
-// tokens of 128 experts 4.5, 100000 31.
+// issue at half rate, are most of them) and by three launches that wait for one another:
+// 16384 tokens, 256 experts, k 8 13.4 us (12.5 with the logits in L2; they are 1.2 us'
+// reading; the kernels alone, cold: choice 8.1, sums 4.7, places 5.1); a token 2.8 us, 500
+// tokens of 128 experts 4.6, 100000 31.
 //
 // Combine.  out[t] = add[t] + sum_j weight[t][j] y[slot[t][j]], in FP32, j
 // ascending, rounded once; a thread has 8 numbers of a row, and its loads are
-// all under way at once.  Bound by the memory: 4096 tokens, 8 rows of 4096 each, 46.5 us for
-// 302 MB (6.5 TB/s); one token 2.5 us, the launch and two round trips.
+// all under way at once.  Bound by the memory: 4096 tokens, 8 rows of 4096 each, 47.6 us for
+// 302 MB (6.3 TB/s); one token 1.9 us, the launch and two round trips.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

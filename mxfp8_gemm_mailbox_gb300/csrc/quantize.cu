@@ -15,7 +15,7 @@
 // than the memory: 139 us below).
 //
 // Measured: 16384 x 8192 BF16 to MXFP4 and back 103 us for 687 MB, 6.7 TB/s (the copy rate is
-// 6.78); one share a thread 106, four 105.  64 gathered rows of 7168: 1.8 us, the launch and
+// 6.78); one share a thread 106, four 105.  64 gathered rows of 7168: 1.7 us, the launch and
 // two round trips.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

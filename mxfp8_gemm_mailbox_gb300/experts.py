@@ -29,7 +29,9 @@ class Routing(NamedTuple):
     """``weight`` FP32 and ``expert`` int32 [tokens][k], ``slot`` int32 [tokens][k]
     (the row of each choice in the experts' products, -1 for none), ``row`` int32
     [tokens * k] (the token of each row, -1 past the last), ``begin`` int32
-    [experts + 1] (where each expert's rows begin)."""
+    [experts + 1] (where each expert's rows begin).  The five lie in one piece of memory
+    (with the call's workspace): keeping or saving one keeps or saves all, a ``clone`` of
+    it does not."""
 
     weight: torch.Tensor
     expert: torch.Tensor
@@ -78,9 +80,11 @@ class ExpertProduct:
     ``gated``: N holds a gate's rows, then as many of an up matrix, and the result is
     silu(gate) x up, N / 2 wide.
 
-    The codes stay borrowed; the scales are copied, once, into the products' order, and
-    the constructor waits for that.  The workspace (5 MB) and the flags word live here;
-    ``workspace``: another product's, to be shared.  Calls that share one are ordered on
+    For matrices that stay: the codes are borrowed and read in place, while the scales are
+    copied, once, into the products' order, and the constructor waits for that.  New codes
+    written into ``w`` are what the next call reads; for new scales, make another object.
+    The workspace (5 MB) and the flags word live here; ``workspace``: another product's, to
+    be shared.  Calls that share one are ordered on
     one stream, made by one host thread at a time, and the object outlives what they have
     queued on another stream than the one it was made on."""
 
